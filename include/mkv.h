@@ -380,6 +380,235 @@ mkv_status mkv_basis_static(const void* k, const void* v, int batch, int n_kv_he
                             int64_t ctx_len, float* basis, float* eigvals,
                             mkv_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions and an uncompressed, paged key-value cache.
+ *
+ * Interface additions with no counterpart in the paper: what a program needs
+ * next to the compressed cache.  mkv_rope makes the rotated keys and queries
+ * that mkv_compress, mkv_append and mkv_decode take; the paged cache serves
+ * layers and sequences that are not compressed, and is cut down by accumulated
+ * attention weight instead.
+ *
+ * These calls hold no ctx.  They work on the calling thread's current CUDA
+ * device, to which every device pointer and `stream` must belong, launch on
+ * `stream` without host synchronisation or allocation, and can be captured
+ * into a CUDA graph.  Scratch memory is the caller's (`workspace`): calls that
+ * may overlap in time, replays of captured graphs included, need workspaces of
+ * their own.  Nothing in a workspace has to be initialised or kept.
+ * Argument errors return MKV_ERR_INVALID_ARG before any CUDA call, with the
+ * reason in mkv_last_error_string.
+ * ------------------------------------------------------------------------- */
+
+/* Element types. */
+enum {
+  MKV_DT_F16 = 0,
+  MKV_DT_BF16 = 1,
+  MKV_DT_F32 = 2,
+  MKV_DT_E4M3 = 3   /* 8-bit float, 4 exponent and 3 mantissa bits, largest 448 */
+};
+
+/* How the rotation's frequencies are scaled for contexts longer than trained. */
+enum {
+  MKV_ROPE_NONE = 0,
+  MKV_ROPE_LINEAR = 1, /* every frequency divided by `factor` */
+  MKV_ROPE_NTK = 2,    /* base * factor^(rot_dim / (rot_dim - 2)) */
+  MKV_ROPE_YARN = 3,   /* YaRN (arXiv 2309.00071): pairs that turn more than beta_fast
+                          times over `original` positions keep their frequency, those
+                          below beta_slow are divided by `factor`, a ramp between;
+                          vectors multiplied by 0.1 ln(factor) + 1 */
+  MKV_ROPE_BANDED = 4  /* wavelengths below original / high_freq keep their frequency,
+                          above original / low_freq divided by `factor`, blended in
+                          original / wavelength between */
+};
+
+#define MKV_ROPE_MAX_PAIRS 128
+
+typedef struct {
+  int32_t head_dim;     /* 1..4096 */
+  int32_t rot_dim;      /* rotated leading elements: even, 2..min(head_dim, 256) */
+  int32_t interleaved;  /* 1: pair i = elements 2i, 2i + 1; 0: elements i, i + rot_dim / 2 */
+  int32_t scaling;      /* MKV_ROPE_* */
+  double base;          /* > 1; pair i turns by base^(-2i / rot_dim) radians a position */
+  double factor;        /* >= 1 (LINEAR, NTK, YARN, BANDED) */
+  double original;      /* > 0: positions the model was trained on (YARN, BANDED) */
+  double low_freq;      /* 0 < low_freq < high_freq (BANDED) */
+  double high_freq;
+  double beta_fast;     /* beta_fast >= beta_slow > 0 (YARN) */
+  double beta_slow;
+  double attn_factor;   /* > 0: multiplies rotated elements; 0: the scaling's own (1, or YaRN's) */
+} mkv_rope_config;
+
+/* A rotation ready to use: plain host data, made by mkv_rope_plan_init.
+ * turn[i]: the part of a full turn that pair i advances per position, times
+ * 2^64, so that position * turn[i] modulo 2^64 is the exact phase at any
+ * position. */
+typedef struct {
+  uint64_t turn[MKV_ROPE_MAX_PAIRS];
+  float mult;
+  int32_t head_dim, rot_dim, interleaved;
+} mkv_rope_plan;
+
+/* Host only, no GPU.  MKV_ERR_INVALID_ARG for a value outside the ranges above. */
+mkv_status mkv_rope_plan_init(const mkv_rope_config* cfg, mkv_rope_plan* plan);
+
+typedef struct {
+  const void* x;          /* device [batch][tokens][heads][head_dim] of `dtype` */
+  void* out;              /* device, the same shape; may be x with the same strides */
+  const int32_t* pos;     /* device [batch][tokens] positions (any int32), or NULL: first_pos + token */
+  int64_t x_stride[3];    /* elements between batches, tokens, heads (a head's elements are */
+  int64_t out_stride[3];  /* adjacent); x's may be 0 or negative, out's positive where the extent > 1 */
+  int64_t pos_stride;     /* elements between the batches of pos (tokens are adjacent) */
+  int64_t tokens;         /* >= 0 */
+  int32_t batch, heads;   /* >= 0 */
+  int32_t dtype;          /* MKV_DT_F16, BF16 or F32 */
+  int32_t first_pos;      /* position of token 0 of every batch entry when pos is NULL */
+  int32_t transposed;     /* 1: the transposed rotation (angles negated): the gradient of the
+                             call with 0; and its inverse when plan->mult is 1 */
+} mkv_rope_args;
+
+/* Rotates every pair of the first rot_dim elements of every head by its angle
+ * position * frequency: (a, b) -> mult * (a cos - b sin, a sin + b cos); the
+ * rest of the head is copied.  Computed in fp32 from the exact phase, rounded
+ * once to `dtype`.  Apart from x == out, out must not overlap x's elements.
+ * 16-byte loads are used where rot_dim, head_dim, pointers and strides allow
+ * it, single elements otherwise. */
+mkv_status mkv_rope(const mkv_rope_plan* plan, const mkv_rope_args* args, mkv_stream_t stream);
+
+/* A paged cache: a view of memory that the caller owns, nothing is kept.
+ * Slot t of sequence b lies in row t mod page_size of page
+ * page_table[b * table_stride + t / page_size]. */
+typedef struct {
+  void* k_pages;              /* device [n_pages][n_kv_heads][page_size][head_dim], 16-byte aligned */
+  void* v_pages;
+  const int32_t* page_table;  /* device [batch][max_pages], row stride table_stride */
+  const float* k_scale;       /* E4M3 only: device [n_kv_heads], an element stands for value * scale; */
+  const float* v_scale;       /*   NULL: 1.  Scales must be positive and finite. */
+  int32_t* status;            /* device word, or NULL: bits set by kernels (see mkv_paged_check) */
+  int64_t table_stride;       /* >= max_pages */
+  int32_t dtype;              /* MKV_DT_F16, BF16 or E4M3 */
+  int32_t batch;              /* 1..65535 */
+  int32_t n_kv_heads;         /* 1..65535 */
+  int32_t head_dim;           /* 64, 128 or 256 */
+  int32_t page_size;          /* 16..256, multiple of 16 */
+  int32_t n_pages;            /* >= 1 */
+  int32_t max_pages;          /* pages of the longest sequence the table has room for, >= 1;
+                                 max_pages * page_size <= 2^30 */
+} mkv_paged_cache;
+
+/* Checks a cache view without touching any GPU. */
+mkv_status mkv_paged_validate(const mkv_paged_cache* cache);
+
+typedef struct {
+  const void* k;          /* device [n][n_kv_heads][head_dim] of in_dtype */
+  const void* v;
+  const void* q;          /* device [n][n_q_heads][head_dim], or NULL */
+  void* q_out;            /* device [n][n_q_heads][head_dim]: the rotated queries; may be q */
+  const int32_t* seq;     /* device [n]: the sequence a token belongs to; NULL: token i to sequence i */
+  const int32_t* slot;    /* device [n]: its slot; negative: the token is padding, nothing of it is
+                             written to the cache (its q is rotated all the same) */
+  const int32_t* pos;     /* device [n]: position of the rotation; NULL: the slot */
+  float* acc;             /* device [batch][n_kv_heads][meta_stride], or NULL: the slot's accumulated
+                             weight is set to 0 */
+  int32_t* pos_meta;      /* device [batch][n_kv_heads][meta_stride], or NULL: the slot's position is noted */
+  int64_t k_stride[2];    /* elements between tokens, heads; multiples of 8 */
+  int64_t v_stride[2];
+  int64_t q_stride[2];
+  int64_t q_out_stride[2];
+  int64_t meta_stride;    /* >= every slot + 1 */
+  int64_t n;              /* tokens, >= 0 */
+  int32_t n_q_heads;      /* with q */
+  int32_t in_dtype;       /* MKV_DT_F16 or BF16; the cache's type unless that is E4M3 */
+} mkv_paged_append_args;
+
+/* Writes n new tokens into their slots: keys rotated by `plan` (NULL: not
+ * rotated), values as they are, both rounded to the cache's type (E4M3:
+ * divided by the head's scale, nearest even, saturated at 448); queries are
+ * rotated with the same positions.  Two tokens of a call must not share a
+ * slot.  plan->rot_dim must be a multiple of 16 (half pairs) or 8
+ * (interleaved) and plan->head_dim the cache's.  A token whose sequence, slot
+ * or page lies outside the cache is left out and reported in `status`. */
+mkv_status mkv_paged_append(const mkv_paged_cache* cache, const mkv_rope_plan* plan,
+                            const mkv_paged_append_args* args, mkv_stream_t stream);
+
+typedef struct {
+  const void* q;            /* device [batch][n_q_heads][head_dim], 16-byte aligned; F16 or BF16, the
+                               cache's type unless that is E4M3 */
+  void* out;                /* device [batch][n_q_heads][head_dim] of out_dtype, contiguous, 16-byte aligned */
+  float* lse;               /* device [batch][n_q_heads], or NULL: ln of the sum of exp(score) */
+  const int32_t* seq_lens;  /* device [batch]: cached tokens of each sequence, 0 .. max_len */
+  float* acc;               /* device [batch][n_kv_heads][acc_stride], or NULL: every token's softmax
+                               weights, summed over the group's query heads, are added */
+  void* workspace;          /* device, 16-byte aligned, of mkv_paged_decode_workspace bytes */
+  uint64_t workspace_bytes;
+  int64_t q_stride[2];      /* elements between sequences, heads; multiples of 8 */
+  int64_t acc_stride;       /* >= max_len */
+  int64_t max_len;          /* bound on seq_lens; 0: max_pages * page_size */
+  int32_t n_q_heads;        /* a multiple of n_kv_heads; at most 16 per KV head */
+  int32_t q_dtype;
+  int32_t out_dtype;        /* q_dtype or MKV_DT_F32 */
+  float scale;              /* on q . k, > 0; 0: 1 / sqrt(head_dim) */
+} mkv_paged_decode_args;
+
+/* Bytes of workspace that mkv_paged_decode needs with these arguments on the
+ * current device (pointers are not looked at, except whether acc is NULL);
+ * 0 for invalid arguments. */
+uint64_t mkv_paged_decode_workspace(const mkv_paged_cache* cache, const mkv_paged_decode_args* args);
+
+/* Attention of one new token per sequence over its seq_lens[b] cached tokens
+ * (the new token's own row among them, once appended): softmax of
+ * scale * q . k in fp32, weighted sum of v.  Query head i reads KV head
+ * i / g, g = n_q_heads / n_kv_heads.  A sequence of length 0 gives zeros and
+ * an lse of -inf.  Slots at or behind seq_lens[b] are never used, whatever
+ * they hold.  A length below 0 or above max_len counts as 0 or max_len, and a
+ * page outside the cache as absent tokens; both are reported in `status`.
+ * Results do not depend on timing: no atomics, a fixed order of summation for
+ * given lengths and bounds. */
+mkv_status mkv_paged_decode(const mkv_paged_cache* cache, const mkv_paged_decode_args* args,
+                            mkv_stream_t stream);
+
+typedef struct {
+  const float* acc;         /* device [batch][n_kv_heads][meta_stride]: accumulated weights */
+  const int32_t* pos;       /* device, same shape: position of the token in each slot */
+  float* acc_out;           /* device [batch][n_kv_heads][out_stride]; may be acc (then out_stride */
+  int32_t* pos_out;         /*   = meta_stride), likewise pos */
+  const int32_t* seq_lens;  /* device [batch], 0 .. max_len */
+  const int32_t* next_pos;  /* device [batch]: position of the sequence's next token */
+  int32_t* lens_out;        /* device [batch]: min(seq_lens, budget); may be seq_lens */
+  int32_t* src;             /* device [batch][n_kv_heads][budget]: the slot whose token slot i now holds,
+                               -1 from the new length on */
+  void* workspace;          /* device, 16-byte aligned, of mkv_paged_evict_workspace bytes */
+  uint64_t workspace_bytes;
+  int64_t meta_stride;      /* >= max_len */
+  int64_t out_stride;       /* >= min(budget, max_len) */
+  int64_t max_len;          /* bound on seq_lens; 0: max_pages * page_size */
+  int32_t budget;           /* tokens to keep, >= 1 */
+  int32_t sink;             /* tokens at positions below this are kept, >= 0 */
+  int32_t recent;           /* tokens at positions >= next_pos - recent are kept, >= 0;
+                               sink + recent <= budget */
+} mkv_paged_evict_args;
+
+/* Bytes of workspace that mkv_paged_evict needs; 0 for invalid arguments. */
+uint64_t mkv_paged_evict_workspace(const mkv_paged_cache* cache, const mkv_paged_evict_args* args);
+
+/* Cuts every (sequence, KV head) with more than `budget` tokens down to
+ * `budget`: protected tokens first (sink, recent), then those of the highest
+ * accumulated weight (ties to the lower slot; a NaN weight or one below 0
+ * counts as 0).  In place, without an order among slots: kept tokens in slots
+ * below the budget stay where they are, and the i-th freed slot below the
+ * budget receives the i-th kept token from the slots behind it, so that a
+ * step which is one token over the budget moves one row.  Attention does not
+ * depend on the order of slots; pos_out says which token lies where.  Rows
+ * behind the new length are left as they were.  Heads keep different tokens;
+ * the lengths stay equal.  A page outside the cache is skipped and reported
+ * in `status`, a length outside 0 .. max_len counts as the nearer bound. */
+mkv_status mkv_paged_evict(const mkv_paged_cache* cache, const mkv_paged_evict_args* args,
+                           mkv_stream_t stream);
+
+/* Reads and clears a device status word after all work on the current device
+ * (synchronous): MKV_ERR_DEVICE_CHECK if a kernel met a page, slot, sequence
+ * or length outside the cache since the last check, else MKV_OK. */
+mkv_status mkv_paged_check(int32_t* status);
+
 #ifdef __cplusplus
 }
 #endif

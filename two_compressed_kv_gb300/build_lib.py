@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmkv.so")
 SOURCES = ["mkv_api.cu", "k_compress.cu", "k_score.cu", "k_select.cu", "k_attn.cu", "k_checks.cu",
-           "k_append.cu"]
+           "k_append.cu", "paged_api.cu", "k_rope.cu", "k_paged_attn_64.cu", "k_paged_attn_128.cu",
+           "k_paged_attn_256.cu", "k_paged_join.cu", "k_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
          "--expt-relaxed-constexpr", "-I", os.path.join(HERE, "..", "include")]

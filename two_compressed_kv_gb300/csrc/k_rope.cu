@@ -1,0 +1,363 @@
+// Rotary positions, alone and fused into the write of new tokens into a paged
+// cache.
+//
+// Pair i of a head at position t is turned by theta = t * f_i:
+//   (a, b) -> m * (a cos(theta) - b sin(theta), a sin(theta) + b cos(theta)).
+// The phase is kept as a fraction of a full turn in 64-bit fixed point:
+// turn_i = f_i / (2 pi) * 2^64, so that t * turn_i modulo 2^64 -- one wrapping
+// integer product -- is the exactly reduced phase at every position, where a
+// product in 32-bit floating point is off by 0.03 radians at a million.  Its
+// upper 32 bits, read as a signed fraction in [-1/2, 1/2), go to sincospif.
+//
+// What bounds it: memory, once each element's load and store is 16 bytes wide
+// and a thread's angles (the instructions are in sincospif) are shared by all
+// heads it handles.
+#include "paged_internal.cuh"
+
+namespace mkv {
+namespace {
+
+constexpr int RT = 256;   // threads per block
+
+struct alignas(16) Vec16 {
+  uint32_t w[4];
+};
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<__half> {
+  static constexpr int V = 8;
+  static __device__ __forceinline__ void unpack(const Vec16& v, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&v.w[i]));
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
+    }
+  }
+  static __device__ __forceinline__ Vec16 pack(const float (&f)[8]) {
+    Vec16 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      v.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return v;
+  }
+  static __device__ __forceinline__ float get(__half x) { return __half2float(x); }
+  static __device__ __forceinline__ __half put(float x) { return __float2half_rn(x); }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+  static constexpr int V = 8;
+  static __device__ __forceinline__ void unpack(const Vec16& v, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(v.w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(v.w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ Vec16 pack(const float (&f)[8]) {
+    Vec16 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      v.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return v;
+  }
+  static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
+};
+template <>
+struct Elem<float> {
+  static constexpr int V = 4;
+  static __device__ __forceinline__ void unpack(const Vec16& v, float (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v.w[i]);
+  }
+  static __device__ __forceinline__ Vec16 pack(const float (&f)[4]) {
+    Vec16 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.w[i] = __float_as_uint(f[i]);
+    return v;
+  }
+  static __device__ __forceinline__ float get(float x) { return x; }
+  static __device__ __forceinline__ float put(float x) { return x; }
+};
+
+// m * (cos, sin) of position * turn.
+__device__ __forceinline__ void angle(int32_t pos, uint64_t turn, float mult, float sin_mult,
+                                      float& c, float& s) {
+  const uint64_t phase = (uint64_t)(int64_t)pos * turn;
+  const float half_turns = (float)(int32_t)(uint32_t)(phase >> 32) * 4.656612873077393e-10f;  // 2^-31
+  sincospif(half_turns, &s, &c);
+  c *= mult;
+  s *= sin_mult;
+}
+
+// Angles of one thread's unit: V pairs (half pairs: two vectors of V elements,
+// rot/2 apart) or V/2 pairs (interleaved: one vector).
+template <int NP>
+__device__ __forceinline__ void angles(const mkv_rope_plan& plan, int first, int32_t pos, float sign,
+                                       float (&c)[NP], float (&s)[NP]) {
+#pragma unroll
+  for (int i = 0; i < NP; ++i) angle(pos, plan.turn[first + i], plan.mult, plan.mult * sign, c[i], s[i]);
+}
+
+template <int V>
+__device__ __forceinline__ void turn_half(float (&a)[V], float (&b)[V], const float (&c)[V],
+                                          const float (&s)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float x = a[i], y = b[i];
+    a[i] = x * c[i] - y * s[i];
+    b[i] = x * s[i] + y * c[i];
+  }
+}
+template <int V>
+__device__ __forceinline__ void turn_inter(float (&a)[V], const float (&c)[V / 2],
+                                           const float (&s)[V / 2]) {
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    const float x = a[2 * i], y = a[2 * i + 1];
+    a[2 * i] = x * c[i] - y * s[i];
+    a[2 * i + 1] = x * s[i] + y * c[i];
+  }
+}
+
+// i / units and i % units of a 64-bit i; nearly always in 32 bits.
+__device__ __forceinline__ void split_index(int64_t i, int units, int64_t& q, int& r) {
+  if (i < (int64_t)1 << 32) {
+    const uint32_t u = (uint32_t)i;
+    q = u / (uint32_t)units;
+    r = (int)(u - (uint32_t)q * (uint32_t)units);
+  } else {
+    q = i / units;
+    r = (int)(i - q * units);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 16-byte form: a thread takes one unit of one token for `heads_per` heads, two
+// heads at a time so that their loads are in flight together.
+// grid: (ceil(tokens * units / 256), ceil(heads / heads_per), batch)
+// ---------------------------------------------------------------------------
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(RT) rope_vec_kernel(const __grid_constant__ RopeParams p) {
+  using E = Elem<T>;
+  constexpr int V = E::V, NP = HALF ? V : V / 2, HB = 2;
+  int64_t t;
+  int u;
+  const int64_t idx = (int64_t)blockIdx.x * RT + threadIdx.x;
+  split_index(idx, p.units, t, u);
+  if (t >= p.tokens) return;
+  const int b = blockIdx.z;
+  const int h0 = blockIdx.y * p.heads_per, h1 = min(p.heads, h0 + p.heads_per);
+  const T* x = static_cast<const T*>(p.x) + b * p.xs[0] + t * p.xs[1];
+  T* o = static_cast<T*>(p.out) + b * p.os[0] + t * p.os[1];
+  if (u >= p.rot_units) {
+    const int e = p.plan.rot_dim + (u - p.rot_units) * V;
+    for (int h = h0; h < h1; ++h)
+      *reinterpret_cast<Vec16*>(o + h * p.os[2] + e) =
+          *reinterpret_cast<const Vec16*>(x + h * p.xs[2] + e);
+    return;
+  }
+  const int32_t pos = p.pos ? p.pos[b * p.pos_stride + t] : (int32_t)(p.first_pos + t);
+  float c[NP], s[NP];
+  angles<NP>(p.plan, u * NP, pos, p.sign, c, s);
+  const int e0 = u * V, e1 = e0 + (HALF ? p.plan.rot_dim / 2 : 0);
+  for (int h = h0; h < h1; h += HB) {
+    Vec16 a[HB], d[HB];
+#pragma unroll
+    for (int k = 0; k < HB; ++k)
+      if (h + k < h1) {
+        const T* r = x + (h + k) * p.xs[2];
+        a[k] = *reinterpret_cast<const Vec16*>(r + e0);
+        if (HALF) d[k] = *reinterpret_cast<const Vec16*>(r + e1);
+      }
+#pragma unroll
+    for (int k = 0; k < HB; ++k)
+      if (h + k < h1) {
+        T* r = o + (h + k) * p.os[2];
+        float fa[V];
+        E::unpack(a[k], fa);
+        if constexpr (HALF) {
+          float fb[V];
+          E::unpack(d[k], fb);
+          turn_half<V>(fa, fb, c, s);
+          *reinterpret_cast<Vec16*>(r + e1) = E::pack(fb);
+        } else {
+          turn_inter<V>(fa, c, s);
+        }
+        *reinterpret_cast<Vec16*>(r + e0) = E::pack(fa);
+      }
+  }
+}
+
+// Element form for sizes, strides or addresses that 16-byte accesses do not
+// fit: a unit is one pair, or one copied element.
+template <typename T>
+__global__ void __launch_bounds__(RT) rope_elem_kernel(const __grid_constant__ RopeParams p) {
+  using E = Elem<T>;
+  int64_t t;
+  int u;
+  split_index((int64_t)blockIdx.x * RT + threadIdx.x, p.units, t, u);
+  if (t >= p.tokens) return;
+  const int b = blockIdx.z;
+  const int h0 = blockIdx.y * p.heads_per, h1 = min(p.heads, h0 + p.heads_per);
+  const T* x = static_cast<const T*>(p.x) + b * p.xs[0] + t * p.xs[1];
+  T* o = static_cast<T*>(p.out) + b * p.os[0] + t * p.os[1];
+  if (u >= p.rot_units) {
+    const int e = p.plan.rot_dim + (u - p.rot_units);
+    for (int h = h0; h < h1; ++h) o[h * p.os[2] + e] = x[h * p.xs[2] + e];
+    return;
+  }
+  const int32_t pos = p.pos ? p.pos[b * p.pos_stride + t] : (int32_t)(p.first_pos + t);
+  float c, s;
+  angle(pos, p.plan.turn[u], p.plan.mult, p.plan.mult * p.sign, c, s);
+  const int e0 = p.plan.interleaved ? 2 * u : u;
+  const int e1 = p.plan.interleaved ? 2 * u + 1 : u + p.plan.rot_dim / 2;
+  for (int h = h0; h < h1; ++h) {
+    const float a = E::get(x[h * p.xs[2] + e0]), d = E::get(x[h * p.xs[2] + e1]);
+    o[h * p.os[2] + e0] = E::put(a * c - d * s);
+    o[h * p.os[2] + e1] = E::put(a * s + d * c);
+  }
+}
+
+template <typename T>
+cudaError_t launch_rope_t(const RopeParams& p, bool vec, cudaStream_t st) {
+  const int64_t blocks = (p.tokens * p.units + RT - 1) / RT;
+  const dim3 grid((unsigned)blocks, (p.heads + p.heads_per - 1) / p.heads_per, p.batch);
+  if (!vec)
+    rope_elem_kernel<T><<<grid, RT, 0, st>>>(p);
+  else if (p.plan.interleaved)
+    rope_vec_kernel<T, false><<<grid, RT, 0, st>>>(p);
+  else
+    rope_vec_kernel<T, true><<<grid, RT, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// append: rows of new tokens into their pages.  The heads of a token are one
+// list: keys, values, queries; a thread takes one unit of one token for
+// `heads_per` entries of the list.
+// grid: (ceil(n * units / 256), ceil(heads_total / heads_per))
+// ---------------------------------------------------------------------------
+template <typename T, bool E4M3>
+__device__ __forceinline__ void store_row(uint8_t* row, int e, const float (&f)[8], float scale) {
+  if constexpr (E4M3) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] / scale, f[4 * i + 1] / scale),
+                                                   __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] / scale, f[4 * i + 3] / scale),
+                                                   __NV_SATFINITE, __NV_E4M3);
+      w[i] = lo | (hi << 16);
+    }
+    *reinterpret_cast<uint2*>(row + e) = make_uint2(w[0], w[1]);
+  } else {
+    *reinterpret_cast<Vec16*>(row + 2 * e) = Elem<T>::pack(f);
+  }
+}
+
+template <typename T, bool HALF, bool E4M3>
+__global__ void __launch_bounds__(RT) append_rows_kernel(const __grid_constant__ AppendRowsParams p) {
+  using E = Elem<T>;
+  constexpr int V = 8, NP = HALF ? V : V / 2;
+  int64_t t;
+  int u;
+  split_index((int64_t)blockIdx.x * RT + threadIdx.x, p.units, t, u);
+  if (t >= p.a.n) return;
+  const int H = p.c.n_kv_heads, ps = p.c.page_size;
+  const int l0 = blockIdx.y * p.heads_per, l1 = min(p.heads_total, l0 + p.heads_per);
+  const int32_t slot = p.a.slot[t];
+  const int32_t pos = p.a.pos ? p.a.pos[t] : slot;
+  int64_t seq = t;
+  int32_t page = -1;
+  bool live = false;
+  if (l0 < 2 * H && slot >= 0) {
+    if (p.a.seq) seq = p.a.seq[t];
+    live = seq >= 0 && seq < p.c.batch && slot / ps < p.c.max_pages &&
+           !((p.a.acc || p.a.pos_meta) && slot >= p.a.meta_stride);
+    if (live) {
+      page = p.c.page_table[seq * p.c.table_stride + slot / ps];
+      live = page >= 0 && page < p.c.n_pages;
+    }
+    if (!live && p.c.status && u == 0) atomicOr(p.c.status, DEV_ERR_CHECK);
+  }
+  const int rot = p.plan.rot_dim;
+  const bool turns = u < p.rot_units;
+  float c[NP], s[NP];
+  if (turns) angles<NP>(p.plan, u * NP, pos, 1.f, c, s);
+  // elements of the unit: one vector, or two half a rotation apart
+  const int e0 = turns ? u * V : rot + (u - p.rot_units) * V;
+  const int e1 = e0 + rot / 2;
+  const int row_bytes = p.c.head_dim * (E4M3 ? 1 : 2);
+  for (int l = l0; l < l1; ++l) {
+    const int which = l < H ? 0 : l < 2 * H ? 1 : 2;
+    const int h = which == 0 ? l : which == 1 ? l - H : l - 2 * H;
+    if (which < 2 && !live) continue;
+    const int64_t* st = which == 0 ? p.a.k_stride : which == 1 ? p.a.v_stride : p.a.q_stride;
+    const T* x = static_cast<const T*>(which == 0 ? p.a.k : which == 1 ? p.a.v : p.a.q) + t * st[0] + h * st[1];
+    float fa[V], fb[V];
+    E::unpack(*reinterpret_cast<const Vec16*>(x + e0), fa);
+    const bool two = HALF && turns;
+    if (two) E::unpack(*reinterpret_cast<const Vec16*>(x + e1), fb);
+    if (turns && which != 1) {
+      if constexpr (HALF)
+        turn_half<V>(fa, fb, c, s);
+      else
+        turn_inter<V>(fa, c, s);
+    }
+    if (which == 2) {
+      T* o = static_cast<T*>(p.a.q_out) + t * p.a.q_out_stride[0] + h * p.a.q_out_stride[1];
+      *reinterpret_cast<Vec16*>(o + e0) = E::pack(fa);
+      if (two) *reinterpret_cast<Vec16*>(o + e1) = E::pack(fb);
+    } else {
+      uint8_t* pool = static_cast<uint8_t*>(which == 0 ? p.c.k_pages : p.c.v_pages);
+      uint8_t* row = pool + (((int64_t)page * H + h) * ps + slot % ps) * row_bytes;
+      const float* sc = which == 0 ? p.c.k_scale : p.c.v_scale;
+      const float scale = E4M3 && sc ? sc[h] : 1.f;
+      store_row<T, E4M3>(row, e0, fa, scale);
+      if (two) store_row<T, E4M3>(row, e1, fb, scale);
+      if (which == 0 && u == 0) {
+        const int64_t m = (seq * H + h) * p.a.meta_stride + slot;
+        if (p.a.acc) p.a.acc[m] = 0.f;
+        if (p.a.pos_meta) p.a.pos_meta[m] = pos;
+      }
+    }
+  }
+}
+
+template <typename T, bool E4M3>
+cudaError_t launch_append_t(const AppendRowsParams& p, cudaStream_t st) {
+  const int64_t blocks = (p.a.n * p.units + RT - 1) / RT;
+  const dim3 grid((unsigned)blocks, (p.heads_total + p.heads_per - 1) / p.heads_per);
+  if (p.plan.interleaved || p.rot_units == 0)
+    append_rows_kernel<T, false, E4M3><<<grid, RT, 0, st>>>(p);
+  else
+    append_rows_kernel<T, true, E4M3><<<grid, RT, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeParams& p, int dtype, bool vec, cudaStream_t st) {
+  switch (dtype) {
+    case MKV_DT_F16: return launch_rope_t<__half>(p, vec, st);
+    case MKV_DT_BF16: return launch_rope_t<__nv_bfloat16>(p, vec, st);
+    default: return launch_rope_t<float>(p, vec, st);
+  }
+}
+
+cudaError_t launch_append_rows(const AppendRowsParams& p, cudaStream_t st) {
+  const bool e4m3 = p.c.dtype == MKV_DT_E4M3;
+  if (p.a.in_dtype == MKV_DT_F16)
+    return e4m3 ? launch_append_t<__half, true>(p, st) : launch_append_t<__half, false>(p, st);
+  return e4m3 ? launch_append_t<__nv_bfloat16, true>(p, st) : launch_append_t<__nv_bfloat16, false>(p, st);
+}
+
+}  // namespace mkv

@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "mkv_internal.cuh"
+#include "paged_internal.cuh"
 #include "ptx.cuh"
 
 using namespace mkv;
@@ -34,6 +35,30 @@ mkv_status cuda_fail(cudaError_t e, const char* what) {
   } while (0)
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+namespace mkv {
+
+mkv_status set_error(mkv_status s, const char* text) noexcept {
+  try {
+    g_last_error = text;
+  } catch (...) {
+  }
+  return s;
+}
+
+mkv_status set_cuda_error(cudaError_t e, const char* what) noexcept {
+  try {
+    return cuda_fail(e, what);
+  } catch (...) {
+    return MKV_ERR_CUDA;
+  }
+}
+
+}  // namespace mkv
+
+namespace {
 
 struct KernelTimer {
   std::vector<std::pair<cudaEvent_t, cudaEvent_t>> pending;

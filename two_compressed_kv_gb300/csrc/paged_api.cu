@@ -1,0 +1,475 @@
+// Host side of the rotary and paged-cache calls in include/mkv.h: argument
+// checks, workspace layout and launch order.  No state is kept between calls.
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+
+#include "paged_internal.cuh"
+
+using namespace mkv;
+
+namespace {
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr int64_t kMaxGrid = 0x7fffffff;
+
+#define CKP(call)                                              \
+  do {                                                         \
+    cudaError_t e_ = (call);                                   \
+    if (e_ != cudaSuccess) return set_cuda_error(e_, #call);   \
+  } while (0)
+
+mkv_status bad(const char* text) { return set_error(MKV_ERR_INVALID_ARG, text); }
+
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool is16(int dtype) { return dtype == MKV_DT_F16 || dtype == MKV_DT_BF16; }
+int elem_bytes(int dtype) { return dtype == MKV_DT_F32 ? 4 : dtype == MKV_DT_E4M3 ? 1 : 2; }
+
+// SMs of the current device.
+mkv_status sm_count(int* out) {
+  int dev = 0;
+  CKP(cudaGetDevice(&dev));
+  CKP(cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev));
+  return MKV_OK;
+}
+
+// Heads a thread takes so that its angles serve several heads while the grid
+// still has at least `want` threads.
+int heads_per_thread(int64_t threads, int heads, int64_t want, int most) {
+  int per = 1;
+  while (per < most && per < heads && threads * up(heads, 2 * per) >= want) per *= 2;
+  return std::min(per, heads);
+}
+
+const char* check_plan(const mkv_rope_plan* p) {
+  if (p->head_dim < 1 || p->head_dim > 4096 || p->rot_dim < 2 || p->rot_dim % 2 != 0 ||
+      p->rot_dim > p->head_dim || p->rot_dim > 2 * MKV_ROPE_MAX_PAIRS || p->interleaved < 0 ||
+      p->interleaved > 1 || !std::isfinite(p->mult))
+    return "the rope plan was not made by mkv_rope_plan_init";
+  return nullptr;
+}
+
+const char* check_cache(const mkv_paged_cache* c) {
+  if (!c) return "paged cache: NULL view";
+  if (!c->k_pages || !c->v_pages || !c->page_table) return "paged cache: NULL pages or page table";
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages)) return "paged cache: pages must be 16-byte aligned";
+  if (c->dtype != MKV_DT_F16 && c->dtype != MKV_DT_BF16 && c->dtype != MKV_DT_E4M3)
+    return "paged cache: dtype must be F16, BF16 or E4M3";
+  if ((c->k_scale || c->v_scale) && c->dtype != MKV_DT_E4M3) return "paged cache: scales are for E4M3 only";
+  if (c->batch < 1 || c->batch > 65535) return "paged cache: batch must be 1..65535";
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 65535) return "paged cache: n_kv_heads must be 1..65535";
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return "paged cache: head_dim must be 64, 128 or 256";
+  if (c->page_size < 16 || c->page_size > 256 || c->page_size % 16 != 0)
+    return "paged cache: page_size must be a multiple of 16 from 16 to 256";
+  if (c->n_pages < 1 || c->max_pages < 1) return "paged cache: n_pages and max_pages must be >= 1";
+  if ((int64_t)c->max_pages * c->page_size > ((int64_t)1 << 30))
+    return "paged cache: max_pages * page_size must be <= 2^30";
+  if (c->table_stride < c->max_pages) return "paged cache: table_stride must be >= max_pages";
+  if ((int64_t)c->n_pages * c->n_kv_heads > kMaxGrid / (c->page_size / 16))
+    return "paged cache: too many pages (2^31 blocks of 16 rows at most)";
+  return nullptr;
+}
+
+// ---- decode ------------------------------------------------------------------
+
+// With at most this many tokens a sequence, or more sequences than the split
+// kernel's prefix sums hold, one CTA takes a whole stream and no join follows.
+constexpr int64_t kWholeTokens = 1024;
+// Smallest share of a CTA of the split kernel: 8 blocks of 16 tokens.
+constexpr int kMinBlocks = 8;
+
+struct DecodeLayout {
+  bool split;
+  int G;
+  int64_t limit;
+  int64_t score_stride;
+  uint64_t part_o, part_ml, lse2, pre, scores, total;   // byte offsets
+};
+
+const char* check_decode(const mkv_paged_cache* c, const mkv_paged_decode_args* a) {
+  if (const char* e = check_cache(c)) return e;
+  if (!a) return "mkv_paged_decode: NULL arguments";
+  if (a->n_q_heads < 1 || a->n_q_heads % c->n_kv_heads != 0)
+    return "mkv_paged_decode: n_q_heads must be a multiple of n_kv_heads";
+  if (a->n_q_heads / c->n_kv_heads > MAX_G) return "mkv_paged_decode: at most 16 query heads per KV head";
+  if (!is16(a->q_dtype) || (c->dtype != MKV_DT_E4M3 && a->q_dtype != c->dtype))
+    return "mkv_paged_decode: q must be F16 or BF16, of the cache's type unless that is E4M3";
+  if (a->out_dtype != a->q_dtype && a->out_dtype != MKV_DT_F32)
+    return "mkv_paged_decode: out must be of q's type or F32";
+  if (a->max_len < 0 || a->max_len > (int64_t)c->max_pages * c->page_size)
+    return "mkv_paged_decode: max_len must be 0..max_pages * page_size";
+  if (!(a->scale >= 0.f) || std::isinf(a->scale)) return "mkv_paged_decode: scale must be >= 0 and finite";
+  if ((int64_t)c->batch * a->n_q_heads > kMaxGrid) return "mkv_paged_decode: too many heads";
+  return nullptr;
+}
+
+int64_t decode_limit(const mkv_paged_cache* c, const mkv_paged_decode_args* a) {
+  const int64_t cap = (int64_t)c->max_pages * c->page_size;
+  return a->max_len ? std::min(a->max_len, cap) : cap;
+}
+
+DecodeLayout decode_layout(const mkv_paged_cache* c, const mkv_paged_decode_args* a, int sms) {
+  DecodeLayout l;
+  const int64_t g = a->n_q_heads / c->n_kv_heads;
+  const int64_t streams = (int64_t)c->batch * c->n_kv_heads;
+  l.limit = decode_limit(c, a);
+  l.split = l.limit > kWholeTokens && c->batch <= PA_MAX_B;
+  // two CTAs an SM, or one where its ring fills the SM (16-bit rows of 512 bytes)
+  const int ctas = c->head_dim * elem_bytes(c->dtype) >= 512 ? 1 : 2;
+  l.G = (int)std::min<int64_t>((int64_t)sms * ctas,
+                               streams * up(up(l.limit, PA_BLOCK), kMinBlocks));
+  l.score_stride = up(l.limit, 16) * 16;
+  uint64_t at = 0;
+  auto place = [&](uint64_t bytes) {
+    const uint64_t here = at;
+    at += (bytes + 255) & ~(uint64_t)255;
+    return here;
+  };
+  l.part_o = place(l.split ? 2ull * l.G * g * c->head_dim * 4 : 0);
+  l.part_ml = place(l.split ? 2ull * l.G * g * 8 : 0);
+  l.pre = place(l.split ? 8ull * (c->batch + 1) : 0);
+  l.lse2 = place((uint64_t)streams * g * 4);
+  l.scores = place(a->acc ? (uint64_t)streams * g * l.score_stride * 4 : 0);
+  l.total = at;
+  return l;
+}
+
+// ---- evict -------------------------------------------------------------------
+
+const char* check_evict(const mkv_paged_cache* c, const mkv_paged_evict_args* a) {
+  if (const char* e = check_cache(c)) return e;
+  if (!a) return "mkv_paged_evict: NULL arguments";
+  const int64_t cap = (int64_t)c->max_pages * c->page_size;
+  if (a->max_len < 0 || a->max_len > cap) return "mkv_paged_evict: max_len must be 0..max_pages * page_size";
+  const int64_t limit = a->max_len ? a->max_len : cap;
+  if (a->budget < 1) return "mkv_paged_evict: budget must be >= 1";
+  if (a->sink < 0 || a->recent < 0 || (int64_t)a->sink + a->recent > a->budget)
+    return "mkv_paged_evict: sink and recent must be >= 0 and together at most the budget";
+  if (a->meta_stride < limit) return "mkv_paged_evict: meta_stride must be >= max_len";
+  if (a->out_stride < std::min<int64_t>(a->budget, limit))
+    return "mkv_paged_evict: out_stride must be >= min(budget, max_len)";
+  const int64_t streams = (int64_t)c->batch * c->n_kv_heads;
+  if (streams * 8 > kMaxGrid || streams * up(std::min<int64_t>(a->budget, limit), 64) > kMaxGrid)
+    return "mkv_paged_evict: too many streams";
+  return nullptr;
+}
+
+}  // namespace
+
+extern "C" {
+
+mkv_status mkv_rope_plan_init(const mkv_rope_config* cfg, mkv_rope_plan* plan) {
+  if (!cfg || !plan) return bad("mkv_rope_plan_init: NULL argument");
+  const mkv_rope_config& c = *cfg;
+  if (c.head_dim < 1 || c.head_dim > 4096) return bad("mkv_rope_plan_init: head_dim must be 1..4096");
+  if (c.rot_dim < 2 || c.rot_dim % 2 != 0 || c.rot_dim > c.head_dim || c.rot_dim > 2 * MKV_ROPE_MAX_PAIRS)
+    return bad("mkv_rope_plan_init: rot_dim must be even, 2..min(head_dim, 256)");
+  if (c.interleaved < 0 || c.interleaved > 1) return bad("mkv_rope_plan_init: interleaved must be 0 or 1");
+  if (c.scaling < MKV_ROPE_NONE || c.scaling > MKV_ROPE_BANDED) return bad("mkv_rope_plan_init: unknown scaling");
+  if (!(c.base > 1.0) || !std::isfinite(c.base)) return bad("mkv_rope_plan_init: base must be > 1 and finite");
+  if (c.scaling != MKV_ROPE_NONE && (!(c.factor >= 1.0) || !std::isfinite(c.factor)))
+    return bad("mkv_rope_plan_init: factor must be >= 1 and finite");
+  if (c.scaling == MKV_ROPE_NTK && c.rot_dim < 4) return bad("mkv_rope_plan_init: NTK scaling needs rot_dim >= 4");
+  if (c.scaling >= MKV_ROPE_YARN && (!(c.original > 0.0) || !std::isfinite(c.original)))
+    return bad("mkv_rope_plan_init: original must be > 0 and finite");
+  if (c.scaling == MKV_ROPE_YARN &&
+      (!(c.beta_slow > 0.0) || !(c.beta_fast >= c.beta_slow) || !std::isfinite(c.beta_fast)))
+    return bad("mkv_rope_plan_init: beta_fast >= beta_slow > 0");
+  if (c.scaling == MKV_ROPE_BANDED &&
+      (!(c.low_freq > 0.0) || !(c.high_freq > c.low_freq) || !std::isfinite(c.high_freq)))
+    return bad("mkv_rope_plan_init: 0 < low_freq < high_freq");
+  if (!(c.attn_factor >= 0.0) || !std::isfinite((float)c.attn_factor))
+    return bad("mkv_rope_plan_init: attn_factor must be >= 0 and finite");
+
+  std::memset(plan, 0, sizeof(*plan));
+  plan->head_dim = c.head_dim;
+  plan->rot_dim = c.rot_dim;
+  plan->interleaved = c.interleaved;
+  const double n = c.rot_dim;
+  double base = c.base, mult = 1.0;
+  if (c.scaling == MKV_ROPE_NTK) base *= std::pow(c.factor, n / (n - 2.0));
+  if (c.scaling == MKV_ROPE_YARN) mult = 0.1 * std::log(c.factor) + 1.0;
+  if (c.attn_factor > 0.0) mult = c.attn_factor;
+  plan->mult = (float)mult;
+  // YaRN: index of the pair that turns `turns` times over the original context
+  auto pair_of = [&](double turns) {
+    return n * std::log(c.original / (turns * kTwoPi)) / (2.0 * std::log(c.base));
+  };
+  double lo = 0.0, hi = 1.0;
+  if (c.scaling == MKV_ROPE_YARN) {
+    lo = std::max(0.0, std::floor(pair_of(c.beta_fast)));
+    hi = std::min(n - 1.0, std::ceil(pair_of(c.beta_slow)));
+  }
+  for (int i = 0; i < c.rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / n);
+    if (c.scaling == MKV_ROPE_LINEAR) {
+      f /= c.factor;
+    } else if (c.scaling == MKV_ROPE_YARN) {
+      const double ramp = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
+      f = f * (1.0 - ramp) + f / c.factor * ramp;
+    } else if (c.scaling == MKV_ROPE_BANDED) {
+      const double turns = c.original * f / kTwoPi;   // original / wavelength
+      const double keep =
+          std::min(1.0, std::max(0.0, (turns - c.low_freq) / (c.high_freq - c.low_freq)));
+      f = f * keep + f / c.factor * (1.0 - keep);
+    }
+    // f <= 1 radian, so the fraction of a turn is below 2^62 of 2^64
+    plan->turn[i] = (uint64_t)std::llround(std::ldexp(f / kTwoPi, 64));
+  }
+  return MKV_OK;
+}
+
+mkv_status mkv_rope(const mkv_rope_plan* plan, const mkv_rope_args* a, mkv_stream_t stream) {
+  if (!plan || !a) return bad("mkv_rope: NULL plan or arguments");
+  if (const char* e = check_plan(plan)) return bad(e);
+  if (a->batch < 0 || a->heads < 0 || a->tokens < 0) return bad("mkv_rope: negative size");
+  if (a->batch > 65535 || a->heads > 65535) return bad("mkv_rope: batch and heads must be <= 65535");
+  if (a->dtype != MKV_DT_F16 && a->dtype != MKV_DT_BF16 && a->dtype != MKV_DT_F32)
+    return bad("mkv_rope: dtype must be F16, BF16 or F32");
+  if (a->transposed < 0 || a->transposed > 1) return bad("mkv_rope: transposed must be 0 or 1");
+  if (a->batch == 0 || a->heads == 0 || a->tokens == 0) return MKV_OK;
+  if (!a->x || !a->out) return bad("mkv_rope: NULL x or out");
+  if (!a->pos && (int64_t)a->first_pos + a->tokens > (int64_t)1 << 31)
+    return bad("mkv_rope: positions exceed 32 bits");
+  const int64_t extent[3] = {a->batch, a->tokens, a->heads};
+  for (int i = 0; i < 3; ++i) {
+    if (extent[i] > 1 && a->out_stride[i] <= 0) return bad("mkv_rope: out's strides must be positive");
+    if (a->x == a->out && extent[i] > 1 && a->x_stride[i] != a->out_stride[i])
+      return bad("mkv_rope: in place, x and out need the same strides");
+  }
+  const int es = elem_bytes(a->dtype), V = 16 / es;
+  const uintptr_t mask = reinterpret_cast<uintptr_t>(a->x) | reinterpret_cast<uintptr_t>(a->out);
+  if (mask & (uintptr_t)(es - 1)) return bad("mkv_rope: x and out must be aligned to their elements");
+  bool vec = (mask & 15u) == 0 && plan->head_dim % V == 0 &&
+             plan->rot_dim % (plan->interleaved ? V : 2 * V) == 0;
+  for (int i = 0; i < 3; ++i)
+    if (extent[i] > 1 && (a->x_stride[i] % V != 0 || a->out_stride[i] % V != 0)) vec = false;
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.plan = *plan;
+  p.x = a->x;
+  p.out = a->out;
+  p.pos = a->pos;
+  for (int i = 0; i < 3; ++i) p.xs[i] = a->x_stride[i], p.os[i] = a->out_stride[i];
+  p.pos_stride = a->pos_stride;
+  p.tokens = a->tokens;
+  p.batch = a->batch;
+  p.heads = a->heads;
+  p.first_pos = a->first_pos;
+  p.sign = a->transposed ? -1.f : 1.f;
+  const int rest = plan->head_dim - plan->rot_dim;
+  if (vec) {
+    p.rot_units = plan->interleaved ? plan->rot_dim / V : plan->rot_dim / (2 * V);
+    p.units = p.rot_units + rest / V;
+  } else {
+    p.rot_units = plan->rot_dim / 2;
+    p.units = p.rot_units + rest;
+  }
+  if (p.tokens > kMaxGrid / p.units * 256) return bad("mkv_rope: too many tokens");
+  int sms = 0;
+  mkv_status s = sm_count(&sms);
+  if (s != MKV_OK) return s;
+  p.heads_per = heads_per_thread((int64_t)a->batch * a->tokens * p.units, a->heads, (int64_t)sms * 2048, 8);
+  CKP(launch_rope(p, a->dtype, vec, reinterpret_cast<cudaStream_t>(stream)));
+  return MKV_OK;
+}
+
+mkv_status mkv_paged_validate(const mkv_paged_cache* cache) {
+  const char* e = check_cache(cache);
+  return e ? bad(e) : MKV_OK;
+}
+
+mkv_status mkv_paged_append(const mkv_paged_cache* c, const mkv_rope_plan* plan,
+                            const mkv_paged_append_args* a, mkv_stream_t stream) {
+  if (const char* e = check_cache(c)) return bad(e);
+  if (!a) return bad("mkv_paged_append: NULL arguments");
+  if (plan) {
+    if (const char* e = check_plan(plan)) return bad(e);
+    if (plan->head_dim != c->head_dim) return bad("mkv_paged_append: the plan's head_dim is not the cache's");
+    if (plan->rot_dim % (plan->interleaved ? 8 : 16) != 0)
+      return bad("mkv_paged_append: rot_dim must be a multiple of 16 (half pairs) or 8 (interleaved)");
+  }
+  if (a->n < 0) return bad("mkv_paged_append: n must be >= 0");
+  if (!is16(a->in_dtype) || (c->dtype != MKV_DT_E4M3 && a->in_dtype != c->dtype))
+    return bad("mkv_paged_append: inputs must be F16 or BF16, of the cache's type unless that is E4M3");
+  if (a->n == 0) return MKV_OK;
+  if (!a->k || !a->v || !a->slot) return bad("mkv_paged_append: NULL k, v or slot");
+  if (!a->seq && a->n > c->batch) return bad("mkv_paged_append: more tokens than sequences need seq");
+  if (!aligned16(a->k) || !aligned16(a->v) || !aligned16(a->q) || !aligned16(a->q_out))
+    return bad("mkv_paged_append: k, v, q and q_out must be 16-byte aligned");
+  if (a->q && (!a->q_out || a->n_q_heads < 1 || a->n_q_heads > 1 << 20))
+    return bad("mkv_paged_append: q needs q_out and n_q_heads >= 1");
+  for (int i = 0; i < 2; ++i) {
+    if (a->k_stride[i] % 8 != 0 || a->v_stride[i] % 8 != 0 ||
+        (a->q && (a->q_stride[i] % 8 != 0 || a->q_out_stride[i] % 8 != 0)))
+      return bad("mkv_paged_append: strides must be multiples of 8 elements");
+    if (a->q && a->q_out_stride[i] <= 0 && (i == 0 ? a->n : a->n_q_heads) > 1)
+      return bad("mkv_paged_append: q_out's strides must be positive");
+    if (a->q && a->q == a->q_out && a->q_stride[i] != a->q_out_stride[i])
+      return bad("mkv_paged_append: in place, q and q_out need the same strides");
+  }
+  if ((a->acc || a->pos_meta) && a->meta_stride < 1) return bad("mkv_paged_append: meta_stride must be >= 1");
+  AppendRowsParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (plan) p.plan = *plan;
+  p.c = *c;
+  p.a = *a;
+  const int rot = p.plan.rot_dim;
+  p.rot_units = p.plan.interleaved ? rot / 8 : rot / 16;
+  p.units = p.rot_units + (c->head_dim - rot) / 8;
+  p.heads_total = 2 * c->n_kv_heads + (a->q ? a->n_q_heads : 0);
+  if (a->n > kMaxGrid / p.units * 256) return bad("mkv_paged_append: too many tokens");
+  int sms = 0;
+  mkv_status s = sm_count(&sms);
+  if (s != MKV_OK) return s;
+  p.heads_per = heads_per_thread(a->n * p.units, p.heads_total, (int64_t)sms * 2048, 8);
+  while (up(p.heads_total, p.heads_per) > 65535) p.heads_per *= 2;
+  CKP(launch_append_rows(p, reinterpret_cast<cudaStream_t>(stream)));
+  return MKV_OK;
+}
+
+uint64_t mkv_paged_decode_workspace(const mkv_paged_cache* c, const mkv_paged_decode_args* a) {
+  if (const char* e = check_decode(c, a)) {
+    bad(e);
+    return 0;
+  }
+  int sms = 0;
+  if (sm_count(&sms) != MKV_OK) return 0;
+  return decode_layout(c, a, sms).total;
+}
+
+mkv_status mkv_paged_decode(const mkv_paged_cache* c, const mkv_paged_decode_args* a, mkv_stream_t stream) {
+  if (const char* e = check_decode(c, a)) return bad(e);
+  if (!a->q || !a->out || !a->seq_lens) return bad("mkv_paged_decode: NULL q, out or seq_lens");
+  if (!aligned16(a->q) || !aligned16(a->out)) return bad("mkv_paged_decode: q and out must be 16-byte aligned");
+  if (a->q_stride[0] % 8 != 0 || a->q_stride[1] % 8 != 0)
+    return bad("mkv_paged_decode: q's strides must be multiples of 8 elements");
+  if (a->acc && a->acc_stride < decode_limit(c, a)) return bad("mkv_paged_decode: acc_stride must be >= max_len");
+  if (!a->workspace || !aligned16(a->workspace)) return bad("mkv_paged_decode: workspace must be 16-byte aligned");
+  int sms = 0;
+  mkv_status s = sm_count(&sms);
+  if (s != MKV_OK) return s;
+  const DecodeLayout l = decode_layout(c, a, sms);
+  if (a->workspace_bytes < l.total) return bad("mkv_paged_decode: workspace too small");
+  if (a->acc && (int64_t)c->batch * c->n_kv_heads * up(l.limit, 1024) > kMaxGrid)
+    return bad("mkv_paged_decode: too many tokens for accumulated weights");
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  PagedAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.kp = static_cast<const uint8_t*>(c->k_pages);
+  p.vp = static_cast<const uint8_t*>(c->v_pages);
+  p.table = c->page_table;
+  p.ks = c->k_scale;
+  p.vs = c->v_scale;
+  p.status = c->status;
+  p.table_stride = c->table_stride;
+  p.B = c->batch;
+  p.H = c->n_kv_heads;
+  p.g = a->n_q_heads / c->n_kv_heads;
+  p.n_pages = c->n_pages;
+  p.bpp = c->page_size / PA_BLOCK;
+  p.limit = (int)l.limit;
+  p.q = a->q;
+  p.q_sb = a->q_stride[0];
+  p.q_sh = a->q_stride[1];
+  p.q_bf16 = a->q_dtype == MKV_DT_BF16;
+  p.out = a->out;
+  p.out_type = a->out_dtype;
+  p.lse = a->lse;
+  p.lens = a->seq_lens;
+  const double scale = a->scale > 0.f ? (double)a->scale : 1.0 / std::sqrt((double)c->head_dim);
+  p.scale2 = (float)(scale * 1.4426950408889634);
+  p.acc = a->acc;
+  p.acc_stride = a->acc_stride;
+  p.part_o = reinterpret_cast<float*>(ws + l.part_o);
+  p.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
+  p.lse2 = reinterpret_cast<float*>(ws + l.lse2);
+  p.pre = reinterpret_cast<int64_t*>(ws + l.pre);
+  p.scores = a->acc ? reinterpret_cast<float*>(ws + l.scores) : nullptr;
+  p.score_stride = l.score_stride;
+  p.G = l.G;
+  p.min_blocks = kMinBlocks;
+  p.split = l.split;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  switch (c->head_dim) {
+    case 64: CKP(launch_paged_attn_64(p, c->dtype, st)); break;
+    case 128: CKP(launch_paged_attn_128(p, c->dtype, st)); break;
+    default: CKP(launch_paged_attn_256(p, c->dtype, st)); break;
+  }
+  if (l.split) CKP(launch_paged_merge(p, c->head_dim, st));
+  if (a->acc) CKP(launch_paged_weights(p, st));
+  return MKV_OK;
+}
+
+uint64_t mkv_paged_evict_workspace(const mkv_paged_cache* c, const mkv_paged_evict_args* a) {
+  if (const char* e = check_evict(c, a)) {
+    bad(e);
+    return 0;
+  }
+  return (uint64_t)c->batch * c->n_kv_heads * 2 * a->budget * 4;
+}
+
+mkv_status mkv_paged_evict(const mkv_paged_cache* c, const mkv_paged_evict_args* a, mkv_stream_t stream) {
+  if (const char* e = check_evict(c, a)) return bad(e);
+  if (!a->acc || !a->pos || !a->acc_out || !a->pos_out || !a->seq_lens || !a->next_pos || !a->lens_out || !a->src)
+    return bad("mkv_paged_evict: NULL pointer");
+  if ((static_cast<const void*>(a->acc_out) == a->acc || static_cast<const void*>(a->pos_out) == a->pos) &&
+      a->out_stride != a->meta_stride)
+    return bad("mkv_paged_evict: in place, out_stride must be meta_stride");
+  if (!a->workspace || !aligned16(a->workspace)) return bad("mkv_paged_evict: workspace must be 16-byte aligned");
+  if (a->workspace_bytes < mkv_paged_evict_workspace(c, a)) return bad("mkv_paged_evict: workspace too small");
+  int sms = 0;
+  mkv_status s = sm_count(&sms);
+  if (s != MKV_OK) return s;
+  EvictParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.kp = static_cast<uint8_t*>(c->k_pages);
+  p.vp = static_cast<uint8_t*>(c->v_pages);
+  p.table = c->page_table;
+  p.status = c->status;
+  p.table_stride = c->table_stride;
+  p.B = c->batch;
+  p.H = c->n_kv_heads;
+  p.n_pages = c->n_pages;
+  p.ps = c->page_size;
+  p.row_bytes = c->head_dim * elem_bytes(c->dtype);
+  p.limit = (int)(a->max_len ? a->max_len : (int64_t)c->max_pages * c->page_size);
+  p.acc = a->acc;
+  p.pos = a->pos;
+  p.acc_out = a->acc_out;
+  p.pos_out = a->pos_out;
+  p.lens = a->seq_lens;
+  p.next_pos = a->next_pos;
+  p.lens_out = a->lens_out;
+  p.src = a->src;
+  p.meta_stride = a->meta_stride;
+  p.out_stride = a->out_stride;
+  p.budget = a->budget;
+  p.sink = a->sink;
+  p.recent = a->recent;
+  p.lists = static_cast<int32_t*>(a->workspace);
+  // CTAs of a stream: while they fit the SMs and each has 4096 slots or more
+  const int64_t streams = (int64_t)p.B * p.H;
+  p.R = 1;
+  while (p.R < 8 && streams * 2 * p.R <= sms && (int64_t)p.limit >= 8192 * (int64_t)p.R) p.R *= 2;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  CKP(launch_evict_select(p, st));
+  CKP(launch_evict_move(p, st));
+  return MKV_OK;
+}
+
+mkv_status mkv_paged_check(int32_t* status) {
+  if (!status) return bad("mkv_paged_check: NULL status word");
+  CKP(cudaDeviceSynchronize());
+  int32_t v = 0;
+  CKP(cudaMemcpy(&v, status, sizeof(v), cudaMemcpyDeviceToHost));
+  if (v == 0) return MKV_OK;
+  CKP(cudaMemset(status, 0, sizeof(v)));
+  CKP(cudaDeviceSynchronize());
+  return set_error(MKV_ERR_DEVICE_CHECK, "a page, slot, sequence or length lay outside the paged cache");
+}
+
+}  // extern "C"

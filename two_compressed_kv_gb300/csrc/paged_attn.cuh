@@ -1,0 +1,554 @@
+// Attention of one new token per sequence over a paged cache: the streaming
+// kernel, included by one translation unit per head dimension.
+//
+// For a stream (sequence b, KV head h) with g query heads and n cached tokens:
+//   z_it = scale q_i . k_t,  p_it = exp(z_it - max_t z_it),
+//   o_i = sum_t p_it v_t / sum_t p_it,
+// in one pass over the tokens with a running maximum m and sum l: when m grows
+// by d, l and o are multiplied by exp(-d).  Parts of a stream are joined the
+// same way.
+//
+// What bounds it: each key and value row is used once for at most 16 query
+// heads, 2 g operations per byte (fp16), so DRAM bounds it and the kernel is
+// built to keep enough copies in flight with few instructions per byte:
+//   - a warp works alone on blocks of 16 tokens; no barrier between warps until
+//     its part of a stream is done;
+//   - rows come by 16-byte cp.async into a ring in shared memory that each lane
+//     uses as its own queue: a lane copies exactly the pieces that its matrix
+//     fragments need and reads back only those, so the ring needs neither
+//     swizzle nor warp synchronisation and is free of bank conflicts;
+//   - S = Q K^T and O = P V run as m16n8k16 with the query heads as rows.  The
+//     order of the contracted dimension is free, so a lane's 16 bytes of a key
+//     row are two steps' B fragments as they are; value rows of token pairs are
+//     interleaved by byte permutes.  The S accumulator is the P operand as is.
+//     m16n8k16 needs about a sixth of its rate here, far from a bound, and
+//     unlike tcgen05 takes both operands' layout as the loads deliver it.
+//   - P in 16 bits would cost half the output's precision, so it is split into
+//     a high and a low part.  With g <= 8 the low part sits in the operand's
+//     rows 8..15, which are free: no instruction more.  Probabilities carry a
+//     factor 2^12, which cancels, so that small ones stay normal in fp16.
+#pragma once
+
+#include <math_constants.h>
+
+#include "paged_internal.cuh"
+#include "ptx.cuh"
+
+namespace mkv {
+namespace {
+
+constexpr int PA_NW = 4;              // warps per CTA
+
+__device__ __forceinline__ void cpa16_zfill(uint32_t dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cpa8_zfill(uint32_t dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ void mma_bf16(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(pair & 0xffffu), __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+
+// Two probabilities as 16-bit pairs: rounded, and what the rounding left.
+template <bool BF16>
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(a - __low2float(h), b - __high2float(h));
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+  } else {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+  }
+}
+
+
+template <int CT, int D, bool WIDE>
+struct PA {
+  static constexpr int ES = CT == MKV_DT_E4M3 ? 1 : 2;
+  static constexpr bool BF16 = CT == MKV_DT_BF16;
+  static constexpr int ROW = D * ES;                       // bytes of a row
+  static constexpr int KL = ROW / 64;                      // 16-byte pieces of a key row per lane
+  static constexpr int VB = ROW / 8 < 16 ? ROW / 8 : 16;   // bytes of a value piece
+  static constexpr int VL = ROW / (8 * VB);                // value pieces of a row per lane
+  static constexpr int EV = VB / ES;                       // elements of a value piece
+  static constexpr int KS = D / 16;                        // contraction steps of S
+  static constexpr int NT = D / 8;                         // n-tiles of O
+  static constexpr int STAGE = 2 * PA_BLOCK * ROW;         // bytes of one block's keys and values
+  static constexpr int STAGES = STAGE >= 16384 ? 3 : STAGE >= 8192 ? 3 : STAGE >= 4096 ? 6 : 8;
+  static constexpr int HR = WIDE ? 16 : 8;                 // head rows
+  static constexpr int MERGE = PA_NW * HR * (D + 4) * 4;
+  static constexpr int RING = PA_NW * STAGES * STAGE;
+  static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+  static constexpr int CTAS = SMEM <= 100 * 1024 ? 2 : 1;  // per SM
+};
+
+// ---------------------------------------------------------------------------
+// grid: split ? G : streams; block: 4 warps; dynamic smem PA::SMEM
+// ---------------------------------------------------------------------------
+template <int CT, int D, bool WIDE>
+__global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
+    paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
+  using C = PA<CT, D, WIDE>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int64_t pre[PA_MAX_B + 1];        // split: blocks before each sequence
+  __shared__ float sm_m[PA_NW][C::HR], sm_l[PA_NW][C::HR];
+  __shared__ int64_t warp_sum[PA_NW];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = lane >> 2, c = lane & 3;       // fragment row (head) and column group
+  const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::STAGE);
+
+  griddep_launch();                            // the join's prologue may start; it waits for the end
+  // this CTA's range of blocks, counted over all streams
+  int64_t g0 = 0, g1 = 0, at = 0;
+  int b = 0;
+  if (p.split) {
+    // prefix sums of the sequences' blocks: each thread a run of sequences
+    const int run = (p.B + PA_NW * 32 - 1) / (PA_NW * 32);
+    int64_t sum = 0;
+    for (int k = 0; k < run; ++k) {
+      const int i = tid * run + k;
+      if (i < p.B) sum += (int64_t)((paged_len(p, i) + PA_BLOCK - 1) / PA_BLOCK) * p.H;
+    }
+    int64_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(~0u, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int64_t base = inc - sum;
+    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    for (int k = 0; k < run; ++k) {
+      const int i = tid * run + k;
+      if (i < p.B) {
+        pre[i] = base;
+        base += (int64_t)((paged_len(p, i) + PA_BLOCK - 1) / PA_BLOCK) * p.H;
+      }
+      if (i == p.B - 1) pre[p.B] = base;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int i = tid; i <= p.B; i += PA_NW * 32) p.pre[i] = pre[i];   // for the join
+    const int64_t total = pre[p.B];
+    int64_t per = (total + p.G - 1) / p.G;
+    if (per < p.min_blocks) per = p.min_blocks;
+    g0 = (int64_t)blockIdx.x * per;
+    g1 = min(total, g0 + per);
+    if (g0 >= g1) return;
+    int lo = 0, hi = p.B - 1;                  // last b with pre[b] <= g0 that has blocks
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= g0) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    at = g0;
+  }
+
+  while (true) {
+    // next piece: blocks [j0, j1) of stream (b, h)
+    int h, j0, j1, n, nb;
+    if (p.split) {
+      if (at >= g1) break;
+      while (pre[b + 1] <= at) ++b;
+      n = paged_len(p, b);
+      nb = (n + PA_BLOCK - 1) / PA_BLOCK;
+      const int64_t off = at - pre[b];
+      h = (int)(off / nb);
+      j0 = (int)(off - (int64_t)h * nb);
+      j1 = (int)min((int64_t)nb, j0 + (g1 - at));
+    } else {
+      b = blockIdx.x / p.H;
+      h = blockIdx.x - b * p.H;
+      n = paged_len(p, b);
+      nb = (n + PA_BLOCK - 1) / PA_BLOCK;
+      j0 = 0;
+      j1 = nb;
+      if (h == 0 && tid == 0 && p.status && p.lens[b] != n) atomicOr(p.status, DEV_ERR_CHECK);
+    }
+    if (p.split && h == 0 && j0 == 0 && tid == 0 && p.status && p.lens[b] != n)
+      atomicOr(p.status, DEV_ERR_CHECK);
+    const int64_t stream = (int64_t)b * p.H + h;
+
+    // Q fragments: row r is query head h * g + r (and r + 8), zero past g.
+    // 8-bit caches: both fp16 and bf16 queries go to fp16, scaled by a power of
+    // two so that the head's largest element lies in [1, 2).
+    uint32_t qa[C::KS][WIDE ? 4 : 2];
+    float sc[WIDE ? 2 : 1];
+#pragma unroll
+    for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
+      const int i = r + 8 * w;
+      const bool live = i < p.g;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)b * p.q_sb +
+                          (int64_t)(h * p.g + (live ? i : 0)) * p.q_sh;
+      sc[w] = p.scale2 * (CT == MKV_DT_E4M3 && p.ks ? p.ks[h] : 1.f);
+      if constexpr (CT == MKV_DT_E4M3) {
+        // element 64 i + 16 c + 4 j + {0, 1}, {2, 3} for step 4 i + j
+        float f[C::KS][4];
+        float top = 0.f;
+#pragma unroll
+        for (int s = 0; s < C::KS; ++s) {
+          const uint2 v = *reinterpret_cast<const uint2*>(q + (s / 4) * 64 + 16 * c + 4 * (s % 4));
+          const uint32_t x[2] = {v.x, v.y};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint16_t u = (uint16_t)(x[k / 2] >> (16 * (k % 2)));
+            f[s][k] = p.q_bf16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
+            top = fmaxf(top, fabsf(f[s][k]));
+          }
+        }
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        // 2^e <= top < 2^(e+1); a zero, tiny or infinite head is left as it is
+        int e = (int)(__float_as_uint(top) >> 23) - 127;
+        if (e < -100 || e > 126) e = 0;
+        const float f1 = __uint_as_float((uint32_t)(127 - e) << 23);
+        sc[w] *= __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int s = 0; s < C::KS; ++s) {
+          const __half2 a = __floats2half2_rn(f[s][0] * f1, f[s][1] * f1);
+          const __half2 d = __floats2half2_rn(f[s][2] * f1, f[s][3] * f1);
+          qa[s][w] = live ? *reinterpret_cast<const uint32_t*>(&a) : 0u;
+          qa[s][(WIDE ? 2 : 1) + w] = live ? *reinterpret_cast<const uint32_t*>(&d) : 0u;
+        }
+      } else {
+        // element 32 i + 8 c + 4 j + {0, 1}, {2, 3} for step 2 i + j
+#pragma unroll
+        for (int i2 = 0; i2 < C::KS / 2; ++i2) {
+          const uint4 v = *reinterpret_cast<const uint4*>(q + 32 * i2 + 8 * c);
+          constexpr int hi = WIDE ? 2 : 1;
+          qa[2 * i2][w] = live ? v.x : 0u;
+          qa[2 * i2][hi + w] = live ? v.y : 0u;
+          qa[2 * i2 + 1][w] = live ? v.z : 0u;
+          qa[2 * i2 + 1][hi + w] = live ? v.w : 0u;
+        }
+      }
+    }
+
+    float o[C::NT][4];
+#pragma unroll
+    for (int i = 0; i < C::NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m[WIDE ? 2 : 1], l[WIDE ? 2 : 1];
+#pragma unroll
+    for (int w = 0; w < (WIDE ? 2 : 1); ++w) m[w] = -CUDART_INF_F, l[w] = 0.f;
+
+    // this warp's blocks: j0 + warp, + 4, ...; lane i holds the pool row of
+    // the i-th of the next 32 (in blocks of 16 rows; -1: page outside the cache)
+    const int count = max(0, (j1 - j0 - warp + PA_NW - 1) / PA_NW);
+    auto entries = [&](int first) {
+      const int j = j0 + warp + PA_NW * (first + lane);
+      int e = -1;
+      if (first + lane < count) {
+        const int pg = j / p.bpp;
+        const int page = p.table[(int64_t)b * p.table_stride + pg];
+        if (page >= 0 && page < p.n_pages)
+          e = (page * p.H + h) * p.bpp + (j - pg * p.bpp);
+        else if (p.status)
+          atomicOr(p.status, DEV_ERR_CHECK);
+      }
+      return e;
+    };
+    int ent = entries(0), ent_next = entries(32);
+    int valid_bits = 0;                        // bit of a ring slot: its page is there
+    auto issue = [&](int i, int slot) {
+      if (i < count) {
+        if ((i & 31) == 0 && i > 0) {
+          ent = ent_next;
+          ent_next = entries(i + 32);
+        }
+        const int e = __shfl_sync(~0u, ent, i & 31);
+        const int rows = e < 0 ? 0 : n - (j0 + warp + PA_NW * i) * PA_BLOCK;
+        valid_bits = e < 0 ? valid_bits & ~(1 << slot) : valid_bits | (1 << slot);
+        const int64_t off = (int64_t)max(e, 0) * (PA_BLOCK * C::ROW);
+        const uint32_t dst = ring + slot * C::STAGE;
+        const uint8_t* k = p.kp + off + r * C::ROW + 16 * c;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int x = 0; x < C::KL; ++x)
+            cpa16_zfill(dst + (t * C::KL + x) * 512 + lane * 16, k + 8 * t * C::ROW + 64 * x,
+                        8 * t + r < rows ? 16u : 0u);
+        const uint8_t* v = p.vp + off + C::VB * r;
+        const uint32_t dv = dst + PA_BLOCK * C::ROW + lane * C::VB;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int row = 2 * c + (t & 1) + 8 * (t >> 1);
+#pragma unroll
+          for (int x = 0; x < C::VL; ++x) {
+            const uint8_t* src = v + row * C::ROW + x * 8 * C::VB;
+            const uint32_t to = dv + (t * C::VL + x) * 32 * C::VB;
+            if constexpr (C::VB == 16)
+              cpa16_zfill(to, src, row < rows ? 16u : 0u);
+            else
+              cpa8_zfill(to, src, row < rows ? 8u : 0u);
+          }
+        }
+      }
+      cpa_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < C::STAGES - 1; ++s) issue(s, s);
+    float* score_row = p.scores ? p.scores + (stream * p.g + r) * p.score_stride : nullptr;
+
+    int slot = 0;
+    for (int i = 0; i < count; ++i) {
+      issue(i + C::STAGES - 1, slot == 0 ? C::STAGES - 1 : slot - 1);
+      cpa_wait<C::STAGES - 1>();
+      const uint32_t src = ring + slot * C::STAGE;
+      float s[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+        for (int x = 0; x < C::KL; ++x) {
+          const uint4 v = lds16(src + (t * C::KL + x) * 512 + lane * 16);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          constexpr int PER = CT == MKV_DT_E4M3 ? 4 : 2;   // steps in a piece
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            const int ks = x * PER + k;
+            uint32_t a[4];
+            if constexpr (WIDE) {
+              a[0] = qa[ks][0], a[1] = qa[ks][1], a[2] = qa[ks][2], a[3] = qa[ks][3];
+            } else {
+              a[0] = qa[ks][0], a[1] = 0u, a[2] = qa[ks][1], a[3] = 0u;
+            }
+            if constexpr (CT == MKV_DT_E4M3)
+              mma16816(s[t], a, e4m3x2_to_f16x2(w[k]), e4m3x2_to_f16x2(w[k] >> 16));
+            else if constexpr (C::BF16)
+              mma_bf16(s[t], a, w[2 * k], w[2 * k + 1]);
+            else
+              mma16816(s[t], a, w[2 * k], w[2 * k + 1]);
+          }
+        }
+      }
+      const int tok = (j0 + warp + PA_NW * i) * PA_BLOCK + 2 * c;
+      const int left = (valid_bits >> slot & 1) ? n : 0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int k = 0; k < (WIDE ? 4 : 2); ++k) {
+          s[t][k] *= sc[k / 2];
+          if (tok + 8 * t + (k & 1) >= left) s[t][k] = -CUDART_INF_F;
+        }
+      if (p.scores) {
+#pragma unroll
+        for (int w = 0; w < (WIDE ? 2 : 1); ++w)
+          if (r + 8 * w < p.g) {
+            float* to = score_row + 8 * w * p.score_stride + tok;
+            *reinterpret_cast<float2*>(to) = make_float2(s[0][2 * w], s[0][2 * w + 1]);
+            *reinterpret_cast<float2*>(to + 8) = make_float2(s[1][2 * w], s[1][2 * w + 1]);
+          }
+      }
+      // running maximum and sum
+      float mref[WIDE ? 2 : 1];
+      bool grows = false;
+      float mn[WIDE ? 2 : 1];
+#pragma unroll
+      for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
+        float x = fmaxf(fmaxf(s[0][2 * w], s[0][2 * w + 1]), fmaxf(s[1][2 * w], s[1][2 * w + 1]));
+        x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
+        mn[w] = fmaxf(m[w], x);
+        grows |= mn[w] > m[w];
+        mref[w] = (mn[w] == -CUDART_INF_F ? 0.f : mn[w]) - PA_BIAS;
+      }
+      if (__any_sync(~0u, grows)) {
+        float f[WIDE ? 2 : 1];
+#pragma unroll
+        for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
+          f[w] = mn[w] > m[w] ? exp2f(m[w] - mn[w]) : 1.f;
+          l[w] *= f[w];
+          m[w] = mn[w];
+        }
+#pragma unroll
+        for (int x = 0; x < C::NT; ++x) {
+          o[x][0] *= f[0], o[x][1] *= f[0];
+          o[x][2] *= f[WIDE ? 1 : 0], o[x][3] *= f[WIDE ? 1 : 0];
+        }
+      }
+      uint32_t ph[WIDE ? 4 : 2], pl[WIDE ? 4 : 2];   // [token half][row half]
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
+          const float a = exp2f(s[t][2 * w] - mref[w]), d = exp2f(s[t][2 * w + 1] - mref[w]);
+          l[w] += a + d;
+          split_pair<C::BF16>(a, d, ph[t * (WIDE ? 2 : 1) + w], pl[t * (WIDE ? 2 : 1) + w]);
+        }
+      uint32_t pa[4], pb[4];
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) pa[k] = ph[k], pb[k] = pl[k];
+      } else {
+        pa[0] = ph[0], pa[1] = pl[0], pa[2] = ph[1], pa[3] = pl[1];
+      }
+      const uint32_t sv = src + PA_BLOCK * C::ROW + lane * C::VB;
+      auto pv = [&](int nt, uint32_t b0, uint32_t b1) {
+        if constexpr (C::BF16) {
+          mma_bf16(o[nt], pa, b0, b1);
+          if constexpr (WIDE) mma_bf16(o[nt], pb, b0, b1);
+        } else {
+          mma16816(o[nt], pa, b0, b1);
+          if constexpr (WIDE) mma16816(o[nt], pb, b0, b1);
+        }
+      };
+#pragma unroll
+      for (int x = 0; x < C::VL; ++x) {
+        uint32_t v[4][C::VB / 4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t from = sv + (t * C::VL + x) * 32 * C::VB;
+          if constexpr (C::VB == 16) {
+            const uint4 y = lds16(from);
+            v[t][0] = y.x, v[t][1] = y.y, v[t][2] = y.z, v[t][3] = y.w;
+          } else {
+            const uint2 y = lds8(from);
+            v[t][0] = y.x, v[t][1] = y.y;
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < C::VB / 4; ++y) {
+          if constexpr (CT == MKV_DT_E4M3) {
+            const uint32_t a0 = __byte_perm(v[0][y], v[1][y], 0x5140), a1 = __byte_perm(v[0][y], v[1][y], 0x7362);
+            const uint32_t d0 = __byte_perm(v[2][y], v[3][y], 0x5140), d1 = __byte_perm(v[2][y], v[3][y], 0x7362);
+            const int nt = x * C::EV + 4 * y;
+            pv(nt, e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(d0));
+            pv(nt + 1, e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(d0 >> 16));
+            pv(nt + 2, e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(d1));
+            pv(nt + 3, e4m3x2_to_f16x2(a1 >> 16), e4m3x2_to_f16x2(d1 >> 16));
+          } else {
+            const int nt = x * C::EV + 2 * y;
+            pv(nt, __byte_perm(v[0][y], v[1][y], 0x5410), __byte_perm(v[2][y], v[3][y], 0x5410));
+            pv(nt + 1, __byte_perm(v[0][y], v[1][y], 0x7632), __byte_perm(v[2][y], v[3][y], 0x7632));
+          }
+        }
+      }
+      slot = slot + 1 == C::STAGES ? 0 : slot + 1;
+    }
+
+    // join the warps: the ring is drained and becomes [warp][head][D + 4]
+    cpa_wait<0>();
+#pragma unroll
+    for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
+      l[w] += __shfl_xor_sync(~0u, l[w], 1);
+      l[w] += __shfl_xor_sync(~0u, l[w], 2);
+      if (c == 0) sm_m[warp][r + 8 * w] = m[w], sm_l[warp][r + 8 * w] = l[w];
+    }
+    __syncthreads();
+    float* mg = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
+      const int head = r + 8 * w;
+      float top = sm_m[0][head];
+#pragma unroll
+      for (int k = 1; k < PA_NW; ++k) top = fmaxf(top, sm_m[k][head]);
+      const float f = m[w] == -CUDART_INF_F ? 0.f : exp2f(m[w] - top);
+      float* to = mg + (warp * C::HR + head) * (D + 4);
+#pragma unroll
+      for (int x = 0; x < C::NT / C::EV; ++x)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < C::EV; e += 4) {
+            float4 v;
+            float* vv = &v.x;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float* a = o[x * C::EV + e + y];
+              // g <= 8: rows 8..15 hold the low parts of the same heads.  A part
+              // without a live token stays zero even where f is.
+              const float t = WIDE ? a[2 * w + k] : a[k] + a[2 + k];
+              vv[y] = m[w] == -CUDART_INF_F ? 0.f : t * f;
+            }
+            *reinterpret_cast<float4*>(to + x * 8 * C::EV + (2 * c + k) * C::EV + e) = v;
+          }
+    }
+    __syncthreads();
+    const bool whole = j0 == 0 && j1 == nb;
+    const float vs = CT == MKV_DT_E4M3 && p.vs ? p.vs[h] : 1.f;
+    const int64_t part = 2 * (int64_t)blockIdx.x + (j0 == 0 ? 1 : 0);
+    for (int e = tid; e < p.g * (D / 4); e += PA_NW * 32) {
+      const int head = e / (D / 4), d = (e - head * (D / 4)) * 4;
+      float top = sm_m[0][head];
+#pragma unroll
+      for (int k = 1; k < PA_NW; ++k) top = fmaxf(top, sm_m[k][head]);
+      float sum = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < PA_NW; ++k) {
+        const float mk = sm_m[k][head];
+        sum += mk == -CUDART_INF_F ? sm_l[k][head] : sm_l[k][head] * exp2f(mk - top);
+        const float4 v = *reinterpret_cast<const float4*>(mg + (k * C::HR + head) * (D + 4) + d);
+        a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+      }
+      a.x *= vs, a.y *= vs, a.z *= vs, a.w *= vs;
+      if (whole) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int64_t row = stream * p.g + head;
+        store_out4(p, row * D + d, a, inv);
+        if (d == 0) {
+          const float z = sum == 0.f ? -CUDART_INF_F : top - PA_BIAS + log2f(sum);
+          if (p.lse) p.lse[row] = z * 0.6931471805599453f;
+          p.lse2[row] = z;
+        }
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + (part * p.g + head) * D + d) = a;
+        if (d == 0) {
+          p.part_ml[(part * p.g + head) * 2] = top;
+          p.part_ml[(part * p.g + head) * 2 + 1] = sum;
+        }
+      }
+    }
+    if (!p.split) break;
+    at += j1 - j0;
+    if (at < g1) __syncthreads();   // the merge area becomes the ring again
+  }
+}
+
+template <int CT, int D, bool WIDE>
+cudaError_t launch_pa(const PagedAttnParams& p, cudaStream_t st) {
+  using C = PA<CT, D, WIDE>;
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<CT, D, WIDE>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = p.split ? p.G : (int64_t)p.B * p.H;
+  paged_attn_kernel<CT, D, WIDE><<<(unsigned)grid, PA_NW * 32, C::SMEM, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_pa_d(const PagedAttnParams& p, int cache_type, cudaStream_t st) {
+  const bool wide = p.g > 8;
+  switch (cache_type) {
+    case MKV_DT_F16: return wide ? launch_pa<MKV_DT_F16, D, true>(p, st) : launch_pa<MKV_DT_F16, D, false>(p, st);
+    case MKV_DT_BF16: return wide ? launch_pa<MKV_DT_BF16, D, true>(p, st) : launch_pa<MKV_DT_BF16, D, false>(p, st);
+    default: return wide ? launch_pa<MKV_DT_E4M3, D, true>(p, st) : launch_pa<MKV_DT_E4M3, D, false>(p, st);
+  }
+}
+
+}  // namespace
+}  // namespace mkv

@@ -1,0 +1,136 @@
+// Internal declarations of the rotary and paged-cache operators.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mkv.h"
+#include "mkv_internal.cuh"
+
+namespace mkv {
+
+// Sets the text that mkv_last_error_string returns; `s` is passed through.
+mkv_status set_error(mkv_status s, const char* text) noexcept;
+mkv_status set_cuda_error(cudaError_t e, const char* what) noexcept;
+
+// ---------------------------------------------------------------------------
+// rope and append
+// ---------------------------------------------------------------------------
+struct RopeParams {
+  mkv_rope_plan plan;
+  const void* x;
+  void* out;
+  const int32_t* pos;
+  int64_t xs[3], os[3], pos_stride;
+  int64_t tokens;
+  int batch, heads;
+  int first_pos;
+  int units;          // per head: work of one thread (a vector pair, a vector, a pair or an element)
+  int rot_units;      // those that rotate; the rest copy
+  int heads_per;      // heads a thread handles
+  float sign;         // -1: transposed
+};
+cudaError_t launch_rope(const RopeParams& p, int dtype, bool vec, cudaStream_t st);
+
+struct AppendRowsParams {
+  mkv_rope_plan plan;             // rot_dim 0: no rotation
+  mkv_paged_cache c;
+  mkv_paged_append_args a;
+  int units, rot_units, heads_per, heads_total;
+};
+cudaError_t launch_append_rows(const AppendRowsParams& p, cudaStream_t st);
+
+// ---------------------------------------------------------------------------
+// attention over the paged cache
+// ---------------------------------------------------------------------------
+constexpr int PA_BLOCK = 16;      // tokens per block: the unit of work; a block lies in one page
+constexpr int PA_MAX_B = 1024;    // sequences whose prefix sums fit the split kernel
+constexpr float PA_BIAS = 12.f;   // probabilities carry a factor 2^12 until the division by their sum
+
+struct PagedAttnParams {
+  const uint8_t *kp, *vp;
+  const int32_t* table;
+  const float *ks, *vs;
+  int32_t* status;
+  int64_t table_stride;
+  int B, H, g, n_pages, bpp;      // bpp: blocks per page
+  int limit;                      // largest length: min(max_len, max_pages * page_size)
+  const void* q;
+  int64_t q_sb, q_sh;
+  int q_bf16;
+  void* out;
+  int out_type;                   // MKV_DT_*
+  float* lse;
+  const int32_t* lens;
+  float scale2;                   // scale * log2(e)
+  float* acc;
+  int64_t acc_stride;
+  // workspace
+  float* part_o;                  // [2 G][g][D]: unnormalised sums of split streams
+  float* part_ml;                 // [2 G][g][2]: running maximum (log2 domain) and sum
+  float* lse2;                    // [B H g]: log2 of the sum of exp2(scores)
+  int64_t* pre;                   // [B + 1]: blocks before each sequence (split)
+  float* scores;                  // [B H g][score_stride], log2 domain; only with acc
+  int64_t score_stride;
+  int G;                          // CTAs of the split kernel
+  int min_blocks;                 // smallest share of a CTA, in blocks
+  int split;                      // 0: one CTA per stream
+};
+
+// Cached tokens of sequence b as the kernels count them.
+__device__ __forceinline__ int paged_len(const PagedAttnParams& p, int b) {
+  const int n = p.lens[b];
+  return n < 0 ? 0 : min(n, p.limit);
+}
+
+// Four outputs a * f from element `at` on, rounded to the output's type.
+__device__ __forceinline__ void store_out4(const PagedAttnParams& p, int64_t at, float4 a, float f) {
+  a.x *= f, a.y *= f, a.z *= f, a.w *= f;
+  if (p.out_type == MKV_DT_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = a;
+  } else if (p.out_type == MKV_DT_BF16) {
+    __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at);
+    o[0] = __floats2bfloat162_rn(a.x, a.y);
+    o[1] = __floats2bfloat162_rn(a.z, a.w);
+  } else {
+    __half2* o = reinterpret_cast<__half2*>(static_cast<__half*>(p.out) + at);
+    o[0] = __floats2half2_rn(a.x, a.y);
+    o[1] = __floats2half2_rn(a.z, a.w);
+  }
+}
+
+// g <= 8 and g <= 16 variants per head dim (one translation unit each)
+cudaError_t launch_paged_attn_64(const PagedAttnParams& p, int cache_type, cudaStream_t st);
+cudaError_t launch_paged_attn_128(const PagedAttnParams& p, int cache_type, cudaStream_t st);
+cudaError_t launch_paged_attn_256(const PagedAttnParams& p, int cache_type, cudaStream_t st);
+cudaError_t launch_paged_merge(const PagedAttnParams& p, int D, cudaStream_t st);
+cudaError_t launch_paged_weights(const PagedAttnParams& p, cudaStream_t st);
+
+// ---------------------------------------------------------------------------
+// eviction
+// ---------------------------------------------------------------------------
+struct EvictParams {
+  uint8_t *kp, *vp;
+  const int32_t* table;
+  int32_t* status;
+  int64_t table_stride;
+  int B, H, n_pages, ps, row_bytes;
+  int limit;
+  const float* acc;
+  const int32_t* pos;
+  float* acc_out;
+  int32_t* pos_out;
+  const int32_t *lens, *next_pos;
+  int32_t *lens_out, *src;
+  int64_t meta_stride, out_stride;
+  int budget, sink, recent;
+  int32_t* lists;                 // workspace: [B H][2][budget] movers, then holes
+  int R;                          // CTAs (one cluster) per stream
+};
+cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t st);
+cudaError_t launch_evict_move(const EvictParams& p, cudaStream_t st);
+
+}  // namespace mkv

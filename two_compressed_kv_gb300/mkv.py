@@ -60,11 +60,68 @@ class mkv_stats_t(Structure):
 HEADER_NP = np.dtype([("off16", "<u4"), ("strategy", "u1"), ("rsv", "u1"), ("rows", "<u2")])
 
 
+MKV_DT_F16, MKV_DT_BF16, MKV_DT_F32, MKV_DT_E4M3 = range(4)
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
+MKV_ROPE_MAX_PAIRS = 128
+
+
+class mkv_rope_config(Structure):
+    _fields_ = [("head_dim", c_int32), ("rot_dim", c_int32), ("interleaved", c_int32),
+                ("scaling", c_int32), ("base", c_double), ("factor", c_double),
+                ("original", c_double), ("low_freq", c_double), ("high_freq", c_double),
+                ("beta_fast", c_double), ("beta_slow", c_double), ("attn_factor", c_double)]
+
+
+class MkvRopePlan(Structure):
+    """A rotation ready to use (mkv_rope_plan_init): plain host data."""
+    _fields_ = [("turn", c_uint64 * MKV_ROPE_MAX_PAIRS), ("mult", c_float),
+                ("head_dim", c_int32), ("rot_dim", c_int32), ("interleaved", c_int32)]
+
+
+class mkv_rope_args(Structure):
+    _fields_ = [("x", c_void_p), ("out", c_void_p), ("pos", c_void_p), ("x_stride", c_int64 * 3),
+                ("out_stride", c_int64 * 3), ("pos_stride", c_int64), ("tokens", c_int64),
+                ("batch", c_int32), ("heads", c_int32), ("dtype", c_int32),
+                ("first_pos", c_int32), ("transposed", c_int32)]
+
+
+class mkv_paged_cache(Structure):
+    _fields_ = [("k_pages", c_void_p), ("v_pages", c_void_p), ("page_table", c_void_p),
+                ("k_scale", c_void_p), ("v_scale", c_void_p), ("status", c_void_p),
+                ("table_stride", c_int64), ("dtype", c_int32), ("batch", c_int32),
+                ("n_kv_heads", c_int32), ("head_dim", c_int32), ("page_size", c_int32),
+                ("n_pages", c_int32), ("max_pages", c_int32)]
+
+
+class mkv_paged_append_args(Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("q", c_void_p), ("q_out", c_void_p),
+                ("seq", c_void_p), ("slot", c_void_p), ("pos", c_void_p), ("acc", c_void_p),
+                ("pos_meta", c_void_p), ("k_stride", c_int64 * 2), ("v_stride", c_int64 * 2),
+                ("q_stride", c_int64 * 2), ("q_out_stride", c_int64 * 2), ("meta_stride", c_int64),
+                ("n", c_int64), ("n_q_heads", c_int32), ("in_dtype", c_int32)]
+
+
+class mkv_paged_decode_args(Structure):
+    _fields_ = [("q", c_void_p), ("out", c_void_p), ("lse", c_void_p), ("seq_lens", c_void_p),
+                ("acc", c_void_p), ("workspace", c_void_p), ("workspace_bytes", c_uint64),
+                ("q_stride", c_int64 * 2), ("acc_stride", c_int64), ("max_len", c_int64),
+                ("n_q_heads", c_int32), ("q_dtype", c_int32), ("out_dtype", c_int32),
+                ("scale", c_float)]
+
+
+class mkv_paged_evict_args(Structure):
+    _fields_ = [("acc", c_void_p), ("pos", c_void_p), ("acc_out", c_void_p),
+                ("pos_out", c_void_p), ("seq_lens", c_void_p), ("next_pos", c_void_p),
+                ("lens_out", c_void_p), ("src", c_void_p), ("workspace", c_void_p),
+                ("workspace_bytes", c_uint64), ("meta_stride", c_int64), ("out_stride", c_int64),
+                ("max_len", c_int64), ("budget", c_int32), ("sink", c_int32), ("recent", c_int32)]
+
+
 class MkvError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
         msg = f"{where}: {mkv_status_string(status)}"
-        if status == MKV_ERR_CUDA or status == MKV_ERR_OOM:
+        if status in (MKV_ERR_CUDA, MKV_ERR_OOM) or where.startswith(("mkv_rope", "mkv_paged")):
             msg += f" ({mkv_last_error_string()})"
         super().__init__(msg)
 
@@ -94,6 +151,15 @@ def _load():
         "mkv_set_flags": (c_int, [P, c_uint32]),
         "mkv_debug_set_pdl": (c_int, [P, c_uint32]),
         "mkv_debug_set_check_extent": (c_int, [P, c_uint64]),
+        "mkv_rope_plan_init": (c_int, [P, P]),
+        "mkv_rope": (c_int, [P, P, P]),
+        "mkv_paged_validate": (c_int, [P]),
+        "mkv_paged_append": (c_int, [P, P, P, P]),
+        "mkv_paged_decode_workspace": (c_uint64, [P, P]),
+        "mkv_paged_decode": (c_int, [P, P, P]),
+        "mkv_paged_evict_workspace": (c_uint64, [P, P]),
+        "mkv_paged_evict": (c_int, [P, P, P]),
+        "mkv_paged_check": (c_int, [P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -322,6 +388,339 @@ def mkv_basis_static(k, v, basis, eigvals, stream=None) -> None:
     with torch.cuda.device(k.device):
         _check(_lib.mkv_basis_static(pk, pv, B, H, T, pb, pe, _stream_ptr(stream, k.device)),
                "mkv_basis_static")
+
+
+# ---- rotary positions and the paged cache ----------------------------------------------------
+
+_DTYPES = {}
+
+
+def _dt(t, name, allowed):
+    """MKV_DT_* of a tensor whose type must be one of `allowed`."""
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float16: MKV_DT_F16, torch.bfloat16: MKV_DT_BF16,
+                        torch.float32: MKV_DT_F32, torch.float8_e4m3fn: MKV_DT_E4M3})
+    d = _DTYPES.get(t.dtype)
+    if d not in allowed:
+        raise TypeError(f"{name} has type {t.dtype}, which the call does not take")
+    return d
+
+
+def _vec(t, name, dev, shape=None):
+    """Address of a CUDA tensor on `dev` whose last dimension is contiguous."""
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _flat(t, name, dev, dtype, shape):
+    """Address of a contiguous CUDA tensor of the given type and shape on `dev`."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _cuda(t, name):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return t.device
+
+
+def _launch(fn, where, dev, stream, *args):
+    """fn(*args, stream) with the tensors' device current."""
+    import torch
+    sp = _stream_ptr(stream, dev)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, sp)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, sp)
+    if st != MKV_OK:
+        raise MkvError(st, where)
+
+
+def _new(shape, dtype, dev, stream):
+    """A tensor from torch's caching allocator whose memory belongs to the stream that uses it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _scratch(nbytes, dev, stream):
+    """A workspace for one call on `stream`."""
+    import torch
+    return _new(nbytes, torch.uint8, dev, stream)
+
+
+def mkv_rope_plan(head_dim, rot_dim=None, base=10000.0, interleaved=False, scaling="none",
+                  factor=1.0, original=0.0, low_freq=1.0, high_freq=4.0, beta_fast=32.0,
+                  beta_slow=1.0, attn_factor=0.0) -> MkvRopePlan:
+    """The rotation that mkv_rope and mkv_paged_append take.  scaling: "none", "linear", "ntk",
+    "yarn" or "banded" (see mkv_rope_config in include/mkv.h)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    cfg = mkv_rope_config(head_dim, head_dim if rot_dim is None else rot_dim, int(interleaved),
+                          ROPE_SCALINGS[scaling], base, factor, original, low_freq, high_freq,
+                          beta_fast, beta_slow, attn_factor)
+    plan = MkvRopePlan()
+    _check(_lib.mkv_rope_plan_init(ctypes.byref(cfg), ctypes.byref(plan)), "mkv_rope_plan_init")
+    return plan
+
+
+def mkv_rope(plan, x, pos=None, out=None, transposed=False, first_pos=0, stream=None):
+    """Rotates x [batch, tokens, heads, head_dim] (fp16, bf16 or fp32; any strides, the last
+    dimension contiguous) by the positions pos (int32 [batch, tokens]; None: first_pos + token)
+    into out (new where None; may be x; e.g. a transposed view of a [batch, heads, tokens,
+    head_dim] tensor).  transposed: the gradient of the call.  Returns out."""
+    import torch
+    dev = _cuda(x, "x")
+    if x.dim() != 4 or x.shape[3] != plan.head_dim:
+        raise ValueError(f"x must be [batch, tokens, heads, {plan.head_dim}], got {tuple(x.shape)}")
+    a = mkv_rope_args()
+    a.dtype = _dt(x, "x", (MKV_DT_F16, MKV_DT_BF16, MKV_DT_F32))
+    if out is None:
+        out = _new(x.shape, x.dtype, dev, stream)
+    elif out.dtype != x.dtype:
+        raise TypeError(f"out must be {x.dtype}, got {out.dtype}")
+    a.x = _vec(x, "x", dev)
+    a.out = _vec(out, "out", dev, x.shape)
+    a.batch, a.tokens, a.heads = x.shape[:3]
+    a.x_stride[:] = x.stride()[:3]
+    a.out_stride[:] = out.stride()[:3]
+    if pos is not None:
+        if pos.dtype != torch.int32:
+            raise TypeError(f"pos must be torch.int32, got {pos.dtype}")
+        a.pos = _vec(pos, "pos", dev, x.shape[:2])
+        a.pos_stride = pos.stride(0)
+    a.first_pos = first_pos
+    a.transposed = int(transposed)
+    _launch(_lib.mkv_rope, "mkv_rope", dev, stream, ctypes.byref(plan), ctypes.byref(a))
+    return out
+
+
+class MkvPaged:
+    """A paged cache over the caller's tensors: k_pages, v_pages [n_pages, kv_heads, page_size,
+    head_dim] (fp16, bf16 or float8_e4m3fn), page_table int32 [batch, max_pages] (rows may be
+    strided), k_scale and v_scale fp32 [kv_heads] (float8 only).  Holds the tensors and a status
+    word; check() reports what kernels found outside the cache."""
+
+    def __init__(self, k_pages, v_pages, page_table, k_scale=None, v_scale=None):
+        import torch
+        dev = self.device = _cuda(k_pages, "k_pages")
+        if k_pages.dim() != 4:
+            raise ValueError("k_pages must be [n_pages, kv_heads, page_size, head_dim]")
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [batch, max_pages]")
+        v = self.view = mkv_paged_cache()
+        v.dtype = _dt(k_pages, "k_pages", (MKV_DT_F16, MKV_DT_BF16, MKV_DT_E4M3))
+        v.k_pages = _flat(k_pages, "k_pages", dev, k_pages.dtype, k_pages.shape)
+        v.v_pages = _flat(v_pages, "v_pages", dev, k_pages.dtype, k_pages.shape)
+        if page_table.dtype != torch.int32:
+            raise TypeError(f"page_table must be torch.int32, got {page_table.dtype}")
+        v.page_table = _vec(page_table, "page_table", dev)
+        v.batch, v.max_pages = page_table.shape
+        v.table_stride = max(page_table.stride(0), page_table.shape[1]) if v.batch == 1 \
+            else page_table.stride(0)
+        v.n_pages, v.n_kv_heads, v.page_size, v.head_dim = k_pages.shape
+        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if s is not None:
+                setattr(v, name, _flat(s, name, dev, torch.float32, (v.n_kv_heads,)))
+        self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        v.status = self.status.data_ptr()
+        self._ref = ctypes.byref(v)
+        _check(_lib.mkv_paged_validate(self._ref), "mkv_paged_validate")
+
+    @property
+    def capacity(self) -> int:
+        """Slots the page table has room for in a sequence."""
+        return self.view.max_pages * self.view.page_size
+
+    def check(self) -> int:
+        """MKV_OK, or MKV_ERR_DEVICE_CHECK when a kernel met a page, slot, sequence or length
+        outside the cache since the last check (synchronous)."""
+        import torch
+        with torch.cuda.device(self.device):
+            return _lib.mkv_paged_check(self.status.data_ptr())
+
+
+def _meta(t, name, dev, dtype, v):
+    """Address and row length of per-slot data [batch, kv_heads, slots]."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [batch, kv_heads, slots]")
+    return _flat(t, name, dev, dtype, (v.batch, v.n_kv_heads, t.shape[2])), t.shape[2]
+
+
+def mkv_paged_append(cache, k, v, slot, seq=None, plan=None, pos=None, q=None, q_out=None,
+                     acc=None, pos_meta=None, stream=None):
+    """Writes n tokens into the cache: k, v [n, kv_heads, head_dim], slot (and seq, pos) int32 [n];
+    keys are rotated by plan at pos (None: the slot).  A negative slot is padding.  q [n, q_heads,
+    head_dim] is rotated into q_out (new where None), which is returned.  acc (fp32) and pos_meta
+    (int32) [batch, kv_heads, slots]: set to 0 and to the position in the written slots."""
+    import torch
+    dev, w = cache.device, cache.view
+    a = mkv_paged_append_args()
+    n = a.n = k.shape[0]
+    a.in_dtype = _dt(k, "k", (MKV_DT_F16, MKV_DT_BF16))
+    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise TypeError("k, v and q must be of one type")
+    a.k = _vec(k, "k", dev, (n, w.n_kv_heads, w.head_dim))
+    a.v = _vec(v, "v", dev, (n, w.n_kv_heads, w.head_dim))
+    a.k_stride[:] = k.stride()[:2]
+    a.v_stride[:] = v.stride()[:2]
+    a.slot = _flat(slot, "slot", dev, torch.int32, (n,))
+    if seq is not None:
+        a.seq = _flat(seq, "seq", dev, torch.int32, (n,))
+    if pos is not None:
+        a.pos = _flat(pos, "pos", dev, torch.int32, (n,))
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [n, q_heads, head_dim]")
+        a.n_q_heads = q.shape[1]
+        a.q = _vec(q, "q", dev, (n, q.shape[1], w.head_dim))
+        if q_out is None:
+            q_out = _new(q.shape, q.dtype, dev, stream)
+        elif q_out.dtype != q.dtype:
+            raise TypeError(f"q_out must be {q.dtype}, got {q_out.dtype}")
+        a.q_out = _vec(q_out, "q_out", dev, q.shape)
+        a.q_stride[:] = q.stride()[:2]
+        a.q_out_stride[:] = q_out.stride()[:2]
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    strides = set()
+    if acc is not None:
+        a.acc, a.meta_stride = _meta(acc, "acc", dev, torch.float32, w)
+        strides.add(a.meta_stride)
+    if pos_meta is not None:
+        a.pos_meta, a.meta_stride = _meta(pos_meta, "pos_meta", dev, torch.int32, w)
+        strides.add(a.meta_stride)
+    if len(strides) > 1:
+        raise ValueError("acc and pos_meta must have the same shape")
+    _launch(_lib.mkv_paged_append, "mkv_paged_append", dev, stream, cache._ref,
+            None if plan is None else ctypes.byref(plan), ctypes.byref(a))
+    return q_out
+
+
+def mkv_paged_decode(cache, q, seq_lens, out=None, lse=None, acc=None, max_len=0, scale=0.0,
+                     out_dtype=None, workspace=None, stream=None):
+    """Attention of one new token per sequence, q [batch, q_heads, head_dim], over its seq_lens
+    (int32 [batch]) cached tokens.  out: contiguous, of q's type or fp32 (new, of out_dtype,
+    where None), returned.  lse: fp32 [batch, q_heads] or None.  acc: fp32 [batch, kv_heads,
+    slots] or None; every token's weights are added.  max_len: a bound on seq_lens (0: the page
+    table's capacity).  workspace: a uint8 tensor (None: taken from torch's allocator)."""
+    import torch
+    dev, w = cache.device, cache.view
+    if q.dim() != 3:
+        raise ValueError("q must be [batch, q_heads, head_dim]")
+    a = mkv_paged_decode_args()
+    shape = (w.batch, q.shape[1], w.head_dim)
+    a.n_q_heads = q.shape[1]
+    a.q_dtype = _dt(q, "q", (MKV_DT_F16, MKV_DT_BF16))
+    a.q = _vec(q, "q", dev, shape)
+    a.q_stride[:] = q.stride()[:2]
+    if out is None:
+        out = _new(shape, out_dtype or q.dtype, dev, stream)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+    a.out_dtype = _dt(out, "out", (MKV_DT_F16, MKV_DT_BF16, MKV_DT_F32))
+    a.out = _flat(out, "out", dev, out.dtype, shape)
+    a.seq_lens = _flat(seq_lens, "seq_lens", dev, torch.int32, (w.batch,))
+    if lse is not None:
+        a.lse = _flat(lse, "lse", dev, torch.float32, shape[:2])
+    a.max_len = max_len
+    if acc is not None:
+        a.acc, a.acc_stride = _meta(acc, "acc", dev, torch.float32, w)
+        if max_len == 0:
+            a.max_len = min(cache.capacity, a.acc_stride)
+    a.scale = scale
+    ref = ctypes.byref(a)
+    if workspace is None:
+        need = _need(_lib.mkv_paged_decode_workspace, "mkv_paged_decode", dev, cache._ref, ref)
+        workspace = _scratch(need, dev, stream)
+    a.workspace, a.workspace_bytes = _workspace(workspace, dev)
+    _launch(_lib.mkv_paged_decode, "mkv_paged_decode", dev, stream, cache._ref, ref)
+    return out
+
+
+def _need(fn, where, dev, *args):
+    import torch
+    if torch.cuda.current_device() == dev.index:
+        n = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            n = fn(*args)
+    if n == 0:
+        raise MkvError(MKV_ERR_INVALID_ARG, where)
+    return n
+
+
+def _workspace(t, dev):
+    import torch
+    return _flat(t, "workspace", dev, torch.uint8, (t.numel(),)), t.numel()
+
+
+def mkv_paged_decode_workspace(cache, q_heads, max_len=0, weights=False) -> int:
+    """Bytes of workspace of mkv_paged_decode for these sizes (weights: with acc)."""
+    a = mkv_paged_decode_args(n_q_heads=q_heads, max_len=max_len, acc=1 if weights else None)
+    a.q_dtype = a.out_dtype = MKV_DT_F16 if cache.view.dtype == MKV_DT_E4M3 else cache.view.dtype
+    return _need(_lib.mkv_paged_decode_workspace, "mkv_paged_decode_workspace", cache.device,
+                 cache._ref, ctypes.byref(a))
+
+
+def mkv_paged_evict(cache, acc, pos, seq_lens, next_pos, budget, sink=0, recent=0, acc_out=None,
+                    pos_out=None, lens_out=None, src=None, max_len=0, workspace=None, stream=None):
+    """Cuts every (sequence, KV head) down to `budget` tokens by accumulated weight, in place in
+    the pages.  acc (fp32), pos (int32) [batch, kv_heads, slots]; acc_out and pos_out [batch,
+    kv_heads, slots_out] (None: in place, acc and pos themselves); seq_lens, next_pos int32
+    [batch]; lens_out int32 [batch] (None: seq_lens); src int32 [batch, kv_heads, budget] (new
+    where None): the slot each kept token came from.  Returns src."""
+    import torch
+    dev, w = cache.device, cache.view
+    a = mkv_paged_evict_args()
+    a.acc, a.meta_stride = _meta(acc, "acc", dev, torch.float32, w)
+    a.pos = _flat(pos, "pos", dev, torch.int32, acc.shape)
+    if (acc_out is None) != (pos_out is None):
+        raise ValueError("acc_out and pos_out go together")
+    if acc_out is None:
+        acc_out, pos_out = acc, pos
+    a.acc_out, a.out_stride = _meta(acc_out, "acc_out", dev, torch.float32, w)
+    a.pos_out = _flat(pos_out, "pos_out", dev, torch.int32, acc_out.shape)
+    a.seq_lens = _flat(seq_lens, "seq_lens", dev, torch.int32, (w.batch,))
+    a.next_pos = _flat(next_pos, "next_pos", dev, torch.int32, (w.batch,))
+    a.lens_out = a.seq_lens if lens_out is None else _flat(lens_out, "lens_out", dev, torch.int32,
+                                                           (w.batch,))
+    a.budget, a.sink, a.recent = budget, sink, recent
+    a.max_len = max_len or min(cache.capacity, a.meta_stride)
+    shape = (w.batch, w.n_kv_heads, max(0, budget))
+    if src is None:
+        src = _new(shape, torch.int32, dev, stream)
+    a.src = _flat(src, "src", dev, torch.int32, shape)
+    ref = ctypes.byref(a)
+    if workspace is None:
+        need = _need(_lib.mkv_paged_evict_workspace, "mkv_paged_evict", dev, cache._ref, ref)
+        workspace = _scratch(need, dev, stream)
+    a.workspace, a.workspace_bytes = _workspace(workspace, dev)
+    _launch(_lib.mkv_paged_evict, "mkv_paged_evict", dev, stream, cache._ref, ref)
+    return src
 
 
 class Mkv:
