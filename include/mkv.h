@@ -490,7 +490,7 @@ typedef struct {
   int32_t n_kv_heads;         /* 1..65535 */
   int32_t head_dim;           /* 64, 128 or 256 */
   int32_t page_size;          /* 16..256, multiple of 16 */
-  int32_t n_pages;            /* >= 1 */
+  int32_t n_pages;            /* >= 1; n_pages * n_kv_heads * page_size < 2^31 */
   int32_t max_pages;          /* pages of the longest sequence the table has room for, >= 1;
                                  max_pages * page_size <= 2^30 */
 } mkv_paged_cache;
@@ -606,7 +606,8 @@ mkv_status mkv_paged_evict(const mkv_paged_cache* cache, const mkv_paged_evict_a
 
 /* Reads and clears a device status word after all work on the current device
  * (synchronous): MKV_ERR_DEVICE_CHECK if a kernel met a page, slot, sequence
- * or length outside the cache since the last check, else MKV_OK. */
+ * or length outside the cache since the last check, MKV_ERR_TIMEOUT if a
+ * bounded wait for a copy gave up (outputs undefined then), else MKV_OK. */
 mkv_status mkv_paged_check(int32_t* status);
 
 #ifdef __cplusplus

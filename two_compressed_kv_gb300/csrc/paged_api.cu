@@ -5,6 +5,8 @@
 #include <cstdio>
 #include <cstring>
 
+#include <cudaTypedefs.h>
+
 #include "paged_internal.cuh"
 
 using namespace mkv;
@@ -68,8 +70,8 @@ const char* check_cache(const mkv_paged_cache* c) {
   if ((int64_t)c->max_pages * c->page_size > ((int64_t)1 << 30))
     return "paged cache: max_pages * page_size must be <= 2^30";
   if (c->table_stride < c->max_pages) return "paged cache: table_stride must be >= max_pages";
-  if ((int64_t)c->n_pages * c->n_kv_heads > kMaxGrid / (c->page_size / 16))
-    return "paged cache: too many pages (2^31 blocks of 16 rows at most)";
+  if ((int64_t)c->n_pages * c->n_kv_heads > kMaxGrid / c->page_size)
+    return "paged cache: too many pages (n_pages * n_kv_heads * page_size must be below 2^31)";
   return nullptr;
 }
 
@@ -158,6 +160,34 @@ const char* check_evict(const mkv_paged_cache* c, const mkv_paged_evict_args* a)
 }
 
 }  // namespace
+
+namespace mkv {
+
+cudaError_t encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int row_bytes, int box_rows) {
+  // the driver's encoder, looked up once: it is the process's, not a device's
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                           cudaEnableDefault, &found);
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(
+        e == cudaSuccess && found == cudaDriverEntryPointSuccess ? fn : nullptr);
+  }();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint32_t w = row_bytes < 128 ? row_bytes : 128;
+  // columns of w bytes, rows, column groups of a row
+  const cuuint64_t dim[3] = {w, (cuuint64_t)rows, (cuuint64_t)row_bytes / w};
+  const cuuint64_t stride[2] = {(cuuint64_t)row_bytes, w};
+  const cuuint32_t box[3] = {w, (cuuint32_t)box_rows, (cuuint32_t)row_bytes / w};
+  const cuuint32_t step[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dim, stride, box, step,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            w == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace mkv
 
 extern "C" {
 
@@ -366,6 +396,7 @@ mkv_status mkv_paged_decode(const mkv_paged_cache* c, const mkv_paged_decode_arg
   p.vs = c->v_scale;
   p.status = c->status;
   p.table_stride = c->table_stride;
+  p.rows = (int64_t)c->n_pages * c->n_kv_heads * c->page_size;
   p.B = c->batch;
   p.H = c->n_kv_heads;
   p.g = a->n_q_heads / c->n_kv_heads;
@@ -469,6 +500,7 @@ mkv_status mkv_paged_check(int32_t* status) {
   if (v == 0) return MKV_OK;
   CKP(cudaMemset(status, 0, sizeof(v)));
   CKP(cudaDeviceSynchronize());
+  if (!(v & DEV_ERR_CHECK)) return set_error(MKV_ERR_TIMEOUT, "a bounded device-side wait gave up");
   return set_error(MKV_ERR_DEVICE_CHECK, "a page, slot, sequence or length lay outside the paged cache");
 }
 

@@ -13,10 +13,10 @@
 // built to keep enough copies in flight with few instructions per byte:
 //   - a warp works alone on blocks of 16 tokens; no barrier between warps until
 //     its part of a stream is done;
-//   - rows come by 16-byte cp.async into a ring in shared memory that each lane
-//     uses as its own queue: a lane copies exactly the pieces that its matrix
-//     fragments need and reads back only those, so the ring needs neither
-//     swizzle nor warp synchronisation and is free of bank conflicts;
+//   - the 16 rows of a block come by one TMA copy for keys and one for values
+//     into the warp's own ring in shared memory, 128-byte swizzled; column n of a
+//     fragment is token n ^ 4 (n & 1) of its 8, which makes both operands' reads
+//     free of bank conflicts under that swizzle;
 //   - S = Q K^T and O = P V run as m16n8k16 with the query heads as rows.  The
 //     order of the contracted dimension is free, so a lane's 16 bytes of a key
 //     row are two steps' B fragments as they are; value rows of token pairs are
@@ -33,18 +33,13 @@
 
 #include "paged_internal.cuh"
 #include "ptx.cuh"
+#include "tc05.cuh"
 
 namespace mkv {
 namespace {
 
 constexpr int PA_NW = 4;              // warps per CTA
 
-__device__ __forceinline__ void cpa16_zfill(uint32_t dst, const void* src, uint32_t n) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cpa8_zfill(uint32_t dst, const void* src, uint32_t n) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 r;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
@@ -90,6 +85,7 @@ struct PA {
   static constexpr int ES = CT == MKV_DT_E4M3 ? 1 : 2;
   static constexpr bool BF16 = CT == MKV_DT_BF16;
   static constexpr int ROW = D * ES;                       // bytes of a row
+  static constexpr int SW = ROW < 128 ? ROW : 128;         // swizzled width
   static constexpr int KL = ROW / 64;                      // 16-byte pieces of a key row per lane
   static constexpr int VB = ROW / 8 < 16 ? ROW / 8 : 16;   // bytes of a value piece
   static constexpr int VL = ROW / (8 * VB);                // value pieces of a row per lane
@@ -97,28 +93,52 @@ struct PA {
   static constexpr int KS = D / 16;                        // contraction steps of S
   static constexpr int NT = D / 8;                         // n-tiles of O
   static constexpr int STAGE = 2 * PA_BLOCK * ROW;         // bytes of one block's keys and values
-  static constexpr int STAGES = STAGE >= 16384 ? 3 : STAGE >= 8192 ? 3 : STAGE >= 4096 ? 6 : 8;
+  static constexpr int STAGES = STAGE >= 8192 ? 3 : STAGE >= 4096 ? 6 : 8;
   static constexpr int HR = WIDE ? 16 : 8;                 // head rows
   static constexpr int MERGE = PA_NW * HR * (D + 4) * 4;
   static constexpr int RING = PA_NW * STAGES * STAGE;
-  static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+  static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + 1024;   // and its alignment
   static constexpr int CTAS = SMEM <= 100 * 1024 ? 2 : 1;  // per SM
 };
+
+// Byte offset of 16-byte piece `piece` of row `row` in a block's keys or values:
+// [row / SW columns][16 rows][SW bytes], pieces of a row permuted by the TMA
+// swizzle (128 bytes: by row mod 8; 64 bytes: by row / 2 mod 4).
+template <int SW>
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+  if constexpr (SW == 128)
+    return (uint32_t)((piece >> 3) * (PA_BLOCK * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+  else
+    return (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+}
 
 // ---------------------------------------------------------------------------
 // grid: split ? G : streams; block: 4 warps; dynamic smem PA::SMEM
 // ---------------------------------------------------------------------------
 template <int CT, int D, bool WIDE>
 __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
-    paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
+    paged_attn_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap) {
   using C = PA<CT, D, WIDE>;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // the swizzle goes by address bits 7..9
+  __shared__ uint64_t full[PA_NW][C::STAGES];
   __shared__ int64_t pre[PA_MAX_B + 1];        // split: blocks before each sequence
   __shared__ float sm_m[PA_NW][C::HR], sm_l[PA_NW][C::HR];
   __shared__ int64_t warp_sum[PA_NW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;       // fragment row (head) and column group
-  const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::STAGE);
+  uint8_t* const ring_p = smem + warp * (C::STAGES * C::STAGE);
+  const uint32_t ring = smem_u32(ring_p);
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < C::STAGES; ++k) mbar_init(&full[warp][k], 1);
+    mbar_init_fence();
+  }
+  __syncwarp();
+  uint32_t phases = 0;                         // bit of a ring slot: parity of its next fill
+  uint32_t pending = 0;                        // bit of a ring slot: a copy into it is in flight
+  bool gave_up = false;                        // a bounded wait ran out: outputs undefined
 
   griddep_launch();                            // the join's prologue may start; it waits for the end
   // this CTA's range of blocks, counted over all streams
@@ -257,7 +277,7 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
 
     // this warp's blocks: j0 + warp, + 4, ...; lane i holds the pool row of
     // the i-th of the next 32 (in blocks of 16 rows; -1: page outside the cache)
-    const int count = max(0, (j1 - j0 - warp + PA_NW - 1) / PA_NW);
+    const int count = gave_up ? 0 : max(0, (j1 - j0 - warp + PA_NW - 1) / PA_NW);
     auto entries = [&](int first) {
       const int j = j0 + warp + PA_NW * (first + lane);
       int e = -1;
@@ -274,57 +294,48 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
     int ent = entries(0), ent_next = entries(32);
     int valid_bits = 0;                        // bit of a ring slot: its page is there
     auto issue = [&](int i, int slot) {
-      if (i < count) {
-        if ((i & 31) == 0 && i > 0) {
-          ent = ent_next;
-          ent_next = entries(i + 32);
-        }
-        const int e = __shfl_sync(~0u, ent, i & 31);
-        const int rows = e < 0 ? 0 : n - (j0 + warp + PA_NW * i) * PA_BLOCK;
-        valid_bits = e < 0 ? valid_bits & ~(1 << slot) : valid_bits | (1 << slot);
-        const int64_t off = (int64_t)max(e, 0) * (PA_BLOCK * C::ROW);
-        const uint32_t dst = ring + slot * C::STAGE;
-        const uint8_t* k = p.kp + off + r * C::ROW + 16 * c;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int x = 0; x < C::KL; ++x)
-            cpa16_zfill(dst + (t * C::KL + x) * 512 + lane * 16, k + 8 * t * C::ROW + 64 * x,
-                        8 * t + r < rows ? 16u : 0u);
-        const uint8_t* v = p.vp + off + C::VB * r;
-        const uint32_t dv = dst + PA_BLOCK * C::ROW + lane * C::VB;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int row = 2 * c + (t & 1) + 8 * (t >> 1);
-#pragma unroll
-          for (int x = 0; x < C::VL; ++x) {
-            const uint8_t* src = v + row * C::ROW + x * 8 * C::VB;
-            const uint32_t to = dv + (t * C::VL + x) * 32 * C::VB;
-            if constexpr (C::VB == 16)
-              cpa16_zfill(to, src, row < rows ? 16u : 0u);
-            else
-              cpa8_zfill(to, src, row < rows ? 8u : 0u);
-          }
-        }
+      if (i >= count) return;
+      if ((i & 31) == 0 && i > 0) {
+        ent = ent_next;
+        ent_next = entries(i + 32);
       }
-      cpa_commit();
+      const int e = __shfl_sync(~0u, ent, i & 31);
+      valid_bits = e < 0 ? valid_bits & ~(1 << slot) : valid_bits | (1 << slot);
+      if (e >= 0) pending |= 1u << slot;
+      if (e >= 0 && lane == 0) {
+        uint64_t* bar = &full[warp][slot];
+        mbar_arrive_expect_tx(bar, C::STAGE);
+        tma_load_3d(ring_p + slot * C::STAGE, &kmap, 0, e * PA_BLOCK, 0, bar);
+        tma_load_3d(ring_p + slot * C::STAGE + PA_BLOCK * C::ROW, &vmap, 0, e * PA_BLOCK, 0, bar);
+      }
     };
 #pragma unroll
     for (int s = 0; s < C::STAGES - 1; ++s) issue(s, s);
     float* score_row = p.scores ? p.scores + (stream * p.g + r) * p.score_stride : nullptr;
 
     int slot = 0;
-    for (int i = 0; i < count; ++i) {
+    for (int i = 0; i < count && !gave_up; ++i) {
+      // the slot before this one was read in the last step, by all lanes
+      __syncwarp();
       issue(i + C::STAGES - 1, slot == 0 ? C::STAGES - 1 : slot - 1);
-      cpa_wait<C::STAGES - 1>();
       const uint32_t src = ring + slot * C::STAGE;
+      const bool there = valid_bits >> slot & 1;
+      if (there) {
+        const bool ok = mbar_wait(&full[warp][slot], phases >> slot & 1);
+        if (!__all_sync(~0u, ok)) {
+          if (lane == 0 && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
+          gave_up = true;
+        }
+        phases ^= 1u << slot;
+        pending &= ~(1u << slot);
+      }
       float s[2][4];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
         for (int x = 0; x < C::KL; ++x) {
-          const uint4 v = lds16(src + (t * C::KL + x) * 512 + lane * 16);
+          const uint4 v = lds16(src + piece_at<C::SW>(8 * t + (r ^ ((r & 1) << 2)), 4 * x + c));
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           constexpr int PER = CT == MKV_DT_E4M3 ? 4 : 2;   // steps in a piece
 #pragma unroll
@@ -345,23 +356,31 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
           }
         }
       }
-      const int tok = (j0 + warp + PA_NW * i) * PA_BLOCK + 2 * c;
-      const int left = (valid_bits >> slot & 1) ? n : 0;
+      // columns 2 c and 2 c + 1 are tokens 2 c and (2 c + 1) ^ 4 of 8
+      const int tok0 = (j0 + warp + PA_NW * i) * PA_BLOCK;
+      const int left = there ? n - tok0 : 0;   // live tokens of the block (16 or more: all)
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int k = 0; k < (WIDE ? 4 : 2); ++k) {
-          s[t][k] *= sc[k / 2];
-          if (tok + 8 * t + (k & 1) >= left) s[t][k] = -CUDART_INF_F;
-        }
+        for (int k = 0; k < (WIDE ? 4 : 2); ++k) s[t][k] *= sc[k / 2];
+      if (left < PA_BLOCK) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int k = 0; k < (WIDE ? 4 : 2); ++k)
+            if (8 * t + ((k & 1) ? (2 * c + 1) ^ 4 : 2 * c) >= left) s[t][k] = -CUDART_INF_F;
+      }
       if (p.scores) {
 #pragma unroll
-        for (int w = 0; w < (WIDE ? 2 : 1); ++w)
+        for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
+          // lane c ^ 2 of the row has token 2 c + 1
+          const float x0 = __shfl_xor_sync(~0u, s[0][2 * w + 1], 2), x1 = __shfl_xor_sync(~0u, s[1][2 * w + 1], 2);
           if (r + 8 * w < p.g) {
-            float* to = score_row + 8 * w * p.score_stride + tok;
-            *reinterpret_cast<float2*>(to) = make_float2(s[0][2 * w], s[0][2 * w + 1]);
-            *reinterpret_cast<float2*>(to + 8) = make_float2(s[1][2 * w], s[1][2 * w + 1]);
+            float* to = score_row + 8 * w * p.score_stride + tok0 + 2 * c;
+            *reinterpret_cast<float2*>(to) = make_float2(s[0][2 * w], x0);
+            *reinterpret_cast<float2*>(to + 8) = make_float2(s[1][2 * w], x1);
           }
+        }
       }
       // running maximum and sum
       float mref[WIDE ? 2 : 1];
@@ -406,7 +425,7 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
       } else {
         pa[0] = ph[0], pa[1] = pl[0], pa[2] = ph[1], pa[3] = pl[1];
       }
-      const uint32_t sv = src + PA_BLOCK * C::ROW + lane * C::VB;
+      const uint32_t sv = src + PA_BLOCK * C::ROW;
       auto pv = [&](int nt, uint32_t b0, uint32_t b1) {
         if constexpr (C::BF16) {
           mma_bf16(o[nt], pa, b0, b1);
@@ -421,13 +440,18 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
         uint32_t v[4][C::VB / 4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const uint32_t from = sv + (t * C::VL + x) * 32 * C::VB;
+          const int row = 8 * (t >> 1) + ((t & 1) ? (2 * c + 1) ^ 4 : 2 * c);
           if constexpr (C::VB == 16) {
-            const uint4 y = lds16(from);
+            const uint4 y = lds16(sv + piece_at<C::SW>(row, 8 * x + r));
             v[t][0] = y.x, v[t][1] = y.y, v[t][2] = y.z, v[t][3] = y.w;
           } else {
-            const uint2 y = lds8(from);
+            const uint2 y = lds8(sv + piece_at<C::SW>(row, r >> 1) + 8 * (r & 1));
             v[t][0] = y.x, v[t][1] = y.y;
+          }
+          // what lies behind the sequence in its last page may be anything
+          if (left < PA_BLOCK && row >= left) {
+#pragma unroll
+            for (int y = 0; y < C::VB / 4; ++y) v[t][y] = 0u;
           }
         }
 #pragma unroll
@@ -450,8 +474,13 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
       slot = slot + 1 == C::STAGES ? 0 : slot + 1;
     }
 
+    if (gave_up) {
+      // copies in flight must have landed before the ring is used for anything else
+      for (int k = 0; k < C::STAGES; ++k)
+        if (pending >> k & 1) mbar_wait(&full[warp][k], phases >> k & 1);
+      pending = 0;
+    }
     // join the warps: the ring is drained and becomes [warp][head][D + 4]
-    cpa_wait<0>();
 #pragma unroll
     for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
       l[w] += __shfl_xor_sync(~0u, l[w], 1);
@@ -525,18 +554,24 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
     }
     if (!p.split) break;
     at += j1 - j0;
-    if (at < g1) __syncthreads();   // the merge area becomes the ring again
+    if (at < g1) {                  // the merge area becomes the ring again
+      fence_proxy_async();
+      __syncthreads();
+    }
   }
 }
 
 template <int CT, int D, bool WIDE>
 cudaError_t launch_pa(const PagedAttnParams& p, cudaStream_t st) {
   using C = PA<CT, D, WIDE>;
+  CUtensorMap kmap, vmap;
+  if (cudaError_t e = encode_rows_map(&kmap, p.kp, p.rows, C::ROW, PA_BLOCK)) return e;
+  if (cudaError_t e = encode_rows_map(&vmap, p.vp, p.rows, C::ROW, PA_BLOCK)) return e;
   cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<CT, D, WIDE>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t grid = p.split ? p.G : (int64_t)p.B * p.H;
-  paged_attn_kernel<CT, D, WIDE><<<(unsigned)grid, PA_NW * 32, C::SMEM, st>>>(p);
+  paged_attn_kernel<CT, D, WIDE><<<(unsigned)grid, PA_NW * 32, C::SMEM, st>>>(p, kmap, vmap);
   return cudaGetLastError();
 }
 

@@ -1,6 +1,7 @@
 // Internal declarations of the rotary and paged-cache operators.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -56,6 +57,7 @@ struct PagedAttnParams {
   const float *ks, *vs;
   int32_t* status;
   int64_t table_stride;
+  int64_t rows;                   // of a pool: n_pages * H * page_size
   int B, H, g, n_pages, bpp;      // bpp: blocks per page
   int limit;                      // largest length: min(max_len, max_pages * page_size)
   const void* q;
@@ -101,6 +103,11 @@ __device__ __forceinline__ void store_out4(const PagedAttnParams& p, int64_t at,
     o[1] = __floats2half2_rn(a.z, a.w);
   }
 }
+
+// Tensor map of a pool as [rows][row_bytes]: copies of `box_rows` whole rows,
+// laid out [row_bytes / w][box_rows][w] with w = min(row_bytes, 128), swizzled
+// over w bytes.
+cudaError_t encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int row_bytes, int box_rows);
 
 // g <= 8 and g <= 16 variants per head dim (one translation unit each)
 cudaError_t launch_paged_attn_64(const PagedAttnParams& p, int cache_type, cudaStream_t st);
