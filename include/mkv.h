@@ -395,8 +395,8 @@ mkv_status mkv_basis_static(const void* k, const void* v, int batch, int n_kv_he
  * into a CUDA graph.  Scratch memory is the caller's (`workspace`): calls that
  * may overlap in time, replays of captured graphs included, need workspaces of
  * their own.  Nothing in a workspace has to be initialised or kept.
- * Argument errors return MKV_ERR_INVALID_ARG before any CUDA call, with the
- * reason in mkv_last_error_string.
+ * Argument errors return MKV_ERR_INVALID_ARG before anything is launched, with
+ * the reason in mkv_last_error_string.
  * ------------------------------------------------------------------------- */
 
 /* Element types. */

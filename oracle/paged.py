@@ -89,8 +89,10 @@ def evict(acc, pos, next_pos, budget, sink=0, recent=0):
     if n <= budget:
         return np.arange(n)
     safe = (pos < sink) | (pos.astype(np.int64) >= int(next_pos) - recent)
-    a = np.where(np.nan_to_num(acc, nan=0.0, posinf=np.inf) > 0, acc, 0.0)
-    order = sorted(range(n), key=lambda t: (not safe[t], -np.inf if safe[t] else -float(a[t]), t))
-    keep = set(order[:budget])
-    behind = iter(sorted(t for t in keep if t >= budget))
-    return np.array([t if t in keep else next(behind) for t in range(budget)])
+    a = np.where(np.nan_to_num(acc, nan=0.0, posinf=np.inf) > 0, acc, 0.0).astype(np.float64)
+    a[safe] = np.inf
+    keep = np.zeros(n, bool)
+    keep[np.lexsort((np.arange(n), -a, ~safe))[:budget]] = True
+    src = np.arange(budget)
+    src[~keep[:budget]] = budget + np.nonzero(keep[budget:])[0]
+    return src

@@ -478,7 +478,11 @@ def evict_case(M, lens, heads, dim, page, budget, sink, recent, dtype=F16, seed=
                weights=None, max_len=0, pos=None, spare=3):
     b = len(lens)
     cache = Cache(M, dtype, lens, heads, dim, page, seed=seed, spare=spare)
-    slots = max(max(lens), 1) + 5
+    slots = max(max(lens) + 5, max_len)
+    if max_len:                                  # a table with room for the bound
+        room = torch.full((b, -(-max_len // page)), -1, dtype=torch.int32, device=DEV)
+        room[:, : cache.table.shape[1]] = cache.table
+        cache.c = M.MkvPaged(*cache.pools, room, *cache.dev_scales)
     g = torch.Generator().manual_seed(seed + 50)
     acc = torch.exp(3 * torch.randn((b, heads, slots), generator=g)) if weights is None else weights(b, heads, slots, g)
     if pos is None:
@@ -555,12 +559,31 @@ def test_evict_ties_and_odd_weights(M, name, n):
 
 
 def test_evict_sizes_of_cluster(M):
-    """1, 2, 4 and 8 CTAs a stream; slices that fit shared memory and that do not."""
+    """1, 2, 4 and 8 CTAs a stream; slices of 8 and 16 keys a thread, and longer ones."""
     evict_case(M, [8191, 4097], 1, 64, 256, 4096, 4, 100, E4M3, seed=1)
     evict_case(M, [8192] * 3, 8, 64, 256, 1000, 0, 999, E4M3, seed=2)
     evict_case(M, [16385] * 3 + [5], 8, 64, 256, 16384, 0, 0, E4M3, seed=3)
-    evict_case(M, [400001], 1, 64, 256, 3001, 4, 700, E4M3, seed=4)          # 8 slices of 50176 keys
-    evict_case(M, [50000, 45000] + [10] * 158, 1, 64, 256, 9000, 4, 700, E4M3, seed=5, spare=0)   # one CTA, 50176 keys
+    evict_case(M, [100000, 131072, 98765], 1, 64, 256, 7000, 0, 99, E4M3, seed=8)
+    evict_case(M, [400001], 1, 64, 256, 3001, 4, 700, E4M3, seed=4)          # 8 slices of 50176
+    evict_case(M, [400001], 1, 64, 256, 300001, 4, 700, E4M3, seed=4)        # most are kept
+    evict_case(M, [50000, 45000] + [10] * 158, 1, 64, 256, 9000, 4, 700, E4M3, seed=5, spare=0)   # one CTA a stream
+    # the long form by the bound alone, and many slots
+    evict_case(M, [5000, 45, 9001] + [10] * 77, 1, 64, 256, 2000, 4, 700, E4M3, seed=6, spare=0, max_len=300000)
+    evict_case(M, [2210000], 1, 64, 256, 5000, 4, 700, E4M3, seed=7)
+
+
+@pytest.mark.parametrize("name", ["zeros", "same", "sampled"])
+def test_evict_long_streams_that_mislead_the_sample(M, name):
+    """Ties over a whole long stream; and large weights at just the slots that a bound is taken
+    from (every 49th of 8 slices of 50176 slots), so that too few others reach it."""
+    def weights(b, h, s, g):
+        r = torch.rand((b, h, s), generator=g)
+        if name == "zeros":
+            return torch.where(r < 0.999, torch.zeros(()), r)
+        if name == "same":
+            return torch.full((b, h, s), 0.25)
+        return torch.where(torch.arange(s) % 49 == 0, 100 + r, r)
+    evict_case(M, [8 * 50176], 1, 64, 256, 20000, 4, 300, E4M3, weights=weights, seed=9)
 
 
 def test_evict_protected_beyond_budget(M):

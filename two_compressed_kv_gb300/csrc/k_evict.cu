@@ -27,8 +27,7 @@ namespace {
 
 constexpr int ET = 1024, EW = ET / 32;
 constexpr int E_BINS = 2048;
-constexpr int E_MAX_R = 8;
-constexpr int E_CAP = 40960;              // keys of a slice held in shared memory
+constexpr int E_SHORT = 16 * ET;          // slots of a slice whose keys stay in registers
 constexpr uint32_t KEY_SAFE = 0x7fffffffu;
 
 __device__ __forceinline__ int evict_len(const EvictParams& p, int b) {
@@ -61,189 +60,399 @@ __device__ __forceinline__ int block_prefix(int v, int* ws, int* all) {
   return inc - v + (warp ? ws[warp - 1] : 0);
 }
 
-// ---------------------------------------------------------------------------
-// grid: streams * R, cluster R; block 1024; dynamic smem: the slice's keys
-// ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(ET) evict_select_kernel(const __grid_constant__ EvictParams p,
-                                                          int key_cap) {
-  cg::cluster_group cl = cg::this_cluster();
-  extern __shared__ uint32_t keys[];
-  __shared__ int hist[E_BINS];
-  __shared__ int ws[EW];
-  __shared__ int cnt[EW][4];              // per warp: above / equal keys, below and from slot m
-  __shared__ int pick[3];                 // bin, keys above it, keys in it
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int R = p.R, rank = R > 1 ? (int)cl.block_rank() : 0;
+// What both selection kernels know of their stream and slice.
+struct Slice {
+  const float* acc;
+  const int32_t* pos;
+  int32_t *src, *movers, *holes;
+  int64_t from;                           // positions from here on are protected
+  int n, m, sink;
+  int sl, s0, s1, wl, w0, w1;             // slots of a CTA; this CTA's; of a warp; this warp's
+};
+
+__device__ __forceinline__ uint32_t form_key(const Slice& s, float a, int q) {
+  if (q < s.sink || q >= s.from) return KEY_SAFE;
+  return a > 0.f ? __float_as_uint(a) : 0u;
+}
+
+template <int R>
+__device__ __forceinline__ void cluster_barrier() {
+  if constexpr (R > 1) cg::this_cluster().sync(); else __syncthreads();
+}
+
+// Fills `s`; false where nothing is to be evicted (then src is written).
+template <int R>
+__device__ __forceinline__ bool slice_of(const EvictParams& p, int rank, Slice& s) {
   const int64_t stream = blockIdx.x / R;
   const int b = (int)(stream / p.H), h = (int)(stream - (int64_t)b * p.H);
-  const int n = evict_len(p, b), m = p.budget;
-  int32_t* src = p.src + stream * m;
-  griddep_launch();
-  if (h == 0 && rank == 0 && tid == 0 && p.status && p.lens[b] != n) atomicOr(p.status, DEV_ERR_CHECK);
-  if (n <= m) {                           // nothing to evict (uniform in the cluster)
-    for (int64_t i = rank * ET + tid; i < m; i += (int64_t)R * ET) src[i] = i < n ? (int)i : -1;
-    return;
+  s.n = evict_len(p, b);
+  s.m = p.budget;
+  s.src = p.src + stream * s.m;
+  if (h == 0 && rank == 0 && threadIdx.x == 0 && p.status && p.lens[b] != s.n) atomicOr(p.status, DEV_ERR_CHECK);
+  if (s.n <= s.m) {
+    for (int64_t i = rank * ET + threadIdx.x; i < s.m; i += (int64_t)R * ET) s.src[i] = i < s.n ? (int)i : -1;
+    return false;
   }
-  const float* acc = p.acc + stream * p.meta_stride;
-  const int32_t* pos = p.pos + stream * p.meta_stride;
-  const int64_t from = (int64_t)p.next_pos[b] - p.recent;
-  auto compute = [&](int t) -> uint32_t {
-    const int q = pos[t];
-    const float a = acc[t];
-    if (q < p.sink || q >= from) return KEY_SAFE;
-    return a > 0.f ? __float_as_uint(a) : 0u;
-  };
-  // this CTA's slots; a warp's share is a multiple of 32 slots
-  const int sl = ((n + R - 1) / R + ET - 1) / ET * ET;
-  const int s0 = min(n, rank * sl), s1 = min(n, s0 + sl);
-  const int held = min(s1 - s0, key_cap);
-#pragma unroll 4
-  for (int i = tid; i < held; i += ET) keys[i] = compute(s0 + i);
-  auto key = [&](int t) -> uint32_t { return t - s0 < held ? keys[t - s0] : compute(t); };
-  auto sync_all = [&]() {
-    if (R > 1) cl.sync(); else __syncthreads();
-  };
+  s.acc = p.acc + stream * p.meta_stride;
+  s.pos = p.pos + stream * p.meta_stride;
+  s.movers = p.lists + stream * 2 * s.m;
+  s.holes = s.movers + s.m;
+  s.sink = p.sink;
+  s.from = (int64_t)p.next_pos[b] - p.recent;
+  s.sl = ((s.n + R - 1) / R + ET - 1) / ET * ET;
+  s.wl = s.sl / EW;
+  s.s0 = min(s.n, rank * s.sl);
+  s.s1 = min(s.n, s.s0 + s.sl);
+  s.w0 = min(s.s1, s.s0 + ((int)threadIdx.x >> 5) * s.wl);
+  s.w1 = min(s.s1, s.w0 + s.wl);
+  return true;
+}
 
-  // the m-th largest key, 11 + 10 + 10 bits at a time.  `above`: keep keys > lim;
-  // `need`: of those equal to lim, the lowest slots
-  uint32_t prefix = 0, lim = 0;
-  int need = m;
-  int shift = 20;
-  for (int level = 0; level < 3; ++level) {
-    const int bins = level == 0 ? 2048 : 1024;
-    const uint32_t hi_mask = level == 0 ? 0u : 0xffffffffu << (shift + 10);
-    for (int i = tid; i < bins; i += ET) hist[i] = 0;
-    __syncthreads();
-    for (int t = s0 + tid; t < s1; t += ET) {
-      const uint32_t k = key(t);
-      if ((k & hi_mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
-    }
-    sync_all();
-    // counts of bins from the top: thread i takes bins (bins - 1 - i PER ...)
-    int mine[2] = {0, 0};
-    const int per = bins / ET;
+// The bin of the `need`-th largest key, from the ranks' histograms of `bins`
+// bins: pick = {bin, keys in bins above, keys in it}.  Returns the keys in all.
+// Ends with a block barrier.
+template <int R>
+__device__ __forceinline__ int pick_bin(int* hist, int bins, int need, int* ws, int* pick) {
+  cg::cluster_group cl = cg::this_cluster();
+  constexpr int MAXPER = E_BINS / ET;
+  const int per = bins / ET;
+  int mine[MAXPER] = {}, sum = 0;
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-      if (x < per) {
-        const int bin = bins - 1 - (tid * per + x);
-        if (R > 1)
-          for (int q = 0; q < R; ++q) mine[x] += *cl.map_shared_rank(&hist[bin], q);
-        else
-          mine[x] = hist[bin];
-      }
-    int all;
-    int before = block_prefix(mine[0] + mine[1], ws, &all);
+  for (int x = 0; x < MAXPER; ++x)
+    if (x < per) {
+      const int bin = bins - 1 - ((int)threadIdx.x * per + x);   // from the top
+      int v[R];
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-      if (x < per) {
-        if (before < need && before + mine[x] >= need) {
-          pick[0] = bins - 1 - (tid * per + x);
-          pick[1] = before;
-          pick[2] = mine[x];
-        }
-        before += mine[x];
-      }
-    sync_all();                           // pick is set; every rank has read the histograms
-    prefix |= (uint32_t)pick[0] << shift;
-    need -= pick[1];
-    const bool all_in = pick[2] == need;
-    __syncthreads();                      // pick may be written again
-    if (all_in || level == 2) {
-      lim = prefix;
-      if (all_in) {                       // the whole bin is kept: no key equals lim's predecessor
-        need = 0;
-        break;
-      }
+      for (int q = 0; q < R; ++q) v[q] = R > 1 ? *cl.map_shared_rank(&hist[bin], q) : hist[bin];
+#pragma unroll
+      for (int q = 0; q < R; ++q) mine[x] += v[q];
+      sum += mine[x];
     }
-    shift -= 10;
-  }
-  const bool whole_bin = need == 0;       // keep keys >= lim, else > lim and `need` equal ones
-  auto above = [&](uint32_t k) { return whole_bin ? k >= lim : k > lim; };
-  auto equal = [&](uint32_t k) { return !whole_bin && k == lim; };
+  int all;
+  int before = block_prefix(sum, ws, &all);
+#pragma unroll
+  for (int x = 0; x < MAXPER; ++x)
+    if (x < per) {
+      if (before < need && before + mine[x] >= need) {
+        pick[0] = bins - 1 - ((int)threadIdx.x * per + x);
+        pick[1] = before;
+        pick[2] = mine[x];
+      }
+      before += mine[x];
+    }
+  __syncthreads();
+  return all;
+}
 
-  // counts of this warp's run of slots
-  const int wl = sl / EW;
-  const int w0 = min(s1, s0 + warp * wl), w1 = min(s1, w0 + wl);
-  int ab[2] = {0, 0}, eq[2] = {0, 0};
-#pragma unroll 2
-  for (int t0 = w0; t0 < w1; t0 += 32) {
-    const int t = t0 + lane;
-    const uint32_t k = t < w1 ? key(t) : 0u;
-    const bool up = t < w1 && above(k), same = t < w1 && equal(k);
-    const unsigned lo = __ballot_sync(~0u, t < m);
-    const unsigned u = __ballot_sync(~0u, up), s = __ballot_sync(~0u, same);
-    ab[0] += __popc(u & lo), ab[1] += __popc(u & ~lo);
-    eq[0] += __popc(s & lo), eq[1] += __popc(s & ~lo);
-  }
-  if (lane == 0) cnt[warp][0] = ab[0], cnt[warp][1] = ab[1], cnt[warp][2] = eq[0], cnt[warp][3] = eq[1];
-  sync_all();
-  // equal keys, movers and freed slots of all warps before this one, in slot order
-  int eq_before = 0, movers = 0, holes = 0, all_movers = 0;
-  {
-    const int total = R * EW, me = rank * EW + warp;
-    int run_eq = 0, run_mv = 0, run_ho = 0;
-    for (int g = 0; g < total; g += 32) {
-      const int w = g + lane;             // all entries of one rank: EW = 32
-      const int* e = R > 1 ? cl.map_shared_rank(&cnt[lane][0], g / EW) : &cnt[lane][0];
-      const int a1 = e[1], e0 = e[2], e1 = e[3], a0 = e[0];
-      int inc = e0 + e1;
+// From every warp's counts (keys above the limit, and equal to it, below and
+// from slot m): equal keys, movers and freed slots of all warps before this
+// one, in slot order, and all movers.  Lane i takes warp i of every rank.
+struct Ranks {
+  int eq, movers, holes, all_movers;
+};
+template <int R>
+__device__ __forceinline__ Ranks rank_warps(const Slice& s, int4* cnt, int need, int rank) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Ranks o = {0, 0, 0, 0};
+  int4 e[R];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(~0u, inc, o);
-        if (lane >= o) inc += u;
-      }
-      const int eb = run_eq + inc - (e0 + e1);
-      const int k0 = min(max(need - eb, 0), e0), k1 = min(max(need - eb - e0, 0), e1);
-      const int first = min(n, (w / EW) * sl) + (w % EW) * wl;
-      const int last = min(first + wl, min(n, (w / EW) * sl + sl));
-      const int slots_lo = max(0, min(last, m) - first);
-      const int mv = a1 + k1, ho = slots_lo - a0 - k0;
-      int im = mv, ih = ho;
+  for (int q = 0; q < R; ++q) e[q] = R > 1 ? *cl.map_shared_rank(&cnt[lane], q) : cnt[lane];
+  int run_eq = 0, run_mv = 0, run_ho = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(~0u, im, o), v = __shfl_up_sync(~0u, ih, o);
-        if (lane >= o) im += u, ih += v;
-      }
-      if (g == (me & ~31)) {
-        eq_before = __shfl_sync(~0u, eb, me & 31);
-        movers = run_mv + __shfl_sync(~0u, im - mv, me & 31);
-        holes = run_ho + __shfl_sync(~0u, ih - ho, me & 31);
-      }
-      run_eq += __shfl_sync(~0u, inc, 31);
-      run_mv += __shfl_sync(~0u, im, 31);
-      run_ho += __shfl_sync(~0u, ih, 31);
+  for (int q = 0; q < R; ++q) {
+    const int eqs = e[q].z + e[q].w;
+    int inc = eqs;
+#pragma unroll
+    for (int o2 = 1; o2 < 32; o2 <<= 1) {
+      const int u = __shfl_up_sync(~0u, inc, o2);
+      if (lane >= o2) inc += u;
     }
-    all_movers = run_mv;
+    const int eb = run_eq + inc - eqs;
+    const int k0 = min(max(need - eb, 0), e[q].z), k1 = min(max(need - eb - e[q].z, 0), e[q].w);
+    const int r0 = min(s.n, q * s.sl), r1 = min(s.n, r0 + s.sl);
+    const int first = min(r1, r0 + lane * s.wl), last = min(r1, first + s.wl);
+    const int mv = e[q].y + k1, ho = max(0, min(last, s.m) - first) - e[q].x - k0;
+    int im = mv, ih = ho;
+#pragma unroll
+    for (int o2 = 1; o2 < 32; o2 <<= 1) {
+      const int u = __shfl_up_sync(~0u, im, o2), v = __shfl_up_sync(~0u, ih, o2);
+      if (lane >= o2) im += u, ih += v;
+    }
+    if (q == rank) {
+      o.eq = __shfl_sync(~0u, eb, warp);
+      o.movers = run_mv + __shfl_sync(~0u, im - mv, warp);
+      o.holes = run_ho + __shfl_sync(~0u, ih - ho, warp);
+    }
+    run_eq += __shfl_sync(~0u, inc, 31);
+    run_mv += __shfl_sync(~0u, im, 31);
+    run_ho += __shfl_sync(~0u, ih, 31);
   }
-  int32_t* mover_list = p.lists + stream * 2 * m;
-  int32_t* hole_list = mover_list + m;
+  o.all_movers = run_mv;
+  return o;
+}
+
+// Writes the movers and freed slots of 32 slots from t0 on, given as bit masks,
+// into the lists.  The ranks are below m; the checks hold that too where
+// another stream writes the weights meanwhile and passes see different keys.
+__device__ __forceinline__ void list_word(const Slice& s, Ranks& k, int t0, unsigned mv, unsigned ho) {
+  const int lane = threadIdx.x & 31;
   const unsigned below = (1u << lane) - 1u;
-  for (int t0 = w0; t0 < w1; t0 += 32) {
-    const int t = t0 + lane;
-    const bool in = t < w1;
-    const uint32_t k = in ? key(t) : 0u;
-    const unsigned same = __ballot_sync(~0u, in && equal(k));
-    const bool keep = in && (above(k) || ((same >> lane & 1) && eq_before + __popc(same & below) < need));
-    const unsigned mv = __ballot_sync(~0u, keep && t >= m), ho = __ballot_sync(~0u, in && !keep && t < m);
-    // The ranks are below m; the checks hold that too where another stream
-    // writes the weights meanwhile and the passes see different keys.
-    const int im = movers + __popc(mv & below), ih = holes + __popc(ho & below);
-    if (keep && t >= m && im < m) mover_list[im] = t;
-    if (in && t < m) {
-      if (keep)
-        src[t] = t;
-      else if (ih >= 0 && ih < m)
-        hole_list[ih] = t;
+  const int im = k.movers + __popc(mv & below), ih = k.holes + __popc(ho & below);
+  if ((mv >> lane & 1) && im >= 0 && im < s.m) s.movers[im] = t0 + lane;
+  if ((ho >> lane & 1) && ih >= 0 && ih < s.m) s.holes[ih] = t0 + lane;
+  k.movers += __popc(mv);
+  k.holes += __popc(ho);
+}
+
+// The i-th freed slot receives the i-th mover.
+template <int R>
+__device__ __forceinline__ void fill_holes(const Slice& s, int all_movers, int rank) {
+  cluster_barrier<R>();                   // lists are complete, and no rank's counts are read any more
+  for (int i = rank * ET + threadIdx.x; i < min(all_movers, s.m); i += R * ET) {
+    const int t = s.holes[i];
+    if (t >= 0 && t < s.m) s.src[t] = s.movers[i];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// select, short slices: every key stays in a register, slot w0 + 32 j + lane in
+// register j, so that a ballot is 32 slots in order.  Each level has a
+// histogram of its own and costs one cluster barrier: nothing that another rank
+// still reads is written again.
+// grid: streams * R, cluster R; block 1024
+// ---------------------------------------------------------------------------
+template <int R, int KPT>
+__global__ void __launch_bounds__(ET, 1) evict_select_kernel(const __grid_constant__ EvictParams p) {
+  __shared__ int hist[E_BINS + 2 * (E_BINS / 2)];
+  __shared__ int ws[EW];
+  __shared__ int4 cnt[EW];
+  __shared__ int pick[3];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int rank = R > 1 ? (int)cg::this_cluster().block_rank() : 0;
+  griddep_launch();
+  Slice s;
+  if (!slice_of<R>(p, rank, s)) return;
+  uint32_t key[KPT];
+  {
+    float a[KPT];
+    int q[KPT];
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      const int t = s.w0 + 32 * j + lane;
+      if (t < s.w1) a[j] = s.acc[t], q[j] = s.pos[t];
     }
-    eq_before += __popc(same);
-    movers += __popc(mv);
-    holes += __popc(ho);
+    for (int i = tid; i < 2 * E_BINS; i += ET) hist[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      key[j] = 0;
+      if (s.w0 + 32 * j + lane < s.w1) {
+        key[j] = form_key(s, a[j], q[j]);
+        atomicAdd(&hist[key[j] >> 20], 1);
+      }
+    }
   }
-  sync_all();                             // lists are complete (and no rank's counts are read any more)
-  for (int i = rank * ET + tid; i < min(all_movers, m); i += R * ET) {
-    const int t = hole_list[i];
-    if (t >= 0 && t < m) src[t] = mover_list[i];
+  // the m-th largest key, 11 + 10 + 10 bits at a time: keys > lim are kept, and
+  // of those equal to lim the `need` with the lowest slots
+  uint32_t lim = 0;
+  int need = s.m;
+#pragma unroll
+  for (int level = 0; level < 3; ++level) {
+    constexpr int kShift[3] = {20, 10, 0}, kBase[3] = {0, E_BINS, E_BINS + E_BINS / 2};
+    const int shift = kShift[level];
+    int* hl = hist + kBase[level];
+    if (level > 0) {
+#pragma unroll
+      for (int j = 0; j < KPT; ++j)
+        if (s.w0 + 32 * j + lane < s.w1 && (key[j] ^ lim) >> (shift + 10) == 0u)
+          atomicAdd(&hl[(key[j] >> shift) & 1023], 1);
+    }
+    cluster_barrier<R>();
+    pick_bin<R>(hl, level == 0 ? E_BINS : E_BINS / 2, need, ws, pick);
+    lim |= (uint32_t)pick[0] << shift;
+    need -= pick[1];
+    if (pick[2] == need) {                // the whole bin is kept: keys > lim - 1
+      need = 0;
+      break;
+    }
   }
+  const int64_t over = need == 0 ? (int64_t)lim - 1 : (int64_t)lim;
+  {
+    int c0 = 0, c1 = 0, c2 = 0, c3 = 0;
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      const int t = s.w0 + 32 * j + lane;
+      const int u = t < s.w1 && (int64_t)key[j] > over, e = t < s.w1 && need && key[j] == lim;
+      if (t < s.m) c0 += u, c2 += e; else c1 += u, c3 += e;
+    }
+    c0 = __reduce_add_sync(~0u, c0);
+    c1 = __reduce_add_sync(~0u, c1);
+    c2 = __reduce_add_sync(~0u, c2);
+    c3 = __reduce_add_sync(~0u, c3);
+    if (lane == 0) cnt[tid >> 5] = make_int4(c0, c1, c2, c3);
+  }
+  cluster_barrier<R>();
+  Ranks k = rank_warps<R>(s, cnt, need, rank);
+  const unsigned below = (1u << lane) - 1u;
+#pragma unroll
+  for (int j = 0; j < KPT; ++j) {
+    const int t0 = s.w0 + 32 * j, t = t0 + lane;
+    if (t0 < s.w1) {
+      const bool in = t < s.w1;
+      bool keep = in && (int64_t)key[j] > over;
+      const unsigned eq = __ballot_sync(~0u, in && need && key[j] == lim);
+      if (eq >> lane & 1) keep = k.eq + __popc(eq & below) < need;
+      k.eq += __popc(eq);
+      if (keep && t < s.m) s.src[t] = t;
+      const unsigned mv = __ballot_sync(~0u, keep && t >= s.m), ho = __ballot_sync(~0u, in && !keep && t < s.m);
+      list_word(s, k, t0, mv, ho);
+    }
+  }
+  fill_holes<R>(s, k.all_movers, rank);
+}
+
+// ---------------------------------------------------------------------------
+// select, long slices: the keys do not fit, and most are far below the m-th
+// largest.  A sample of 1024 keys a CTA gives a bound that, with five standard
+// deviations to spare, fewer than m keys do not reach; one pass over the cache
+// counts the keys from the bound on and lists them, per warp in slot order, in
+// the workspace; all that follows reads the lists alone.  Where the bound was
+// too high after all (the histogram tells), the pass is done again without one.
+// grid: streams * R, cluster R; block 1024
+// ---------------------------------------------------------------------------
+template <int R>
+__global__ void __launch_bounds__(ET, 1) evict_select_long_kernel(const __grid_constant__ EvictParams p) {
+  __shared__ int sample[E_BINS];
+  __shared__ int hist[2][E_BINS + 2 * (E_BINS / 2)];
+  __shared__ int ws[EW];
+  __shared__ int4 cnt[EW];
+  __shared__ int pick[3];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const unsigned below = (1u << lane) - 1u;
+  const int rank = R > 1 ? (int)cg::this_cluster().block_rank() : 0;
+  griddep_launch();
+  Slice s;
+  if (!slice_of<R>(p, rank, s)) return;
+  uint2* list = p.listed + (blockIdx.x / R) * p.list_slots + s.w0;
+  for (int i = tid; i < E_BINS; i += ET) sample[i] = 0;
+  for (int i = tid; i < 4 * E_BINS; i += ET) (&hist[0][0])[i] = 0;
+  __syncthreads();
+  // sample: slot i of every (s1 - s0) / 1024
+  const int64_t len = s.s1 - s.s0;
+  const int mine_at = s.s0 + (int)(len * tid / ET);
+  const bool sampled = len > 0;
+  if (sampled) atomicAdd(&sample[form_key(s, s.acc[mine_at], s.pos[mine_at]) >> 20], 1);
+  for (int t = s.w0 + lane; t < min(s.w1, s.m); t += 32) s.src[t] = -1;    // marks freed slots
+  cluster_barrier<R>();
+  // every CTA with slots has ET samples; expected above the m-th key: part * m / n
+  const int ctas = (s.n + s.sl - 1) / s.sl;
+  const float want = (float)ctas * ET * ((float)s.m / (float)s.n);
+  const int goal = (int)(want + 5.f * sqrtf(want) + 16.f);
+  uint32_t floor_key = 0;
+  if (goal < ctas * ET / 2) {
+    pick_bin<R>(sample, E_BINS, goal, ws, pick);
+    floor_key = (uint32_t)pick[0] << 20;
+  }
+  int held = 0;                           // keys in this warp's list
+  uint32_t lim = 0;
+  int need = s.m;
+  int* h0 = hist[0];
+#pragma unroll 1
+  for (int attempt = 0; attempt < 2; ++attempt) {
+    held = 0;
+    h0 = hist[attempt];
+    auto put = [&](uint32_t k, int t, bool in) {
+      if (in) atomicAdd(&h0[k >> 20], 1);
+      const unsigned w = __ballot_sync(~0u, in);
+      if (in) list[held + __popc(w & below)] = make_uint2(k, (uint32_t)t);
+      held += __popc(w);
+    };
+    constexpr int U = 8;                  // words of 32 slots in flight
+    for (int t0 = s.w0; t0 < s.w1; t0 += 32 * U) {
+      float a[U];
+      int q[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int t = t0 + 32 * j + lane;
+        a[j] = 0.f, q[j] = 0;
+        if (t < s.w1) a[j] = s.acc[t], q[j] = s.pos[t];
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int t = t0 + 32 * j + lane;
+        const uint32_t k = form_key(s, a[j], q[j]);
+        const bool in = t < s.w1 && k >= floor_key;
+        if (__any_sync(~0u, in)) put(k, t, in);
+      }
+    }
+    __syncwarp();
+    cluster_barrier<R>();
+    const int all = pick_bin<R>(h0, E_BINS, need, ws, pick);
+    if (all >= need || floor_key == 0) break;
+    floor_key = 0;                        // uniform in the cluster: all ranks see the same counts
+  }
+#pragma unroll
+  for (int level = 0; level < 3; ++level) {
+    constexpr int kShift[3] = {20, 10, 0}, kBase[3] = {0, E_BINS, E_BINS + E_BINS / 2};
+    const int shift = kShift[level];
+    int* hl = h0 + kBase[level];
+    if (level > 0) {
+#pragma unroll 4
+      for (int i = lane; i < held; i += 32) {
+        const uint32_t k = list[i].x;
+        if ((k ^ lim) >> (shift + 10) == 0u) atomicAdd(&hl[(k >> shift) & 1023], 1);
+      }
+      cluster_barrier<R>();
+      pick_bin<R>(hl, E_BINS / 2, need, ws, pick);
+    }
+    lim |= (uint32_t)pick[0] << shift;
+    need -= pick[1];
+    if (pick[2] == need) {
+      need = 0;
+      break;
+    }
+  }
+  const int64_t over = need == 0 ? (int64_t)lim - 1 : (int64_t)lim;
+  {
+    int c0 = 0, c1 = 0, c2 = 0, c3 = 0;
+#pragma unroll 4
+    for (int i = lane; i < held; i += 32) {
+      const uint2 v = list[i];
+      const int u = (int64_t)v.x > over, e = need && v.x == lim;
+      if ((int)v.y < s.m) c0 += u, c2 += e; else c1 += u, c3 += e;
+    }
+    c0 = __reduce_add_sync(~0u, c0);
+    c1 = __reduce_add_sync(~0u, c1);
+    c2 = __reduce_add_sync(~0u, c2);
+    c3 = __reduce_add_sync(~0u, c3);
+    if (lane == 0) cnt[tid >> 5] = make_int4(c0, c1, c2, c3);
+  }
+  cluster_barrier<R>();
+  Ranks k = rank_warps<R>(s, cnt, need, rank);
+  for (int i0 = 0; i0 < held; i0 += 32) {
+    const bool in = i0 + lane < held;
+    const uint2 v = in ? list[i0 + lane] : make_uint2(0u, 0u);
+    const int t = (int)v.y;
+    bool keep = in && (int64_t)v.x > over;
+    const unsigned eq = __ballot_sync(~0u, in && need && v.x == lim);
+    if (eq >> lane & 1) keep = k.eq + __popc(eq & below) < need;
+    k.eq += __popc(eq);
+    if (keep && t < s.m) s.src[t] = t;
+    const unsigned mv = __ballot_sync(~0u, keep && t >= s.m);
+    const int im = k.movers + __popc(mv & below);
+    if ((mv >> lane & 1) && im >= 0 && im < s.m) s.movers[im] = t;
+    k.movers += __popc(mv);
+  }
+  __syncwarp();
+  // slots below m that were not kept; the warp's own marks
+#pragma unroll 4
+  for (int t0 = s.w0; t0 < min(s.w1, s.m); t0 += 32) {
+    const int t = t0 + lane;
+    const unsigned ho = __ballot_sync(~0u, t < min(s.w1, s.m) && s.src[t] < 0);
+    list_word(s, k, t0, 0u, ho);
+  }
+  fill_holes<R>(s, k.all_movers, rank);
 }
 
 // ---------------------------------------------------------------------------
@@ -314,14 +523,33 @@ __global__ void __launch_bounds__(MT) evict_move_kernel(const __grid_constant__ 
 
 }  // namespace
 
+namespace {
+
+// Slots of a CTA of a stream of n tokens.
+int64_t evict_slice(int64_t n, int R) { return ((n + R - 1) / R + ET - 1) / ET * ET; }
+
+template <int R>
+cudaError_t select_r(const EvictParams& p, cudaStream_t st) {
+  const dim3 grid((unsigned)((int64_t)p.B * p.H * R));
+  const int64_t sl = evict_slice(p.limit, R);
+  if (sl <= 8 * ET) return launch_kernel(evict_select_kernel<R, 8>, grid, dim3(ET), 0, st, false, R, p);
+  if (sl <= E_SHORT) return launch_kernel(evict_select_kernel<R, E_SHORT / ET>, grid, dim3(ET), 0, st, false, R, p);
+  return launch_kernel(evict_select_long_kernel<R>, grid, dim3(ET), 0, st, false, R, p);
+}
+
+}  // namespace
+
+int64_t evict_list_slots(int64_t limit, int R) {
+  return evict_slice(limit, R) <= E_SHORT ? 0 : limit;
+}
+
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t st) {
-  const int sl = ((p.limit + p.R - 1) / p.R + ET - 1) / ET * ET;
-  const int cap = sl < E_CAP ? sl : E_CAP;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       E_CAP * 4);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(evict_select_kernel, dim3((unsigned)((int64_t)p.B * p.H * p.R)), dim3(ET),
-                       (size_t)cap * 4, st, false, p.R, p, cap);
+  switch (p.R) {
+    case 1: return select_r<1>(p, st);
+    case 2: return select_r<2>(p, st);
+    case 4: return select_r<4>(p, st);
+    default: return select_r<8>(p, st);
+  }
 }
 
 cudaError_t launch_evict_move(const EvictParams& p, cudaStream_t st) {

@@ -141,12 +141,37 @@ DecodeLayout decode_layout(const mkv_paged_cache* c, const mkv_paged_decode_args
 
 // ---- evict -------------------------------------------------------------------
 
+int64_t evict_limit(const mkv_paged_cache* c, const mkv_paged_evict_args* a) {
+  return a->max_len ? a->max_len : (int64_t)c->max_pages * c->page_size;
+}
+
+// Bytes of the lists of movers and freed slots.
+uint64_t evict_list_bytes(const mkv_paged_cache* c, const mkv_paged_evict_args* a) {
+  return ((uint64_t)c->batch * c->n_kv_heads * 2 * a->budget * 4 + 255) & ~(uint64_t)255;
+}
+
+// CTAs of a stream: doubled while all fit the SMs at once and a CTA keeps 4096
+// slots or more (a cluster's barriers cost more than shorter passes save: one
+// CTA takes 21 us for 64 streams of 4097 tokens, two 26).
+int evict_ranks(const mkv_paged_cache* c, int64_t limit, int sms) {
+  const int64_t streams = (int64_t)c->batch * c->n_kv_heads;
+  int R = 1;
+  while (R < 8 && streams * 2 * R <= sms && limit >= 8192 * (int64_t)R) R *= 2;
+  return R;
+}
+
+uint64_t evict_bytes(const mkv_paged_cache* c, const mkv_paged_evict_args* a, int sms) {
+  const int64_t limit = evict_limit(c, a);
+  return evict_list_bytes(c, a) +
+         (uint64_t)c->batch * c->n_kv_heads * evict_list_slots(limit, evict_ranks(c, limit, sms)) * 8;
+}
+
 const char* check_evict(const mkv_paged_cache* c, const mkv_paged_evict_args* a) {
   if (const char* e = check_cache(c)) return e;
   if (!a) return "mkv_paged_evict: NULL arguments";
-  const int64_t cap = (int64_t)c->max_pages * c->page_size;
-  if (a->max_len < 0 || a->max_len > cap) return "mkv_paged_evict: max_len must be 0..max_pages * page_size";
-  const int64_t limit = a->max_len ? a->max_len : cap;
+  if (a->max_len < 0 || a->max_len > (int64_t)c->max_pages * c->page_size)
+    return "mkv_paged_evict: max_len must be 0..max_pages * page_size";
+  const int64_t limit = evict_limit(c, a);
   if (a->budget < 1) return "mkv_paged_evict: budget must be >= 1";
   if (a->sink < 0 || a->recent < 0 || (int64_t)a->sink + a->recent > a->budget)
     return "mkv_paged_evict: sink and recent must be >= 0 and together at most the budget";
@@ -440,7 +465,9 @@ uint64_t mkv_paged_evict_workspace(const mkv_paged_cache* c, const mkv_paged_evi
     bad(e);
     return 0;
   }
-  return (uint64_t)c->batch * c->n_kv_heads * 2 * a->budget * 4;
+  int sms = 0;
+  if (sm_count(&sms) != MKV_OK) return 0;
+  return evict_bytes(c, a, sms);
 }
 
 mkv_status mkv_paged_evict(const mkv_paged_cache* c, const mkv_paged_evict_args* a, mkv_stream_t stream) {
@@ -451,10 +478,11 @@ mkv_status mkv_paged_evict(const mkv_paged_cache* c, const mkv_paged_evict_args*
       a->out_stride != a->meta_stride)
     return bad("mkv_paged_evict: in place, out_stride must be meta_stride");
   if (!a->workspace || !aligned16(a->workspace)) return bad("mkv_paged_evict: workspace must be 16-byte aligned");
-  if (a->workspace_bytes < mkv_paged_evict_workspace(c, a)) return bad("mkv_paged_evict: workspace too small");
+  if (a->workspace_bytes < evict_list_bytes(c, a)) return bad("mkv_paged_evict: workspace too small");
   int sms = 0;
   mkv_status s = sm_count(&sms);
   if (s != MKV_OK) return s;
+  if (a->workspace_bytes < evict_bytes(c, a, sms)) return bad("mkv_paged_evict: workspace too small");
   EvictParams p;
   std::memset(&p, 0, sizeof(p));
   p.kp = static_cast<uint8_t*>(c->k_pages);
@@ -467,7 +495,7 @@ mkv_status mkv_paged_evict(const mkv_paged_cache* c, const mkv_paged_evict_args*
   p.n_pages = c->n_pages;
   p.ps = c->page_size;
   p.row_bytes = c->head_dim * elem_bytes(c->dtype);
-  p.limit = (int)(a->max_len ? a->max_len : (int64_t)c->max_pages * c->page_size);
+  p.limit = (int)evict_limit(c, a);
   p.acc = a->acc;
   p.pos = a->pos;
   p.acc_out = a->acc_out;
@@ -481,11 +509,11 @@ mkv_status mkv_paged_evict(const mkv_paged_cache* c, const mkv_paged_evict_args*
   p.budget = a->budget;
   p.sink = a->sink;
   p.recent = a->recent;
+  const uint64_t lists = evict_list_bytes(c, a);
   p.lists = static_cast<int32_t*>(a->workspace);
-  // CTAs of a stream: while they fit the SMs and each has 4096 slots or more
-  const int64_t streams = (int64_t)p.B * p.H;
-  p.R = 1;
-  while (p.R < 8 && streams * 2 * p.R <= sms && (int64_t)p.limit >= 8192 * (int64_t)p.R) p.R *= 2;
+  p.R = evict_ranks(c, p.limit, sms);
+  p.listed = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a->workspace) + lists);
+  p.list_slots = evict_list_slots(p.limit, p.R);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   CKP(launch_evict_select(p, st));
   CKP(launch_evict_move(p, st));

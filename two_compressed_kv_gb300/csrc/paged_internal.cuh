@@ -135,8 +135,12 @@ struct EvictParams {
   int64_t meta_stride, out_stride;
   int budget, sink, recent;
   int32_t* lists;                 // workspace: [B H][2][budget] movers, then holes
+  uint2* listed;                  // workspace: [B H][list_slots] (key, slot), long slices only
+  int64_t list_slots;
   int R;                          // CTAs (one cluster) per stream
 };
+// Entries of `listed` a stream needs: 0 where slices are short.
+int64_t evict_list_slots(int64_t limit, int R);
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t st);
 cudaError_t launch_evict_move(const EvictParams& p, cudaStream_t st);
 
