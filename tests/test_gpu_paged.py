@@ -558,6 +558,22 @@ def test_evict_ties_and_odd_weights(M, name, n):
     evict_case(M, [n, n // 2 + 1], 1, 64, 128, n // 3, 2, n // 16, weights=weights, seed=n, in_place=name == "odd")
 
 
+@pytest.mark.parametrize("few", [1, 2, 4, 5])
+def test_evict_a_few(M, few):
+    """As many tokens over the budget as are found one by one, and one more; ties; one to eight CTAs;
+    the tokens that leave below, at and behind the budget's end."""
+    ties = lambda b, h, s, g: (torch.rand((b, h, s), generator=g) * 50).floor()
+    same = lambda b, h, s, g: torch.full((b, h, s), 2.0)
+    first = lambda b, h, s, g: torch.arange(s, dtype=torch.float32).expand(b, h, s).contiguous()
+    last = lambda b, h, s, g: -first(b, h, s, g) + s + 1
+    for w in (None, ties, same, first, last):
+        evict_case(M, [96 + few, 97, 96, 3], 2, 64, 16, 96, 4, 10, weights=w, seed=few)
+        evict_case(M, [few + 1, few + 1], 2, 64, 16, 1, 0, 0, weights=w, seed=few, in_place=True)
+        evict_case(M, [4096 + few] * 2, 2, 64, 256, 4096, 4, 64, E4M3, weights=w, seed=few)
+        evict_case(M, [16384 + few], 2, 64, 256, 16384, 0, 16384 - 2, E4M3, weights=w, seed=few)
+        evict_case(M, [70000 + few], 1, 64, 256, 70000, 4, 64, E4M3, weights=w, seed=few)
+
+
 def test_evict_sizes_of_cluster(M):
     """1, 2, 4 and 8 CTAs a stream; slices of 8 and 16 keys a thread, and longer ones."""
     evict_case(M, [8191, 4097], 1, 64, 256, 4096, 4, 100, E4M3, seed=1)

@@ -108,24 +108,37 @@ __device__ __forceinline__ bool slice_of(const EvictParams& p, int rank, Slice& 
   return true;
 }
 
-// The bin of the `need`-th largest key, from the ranks' histograms of `bins`
-// bins: pick = {bin, keys in bins above, keys in it}.  Returns the keys in all.
-// Ends with a block barrier.
+// Adds this CTA's histogram into every rank's `total` (few of its bins are in
+// use: a push of those costs less than every rank's reading of R whole
+// histograms, 10 against 2 thousand cycles for 2048 bins of 8 ranks), then
+// finds the bin of the `need`-th largest key: pick = {bin, keys in bins above,
+// keys in it}.  Returns the keys in all.  `total` must be zero in every rank.
 template <int R>
-__device__ __forceinline__ int pick_bin(int* hist, int bins, int need, int* ws, int* pick) {
-  cg::cluster_group cl = cg::this_cluster();
+__device__ __forceinline__ int pick_bin(int* hist, int* total, int bins, int need, int* ws, int* pick) {
   constexpr int MAXPER = E_BINS / ET;
   const int per = bins / ET;
+  if constexpr (R > 1) {
+    cg::cluster_group cl = cg::this_cluster();
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < MAXPER; ++x)
+      if (x < per) {
+        const int bin = x * ET + (int)threadIdx.x, v = hist[bin];
+        if (v) {
+#pragma unroll
+          for (int q = 0; q < R; ++q) atomicAdd(cl.map_shared_rank(&total[bin], q), v);
+        }
+      }
+    cl.sync();
+  } else {
+    __syncthreads();
+    total = hist;
+  }
   int mine[MAXPER] = {}, sum = 0;
 #pragma unroll
   for (int x = 0; x < MAXPER; ++x)
     if (x < per) {
-      const int bin = bins - 1 - ((int)threadIdx.x * per + x);   // from the top
-      int v[R];
-#pragma unroll
-      for (int q = 0; q < R; ++q) v[q] = R > 1 ? *cl.map_shared_rank(&hist[bin], q) : hist[bin];
-#pragma unroll
-      for (int q = 0; q < R; ++q) mine[x] += v[q];
+      mine[x] = total[bins - 1 - ((int)threadIdx.x * per + x)];   // from the top
       sum += mine[x];
     }
   int all;
@@ -218,41 +231,122 @@ __device__ __forceinline__ void fill_holes(const Slice& s, int all_movers, int r
 // ---------------------------------------------------------------------------
 // select, short slices: every key stays in a register, slot w0 + 32 j + lane in
 // register j, so that a ballot is 32 slots in order.  Each level has a
-// histogram of its own and costs one cluster barrier: nothing that another rank
-// still reads is written again.
+// histogram of its own: nothing that another rank still needs is written again.
+//
+// In the steady state few tokens leave (one a step): up to E_FEW of them are
+// found one by one as the smallest (key, highest slot) instead, without any
+// histogram, and every thread then knows them all.
 // grid: streams * R, cluster R; block 1024
 // ---------------------------------------------------------------------------
+constexpr int E_FEW = 4;
+constexpr int E_HIST = E_BINS + 2 * (E_BINS / 2);   // three levels
+
 template <int R, int KPT>
 __global__ void __launch_bounds__(ET, 1) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ int hist[E_BINS + 2 * (E_BINS / 2)];
+  __shared__ int hist[E_HIST], total[R > 1 ? E_HIST : 1];
   __shared__ int ws[EW];
   __shared__ int4 cnt[EW];
   __shared__ int pick[3];
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int rank = R > 1 ? (int)cg::this_cluster().block_rank() : 0;
+  __shared__ uint2 least[2][EW], leave[E_FEW], left[E_FEW];
+  cg::cluster_group cl = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = R > 1 ? (int)cl.block_rank() : 0;
   griddep_launch();
   Slice s;
   if (!slice_of<R>(p, rank, s)) return;
+  float a[KPT];
+  int pos[KPT];
+#pragma unroll
+  for (int j = 0; j < KPT; ++j) {
+    const int t = s.w0 + 32 * j + lane;
+    if (t < s.w1) a[j] = s.acc[t], pos[j] = s.pos[t];
+  }
   uint32_t key[KPT];
-  {
-    float a[KPT];
-    int q[KPT];
+  auto form = [&](int j) {
+    key[j] = s.w0 + 32 * j + lane < s.w1 ? form_key(s, a[j], pos[j]) : 0u;
+  };
+  if (s.n - s.m <= E_FEW) {
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) form(j);
+    // smallest key, of equal ones the highest slot: (key, ~slot) ascending
+    const int few = s.n - s.m;
+    unsigned gone = 0;                    // registers whose token leaves
+    for (int e = 0; e < few; ++e) {
+      uint32_t k = ~0u, inv = ~0u;        // ~slot
+#pragma unroll
+      for (int j = 0; j < KPT; ++j) {
+        const int t = s.w0 + 32 * j + lane;
+        if (t < s.w1 && !(gone >> j & 1) && key[j] <= k) k = key[j], inv = ~(uint32_t)t;
+      }
+      const uint32_t wk = __reduce_min_sync(~0u, k);
+      const uint32_t wi = __reduce_min_sync(~0u, k == wk ? inv : ~0u);
+      if (lane == 0) least[e & 1][warp] = make_uint2(wk, wi);
+      __syncthreads();
+      const uint2 v = least[e & 1][lane];
+      const uint32_t bk = __reduce_min_sync(~0u, v.x);
+      const uint32_t bi = __reduce_min_sync(~0u, v.x == bk ? v.y : ~0u);
+#pragma unroll
+      for (int j = 0; j < KPT; ++j)
+        if (~(uint32_t)(s.w0 + 32 * j + lane) == bi) gone |= 1u << j;
+      if (tid == 0) (R > 1 ? leave : left)[e] = make_uint2(bk, bi);
+    }
+    if constexpr (R > 1) {
+      // of every rank's smallest, the smallest
+      cl.sync();
+      if (warp == 0) {
+        uint2 v = make_uint2(~0u, ~0u);
+        if (lane < R * E_FEW && lane % E_FEW < few) v = *cl.map_shared_rank(&leave[lane % E_FEW], lane / E_FEW);
+        for (int e = 0; e < few; ++e) {
+          const uint32_t k = __reduce_min_sync(~0u, v.x);
+          const uint32_t i = __reduce_min_sync(~0u, v.x == k ? v.y : ~0u);
+          if (lane == 0) left[e] = make_uint2(k, i);
+          if (v.y == i) v = make_uint2(~0u, ~0u);
+        }
+      }
+      cl.sync();                          // no rank's candidates are read any more
+    } else {
+      __syncthreads();
+    }
+    // the slots that leave, and the kept ones from slot m on, in order
+    int out[E_FEW];
+#pragma unroll
+    for (int e = 0; e < E_FEW; ++e) out[e] = e < few ? (int)~left[e].y : 0x7fffffff;
 #pragma unroll
     for (int j = 0; j < KPT; ++j) {
       const int t = s.w0 + 32 * j + lane;
-      if (t < s.w1) a[j] = s.acc[t], q[j] = s.pos[t];
-    }
-    for (int i = tid; i < 2 * E_BINS; i += ET) hist[i] = 0;
-    __syncthreads();
+      if (t < s.w1 && t < s.m) {
+        int from = t, place = 0;
+        bool is_out = false;
 #pragma unroll
-    for (int j = 0; j < KPT; ++j) {
-      key[j] = 0;
-      if (s.w0 + 32 * j + lane < s.w1) {
-        key[j] = form_key(s, a[j], q[j]);
-        atomicAdd(&hist[key[j] >> 20], 1);
+        for (int e = 0; e < E_FEW; ++e) is_out |= out[e] == t, place += out[e] < t;
+        if (is_out) {
+          // the place-th of slots m .. n - 1 that stay
+          int k = -1;
+          for (from = s.m - 1; k < place && from < s.n - 1;) {
+            ++from;
+            bool stays = true;
+#pragma unroll
+            for (int e = 0; e < E_FEW; ++e) stays &= out[e] != from;
+            k += stays;
+          }
+        }
+        s.src[t] = from;
       }
     }
+    return;
   }
+  for (int i = tid; i < E_HIST; i += ET) {
+    hist[i] = 0;
+    if constexpr (R > 1) total[i] = 0;
+  }
+  if constexpr (R > 1) cl.barrier_arrive();   // totals are zero
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < KPT; ++j) {
+    form(j);
+    if (s.w0 + 32 * j + lane < s.w1) atomicAdd(&hist[key[j] >> 20], 1);
+  }
+  if constexpr (R > 1) cl.barrier_wait();
   // the m-th largest key, 11 + 10 + 10 bits at a time: keys > lim are kept, and
   // of those equal to lim the `need` with the lowest slots
   uint32_t lim = 0;
@@ -268,8 +362,7 @@ __global__ void __launch_bounds__(ET, 1) evict_select_kernel(const __grid_consta
         if (s.w0 + 32 * j + lane < s.w1 && (key[j] ^ lim) >> (shift + 10) == 0u)
           atomicAdd(&hl[(key[j] >> shift) & 1023], 1);
     }
-    cluster_barrier<R>();
-    pick_bin<R>(hl, level == 0 ? E_BINS : E_BINS / 2, need, ws, pick);
+    pick_bin<R>(hl, total + (R > 1 ? kBase[level] : 0), level == 0 ? E_BINS : E_BINS / 2, need, ws, pick);
     lim |= (uint32_t)pick[0] << shift;
     need -= pick[1];
     if (pick[2] == need) {                // the whole bin is kept: keys > lim - 1
@@ -290,7 +383,7 @@ __global__ void __launch_bounds__(ET, 1) evict_select_kernel(const __grid_consta
     c1 = __reduce_add_sync(~0u, c1);
     c2 = __reduce_add_sync(~0u, c2);
     c3 = __reduce_add_sync(~0u, c3);
-    if (lane == 0) cnt[tid >> 5] = make_int4(c0, c1, c2, c3);
+    if (lane == 0) cnt[warp] = make_int4(c0, c1, c2, c3);
   }
   cluster_barrier<R>();
   Ranks k = rank_warps<R>(s, cnt, need, rank);
@@ -323,72 +416,108 @@ __global__ void __launch_bounds__(ET, 1) evict_select_kernel(const __grid_consta
 // ---------------------------------------------------------------------------
 template <int R>
 __global__ void __launch_bounds__(ET, 1) evict_select_long_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ int sample[E_BINS];
-  __shared__ int hist[2][E_BINS + 2 * (E_BINS / 2)];
+  // histograms: of the sample, and of each of two attempts at the pass
+  __shared__ int hist[E_BINS + 2 * E_HIST];
+  extern __shared__ int total[];          // R > 1: as hist, over all ranks
   __shared__ int ws[EW];
   __shared__ int4 cnt[EW];
+  __shared__ int freed[EW];
   __shared__ int pick[3];
-  const int tid = threadIdx.x, lane = tid & 31;
+  cg::cluster_group cl = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned below = (1u << lane) - 1u;
-  const int rank = R > 1 ? (int)cg::this_cluster().block_rank() : 0;
+  const int rank = R > 1 ? (int)cl.block_rank() : 0;
   griddep_launch();
   Slice s;
   if (!slice_of<R>(p, rank, s)) return;
   uint2* list = p.listed + (blockIdx.x / R) * p.list_slots + s.w0;
-  for (int i = tid; i < E_BINS; i += ET) sample[i] = 0;
-  for (int i = tid; i < 4 * E_BINS; i += ET) (&hist[0][0])[i] = 0;
+  for (int i = tid; i < E_BINS + 2 * E_HIST; i += ET) {
+    hist[i] = 0;
+    if constexpr (R > 1) total[i] = 0;
+  }
+  if constexpr (R > 1) cl.barrier_arrive();   // totals are zero
   __syncthreads();
-  // sample: slot i of every (s1 - s0) / 1024
+  // sample: every (s1 - s0) / 1024-th slot
   const int64_t len = s.s1 - s.s0;
-  const int mine_at = s.s0 + (int)(len * tid / ET);
-  const bool sampled = len > 0;
-  if (sampled) atomicAdd(&sample[form_key(s, s.acc[mine_at], s.pos[mine_at]) >> 20], 1);
-  for (int t = s.w0 + lane; t < min(s.w1, s.m); t += 32) s.src[t] = -1;    // marks freed slots
-  cluster_barrier<R>();
+  if (len > 0) {
+    const int t = s.s0 + (int)(len * tid / ET);
+    atomicAdd(&hist[form_key(s, s.acc[t], s.pos[t]) >> 20], 1);
+  }
+  // slots below m that are not kept in the end stay marked
+  for (int64_t t = rank * ET + tid; t < s.m; t += R * ET) s.src[t] = -1;
+  if constexpr (R > 1) cl.barrier_wait();
   // every CTA with slots has ET samples; expected above the m-th key: part * m / n
   const int ctas = (s.n + s.sl - 1) / s.sl;
   const float want = (float)ctas * ET * ((float)s.m / (float)s.n);
   const int goal = (int)(want + 5.f * sqrtf(want) + 16.f);
   uint32_t floor_key = 0;
   if (goal < ctas * ET / 2) {
-    pick_bin<R>(sample, E_BINS, goal, ws, pick);
+    pick_bin<R>(hist, total, E_BINS, goal, ws, pick);
     floor_key = (uint32_t)pick[0] << 20;
+  } else {
+    cluster_barrier<R>();                 // the marks come before any kept slot
   }
   int held = 0;                           // keys in this warp's list
   uint32_t lim = 0;
   int need = s.m;
-  int* h0 = hist[0];
+  int* h0 = hist;
+  int* t0h = total;
+  const bool wide = ((reinterpret_cast<uintptr_t>(s.acc) | reinterpret_cast<uintptr_t>(s.pos)) & 15u) == 0;
 #pragma unroll 1
   for (int attempt = 0; attempt < 2; ++attempt) {
     held = 0;
-    h0 = hist[attempt];
-    auto put = [&](uint32_t k, int t, bool in) {
-      if (in) atomicAdd(&h0[k >> 20], 1);
-      const unsigned w = __ballot_sync(~0u, in);
-      if (in) list[held + __popc(w & below)] = make_uint2(k, (uint32_t)t);
-      held += __popc(w);
+    h0 = hist + E_BINS + attempt * E_HIST;
+    t0h = total + E_BINS + attempt * E_HIST;
+    // 128 slots: lane i has 4 i .. 4 i + 3
+    auto put4 = [&](const uint32_t (&k)[4], int t) {
+      unsigned mine = 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mine |= (unsigned)(t + x < s.w1 && k[x] >= floor_key) << x;
+      if (!__any_sync(~0u, mine)) return;
+      int before = 0, all = 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const unsigned w = __ballot_sync(~0u, mine >> x & 1);
+        before += __popc(w & below);
+        all += __popc(w);
+      }
+      before += held;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (mine >> x & 1) {
+          atomicAdd(&h0[k[x] >> 20], 1);
+          list[before++] = make_uint2(k[x], (uint32_t)(t + x));
+        }
+      held += all;
     };
-    constexpr int U = 8;                  // words of 32 slots in flight
-    for (int t0 = s.w0; t0 < s.w1; t0 += 32 * U) {
-      float a[U];
-      int q[U];
+    constexpr int U = 4;                  // groups in flight
+    for (int g = s.w0; g < s.w1; g += 128 * U) {
+      float4 a[U];
+      int4 q[U];
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const int t = t0 + 32 * j + lane;
-        a[j] = 0.f, q[j] = 0;
-        if (t < s.w1) a[j] = s.acc[t], q[j] = s.pos[t];
+        const int t = g + 128 * j + 4 * lane;
+        a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        q[j] = make_int4(0, 0, 0, 0);
+        if (wide && t + 4 <= s.w1) {
+          a[j] = *reinterpret_cast<const float4*>(s.acc + t);
+          q[j] = *reinterpret_cast<const int4*>(s.pos + t);
+        } else {
+          if (t < s.w1) a[j].x = s.acc[t], q[j].x = s.pos[t];
+          if (t + 1 < s.w1) a[j].y = s.acc[t + 1], q[j].y = s.pos[t + 1];
+          if (t + 2 < s.w1) a[j].z = s.acc[t + 2], q[j].z = s.pos[t + 2];
+          if (t + 3 < s.w1) a[j].w = s.acc[t + 3], q[j].w = s.pos[t + 3];
+        }
       }
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const int t = t0 + 32 * j + lane;
-        const uint32_t k = form_key(s, a[j], q[j]);
-        const bool in = t < s.w1 && k >= floor_key;
-        if (__any_sync(~0u, in)) put(k, t, in);
+        const uint32_t k[4] = {form_key(s, a[j].x, q[j].x), form_key(s, a[j].y, q[j].y),
+                               form_key(s, a[j].z, q[j].z), form_key(s, a[j].w, q[j].w)};
+        put4(k, g + 128 * j + 4 * lane);
       }
     }
     __syncwarp();
-    cluster_barrier<R>();
-    const int all = pick_bin<R>(h0, E_BINS, need, ws, pick);
+    const int all = pick_bin<R>(h0, t0h, E_BINS, need, ws, pick);
     if (all >= need || floor_key == 0) break;
     floor_key = 0;                        // uniform in the cluster: all ranks see the same counts
   }
@@ -396,15 +525,14 @@ __global__ void __launch_bounds__(ET, 1) evict_select_long_kernel(const __grid_c
   for (int level = 0; level < 3; ++level) {
     constexpr int kShift[3] = {20, 10, 0}, kBase[3] = {0, E_BINS, E_BINS + E_BINS / 2};
     const int shift = kShift[level];
-    int* hl = h0 + kBase[level];
     if (level > 0) {
+      int* hl = h0 + kBase[level];
 #pragma unroll 4
       for (int i = lane; i < held; i += 32) {
         const uint32_t k = list[i].x;
         if ((k ^ lim) >> (shift + 10) == 0u) atomicAdd(&hl[(k >> shift) & 1023], 1);
       }
-      cluster_barrier<R>();
-      pick_bin<R>(hl, E_BINS / 2, need, ws, pick);
+      pick_bin<R>(hl, t0h + kBase[level], E_BINS / 2, need, ws, pick);
     }
     lim |= (uint32_t)pick[0] << shift;
     need -= pick[1];
@@ -426,10 +554,11 @@ __global__ void __launch_bounds__(ET, 1) evict_select_long_kernel(const __grid_c
     c1 = __reduce_add_sync(~0u, c1);
     c2 = __reduce_add_sync(~0u, c2);
     c3 = __reduce_add_sync(~0u, c3);
-    if (lane == 0) cnt[tid >> 5] = make_int4(c0, c1, c2, c3);
+    if (lane == 0) cnt[warp] = make_int4(c0, c1, c2, c3);
   }
   cluster_barrier<R>();
   Ranks k = rank_warps<R>(s, cnt, need, rank);
+#pragma unroll 2
   for (int i0 = 0; i0 < held; i0 += 32) {
     const bool in = i0 + lane < held;
     const uint2 v = in ? list[i0 + lane] : make_uint2(0u, 0u);
@@ -444,15 +573,30 @@ __global__ void __launch_bounds__(ET, 1) evict_select_long_kernel(const __grid_c
     if ((mv >> lane & 1) && im >= 0 && im < s.m) s.movers[im] = t;
     k.movers += __popc(mv);
   }
-  __syncwarp();
-  // slots below m that were not kept; the warp's own marks
+  cluster_barrier<R>();                   // kept slots are unmarked, movers listed
+  // freed slots, ranked over an even share of slots 0 .. m - 1 for every warp
+  const int share = ((s.m + R * EW - 1) / (R * EW) + 31) / 32 * 32;
+  const int f0 = min(s.m, (rank * EW + warp) * share), f1 = min(s.m, f0 + share);
+  int mine = 0;
 #pragma unroll 4
-  for (int t0 = s.w0; t0 < min(s.w1, s.m); t0 += 32) {
-    const int t = t0 + lane;
-    const unsigned ho = __ballot_sync(~0u, t < min(s.w1, s.m) && s.src[t] < 0);
-    list_word(s, k, t0, 0u, ho);
+  for (int t = f0 + lane; t < f1; t += 32) mine += __ldcg(s.src + t) < 0;
+  mine = __reduce_add_sync(~0u, mine);
+  if (lane == 0) freed[warp] = mine;
+  cluster_barrier<R>();
+  int rank_of = 0;                        // freed slots before this warp's
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    const int v = q <= rank ? (R > 1 ? *cl.map_shared_rank(&freed[lane], q) : freed[lane]) : 0;
+    rank_of += __reduce_add_sync(~0u, q < rank || (q == rank && lane < warp) ? v : 0);
   }
-  fill_holes<R>(s, k.all_movers, rank);
+  for (int t = f0 + lane; t - lane < f1; t += 32) {
+    const bool ho = t < f1 && __ldcg(s.src + t) < 0;
+    const unsigned w = __ballot_sync(~0u, ho);
+    const int i = rank_of + __popc(w & below);
+    if (ho && i < min(k.all_movers, s.m)) s.src[t] = __ldcg(s.movers + i);
+    rank_of += __popc(w);
+  }
+  if constexpr (R > 1) cl.sync();         // no rank's counts are read any more
 }
 
 // ---------------------------------------------------------------------------
@@ -460,10 +604,9 @@ __global__ void __launch_bounds__(ET, 1) evict_select_long_kernel(const __grid_c
 // ones, new lengths.  A group of row_bytes / 16 lanes copies a row.
 // grid: streams * chunks of MS slots
 // ---------------------------------------------------------------------------
-constexpr int MT = 256, MS = 64;
+constexpr int MT = 256, MS = 128;
 
 __global__ void __launch_bounds__(MT) evict_move_kernel(const __grid_constant__ EvictParams p, int chunks) {
-  __shared__ int32_t sm_src[MS];
   __shared__ int64_t to_row[MS], from_row[MS];   // -1: stays
   const int64_t stream = blockIdx.x / chunks;
   const int c0 = (int)(blockIdx.x - stream * chunks) * MS;
@@ -475,7 +618,6 @@ __global__ void __launch_bounds__(MT) evict_move_kernel(const __grid_constant__ 
     const int t = c0 + tid;
     int s = t < p.budget ? p.src[stream * p.budget + t] : -1;
     if (s >= p.limit) s = -1;
-    sm_src[tid] = s;
     int64_t to = -1, from = -1;
     if (s >= 0 && s != t) {
       const int32_t* tab = p.table + b * p.table_stride;
@@ -534,7 +676,11 @@ cudaError_t select_r(const EvictParams& p, cudaStream_t st) {
   const int64_t sl = evict_slice(p.limit, R);
   if (sl <= 8 * ET) return launch_kernel(evict_select_kernel<R, 8>, grid, dim3(ET), 0, st, false, R, p);
   if (sl <= E_SHORT) return launch_kernel(evict_select_kernel<R, E_SHORT / ET>, grid, dim3(ET), 0, st, false, R, p);
-  return launch_kernel(evict_select_long_kernel<R>, grid, dim3(ET), 0, st, false, R, p);
+  const int totals = R > 1 ? (E_BINS + 2 * E_HIST) * (int)sizeof(int) : 0;
+  const cudaError_t e = cudaFuncSetAttribute(evict_select_long_kernel<R>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, totals);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(evict_select_long_kernel<R>, grid, dim3(ET), totals, st, false, R, p);
 }
 
 }  // namespace
