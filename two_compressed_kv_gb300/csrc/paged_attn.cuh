@@ -40,26 +40,32 @@ namespace {
 
 constexpr int PA_NW = 4;              // warps per CTA
 
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 r;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
-  return r;
+// m16n8k16 products with fp32 accumulation.  Not volatile: the compiler may
+// interleave them with the loads and conversions of the next step.
+template <bool BF16>
+__device__ __forceinline__ void mma_acc(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint2 lds8(uint32_t a) {
-  uint2 r;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
-  return r;
+// Four e4m3 values as two fp16 pairs.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
-__device__ __forceinline__ void mma_bf16(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};\n"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(pair & 0xffffu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Two probabilities as 16-bit pairs: rounded, and what the rounding left.
@@ -93,7 +99,9 @@ struct PA {
   static constexpr int KS = D / 16;                        // contraction steps of S
   static constexpr int NT = D / 8;                         // n-tiles of O
   static constexpr int STAGE = 2 * PA_BLOCK * ROW;         // bytes of one block's keys and values
+  static constexpr int U = STAGE >= 8192 ? 1 : 2;          // blocks of a step
   static constexpr int STAGES = STAGE >= 8192 ? 3 : STAGE >= 4096 ? 6 : 8;
+  static_assert(STAGES % U == 0, "a step's slots do not wrap");
   static constexpr int HR = WIDE ? 16 : 8;                 // head rows
   static constexpr int MERGE = PA_NW * HR * (D + 4) * 4;
   static constexpr int RING = PA_NW * STAGES * STAGE;
@@ -101,15 +109,19 @@ struct PA {
   static constexpr int CTAS = SMEM <= 100 * 1024 ? 2 : 1;  // per SM
 };
 
-// Byte offset of 16-byte piece `piece` of row `row` in a block's keys or values:
-// [row / SW columns][16 rows][SW bytes], pieces of a row permuted by the TMA
-// swizzle (128 bytes: by row mod 8; 64 bytes: by row / 2 mod 4).
+// Byte offset of 16-byte piece `piece` (of the first SW bytes) of row `row` in a
+// block's keys or values: [row / SW columns][16 rows][SW bytes], pieces of a row
+// permuted by the TMA swizzle (128 bytes: by row mod 8; 64 bytes: by row / 2 mod
+// 4).  Neither changes from row to row + 8.
 template <int SW>
 __device__ __forceinline__ uint32_t piece_at(int row, int piece) {
-  if constexpr (SW == 128)
-    return (uint32_t)((piece >> 3) * (PA_BLOCK * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
-  else
-    return (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+  return SW == 128 ? (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4))
+                   : (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+}
+// From the offset `at` of piece c < 4: that of piece 4 x + c.
+template <int SW>
+__device__ __forceinline__ uint32_t piece_step(uint32_t at, int x) {
+  return SW == 128 ? (at ^ ((x & 1) << 6)) + (x >> 1) * (PA_BLOCK * 128) : at;
 }
 
 // ---------------------------------------------------------------------------
@@ -128,8 +140,12 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
   __shared__ int64_t warp_sum[PA_NW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;       // fragment row (head) and column group
+  constexpr int NR = WIDE ? 2 : 1;             // head rows of a lane
+  // this lane's pieces: key row r of 8 (token r ^ 4 (r & 1)), value rows 2 c and (2 c + 1) ^ 4
+  const uint32_t k_at = piece_at<C::SW>(r ^ ((r & 1) << 2), c);
+  const uint32_t v_at[2] = {piece_at<C::SW>(2 * c, C::VB == 16 ? r : r >> 1) + (C::VB == 16 ? 0 : 8 * (r & 1)),
+                            piece_at<C::SW>((2 * c + 1) ^ 4, C::VB == 16 ? r : r >> 1) + (C::VB == 16 ? 0 : 8 * (r & 1))};
   uint8_t* const ring_p = smem + warp * (C::STAGES * C::STAGE);
-  const uint32_t ring = smem_u32(ring_p);
   if (lane == 0) {
 #pragma unroll
     for (int k = 0; k < C::STAGES; ++k) mbar_init(&full[warp][k], 1);
@@ -217,9 +233,9 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
     // 8-bit caches: both fp16 and bf16 queries go to fp16, scaled by a power of
     // two so that the head's largest element lies in [1, 2).
     uint32_t qa[C::KS][WIDE ? 4 : 2];
-    float sc[WIDE ? 2 : 1];
+    float sc[NR];
 #pragma unroll
-    for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
+    for (int w = 0; w < NR; ++w) {
       const int i = r + 8 * w;
       const bool live = i < p.g;
       const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)b * p.q_sb +
@@ -252,7 +268,7 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
           const __half2 a = __floats2half2_rn(f[s][0] * f1, f[s][1] * f1);
           const __half2 d = __floats2half2_rn(f[s][2] * f1, f[s][3] * f1);
           qa[s][w] = live ? *reinterpret_cast<const uint32_t*>(&a) : 0u;
-          qa[s][(WIDE ? 2 : 1) + w] = live ? *reinterpret_cast<const uint32_t*>(&d) : 0u;
+          qa[s][NR + w] = live ? *reinterpret_cast<const uint32_t*>(&d) : 0u;
         }
       } else {
         // element 32 i + 8 c + 4 j + {0, 1}, {2, 3} for step 2 i + j
@@ -271,9 +287,9 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
     float o[C::NT][4];
 #pragma unroll
     for (int i = 0; i < C::NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m[WIDE ? 2 : 1], l[WIDE ? 2 : 1];
+    float m[NR], l[NR];
 #pragma unroll
-    for (int w = 0; w < (WIDE ? 2 : 1); ++w) m[w] = -CUDART_INF_F, l[w] = 0.f;
+    for (int w = 0; w < NR; ++w) m[w] = -CUDART_INF_F, l[w] = 0.f;
 
     // this warp's blocks: j0 + warp, + 4, ...; lane i holds the pool row of
     // the i-th of the next 32 (in blocks of 16 rows; -1: page outside the cache)
@@ -310,169 +326,175 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
       }
     };
 #pragma unroll
-    for (int s = 0; s < C::STAGES - 1; ++s) issue(s, s);
+    for (int k = 0; k < C::STAGES - C::U; ++k) issue(k, k);
     float* score_row = p.scores ? p.scores + (stream * p.g + r) * p.score_stride : nullptr;
 
     int slot = 0;
-    for (int i = 0; i < count && !gave_up; ++i) {
-      // the slot before this one was read in the last step, by all lanes
+    for (int i = 0; i < count && !gave_up; i += C::U) {
+      // the slots before these were read in the last step, by all lanes
       __syncwarp();
-      issue(i + C::STAGES - 1, slot == 0 ? C::STAGES - 1 : slot - 1);
-      const uint32_t src = ring + slot * C::STAGE;
-      const bool there = valid_bits >> slot & 1;
-      if (there) {
-        const bool ok = mbar_wait(&full[warp][slot], phases >> slot & 1);
-        if (!__all_sync(~0u, ok)) {
-          if (lane == 0 && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
-          gave_up = true;
+      const int behind = slot == 0 ? C::STAGES - C::U : slot - C::U;
+#pragma unroll
+      for (int u = 0; u < C::U; ++u) issue(i + C::STAGES - C::U + u, behind + u);
+      int left[C::U];                          // live tokens of a block (16 or more: all)
+      float s[C::U][2][4];
+#pragma unroll
+      for (int u = 0; u < C::U; ++u) {
+        left[u] = 0;
+        if (i + u < count && (valid_bits >> (slot + u) & 1)) {
+          left[u] = n - (j0 + warp + PA_NW * (i + u)) * PA_BLOCK;
+          const bool ok = mbar_wait(&full[warp][slot + u], phases >> (slot + u) & 1);
+          if (!__all_sync(~0u, ok)) {
+            if (lane == 0 && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
+            gave_up = true;
+          }
+          phases ^= 1u << (slot + u);
+          pending &= ~(1u << (slot + u));
         }
-        phases ^= 1u << slot;
-        pending &= ~(1u << slot);
-      }
-      float s[2][4];
+        // S = Q K^T
+        const uint8_t* sk = ring_p + (slot + u) * C::STAGE;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+        for (int t = 0; t < 2; ++t) {
+          s[u][t][0] = s[u][t][1] = s[u][t][2] = s[u][t][3] = 0.f;
 #pragma unroll
-        for (int x = 0; x < C::KL; ++x) {
-          const uint4 v = lds16(src + piece_at<C::SW>(8 * t + (r ^ ((r & 1) << 2)), 4 * x + c));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          constexpr int PER = CT == MKV_DT_E4M3 ? 4 : 2;   // steps in a piece
+          for (int x = 0; x < C::KL; ++x) {
+            const uint4 v = *reinterpret_cast<const uint4*>(sk + piece_step<C::SW>(k_at, x) + t * 8 * C::SW);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            constexpr int PER = CT == MKV_DT_E4M3 ? 4 : 2;   // steps in a piece
 #pragma unroll
-          for (int k = 0; k < PER; ++k) {
-            const int ks = x * PER + k;
-            uint32_t a[4];
-            if constexpr (WIDE) {
-              a[0] = qa[ks][0], a[1] = qa[ks][1], a[2] = qa[ks][2], a[3] = qa[ks][3];
-            } else {
-              a[0] = qa[ks][0], a[1] = 0u, a[2] = qa[ks][1], a[3] = 0u;
+            for (int k = 0; k < PER; ++k) {
+              const int ks = x * PER + k;
+              const uint32_t a[4] = {qa[ks][0], WIDE ? qa[ks][1] : 0u, qa[ks][NR],
+                                     WIDE ? qa[ks][WIDE ? 3 : 0] : 0u};
+              if constexpr (CT == MKV_DT_E4M3) {
+                uint32_t b0, b1;
+                e4m3x4_to_f16(w[k], b0, b1);
+                mma_acc<false>(s[u][t], a, b0, b1);
+              } else {
+                mma_acc<C::BF16>(s[u][t], a, w[2 * k], w[2 * k + 1]);
+              }
             }
-            if constexpr (CT == MKV_DT_E4M3)
-              mma16816(s[t], a, e4m3x2_to_f16x2(w[k]), e4m3x2_to_f16x2(w[k] >> 16));
-            else if constexpr (C::BF16)
-              mma_bf16(s[t], a, w[2 * k], w[2 * k + 1]);
-            else
-              mma16816(s[t], a, w[2 * k], w[2 * k + 1]);
+          }
+        }
+        // columns 2 c and 2 c + 1 are tokens 2 c and (2 c + 1) ^ 4 of 8
+        if (left[u] < PA_BLOCK) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (8 * t + ((k & 1) ? (2 * c + 1) ^ 4 : 2 * c) >= left[u]) s[u][t][k] = -CUDART_INF_F;
+        }
+        if (p.scores && i + u < count) {
+          const int tok0 = (j0 + warp + PA_NW * (i + u)) * PA_BLOCK;
+#pragma unroll
+          for (int w = 0; w < NR; ++w) {
+            // lane c ^ 2 of the row has token 2 c + 1
+            const float x0 = __shfl_xor_sync(~0u, s[u][0][2 * w + 1], 2);
+            const float x1 = __shfl_xor_sync(~0u, s[u][1][2 * w + 1], 2);
+            if (r + 8 * w < p.g) {
+              float* to = score_row + 8 * w * p.score_stride + tok0 + 2 * c;
+              *reinterpret_cast<float2*>(to) = make_float2(s[u][0][2 * w] * sc[w], x0 * sc[w]);
+              *reinterpret_cast<float2*>(to + 8) = make_float2(s[u][1][2 * w] * sc[w], x1 * sc[w]);
+            }
           }
         }
       }
-      // columns 2 c and 2 c + 1 are tokens 2 c and (2 c + 1) ^ 4 of 8
-      const int tok0 = (j0 + warp + PA_NW * i) * PA_BLOCK;
-      const int left = there ? n - tok0 : 0;   // live tokens of the block (16 or more: all)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int k = 0; k < (WIDE ? 4 : 2); ++k) s[t][k] *= sc[k / 2];
-      if (left < PA_BLOCK) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int k = 0; k < (WIDE ? 4 : 2); ++k)
-            if (8 * t + ((k & 1) ? (2 * c + 1) ^ 4 : 2 * c) >= left) s[t][k] = -CUDART_INF_F;
-      }
-      if (p.scores) {
-#pragma unroll
-        for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
-          // lane c ^ 2 of the row has token 2 c + 1
-          const float x0 = __shfl_xor_sync(~0u, s[0][2 * w + 1], 2), x1 = __shfl_xor_sync(~0u, s[1][2 * w + 1], 2);
-          if (r + 8 * w < p.g) {
-            float* to = score_row + 8 * w * p.score_stride + tok0 + 2 * c;
-            *reinterpret_cast<float2*>(to) = make_float2(s[0][2 * w], x0);
-            *reinterpret_cast<float2*>(to + 8) = make_float2(s[1][2 * w], x1);
-          }
-        }
-      }
-      // running maximum and sum
-      float mref[WIDE ? 2 : 1];
+      // running maximum (of the unscaled products: the scale is positive) and sum
+      float mref[NR], mn[NR];
       bool grows = false;
-      float mn[WIDE ? 2 : 1];
 #pragma unroll
-      for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
-        float x = fmaxf(fmaxf(s[0][2 * w], s[0][2 * w + 1]), fmaxf(s[1][2 * w], s[1][2 * w + 1]));
+      for (int w = 0; w < NR; ++w) {
+        float x = -CUDART_INF_F;
+#pragma unroll
+        for (int u = 0; u < C::U; ++u)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) x = fmaxf(x, fmaxf(s[u][t][2 * w], s[u][t][2 * w + 1]));
         x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
         x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
         mn[w] = fmaxf(m[w], x);
         grows |= mn[w] > m[w];
-        mref[w] = (mn[w] == -CUDART_INF_F ? 0.f : mn[w]) - PA_BIAS;
+        mref[w] = PA_BIAS - (mn[w] == -CUDART_INF_F ? 0.f : mn[w] * sc[w]);
       }
       if (__any_sync(~0u, grows)) {
-        float f[WIDE ? 2 : 1];
+        float f[NR];
 #pragma unroll
-        for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
-          f[w] = mn[w] > m[w] ? exp2f(m[w] - mn[w]) : 1.f;
+        for (int w = 0; w < NR; ++w) {
+          f[w] = mn[w] > m[w] ? exp2_fast((m[w] - mn[w]) * sc[w]) : 1.f;
           l[w] *= f[w];
           m[w] = mn[w];
         }
 #pragma unroll
         for (int x = 0; x < C::NT; ++x) {
           o[x][0] *= f[0], o[x][1] *= f[0];
-          o[x][2] *= f[WIDE ? 1 : 0], o[x][3] *= f[WIDE ? 1 : 0];
+          o[x][2] *= f[NR - 1], o[x][3] *= f[NR - 1];
         }
       }
-      uint32_t ph[WIDE ? 4 : 2], pl[WIDE ? 4 : 2];   // [token half][row half]
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int u = 0; u < C::U; ++u) {
+        uint32_t ph[2 * NR], pl[2 * NR];       // [token half][row half]
 #pragma unroll
-        for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
-          const float a = exp2f(s[t][2 * w] - mref[w]), d = exp2f(s[t][2 * w + 1] - mref[w]);
-          l[w] += a + d;
-          split_pair<C::BF16>(a, d, ph[t * (WIDE ? 2 : 1) + w], pl[t * (WIDE ? 2 : 1) + w]);
-        }
-      uint32_t pa[4], pb[4];
-      if constexpr (WIDE) {
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) pa[k] = ph[k], pb[k] = pl[k];
-      } else {
-        pa[0] = ph[0], pa[1] = pl[0], pa[2] = ph[1], pa[3] = pl[1];
-      }
-      const uint32_t sv = src + PA_BLOCK * C::ROW;
-      auto pv = [&](int nt, uint32_t b0, uint32_t b1) {
-        if constexpr (C::BF16) {
-          mma_bf16(o[nt], pa, b0, b1);
-          if constexpr (WIDE) mma_bf16(o[nt], pb, b0, b1);
-        } else {
-          mma16816(o[nt], pa, b0, b1);
-          if constexpr (WIDE) mma16816(o[nt], pb, b0, b1);
-        }
-      };
+          for (int w = 0; w < NR; ++w) {
+            const float a = exp2_fast(fmaf(s[u][t][2 * w], sc[w], mref[w]));
+            const float d = exp2_fast(fmaf(s[u][t][2 * w + 1], sc[w], mref[w]));
+            l[w] += a + d;
+            split_pair<C::BF16>(a, d, ph[t * NR + w], pl[t * NR + w]);
+          }
+        // g <= 8: the low parts are the operand's rows 8..15
+        const uint32_t pa[4] = {ph[0], WIDE ? ph[1] : pl[0], ph[NR], WIDE ? ph[2 * NR - 1] : pl[1]};
+        const uint32_t pb[4] = {pl[0], pl[1], pl[NR], pl[2 * NR - 1]};
+        auto pv = [&](int nt, uint32_t b0, uint32_t b1) {
+          mma_acc<C::BF16>(o[nt], pa, b0, b1);
+          if constexpr (WIDE) mma_acc<C::BF16>(o[nt], pb, b0, b1);
+        };
+        const uint8_t* sv = ring_p + (slot + u) * C::STAGE + PA_BLOCK * C::ROW;
 #pragma unroll
-      for (int x = 0; x < C::VL; ++x) {
-        uint32_t v[4][C::VB / 4];
+        for (int x = 0; x < C::VL; ++x) {
+          uint32_t v[4][C::VB / 4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int row = 8 * (t >> 1) + ((t & 1) ? (2 * c + 1) ^ 4 : 2 * c);
-          if constexpr (C::VB == 16) {
-            const uint4 y = lds16(sv + piece_at<C::SW>(row, 8 * x + r));
-            v[t][0] = y.x, v[t][1] = y.y, v[t][2] = y.z, v[t][3] = y.w;
-          } else {
-            const uint2 y = lds8(sv + piece_at<C::SW>(row, r >> 1) + 8 * (r & 1));
-            v[t][0] = y.x, v[t][1] = y.y;
+          for (int t = 0; t < 4; ++t) {
+            const uint8_t* from = sv + v_at[t & 1] + (t >> 1) * 8 * C::SW + x * PA_BLOCK * C::SW;
+            if constexpr (C::VB == 16) {
+              const uint4 y = *reinterpret_cast<const uint4*>(from);
+              v[t][0] = y.x, v[t][1] = y.y, v[t][2] = y.z, v[t][3] = y.w;
+            } else {
+              const uint2 y = *reinterpret_cast<const uint2*>(from);
+              v[t][0] = y.x, v[t][1] = y.y;
+            }
           }
           // what lies behind the sequence in its last page may be anything
-          if (left < PA_BLOCK && row >= left) {
+          if (left[u] < PA_BLOCK) {
 #pragma unroll
-            for (int y = 0; y < C::VB / 4; ++y) v[t][y] = 0u;
+            for (int t = 0; t < 4; ++t)
+              if (8 * (t >> 1) + ((t & 1) ? (2 * c + 1) ^ 4 : 2 * c) >= left[u]) {
+#pragma unroll
+                for (int y = 0; y < C::VB / 4; ++y) v[t][y] = 0u;
+              }
           }
-        }
 #pragma unroll
-        for (int y = 0; y < C::VB / 4; ++y) {
-          if constexpr (CT == MKV_DT_E4M3) {
-            const uint32_t a0 = __byte_perm(v[0][y], v[1][y], 0x5140), a1 = __byte_perm(v[0][y], v[1][y], 0x7362);
-            const uint32_t d0 = __byte_perm(v[2][y], v[3][y], 0x5140), d1 = __byte_perm(v[2][y], v[3][y], 0x7362);
-            const int nt = x * C::EV + 4 * y;
-            pv(nt, e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(d0));
-            pv(nt + 1, e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(d0 >> 16));
-            pv(nt + 2, e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(d1));
-            pv(nt + 3, e4m3x2_to_f16x2(a1 >> 16), e4m3x2_to_f16x2(d1 >> 16));
-          } else {
-            const int nt = x * C::EV + 2 * y;
-            pv(nt, __byte_perm(v[0][y], v[1][y], 0x5410), __byte_perm(v[2][y], v[3][y], 0x5410));
-            pv(nt + 1, __byte_perm(v[0][y], v[1][y], 0x7632), __byte_perm(v[2][y], v[3][y], 0x7632));
+          for (int y = 0; y < C::VB / 4; ++y) {
+            if constexpr (CT == MKV_DT_E4M3) {
+              uint32_t b0[4], b1[4];
+              e4m3x4_to_f16(__byte_perm(v[0][y], v[1][y], 0x5140), b0[0], b0[1]);
+              e4m3x4_to_f16(__byte_perm(v[0][y], v[1][y], 0x7362), b0[2], b0[3]);
+              e4m3x4_to_f16(__byte_perm(v[2][y], v[3][y], 0x5140), b1[0], b1[1]);
+              e4m3x4_to_f16(__byte_perm(v[2][y], v[3][y], 0x7362), b1[2], b1[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) pv(x * C::EV + 4 * y + k, b0[k], b1[k]);
+            } else {
+              const int nt = x * C::EV + 2 * y;
+              pv(nt, __byte_perm(v[0][y], v[1][y], 0x5410), __byte_perm(v[2][y], v[3][y], 0x5410));
+              pv(nt + 1, __byte_perm(v[0][y], v[1][y], 0x7632), __byte_perm(v[2][y], v[3][y], 0x7632));
+            }
           }
         }
       }
-      slot = slot + 1 == C::STAGES ? 0 : slot + 1;
+      slot = slot + C::U == C::STAGES ? 0 : slot + C::U;
     }
+    // the maximum in the scaled domain from here on
+#pragma unroll
+    for (int w = 0; w < NR; ++w) m[w] = m[w] == -CUDART_INF_F ? m[w] : m[w] * sc[w];
 
     if (gave_up) {
       // copies in flight must have landed before the ring is used for anything else
@@ -482,7 +504,7 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
     }
     // join the warps: the ring is drained and becomes [warp][head][D + 4]
 #pragma unroll
-    for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
+    for (int w = 0; w < NR; ++w) {
       l[w] += __shfl_xor_sync(~0u, l[w], 1);
       l[w] += __shfl_xor_sync(~0u, l[w], 2);
       if (c == 0) sm_m[warp][r + 8 * w] = m[w], sm_l[warp][r + 8 * w] = l[w];
@@ -490,7 +512,7 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
     __syncthreads();
     float* mg = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
+    for (int w = 0; w < NR; ++w) {
       const int head = r + 8 * w;
       float top = sm_m[0][head];
 #pragma unroll
