@@ -41,11 +41,10 @@ __global__ void __launch_bounds__(JT) paged_join_kernel(const __grid_constant__ 
     }
     return;
   }
-  int64_t per = (p.pre[p.B] + p.G - 1) / p.G;
-  if (per < p.min_blocks) per = p.min_blocks;
-  const int64_t nb = (n + PA_BLOCK - 1) / PA_BLOCK;
-  const int64_t first = p.pre[b] + h * nb;
-  const int i0 = (int)(first / per), i1 = (int)((first + nb - 1) / per);
+  const PagedShares shares(p, p.pre[p.B]);
+  const int64_t load = paged_load(p, n);
+  const int64_t first = p.pre[b] + h * load;
+  const int i0 = shares.of(first + p.piece_load), i1 = shares.of(first + load - 1);
   if (i0 == i1) return;                        // written by its CTA
   float m = -CUDART_INF_F, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);

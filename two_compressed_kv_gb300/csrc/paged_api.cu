@@ -83,6 +83,16 @@ constexpr int64_t kWholeTokens = 1024;
 // Smallest share of a CTA of the split kernel: 8 blocks of 16 tokens.
 constexpr int kMinBlocks = 8;
 
+// What a part of a stream costs a CTA apart from its blocks (its queries, the
+// first copies' latency, the join of the warps), in blocks.  On 256 ragged
+// streams 86.5 us with 32, 88 with 8; on equal long streams no difference.
+constexpr int kPieceLoad = 32;
+// Sixteenths of the load handed out in small shares, from so many blocks a CTA
+// on: 128K batch 8 takes 720 us with none, 683 with 3, 686 with 4; 32K batch 4
+// 97, 94 and 92 us.
+constexpr int kTail16 = 4;
+constexpr int kTailFrom = 64;
+
 struct DecodeLayout {
   bool split;
   int G;
@@ -119,8 +129,7 @@ DecodeLayout decode_layout(const mkv_paged_cache* c, const mkv_paged_decode_args
   const int64_t streams = (int64_t)c->batch * c->n_kv_heads;
   l.limit = decode_limit(c, a);
   l.split = l.limit > kWholeTokens && c->batch <= PA_MAX_B;
-  // two CTAs an SM, or one where its ring fills the SM (16-bit rows of 512 bytes)
-  const int ctas = c->head_dim * elem_bytes(c->dtype) >= 512 ? 1 : 2;
+  const int ctas = paged_ctas(c->head_dim * elem_bytes(c->dtype));
   l.G = (int)std::min<int64_t>((int64_t)sms * ctas,
                                streams * up(up(l.limit, PA_BLOCK), kMinBlocks));
   l.score_stride = up(l.limit, 16) * 16;
@@ -130,8 +139,8 @@ DecodeLayout decode_layout(const mkv_paged_cache* c, const mkv_paged_decode_args
     at += (bytes + 255) & ~(uint64_t)255;
     return here;
   };
-  l.part_o = place(l.split ? 2ull * l.G * g * c->head_dim * 4 : 0);
-  l.part_ml = place(l.split ? 2ull * l.G * g * 8 : 0);
+  l.part_o = place(l.split ? 2ull * PA_SHARES * l.G * g * c->head_dim * 4 : 0);
+  l.part_ml = place(l.split ? 2ull * PA_SHARES * l.G * g * 8 : 0);
   l.pre = place(l.split ? 8ull * (c->batch + 1) : 0);
   l.lse2 = place((uint64_t)streams * g * 4);
   l.scores = place(a->acc ? (uint64_t)streams * g * l.score_stride * 4 : 0);
@@ -449,6 +458,9 @@ mkv_status mkv_paged_decode(const mkv_paged_cache* c, const mkv_paged_decode_arg
   p.G = l.G;
   p.min_blocks = kMinBlocks;
   p.split = l.split;
+  p.piece_load = kPieceLoad;
+  p.tail16 = kTail16;
+  p.tail_from = kTailFrom;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   switch (c->head_dim) {
     case 64: CKP(launch_paged_attn_64(p, c->dtype, st)); break;

@@ -26,7 +26,9 @@
 //   - P in 16 bits would cost half the output's precision, so it is split into
 //     a high and a low part.  With g <= 8 the low part sits in the operand's
 //     rows 8..15, which are free: no instruction more.  Probabilities carry a
-//     factor 2^12, which cancels, so that small ones stay normal in fp16.
+//     factor 2^12, which cancels, so that small ones stay normal in fp16 and the
+//     reference of the exponents need not follow every new maximum: up to 2^3
+//     above it still fits.
 #pragma once
 
 #include <math_constants.h>
@@ -100,13 +102,14 @@ struct PA {
   static constexpr int NT = D / 8;                         // n-tiles of O
   static constexpr int STAGE = 2 * PA_BLOCK * ROW;         // bytes of one block's keys and values
   static constexpr int U = STAGE >= 8192 ? 1 : 2;          // blocks of a step
-  static constexpr int STAGES = STAGE >= 8192 ? 3 : STAGE >= 4096 ? 6 : 8;
+  static constexpr int STAGES = STAGE >= 8192 ? 3 : STAGE >= 4096 ? 4 : 8;
   static_assert(STAGES % U == 0, "a step's slots do not wrap");
   static constexpr int HR = WIDE ? 16 : 8;                 // head rows
   static constexpr int MERGE = PA_NW * HR * (D + 4) * 4;
   static constexpr int RING = PA_NW * STAGES * STAGE;
   static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + 1024;   // and its alignment
-  static constexpr int CTAS = SMEM <= 100 * 1024 ? 2 : 1;  // per SM
+  static constexpr int CTAS = paged_ctas(ROW);             // per SM
+  static_assert(CTAS * (SMEM + 10 * 1024) <= 228 * 1024, "resident CTAs' shared memory");
 };
 
 // Byte offset of 16-byte piece `piece` (of the first SW bytes) of row `row` in a
@@ -125,7 +128,7 @@ __device__ __forceinline__ uint32_t piece_step(uint32_t at, int x) {
 }
 
 // ---------------------------------------------------------------------------
-// grid: split ? G : streams; block: 4 warps; dynamic smem PA::SMEM
+// grid: split ? 3 G : streams; block: 4 warps; dynamic smem PA::SMEM
 // ---------------------------------------------------------------------------
 template <int CT, int D, bool WIDE>
 __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
   extern __shared__ __align__(16) uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // the swizzle goes by address bits 7..9
   __shared__ uint64_t full[PA_NW][C::STAGES];
-  __shared__ int64_t pre[PA_MAX_B + 1];        // split: blocks before each sequence
+  __shared__ int64_t pre[PA_MAX_B + 1];        // split: load before each sequence
   __shared__ float sm_m[PA_NW][C::HR], sm_l[PA_NW][C::HR];
   __shared__ int64_t warp_sum[PA_NW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -157,16 +160,16 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
   bool gave_up = false;                        // a bounded wait ran out: outputs undefined
 
   griddep_launch();                            // the join's prologue may start; it waits for the end
-  // this CTA's range of blocks, counted over all streams
+  // this CTA's share of the load, counted over all streams
   int64_t g0 = 0, g1 = 0, at = 0;
   int b = 0;
   if (p.split) {
-    // prefix sums of the sequences' blocks: each thread a run of sequences
+    // prefix sums of the sequences' load: each thread a run of sequences
     const int run = (p.B + PA_NW * 32 - 1) / (PA_NW * 32);
     int64_t sum = 0;
     for (int k = 0; k < run; ++k) {
       const int i = tid * run + k;
-      if (i < p.B) sum += (int64_t)((paged_len(p, i) + PA_BLOCK - 1) / PA_BLOCK) * p.H;
+      if (i < p.B) sum += paged_load(p, paged_len(p, i)) * p.H;
     }
     int64_t inc = sum;
 #pragma unroll
@@ -182,18 +185,16 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
       const int i = tid * run + k;
       if (i < p.B) {
         pre[i] = base;
-        base += (int64_t)((paged_len(p, i) + PA_BLOCK - 1) / PA_BLOCK) * p.H;
+        base += paged_load(p, paged_len(p, i)) * p.H;
       }
       if (i == p.B - 1) pre[p.B] = base;
     }
     __syncthreads();
     if (blockIdx.x == 0)
       for (int i = tid; i <= p.B; i += PA_NW * 32) p.pre[i] = pre[i];   // for the join
-    const int64_t total = pre[p.B];
-    int64_t per = (total + p.G - 1) / p.G;
-    if (per < p.min_blocks) per = p.min_blocks;
-    g0 = (int64_t)blockIdx.x * per;
-    g1 = min(total, g0 + per);
+    const PagedShares shares(p, pre[p.B]);
+    g0 = shares.first(blockIdx.x);
+    g1 = shares.first(blockIdx.x + 1);
     if (g0 >= g1) return;
     int lo = 0, hi = p.B - 1;                  // last b with pre[b] <= g0 that has blocks
     while (lo < hi) {
@@ -213,9 +214,13 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
       n = paged_len(p, b);
       nb = (n + PA_BLOCK - 1) / PA_BLOCK;
       const int64_t off = at - pre[b];
-      h = (int)(off / nb);
-      j0 = (int)(off - (int64_t)h * nb);
-      j1 = (int)min((int64_t)nb, j0 + (g1 - at));
+      const int load = (int)paged_load(p, n);
+      h = (int)(off / load);
+      const int v0 = (int)(off - (int64_t)h * load), v1 = (int)min((int64_t)load, v0 + (g1 - at));
+      at += v1 - v0;
+      j0 = max(0, v0 - p.piece_load);
+      j1 = v1 - p.piece_load;
+      if (j1 <= j0) continue;
     } else {
       b = blockIdx.x / p.H;
       h = blockIdx.x - b * p.H;
@@ -287,9 +292,12 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
     float o[C::NT][4];
 #pragma unroll
     for (int i = 0; i < C::NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m[NR], l[NR];
+    // reference of the exponents (the largest score so far or a little less), sum,
+    // what is added to a scaled score (so large at first that any score moves the
+    // reference, and that a masked one still weighs nothing), and a step's largest score
+    float m[NR], l[NR], mref[NR], top[NR];
 #pragma unroll
-    for (int w = 0; w < NR; ++w) m[w] = -CUDART_INF_F, l[w] = 0.f;
+    for (int w = 0; w < NR; ++w) m[w] = -CUDART_INF_F, l[w] = 0.f, mref[w] = PA_UNSET;
 
     // this warp's blocks: j0 + warp, + 4, ...; lane i holds the pool row of
     // the i-th of the next 32 (in blocks of 16 rows; -1: page outside the cache)
@@ -399,29 +407,31 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
           }
         }
       }
-      // running maximum (of the unscaled products: the scale is positive) and sum
-      float mref[NR], mn[NR];
+      // The reference m (of the unscaled products: the scale is positive) moves
+      // only where a score passes it by more than PA_SLACK, which a lane sees
+      // from its own scores: after a few steps that hardly happens, and the
+      // lanes' maximum and the scaling of o are skipped.
       bool grows = false;
 #pragma unroll
       for (int w = 0; w < NR; ++w) {
-        float x = -CUDART_INF_F;
+        top[w] = -CUDART_INF_F;
 #pragma unroll
         for (int u = 0; u < C::U; ++u)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) x = fmaxf(x, fmaxf(s[u][t][2 * w], s[u][t][2 * w + 1]));
-        x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
-        mn[w] = fmaxf(m[w], x);
-        grows |= mn[w] > m[w];
-        mref[w] = PA_BIAS - (mn[w] == -CUDART_INF_F ? 0.f : mn[w] * sc[w]);
+          for (int t = 0; t < 2; ++t) top[w] = fmaxf(top[w], fmaxf(s[u][t][2 * w], s[u][t][2 * w + 1]));
+        grows |= fmaf(top[w], sc[w], mref[w]) > PA_BIAS + PA_SLACK;
       }
       if (__any_sync(~0u, grows)) {
         float f[NR];
 #pragma unroll
         for (int w = 0; w < NR; ++w) {
-          f[w] = mn[w] > m[w] ? exp2_fast((m[w] - mn[w]) * sc[w]) : 1.f;
+          float x = fmaxf(top[w], __shfl_xor_sync(~0u, top[w], 1));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
+          x = fmaxf(x, m[w]);
+          f[w] = x > m[w] ? exp2_fast((m[w] - x) * sc[w]) : 1.f;
           l[w] *= f[w];
-          m[w] = mn[w];
+          m[w] = x;
+          if (x != -CUDART_INF_F) mref[w] = PA_BIAS - __fmul_rn(x, sc[w]);   // rounded as in the join
         }
 #pragma unroll
         for (int x = 0; x < C::NT; ++x) {
@@ -492,9 +502,9 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
       }
       slot = slot + C::U == C::STAGES ? 0 : slot + C::U;
     }
-    // the maximum in the scaled domain from here on
+    // the reference in the scaled domain from here on
 #pragma unroll
-    for (int w = 0; w < NR; ++w) m[w] = m[w] == -CUDART_INF_F ? m[w] : m[w] * sc[w];
+    for (int w = 0; w < NR; ++w) m[w] = m[w] == -CUDART_INF_F ? m[w] : __fmul_rn(m[w], sc[w]);
 
     if (gave_up) {
       // copies in flight must have landed before the ring is used for anything else
@@ -575,7 +585,6 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
       }
     }
     if (!p.split) break;
-    at += j1 - j0;
     if (at < g1) {                  // the merge area becomes the ring again
       fence_proxy_async();
       __syncthreads();
@@ -592,7 +601,7 @@ cudaError_t launch_pa(const PagedAttnParams& p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<CT, D, WIDE>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const int64_t grid = p.split ? p.G : (int64_t)p.B * p.H;
+  const int64_t grid = p.split ? PA_SHARES * p.G : (int64_t)p.B * p.H;
   paged_attn_kernel<CT, D, WIDE><<<(unsigned)grid, PA_NW * 32, C::SMEM, st>>>(p, kmap, vmap);
   return cudaGetLastError();
 }

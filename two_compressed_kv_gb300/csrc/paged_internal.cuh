@@ -49,7 +49,14 @@ cudaError_t launch_append_rows(const AppendRowsParams& p, cudaStream_t st);
 // ---------------------------------------------------------------------------
 constexpr int PA_BLOCK = 16;      // tokens per block: the unit of work; a block lies in one page
 constexpr int PA_MAX_B = 1024;    // sequences whose prefix sums fit the split kernel
+constexpr float PA_SLACK = 3.f;    // how far scores (log2) may pass the reference of the exponents
+constexpr float PA_UNSET = 1e38f;
 constexpr float PA_BIAS = 12.f;   // probabilities carry a factor 2^12 until the division by their sum
+
+// CTAs of the streaming kernel per SM, by the bytes of a row: its rings and
+// accumulators grow with the row, and with short rows the latency of a step
+// counts more.
+constexpr int paged_ctas(int row_bytes) { return row_bytes >= 512 ? 1 : row_bytes >= 256 ? 2 : 3; }
 
 struct PagedAttnParams {
   const uint8_t *kp, *vp;
@@ -71,14 +78,17 @@ struct PagedAttnParams {
   float* acc;
   int64_t acc_stride;
   // workspace
-  float* part_o;                  // [2 G][g][D]: unnormalised sums of split streams
-  float* part_ml;                 // [2 G][g][2]: running maximum (log2 domain) and sum
+  float* part_o;                  // [6 G][g][D]: unnormalised sums of split streams
+  float* part_ml;                 // [6 G][g][2]: running maximum (log2 domain) and sum
   float* lse2;                    // [B H g]: log2 of the sum of exp2(scores)
-  int64_t* pre;                   // [B + 1]: blocks before each sequence (split)
+  int64_t* pre;                   // [B + 1]: load before each sequence (split)
   float* scores;                  // [B H g][score_stride], log2 domain; only with acc
   int64_t score_stride;
-  int G;                          // CTAs of the split kernel
+  int G;                          // CTAs that are resident at once in the split kernel
   int min_blocks;                 // smallest share of a CTA, in blocks
+  int piece_load;                 // what a part of a stream costs apart from its blocks, in blocks
+  int tail16;                     // sixteenths of the load that are handed out in small shares
+  int tail_from;                  // from this many blocks a CTA on
   int split;                      // 0: one CTA per stream
 };
 
@@ -87,6 +97,37 @@ __device__ __forceinline__ int paged_len(const PagedAttnParams& p, int b) {
   const int n = p.lens[b];
   return n < 0 ? 0 : min(n, p.limit);
 }
+
+// Load of a stream of n tokens: its blocks and a fixed cost.
+__device__ __forceinline__ int64_t paged_load(const PagedAttnParams& p, int n) {
+  return n == 0 ? 0 : (n + PA_BLOCK - 1) / PA_BLOCK + p.piece_load;
+}
+
+// How the split kernel's CTAs share the load of all streams: the first G, which
+// run at once, take equal large shares, and 2 G more take what is left in
+// small ones as SMs become free, so that an SM that gets less of the memory's
+// bandwidth than others does not finish late.  A function of the lengths alone.
+constexpr int PA_SHARES = 3;
+struct PagedShares {
+  int64_t total, big, small;
+  int G;
+  __device__ __forceinline__ PagedShares(const PagedAttnParams& p, int64_t total_) : total(total_), G(p.G) {
+    if (total < (int64_t)G * p.tail_from) {
+      big = max((total + G - 1) / G, (int64_t)p.min_blocks);
+      small = 1;
+    } else {
+      big = total * (16 - p.tail16) / 16 / G;
+      small = (total - big * G + 2 * G - 1) / (2 * G);
+    }
+  }
+  // start of share i, and the share that load v belongs to
+  __device__ __forceinline__ int64_t first(int64_t i) const {
+    return min(total, i < G ? i * big : G * big + (i - G) * small);
+  }
+  __device__ __forceinline__ int of(int64_t v) const {
+    return (int)(v < G * big ? v / big : G + (v - G * big) / small);
+  }
+};
 
 // Four outputs a * f from element `at` on, rounded to the output's type.
 __device__ __forceinline__ void store_out4(const PagedAttnParams& p, int64_t at, float4 a, float f) {
