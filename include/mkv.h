@@ -521,8 +521,8 @@ typedef struct {
 } mkv_paged_append_args;
 
 /* Writes n new tokens into their slots: keys rotated by `plan` (NULL: not
- * rotated), values as they are, both rounded to the cache's type (E4M3:
- * divided by the head's scale, nearest even, saturated at 448); queries are
+ * rotated), values as they are, both rounded to the cache's type (E4M3: times
+ * the reciprocal of the head's scale, nearest even, saturated at 448); queries are
  * rotated with the same positions.  Two tokens of a call must not share a
  * slot.  plan->rot_dim must be a multiple of 16 (half pairs) or 8
  * (interleaved) and plan->head_dim the cache's.  A token whose sequence, slot

@@ -389,7 +389,7 @@ mkv_status mkv_paged_append(const mkv_paged_cache* c, const mkv_rope_plan* plan,
   int sms = 0;
   mkv_status s = sm_count(&sms);
   if (s != MKV_OK) return s;
-  p.heads_per = heads_per_thread(a->n * p.units, p.heads_total, (int64_t)sms * 2048, 8);
+  p.heads_per = heads_per_thread(a->n * p.units, p.heads_total, (int64_t)sms * 2048, 16);
   while (up(p.heads_total, p.heads_per) > 65535) p.heads_per *= 2;
   CKP(launch_append_rows(p, reinterpret_cast<cudaStream_t>(stream)));
   return MKV_OK;
