@@ -14,25 +14,25 @@
 //   - a warp works alone on blocks of 16 tokens; no barrier between warps until
 //     its part of a stream is done;
 //   - the 16 rows of a block come by one TMA copy for keys and one for values
-//     into the warp's own ring in shared memory, 128-byte swizzled; column n of a
-//     fragment is token n ^ 4 (n & 1) of its 8, which makes both operands' reads
-//     free of bank conflicts under that swizzle;
-//   - S = Q K^T and O = P V run as m16n8k16 with the query heads as rows.  The
-//     order of the contracted dimension is free, so a lane's 16 bytes of a key
-//     row are two steps' B fragments as they are; value rows of token pairs are
-//     interleaved by byte permutes.  The S accumulator is the P operand as is.
-//     m16n8k16 needs about a sixth of its rate here, far from a bound, and
-//     unlike tcgen05 takes both operands' layout as the loads deliver it.
-//   - P in 16 bits would cost half the output's precision, so it is split into
-//     a high and a low part.  With g <= 8 the low part sits in the operand's
-//     rows 8..15, which are free: no instruction more.  Probabilities carry a
-//     factor 2^12, which cancels, so that small ones stay normal in fp16 and the
-//     reference of the exponents need not follow every new maximum: up to 2^3
-//     above it still fits.
+//     into the warp's own ring in shared memory, 128-byte swizzled;
+//   - transposed products, S^T = K Q^T and O^T = V^T P^T as m16n8k16: tokens,
+//     then channels, are the 16 rows, and 8 query heads fill the 8 columns, so
+//     that no row is padding (with heads as rows, half of the work and of the
+//     accumulators is).  16-bit rows reach the fragments by ldmatrix, values
+//     transposed on the way; of e4m3 rows a lane reads 16 bytes, pairs tokens by
+//     byte permutes and converts to fp16, exactly.  There row n of a fragment is
+//     token n ^ 4 (n & 1) of 8, which keeps the reads free of bank conflicts.
+//     tcgen05 would need the operands unpacked back into shared memory, and
+//     m16n8k16 is far from its rate here;
+//   - P in 16 bits would cost half the output's precision, so it goes in as a
+//     high and a low part.  Probabilities carry a factor 2^12, which cancels, so
+//     that small ones stay normal in fp16 and the reference of the exponents need
+//     not follow every new maximum: up to 2^3 above it still fits.
 #pragma once
 
 #include <math_constants.h>
 
+#include "decode_common.cuh"
 #include "paged_internal.cuh"
 #include "ptx.cuh"
 #include "tc05.cuh"
@@ -87,6 +87,26 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
   }
 }
 
+// Four 8 x 8 tiles of 16-bit elements, rows at the lanes' addresses (lanes 8 i ..
+// 8 i + 7: tile i); lane 4 r + c gets elements 2 c, 2 c + 1 of row r, or (TRANS)
+// of column r.  Ordered with the waits on the ring, otherwise free to move.
+template <bool TRANS>
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+// An 8 x 8 tile of 16-bit elements, a row's pair a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+  return r;
+}
 
 template <int CT, int D, bool WIDE>
 struct PA {
@@ -94,17 +114,16 @@ struct PA {
   static constexpr bool BF16 = CT == MKV_DT_BF16;
   static constexpr int ROW = D * ES;                       // bytes of a row
   static constexpr int SW = ROW < 128 ? ROW : 128;         // swizzled width
-  static constexpr int KL = ROW / 64;                      // 16-byte pieces of a key row per lane
-  static constexpr int VB = ROW / 8 < 16 ? ROW / 8 : 16;   // bytes of a value piece
-  static constexpr int VL = ROW / (8 * VB);                // value pieces of a row per lane
-  static constexpr int EV = VB / ES;                       // elements of a value piece
-  static constexpr int KS = D / 16;                        // contraction steps of S
-  static constexpr int NT = D / 8;                         // n-tiles of O
+  static constexpr int KL = ROW / 64;                      // e4m3: 16-byte pieces of a key row per lane
+  static constexpr int VB = ROW / 8 < 16 ? ROW / 8 : 16;   // e4m3: bytes of a value piece
+  static constexpr int VL = ROW / (8 * VB);                // e4m3: value pieces of a row per lane
+  static constexpr int NH = WIDE ? 2 : 1;                  // groups of 8 heads
+  static constexpr int KS = D / 16;                        // contraction steps of S^T, row tiles of O^T
   static constexpr int STAGE = 2 * PA_BLOCK * ROW;         // bytes of one block's keys and values
   static constexpr int U = STAGE >= 8192 ? 1 : 2;          // blocks of a step
   static constexpr int STAGES = STAGE >= 8192 ? 3 : STAGE >= 4096 ? 4 : 8;
   static_assert(STAGES % U == 0, "a step's slots do not wrap");
-  static constexpr int HR = WIDE ? 16 : 8;                 // head rows
+  static constexpr int HR = 8 * NH;                        // head rows
   static constexpr int MERGE = PA_NW * HR * (D + 4) * 4;
   static constexpr int RING = PA_NW * STAGES * STAGE;
   static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + 1024;   // and its alignment
@@ -121,10 +140,10 @@ __device__ __forceinline__ uint32_t piece_at(int row, int piece) {
   return SW == 128 ? (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4))
                    : (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
 }
-// From the offset `at` of piece c < 4: that of piece 4 x + c.
-template <int SW>
-__device__ __forceinline__ uint32_t piece_step(uint32_t at, int x) {
-  return SW == 128 ? (at ^ ((x & 1) << 6)) + (x >> 1) * (PA_BLOCK * 128) : at;
+// From the offset `at` of a piece: that of the piece `by` further, where `by` has
+// no bit in common with the piece's number in its 128 bytes.
+__device__ __forceinline__ uint32_t piece_on(uint32_t at, int by) {
+  return (at ^ ((uint32_t)(by & 7) << 4)) + (uint32_t)(by >> 3) * (PA_BLOCK * 128);
 }
 
 // ---------------------------------------------------------------------------
@@ -142,13 +161,21 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
   __shared__ float sm_m[PA_NW][C::HR], sm_l[PA_NW][C::HR];
   __shared__ int64_t warp_sum[PA_NW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r = lane >> 2, c = lane & 3;       // fragment row (head) and column group
-  constexpr int NR = WIDE ? 2 : 1;             // head rows of a lane
-  // this lane's pieces: key row r of 8 (token r ^ 4 (r & 1)), value rows 2 c and (2 c + 1) ^ 4
-  const uint32_t k_at = piece_at<C::SW>(r ^ ((r & 1) << 2), c);
-  const uint32_t v_at[2] = {piece_at<C::SW>(2 * c, C::VB == 16 ? r : r >> 1) + (C::VB == 16 ? 0 : 8 * (r & 1)),
-                            piece_at<C::SW>((2 * c + 1) ^ 4, C::VB == 16 ? r : r >> 1) + (C::VB == 16 ? 0 : 8 * (r & 1))};
+  const int r = lane >> 2, c = lane & 3;       // fragment row and column pair
+  constexpr int NH = C::NH;
+  constexpr bool E4 = CT == MKV_DT_E4M3;
   uint8_t* const ring_p = smem + warp * (C::STAGES * C::STAGE);
+  // where this lane reads.  ldmatrix: keys, tokens 0..7, 8..15 of the first and
+  // second 8 channels; values, 8 channels of tokens 0..7, the next 8, then 8..15.
+  // e4m3: key row of token r, value rows of its column pair's tokens.
+  const uint32_t k_at = E4 ? piece_at<C::SW>(r ^ ((r & 1) << 2), c)
+                           : piece_at<128>((lane & 7) + (lane & 8), lane >> 4);
+  const uint32_t v_at = E4 ? piece_at<C::SW>(2 * c, C::VB == 16 ? r : r >> 1) + (C::VB == 16 ? 0 : 8 * (r & 1))
+                           : piece_at<128>((lane & 7) + ((lane >> 1) & 8), (lane >> 3) & 1);
+  const uint32_t v_at1 = E4 ? piece_at<C::SW>((2 * c + 1) ^ 4, C::VB == 16 ? r : r >> 1) + (C::VB == 16 ? 0 : 8 * (r & 1))
+                            : 0u;
+  // token of this lane's first row of S^T (the second is 8 further)
+  const int tok_r = E4 ? r ^ ((r & 1) << 2) : r;
   if (lane == 0) {
 #pragma unroll
     for (int k = 0; k < C::STAGES; ++k) mbar_init(&full[warp][k], 1);
@@ -159,6 +186,7 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
   uint32_t pending = 0;                        // bit of a ring slot: a copy into it is in flight
   bool gave_up = false;                        // a bounded wait ran out: outputs undefined
 
+  griddep_wait();                              // lengths and caches may come from the kernel before
   griddep_launch();                            // the join's prologue may start; it waits for the end
   // this CTA's share of the load, counted over all streams
   int64_t g0 = 0, g1 = 0, at = 0;
@@ -234,71 +262,6 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
       atomicOr(p.status, DEV_ERR_CHECK);
     const int64_t stream = (int64_t)b * p.H + h;
 
-    // Q fragments: row r is query head h * g + r (and r + 8), zero past g.
-    // 8-bit caches: both fp16 and bf16 queries go to fp16, scaled by a power of
-    // two so that the head's largest element lies in [1, 2).
-    uint32_t qa[C::KS][WIDE ? 4 : 2];
-    float sc[NR];
-#pragma unroll
-    for (int w = 0; w < NR; ++w) {
-      const int i = r + 8 * w;
-      const bool live = i < p.g;
-      const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)b * p.q_sb +
-                          (int64_t)(h * p.g + (live ? i : 0)) * p.q_sh;
-      sc[w] = p.scale2 * (CT == MKV_DT_E4M3 && p.ks ? p.ks[h] : 1.f);
-      if constexpr (CT == MKV_DT_E4M3) {
-        // element 64 i + 16 c + 4 j + {0, 1}, {2, 3} for step 4 i + j
-        float f[C::KS][4];
-        float top = 0.f;
-#pragma unroll
-        for (int s = 0; s < C::KS; ++s) {
-          const uint2 v = *reinterpret_cast<const uint2*>(q + (s / 4) * 64 + 16 * c + 4 * (s % 4));
-          const uint32_t x[2] = {v.x, v.y};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint16_t u = (uint16_t)(x[k / 2] >> (16 * (k % 2)));
-            f[s][k] = p.q_bf16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
-            top = fmaxf(top, fabsf(f[s][k]));
-          }
-        }
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        // 2^e <= top < 2^(e+1); a zero, tiny or infinite head is left as it is
-        int e = (int)(__float_as_uint(top) >> 23) - 127;
-        if (e < -100 || e > 126) e = 0;
-        const float f1 = __uint_as_float((uint32_t)(127 - e) << 23);
-        sc[w] *= __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-        for (int s = 0; s < C::KS; ++s) {
-          const __half2 a = __floats2half2_rn(f[s][0] * f1, f[s][1] * f1);
-          const __half2 d = __floats2half2_rn(f[s][2] * f1, f[s][3] * f1);
-          qa[s][w] = live ? *reinterpret_cast<const uint32_t*>(&a) : 0u;
-          qa[s][NR + w] = live ? *reinterpret_cast<const uint32_t*>(&d) : 0u;
-        }
-      } else {
-        // element 32 i + 8 c + 4 j + {0, 1}, {2, 3} for step 2 i + j
-#pragma unroll
-        for (int i2 = 0; i2 < C::KS / 2; ++i2) {
-          const uint4 v = *reinterpret_cast<const uint4*>(q + 32 * i2 + 8 * c);
-          constexpr int hi = WIDE ? 2 : 1;
-          qa[2 * i2][w] = live ? v.x : 0u;
-          qa[2 * i2][hi + w] = live ? v.y : 0u;
-          qa[2 * i2 + 1][w] = live ? v.z : 0u;
-          qa[2 * i2 + 1][hi + w] = live ? v.w : 0u;
-        }
-      }
-    }
-
-    float o[C::NT][4];
-#pragma unroll
-    for (int i = 0; i < C::NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    // reference of the exponents (the largest score so far or a little less), sum,
-    // what is added to a scaled score (so large at first that any score moves the
-    // reference, and that a masked one still weighs nothing), and a step's largest score
-    float m[NR], l[NR], mref[NR], top[NR];
-#pragma unroll
-    for (int w = 0; w < NR; ++w) m[w] = -CUDART_INF_F, l[w] = 0.f, mref[w] = PA_UNSET;
-
     // this warp's blocks: j0 + warp, + 4, ...; lane i holds the pool row of
     // the i-th of the next 32 (in blocks of 16 rows; -1: page outside the cache)
     const int count = gave_up ? 0 : max(0, (j1 - j0 - warp + PA_NW - 1) / PA_NW);
@@ -335,7 +298,76 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
     };
 #pragma unroll
     for (int k = 0; k < C::STAGES - C::U; ++k) issue(k, k);
-    float* score_row = p.scores ? p.scores + (stream * p.g + r) * p.score_stride : nullptr;
+
+    // Q^T fragments: column r of group w is query head 8 w + r of the stream's g,
+    // zero past g.  8-bit caches: fp16 and bf16 queries both go to fp16, scaled by
+    // a power of two so that the head's largest element lies in [1, 2).
+    // sc: scale of the scores of this lane's columns 2 c, 2 c + 1.
+    uint32_t qb[NH][C::KS][2];
+    float sc[NH][2];
+#pragma unroll
+    for (int w = 0; w < NH; ++w) {
+      const int i = r + 8 * w;
+      const bool live = i < p.g;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)b * p.q_sb +
+                          (int64_t)(h * p.g + (live ? i : 0)) * p.q_sh;
+      if constexpr (E4) {
+        // channels 64 i + 16 c + 4 j + {0, 1}, {2, 3} in step 4 i + j
+        uint2 v[C::KS];
+#pragma unroll
+        for (int s = 0; s < C::KS; ++s)
+          v[s] = *reinterpret_cast<const uint2*>(q + (s / 4) * 64 + 16 * c + 4 * (s % 4));
+        auto get = [&](int s, int k) {
+          const uint16_t u = (uint16_t)((k < 2 ? v[s].x : v[s].y) >> (16 * (k % 2)));
+          return p.q_bf16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
+        };
+        float top = 0.f;
+#pragma unroll
+        for (int s = 0; s < C::KS; ++s)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(get(s, k)));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        // 2^e <= top < 2^(e+1); a zero, tiny or infinite head is left as it is
+        int e = (int)(__float_as_uint(top) >> 23) - 127;
+        if (e < -100 || e > 126) e = 0;
+        const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+        const float back = __uint_as_float((uint32_t)(127 + e) << 23) * p.scale2 * (p.ks ? p.ks[h] : 1.f);
+        sc[w][0] = __shfl_sync(~0u, back, 8 * c);
+        sc[w][1] = __shfl_sync(~0u, back, 8 * c + 4);
+#pragma unroll
+        for (int s = 0; s < C::KS; ++s) {
+          const __half2 x = __floats2half2_rn(get(s, 0) * f, get(s, 1) * f);
+          const __half2 y = __floats2half2_rn(get(s, 2) * f, get(s, 3) * f);
+          qb[w][s][0] = live ? *reinterpret_cast<const uint32_t*>(&x) : 0u;
+          qb[w][s][1] = live ? *reinterpret_cast<const uint32_t*>(&y) : 0u;
+        }
+      } else {
+        sc[w][0] = sc[w][1] = p.scale2;
+#pragma unroll
+        for (int s = 0; s < C::KS; ++s)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(q + 16 * s + 8 * k + 2 * c);
+            qb[w][s][k] = live ? v : 0u;
+          }
+      }
+    }
+
+    float o[NH][C::KS][4];                     // O^T: rows channels, columns heads
+#pragma unroll
+    for (int w = 0; w < NH; ++w)
+#pragma unroll
+      for (int j = 0; j < C::KS; ++j) o[w][j][0] = o[w][j][1] = o[w][j][2] = o[w][j][3] = 0.f;
+    // for each of the lane's heads: reference of the exponents (the largest score so
+    // far or a little less), sum over its own tokens, what is added to a scaled score
+    // (so large at first that any score moves the reference, and that a masked one
+    // still weighs nothing)
+    float m[NH][2], l[NH][2], mref[NH][2];
+#pragma unroll
+    for (int w = 0; w < NH; ++w)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) m[w][k] = -CUDART_INF_F, l[w][k] = 0.f, mref[w][k] = PA_UNSET;
 
     int slot = 0;
     for (int i = 0; i < count && !gave_up; i += C::U) {
@@ -345,7 +377,7 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
 #pragma unroll
       for (int u = 0; u < C::U; ++u) issue(i + C::STAGES - C::U + u, behind + u);
       int left[C::U];                          // live tokens of a block (16 or more: all)
-      float s[C::U][2][4];
+      float s[C::U][NH][4];                    // S^T: rows tokens tok_r, + 8; columns heads
 #pragma unroll
       for (int u = 0; u < C::U; ++u) {
         left[u] = 0;
@@ -359,52 +391,52 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
           phases ^= 1u << (slot + u);
           pending &= ~(1u << (slot + u));
         }
-        // S = Q K^T
-        const uint8_t* sk = ring_p + (slot + u) * C::STAGE;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          s[u][t][0] = s[u][t][1] = s[u][t][2] = s[u][t][3] = 0.f;
+        for (int w = 0; w < NH; ++w) s[u][w][0] = s[u][w][1] = s[u][w][2] = s[u][w][3] = 0.f;
+        const uint8_t* sk = ring_p + (slot + u) * C::STAGE;
+        if constexpr (E4) {
 #pragma unroll
           for (int x = 0; x < C::KL; ++x) {
-            const uint4 v = *reinterpret_cast<const uint4*>(sk + piece_step<C::SW>(k_at, x) + t * 8 * C::SW);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            constexpr int PER = CT == MKV_DT_E4M3 ? 4 : 2;   // steps in a piece
+            const uint4 v0 = *reinterpret_cast<const uint4*>(sk + piece_on(k_at, 4 * x));
+            const uint4 v1 = *reinterpret_cast<const uint4*>(sk + piece_on(k_at, 4 * x) + 8 * C::SW);
+            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-            for (int k = 0; k < PER; ++k) {
-              const int ks = x * PER + k;
-              const uint32_t a[4] = {qa[ks][0], WIDE ? qa[ks][1] : 0u, qa[ks][NR],
-                                     WIDE ? qa[ks][WIDE ? 3 : 0] : 0u};
-              if constexpr (CT == MKV_DT_E4M3) {
-                uint32_t b0, b1;
-                e4m3x4_to_f16(w[k], b0, b1);
-                mma_acc<false>(s[u][t], a, b0, b1);
-              } else {
-                mma_acc<C::BF16>(s[u][t], a, w[2 * k], w[2 * k + 1]);
-              }
+            for (int k = 0; k < 4; ++k) {
+              uint32_t a[4];
+              e4m3x4_to_f16(w0[k], a[0], a[2]);
+              e4m3x4_to_f16(w1[k], a[1], a[3]);
+#pragma unroll
+              for (int w = 0; w < NH; ++w) mma_acc<false>(s[u][w], a, qb[w][4 * x + k][0], qb[w][4 * x + k][1]);
             }
           }
+        } else {
+          const uint32_t sa = smem_u32(sk);
+#pragma unroll
+          for (int ks = 0; ks < C::KS; ++ks) {
+            uint32_t a[4];
+            ldsm4<false>(sa + piece_on(k_at, 2 * ks), a);
+#pragma unroll
+            for (int w = 0; w < NH; ++w) mma_acc<C::BF16>(s[u][w], a, qb[w][ks][0], qb[w][ks][1]);
+          }
         }
-        // columns 2 c and 2 c + 1 are tokens 2 c and (2 c + 1) ^ 4 of 8
         if (left[u] < PA_BLOCK) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int w = 0; w < NH; ++w)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (8 * t + ((k & 1) ? (2 * c + 1) ^ 4 : 2 * c) >= left[u]) s[u][t][k] = -CUDART_INF_F;
+              if (tok_r + 8 * (k >> 1) >= left[u]) s[u][w][k] = -CUDART_INF_F;
         }
         if (p.scores && i + u < count) {
-          const int tok0 = (j0 + warp + PA_NW * (i + u)) * PA_BLOCK;
+          // 8 rows of a column are one 32-byte sector
+          const int tok0 = (j0 + warp + PA_NW * (i + u)) * PA_BLOCK + tok_r;
 #pragma unroll
-          for (int w = 0; w < NR; ++w) {
-            // lane c ^ 2 of the row has token 2 c + 1
-            const float x0 = __shfl_xor_sync(~0u, s[u][0][2 * w + 1], 2);
-            const float x1 = __shfl_xor_sync(~0u, s[u][1][2 * w + 1], 2);
-            if (r + 8 * w < p.g) {
-              float* to = score_row + 8 * w * p.score_stride + tok0 + 2 * c;
-              *reinterpret_cast<float2*>(to) = make_float2(s[u][0][2 * w] * sc[w], x0 * sc[w]);
-              *reinterpret_cast<float2*>(to + 8) = make_float2(s[u][1][2 * w] * sc[w], x1 * sc[w]);
+          for (int w = 0; w < NH; ++w)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int head = 8 * w + 2 * c + (k & 1);
+              if (head < p.g)
+                p.scores[(stream * p.g + head) * p.score_stride + tok0 + 8 * (k >> 1)] = s[u][w][k] * sc[w][k & 1];
             }
-          }
         }
       }
       // The reference m (of the unscaled products: the scale is positive) moves
@@ -412,91 +444,112 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
       // from its own scores: after a few steps that hardly happens, and the
       // lanes' maximum and the scaling of o are skipped.
       bool grows = false;
+      float top[NH][2];
 #pragma unroll
-      for (int w = 0; w < NR; ++w) {
-        top[w] = -CUDART_INF_F;
+      for (int w = 0; w < NH; ++w)
 #pragma unroll
-        for (int u = 0; u < C::U; ++u)
+        for (int k = 0; k < 2; ++k) {
+          top[w][k] = -CUDART_INF_F;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) top[w] = fmaxf(top[w], fmaxf(s[u][t][2 * w], s[u][t][2 * w + 1]));
-        grows |= fmaf(top[w], sc[w], mref[w]) > PA_BIAS + PA_SLACK;
-      }
-      if (__any_sync(~0u, grows)) {
-        float f[NR];
-#pragma unroll
-        for (int w = 0; w < NR; ++w) {
-          float x = fmaxf(top[w], __shfl_xor_sync(~0u, top[w], 1));
-          x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
-          x = fmaxf(x, m[w]);
-          f[w] = x > m[w] ? exp2_fast((m[w] - x) * sc[w]) : 1.f;
-          l[w] *= f[w];
-          m[w] = x;
-          if (x != -CUDART_INF_F) mref[w] = PA_BIAS - __fmul_rn(x, sc[w]);   // rounded as in the join
+          for (int u = 0; u < C::U; ++u) top[w][k] = fmaxf(top[w][k], fmaxf(s[u][w][k], s[u][w][k + 2]));
+          grows |= fmaf(top[w][k], sc[w][k], mref[w][k]) > PA_BIAS + PA_SLACK;
         }
+      if (__any_sync(~0u, grows)) {
 #pragma unroll
-        for (int x = 0; x < C::NT; ++x) {
-          o[x][0] *= f[0], o[x][1] *= f[0];
-          o[x][2] *= f[NR - 1], o[x][3] *= f[NR - 1];
+        for (int w = 0; w < NH; ++w) {
+          float f[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float x = top[w][k];
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+            x = fmaxf(x, m[w][k]);
+            f[k] = x > m[w][k] ? exp2_fast((m[w][k] - x) * sc[w][k]) : 1.f;
+            l[w][k] *= f[k];
+            m[w][k] = x;
+            if (x != -CUDART_INF_F) mref[w][k] = PA_BIAS - __fmul_rn(x, sc[w][k]);   // rounded as in the join
+          }
+#pragma unroll
+          for (int j = 0; j < C::KS; ++j) {
+            o[w][j][0] *= f[0], o[w][j][1] *= f[1];
+            o[w][j][2] *= f[0], o[w][j][3] *= f[1];
+          }
         }
       }
 #pragma unroll
       for (int u = 0; u < C::U; ++u) {
-        uint32_t ph[2 * NR], pl[2 * NR];       // [token half][row half]
+        uint32_t ph[NH][2], pl[NH][2];         // P^T: tokens 0..7 and 8..15, high and low parts
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int w = 0; w < NH; ++w)
 #pragma unroll
-          for (int w = 0; w < NR; ++w) {
-            const float a = exp2_fast(fmaf(s[u][t][2 * w], sc[w], mref[w]));
-            const float d = exp2_fast(fmaf(s[u][t][2 * w + 1], sc[w], mref[w]));
-            l[w] += a + d;
-            split_pair<C::BF16>(a, d, ph[t * NR + w], pl[t * NR + w]);
+          for (int t = 0; t < 2; ++t) {
+            const float x = exp2_fast(fmaf(s[u][w][2 * t], sc[w][0], mref[w][0]));
+            const float y = exp2_fast(fmaf(s[u][w][2 * t + 1], sc[w][1], mref[w][1]));
+            l[w][0] += x;
+            l[w][1] += y;
+            split_pair<C::BF16>(x, y, ph[w][t], pl[w][t]);
+            ph[w][t] = transpose8(ph[w][t]);
+            pl[w][t] = transpose8(pl[w][t]);
           }
-        // g <= 8: the low parts are the operand's rows 8..15
-        const uint32_t pa[4] = {ph[0], WIDE ? ph[1] : pl[0], ph[NR], WIDE ? ph[2 * NR - 1] : pl[1]};
-        const uint32_t pb[4] = {pl[0], pl[1], pl[NR], pl[2 * NR - 1]};
-        auto pv = [&](int nt, uint32_t b0, uint32_t b1) {
-          mma_acc<C::BF16>(o[nt], pa, b0, b1);
-          if constexpr (WIDE) mma_acc<C::BF16>(o[nt], pb, b0, b1);
+        auto pv = [&](int j, const uint32_t (&a)[4]) {
+#pragma unroll
+          for (int w = 0; w < NH; ++w) {
+            mma_acc<C::BF16>(o[w][j], a, ph[w][0], ph[w][1]);
+            mma_acc<C::BF16>(o[w][j], a, pl[w][0], pl[w][1]);
+          }
         };
         const uint8_t* sv = ring_p + (slot + u) * C::STAGE + PA_BLOCK * C::ROW;
+        const bool part = left[u] < PA_BLOCK;  // what lies behind the sequence in its last page may be anything
+        if constexpr (E4) {
 #pragma unroll
-        for (int x = 0; x < C::VL; ++x) {
-          uint32_t v[4][C::VB / 4];
+          for (int x = 0; x < C::VL; ++x) {
+            uint32_t v[4][C::VB / 4];          // tokens 2 c, (2 c + 1) ^ 4, and 8 further
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint8_t* from = sv + v_at[t & 1] + (t >> 1) * 8 * C::SW + x * PA_BLOCK * C::SW;
-            if constexpr (C::VB == 16) {
-              const uint4 y = *reinterpret_cast<const uint4*>(from);
-              v[t][0] = y.x, v[t][1] = y.y, v[t][2] = y.z, v[t][3] = y.w;
-            } else {
-              const uint2 y = *reinterpret_cast<const uint2*>(from);
-              v[t][0] = y.x, v[t][1] = y.y;
-            }
-          }
-          // what lies behind the sequence in its last page may be anything
-          if (left[u] < PA_BLOCK) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-              if (8 * (t >> 1) + ((t & 1) ? (2 * c + 1) ^ 4 : 2 * c) >= left[u]) {
-#pragma unroll
-                for (int y = 0; y < C::VB / 4; ++y) v[t][y] = 0u;
+            for (int t = 0; t < 4; ++t) {
+              const uint8_t* from = sv + piece_on(t & 1 ? v_at1 : v_at, 8 * x) + (t >> 1) * 8 * C::SW;
+              if constexpr (C::VB == 16) {
+                const uint4 y = *reinterpret_cast<const uint4*>(from);
+                v[t][0] = y.x, v[t][1] = y.y, v[t][2] = y.z, v[t][3] = y.w;
+              } else {
+                const uint2 y = *reinterpret_cast<const uint2*>(from);
+                v[t][0] = y.x, v[t][1] = y.y;
               }
-          }
-#pragma unroll
-          for (int y = 0; y < C::VB / 4; ++y) {
-            if constexpr (CT == MKV_DT_E4M3) {
-              uint32_t b0[4], b1[4];
-              e4m3x4_to_f16(__byte_perm(v[0][y], v[1][y], 0x5140), b0[0], b0[1]);
-              e4m3x4_to_f16(__byte_perm(v[0][y], v[1][y], 0x7362), b0[2], b0[3]);
-              e4m3x4_to_f16(__byte_perm(v[2][y], v[3][y], 0x5140), b1[0], b1[1]);
-              e4m3x4_to_f16(__byte_perm(v[2][y], v[3][y], 0x7362), b1[2], b1[3]);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) pv(x * C::EV + 4 * y + k, b0[k], b1[k]);
-            } else {
-              const int nt = x * C::EV + 2 * y;
-              pv(nt, __byte_perm(v[0][y], v[1][y], 0x5410), __byte_perm(v[2][y], v[3][y], 0x5410));
-              pv(nt + 1, __byte_perm(v[0][y], v[1][y], 0x7632), __byte_perm(v[2][y], v[3][y], 0x7632));
             }
+            if (part) {
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+                if (8 * (t >> 1) + ((t & 1) ? (2 * c + 1) ^ 4 : 2 * c) >= left[u]) {
+#pragma unroll
+                  for (int y = 0; y < C::VB / 4; ++y) v[t][y] = 0u;
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < C::VB / 4; ++y) {
+              uint32_t a[4], d[4];
+              e4m3x4_to_f16(__byte_perm(v[0][y], v[1][y], 0x5140), a[0], a[1]);
+              e4m3x4_to_f16(__byte_perm(v[2][y], v[3][y], 0x5140), a[2], a[3]);
+              pv(x * (C::VB / 2) + 2 * y, a);
+              e4m3x4_to_f16(__byte_perm(v[0][y], v[1][y], 0x7362), d[0], d[1]);
+              e4m3x4_to_f16(__byte_perm(v[2][y], v[3][y], 0x7362), d[2], d[3]);
+              pv(x * (C::VB / 2) + 2 * y + 1, d);
+            }
+          }
+        } else {
+          const uint32_t sa = smem_u32(sv);
+#pragma unroll
+          for (int j = 0; j < C::KS; ++j) {
+            uint32_t a[4];
+            ldsm4<true>(sa + piece_on(v_at, 2 * j), a);
+            if (part) {
+              // pairs of tokens 2 c, 2 c + 1 and 8 further
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const int tok = 2 * c + 8 * (t >> 1);
+                a[t] &= (tok < left[u] ? 0xffffu : 0u) | (tok + 1 < left[u] ? 0xffff0000u : 0u);
+              }
+            }
+            pv(j, a);
           }
         }
       }
@@ -504,7 +557,9 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
     }
     // the reference in the scaled domain from here on
 #pragma unroll
-    for (int w = 0; w < NR; ++w) m[w] = m[w] == -CUDART_INF_F ? m[w] : __fmul_rn(m[w], sc[w]);
+    for (int w = 0; w < NH; ++w)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) m[w][k] = m[w][k] == -CUDART_INF_F ? m[w][k] : __fmul_rn(m[w][k], sc[w][k]);
 
     if (gave_up) {
       // copies in flight must have landed before the ring is used for anything else
@@ -514,40 +569,42 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
     }
     // join the warps: the ring is drained and becomes [warp][head][D + 4]
 #pragma unroll
-    for (int w = 0; w < NR; ++w) {
-      l[w] += __shfl_xor_sync(~0u, l[w], 1);
-      l[w] += __shfl_xor_sync(~0u, l[w], 2);
-      if (c == 0) sm_m[warp][r + 8 * w] = m[w], sm_l[warp][r + 8 * w] = l[w];
-    }
+    for (int w = 0; w < NH; ++w)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float x = l[w][k];
+        x += __shfl_xor_sync(~0u, x, 4);
+        x += __shfl_xor_sync(~0u, x, 8);
+        x += __shfl_xor_sync(~0u, x, 16);
+        if (r == 0) sm_m[warp][8 * w + 2 * c + k] = m[w][k], sm_l[warp][8 * w + 2 * c + k] = x;
+      }
     __syncthreads();
     float* mg = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int w = 0; w < NR; ++w) {
-      const int head = r + 8 * w;
-      float top = sm_m[0][head];
+    for (int w = 0; w < NH; ++w)
 #pragma unroll
-      for (int k = 1; k < PA_NW; ++k) top = fmaxf(top, sm_m[k][head]);
-      const float f = m[w] == -CUDART_INF_F ? 0.f : exp2f(m[w] - top);
-      float* to = mg + (warp * C::HR + head) * (D + 4);
+      for (int k = 0; k < 2; ++k) {
+        const int head = 8 * w + 2 * c + k;
+        float top = sm_m[0][head];
 #pragma unroll
-      for (int x = 0; x < C::NT / C::EV; ++x)
+        for (int x = 1; x < PA_NW; ++x) top = fmaxf(top, sm_m[x][head]);
+        // a part without a live token stays zero
+        const bool none = m[w][k] == -CUDART_INF_F;
+        const float f = none ? 0.f : exp2f(m[w][k] - top);
+        float* to = mg + (warp * C::HR + head) * (D + 4);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int e = 0; e < C::EV; e += 4) {
-            float4 v;
-            float* vv = &v.x;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float* a = o[x * C::EV + e + y];
-              // g <= 8: rows 8..15 hold the low parts of the same heads.  A part
-              // without a live token stays zero even where f is.
-              const float t = WIDE ? a[2 * w + k] : a[k] + a[2 + k];
-              vv[y] = m[w] == -CUDART_INF_F ? 0.f : t * f;
-            }
-            *reinterpret_cast<float4*>(to + x * 8 * C::EV + (2 * c + k) * C::EV + e) = v;
+        for (int j = 0; j < C::KS; ++j) {
+          const float x = none ? 0.f : o[w][j][k] * f, y = none ? 0.f : o[w][j][2 + k] * f;
+          if constexpr (E4) {
+            // tile j: channels 2 j, 2 j + 1 of the lane's piece
+            constexpr int T = C::VB / 2;       // tiles of a piece
+            *reinterpret_cast<float2*>(to + (j / T) * 8 * C::VB + C::VB * r + 2 * (j % T)) = make_float2(x, y);
+          } else {
+            to[16 * j + r] = x;
+            to[16 * j + 8 + r] = y;
           }
-    }
+        }
+      }
     __syncthreads();
     const bool whole = j0 == 0 && j1 == nb;
     const float vs = CT == MKV_DT_E4M3 && p.vs ? p.vs[h] : 1.f;
@@ -602,8 +659,8 @@ cudaError_t launch_pa(const PagedAttnParams& p, cudaStream_t st) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t grid = p.split ? PA_SHARES * p.G : (int64_t)p.B * p.H;
-  paged_attn_kernel<CT, D, WIDE><<<(unsigned)grid, PA_NW * 32, C::SMEM, st>>>(p, kmap, vmap);
-  return cudaGetLastError();
+  return launch_kernel(paged_attn_kernel<CT, D, WIDE>, dim3((unsigned)grid), dim3(PA_NW * 32), C::SMEM, st, true, 0,
+                       p, kmap, vmap);
 }
 
 template <int D>
