@@ -289,16 +289,3 @@ def test_oracle_evict_by_hand():
     assert P.evict(acc, pos, 6, 3, recent=2).tolist() == [4, 5, 2]
     assert P.evict(np.array([np.nan, -1.0, 2.0], np.float32), np.arange(3), 9, 2).tolist() == [0, 2]
 
-
-def test_packed_arguments_have_the_structs_layout(M):
-    """The binding packs sizes in one go; field by field the struct must say the same."""
-    for packer, cls in ((M._ROPE_ARGS, M.mkv_rope_args), (M._APPEND_ARGS, M.mkv_paged_append_args),
-                        (M._DECODE_ARGS, M.mkv_paged_decode_args), (M._EVICT_ARGS, M.mkv_paged_evict_args)):
-        assert packer.size == ctypes.sizeof(cls)
-        n = sum(getattr(t, "_length_", 1) for _, t in cls._fields_)
-        got = cls.from_buffer_copy(packer.pack(*range(1, n + 1)))
-        flat = []
-        for name, _ in cls._fields_:
-            v = getattr(got, name)
-            flat += list(v) if isinstance(v, ctypes.Array) else [v]
-        assert flat == list(range(1, n + 1)), cls

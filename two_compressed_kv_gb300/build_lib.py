@@ -1,7 +1,8 @@
-"""Builds libmkv.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Builds libmkv.so (the C-ABI library) in-tree with nvcc for sm_103a, and
+_marshal.so, the tensor marshalling of its Python binding, with g++.
 
-Each .cu translation unit is compiled in parallel, then linked into one shared
-library next to this file.  Usage: python -m two_compressed_kv_gb300.build_lib
+Each translation unit is compiled in parallel, then the .cu ones are linked
+into one shared library next to this file.  Usage: python -m two_compressed_kv_gb300.build_lib
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmkv.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 SOURCES = ["mkv_api.cu", "k_compress.cu", "k_score.cu", "k_select.cu", "k_attn.cu", "k_checks.cu",
            "k_append.cu", "paged_api.cu", "k_rope.cu", "k_paged_attn_64.cu", "k_paged_attn_128.cu",
            "k_paged_attn_256.cu", "k_paged_join.cu", "k_evict.cu"]
@@ -37,6 +39,25 @@ def _run(cmd):
     return r.stdout
 
 
+def _marshal_cmd(out: str):
+    """Compiles csrc/py_marshal.cpp against this interpreter and its torch."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), cuda,
+           os.path.join(HERE, "..", "include")]
+    lib = os.path.join(root, "lib")
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             os.path.join(CSRC, "py_marshal.cpp"), "-o", out]
+            + [f for i in inc for f in ("-isystem", i)]
+            + ["-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+               "-ltorch_cuda", "-lc10_cuda"])
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nv = nvcc()
@@ -45,8 +66,11 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     for src in SOURCES:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
         jobs.append(([nv, "-c", os.path.join(CSRC, src), "-o", obj] + ARCH + FLAGS + extra, obj))
-    with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        marshal = ex.submit(_run, _marshal_cmd(MARSHAL + ".tmp"))
         outs = list(ex.map(lambda j: _run(j[0]), jobs))
+        marshal.result()
+    os.replace(MARSHAL + ".tmp", MARSHAL)
     if verbose or ptxas_info:
         for (cmd, _), out in zip(jobs, outs):
             print(" ".join(cmd[:3]))

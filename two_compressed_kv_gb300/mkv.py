@@ -9,7 +9,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from ctypes import (POINTER, Structure, c_char_p, c_double, c_float, c_int, c_int32, c_int64,
                     c_uint8, c_uint16, c_uint32, c_uint64, c_void_p)
 
@@ -77,6 +76,10 @@ class MkvRopePlan(Structure):
     """A rotation ready to use (mkv_rope_plan_init): plain host data."""
     _fields_ = [("turn", c_uint64 * MKV_ROPE_MAX_PAIRS), ("mult", c_float),
                 ("head_dim", c_int32), ("rot_dim", c_int32), ("interleaved", c_int32)]
+
+    @property
+    def address(self) -> int:
+        return ctypes.addressof(self)
 
 
 class mkv_rope_args(Structure):
@@ -394,98 +397,35 @@ def mkv_basis_static(k, v, basis, eigvals, stream=None) -> None:
 # ---- rotary positions and the paged cache ----------------------------------------------------
 #
 # These calls come once a layer and token, and their kernels take a few microseconds where the
-# batch is small, so the marshalling is kept short: sizes are packed into the argument struct in
-# one go, the current stream is read as an address, and the workspace size of a shape is
-# remembered by the cache object.
+# batch is small, so the tensors are checked and the argument structs filled in C++ (_marshal,
+# csrc/py_marshal.cpp).
 
-_DTYPES = {}
 _T = None                      # torch, once a call needs it
-_ROPE_ARGS = struct.Struct("@3P3q3qqq5i4x")
-_APPEND_ARGS = struct.Struct("@9P2q2q2q2qqq2i")
-_DECODE_ARGS = struct.Struct("@6PQ2qqq3if")
-_EVICT_ARGS = struct.Struct("@9PQqqq3i4x")
-_F16_TYPES = (MKV_DT_F16, MKV_DT_BF16)
-_FLOAT_TYPES = (MKV_DT_F16, MKV_DT_BF16, MKV_DT_F32)
+_M = None                      # the marshalling module
 
 
-def _torch():
-    global _T
-    if _T is None:
+def _native():
+    """The marshalling module; loaded with torch by the first call that needs it."""
+    global _T, _M
+    if _M is None:
         import torch
-        _DTYPES.update({torch.float16: MKV_DT_F16, torch.bfloat16: MKV_DT_BF16,
-                        torch.float32: MKV_DT_F32, torch.float8_e4m3fn: MKV_DT_E4M3})
-        _T = torch
-    return _T
+
+        from . import _marshal
+        _marshal.bind(*(ctypes.cast(getattr(_lib, f), c_void_p).value for f in (
+            "mkv_rope", "mkv_paged_append", "mkv_paged_decode_workspace", "mkv_paged_decode",
+            "mkv_paged_evict_workspace", "mkv_paged_evict")))
+        _T, _M = torch, _marshal
+    return _M
 
 
-def _dt(t, name, allowed):
-    """MKV_DT_* of a tensor whose type must be one of `allowed`."""
-    d = _DTYPES.get(t.dtype)
-    if d not in allowed:
-        raise TypeError(f"{name} has type {t.dtype}, which the call does not take")
-    return d
+def _done(status: int, where: str):
+    if status != MKV_OK:
+        raise MkvError(status, where)
 
 
-def _cuda(t, name):
-    """Index of a tensor's CUDA device."""
-    if not isinstance(t, _torch().Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be on a CUDA device")
-    return dev
-
-
-def _vec(t, name, dev, shape):
-    """(address, strides) of a tensor of that shape on device `dev` whose last dimension is
-    contiguous."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    return t.data_ptr(), st
-
-
-def _flat(t, name, dev, dtype, shape):
-    """Address of a contiguous tensor of the given type and shape on device `dev`."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _meta(t, name, dev, dtype, v):
-    """Address and row length of per-slot data [batch, kv_heads, slots]."""
-    sh = t.shape
-    if len(sh) != 3:
-        raise ValueError(f"{name} must be [batch, kv_heads, slots]")
-    return _flat(t, name, dev, dtype, (v.batch, v.n_kv_heads, sh[2])), sh[2]
-
-
-def _on_device(dev, fn, *args):
-    """fn(*args) with `dev` the current device."""
-    if _T._C._cuda_getDevice() == dev:
-        return fn(*args)
-    with _T.cuda.device(dev):
-        return fn(*args)
-
-
-def _launch(fn, where, dev, stream, *args):
-    if stream is None:
-        sp = _T._C._cuda_getCurrentRawStream(dev)
-    else:
-        sp = stream if isinstance(stream, int) else stream.cuda_stream
-    st = _on_device(dev, fn, *args, sp)
-    if st != MKV_OK:
-        raise MkvError(st, where)
+def _address(stream):
+    """A stream (torch.cuda.Stream or its address) as an address; None stays None."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def _new(shape, dtype, dev, stream):
@@ -496,24 +436,6 @@ def _new(shape, dtype, dev, stream):
         stream = _T.cuda.ExternalStream(stream, device=dev)
     with _T.cuda.stream(stream):
         return _T.empty(shape, dtype=dtype, device=dev)
-
-
-def _workspace(t, fn, where, cache, key, args, stream):
-    """(tensor, address, bytes) of a call's workspace: the caller's, or a new one of the size that
-    fn(cache, args) gives for the sizes in `key`."""
-    dev = cache.device.index
-    if t is None:
-        need = cache._sizes.get(key)
-        if need is None:
-            need = _on_device(dev, fn, cache._ref, args)
-            if need == 0:
-                raise MkvError(MKV_ERR_INVALID_ARG, where)
-            if len(cache._sizes) >= 256:
-                cache._sizes.clear()
-            cache._sizes[key] = need
-        t = _new(need, _T.uint8, dev, stream)
-    n = t.numel()
-    return t, _flat(t, "workspace", dev, _T.uint8, (n,)), n
 
 
 def mkv_rope_plan(head_dim, rot_dim=None, base=10000.0, interleaved=False, scaling="none",
@@ -536,26 +458,10 @@ def mkv_rope(plan, x, pos=None, out=None, transposed=False, first_pos=0, stream=
     dimension contiguous) by the positions pos (int32 [batch, tokens]; None: first_pos + token)
     into out (new where None; may be x; e.g. a transposed view of a [batch, heads, tokens,
     head_dim] tensor).  transposed: the gradient of the call.  Returns out."""
-    dev = _cuda(x, "x")
-    shape = x.shape
-    if len(shape) != 4 or shape[3] != plan.head_dim:
-        raise ValueError(f"x must be [batch, tokens, heads, {plan.head_dim}], got {tuple(shape)}")
-    dt = _dt(x, "x", _FLOAT_TYPES)
-    if out is None:
-        out = _new(shape, x.dtype, dev, stream)
-    elif out.dtype != x.dtype:
-        raise TypeError(f"out must be {x.dtype}, got {out.dtype}")
-    px, sx = _vec(x, "x", dev, shape)
-    po, so = _vec(out, "out", dev, shape)
-    b, t, h, _ = shape
-    pp = ps = 0
-    if pos is not None:
-        if pos.dtype != _T.int32:
-            raise TypeError(f"pos must be torch.int32, got {pos.dtype}")
-        pp, sp = _vec(pos, "pos", dev, (b, t))
-        ps = sp[0]
-    args = _ROPE_ARGS.pack(px, po, pp, *sx[:3], *so[:3], ps, t, b, h, dt, first_pos, transposed)
-    _launch(_lib.mkv_rope, "mkv_rope", dev, stream, ctypes.byref(plan), args)
+    m = _native()
+    if out is None and isinstance(x, _T.Tensor):
+        out = _new(x.shape, x.dtype, x.device, stream)
+    _done(m.rope(plan.address, x, pos, out, transposed, first_pos, _address(stream)), "mkv_rope")
     return out
 
 
@@ -566,42 +472,54 @@ class MkvPaged:
     word; check() reports what kernels found outside the cache."""
 
     def __init__(self, k_pages, v_pages, page_table, k_scale=None, v_scale=None):
-        dev = _cuda(k_pages, "k_pages")
+        _native()
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages), ("page_table", page_table)):
+            if not isinstance(t, _T.Tensor):
+                raise TypeError(f"{name} must be a torch tensor")
         if k_pages.dim() != 4:
             raise ValueError("k_pages must be [n_pages, kv_heads, page_size, head_dim]")
         if page_table.dim() != 2:
             raise ValueError("page_table must be [batch, max_pages]")
+        types = {_T.float16: MKV_DT_F16, _T.bfloat16: MKV_DT_BF16, _T.float8_e4m3fn: MKV_DT_E4M3}
+        if k_pages.dtype not in types:
+            raise TypeError(f"k_pages must be one of {list(types)}, got {k_pages.dtype}")
         v = self.view = mkv_paged_cache()
-        v.dtype = _dt(k_pages, "k_pages", (MKV_DT_F16, MKV_DT_BF16, MKV_DT_E4M3))
-        v.k_pages = _flat(k_pages, "k_pages", dev, k_pages.dtype, k_pages.shape)
-        v.v_pages = _flat(v_pages, "v_pages", dev, k_pages.dtype, k_pages.shape)
+        v.dtype = types[k_pages.dtype]
+        v.k_pages = _dptr(k_pages, k_pages.dtype, "k_pages")
+        v.v_pages = _dptr(v_pages, k_pages.dtype, "v_pages", k_pages.shape)
         if page_table.dtype != _T.int32:
             raise TypeError(f"page_table must be torch.int32, got {page_table.dtype}")
-        v.page_table, st = _vec(page_table, "page_table", dev, page_table.shape)
         v.batch, v.max_pages = page_table.shape
-        v.table_stride = max(st[0], v.max_pages) if v.batch == 1 else st[0]
+        if page_table.stride(1) != 1 and v.max_pages > 1:
+            raise ValueError("page_table must be contiguous in its last dimension")
+        v.page_table = page_table.data_ptr()
+        v.table_stride = max(page_table.stride(0), v.max_pages) if v.batch == 1 else page_table.stride(0)
         v.n_pages, v.n_kv_heads, v.page_size, v.head_dim = k_pages.shape
         for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
             if s is not None:
-                setattr(v, name, _flat(s, name, dev, _T.float32, (v.n_kv_heads,)))
+                setattr(v, name, _dptr(s, _T.float32, name, (v.n_kv_heads,)))
+        for t in (v_pages, page_table, k_scale, v_scale):
+            if t is not None and t.device != k_pages.device:
+                raise ValueError(f"all tensors of a cache must be on {k_pages.device}, one is on {t.device}")
         self.device = k_pages.device
         self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
         self.k_scale, self.v_scale = k_scale, v_scale
         self.status = _T.zeros(1, dtype=_T.int32, device=self.device)
         v.status = self.status.data_ptr()
-        self._ref = ctypes.byref(v)
-        self._sizes = {}                 # workspace bytes by the sizes they depend on
-        _check(_lib.mkv_paged_validate(self._ref), "mkv_paged_validate")
+        _check(_lib.mkv_paged_validate(ctypes.byref(v)), "mkv_paged_validate")
+        self._address, self._dev = ctypes.addressof(v), self.device.index
+        self._capacity = v.max_pages * v.page_size
 
     @property
     def capacity(self) -> int:
         """Slots the page table has room for in a sequence."""
-        return self.view.max_pages * self.view.page_size
+        return self._capacity
 
     def check(self) -> int:
         """MKV_OK, or MKV_ERR_DEVICE_CHECK when a kernel met a page, slot, sequence or length
         outside the cache since the last check (synchronous)."""
-        return _on_device(self.device.index, _lib.mkv_paged_check, self.status.data_ptr())
+        with _T.cuda.device(self.device):
+            return _lib.mkv_paged_check(self.status.data_ptr())
 
 
 def mkv_paged_append(cache, k, v, slot, seq=None, plan=None, pos=None, q=None, q_out=None,
@@ -610,44 +528,10 @@ def mkv_paged_append(cache, k, v, slot, seq=None, plan=None, pos=None, q=None, q
     keys are rotated by plan at pos (None: the slot).  A negative slot is padding.  q [n, q_heads,
     head_dim] is rotated into q_out (new where None), which is returned.  acc (fp32) and pos_meta
     (int32) [batch, kv_heads, slots]: set to 0 and to the position in the written slots."""
-    dev, w = cache.device.index, cache.view
-    n, hd = k.shape[0], w.head_dim
-    dt = _dt(k, "k", _F16_TYPES)
-    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
-        raise TypeError("k, v and q must be of one type")
-    shape, i32 = (n, w.n_kv_heads, hd), _T.int32
-    pk, sk = _vec(k, "k", dev, shape)
-    pv, sv = _vec(v, "v", dev, shape)
-    p_slot = _flat(slot, "slot", dev, i32, (n,))
-    p_seq = 0 if seq is None else _flat(seq, "seq", dev, i32, (n,))
-    p_pos = 0 if pos is None else _flat(pos, "pos", dev, i32, (n,))
-    pq = po = hq = 0
-    sq = so = (0, 0)
-    if q is not None:
-        qs = q.shape
-        if len(qs) != 3:
-            raise ValueError("q must be [n, q_heads, head_dim]")
-        hq = qs[1]
-        pq, sq = _vec(q, "q", dev, (n, hq, hd))
-        if q_out is None:
-            q_out = _new(qs, q.dtype, dev, stream)
-        elif q_out.dtype != q.dtype:
-            raise TypeError(f"q_out must be {q.dtype}, got {q_out.dtype}")
-        po, so = _vec(q_out, "q_out", dev, qs)
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    p_acc = p_meta = ms = 0
-    if acc is not None:
-        p_acc, ms = _meta(acc, "acc", dev, _T.float32, w)
-    if pos_meta is not None:
-        p_meta, m2 = _meta(pos_meta, "pos_meta", dev, i32, w)
-        if acc is not None and m2 != ms:
-            raise ValueError("acc and pos_meta must have the same shape")
-        ms = m2
-    args = _APPEND_ARGS.pack(pk, pv, pq, po, p_seq, p_slot, p_pos, p_acc, p_meta, sk[0], sk[1],
-                             sv[0], sv[1], sq[0], sq[1], so[0], so[1], ms, n, hq, dt)
-    _launch(_lib.mkv_paged_append, "mkv_paged_append", dev, stream, cache._ref,
-            None if plan is None else ctypes.byref(plan), args)
+    if q_out is None and isinstance(q, _T.Tensor):
+        q_out = _new(q.shape, q.dtype, q.device, stream)
+    _done(_M.append(cache._address, cache._dev, None if plan is None else plan.address, k, v, slot, seq,
+                    pos, q, q_out, acc, pos_meta, _address(stream)), "mkv_paged_append")
     return q_out
 
 
@@ -658,32 +542,12 @@ def mkv_paged_decode(cache, q, seq_lens, out=None, lse=None, acc=None, max_len=0
     where None), returned.  lse: fp32 [batch, q_heads] or None.  acc: fp32 [batch, kv_heads,
     slots] or None; every token's weights are added.  max_len: a bound on seq_lens (0: the page
     table's capacity).  workspace: a uint8 tensor (None: taken from torch's allocator)."""
-    dev, w = cache.device.index, cache.view
-    qs = q.shape
-    if len(qs) != 3:
-        raise ValueError("q must be [batch, q_heads, head_dim]")
-    b, hq = w.batch, qs[1]
-    shape = (b, hq, w.head_dim)
-    qt = _dt(q, "q", _F16_TYPES)
-    pq, sq = _vec(q, "q", dev, shape)
-    if out is None:
-        out = _new(shape, out_dtype or q.dtype, dev, stream)
+    if out is None and isinstance(q, _T.Tensor):
+        out = _new(q.shape, out_dtype or q.dtype, q.device, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
-    ot = _dt(out, "out", _FLOAT_TYPES)
-    po = _flat(out, "out", dev, out.dtype, shape)
-    pl = _flat(seq_lens, "seq_lens", dev, _T.int32, (b,))
-    pe = 0 if lse is None else _flat(lse, "lse", dev, _T.float32, (b, hq))
-    pa = sa = 0
-    if acc is not None:
-        pa, sa = _meta(acc, "acc", dev, _T.float32, w)
-        if max_len == 0:
-            max_len = min(cache.capacity, sa)
-    pack = lambda ws, nb: _DECODE_ARGS.pack(pq, po, pe, pl, pa, ws, nb, sq[0], sq[1], sa, max_len,
-                                            hq, qt, ot, scale)
-    workspace, pw, nb = _workspace(workspace, _lib.mkv_paged_decode_workspace, "mkv_paged_decode",
-                                   cache, (hq, max_len, qt, ot, scale, pa != 0), pack(0, 0), stream)
-    _launch(_lib.mkv_paged_decode, "mkv_paged_decode", dev, stream, cache._ref, pack(pw, nb))
+    _done(_M.decode(cache._address, cache._dev, cache._capacity, q, seq_lens, out, lse, acc, max_len, scale,
+                    workspace, _address(stream)), "mkv_paged_decode")
     return out
 
 
@@ -692,7 +556,8 @@ def mkv_paged_decode_workspace(cache, q_heads, max_len=0, weights=False) -> int:
     qt = MKV_DT_F16 if cache.view.dtype == MKV_DT_E4M3 else cache.view.dtype
     a = mkv_paged_decode_args(n_q_heads=q_heads, max_len=max_len, acc=1 if weights else None,
                               q_dtype=qt, out_dtype=qt)
-    n = _on_device(cache.device.index, _lib.mkv_paged_decode_workspace, cache._ref, ctypes.byref(a))
+    with _T.cuda.device(cache.device):
+        n = _lib.mkv_paged_decode_workspace(ctypes.byref(cache.view), ctypes.byref(a))
     if n == 0:
         raise MkvError(MKV_ERR_INVALID_ARG, "mkv_paged_decode_workspace")
     return n
@@ -705,32 +570,11 @@ def mkv_paged_evict(cache, acc, pos, seq_lens, next_pos, budget, sink=0, recent=
     kv_heads, slots_out] (None: in place, acc and pos themselves); seq_lens, next_pos int32
     [batch]; lens_out int32 [batch] (None: seq_lens); src int32 [batch, kv_heads, budget] (new
     where None): the slot each kept token came from.  Returns src."""
-    dev, w = cache.device.index, cache.view
-    i32, b = _T.int32, w.batch
-    pa, ms = _meta(acc, "acc", dev, _T.float32, w)
-    pp = _flat(pos, "pos", dev, i32, acc.shape)
-    if (acc_out is None) != (pos_out is None):
-        raise ValueError("acc_out and pos_out go together")
-    if acc_out is None:
-        pao, os_, ppo = pa, ms, pp
-    else:
-        pao, os_ = _meta(acc_out, "acc_out", dev, _T.float32, w)
-        ppo = _flat(pos_out, "pos_out", dev, i32, acc_out.shape)
-    pl = _flat(seq_lens, "seq_lens", dev, i32, (b,))
-    pn = _flat(next_pos, "next_pos", dev, i32, (b,))
-    plo = pl if lens_out is None else _flat(lens_out, "lens_out", dev, i32, (b,))
-    if max_len == 0:
-        max_len = min(cache.capacity, ms)
-    shape = (b, w.n_kv_heads, max(0, budget))
     if src is None:
-        src = _new(shape, i32, dev, stream)
-    ps = _flat(src, "src", dev, i32, shape)
-    pack = lambda ws, nb: _EVICT_ARGS.pack(pa, pp, pao, ppo, pl, pn, plo, ps, ws, nb, ms, os_,
-                                           max_len, budget, sink, recent)
-    workspace, pw, nb = _workspace(workspace, _lib.mkv_paged_evict_workspace, "mkv_paged_evict",
-                                   cache, (ms, os_, max_len, budget, sink, recent), pack(0, 0),
-                                   stream)
-    _launch(_lib.mkv_paged_evict, "mkv_paged_evict", dev, stream, cache._ref, pack(pw, nb))
+        v = cache.view
+        src = _new((v.batch, v.n_kv_heads, max(0, budget)), _T.int32, cache.device, stream)
+    _done(_M.evict(cache._address, cache._dev, cache._capacity, acc, pos, seq_lens, next_pos, budget, sink, recent,
+                   acc_out, pos_out, lens_out, src, max_len, workspace, _address(stream)), "mkv_paged_evict")
     return src
 
 
