@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(ET, 1) evict_select_kernel(const __grid_consta
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = R > 1 ? (int)cl.block_rank() : 0;
+  griddep_wait();
   griddep_launch();
   Slice s;
   if (!slice_of<R>(p, rank, s)) return;
@@ -427,6 +428,7 @@ __global__ void __launch_bounds__(ET, 1) evict_select_long_kernel(const __grid_c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned below = (1u << lane) - 1u;
   const int rank = R > 1 ? (int)cl.block_rank() : 0;
+  griddep_wait();
   griddep_launch();
   Slice s;
   if (!slice_of<R>(p, rank, s)) return;
@@ -613,6 +615,7 @@ __global__ void __launch_bounds__(MT) evict_move_kernel(const __grid_constant__ 
   const int b = (int)(stream / p.H), h = (int)(stream - (int64_t)b * p.H);
   const int tid = threadIdx.x;
   griddep_wait();
+  griddep_launch();
   int moved = 0;
   if (tid < MS) {
     const int t = c0 + tid;
@@ -674,13 +677,13 @@ template <int R>
 cudaError_t select_r(const EvictParams& p, cudaStream_t st) {
   const dim3 grid((unsigned)((int64_t)p.B * p.H * R));
   const int64_t sl = evict_slice(p.limit, R);
-  if (sl <= 8 * ET) return launch_kernel(evict_select_kernel<R, 8>, grid, dim3(ET), 0, st, false, R, p);
-  if (sl <= E_SHORT) return launch_kernel(evict_select_kernel<R, E_SHORT / ET>, grid, dim3(ET), 0, st, false, R, p);
+  if (sl <= 8 * ET) return launch_kernel(evict_select_kernel<R, 8>, grid, dim3(ET), 0, st, true, R, p);
+  if (sl <= E_SHORT) return launch_kernel(evict_select_kernel<R, E_SHORT / ET>, grid, dim3(ET), 0, st, true, R, p);
   const int totals = R > 1 ? (E_BINS + 2 * E_HIST) * (int)sizeof(int) : 0;
   const cudaError_t e = cudaFuncSetAttribute(evict_select_long_kernel<R>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, totals);
   if (e != cudaSuccess) return e;
-  return launch_kernel(evict_select_long_kernel<R>, grid, dim3(ET), totals, st, false, R, p);
+  return launch_kernel(evict_select_long_kernel<R>, grid, dim3(ET), totals, st, true, R, p);
 }
 
 }  // namespace

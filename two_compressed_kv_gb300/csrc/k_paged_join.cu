@@ -14,13 +14,14 @@ constexpr int JT = 256;
 // ---------------------------------------------------------------------------
 // join: o = sum_k o_k exp2(m_k - M) / sum_k l_k exp2(m_k - M) over the parts k
 // of one stream, in a fixed order.  The parts lie in L2; a CTA takes one query
-// head, its threads 4 elements each of every (1024 / D)-th part, so that the
-// longest stream (a part from every CTA) is still a few loads per thread.
+// head, its threads 4 elements each of every (4 T / D)-th part.  T = 1024 threads
+// where the heads are so few that all such CTAs run at once: a part from every
+// CTA of the split kernel is then still a few loads per thread.
 // grid: streams * g
 // ---------------------------------------------------------------------------
-template <int D>
-__global__ void __launch_bounds__(JT) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
-  constexpr int LD = D / 4, NG = JT / LD;      // threads of a part, parts at a time
+template <int D, int T>
+__global__ void __launch_bounds__(T) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
+  constexpr int LD = D / 4, NG = T / LD;       // threads of a part, parts at a time
   __shared__ float4 so[NG][LD];
   __shared__ float sm[NG], sl[NG];
   const int64_t row = blockIdx.x;
@@ -28,9 +29,9 @@ __global__ void __launch_bounds__(JT) paged_join_kernel(const __grid_constant__ 
   const int head = (int)(row - stream * p.g);
   const int b = (int)(stream / p.H), h = (int)(stream - (int64_t)b * p.H);
   const int grp = threadIdx.x / LD, d = (threadIdx.x - grp * LD);
-  const int n = paged_len(p, b);
   griddep_wait();
   griddep_launch();
+  const int n = paged_len(p, b);
   if (n == 0) {
     // no CTA of the split kernel meets an empty stream
     if (grp == 0) store_out4(p, row * D + 4 * d, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
@@ -101,8 +102,9 @@ __global__ void __launch_bounds__(JT) paged_weights_kernel(const __grid_constant
   const int64_t stream = blockIdx.x / chunks;
   const int t = (int)(blockIdx.x - stream * chunks) * WT + threadIdx.x * 4;
   const int b = (int)(stream / p.H);
-  const int n = paged_len(p, b);
   griddep_wait();
+  griddep_launch();
+  const int n = paged_len(p, b);
   if (threadIdx.x < p.g) z[threadIdx.x] = p.lse2[stream * p.g + threadIdx.x];
   __syncthreads();
   if (t >= n) return;
@@ -132,12 +134,23 @@ __global__ void __launch_bounds__(JT) paged_weights_kernel(const __grid_constant
 
 }  // namespace
 
+namespace {
+
+template <int D>
+cudaError_t join_d(const PagedAttnParams& p, cudaStream_t st) {
+  const int64_t rows = (int64_t)p.B * p.H * p.g;
+  const dim3 grid((unsigned)rows);
+  if (rows <= 2 * p.sms) return launch_kernel(paged_join_kernel<D, 1024>, grid, dim3(1024), 0, st, true, 0, p);
+  return launch_kernel(paged_join_kernel<D, JT>, grid, dim3(JT), 0, st, true, 0, p);
+}
+
+}  // namespace
+
 cudaError_t launch_paged_merge(const PagedAttnParams& p, int D, cudaStream_t st) {
-  const dim3 grid((unsigned)((int64_t)p.B * p.H * p.g));
   switch (D) {
-    case 64: return launch_kernel(paged_join_kernel<64>, grid, dim3(JT), 0, st, true, 0, p);
-    case 128: return launch_kernel(paged_join_kernel<128>, grid, dim3(JT), 0, st, true, 0, p);
-    default: return launch_kernel(paged_join_kernel<256>, grid, dim3(JT), 0, st, true, 0, p);
+    case 64: return join_d<64>(p, st);
+    case 128: return join_d<128>(p, st);
+    default: return join_d<256>(p, st);
   }
 }
 

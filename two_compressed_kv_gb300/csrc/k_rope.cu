@@ -12,6 +12,7 @@
 // What bounds it: memory, once each element's load and store is 16 bytes wide
 // and a thread's angles (the instructions are in sincospif) are shared by all
 // heads it handles.
+#include "decode_common.cuh"
 #include "paged_internal.cuh"
 
 namespace mkv {
@@ -183,6 +184,8 @@ __device__ __forceinline__ void turn_heads(int h0, int h1, bool turns, const flo
 // ---------------------------------------------------------------------------
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(RT) rope_vec_kernel(const __grid_constant__ RopeParams p) {
+  griddep_wait();
+  griddep_launch();
   constexpr int V = Elem<T>::V, NP = HALF ? V : V / 2;
   int64_t t;
   int u;
@@ -217,6 +220,8 @@ __global__ void __launch_bounds__(RT) rope_vec_kernel(const __grid_constant__ Ro
 // fit: a unit is one pair, or one copied element.
 template <typename T>
 __global__ void __launch_bounds__(RT) rope_elem_kernel(const __grid_constant__ RopeParams p) {
+  griddep_wait();
+  griddep_launch();
   using E = Elem<T>;
   int64_t t;
   int u;
@@ -247,13 +252,9 @@ template <typename T>
 cudaError_t launch_rope_t(const RopeParams& p, bool vec, cudaStream_t st) {
   const int64_t blocks = (p.tokens * p.units + RT - 1) / RT;
   const dim3 grid((unsigned)blocks, (p.heads + p.heads_per - 1) / p.heads_per, p.batch);
-  if (!vec)
-    rope_elem_kernel<T><<<grid, RT, 0, st>>>(p);
-  else if (p.plan.interleaved)
-    rope_vec_kernel<T, false><<<grid, RT, 0, st>>>(p);
-  else
-    rope_vec_kernel<T, true><<<grid, RT, 0, st>>>(p);
-  return cudaGetLastError();
+  if (!vec) return launch_kernel(rope_elem_kernel<T>, grid, dim3(RT), 0, st, true, 0, p);
+  if (p.plan.interleaved) return launch_kernel(rope_vec_kernel<T, false>, grid, dim3(RT), 0, st, true, 0, p);
+  return launch_kernel(rope_vec_kernel<T, true>, grid, dim3(RT), 0, st, true, 0, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -293,6 +294,8 @@ __device__ __forceinline__ void store_row(uint8_t* row, int e, const Vec16& v, f
 
 template <typename T, bool HALF, bool E4M3>
 __global__ void __launch_bounds__(RT) append_rows_kernel(const __grid_constant__ AppendRowsParams p) {
+  griddep_wait();
+  griddep_launch();
   using E = Elem<T>;
   constexpr int V = 8, NP = HALF ? V : V / 2, HB = 2;
   int64_t t;
@@ -410,10 +413,8 @@ cudaError_t launch_append_t(const AppendRowsParams& p, cudaStream_t st) {
   const int64_t blocks = (p.a.n * p.units + RT - 1) / RT;
   const dim3 grid((unsigned)blocks, (p.heads_total + p.heads_per - 1) / p.heads_per);
   if (p.plan.interleaved || p.rot_units == 0)
-    append_rows_kernel<T, false, E4M3><<<grid, RT, 0, st>>>(p);
-  else
-    append_rows_kernel<T, true, E4M3><<<grid, RT, 0, st>>>(p);
-  return cudaGetLastError();
+    return launch_kernel(append_rows_kernel<T, false, E4M3>, grid, dim3(RT), 0, st, true, 0, p);
+  return launch_kernel(append_rows_kernel<T, true, E4M3>, grid, dim3(RT), 0, st, true, 0, p);
 }
 
 }  // namespace

@@ -455,6 +455,7 @@ mkv_status mkv_paged_decode(const mkv_paged_cache* c, const mkv_paged_decode_arg
   p.pre = reinterpret_cast<int64_t*>(ws + l.pre);
   p.scores = a->acc ? reinterpret_cast<float*>(ws + l.scores) : nullptr;
   p.score_stride = l.score_stride;
+  p.sms = sms;
   p.G = l.G;
   p.min_blocks = kMinBlocks;
   p.split = l.split;

@@ -84,6 +84,7 @@ struct PagedAttnParams {
   int64_t* pre;                   // [B + 1]: load before each sequence (split)
   float* scores;                  // [B H g][score_stride], log2 domain; only with acc
   int64_t score_stride;
+  int sms;                        // of the device
   int G;                          // CTAs that are resident at once in the split kernel
   int min_blocks;                 // smallest share of a CTA, in blocks
   int piece_load;                 // what a part of a stream costs apart from its blocks, in blocks
