@@ -280,7 +280,7 @@ def test_decode_one_long_stream(M):
 
 def test_decode_many_sequences(M):
     """More sequences than the split kernel's prefix sums hold, and the most that they hold."""
-    for b in (1024, 1025):
+    for b in (512, 513, 1025):
         lens = [(37 * i) % 1500 if i % 97 == 0 else i % 5 for i in range(b)]
         cache = Cache(M, E4M3, lens, 1, 64, 256, seed=2, spare=0)
         decode_run(M, cache, 1, 2, 64, F16)

@@ -40,8 +40,6 @@
 namespace mkv {
 namespace {
 
-constexpr int PA_NW = 4;              // warps per CTA
-
 // m16n8k16 products with fp32 accumulation.  Not volatile: the compiler may
 // interleave them with the loads and conversions of the next step.
 template <bool BF16>
@@ -108,7 +106,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-template <int CT, int D, bool WIDE>
+template <int CT, int D, bool WIDE, int NW>
 struct PA {
   static constexpr int ES = CT == MKV_DT_E4M3 ? 1 : 2;
   static constexpr bool BF16 = CT == MKV_DT_BF16;
@@ -124,11 +122,11 @@ struct PA {
   static constexpr int STAGES = STAGE >= 8192 ? 3 : STAGE >= 4096 ? 4 : 8;
   static_assert(STAGES % U == 0, "a step's slots do not wrap");
   static constexpr int HR = 8 * NH;                        // head rows
-  static constexpr int MERGE = PA_NW * HR * (D + 4) * 4;
-  static constexpr int RING = PA_NW * STAGES * STAGE;
+  static constexpr int MERGE = NW * HR * (D + 4) * 4;
+  static constexpr int RING = NW * STAGES * STAGE;
   static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + 1024;   // and its alignment
-  static constexpr int CTAS = paged_ctas(ROW);             // per SM
-  static_assert(CTAS * (SMEM + 10 * 1024) <= 228 * 1024, "resident CTAs' shared memory");
+  static constexpr int CTAS = NW == 8 ? 1 : paged_ctas(ROW);   // per SM
+  static_assert(CTAS * (SMEM + 9 * 1024) <= 228 * 1024, "resident CTAs' shared memory");
 };
 
 // Byte offset of 16-byte piece `piece` (of the first SW bytes) of row `row` in a
@@ -147,19 +145,20 @@ __device__ __forceinline__ uint32_t piece_on(uint32_t at, int by) {
 }
 
 // ---------------------------------------------------------------------------
-// grid: split ? 3 G : streams; block: 4 warps; dynamic smem PA::SMEM
+// grid: split ? 3 G : streams; block: NW warps; dynamic smem PA::SMEM
 // ---------------------------------------------------------------------------
-template <int CT, int D, bool WIDE>
-__global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
+template <int CT, int D, bool WIDE, int NW>
+__global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
     paged_attn_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
-  using C = PA<CT, D, WIDE>;
+  using C = PA<CT, D, WIDE, NW>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // the swizzle goes by address bits 7..9
-  __shared__ uint64_t full[PA_NW][C::STAGES];
-  __shared__ int64_t pre[PA_MAX_B + 1];        // split: load before each sequence
-  __shared__ float sm_m[PA_NW][C::HR], sm_l[PA_NW][C::HR];
-  __shared__ int64_t warp_sum[PA_NW];
+  __shared__ uint64_t full[NW][C::STAGES];
+  __shared__ int64_t pre[PA_MAX_B + 1];        // split: load before each sequence,
+  __shared__ int len_of[PA_MAX_B];             // and its length
+  __shared__ float sm_m[NW][C::HR], sm_l[NW][C::HR];
+  __shared__ int64_t warp_sum[NW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;       // fragment row and column pair
   constexpr int NH = C::NH;
@@ -193,11 +192,14 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
   int b = 0;
   if (p.split) {
     // prefix sums of the sequences' load: each thread a run of sequences
-    const int run = (p.B + PA_NW * 32 - 1) / (PA_NW * 32);
+    const int run = (p.B + NW * 32 - 1) / (NW * 32);
     int64_t sum = 0;
     for (int k = 0; k < run; ++k) {
       const int i = tid * run + k;
-      if (i < p.B) sum += paged_load(p, paged_len(p, i)) * p.H;
+      if (i < p.B) {
+        len_of[i] = paged_len(p, i);
+        sum += paged_load(p, len_of[i]) * p.H;
+      }
     }
     int64_t inc = sum;
 #pragma unroll
@@ -213,13 +215,13 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
       const int i = tid * run + k;
       if (i < p.B) {
         pre[i] = base;
-        base += paged_load(p, paged_len(p, i)) * p.H;
+        base += paged_load(p, len_of[i]) * p.H;
       }
       if (i == p.B - 1) pre[p.B] = base;
     }
     __syncthreads();
     if (blockIdx.x == 0)
-      for (int i = tid; i <= p.B; i += PA_NW * 32) p.pre[i] = pre[i];   // for the join
+      for (int i = tid; i <= p.B; i += NW * 32) p.pre[i] = pre[i];   // for the join
     const PagedShares shares(p, pre[p.B]);
     g0 = shares.first(blockIdx.x);
     g1 = shares.first(blockIdx.x + 1);
@@ -239,11 +241,11 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
     if (p.split) {
       if (at >= g1) break;
       while (pre[b + 1] <= at) ++b;
-      n = paged_len(p, b);
+      n = len_of[b];
       nb = (n + PA_BLOCK - 1) / PA_BLOCK;
       const int64_t off = at - pre[b];
       const int load = (int)paged_load(p, n);
-      h = (int)(off / load);
+      h = (int)div_small(off, load);
       const int v0 = (int)(off - (int64_t)h * load), v1 = (int)min((int64_t)load, v0 + (g1 - at));
       at += v1 - v0;
       j0 = max(0, v0 - p.piece_load);
@@ -264,9 +266,9 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
 
     // this warp's blocks: j0 + warp, + 4, ...; lane i holds the pool row of
     // the i-th of the next 32 (in blocks of 16 rows; -1: page outside the cache)
-    const int count = gave_up ? 0 : max(0, (j1 - j0 - warp + PA_NW - 1) / PA_NW);
+    const int count = gave_up ? 0 : max(0, (j1 - j0 - warp + NW - 1) / NW);
     auto entries = [&](int first) {
-      const int j = j0 + warp + PA_NW * (first + lane);
+      const int j = j0 + warp + NW * (first + lane);
       int e = -1;
       if (first + lane < count) {
         const int pg = j / p.bpp;
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
       for (int u = 0; u < C::U; ++u) {
         left[u] = 0;
         if (i + u < count && (valid_bits >> (slot + u) & 1)) {
-          left[u] = n - (j0 + warp + PA_NW * (i + u)) * PA_BLOCK;
+          left[u] = n - (j0 + warp + NW * (i + u)) * PA_BLOCK;
           const bool ok = mbar_wait(&full[warp][slot + u], phases >> (slot + u) & 1);
           if (!__all_sync(~0u, ok)) {
             if (lane == 0 && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
@@ -428,7 +430,7 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
         }
         if (p.scores && i + u < count) {
           // 8 rows of a column are one 32-byte sector
-          const int tok0 = (j0 + warp + PA_NW * (i + u)) * PA_BLOCK + tok_r;
+          const int tok0 = (j0 + warp + NW * (i + u)) * PA_BLOCK + tok_r;
 #pragma unroll
           for (int w = 0; w < NH; ++w)
 #pragma unroll
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
         const int head = 8 * w + 2 * c + k;
         float top = sm_m[0][head];
 #pragma unroll
-        for (int x = 1; x < PA_NW; ++x) top = fmaxf(top, sm_m[x][head]);
+        for (int x = 1; x < NW; ++x) top = fmaxf(top, sm_m[x][head]);
         // a part without a live token stays zero
         const bool none = m[w][k] == -CUDART_INF_F;
         const float f = none ? 0.f : exp2f(m[w][k] - top);
@@ -609,15 +611,15 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
     const bool whole = j0 == 0 && j1 == nb;
     const float vs = CT == MKV_DT_E4M3 && p.vs ? p.vs[h] : 1.f;
     const int64_t part = 2 * (int64_t)blockIdx.x + (j0 == 0 ? 1 : 0);
-    for (int e = tid; e < p.g * (D / 4); e += PA_NW * 32) {
+    for (int e = tid; e < p.g * (D / 4); e += NW * 32) {
       const int head = e / (D / 4), d = (e - head * (D / 4)) * 4;
       float top = sm_m[0][head];
 #pragma unroll
-      for (int k = 1; k < PA_NW; ++k) top = fmaxf(top, sm_m[k][head]);
+      for (int k = 1; k < NW; ++k) top = fmaxf(top, sm_m[k][head]);
       float sum = 0.f;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < PA_NW; ++k) {
+      for (int k = 0; k < NW; ++k) {
         const float mk = sm_m[k][head];
         sum += mk == -CUDART_INF_F ? sm_l[k][head] : sm_l[k][head] * exp2f(mk - top);
         const float4 v = *reinterpret_cast<const float4*>(mg + (k * C::HR + head) * (D + 4) + d);
@@ -649,18 +651,27 @@ __global__ void __launch_bounds__(PA_NW * 32, PA<CT, D, WIDE>::CTAS)
   }
 }
 
-template <int CT, int D, bool WIDE>
-cudaError_t launch_pa(const PagedAttnParams& p, cudaStream_t st) {
-  using C = PA<CT, D, WIDE>;
+template <int CT, int D, bool WIDE, int NW>
+cudaError_t launch_pa_nw(const PagedAttnParams& p, cudaStream_t st) {
+  using C = PA<CT, D, WIDE, NW>;
   CUtensorMap kmap, vmap;
   if (cudaError_t e = encode_rows_map(&kmap, p.kp, p.rows, C::ROW, PA_BLOCK)) return e;
   if (cudaError_t e = encode_rows_map(&vmap, p.vp, p.rows, C::ROW, PA_BLOCK)) return e;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<CT, D, WIDE>,
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<CT, D, WIDE, NW>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t grid = p.split ? PA_SHARES * p.G : (int64_t)p.B * p.H;
-  return launch_kernel(paged_attn_kernel<CT, D, WIDE>, dim3((unsigned)grid), dim3(PA_NW * 32), C::SMEM, st, true, 0,
+  return launch_kernel(paged_attn_kernel<CT, D, WIDE, NW>, dim3((unsigned)grid), dim3(NW * 32), C::SMEM, st, true, 0,
                        p, kmap, vmap);
+}
+
+// 4 warps a CTA and several CTAs an SM; where an SM gets one CTA at most, 8 warps
+// (rows of 512 bytes, whose rings do not fit, apart).
+template <int CT, int D, bool WIDE>
+cudaError_t launch_pa(const PagedAttnParams& p, cudaStream_t st) {
+  if constexpr (PA<CT, D, WIDE, 4>::ROW < 512)
+    if ((p.split ? p.G : (int64_t)p.B * p.H) <= p.sms) return launch_pa_nw<CT, D, WIDE, 8>(p, st);
+  return launch_pa_nw<CT, D, WIDE, 4>(p, st);
 }
 
 template <int D>

@@ -48,7 +48,7 @@ cudaError_t launch_append_rows(const AppendRowsParams& p, cudaStream_t st);
 // attention over the paged cache
 // ---------------------------------------------------------------------------
 constexpr int PA_BLOCK = 16;      // tokens per block: the unit of work; a block lies in one page
-constexpr int PA_MAX_B = 1024;    // sequences whose prefix sums fit the split kernel
+constexpr int PA_MAX_B = 512;     // sequences whose prefix sums fit the split kernel
 constexpr float PA_SLACK = 3.f;    // how far scores (log2) may pass the reference of the exponents
 constexpr float PA_UNSET = 1e38f;
 constexpr float PA_BIAS = 12.f;   // probabilities carry a factor 2^12 until the division by their sum
@@ -99,6 +99,12 @@ __device__ __forceinline__ int paged_len(const PagedAttnParams& p, int b) {
   return n < 0 ? 0 : min(n, p.limit);
 }
 
+// a / b, mostly of numbers that fit 32 bits (a 64-bit division is some hundred
+// instructions in a prologue that every share pays).
+__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Load of a stream of n tokens: its blocks and a fixed cost.
 __device__ __forceinline__ int64_t paged_load(const PagedAttnParams& p, int n) {
   return n == 0 ? 0 : (n + PA_BLOCK - 1) / PA_BLOCK + p.piece_load;
@@ -114,11 +120,11 @@ struct PagedShares {
   int G;
   __device__ __forceinline__ PagedShares(const PagedAttnParams& p, int64_t total_) : total(total_), G(p.G) {
     if (total < (int64_t)G * p.tail_from) {
-      big = max((total + G - 1) / G, (int64_t)p.min_blocks);
+      big = max(div_small(total + G - 1, G), (int64_t)p.min_blocks);
       small = 1;
     } else {
-      big = total * (16 - p.tail16) / 16 / G;
-      small = (total - big * G + 2 * G - 1) / (2 * G);
+      big = div_small(total * (16 - p.tail16) / 16, G);
+      small = div_small(total - big * G + 2 * G - 1, 2 * G);
     }
   }
   // start of share i, and the share that load v belongs to
@@ -126,7 +132,7 @@ struct PagedShares {
     return min(total, i < G ? i * big : G * big + (i - G) * small);
   }
   __device__ __forceinline__ int of(int64_t v) const {
-    return (int)(v < G * big ? v / big : G + (v - G * big) / small);
+    return (int)(v < G * big ? div_small(v, big) : G + div_small(v - G * big, small));
   }
 };
 
