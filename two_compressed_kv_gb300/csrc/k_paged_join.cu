@@ -37,7 +37,6 @@ __global__ void __launch_bounds__(T) paged_join_kernel(const __grid_constant__ P
     if (grp == 0) store_out4(p, row * D + 4 * d, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
     if (threadIdx.x == 0) {
       if (p.lse) p.lse[row] = -CUDART_INF_F;
-      p.lse2[row] = -CUDART_INF_F;
       if (h == 0 && head == 0 && p.status && p.lens[b] != n) atomicOr(p.status, DEV_ERR_CHECK);
     }
     return;
@@ -81,15 +80,13 @@ __global__ void __launch_bounds__(T) paged_join_kernel(const __grid_constant__ P
     }
     store_out4(p, row * D + 4 * d, a, sum == 0.f ? 0.f : 1.f / sum);
     if (d == 0) {
-      const float z = sum == 0.f ? -CUDART_INF_F : top - PA_BIAS + log2f(sum);
-      if (p.lse) p.lse[row] = z * 0.6931471805599453f;
-      p.lse2[row] = z;
+      store_stat(p, row, top, sum);
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// weights: acc[t] += sum over the group of exp2(score - lse2).  One owner per
+// weights: acc[t] += sum over the group of exp2(score - reference) / sum.  One owner per
 // token: no atomics.  Memory-bound: 4 g bytes read and 8 read and written per
 // token against 4 D for its fp16 rows.
 // grid: streams * chunks of WT tokens
@@ -98,14 +95,14 @@ constexpr int WT = 1024;
 
 __global__ void __launch_bounds__(JT) paged_weights_kernel(const __grid_constant__ PagedAttnParams p,
                                                            int chunks) {
-  __shared__ float z[MAX_G];
+  __shared__ float4 z[MAX_G];
   const int64_t stream = blockIdx.x / chunks;
   const int t = (int)(blockIdx.x - stream * chunks) * WT + threadIdx.x * 4;
   const int b = (int)(stream / p.H);
   griddep_wait();
   griddep_launch();
   const int n = paged_len(p, b);
-  if (threadIdx.x < p.g) z[threadIdx.x] = p.lse2[stream * p.g + threadIdx.x];
+  if (threadIdx.x < p.g) z[threadIdx.x] = p.stat[stream * p.g + threadIdx.x];
   __syncthreads();
   if (t >= n) return;
   float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -113,11 +110,15 @@ __global__ void __launch_bounds__(JT) paged_weights_kernel(const __grid_constant
 #pragma unroll 4
   for (int i = 0; i < p.g; ++i) {
     const float4 v = *reinterpret_cast<const float4*>(s + i * p.score_stride);
-    // a masked token weighs nothing, in a row without any live token too
-    w.x += v.x == -CUDART_INF_F ? 0.f : exp2f(v.x - z[i]);
-    w.y += v.y == -CUDART_INF_F ? 0.f : exp2f(v.y - z[i]);
-    w.z += v.z == -CUDART_INF_F ? 0.f : exp2f(v.z - z[i]);
-    w.w += v.w == -CUDART_INF_F ? 0.f : exp2f(v.w - z[i]);
+    // a masked token weighs nothing, in a row without any live token too; the
+    // difference to the reference comes first, so that no digit of a token that
+    // weighs much is lost
+    const float4 y = z[i];
+    auto weight = [&](float x) { return x == -CUDART_INF_F ? 0.f : exp2f(fmaf(x, y.z, -y.x) - y.y); };
+    w.x += weight(v.x);
+    w.y += weight(v.y);
+    w.z += weight(v.z);
+    w.w += weight(v.w);
   }
   float* a = p.acc + stream * p.acc_stride + t;
   if (t + 4 <= n && (reinterpret_cast<uintptr_t>(a) & 15u) == 0) {

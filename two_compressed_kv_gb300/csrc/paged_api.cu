@@ -98,7 +98,7 @@ struct DecodeLayout {
   int G;
   int64_t limit;
   int64_t score_stride;
-  uint64_t part_o, part_ml, lse2, pre, scores, total;   // byte offsets
+  uint64_t part_o, part_ml, stat, pre, scores, total;   // byte offsets
 };
 
 const char* check_decode(const mkv_paged_cache* c, const mkv_paged_decode_args* a) {
@@ -142,7 +142,7 @@ DecodeLayout decode_layout(const mkv_paged_cache* c, const mkv_paged_decode_args
   l.part_o = place(l.split ? 2ull * PA_SHARES * l.G * g * c->head_dim * 4 : 0);
   l.part_ml = place(l.split ? 2ull * PA_SHARES * l.G * g * 8 : 0);
   l.pre = place(l.split ? 8ull * (c->batch + 1) : 0);
-  l.lse2 = place((uint64_t)streams * g * 4);
+  l.stat = place((uint64_t)streams * g * 16);
   l.scores = place(a->acc ? (uint64_t)streams * g * l.score_stride * 4 : 0);
   l.total = at;
   return l;
@@ -451,7 +451,7 @@ mkv_status mkv_paged_decode(const mkv_paged_cache* c, const mkv_paged_decode_arg
   p.acc_stride = a->acc_stride;
   p.part_o = reinterpret_cast<float*>(ws + l.part_o);
   p.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
-  p.lse2 = reinterpret_cast<float*>(ws + l.lse2);
+  p.stat = reinterpret_cast<float4*>(ws + l.stat);
   p.pre = reinterpret_cast<int64_t*>(ws + l.pre);
   p.scores = a->acc ? reinterpret_cast<float*>(ws + l.scores) : nullptr;
   p.score_stride = l.score_stride;

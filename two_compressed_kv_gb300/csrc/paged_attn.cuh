@@ -371,6 +371,15 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
 #pragma unroll
       for (int k = 0; k < 2; ++k) m[w][k] = -CUDART_INF_F, l[w][k] = 0.f, mref[w][k] = PA_UNSET;
 
+    if (p.scores && j0 == 0 && warp == 0 && r == 0) {
+      // the scores are kept unscaled
+#pragma unroll
+      for (int w = 0; w < NH; ++w)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (8 * w + 2 * c + k < p.g) p.stat[stream * p.g + 8 * w + 2 * c + k].z = sc[w][k];
+    }
+
     int slot = 0;
     for (int i = 0; i < count && !gave_up; i += C::U) {
       // the slots before these were read in the last step, by all lanes
@@ -393,8 +402,13 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
           phases ^= 1u << (slot + u);
           pending &= ~(1u << (slot + u));
         }
+        // Two chains of accumulation, for their latency and because a chain cuts each
+        // sum off towards zero.
+        float s1[NH][4];
 #pragma unroll
-        for (int w = 0; w < NH; ++w) s[u][w][0] = s[u][w][1] = s[u][w][2] = s[u][w][3] = 0.f;
+        for (int w = 0; w < NH; ++w)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[u][w][k] = s1[w][k] = 0.f;
         const uint8_t* sk = ring_p + (slot + u) * C::STAGE;
         if constexpr (E4) {
 #pragma unroll
@@ -408,7 +422,7 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
               e4m3x4_to_f16(w0[k], a[0], a[2]);
               e4m3x4_to_f16(w1[k], a[1], a[3]);
 #pragma unroll
-              for (int w = 0; w < NH; ++w) mma_acc<false>(s[u][w], a, qb[w][4 * x + k][0], qb[w][4 * x + k][1]);
+              for (int w = 0; w < NH; ++w) mma_acc<false>(k & 1 ? s1[w] : s[u][w], a, qb[w][4 * x + k][0], qb[w][4 * x + k][1]);
             }
           }
         } else {
@@ -418,9 +432,13 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
             uint32_t a[4];
             ldsm4<false>(sa + piece_on(k_at, 2 * ks), a);
 #pragma unroll
-            for (int w = 0; w < NH; ++w) mma_acc<C::BF16>(s[u][w], a, qb[w][ks][0], qb[w][ks][1]);
+            for (int w = 0; w < NH; ++w) mma_acc<C::BF16>(ks & 1 ? s1[w] : s[u][w], a, qb[w][ks][0], qb[w][ks][1]);
           }
         }
+#pragma unroll
+        for (int w = 0; w < NH; ++w)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[u][w][k] += s1[w][k];
         if (left[u] < PA_BLOCK) {
 #pragma unroll
           for (int w = 0; w < NH; ++w)
@@ -437,7 +455,7 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
             for (int k = 0; k < 4; ++k) {
               const int head = 8 * w + 2 * c + (k & 1);
               if (head < p.g)
-                p.scores[(stream * p.g + head) * p.score_stride + tok0 + 8 * (k >> 1)] = s[u][w][k] * sc[w][k & 1];
+                p.scores[(stream * p.g + head) * p.score_stride + tok0 + 8 * (k >> 1)] = s[u][w][k];
             }
         }
       }
@@ -494,11 +512,17 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
             ph[w][t] = transpose8(ph[w][t]);
             pl[w][t] = transpose8(pl[w][t]);
           }
+        // The products cut their sums off towards zero, which over many blocks adds
+        // up (2e-5 after 400): a block's are summed by themselves and added to O
+        // with rounding to nearest.
         auto pv = [&](int j, const uint32_t (&a)[4]) {
 #pragma unroll
           for (int w = 0; w < NH; ++w) {
-            mma_acc<C::BF16>(o[w][j], a, ph[w][0], ph[w][1]);
-            mma_acc<C::BF16>(o[w][j], a, pl[w][0], pl[w][1]);
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_acc<C::BF16>(t, a, pl[w][0], pl[w][1]);
+            mma_acc<C::BF16>(t, a, ph[w][0], ph[w][1]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[w][j][k] += t[k];
           }
         };
         const uint8_t* sv = ring_p + (slot + u) * C::STAGE + PA_BLOCK * C::ROW;
@@ -631,9 +655,7 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
         const int64_t row = stream * p.g + head;
         store_out4(p, row * D + d, a, inv);
         if (d == 0) {
-          const float z = sum == 0.f ? -CUDART_INF_F : top - PA_BIAS + log2f(sum);
-          if (p.lse) p.lse[row] = z * 0.6931471805599453f;
-          p.lse2[row] = z;
+          store_stat(p, row, top, sum);
         }
       } else {
         *reinterpret_cast<float4*>(p.part_o + (part * p.g + head) * D + d) = a;

@@ -80,9 +80,10 @@ struct PagedAttnParams {
   // workspace
   float* part_o;                  // [6 G][g][D]: unnormalised sums of split streams
   float* part_ml;                 // [6 G][g][2]: running maximum (log2 domain) and sum
-  float* lse2;                    // [B H g]: log2 of the sum of exp2(scores)
+  float4* stat;                   // [B H g]: reference of the exponents and log2 of the sum over it, in
+                                  // the scaled log2 domain; scale of the kept scores
   int64_t* pre;                   // [B + 1]: load before each sequence (split)
-  float* scores;                  // [B H g][score_stride], log2 domain; only with acc
+  float* scores;                  // [B H g][score_stride], unscaled; only with acc
   int64_t score_stride;
   int sms;                        // of the device
   int G;                          // CTAs that are resident at once in the split kernel
@@ -156,6 +157,13 @@ __device__ __forceinline__ void store_out4(const PagedAttnParams& p, int64_t at,
 // laid out [row_bytes / w][box_rows][w] with w = min(row_bytes, 128), swizzled
 // over w bytes.
 cudaError_t encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int row_bytes, int box_rows);
+
+// Statistics of a finished row (d == 0's thread): the sum of exp2(score - top + PA_BIAS).
+__device__ __forceinline__ void store_stat(const PagedAttnParams& p, int64_t row, float top, float sum) {
+  const float lg = log2f(sum) - PA_BIAS;
+  if (p.lse) p.lse[row] = sum == 0.f ? __int_as_float(0xff800000) : (top + lg) * 0.6931471805599453f;
+  if (p.scores) *reinterpret_cast<float2*>(p.stat + row) = make_float2(top, lg);
+}
 
 // g <= 8 and g <= 16 variants per head dim (one translation unit each)
 cudaError_t launch_paged_attn_64(const PagedAttnParams& p, int cache_type, cudaStream_t st);
