@@ -551,7 +551,8 @@ typedef struct {
 
 /* Bytes of workspace that mkv_paged_decode needs with these arguments on the
  * current device (pointers are not looked at, except whether acc is NULL);
- * 0 for invalid arguments. */
+ * 0 for invalid arguments.  Some megabytes; with acc, 4 more for every query
+ * head and token up to max_len, so give a bound near the lengths. */
 uint64_t mkv_paged_decode_workspace(const mkv_paged_cache* cache, const mkv_paged_decode_args* args);
 
 /* Attention of one new token per sequence over its seq_lens[b] cached tokens
@@ -562,7 +563,7 @@ uint64_t mkv_paged_decode_workspace(const mkv_paged_cache* cache, const mkv_page
  * they hold.  A length below 0 or above max_len counts as 0 or max_len, and a
  * page outside the cache as absent tokens; both are reported in `status`.
  * Results do not depend on timing: no atomics, a fixed order of summation for
- * given lengths and bounds. */
+ * given lengths of all sequences and a given bound. */
 mkv_status mkv_paged_decode(const mkv_paged_cache* cache, const mkv_paged_decode_args* args,
                             mkv_stream_t stream);
 

@@ -759,6 +759,83 @@ def test_streams_and_graphs(M):
         assert torch.equal(got, ref)
 
 
+def test_broadcast_positions_and_empty_calls(M):
+    plan = M.mkv_rope_plan(64)
+    x = rnd((3, 5, 2, 64), BF16, 1)
+    row = torch.arange(5, dtype=torch.int32, device=DEV).view(1, 5) * 7
+    assert torch.equal(M.mkv_rope(plan, x, row.expand(3, 5)), M.mkv_rope(plan, x, row.repeat(3, 1)))
+    for shape in ((0, 5, 2, 64), (3, 0, 2, 64), (3, 5, 0, 64)):
+        assert M.mkv_rope(plan, torch.empty(shape, dtype=F16, device=DEV)).shape == shape
+    cache = Cache(M, F16, [0, 0], 2, 64, 16, seed=1)
+    none = torch.empty((0, 2, 64), dtype=F16, device=DEV)
+    M.mkv_paged_append(cache.c, none, none, torch.empty(0, dtype=torch.int32, device=DEV))
+    # every sequence empty, in both forms of the kernel
+    for cap in (1, 100):
+        c = M.MkvPaged(*cache.pools, torch.full((2, cap), -1, dtype=torch.int32, device=DEV))
+        q = rnd((2, 4, 64), F16, 2)
+        lse = torch.zeros((2, 4), device=DEV)
+        out = M.mkv_paged_decode(c, q, torch.zeros(2, dtype=torch.int32, device=DEV), lse=lse)
+        assert (out == 0).all() and (lse == -math.inf).all() and c.check() == M.MKV_OK
+
+
+def test_8_bit_cache_without_scales(M):
+    """NULL scales stand for 1: the same bits as scales of 1, written and read."""
+    n, one = 40, torch.ones(2, device=DEV)
+    pools = [torch.zeros((4, 2, 16, 128), device=DEV).to(E4M3) for _ in range(4)]
+    table = torch.arange(4, dtype=torch.int32, device=DEV).view(1, 4)
+    a = M.MkvPaged(pools[0], pools[1], table)
+    b = M.MkvPaged(pools[2], pools[3], table, k_scale=one, v_scale=one)
+    k, v, q = rnd((n, 2, 128), F16, 1), rnd((n, 2, 128), F16, 2), rnd((1, 6, 128), F16, 3)
+    i = torch.arange(n, dtype=torch.int32, device=DEV)
+    outs = []
+    for c in (a, b):
+        M.mkv_paged_append(c, k, v, i, seq=torch.zeros_like(i))
+        outs.append(M.mkv_paged_decode(c, q, torch.tensor([n], dtype=torch.int32, device=DEV)))
+    for x, y in ((pools[0], pools[2]), (pools[1], pools[3])):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)) and x.view(torch.uint8).any()
+    assert torch.equal(*outs)
+    assert torch.equal(pools[0].view(torch.uint8)[0, :, :16].transpose(0, 1),
+                       k[:16].to(E4M3).view(torch.uint8))
+
+
+def test_append_queries_in_place(M):
+    cache = Cache(M, F16, [0] * 3, 2, 64, 16, seed=1, room=4)
+    plan = M.mkv_rope_plan(64, interleaved=True)
+    fused = rnd((3, 8, 64), F16, 4)
+    i = torch.arange(3, dtype=torch.int32, device=DEV)
+    k, v = fused[:, 4:6], fused[:, 6:]
+    want = M.mkv_rope(plan, fused[:, :4].unsqueeze(1), i.view(3, 1))[:, 0]
+    rest = fused[:, 4:].clone()
+    q = fused[:, :4]
+    assert M.mkv_paged_append(cache.c, k, v, torch.zeros_like(i), plan=plan, pos=i, q=q, q_out=q) is q
+    assert torch.equal(q, want) and torch.equal(fused[:, 4:], rest)
+
+
+def test_weights_with_default_bound(M):
+    """acc shorter than the page table: it bounds the lengths; a longer sequence is reported."""
+    cache = Cache(M, F16, [100, 37], 2, 64, 16, seed=6, room=500)
+    q = rnd((2, 4, 64), F16, 1)
+    acc = torch.zeros((2, 2, 100), device=DEV)
+    out = M.mkv_paged_decode(cache.c, q, cache.lens, acc=acc)
+    decode_check(cache, q, out, None, acc, torch.zeros_like(acc))
+    cache2 = Cache(M, F16, [100, 37], 2, 64, 16, seed=6, room=500)
+    M.mkv_paged_decode(cache2.c, q, cache2.lens, acc=torch.zeros((2, 2, 99), device=DEV))
+    assert cache2.c.check() == M.MKV_ERR_DEVICE_CHECK
+
+
+def test_calls_on_several_streams_at_once(M):
+    """The same cache read by calls that overlap, each with its own workspace and outputs."""
+    cache = Cache(M, BF16, [3000, 1, 900], 2, 128, 64, seed=12)
+    qs = [rnd((3, 8, 128), BF16, 40 + i) for i in range(4)]
+    want = [M.mkv_paged_decode(cache.c, q, cache.lens) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(5):
+        got = [M.mkv_paged_decode(cache.c, q, cache.lens, stream=st) for q, st in zip(qs, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_binding_checks(M):
     cache = Cache(M, F16, [40], 2, 64, 16, seed=5)
     q = rnd((1, 4, 64), F16, 1)

@@ -541,7 +541,7 @@ def mkv_paged_decode(cache, q, seq_lens, out=None, lse=None, acc=None, max_len=0
     (int32 [batch]) cached tokens.  out: contiguous, of q's type or fp32 (new, of out_dtype,
     where None), returned.  lse: fp32 [batch, q_heads] or None.  acc: fp32 [batch, kv_heads,
     slots] or None; every token's weights are added.  max_len: a bound on seq_lens (0: the page
-    table's capacity).  workspace: a uint8 tensor (None: taken from torch's allocator)."""
+    table's capacity, or acc's slots where those are fewer).  workspace: a uint8 tensor (None: taken from torch's allocator)."""
     if out is None and isinstance(q, _T.Tensor):
         out = _new(q.shape, out_dtype or q.dtype, q.device, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
