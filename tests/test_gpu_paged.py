@@ -281,7 +281,8 @@ def test_decode_one_long_stream(M):
 def test_decode_many_sequences(M):
     """More sequences than the split kernel's prefix sums hold, and the most that they hold."""
     for b in (512, 513, 1025):
-        lens = [(37 * i) % 1500 if i % 97 == 0 else i % 5 for i in range(b)]
+        lens = [(37 * i) % 2600 if i % 97 == 5 else i % 5 for i in range(b)]
+        assert max(lens) > 2048
         cache = Cache(M, E4M3, lens, 1, 64, 256, seed=2, spare=0)
         decode_run(M, cache, 1, 2, 64, F16)
 
@@ -579,6 +580,8 @@ def test_evict_sizes_of_cluster(M):
     evict_case(M, [8191, 4097], 1, 64, 256, 4096, 4, 100, E4M3, seed=1)
     evict_case(M, [8192] * 3, 8, 64, 256, 1000, 0, 999, E4M3, seed=2)
     evict_case(M, [16385] * 3 + [5], 8, 64, 256, 16384, 0, 0, E4M3, seed=3)
+    evict_case(M, [16384] * 2, 8, 64, 256, 5000, 4, 100, E4M3, seed=10)
+    evict_case(M, [40000, 33000, 20], 4, 64, 256, 30001, 4, 100, E4M3, seed=11)
     evict_case(M, [100000, 131072, 98765], 1, 64, 256, 7000, 0, 99, E4M3, seed=8)
     evict_case(M, [400001], 1, 64, 256, 3001, 4, 700, E4M3, seed=4)          # 8 slices of 50176
     evict_case(M, [400001], 1, 64, 256, 300001, 4, 700, E4M3, seed=4)        # most are kept

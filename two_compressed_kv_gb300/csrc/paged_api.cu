@@ -38,7 +38,8 @@ mkv_status sm_count(int* out) {
 }
 
 // Heads a thread takes so that its angles serve several heads while the grid
-// still has at least `want` threads.
+// still has at least `want` threads: a 32K prefill of 8 heads takes 170, 100, 83
+// and 81 us with 1, 2, 4 and 8, one step of 8 x 32 heads 2.4 us with 1, 3.5 with 8.
 int heads_per_thread(int64_t threads, int heads, int64_t want, int most) {
   int per = 1;
   while (per < most && per < heads && threads * up(heads, 2 * per) >= want) per *= 2;
@@ -79,17 +80,23 @@ const char* check_cache(const mkv_paged_cache* c) {
 
 // With at most this many tokens a sequence, or more sequences than the split
 // kernel's prefix sums hold, one CTA takes a whole stream and no join follows.
-constexpr int64_t kWholeTokens = 1024;
+// Us of whole and split streams of n fp16 tokens, group 4, D = 128, in a graph:
+//   8 streams    512: 6.8, 9.7    1024: 9.8, 9.9    2048: 16, 10.9
+//   64 streams   1024: 11.2, 17.1   2048: 18.0, 22.8   4096: 30.4, 33.1
+//   256 streams  1024: 24.6, 36.7   2048: 44.0, 56.0   4096: 84.8, 90.1
+// The longest stream's time is the whole call's where streams are whole, so the
+// bound is kept below where equal lengths would still gain.
+constexpr int64_t whole_tokens(int64_t streams) { return streams >= 64 ? 2048 : 1024; }
 // Smallest share of a CTA of the split kernel: 8 blocks of 16 tokens.
 constexpr int kMinBlocks = 8;
 
 // What a part of a stream costs a CTA apart from its blocks (its queries, the
-// first copies' latency, the join of the warps), in blocks.  On 256 ragged
-// streams 86.5 us with 32, 88 with 8; on equal long streams no difference.
+// first copies' latency, the join of the warps), in blocks.  256 ragged e4m3
+// streams: 80.2 us with 32, 81.2 with 8; equal long streams: no difference.
 constexpr int kPieceLoad = 32;
 // Sixteenths of the load handed out in small shares, from so many blocks a CTA
-// on: 128K batch 8 takes 720 us with none, 683 with 3, 686 with 4; 32K batch 4
-// 97, 94 and 92 us.
+// on.  With 0, 2 and 4: the ragged batch 86, 82 and 80 us, 32K batch 4 94, 97 and
+// 91 us; 128K batch 8 720 us with none, 683 to 691 with 3 or 4.
 constexpr int kTail16 = 4;
 constexpr int kTailFrom = 64;
 
@@ -128,7 +135,7 @@ DecodeLayout decode_layout(const mkv_paged_cache* c, const mkv_paged_decode_args
   const int64_t g = a->n_q_heads / c->n_kv_heads;
   const int64_t streams = (int64_t)c->batch * c->n_kv_heads;
   l.limit = decode_limit(c, a);
-  l.split = l.limit > kWholeTokens && c->batch <= PA_MAX_B;
+  l.split = l.limit > whole_tokens(streams) && c->batch <= PA_MAX_B;
   const int ctas = paged_ctas(c->head_dim * elem_bytes(c->dtype));
   l.G = (int)std::min<int64_t>((int64_t)sms * ctas,
                                streams * up(up(l.limit, PA_BLOCK), kMinBlocks));
@@ -159,13 +166,15 @@ uint64_t evict_list_bytes(const mkv_paged_cache* c, const mkv_paged_evict_args* 
   return ((uint64_t)c->batch * c->n_kv_heads * 2 * a->budget * 4 + 255) & ~(uint64_t)255;
 }
 
-// CTAs of a stream: doubled while all fit the SMs at once and a CTA keeps 4096
-// slots or more (a cluster's barriers cost more than shorter passes save: one
-// CTA takes 21 us for 64 streams of 4097 tokens, two 26).
+// CTAs of a stream, one cluster: doubled while all clusters run at once (8 CTAs:
+// up to 8 streams; 16 clusters of 8 take two turns) and a CTA keeps 8192 slots.
+// Us with 1, 2, 4 and 8 CTAs, fp16 rows of 128: 64 streams of 4096 cut to 2048:
+// 22.6, 25.3, 35.8, 82.8; 16 of 16384: 22.4, 20.5, 21.1, 38.3; 32 of 32768: 31.1,
+// 31.3, 30.2, 59.1; 8 of 131072: 42.0, 35.9, 31.5, 28.7.
 int evict_ranks(const mkv_paged_cache* c, int64_t limit, int sms) {
   const int64_t streams = (int64_t)c->batch * c->n_kv_heads;
   int R = 1;
-  while (R < 8 && streams * 2 * R <= sms && limit >= 8192 * (int64_t)R) R *= 2;
+  while (R < 8 && streams * 2 * R <= sms && (R < 4 || streams <= 8) && limit >= 16384 * (int64_t)R) R *= 2;
   return R;
 }
 
