@@ -240,7 +240,8 @@ def decode_run(M, cache, heads, group, dim, qt, out_dtype=None, weights=True, se
     b = len(cache.lens_list)
     q = rnd((b, heads * group, dim), qt, seed, size)
     lse = torch.full((b, heads * group), 5.0, device=DEV)
-    acc = rnd((b, heads, max(cache.lens_list + [1]) + 3), F32, seed + 1).abs() if weights else None
+    slots = max(cache.lens_list + [1, kw.get("max_len", 0)]) + 3
+    acc = rnd((b, heads, slots), F32, seed + 1).abs() if weights else None
     acc0 = None if acc is None else acc.clone()
     if acc is not None:
         kw.setdefault("max_len", max(cache.lens_list + [1]))
@@ -256,7 +257,7 @@ LENS = [0, 1, 2, 15, 16, 17, 47, 64, 65, 300]
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("group", [1, 7, 16])
 def test_decode_whole_streams(M, dtype, qt, dim, group):
-    """One CTA per stream: short sequences, an empty one, pages that end inside the work of a step."""
+    """Short streams in clusters of one or two CTAs: short sequences, an empty one, pages that end inside the work of a step."""
     for page in (16, 48):
         cache = Cache(M, dtype, LENS, 2, dim, page, seed=group)
         decode_run(M, cache, 2, group, dim, qt, out_dtype=F32 if group == 7 else None)
@@ -264,11 +265,20 @@ def test_decode_whole_streams(M, dtype, qt, dim, group):
 
 @pytest.mark.parametrize("dtype,qt", [(F16, F16), (BF16, BF16), (E4M3, BF16)])
 @pytest.mark.parametrize("dim,group,page", [(64, 4, 16), (128, 4, 64), (128, 9, 48), (256, 8, 256), (256, 12, 32)])
-def test_decode_split_streams(M, dtype, qt, dim, group, page):
-    """Streams cut at any block and joined: long and short ones, empty ones at both ends."""
-    cache = Cache(M, dtype, [0, 2500, 1, 0, 1100, 33, 4097, 0], 2, dim, page, seed=dim)
-    decode_run(M, cache, 2, group, dim, qt, out_dtype=F32)
-    decode_run(M, cache, 2, group, dim, qt, weights=False, seed=9)
+@pytest.mark.parametrize("bound", [4097, 9000])
+def test_decode_long_streams(M, dtype, qt, dim, group, page, bound):
+    """Streams cut and joined: long and short ones, empty ones at both ends.  With a bound of 4097
+    on 16 streams a cluster takes a stream, with 9000 the load is split over all streams."""
+    cache = Cache(M, dtype, [0, 2500, 1, 0, 1100, 33, 4097, 0], 2, dim, page, seed=dim, room=bound - 4097)
+    decode_run(M, cache, 2, group, dim, qt, out_dtype=F32, max_len=bound)
+    decode_run(M, cache, 2, group, dim, qt, weights=False, seed=9, max_len=bound)
+
+
+@pytest.mark.parametrize("heads,ctas", [(1, 8), (3, 4), (6, 2), (9, 1)])
+def test_decode_sizes_of_cluster(M, heads, ctas):
+    """8, 4, 2 and 1 CTAs a stream, with lengths that leave some of them without a token."""
+    cache = Cache(M, F16, [1030, 1, 17, 0, 300, 129, 16, 500], heads, 64, 48, seed=heads)
+    decode_run(M, cache, heads, 3, 64, F16, out_dtype=F32)
 
 
 def test_decode_one_long_stream(M):

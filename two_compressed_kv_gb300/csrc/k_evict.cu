@@ -13,7 +13,10 @@
 //
 // What bounds it: select reads 8 bytes a token once from DRAM and is then
 // bound by the latency of its few cluster-wide steps; move by DRAM, 4 rows of
-// traffic per moved token.
+// traffic per moved token.  Measured, both together: 64 streams of 4097 to 4096
+// 9.4 us; 32 streams of 32768 to 2048 (fp16 rows of 128) 30.6 us, of which 9 are
+// select's 18 thousand cycles; 8 streams of 1048576 to 8192 62.5 us, the pass over
+// 67 MB by 64 SMs 15 us of them.
 #include <cooperative_groups.h>
 
 #include "decode_common.cuh"
@@ -235,7 +238,8 @@ __device__ __forceinline__ void fill_holes(const Slice& s, int all_movers, int r
 //
 // In the steady state few tokens leave (one a step): up to E_FEW of them are
 // found one by one as the smallest (key, highest slot) instead, without any
-// histogram, and every thread then knows them all.
+// histogram, and every thread then knows them all (64 streams of 4097: 15 us a
+// cold call, 21 through the histograms).
 // grid: streams * R, cluster R; block 1024
 // ---------------------------------------------------------------------------
 constexpr int E_FEW = 4;

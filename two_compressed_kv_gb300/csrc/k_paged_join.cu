@@ -16,7 +16,9 @@ constexpr int JT = 256;
 // of one stream, in a fixed order.  The parts lie in L2; a CTA takes one query
 // head, its threads 4 elements each of every (4 T / D)-th part.  T = 1024 threads
 // where the heads are so few that all such CTAs run at once: a part from every
-// CTA of the split kernel is then still a few loads per thread.
+// CTA of the split kernel is then still a few loads per thread (one stream of a
+// million tokens, 8 heads: 135 us for the whole call with 256 threads, 102 with
+// 1024).  Bound by three dependent latencies of L2: lengths, shares, parts.
 // grid: streams * g
 // ---------------------------------------------------------------------------
 template <int D, int T>
@@ -88,7 +90,8 @@ __global__ void __launch_bounds__(T) paged_join_kernel(const __grid_constant__ P
 // ---------------------------------------------------------------------------
 // weights: acc[t] += sum over the group of exp2(score - reference) / sum.  One owner per
 // token: no atomics.  Memory-bound: 4 g bytes read and 8 read and written per
-// token against 4 D for its fp16 rows.
+// token against 4 D for its fp16 rows (128K batch 8, group 4: 268 MB beside the
+// 4.3 GB of keys and values).
 // grid: streams * chunks of WT tokens
 // ---------------------------------------------------------------------------
 constexpr int WT = 1024;

@@ -179,7 +179,9 @@ __device__ __forceinline__ void turn_heads(int h0, int h1, bool turns, const flo
 
 // ---------------------------------------------------------------------------
 // 16-byte form: a thread takes one unit of one token for `heads_per` heads.
-// 4 x 32768 tokens of 8 bf16 heads of 128: 83 us, 6.45 TB/s, 96 % of a copy.
+// 4 x 32768 tokens of 8 bf16 heads of 128: 81 us, 6.65 TB/s, 99 % of a copy; fp32,
+// 64 of 96 interleaved, 28 heads: 28.5 us, 6.2 TB/s; one step of 8 x 32 heads: 2.1
+// us in a graph, a launch.
 // grid: (ceil(tokens * units / 256), ceil(heads / heads_per), batch)
 // ---------------------------------------------------------------------------
 template <typename T, bool HALF>
@@ -260,7 +262,8 @@ cudaError_t launch_rope_t(const RopeParams& p, bool vec, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // append: rows of new tokens into their pages.  The heads of a token are one
 // list: keys, values, queries; a thread takes one unit of one token for
-// `heads_per` entries of the list.
+// `heads_per` entries of the list.  32182 tokens of 8 KV and 32 query heads of
+// 128, bf16 into e4m3: 123 us, 5.9 TB/s; a step of 8 tokens: 2.9 us in a graph.
 // grid: (ceil(n * units / 256), ceil(heads_total / heads_per))
 // ---------------------------------------------------------------------------
 // Eight elements from e on of a cache row; E4M3: times `inv`, saturated.

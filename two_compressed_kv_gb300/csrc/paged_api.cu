@@ -78,15 +78,28 @@ const char* check_cache(const mkv_paged_cache* c) {
 
 // ---- decode ------------------------------------------------------------------
 
-// With at most this many tokens a sequence, or more sequences than the split
-// kernel's prefix sums hold, one CTA takes a whole stream and no join follows.
-// Us of whole and split streams of n fp16 tokens, group 4, D = 128, in a graph:
-//   8 streams    512: 6.8, 9.7    1024: 9.8, 9.9    2048: 16, 10.9
-//   64 streams   1024: 11.2, 17.1   2048: 18.0, 22.8   4096: 30.4, 33.1
-//   256 streams  1024: 24.6, 36.7   2048: 44.0, 56.0   4096: 84.8, 90.1
-// The longest stream's time is the whole call's where streams are whole, so the
-// bound is kept below where equal lengths would still gain.
-constexpr int64_t whole_tokens(int64_t streams) { return streams >= 64 ? 2048 : 1024; }
+// Up to this many tokens a CTA, a cluster of CTAs takes each stream and joins its
+// parts over distributed shared memory; beyond, or with more sequences than fit
+// the split kernel's prefix sums, the load is split over all streams and a second
+// kernel joins.  Us of clusters and of the split, group 4, D = 128, equal lengths:
+//   8 streams    1024: 6.4, 9.9    4096: 8.8, 11.8   16384: 19.2, 20.8
+//   32 streams   1024: 7.2, 11.3   4096: 15.9, 20.2   8192: 26.1, 30.4
+//   64 streams   1024: 9.8, 17.1   4096: 25.9, 33.5
+//   256 streams  1024: 24.6, 36.7  2048: 44.0, 56.0
+// Lengths are not known to the host, and one long sequence among short ones takes
+// as long as its own CTAs: 64 x 4 streams, one of 16384 tokens: 52 us in clusters
+// of 4, 20 split; spread up to 16384: 96 and 80 us.  So the bound is low.
+constexpr int64_t kClusterTokens = 2048;
+
+// CTAs of a stream: as many as run at once for all streams (clusters of 8: 16 of
+// them do not: 16 streams of 4096 take 17.2 us with 8, 12.5 with 4), each with 64
+// tokens or more of the bound (8 streams of 304: 6.3 us with 1, 5.9 with 2, 5.6 with 4).
+int stream_cluster(int64_t streams, int64_t limit) {
+  int n = streams <= 8 ? 8 : streams <= 32 ? 4 : streams <= 64 ? 2 : 1;
+  while (n > 1 && limit < 64 * n) n /= 2;
+  return n;
+}
+
 // Smallest share of a CTA of the split kernel: 8 blocks of 16 tokens.
 constexpr int kMinBlocks = 8;
 
@@ -102,7 +115,7 @@ constexpr int kTailFrom = 64;
 
 struct DecodeLayout {
   bool split;
-  int G;
+  int cluster, G;
   int64_t limit;
   int64_t score_stride;
   uint64_t part_o, part_ml, stat, pre, scores, total;   // byte offsets
@@ -135,7 +148,9 @@ DecodeLayout decode_layout(const mkv_paged_cache* c, const mkv_paged_decode_args
   const int64_t g = a->n_q_heads / c->n_kv_heads;
   const int64_t streams = (int64_t)c->batch * c->n_kv_heads;
   l.limit = decode_limit(c, a);
-  l.split = l.limit > whole_tokens(streams) && c->batch <= PA_MAX_B;
+  l.cluster = stream_cluster(streams, l.limit);
+  l.split = l.limit > kClusterTokens * l.cluster && c->batch <= PA_MAX_B;
+  if (l.split) l.cluster = 1;
   const int ctas = paged_ctas(c->head_dim * elem_bytes(c->dtype));
   l.G = (int)std::min<int64_t>((int64_t)sms * ctas,
                                streams * up(up(l.limit, PA_BLOCK), kMinBlocks));
@@ -468,6 +483,7 @@ mkv_status mkv_paged_decode(const mkv_paged_cache* c, const mkv_paged_decode_arg
   p.G = l.G;
   p.min_blocks = kMinBlocks;
   p.split = l.split;
+  p.cluster = l.cluster;
   p.piece_load = kPieceLoad;
   p.tail16 = kTail16;
   p.tail_from = kTailFrom;

@@ -28,8 +28,14 @@
 //     high and a low part.  Probabilities carry a factor 2^12, which cancels, so
 //     that small ones stay normal in fp16 and the reference of the exponents need
 //     not follow every new maximum: up to 2^3 above it still fits.
+//
+// Measured: 32768 tokens, batch 4, 8 KV heads, fp16: 85 us in the kernel, 6.3 TB/s,
+// 94 % of a copy's rate, 89 us with the join; 131072, batch 8, bf16, with weights:
+// 691 us, 6.3 TB/s; a ragged batch of 256 e4m3 streams: 80 us, 4.5 TB/s, where
+// 64 conversions and 24 products per 4 KB and the starts of parts count.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <math_constants.h>
 
 #include "decode_common.cuh"
@@ -123,8 +129,9 @@ struct PA {
   static_assert(STAGES % U == 0, "a step's slots do not wrap");
   static constexpr int HR = 8 * NH;                        // head rows
   static constexpr int MERGE = NW * HR * (D + 4) * 4;
+  static constexpr int OWN = HR * D * 4;                   // cluster: this CTA's sums, behind the merge area
   static constexpr int RING = NW * STAGES * STAGE;
-  static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + 1024;   // and its alignment
+  static constexpr int SMEM = (RING > MERGE + OWN ? RING : MERGE + OWN) + 1024;   // and its alignment
   static constexpr int CTAS = NW == 8 ? 1 : paged_ctas(ROW);   // per SM
   static_assert(CTAS * (SMEM + 9 * 1024) <= 228 * 1024, "resident CTAs' shared memory");
 };
@@ -145,7 +152,7 @@ __device__ __forceinline__ uint32_t piece_on(uint32_t at, int by) {
 }
 
 // ---------------------------------------------------------------------------
-// grid: split ? 3 G : streams; block: NW warps; dynamic smem PA::SMEM
+// grid: split ? 3 G : streams * cluster; cluster (cluster, 1, 1); block: NW warps; dynamic smem PA::SMEM
 // ---------------------------------------------------------------------------
 template <int CT, int D, bool WIDE, int NW>
 __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
@@ -159,6 +166,7 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
   __shared__ int len_of[PA_MAX_B];             // and its length
   __shared__ float sm_m[NW][C::HR], sm_l[NW][C::HR];
   __shared__ int64_t warp_sum[NW];
+  __shared__ float2 own_ml[C::HR];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;       // fragment row and column pair
   constexpr int NH = C::NH;
@@ -252,13 +260,14 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
       j1 = v1 - p.piece_load;
       if (j1 <= j0) continue;
     } else {
-      b = blockIdx.x / p.H;
-      h = blockIdx.x - b * p.H;
+      const int s = blockIdx.x / p.cluster, rank = blockIdx.x - s * p.cluster;
+      b = s / p.H;
+      h = s - b * p.H;
       n = paged_len(p, b);
       nb = (n + PA_BLOCK - 1) / PA_BLOCK;
-      j0 = 0;
-      j1 = nb;
-      if (h == 0 && tid == 0 && p.status && p.lens[b] != n) atomicOr(p.status, DEV_ERR_CHECK);
+      j0 = (int)((int64_t)nb * rank / p.cluster);
+      j1 = (int)((int64_t)nb * (rank + 1) / p.cluster);
+      if (rank == 0 && h == 0 && tid == 0 && p.status && p.lens[b] != n) atomicOr(p.status, DEV_ERR_CHECK);
     }
     if (p.split && h == 0 && j0 == 0 && tid == 0 && p.status && p.lens[b] != n)
       atomicOr(p.status, DEV_ERR_CHECK);
@@ -632,7 +641,8 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
         }
       }
     __syncthreads();
-    const bool whole = j0 == 0 && j1 == nb;
+    const bool whole = j0 == 0 && j1 == nb && p.cluster == 1;
+    float* own = reinterpret_cast<float*>(smem + C::MERGE);
     const float vs = CT == MKV_DT_E4M3 && p.vs ? p.vs[h] : 1.f;
     const int64_t part = 2 * (int64_t)blockIdx.x + (j0 == 0 ? 1 : 0);
     for (int e = tid; e < p.g * (D / 4); e += NW * 32) {
@@ -657,6 +667,9 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
         if (d == 0) {
           store_stat(p, row, top, sum);
         }
+      } else if (!p.split) {
+        *reinterpret_cast<float4*>(own + head * D + d) = a;
+        if (d == 0) own_ml[head] = make_float2(top, sum);
       } else {
         *reinterpret_cast<float4*>(p.part_o + (part * p.g + head) * D + d) = a;
         if (d == 0) {
@@ -665,7 +678,43 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
         }
       }
     }
-    if (!p.split) break;
+    if (!p.split) {
+      if (p.cluster > 1) {
+        // the ranks' sums, joined over distributed shared memory: each rank an even
+        // share of the elements
+        namespace cg = cooperative_groups;
+        cg::cluster_group cl = cg::this_cluster();
+        cl.sync();
+        for (int e = (int)cl.block_rank() * NW * 32 + tid; e < p.g * (D / 4); e += p.cluster * NW * 32) {
+          const int head = e / (D / 4), d = (e - head * (D / 4)) * 4;
+          float2 ml[8];
+          float4 v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (q < p.cluster) {
+              ml[q] = *cl.map_shared_rank(&own_ml[head], q);
+              v[q] = *reinterpret_cast<const float4*>(cl.map_shared_rank(own + head * D + d, q));
+            }
+          float top = -CUDART_INF_F, sum = 0.f;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (q < p.cluster) top = fmaxf(top, ml[q].x);
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (q < p.cluster) {
+              const float f = ml[q].x == top ? 1.f : exp2f(ml[q].x - top);
+              sum += ml[q].y * f;
+              a.x += v[q].x * f, a.y += v[q].y * f, a.z += v[q].z * f, a.w += v[q].w * f;
+            }
+          const int64_t row = stream * p.g + head;
+          store_out4(p, row * D + d, a, sum == 0.f ? 0.f : 1.f / sum);
+          if (d == 0) store_stat(p, row, top, sum);
+        }
+        cl.sync();                    // no rank's sums are read any more
+      }
+      break;
+    }
     if (at < g1) {                  // the merge area becomes the ring again
       fence_proxy_async();
       __syncthreads();
@@ -682,17 +731,19 @@ cudaError_t launch_pa_nw(const PagedAttnParams& p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<CT, D, WIDE, NW>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const int64_t grid = p.split ? PA_SHARES * p.G : (int64_t)p.B * p.H;
-  return launch_kernel(paged_attn_kernel<CT, D, WIDE, NW>, dim3((unsigned)grid), dim3(NW * 32), C::SMEM, st, true, 0,
+  const int64_t grid = p.split ? PA_SHARES * p.G : (int64_t)p.B * p.H * p.cluster;
+  return launch_kernel(paged_attn_kernel<CT, D, WIDE, NW>, dim3((unsigned)grid), dim3(NW * 32), C::SMEM, st, true, p.cluster,
                        p, kmap, vmap);
 }
 
-// 4 warps a CTA and several CTAs an SM; where an SM gets one CTA at most, 8 warps
-// (rows of 512 bytes, whose rings do not fit, apart).
+// 4 warps a CTA and several CTAs an SM; where all CTAs run at once with one an SM
+// (of 152 SMs clusters of 8 reach about half), 8 warps.  Rows of 512 bytes, whose
+// rings do not fit, apart.
 template <int CT, int D, bool WIDE>
 cudaError_t launch_pa(const PagedAttnParams& p, cudaStream_t st) {
   if constexpr (PA<CT, D, WIDE, 4>::ROW < 512)
-    if ((p.split ? p.G : (int64_t)p.B * p.H) <= p.sms) return launch_pa_nw<CT, D, WIDE, 8>(p, st);
+    if ((p.split ? p.G : (int64_t)p.B * p.H * p.cluster) <= (p.cluster == 8 ? p.sms / 2 : p.sms))
+      return launch_pa_nw<CT, D, WIDE, 8>(p, st);
   return launch_pa_nw<CT, D, WIDE, 4>(p, st);
 }
 

@@ -91,7 +91,8 @@ struct PagedAttnParams {
   int piece_load;                 // what a part of a stream costs apart from its blocks, in blocks
   int tail16;                     // sixteenths of the load that are handed out in small shares
   int tail_from;                  // from this many blocks a CTA on
-  int split;                      // 0: one CTA per stream
+  int split;                      // 0: a cluster of CTAs per stream
+  int cluster;                    // its size, 1 to 8 (split: 1)
 };
 
 // Cached tokens of sequence b as the kernels count them.
