@@ -622,6 +622,17 @@ def test_evict_protected_beyond_budget(M):
     evict_case(M, [200], 2, 64, 16, 32, 4, 10, pos=pos, seed=3)
 
 
+def test_evict_budget_above_the_bound(M):
+    """Nothing leaves; src says so for every slot, and the scratch does not grow with the budget."""
+    evict_case(M, [200, 0, 63], 2, 64, 16, 1000, 4, 10, seed=3, in_place=True)
+    cache = Cache(M, F16, [30], 1, 64, 16, seed=3)
+    acc, pos = torch.rand((1, 1, 32), device=DEV), torch.arange(32, dtype=torch.int32, device=DEV).view(1, 1, 32)
+    n = torch.tensor([30], dtype=torch.int32, device=DEV)
+    ws = torch.empty(512, dtype=torch.uint8, device=DEV)
+    src = M.mkv_paged_evict(cache.c, acc, pos, n, n, 5_000_000, workspace=ws)
+    assert src[0, 0, :30].tolist() == list(range(30)) and (src[0, 0, 30:] == -1).all() and n.item() == 30
+
+
 def test_evict_bad_pages_are_skipped(M):
     cache = Cache(M, F16, [64], 1, 64, 16, seed=2)
     acc = torch.arange(64, device=DEV, dtype=torch.float32).view(1, 1, 64)      # the last 32 are kept

@@ -98,7 +98,7 @@ __device__ __forceinline__ bool slice_of(const EvictParams& p, int rank, Slice& 
   }
   s.acc = p.acc + stream * p.meta_stride;
   s.pos = p.pos + stream * p.meta_stride;
-  s.movers = p.lists + stream * 2 * s.m;
+  s.movers = p.lists + stream * 2 * s.m;         // s.m < s.n <= p.limit here
   s.holes = s.movers + s.m;
   s.sink = p.sink;
   s.from = (int64_t)p.next_pos[b] - p.recent;

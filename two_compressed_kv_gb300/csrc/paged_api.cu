@@ -176,9 +176,11 @@ int64_t evict_limit(const mkv_paged_cache* c, const mkv_paged_evict_args* a) {
   return a->max_len ? a->max_len : (int64_t)c->max_pages * c->page_size;
 }
 
-// Bytes of the lists of movers and freed slots.
+// Bytes of the lists of movers and freed slots.  A budget above the bound evicts
+// nothing and needs none.
 uint64_t evict_list_bytes(const mkv_paged_cache* c, const mkv_paged_evict_args* a) {
-  return ((uint64_t)c->batch * c->n_kv_heads * 2 * a->budget * 4 + 255) & ~(uint64_t)255;
+  const int64_t m = std::min<int64_t>(a->budget, evict_limit(c, a));
+  return ((uint64_t)c->batch * c->n_kv_heads * 2 * m * 4 + 255) & ~(uint64_t)255;
 }
 
 // CTAs of a stream, one cluster: doubled while all clusters run at once (8 CTAs:

@@ -191,7 +191,7 @@ struct EvictParams {
   int32_t *lens_out, *src;
   int64_t meta_stride, out_stride;
   int budget, sink, recent;
-  int32_t* lists;                 // workspace: [B H][2][budget] movers, then holes
+  int32_t* lists;                 // workspace: [B H][2][budget] movers, then holes (budget < limit)
   uint2* listed;                  // workspace: [B H][list_slots] (key, slot), long slices only
   int64_t list_slots;
   int R;                          // CTAs (one cluster) per stream
