@@ -86,7 +86,7 @@ struct PagedAttnParams {
   float* scores;                  // [B H g][score_stride], unscaled; only with acc
   int64_t score_stride;
   int sms;                        // of the device
-  int G;                          // CTAs that are resident at once in the split kernel
+  int G;                          // large shares of the split kernel; 2 G small ones follow
   int min_blocks;                 // smallest share of a CTA, in blocks
   int piece_load;                 // what a part of a stream costs apart from its blocks, in blocks
   int tail16;                     // sixteenths of the load that are handed out in small shares
