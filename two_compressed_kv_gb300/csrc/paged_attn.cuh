@@ -411,13 +411,16 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
           phases ^= 1u << (slot + u);
           pending &= ~(1u << (slot + u));
         }
-        // Two chains of accumulation, for their latency and because a chain cuts each
-        // sum off towards zero.
-        float s1[NH][4];
+        // Chains of accumulation, for their latency and because a chain cuts each sum
+        // off towards zero.
+        constexpr int CH = WIDE ? 2 : 4;
+        float part[CH][NH][4];
 #pragma unroll
-        for (int w = 0; w < NH; ++w)
+        for (int x = 0; x < CH; ++x)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[u][w][k] = s1[w][k] = 0.f;
+          for (int w = 0; w < NH; ++w)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) part[x][w][k] = 0.f;
         const uint8_t* sk = ring_p + (slot + u) * C::STAGE;
         if constexpr (E4) {
 #pragma unroll
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
               e4m3x4_to_f16(w0[k], a[0], a[2]);
               e4m3x4_to_f16(w1[k], a[1], a[3]);
 #pragma unroll
-              for (int w = 0; w < NH; ++w) mma_acc<false>(k & 1 ? s1[w] : s[u][w], a, qb[w][4 * x + k][0], qb[w][4 * x + k][1]);
+              for (int w = 0; w < NH; ++w) mma_acc<false>(part[k % CH][w], a, qb[w][4 * x + k][0], qb[w][4 * x + k][1]);
             }
           }
         } else {
@@ -441,13 +444,16 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
             uint32_t a[4];
             ldsm4<false>(sa + piece_on(k_at, 2 * ks), a);
 #pragma unroll
-            for (int w = 0; w < NH; ++w) mma_acc<C::BF16>(ks & 1 ? s1[w] : s[u][w], a, qb[w][ks][0], qb[w][ks][1]);
+            for (int w = 0; w < NH; ++w) mma_acc<C::BF16>(part[ks % CH][w], a, qb[w][ks][0], qb[w][ks][1]);
           }
         }
 #pragma unroll
         for (int w = 0; w < NH; ++w)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[u][w][k] += s1[w][k];
+          for (int k = 0; k < 4; ++k) {
+            s[u][w][k] = part[0][w][k] + part[1][w][k];
+            if constexpr (CH == 4) s[u][w][k] += part[2][w][k] + part[3][w][k];
+          }
         if (left[u] < PA_BLOCK) {
 #pragma unroll
           for (int w = 0; w < NH; ++w)
