@@ -74,14 +74,20 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Two probabilities as 16-bit pairs: rounded, and what the rounding left.
+// Two probabilities as 16-bit pairs: rounded, what the rounding left, rounded,
+// and (bf16) what that left.
 template <bool BF16>
-__device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo, uint32_t& rest) {
   if constexpr (BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    const __nv_bfloat162 l = __floats2bfloat162_rn(a - __low2float(h), b - __high2float(h));
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = *reinterpret_cast<const uint32_t*>(&l);
+    auto part = [&](float& x, float& y) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+      x -= __low2float(h);
+      y -= __high2float(h);
+      return *reinterpret_cast<const uint32_t*>(&h);
+    };
+    hi = part(a, b);
+    lo = part(a, b);
+    rest = part(a, b);
   } else {
     const __half2 h = __floats2half2_rn(a, b);
     const float2 f = __half22float2(h);
@@ -154,7 +160,7 @@ __device__ __forceinline__ uint32_t piece_on(uint32_t at, int by) {
 // ---------------------------------------------------------------------------
 // grid: split ? 3 G : streams * cluster; cluster (cluster, 1, 1); block: NW warps; dynamic smem PA::SMEM
 // ---------------------------------------------------------------------------
-template <int CT, int D, bool WIDE, int NW>
+template <int CT, int D, bool WIDE, int NW, bool THIRD>
 __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
     paged_attn_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
@@ -514,7 +520,10 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
       }
 #pragma unroll
       for (int u = 0; u < C::U; ++u) {
-        uint32_t ph[NH][2], pl[NH][2];         // P^T: tokens 0..7 and 8..15, high and low parts
+        // P^T: tokens 0..7 and 8..15, high and low parts; two bf16 parts leave 2^-18,
+        // which an fp32 output would show, so there a third follows (a variant of its
+        // own: a test in the loop costs 1 % at 128K)
+        uint32_t ph[NH][2], pl[NH][2], pr[NH][2];
 #pragma unroll
         for (int w = 0; w < NH; ++w)
 #pragma unroll
@@ -523,9 +532,10 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
             const float y = exp2_fast(fmaf(s[u][w][2 * t + 1], sc[w][1], mref[w][1]));
             l[w][0] += x;
             l[w][1] += y;
-            split_pair<C::BF16>(x, y, ph[w][t], pl[w][t]);
+            split_pair<C::BF16>(x, y, ph[w][t], pl[w][t], pr[w][t]);
             ph[w][t] = transpose8(ph[w][t]);
             pl[w][t] = transpose8(pl[w][t]);
+            if constexpr (THIRD) pr[w][t] = transpose8(pr[w][t]);
           }
         // The products cut their sums off towards zero, which over many blocks adds
         // up (2e-5 after 400): a block's are summed by themselves and added to O
@@ -534,6 +544,7 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
 #pragma unroll
           for (int w = 0; w < NH; ++w) {
             float t[4] = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (THIRD) mma_acc<C::BF16>(t, a, pr[w][0], pr[w][1]);
             mma_acc<C::BF16>(t, a, pl[w][0], pl[w][1]);
             mma_acc<C::BF16>(t, a, ph[w][0], ph[w][1]);
 #pragma unroll
@@ -728,18 +739,25 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
   }
 }
 
-template <int CT, int D, bool WIDE, int NW>
-cudaError_t launch_pa_nw(const PagedAttnParams& p, cudaStream_t st) {
+template <int CT, int D, bool WIDE, int NW, bool THIRD>
+cudaError_t launch_pa_third(const PagedAttnParams& p, cudaStream_t st) {
   using C = PA<CT, D, WIDE, NW>;
   CUtensorMap kmap, vmap;
   if (cudaError_t e = encode_rows_map(&kmap, p.kp, p.rows, C::ROW, PA_BLOCK)) return e;
   if (cudaError_t e = encode_rows_map(&vmap, p.vp, p.rows, C::ROW, PA_BLOCK)) return e;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<CT, D, WIDE, NW>,
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<CT, D, WIDE, NW, THIRD>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t grid = p.split ? PA_SHARES * p.G : (int64_t)p.B * p.H * p.cluster;
-  return launch_kernel(paged_attn_kernel<CT, D, WIDE, NW>, dim3((unsigned)grid), dim3(NW * 32), C::SMEM, st, true, p.cluster,
+  return launch_kernel(paged_attn_kernel<CT, D, WIDE, NW, THIRD>, dim3((unsigned)grid), dim3(NW * 32), C::SMEM, st, true, p.cluster,
                        p, kmap, vmap);
+}
+
+template <int CT, int D, bool WIDE, int NW>
+cudaError_t launch_pa_nw(const PagedAttnParams& p, cudaStream_t st) {
+  if constexpr (CT == MKV_DT_BF16)
+    if (p.out_type == MKV_DT_F32) return launch_pa_third<CT, D, WIDE, NW, true>(p, st);
+  return launch_pa_third<CT, D, WIDE, NW, false>(p, st);
 }
 
 // 4 warps a CTA and several CTAs an SM; where all CTAs run at once with one an SM
