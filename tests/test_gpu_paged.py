@@ -783,6 +783,61 @@ def test_streams_and_graphs(M):
         assert torch.equal(got, ref)
 
 
+@pytest.mark.parametrize("bound", [600, 9000])
+def test_graph_replays_with_other_lengths(M, bound):
+    """A captured step (append, decode with weights, eviction) replayed after lengths, slots and
+    queries changed gives what the eager calls give; in clusters and split over the streams."""
+    lens = [500, 129, 128]
+    caches = [Cache(M, F16, lens, 6, 64, 64, seed=5, room=bound - 500) for _ in range(2)]
+    for a, b in zip(caches[0].pools, caches[1].pools):
+        b.copy_(a)
+    plan = M.mkv_rope_plan(64)
+    state = []
+    for _ in caches:
+        state.append(dict(k=torch.zeros((3, 6, 64), dtype=F16, device=DEV), q=torch.zeros((3, 12, 64), dtype=F16, device=DEV),
+                          slot=torch.zeros(3, dtype=torch.int32, device=DEV), lens=torch.zeros(3, dtype=torch.int32, device=DEV),
+                          acc=torch.zeros((3, 6, bound), device=DEV), pos=torch.zeros((3, 6, bound), dtype=torch.int32, device=DEV),
+                          lens_out=torch.zeros(3, dtype=torch.int32, device=DEV),
+                          acc_out=torch.zeros((3, 6, 128), device=DEV), pos_out=torch.zeros((3, 6, 128), dtype=torch.int32, device=DEV),
+                          src=torch.zeros((3, 6, 128), dtype=torch.int32, device=DEV), out=torch.zeros((3, 12, 64), dtype=F16, device=DEV)))
+
+    def step(c, s):
+        q = M.mkv_paged_append(c.c, s["k"], s["k"], s["slot"], plan=plan, q=s["q"], acc=s["acc"], pos_meta=s["pos"])
+        M.mkv_paged_decode(c.c, q, s["lens"], out=s["out"], acc=s["acc"], max_len=bound)
+        M.mkv_paged_evict(c.c, s["acc"], s["pos"], s["lens"], s["lens"], 128, sink=1, recent=8, acc_out=s["acc_out"],
+                          pos_out=s["pos_out"], lens_out=s["lens_out"], src=s["src"], max_len=bound)
+
+    s0 = state[0]
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        step(caches[0], s0)                      # nothing cached yet: lengths 0, token in slot 0
+    torch.cuda.current_stream().wait_stream(st)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(caches[0], s0)
+    for turn, now in enumerate(([500, 20, 3], [0, 1, 0], [137, 20, 2], [500, 129, 128])):
+        for c, s in zip(caches, state):
+            for a, b in zip(c.pools, Cache(M, F16, [500, 129, 128], 6, 64, 64, seed=5, room=bound - 500).pools):
+                c.pools[0 if a is c.pools[0] else 1].copy_(torch.nan_to_num(b))
+            s["k"].copy_(rnd((3, 6, 64), F16, 10 + turn))
+            s["q"].copy_(rnd((3, 12, 64), F16, 20 + turn))
+            s["lens"].copy_(torch.tensor(now, dtype=torch.int32))
+            s["slot"].copy_(torch.tensor([max(0, n - 1) for n in now], dtype=torch.int32))
+            s["acc"].copy_(rnd(s["acc"].shape, F32, 30 + turn).abs())
+            s["pos"].copy_(torch.arange(bound, dtype=torch.int32))
+            for k in ("acc_out", "pos_out"):
+                s[k].zero_()
+        g.replay()
+        step(caches[1], state[1])
+        torch.cuda.synchronize()
+        for k in state[0]:
+            assert torch.equal(state[0][k], state[1][k]), (turn, k)
+        for a, b in zip(caches[0].pools, caches[1].pools):
+            assert torch.equal(a, b), turn
+        assert state[0]["lens_out"].tolist() == [min(n, 128) for n in now]
+    assert all(c.c.check() == M.MKV_OK for c in caches)
+
+
 def test_broadcast_positions_and_empty_calls(M):
     plan = M.mkv_rope_plan(64)
     x = rnd((3, 5, 2, 64), BF16, 1)

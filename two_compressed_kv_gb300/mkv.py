@@ -418,11 +418,6 @@ def _native():
     return _M
 
 
-def _done(status: int, where: str):
-    if status != MKV_OK:
-        raise MkvError(status, where)
-
-
 def _address(stream):
     """A stream (torch.cuda.Stream or its address) as an address; None stays None."""
     return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
@@ -461,7 +456,7 @@ def mkv_rope(plan, x, pos=None, out=None, transposed=False, first_pos=0, stream=
     m = _native()
     if out is None and isinstance(x, _T.Tensor):
         out = _new(x.shape, x.dtype, x.device, stream)
-    _done(m.rope(plan.address, x, pos, out, transposed, first_pos, _address(stream)), "mkv_rope")
+    _check(m.rope(plan.address, x, pos, out, transposed, first_pos, _address(stream)), "mkv_rope")
     return out
 
 
@@ -530,7 +525,7 @@ def mkv_paged_append(cache, k, v, slot, seq=None, plan=None, pos=None, q=None, q
     (int32) [batch, kv_heads, slots]: set to 0 and to the position in the written slots."""
     if q_out is None and isinstance(q, _T.Tensor):
         q_out = _new(q.shape, q.dtype, q.device, stream)
-    _done(_M.append(cache._address, cache._dev, None if plan is None else plan.address, k, v, slot, seq,
+    _check(_M.append(cache._address, cache._dev, None if plan is None else plan.address, k, v, slot, seq,
                     pos, q, q_out, acc, pos_meta, _address(stream)), "mkv_paged_append")
     return q_out
 
@@ -546,7 +541,7 @@ def mkv_paged_decode(cache, q, seq_lens, out=None, lse=None, acc=None, max_len=0
         out = _new(q.shape, out_dtype or q.dtype, q.device, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
-    _done(_M.decode(cache._address, cache._dev, cache._capacity, q, seq_lens, out, lse, acc, max_len, scale,
+    _check(_M.decode(cache._address, cache._dev, cache._capacity, q, seq_lens, out, lse, acc, max_len, scale,
                     workspace, _address(stream)), "mkv_paged_decode")
     return out
 
@@ -573,7 +568,7 @@ def mkv_paged_evict(cache, acc, pos, seq_lens, next_pos, budget, sink=0, recent=
     if src is None:
         v = cache.view
         src = _new((v.batch, v.n_kv_heads, max(0, budget)), _T.int32, cache.device, stream)
-    _done(_M.evict(cache._address, cache._dev, cache._capacity, acc, pos, seq_lens, next_pos, budget, sink, recent,
+    _check(_M.evict(cache._address, cache._dev, cache._capacity, acc, pos, seq_lens, next_pos, budget, sink, recent,
                    acc_out, pos_out, lens_out, src, max_len, workspace, _address(stream)), "mkv_paged_evict")
     return src
 
