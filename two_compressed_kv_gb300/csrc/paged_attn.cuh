@@ -410,12 +410,14 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
         if (i + u < count && (valid_bits >> (slot + u) & 1)) {
           left[u] = n - (j0 + warp + NW * (i + u)) * PA_BLOCK;
           const bool ok = mbar_wait(&full[warp][slot + u], phases >> (slot + u) & 1);
-          if (!__all_sync(~0u, ok)) {
+          if (__all_sync(~0u, ok)) {
+            phases ^= 1u << (slot + u);
+            pending &= ~(1u << (slot + u));
+          } else {
+            // the copy stays pending: it is waited for once more below
             if (lane == 0 && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
             gave_up = true;
           }
-          phases ^= 1u << (slot + u);
-          pending &= ~(1u << (slot + u));
         }
         // Chains of accumulation, for their latency and because a chain cuts each sum
         // off towards zero.
