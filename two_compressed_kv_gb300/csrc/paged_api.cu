@@ -151,12 +151,11 @@ DecodeLayout decode_layout(const mkv_paged_cache* c, const mkv_paged_decode_args
   l.cluster = stream_cluster(streams, l.limit);
   l.split = l.limit > kClusterTokens * l.cluster && c->batch <= PA_MAX_B;
   if (l.split) l.cluster = 1;
-  // Up to 8 query heads a KV head, large shares for two CTAs an SM at most: a third
-  // slot, where there is one, then takes small shares all the time (256 ragged e4m3
-  // streams 79.6 -> 75.3 us, 32 of 32768 61.0 -> 56.7).  With 16 heads the products
-  // bound it and all slots take large ones (32 e4m3 streams of 65536: 124, 133).
-  int ctas = paged_ctas(c->head_dim * elem_bytes(c->dtype));
-  if (g <= 8) ctas = std::min(ctas, 2);
+  // Large shares for two CTAs an SM at most: a third slot, where there is one, then
+  // takes small shares all the time (256 ragged e4m3 streams 79.6 -> 75.3 us, 32 of
+  // 32768 61.0 -> 56.7; 16 heads: 32 e4m3 streams of 65536 141 -> 131.5, 256 ragged
+  // ones 119.5 -> 110.6, 32 fp16 streams of 65536 in rows of 64 105.5 -> 98.0).
+  const int ctas = std::min(2, paged_ctas(c->head_dim * elem_bytes(c->dtype)));
   l.G = (int)std::min<int64_t>((int64_t)sms * ctas,
                                streams * up(up(l.limit, PA_BLOCK), kMinBlocks));
   l.score_stride = up(l.limit, 16) * 16;
