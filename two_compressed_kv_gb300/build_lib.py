@@ -1,8 +1,10 @@
 """Builds libmkv.so (the C-ABI library) in-tree with nvcc for sm_103a, and
-_marshal.so, the tensor marshalling of its Python binding, with g++.
+_marshal.so, the tensor marshalling of its Python binding, with g++ against the
+interpreter's torch.
 
 Each translation unit is compiled in parallel, then the .cu ones are linked
-into one shared library next to this file.  Usage: python -m two_compressed_kv_gb300.build_lib
+into one shared library next to this file.  The library needs nvcc alone:
+without torch it is built all the same, without _marshal.so.  Usage: python -m two_compressed_kv_gb300.build_lib
 """
 from __future__ import annotations
 
@@ -58,6 +60,12 @@ def _marshal_cmd(out: str):
                "-ltorch_cuda", "-lc10_cuda"])
 
 
+def _build_marshal() -> str:
+    tmp = MARSHAL + ".tmp"
+    _run(_marshal_cmd(tmp))
+    return tmp
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nv = nvcc()
@@ -67,10 +75,8 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
         jobs.append(([nv, "-c", os.path.join(CSRC, src), "-o", obj] + ARCH + FLAGS + extra, obj))
     with cf.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
-        marshal = ex.submit(_run, _marshal_cmd(MARSHAL + ".tmp"))
+        marshal = ex.submit(_build_marshal)
         outs = list(ex.map(lambda j: _run(j[0]), jobs))
-        marshal.result()
-    os.replace(MARSHAL + ".tmp", MARSHAL)
     if verbose or ptxas_info:
         for (cmd, _), out in zip(jobs, outs):
             print(" ".join(cmd[:3]))
@@ -78,6 +84,17 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     tmp = LIB + ".tmp"
     _run([nv, "-shared", "-o", tmp] + [o for _, o in jobs] + ARCH + ["-cudart", "static"])
     os.replace(tmp, LIB)
+    # The library stands by itself.  A marshalling module that does not go with it is taken away:
+    # its argument structs may be another version's.
+    try:
+        os.replace(marshal.result(), MARSHAL)
+    except Exception as e:
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)
+        if not (isinstance(e, ImportError) and e.name == "torch"):
+            raise
+        print("torch cannot be imported: built without _marshal.so, which mkv_rope and mkv_paged_* "
+              "need in Python", file=sys.stderr)
     return LIB
 
 
