@@ -289,3 +289,16 @@ def test_oracle_evict_by_hand():
     assert P.evict(acc, pos, 6, 3, recent=2).tolist() == [4, 5, 2]
     assert P.evict(np.array([np.nan, -1.0, 2.0], np.float32), np.arange(3), 9, 2).tolist() == [0, 2]
 
+
+
+# ---- the marshalling module ---------------------------------------------------------------------
+
+def test_missing_marshalling_module_names_the_build(M, monkeypatch):
+    import sys
+
+    import two_compressed_kv_gb300 as package
+    monkeypatch.setattr(M, "_M", None)
+    monkeypatch.delattr(package, "_marshal", raising=False)
+    monkeypatch.setitem(sys.modules, "two_compressed_kv_gb300._marshal", None)
+    with pytest.raises(ImportError, match="two_compressed_kv_gb300.build_lib"):
+        M.mkv_rope(M.mkv_rope_plan(128), None)

@@ -410,7 +410,11 @@ def _native():
     if _M is None:
         import torch
 
-        from . import _marshal
+        try:
+            from . import _marshal
+        except ImportError as e:
+            raise ImportError("the marshalling module _marshal.so is missing or was built for another Python or "
+                              "torch: run python -m two_compressed_kv_gb300.build_lib") from e
         _marshal.bind(*(ctypes.cast(getattr(_lib, f), c_void_p).value for f in (
             "mkv_rope", "mkv_paged_append", "mkv_paged_decode_workspace", "mkv_paged_decode",
             "mkv_paged_evict_workspace", "mkv_paged_evict")))
