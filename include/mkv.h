@@ -510,7 +510,7 @@ typedef struct {
   float* acc;             /* device [batch][n_kv_heads][meta_stride], or NULL: the slot's accumulated
                              weight is set to 0 */
   int32_t* pos_meta;      /* device [batch][n_kv_heads][meta_stride], or NULL: the slot's position is noted */
-  int64_t k_stride[2];    /* elements between tokens, heads; multiples of 8 */
+  int64_t k_stride[2];    /* elements between tokens, heads; multiples of 8 where the extent > 1 */
   int64_t v_stride[2];
   int64_t q_stride[2];
   int64_t q_out_stride[2];
@@ -540,7 +540,7 @@ typedef struct {
                                weights, summed over the group's query heads, are added */
   void* workspace;          /* device, 16-byte aligned, of mkv_paged_decode_workspace bytes */
   uint64_t workspace_bytes;
-  int64_t q_stride[2];      /* elements between sequences, heads; multiples of 8 */
+  int64_t q_stride[2];      /* elements between sequences, heads; multiples of 8 where the extent > 1 */
   int64_t acc_stride;       /* >= max_len */
   int64_t max_len;          /* bound on seq_lens; 0: max_pages * page_size */
   int32_t n_q_heads;        /* a multiple of n_kv_heads; at most 16 per KV head */

@@ -1,0 +1,65 @@
+"""Calls of the paged cache that its documentation allows, beside those of test_gpu_paged.py:
+views of one token or sequence, status words, handles made while a stream is busy, workspaces of
+a stated size, sequences with a common prefix, captured first calls."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as P
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+F16, BF16, F32, E4M3 = torch.float16, torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def M():
+    from two_compressed_kv_gb300 import mkv
+    return mkv
+
+
+def f64(t):
+    return t.detach().to(torch.float32).cpu().numpy().astype(np.float64)
+
+
+def i32(*a):
+    return torch.tensor(a, dtype=torch.int32, device=DEV)
+
+
+def rnd(shape, dtype, seed, size=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * size).to(dtype).to(DEV)
+
+
+def pages(n, heads, page, dim, dtype=F16, seed=0):
+    return [rnd((n, heads, page, dim), F16, seed + i).to(dtype) for i in range(2)]
+
+
+def test_strides_of_extents_of_1(M):
+    """The unused stride of a single token, sequence or head may be anything."""
+    pools, table = pages(4, 2, 16, 64), i32(2, 0, 3, 1).view(1, 4)
+    c = M.MkvPaged(*pools, table)
+    odd = lambda t, at, by: t.as_strided(t.shape, [by if i == at else s for i, s in enumerate(t.stride())])
+    q, n = rnd((1, 8, 64), F16, 5), i32(50)
+    assert torch.equal(M.mkv_paged_decode(c, odd(q, 0, 3), n), M.mkv_paged_decode(c, q, n))
+    plan, outs = M.mkv_rope_plan(64), []
+    k, v = rnd((1, 2, 64), F16, 6), rnd((1, 2, 64), F16, 7)
+    for f in (lambda t: t, lambda t: odd(t, 0, 5)):
+        for p in pools:
+            p[1, :, 2:] = 0
+        qr = M.mkv_paged_append(c, f(k), f(v), i32(50), plan=plan, q=f(q))
+        outs.append([qr.clone()] + [p.clone() for p in pools])
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    # one KV head and one query head
+    pools = pages(2, 1, 16, 64, seed=9)
+    c = M.MkvPaged(*pools, i32(0, 1).view(2, 1))
+    q, n = rnd((2, 1, 64), F16, 5), i32(3, 16)
+    assert torch.equal(M.mkv_paged_decode(c, odd(q, 1, 7), n), M.mkv_paged_decode(c, q, n))
+    was = [p.clone() for p in pools]
+    M.mkv_paged_append(c, odd(q, 1, 7), odd(q, 1, 9), i32(5, 6))
+    for p, w in zip(pools, was):
+        w[0, 0, 5], w[1, 0, 6] = q[0, 0], q[1, 0]
+        assert torch.equal(p, w)
+    assert c.check() == M.MKV_OK

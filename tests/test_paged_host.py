@@ -302,3 +302,31 @@ def test_missing_marshalling_module_names_the_build(M, monkeypatch):
     monkeypatch.setitem(sys.modules, "two_compressed_kv_gb300._marshal", None)
     with pytest.raises(ImportError, match="two_compressed_kv_gb300.build_lib"):
         M.mkv_rope(M.mkv_rope_plan(128), None)
+
+
+# ---- strides of extents of 1 --------------------------------------------------------------------
+# The calls below are refused for a later reason, so that nothing is launched anywhere.
+
+@pytest.mark.parametrize("cache,kw", [
+    (dict(batch=1), dict(q_stride=[1, 128])), (dict(n_kv_heads=1), dict(q_stride=[128, 3], n_q_heads=1)),
+    (dict(batch=1, n_kv_heads=1), dict(q_stride=[-5, 77], n_q_heads=1))])
+def test_decode_ignores_strides_of_extents_of_1(M, cache, kw):
+    a = _decode_args(M, acc=FAKE, acc_stride=511, **kw)
+    assert M.lib.mkv_paged_decode(ctypes.byref(_cache(M, **cache)), ctypes.byref(a), None) == M.MKV_ERR_INVALID_ARG
+    assert "acc_stride" in M.mkv_last_error_string()
+    # the stride of an extent of 2 still counts
+    a = _decode_args(M, acc=FAKE, acc_stride=511, q_stride=[1, 77], n_q_heads=2)
+    assert M.lib.mkv_paged_decode(ctypes.byref(_cache(M, **cache)), ctypes.byref(a), None) == M.MKV_ERR_INVALID_ARG
+    assert "strides" in M.mkv_last_error_string()
+
+
+@pytest.mark.parametrize("cache,kw", [
+    (dict(), dict(n=1, k_stride=[252, 128], v_stride=[1, 128])),
+    (dict(n_kv_heads=1), dict(k_stride=[256, 1], v_stride=[256, 77])),
+    (dict(), dict(n=1, q=FAKE, q_out=2 * FAKE, n_q_heads=4, q_stride=[5, 128], q_out_stride=[0, 128])),
+    (dict(), dict(q=FAKE, q_out=2 * FAKE, n_q_heads=1, q_stride=[512, 3], q_out_stride=[512, -3])),
+    (dict(), dict(n=1, q=FAKE, q_out=FAKE, n_q_heads=4, q_stride=[512, 128], q_out_stride=[1024, 128]))])
+def test_append_ignores_strides_of_extents_of_1(M, cache, kw):
+    a = _append_args(M, acc=FAKE, **kw)
+    assert M.lib.mkv_paged_append(ctypes.byref(_cache(M, **cache)), None, ctypes.byref(a), None) == M.MKV_ERR_INVALID_ARG
+    assert "meta_stride" in M.mkv_last_error_string()

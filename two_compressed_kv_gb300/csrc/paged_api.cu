@@ -27,6 +27,9 @@ mkv_status bad(const char* text) { return set_error(MKV_ERR_INVALID_ARG, text); 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool is16(int dtype) { return dtype == MKV_DT_F16 || dtype == MKV_DT_BF16; }
+// Stride of a dimension that is walked over: 16-byte accesses need multiples of 8
+// elements.  That of an extent of 1 is never used.
+bool stride8(int64_t stride, int64_t extent) { return extent <= 1 || stride % 8 == 0; }
 int elem_bytes(int dtype) { return dtype == MKV_DT_F32 ? 4 : dtype == MKV_DT_E4M3 ? 1 : 2; }
 
 // SMs of the current device.
@@ -397,12 +400,13 @@ mkv_status mkv_paged_append(const mkv_paged_cache* c, const mkv_rope_plan* plan,
   if (a->q && (!a->q_out || a->n_q_heads < 1 || a->n_q_heads > 1 << 20))
     return bad("mkv_paged_append: q needs q_out and n_q_heads >= 1");
   for (int i = 0; i < 2; ++i) {
-    if (a->k_stride[i] % 8 != 0 || a->v_stride[i] % 8 != 0 ||
-        (a->q && (a->q_stride[i] % 8 != 0 || a->q_out_stride[i] % 8 != 0)))
+    const int64_t kv_extent = i == 0 ? a->n : c->n_kv_heads, q_extent = i == 0 ? a->n : a->n_q_heads;
+    if (!stride8(a->k_stride[i], kv_extent) || !stride8(a->v_stride[i], kv_extent) ||
+        (a->q && (!stride8(a->q_stride[i], q_extent) || !stride8(a->q_out_stride[i], q_extent))))
       return bad("mkv_paged_append: strides must be multiples of 8 elements");
-    if (a->q && a->q_out_stride[i] <= 0 && (i == 0 ? a->n : a->n_q_heads) > 1)
+    if (a->q && a->q_out_stride[i] <= 0 && q_extent > 1)
       return bad("mkv_paged_append: q_out's strides must be positive");
-    if (a->q && a->q == a->q_out && a->q_stride[i] != a->q_out_stride[i])
+    if (a->q && a->q == a->q_out && q_extent > 1 && a->q_stride[i] != a->q_out_stride[i])
       return bad("mkv_paged_append: in place, q and q_out need the same strides");
   }
   if ((a->acc || a->pos_meta) && a->meta_stride < 1) return bad("mkv_paged_append: meta_stride must be >= 1");
@@ -439,7 +443,7 @@ mkv_status mkv_paged_decode(const mkv_paged_cache* c, const mkv_paged_decode_arg
   if (const char* e = check_decode(c, a)) return bad(e);
   if (!a->q || !a->out || !a->seq_lens) return bad("mkv_paged_decode: NULL q, out or seq_lens");
   if (!aligned16(a->q) || !aligned16(a->out)) return bad("mkv_paged_decode: q and out must be 16-byte aligned");
-  if (a->q_stride[0] % 8 != 0 || a->q_stride[1] % 8 != 0)
+  if (!stride8(a->q_stride[0], c->batch) || !stride8(a->q_stride[1], a->n_q_heads))
     return bad("mkv_paged_decode: q's strides must be multiples of 8 elements");
   if (a->acc && a->acc_stride < decode_limit(c, a)) return bad("mkv_paged_decode: acc_stride must be >= max_len");
   if (!a->workspace || !aligned16(a->workspace)) return bad("mkv_paged_decode: workspace must be 16-byte aligned");
