@@ -606,9 +606,10 @@ mkv_status mkv_paged_evict(const mkv_paged_cache* cache, const mkv_paged_evict_a
                            mkv_stream_t stream);
 
 /* Reads and clears a device status word after all work on the current device
- * (synchronous): MKV_ERR_DEVICE_CHECK if a kernel met a page, slot, sequence
- * or length outside the cache since the last check, MKV_ERR_TIMEOUT if a
- * bounded wait for a copy gave up (outputs undefined then), else MKV_OK. */
+ * (synchronous): MKV_ERR_TIMEOUT if a bounded wait for a copy gave up since the
+ * last check (outputs undefined then), else MKV_ERR_DEVICE_CHECK if a kernel
+ * met a page, slot, sequence or length outside the cache, else MKV_OK.  Where
+ * both happened, mkv_last_error_string names both. */
 mkv_status mkv_paged_check(int32_t* status);
 
 #ifdef __cplusplus

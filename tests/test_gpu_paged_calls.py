@@ -63,3 +63,14 @@ def test_strides_of_extents_of_1(M):
         w[0, 0, 5], w[1, 0, 6] = q[0, 0], q[1, 0]
         assert torch.equal(p, w)
     assert c.check() == M.MKV_OK
+
+
+def test_check_names_every_bit(M):
+    """A wait that gave up (outputs undefined) is not hidden behind a page outside the cache."""
+    c = M.MkvPaged(*pages(2, 1, 16, 64), i32(0, 1).view(1, 2))
+    for bits, status, words in ((1, M.MKV_ERR_TIMEOUT, ["wait"]), (2, M.MKV_ERR_DEVICE_CHECK, ["page"]),
+                                (3, M.MKV_ERR_TIMEOUT, ["wait", "page"])):
+        c.status.fill_(bits)
+        assert c.check() == status, bits
+        assert all(w in M.mkv_last_error_string() for w in words)
+        assert c.check() == M.MKV_OK

@@ -576,7 +576,11 @@ mkv_status mkv_paged_check(int32_t* status) {
   if (v == 0) return MKV_OK;
   CKP(cudaMemset(status, 0, sizeof(v)));
   CKP(cudaDeviceSynchronize());
-  if (!(v & DEV_ERR_CHECK)) return set_error(MKV_ERR_TIMEOUT, "a bounded device-side wait gave up");
+  // the graver first: outputs are undefined after a wait that gave up, defined otherwise
+  if (v & DEV_ERR_TIMEOUT)
+    return set_error(MKV_ERR_TIMEOUT, v & DEV_ERR_CHECK ? "a bounded device-side wait gave up; a page, slot, sequence or "
+                                                          "length lay outside the paged cache too"
+                                                        : "a bounded device-side wait gave up");
   return set_error(MKV_ERR_DEVICE_CHECK, "a page, slot, sequence or length lay outside the paged cache");
 }
 

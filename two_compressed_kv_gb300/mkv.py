@@ -515,8 +515,10 @@ class MkvPaged:
         return self._capacity
 
     def check(self) -> int:
-        """MKV_OK, or MKV_ERR_DEVICE_CHECK when a kernel met a page, slot, sequence or length
-        outside the cache since the last check (synchronous)."""
+        """What kernels reported since the last check (synchronous): MKV_ERR_TIMEOUT when a bounded
+        wait for a copy gave up (outputs undefined), else MKV_ERR_DEVICE_CHECK when one met a page,
+        slot, sequence or length outside the cache, else MKV_OK.  mkv_last_error_string() names
+        both where both happened."""
         with _T.cuda.device(self.device):
             return _lib.mkv_paged_check(self.status.data_ptr())
 
