@@ -74,3 +74,17 @@ def test_check_names_every_bit(M):
         assert c.check() == status, bits
         assert all(w in M.mkv_last_error_string() for w in words)
         assert c.check() == M.MKV_OK
+
+
+def test_status_word_is_ready_for_any_stream(M):
+    """A handle made while its stream is busy: what a call on another stream reports stays."""
+    pools, table = pages(2, 1, 16, 64), i32(0, 1).view(1, 2)
+    k, slot = rnd((1, 1, 64), F16, 3), i32(1000)
+    side = torch.cuda.Stream()
+    first = M.MkvPaged(*pools, table)            # the kernel is loaded, which waits for the device
+    M.mkv_paged_append(first, k, k, slot, stream=side)
+    assert first.check() == M.MKV_ERR_DEVICE_CHECK
+    torch.cuda._sleep(100_000_000)               # some 50 ms
+    c = M.MkvPaged(*pools, table)
+    M.mkv_paged_append(c, k, k, slot, stream=side)
+    assert c.check() == M.MKV_ERR_DEVICE_CHECK and c.check() == M.MKV_OK

@@ -504,6 +504,9 @@ class MkvPaged:
         self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
         self.k_scale, self.v_scale = k_scale, v_scale
         self.status = _T.zeros(1, dtype=_T.int32, device=self.device)
+        with _T.cuda.device(self.device):        # zero before a call on any stream may set a bit
+            if not _T.cuda.is_current_stream_capturing():
+                _T.cuda.current_stream().synchronize()
         v.status = self.status.data_ptr()
         _check(_lib.mkv_paged_validate(ctypes.byref(v)), "mkv_paged_validate")
         self._address, self._dev = ctypes.addressof(v), self.device.index
