@@ -88,3 +88,29 @@ def test_status_word_is_ready_for_any_stream(M):
     c = M.MkvPaged(*pools, table)
     M.mkv_paged_append(c, k, k, slot, stream=side)
     assert c.check() == M.MKV_ERR_DEVICE_CHECK and c.check() == M.MKV_OK
+
+
+@pytest.mark.parametrize("batch,budget,max_len", [(2, 20, 0), (2, 20, 100), (3, 500, 60), (80, 100, 40000)])
+def test_evict_workspace_of_the_stated_size(M, batch, budget, max_len):
+    """Short and long forms, and a budget above the bound: the size given is enough and needed."""
+    heads, page = 2, 256 if max_len > 1000 else 16
+    cap = (max_len or 128) // page + 1
+    pools = pages(2 * batch, heads, page, 64)
+    table = torch.full((batch, cap), -1, dtype=torch.int32, device=DEV)
+    table[:, :2] = torch.arange(2 * batch, dtype=torch.int32, device=DEV).view(batch, 2)
+    c = M.MkvPaged(*pools, table)
+    slots = max_len or c.capacity
+    acc = torch.rand((batch, heads, slots), device=DEV)
+    pos = torch.arange(slots, dtype=torch.int32, device=DEV).expand(batch, heads, slots).contiguous()
+    lens = torch.full((batch,), min(2 * page, slots), dtype=torch.int32, device=DEV)
+    size = M.mkv_paged_evict_workspace(c, budget, max_len=max_len)
+    assert size > 0
+    out = dict(acc_out=torch.empty_like(acc), pos_out=torch.empty_like(pos), lens_out=torch.empty_like(lens))
+    want = M.mkv_paged_evict(c, acc, pos, lens, lens, budget, max_len=max_len, **out)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    assert torch.equal(want, M.mkv_paged_evict(c, acc, pos, lens, lens, budget, max_len=max_len, workspace=ws, **out))
+    with pytest.raises(M.MkvError, match="workspace"):
+        M.mkv_paged_evict(c, acc, pos, lens, lens, budget, max_len=max_len, workspace=ws[:-256], **out)
+    with pytest.raises(M.MkvError, match="budget"):
+        M.mkv_paged_evict_workspace(c, 0)
+    assert c.check() == M.MKV_OK

@@ -567,13 +567,27 @@ def mkv_paged_decode_workspace(cache, q_heads, max_len=0, weights=False) -> int:
     return n
 
 
+def mkv_paged_evict_workspace(cache, budget, max_len=0) -> int:
+    """Bytes of workspace of mkv_paged_evict for these sizes (max_len: the call's bound; 0: the
+    page table's capacity, which is enough for a call without a bound too)."""
+    a = mkv_paged_evict_args(budget=budget, max_len=max_len, meta_stride=max_len or cache.capacity,
+                             out_stride=budget)
+    with _T.cuda.device(cache.device):
+        n = _lib.mkv_paged_evict_workspace(ctypes.byref(cache.view), ctypes.byref(a))
+    if n == 0:
+        raise MkvError(MKV_ERR_INVALID_ARG, "mkv_paged_evict_workspace")
+    return n
+
+
 def mkv_paged_evict(cache, acc, pos, seq_lens, next_pos, budget, sink=0, recent=0, acc_out=None,
                     pos_out=None, lens_out=None, src=None, max_len=0, workspace=None, stream=None):
     """Cuts every (sequence, KV head) down to `budget` tokens by accumulated weight, in place in
     the pages.  acc (fp32), pos (int32) [batch, kv_heads, slots]; acc_out and pos_out [batch,
     kv_heads, slots_out] (None: in place, acc and pos themselves); seq_lens, next_pos int32
     [batch]; lens_out int32 [batch] (None: seq_lens); src int32 [batch, kv_heads, budget] (new
-    where None): the slot each kept token came from.  Returns src."""
+    where None): the slot each kept token came from.  max_len: a bound on seq_lens (0: acc's slots or
+    the page table's capacity).  workspace: a uint8 tensor of mkv_paged_evict_workspace bytes (None:
+    taken from torch's allocator).  Returns src."""
     if src is None:
         v = cache.view
         src = _new((v.batch, v.n_kv_heads, max(0, budget)), _T.int32, cache.device, stream)
