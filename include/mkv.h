@@ -476,7 +476,10 @@ mkv_status mkv_rope(const mkv_rope_plan* plan, const mkv_rope_args* args, mkv_st
 
 /* A paged cache: a view of memory that the caller owns, nothing is kept.
  * Slot t of sequence b lies in row t mod page_size of page
- * page_table[b * table_stride + t / page_size]. */
+ * page_table[b * table_stride + t / page_size].
+ * Sequences may have pages in common (a prefix stored once) as long as such
+ * pages are only read, by mkv_paged_decode.  mkv_paged_append and
+ * mkv_paged_evict write, and do not look for a page's other users: see there. */
 typedef struct {
   void* k_pages;              /* device [n_pages][n_kv_heads][page_size][head_dim], 16-byte aligned */
   void* v_pages;
@@ -524,7 +527,7 @@ typedef struct {
  * rotated), values as they are, both rounded to the cache's type (E4M3: times
  * the reciprocal of the head's scale, nearest even, saturated at 448); queries are
  * rotated with the same positions.  Two tokens of a call must not share a
- * slot.  plan->rot_dim must be a multiple of 16 (half pairs) or 8
+ * slot, nor a row of a page that is in two tables.  plan->rot_dim must be a multiple of 16 (half pairs) or 8
  * (interleaved) and plan->head_dim the cache's.  A token whose sequence, slot
  * or page lies outside the cache is left out and reported in `status`. */
 mkv_status mkv_paged_append(const mkv_paged_cache* cache, const mkv_rope_plan* plan,
@@ -600,7 +603,13 @@ uint64_t mkv_paged_evict_workspace(const mkv_paged_cache* cache, const mkv_paged
  * step which is one token over the budget moves one row.  Attention does not
  * depend on the order of slots; pos_out says which token lies where.  Rows
  * behind the new length are left as they were.  Heads keep different tokens;
- * the lengths stay equal.  A page outside the cache is skipped and reported
+ * the lengths stay equal.
+ * Every page that holds a slot below the old length of a sequence with more
+ * than `budget` tokens must be that sequence's alone, and in its table once:
+ * rows move within the page itself, so another sequence that names it would
+ * lose its tokens to this one's, or copy them while they change, and nothing
+ * reports it.  Copy pages in common (a prefix) and point the table at the
+ * copies first.  A page outside the cache is skipped and reported
  * in `status`, a length outside 0 .. max_len counts as the nearer bound. */
 mkv_status mkv_paged_evict(const mkv_paged_cache* cache, const mkv_paged_evict_args* args,
                            mkv_stream_t stream);

@@ -114,3 +114,40 @@ def test_evict_workspace_of_the_stated_size(M, batch, budget, max_len):
     with pytest.raises(M.MkvError, match="budget"):
         M.mkv_paged_evict_workspace(c, 0)
     assert c.check() == M.MKV_OK
+
+
+@pytest.mark.parametrize("dtype", [F16, E4M3])
+def test_common_prefix(M, dtype):
+    """Three sequences over the same first pages: attention reads the shared pages; before
+    eviction, which moves rows, all but one of the sequences get copies."""
+    heads, page, dim, shared, budget = 2, 16, 64, 2, 40
+    pools = pages(20, heads, page, dim, dtype, seed=3)
+    lens = [70, 45, 33]
+    table = i32(5, 9, 1, 2, 3, 5, 9, 4, -1, -1, 5, 9, 6, -1, -1).view(3, 5)
+    c = M.MkvPaged(*pools, table)
+    u8 = lambda p: p.view(torch.uint8) if dtype == E4M3 else p
+    kept = lambda: [[f64(torch.cat(list(u8(p)[table[i, : -(-n // page)].long()].view(dtype)), 1)[:, :n])
+                     for i, n in enumerate(lens)] for p in pools]
+    K, V = kept()
+    q, n = rnd((3, 4, dim), F16, 4), i32(*lens)
+    out = f64(M.mkv_paged_decode(c, q, n, out_dtype=F32))
+    for i in range(3):
+        want, _, _, size = P.decode(f64(q[i]), K[i], V[i])
+        assert (np.abs(out[i] - want) <= 2.0**-12 * size).all()
+    # copies for sequences 1 and 2, then every head of every sequence keeps other tokens
+    for i, new in ((1, (10, 11)), (2, (12, 13))):
+        for j in range(shared):
+            for p in pools:
+                u8(p)[new[j]] = u8(p)[int(table[i, j])]
+            table[i, j] = new[j]
+    acc = torch.rand((3, heads, 80), generator=torch.Generator().manual_seed(8)).to(DEV)
+    pos = torch.arange(80, dtype=torch.int32, device=DEV).expand(3, heads, 80).contiguous()
+    a, p = acc.cpu().numpy().copy(), pos.cpu().numpy().copy()
+    M.mkv_paged_evict(c, acc, pos, n, n.clone(), budget, sink=4, recent=8)
+    assert c.check() == M.MKV_OK and n.tolist() == [min(m, budget) for m in lens]
+    was, old, lens = (K, V), lens, n.tolist()
+    for w, now in zip(was, kept()):
+        for i in range(3):
+            for h in range(heads):
+                src = P.evict(a[i, h, : old[i]], p[i, h, : old[i]], old[i], budget, 4, 8)
+                assert (now[i][h] == w[i][h][src]).all()
