@@ -151,3 +151,47 @@ def test_common_prefix(M, dtype):
             for h in range(heads):
                 src = P.evict(a[i, h, : old[i]], p[i, h, : old[i]], old[i], budget, 4, 8)
                 assert (now[i][h] == w[i][h][src]).all()
+
+
+def test_captured_first_calls():
+    """In a new process, the first call of every operator is one that a graph captures."""
+    code = """
+import torch
+from two_compressed_kv_gb300 import mkv as M
+dev = torch.device("cuda:0")
+g = torch.Generator().manual_seed(1)
+rnd = lambda *s: torch.randn(s, generator=g).half().to(dev)
+i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=dev)
+pools = [rnd(8, 2, 16, 64) for _ in range(2)]
+table = i32(*range(8)).view(2, 4)
+c = M.MkvPaged(*pools, table)
+plan = M.mkv_rope_plan(64)
+k, q, slot, lens, nxt = rnd(2, 2, 64), rnd(2, 8, 64), i32(50, 30), i32(51, 31), i32(51, 31)
+acc = torch.rand((2, 2, 64), generator=g).to(dev)
+pos = torch.arange(64, dtype=torch.int32, device=dev).expand(2, 2, 64).contiguous()
+
+def step(c, acc, pos, lens):
+    r = M.mkv_rope(plan, q.view(2, 1, 8, 64), first_pos=7)
+    a = M.mkv_paged_append(c, k, k, slot, plan=plan, q=q, acc=acc, pos_meta=pos)
+    o = M.mkv_paged_decode(c, a, lens, acc=acc)
+    s = M.mkv_paged_evict(c, acc, pos, lens, nxt, 20, sink=2, recent=5)
+    return [r, a, o, s, acc, pos, lens]
+
+other = [p.clone() for p in pools]
+args = [t.clone() for t in (acc, pos, lens)]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step(c, acc, pos, lens)
+graph.replay()
+want = step(M.MkvPaged(*other, table), *args)
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got + pools, want + other))
+assert c.check() == M.MKV_OK
+print("same")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout + r.stderr
