@@ -485,7 +485,7 @@ typedef struct {
   void* v_pages;
   const int32_t* page_table;  /* device [batch][max_pages], row stride table_stride */
   const float* k_scale;       /* E4M3 only: device [n_kv_heads], an element stands for value * scale; */
-  const float* v_scale;       /*   NULL: 1.  Scales must be positive and finite. */
+  const float* v_scale;       /*   NULL: 1.  Scales must be positive, finite and not subnormal. */
   int32_t* status;            /* device word, or NULL: bits set by kernels (see mkv_paged_check) */
   int64_t table_stride;       /* >= max_pages */
   int32_t dtype;              /* MKV_DT_F16, BF16 or E4M3 */
@@ -545,7 +545,8 @@ typedef struct {
   uint64_t workspace_bytes;
   int64_t q_stride[2];      /* elements between sequences, heads; multiples of 8 where the extent > 1 */
   int64_t acc_stride;       /* >= max_len */
-  int64_t max_len;          /* bound on seq_lens; 0: max_pages * page_size */
+  int64_t max_len;          /* bound on seq_lens; 0: max_pages * page_size.  How the work is spread goes by
+                               it, so a bound far above the lengths costs time */
   int32_t n_q_heads;        /* a multiple of n_kv_heads; at most 16 per KV head */
   int32_t q_dtype;
   int32_t out_dtype;        /* q_dtype or MKV_DT_F32 */
@@ -566,7 +567,13 @@ uint64_t mkv_paged_decode_workspace(const mkv_paged_cache* cache, const mkv_page
  * they hold.  A length below 0 or above max_len counts as 0 or max_len, and a
  * page outside the cache as absent tokens; both are reported in `status`.
  * Results do not depend on timing: no atomics, a fixed order of summation for
- * given lengths of all sequences and a given bound. */
+ * given lengths of all sequences and a given bound.
+ * A value row with an infinity or a NaN makes that channel of its sequence's
+ * output non-finite, whatever the token weighs (of infinities alone it may be a
+ * NaN).  F16 and E4M3 caches: a token that weighs less than 2^-37 of the largest
+ * may add nothing to the output; it counts in the sum, lse and acc.
+ * With more than 512 sequences a single CTA reads each (sequence, KV head),
+ * however long it is: a few long sequences are faster in a call of their own. */
 mkv_status mkv_paged_decode(const mkv_paged_cache* cache, const mkv_paged_decode_args* args,
                             mkv_stream_t stream);
 
@@ -584,7 +591,9 @@ typedef struct {
   uint64_t workspace_bytes;
   int64_t meta_stride;      /* >= max_len */
   int64_t out_stride;       /* >= min(budget, max_len) */
-  int64_t max_len;          /* bound on seq_lens; 0: max_pages * page_size */
+  int64_t max_len;          /* bound on seq_lens; 0: max_pages * page_size.  The kernels are chosen by it,
+                               and from some ten thousand slots a (sequence, KV head) on the workspace
+                               has 8 bytes a slot: a bound far above the lengths costs time and memory */
   int32_t budget;           /* tokens to keep, >= 1 */
   int32_t sink;             /* tokens at positions below this are kept, >= 0 */
   int32_t recent;           /* tokens at positions >= next_pos - recent are kept, >= 0;
@@ -604,13 +613,16 @@ uint64_t mkv_paged_evict_workspace(const mkv_paged_cache* cache, const mkv_paged
  * depend on the order of slots; pos_out says which token lies where.  Rows
  * behind the new length are left as they were.  Heads keep different tokens;
  * the lengths stay equal.
+ * Weights come from mkv_paged_decode alone: tokens that were appended and never
+ * attended to weigh 0, and of equal weights the lower slots stay.
  * Every page that holds a slot below the old length of a sequence with more
  * than `budget` tokens must be that sequence's alone, and in its table once:
  * rows move within the page itself, so another sequence that names it would
  * lose its tokens to this one's, or copy them while they change, and nothing
  * reports it.  Copy pages in common (a prefix) and point the table at the
- * copies first.  A page outside the cache is skipped and reported
- * in `status`, a length outside 0 .. max_len counts as the nearer bound. */
+ * copies first.  A row whose old or new page lies outside the
+ * cache is not moved, which `status` reports; src, acc_out and pos_out name its
+ * token all the same.  A length outside 0 .. max_len counts as the nearer bound. */
 mkv_status mkv_paged_evict(const mkv_paged_cache* cache, const mkv_paged_evict_args* args,
                            mkv_stream_t stream);
 

@@ -195,3 +195,20 @@ print("same")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout + r.stderr
+
+
+def test_infinite_value_shows_in_its_channel_alone(M):
+    """An infinity among a live token's values: that channel of its heads is not finite, all else is
+    as it was; behind the sequence it changes nothing."""
+    pools, table = pages(6, 2, 16, 64, seed=5), i32(4, 1, 0, 3, 2, 5).view(2, 3)
+    c = M.MkvPaged(*pools, table)
+    q, n = rnd((2, 8, 64), F16, 6), i32(40, 40)
+    lse = [torch.empty((2, 8), device=DEV) for _ in range(2)]
+    want = M.mkv_paged_decode(c, q, n, lse=lse[0])
+    pools[1][5, :, 8:] = float("inf")            # slots 40 to 47 of sequence 1
+    assert torch.equal(M.mkv_paged_decode(c, q, n, lse=lse[1]), want) and torch.equal(*lse)
+    pools[1][3, 1, 2, 9] = float("-inf")         # slot 2 of sequence 1, head 1, channel 9
+    got = M.mkv_paged_decode(c, q, n, lse=lse[1])
+    assert torch.equal(*lse) and not torch.isfinite(got[1, 4:, 9]).any()
+    got[1, 4:, 9] = want[1, 4:, 9]
+    assert torch.equal(got, want)

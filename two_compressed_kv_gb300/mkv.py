@@ -456,7 +456,8 @@ def mkv_rope(plan, x, pos=None, out=None, transposed=False, first_pos=0, stream=
     """Rotates x [batch, tokens, heads, head_dim] (fp16, bf16 or fp32; any strides, the last
     dimension contiguous) by the positions pos (int32 [batch, tokens]; None: first_pos + token)
     into out (new where None; may be x; e.g. a transposed view of a [batch, heads, tokens,
-    head_dim] tensor).  transposed: the gradient of the call.  Returns out."""
+    head_dim] tensor).  transposed: the gradient of the call.  Returns out, which like the results
+    of all calls here carries no autograd history: a backward pass calls it with transposed=True."""
     m = _native()
     if out is None and isinstance(x, _T.Tensor):
         out = _new(x.shape, x.dtype, x.device, stream)
@@ -468,7 +469,8 @@ class MkvPaged:
     """A paged cache over the caller's tensors: k_pages, v_pages [n_pages, kv_heads, page_size,
     head_dim] (fp16, bf16 or float8_e4m3fn), page_table int32 [batch, max_pages] (rows may be
     strided), k_scale and v_scale fp32 [kv_heads] (float8 only).  Holds the tensors and a status
-    word; check() reports what kernels found outside the cache."""
+    word, so keep it until its calls have ended; check() reports what kernels found outside the
+    cache."""
 
     def __init__(self, k_pages, v_pages, page_table, k_scale=None, v_scale=None):
         _native()
@@ -545,7 +547,9 @@ def mkv_paged_decode(cache, q, seq_lens, out=None, lse=None, acc=None, max_len=0
     (int32 [batch]) cached tokens.  out: contiguous, of q's type or fp32 (new, of out_dtype,
     where None), returned.  lse: fp32 [batch, q_heads] or None.  acc: fp32 [batch, kv_heads,
     slots] or None; every token's weights are added.  max_len: a bound on seq_lens (0: the page
-    table's capacity, or acc's slots where those are fewer).  workspace: a uint8 tensor (None: taken from torch's allocator)."""
+    table's capacity, or, with acc, its slots where those are fewer); one near the lengths is faster.
+    workspace: a uint8 tensor of mkv_paged_decode_workspace bytes (None: taken from torch's
+    allocator)."""
     if out is None and isinstance(q, _T.Tensor):
         out = _new(q.shape, out_dtype or q.dtype, q.device, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
@@ -586,7 +590,7 @@ def mkv_paged_evict(cache, acc, pos, seq_lens, next_pos, budget, sink=0, recent=
     kv_heads, slots_out] (None: in place, acc and pos themselves); seq_lens, next_pos int32
     [batch]; lens_out int32 [batch] (None: seq_lens); src int32 [batch, kv_heads, budget] (new
     where None): the slot each kept token came from.  max_len: a bound on seq_lens (0: acc's slots or
-    the page table's capacity).  workspace: a uint8 tensor of mkv_paged_evict_workspace bytes (None:
+    the page table's capacity, the fewer); one near the lengths is faster.  workspace: a uint8 tensor of mkv_paged_evict_workspace bytes (None:
     taken from torch's allocator).  Returns src."""
     if src is None:
         v = cache.view
