@@ -14,8 +14,8 @@
 // What bounds it: select reads 8 bytes a token once from DRAM and is then
 // bound by the latency of its few cluster-wide steps; move by DRAM, 4 rows of
 // traffic per moved token.  Measured, both together: 64 streams of 4097 to 4096
-// 9.4 us; 32 streams of 32768 to 2048 (fp16 rows of 128) 30.6 us, of which 9 are
-// select's 18 thousand cycles; 8 streams of 1048576 to 8192 62.5 us, the pass over
+// 9.4 us; 32 streams of 32768 to 2048 (fp16 rows of 128) 30.7 us, of which 9 are
+// select's 18 thousand cycles; 8 streams of 1048576 to 8192 62.8 us, the pass over
 // 67 MB by 64 SMs 15 us of them.
 #include <cooperative_groups.h>
 

@@ -91,7 +91,7 @@ const char* check_cache(const mkv_paged_cache* c) {
 //   256 streams  1024: 24.6, 36.7  2048: 44.0, 56.0
 // Lengths are not known to the host, and one long sequence among short ones takes
 // as long as its own CTAs: 64 x 4 streams, one of 16384 tokens: 52 us in clusters
-// of 4, 20 split; spread up to 16384: 96 and 80 us.  So the bound is low.
+// of 4, 20 split; spread up to 16384: 96 and 76 us.  So the bound is low.
 constexpr int64_t kClusterTokens = 2048;
 
 // CTAs of a stream: as many as run at once for all streams (clusters of 8: 16 of
@@ -108,11 +108,11 @@ constexpr int kMinBlocks = 8;
 
 // What a part of a stream costs a CTA apart from its blocks (its queries, the
 // first copies' latency, the join of the warps), in blocks.  256 ragged e4m3
-// streams: 80.2 us with 32, 81.2 with 8; equal long streams: no difference.
+// streams: 76.3 us with 32, 81.8 with 8; equal long streams: no difference.
 constexpr int kPieceLoad = 32;
 // Sixteenths of the load handed out in small shares, from so many blocks a CTA
-// on.  With 0, 2 and 4: the ragged batch 86, 82 and 80 us, 32K batch 4 94, 97 and
-// 91 us; 128K batch 8 720 us with none, 683 to 691 with 3 or 4.
+// on.  With 0, 2 and 4: the ragged batch 90.6, 80.9 and 76.3 us, fp16 32K batch 4
+// 93.4, 92.1 and 88.4, 128K batch 8 633, 603 and 607.
 constexpr int kTail16 = 4;
 constexpr int kTailFrom = 64;
 
