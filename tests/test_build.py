@@ -47,3 +47,19 @@ def test_library_survives_a_failing_marshal_step(box):
     with pytest.raises(RuntimeError, match="g\\+\\+"):
         build_lib.build()
     assert os.path.exists(build_lib.LIB) and not os.path.exists(build_lib.MARSHAL)
+
+
+def test_nothing_half_made_stays(box, monkeypatch):
+    """A failing nvcc step leaves the library and the module of the last build, and no other file."""
+    build_lib.build()
+    here = os.path.dirname(build_lib.LIB)
+    was = sorted(os.listdir(here))
+
+    def run(cmd):
+        if "-c" in cmd:
+            raise RuntimeError("nvcc: no such header")
+        return box(cmd)
+    monkeypatch.setattr(build_lib, "_run", run)
+    with pytest.raises(RuntimeError, match="nvcc"):
+        build_lib.build()
+    assert sorted(os.listdir(here)) == was

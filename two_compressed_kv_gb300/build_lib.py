@@ -61,7 +61,7 @@ def _marshal_cmd(out: str):
 
 
 def _build_marshal() -> str:
-    tmp = MARSHAL + ".tmp"
+    tmp = os.path.join(BUILD, os.path.basename(MARSHAL))
     _run(_marshal_cmd(tmp))
     return tmp
 
