@@ -527,9 +527,10 @@ typedef struct {
  * rotated), values as they are, both rounded to the cache's type (E4M3: times
  * the reciprocal of the head's scale, nearest even, saturated at 448); queries are
  * rotated with the same positions.  Two tokens of a call must not share a
- * slot, nor a row of a page that is in two tables.  plan->rot_dim must be a multiple of 16 (half pairs) or 8
- * (interleaved) and plan->head_dim the cache's.  A token whose sequence, slot
- * or page lies outside the cache is left out and reported in `status`. */
+ * slot, nor a row of a page that is in two tables.  plan->rot_dim must be a
+ * multiple of 16 (half pairs) or 8 (interleaved) and plan->head_dim the cache's.
+ * A token whose sequence, slot or page lies outside the cache is left out and
+ * reported in `status`. */
 mkv_status mkv_paged_append(const mkv_paged_cache* cache, const mkv_rope_plan* plan,
                             const mkv_paged_append_args* args, mkv_stream_t stream);
 
@@ -620,9 +621,9 @@ uint64_t mkv_paged_evict_workspace(const mkv_paged_cache* cache, const mkv_paged
  * rows move within the page itself, so another sequence that names it would
  * lose its tokens to this one's, or copy them while they change, and nothing
  * reports it.  Copy pages in common (a prefix) and point the table at the
- * copies first.  A row whose old or new page lies outside the
- * cache is not moved, which `status` reports; src, acc_out and pos_out name its
- * token all the same.  A length outside 0 .. max_len counts as the nearer bound. */
+ * copies first.
+ * A row whose old or new page lies outside the cache is not moved, which
+ * `status` reports; src, acc_out and pos_out name its token all the same.  A length outside 0 .. max_len counts as the nearer bound. */
 mkv_status mkv_paged_evict(const mkv_paged_cache* cache, const mkv_paged_evict_args* args,
                            mkv_stream_t stream);
 

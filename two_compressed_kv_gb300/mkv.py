@@ -586,12 +586,13 @@ def mkv_paged_evict_workspace(cache, budget, max_len=0) -> int:
 def mkv_paged_evict(cache, acc, pos, seq_lens, next_pos, budget, sink=0, recent=0, acc_out=None,
                     pos_out=None, lens_out=None, src=None, max_len=0, workspace=None, stream=None):
     """Cuts every (sequence, KV head) down to `budget` tokens by accumulated weight, in place in
-    the pages: the pages of a sequence that is cut must be its own (copy a common prefix first).  acc (fp32), pos (int32) [batch, kv_heads, slots]; acc_out and pos_out [batch,
-    kv_heads, slots_out] (None: in place, acc and pos themselves); seq_lens, next_pos int32
-    [batch]; lens_out int32 [batch] (None: seq_lens); src int32 [batch, kv_heads, budget] (new
-    where None): the slot each kept token came from.  max_len: a bound on seq_lens (0: acc's slots or
-    the page table's capacity, the fewer); one near the lengths is faster.  workspace: a uint8 tensor of mkv_paged_evict_workspace bytes (None:
-    taken from torch's allocator).  Returns src."""
+    the pages: the pages of a sequence that is cut must be its own (copy a common prefix first).
+    acc (fp32), pos (int32) [batch, kv_heads, slots]; acc_out and pos_out [batch, kv_heads,
+    slots_out] (None: in place, acc and pos themselves); seq_lens, next_pos int32 [batch]; lens_out
+    int32 [batch] (None: seq_lens); src int32 [batch, kv_heads, budget] (new where None): the slot
+    each kept token came from.  max_len: a bound on seq_lens (0: acc's slots or the page table's
+    capacity, the fewer); one near the lengths is faster.  workspace: a uint8 tensor of
+    mkv_paged_evict_workspace bytes (None: taken from torch's allocator).  Returns src."""
     if src is None:
         v = cache.view
         src = _new((v.batch, v.n_kv_heads, max(0, budget)), _T.int32, cache.device, stream)
