@@ -623,7 +623,8 @@ uint64_t mkv_paged_evict_workspace(const mkv_paged_cache* cache, const mkv_paged
  * reports it.  Copy pages in common (a prefix) and point the table at the
  * copies first.
  * A row whose old or new page lies outside the cache is not moved, which
- * `status` reports; src, acc_out and pos_out name its token all the same.  A length outside 0 .. max_len counts as the nearer bound. */
+ * `status` reports; src, acc_out and pos_out name its token all the same.  A
+ * length outside 0 .. max_len counts as the nearer bound. */
 mkv_status mkv_paged_evict(const mkv_paged_cache* cache, const mkv_paged_evict_args* args,
                            mkv_stream_t stream);
 
