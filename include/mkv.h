@@ -635,6 +635,183 @@ mkv_status mkv_paged_evict(const mkv_paged_cache* cache, const mkv_paged_evict_a
  * both happened, mkv_last_error_string names both. */
 mkv_status mkv_paged_check(int32_t* status);
 
+/* ---------------------------------------------------------------------------
+ * Between a model's projections and the two caches: rotary positions with
+ * several axes, norms of query and key heads with their rotation, attention of
+ * prompts, and of several new tokens over the paged cache.  The conventions of
+ * the paged calls above hold here too.
+ * ------------------------------------------------------------------------- */
+
+#define MKV_ROPE_MAX_AXES 4
+enum {
+  MKV_AXES_BLOCKS = 0,  /* the first sections[0] pairs turn by axis 0, the next by axis 1, ... */
+  MKV_AXES_CYCLIC = 1   /* pairs are dealt to the axes in turn; one that has its share is passed over */
+};
+
+/* Which axis' position each pair turns by. */
+typedef struct {
+  int32_t n_axes;                      /* 1..MKV_ROPE_MAX_AXES */
+  uint8_t axis[MKV_ROPE_MAX_PAIRS];
+} mkv_rope_axes;
+
+/* A rotation with several axes (time, height and width of pictures and video):
+ * axis a turns sections[a] >= 1 pairs, together rot_dim / 2.  restart 0: pair i
+ * has the frequency of pair i of a plan without axes; 1: the pairs of an axis
+ * have those of a plan with rot_dim = 2 sections[a] of their own.  Host only. */
+mkv_status mkv_rope_axes_init(const mkv_rope_config* cfg, const int32_t* sections, int32_t n_axes, int32_t order,
+                              int32_t restart, mkv_rope_plan* plan, mkv_rope_axes* axes);
+
+/* mkv_rope with several axes.  args->pos: device [n_axes][batch][tokens], never
+ * NULL, pos_axis_stride elements between axes; args->first_pos is not used. */
+mkv_status mkv_rope_multi(const mkv_rope_plan* plan, const mkv_rope_axes* axes, const mkv_rope_args* args,
+                          int64_t pos_axis_stride, mkv_stream_t stream);
+
+typedef struct {
+  /* [0]: queries, [1]: keys, which may be left out (x[1] NULL, heads[1] 0) */
+  const void* x[2];          /* device [batch][tokens][heads][head_dim] of `dtype` */
+  void* out[2];              /* device, the same shape; may be x (or grad) with the same strides */
+  const void* grad[2];       /* mkv_norm_rope_grad: device, the gradient of the forward call's out */
+  const void* weight[2];     /* device [head_dim] of weight_dtype, or NULL: 1 (weight_offset is not added then) */
+  float* weight_grad[2];     /* mkv_norm_rope_grad: device [head_dim], written, or NULL */
+  const int32_t* pos;        /* device [n_axes][batch][tokens], or NULL (without axes): first_pos + token */
+  void* workspace;           /* mkv_norm_rope_grad with a weight_grad: 16-byte aligned device memory */
+  uint64_t workspace_bytes;
+  int64_t x_stride[2][3];    /* elements between batches, tokens, heads, as in mkv_rope_args */
+  int64_t out_stride[2][3];
+  int64_t grad_stride[2][3];
+  int64_t pos_stride;        /* elements between the batches of pos, */
+  int64_t pos_axis_stride;   /* and between its axes */
+  int64_t tokens;            /* >= 0 */
+  int32_t batch;             /* 0..65535 */
+  int32_t heads[2];          /* 0..65535 */
+  int32_t dtype;             /* MKV_DT_F16, BF16 or F32 */
+  int32_t weight_dtype;      /* dtype or MKV_DT_F32 */
+  int32_t first_pos;
+  float eps;                 /* >= 0 */
+  float weight_offset;       /* added to the weights: 0, or 1 where they are kept as the difference from 1 */
+} mkv_norm_rope_args;
+
+/* RMS norm of every query and key head and its rotation in one pass:
+ *   y = R(pos) (x r (weight + weight_offset)),  r = 1 / sqrt(mean(x^2) + eps),
+ * the mean over all head_dim elements (head_dim <= 256), R as in mkv_rope with
+ * `plan` (and `axes`, or NULL: one axis).  Computed in fp32, rounded once.  A head
+ * of zeros with eps = 0 is a division by zero. */
+mkv_status mkv_norm_rope(const mkv_rope_plan* plan, const mkv_rope_axes* axes, const mkv_norm_rope_args* args,
+                         mkv_stream_t stream);
+
+/* Gradients of mkv_norm_rope.  With u = R(pos)^T grad, e = u (weight + offset),
+ * n = x r:  out = r (e - n mean(e n)), weight_grad = the sum of u n over all
+ * tokens and heads.  n is formed again from x, nothing has to be kept.  The sums
+ * have a fixed order: the same call gives the same bits on the same GPU. */
+mkv_status mkv_norm_rope_grad(const mkv_rope_plan* plan, const mkv_rope_axes* axes, const mkv_norm_rope_args* args,
+                              mkv_stream_t stream);
+/* Bytes of workspace of that call: 0 without a weight_grad, and for invalid arguments. */
+uint64_t mkv_norm_rope_grad_workspace(const mkv_rope_plan* plan, const mkv_norm_rope_args* args);
+
+/* How scores are formed, here and in mkv_paged_attend, of a query at place p and
+ * a key at place j of its sequence:
+ *   z = scale q . k;  with cap: z = cap tanh(z / cap);  with slopes: z -= slope |p - j|. */
+typedef struct {
+  const void* q;             /* device [batch][q_tokens][n_q_heads][head_dim] of `dtype`, 16-byte aligned */
+  const void* k;             /* device [batch][kv_tokens][n_kv_heads][head_dim] */
+  const void* v;
+  void* out;                 /* device, q's shape */
+  float* lse;                /* device [batch][q_tokens][n_q_heads], or NULL: ln of the sum of exp(z) */
+  const int32_t* q_lens;     /* device [batch]: queries of each sequence, or NULL: q_tokens */
+  const int32_t* kv_lens;    /* device [batch]: keys of each sequence, or NULL: kv_tokens */
+  const int32_t* prefix;     /* device [batch], or NULL: with `causal`, the first prefix[b] keys are seen by all
+                                queries */
+  const int32_t* docs;       /* device [batch][kv_tokens], or NULL: the document of each place (any numbers, in
+                                any order); keys of other documents than the query's are not seen */
+  const float* slopes;       /* device [n_q_heads], or NULL */
+  void* workspace;           /* device, 16-byte aligned, of mkv_prefill_workspace bytes (NULL where that is 0) */
+  uint64_t workspace_bytes;
+  int64_t q_stride[3];       /* elements between batches, tokens, heads: positive multiples of 8 where the */
+  int64_t k_stride[3];       /* extent > 1 */
+  int64_t v_stride[3];
+  int64_t out_stride[3];
+  int64_t docs_stride;       /* elements between the batches of docs */
+  int64_t q_tokens;          /* 0..2^30 */
+  int64_t kv_tokens;         /* 0..2^30 */
+  int32_t batch;             /* 0..65535 */
+  int32_t n_q_heads;         /* a multiple of n_kv_heads; at most 128 per KV head */
+  int32_t n_kv_heads;        /* 1..65535 */
+  int32_t head_dim;          /* 64, 128 or 256 */
+  int32_t dtype;             /* MKV_DT_F16 or BF16 */
+  int32_t causal;            /* 1: key j is seen from p >= j; 0: from everywhere */
+  int32_t window;            /* > 0: only keys with p - j < window (and, without causal, j - p < window) */
+  float scale;               /* > 0; 0: 1 / sqrt(head_dim) */
+  float cap;                 /* > 0: scores are capped; 0: not */
+} mkv_prefill_args;
+
+/* Bytes of workspace of mkv_prefill with these arguments on the current device
+ * (pointers are not looked at, except whether docs is NULL), or UINT64_MAX for
+ * invalid ones.  0 is enough for most calls. */
+uint64_t mkv_prefill_workspace(const mkv_prefill_args* args);
+
+/* Attention of a prompt, or of a part of one over what came before it: softmax of
+ * the scores over the keys that a query sees, weighted sum of v.  Query i of a
+ * sequence with n queries and m keys stands at place p = m - n + i of the keys:
+ * the last query at the last key.  From p < 0 only the prefix is seen with
+ * `causal`, and nothing with docs.  Query head i reads KV head i / g, g =
+ * n_q_heads / n_kv_heads.  A query that sees no key gives zeros and an lse of
+ * -inf.  Rows of out and lse behind a sequence's queries are left as
+ * they were, and keys and values behind its keys may hold anything.
+ * Lengths outside 0..q_tokens or 0..kv_tokens count as the nearer bound.
+ * Scores, their sums and the sum of values are in fp32; the weights are rounded
+ * to `dtype` for the product with v.  A value row with an infinity or a NaN may
+ * make that channel non-finite for queries that do not see it too.  Results do not
+ * depend on timing.  Overlap of out with an input is not allowed. */
+mkv_status mkv_prefill(const mkv_prefill_args* args, mkv_stream_t stream);
+
+typedef struct {
+  const void* q;             /* device [batch][n][n_q_heads][head_dim], 16-byte aligned; F16 or BF16, the cache's
+                                type unless that is E4M3 */
+  void* out;                 /* device, the same shape and type, contiguous, 16-byte aligned */
+  float* lse;                /* device [batch][n][n_q_heads], or NULL */
+  const int32_t* seq_lens;   /* device [batch]: cached tokens with the new ones, 0 .. max_len */
+  const int32_t* new_lens;   /* device [batch]: new tokens of each sequence, 0 .. n, or NULL: n, or seq_lens[b]
+                                where that is less */
+  const uint64_t* tree;      /* device [batch][n], n <= 64: bit j of row i: new token i sees new token j; or
+                                NULL: i sees j <= i */
+  const float* slopes;       /* device [n_q_heads], or NULL */
+  void* workspace;           /* device, 16-byte aligned, of mkv_paged_attend_workspace bytes */
+  uint64_t workspace_bytes;
+  int64_t q_stride[3];       /* elements between sequences, tokens, heads: positive multiples of 8 where the
+                                extent > 1 */
+  int64_t max_len;           /* bound on seq_lens; 0: max_pages * page_size.  How the work is split goes by it */
+  int32_t n;                 /* new tokens of the longest row, 0..65535 */
+  int32_t n_q_heads;         /* a multiple of n_kv_heads; at most 128 per KV head */
+  int32_t q_dtype;
+  int32_t window;            /* > 0: only keys with p - j < window */
+  float scale;
+  float cap;
+} mkv_paged_attend_args;
+
+/* Bytes of workspace of mkv_paged_attend on the current device, or UINT64_MAX for
+ * invalid arguments. */
+uint64_t mkv_paged_attend_workspace(const mkv_paged_cache* cache, const mkv_paged_attend_args* args);
+
+/* Attention of several new tokens per sequence over its cached tokens: a prompt's
+ * next part, a chain of drafts, a tree of them, or (n = 1) single tokens with
+ * capped or biased scores or a window, which mkv_paged_decode does not have.  The
+ * new tokens' own rows are in the cache already (mkv_paged_append): new token i of
+ * a sequence with m of them and length L lies in slot L - m + i.  All slots before
+ * L - m are seen by all new tokens; of the new ones, token i sees those that its
+ * row of `tree` names, itself only if its own bit is set (bits from m on do not
+ * count).  Place of slot t < L - m: t; of new token i in a tree: L - m + the
+ * number of other new tokens that it sees (its depth, where rows name ancestors);
+ * else its slot.  Slots that mkv_paged_evict has moved have no order: use window
+ * and slopes on sequences that were never cut.
+ * The scores as above, softmax and weighted sum in fp32, weights rounded to 16
+ * bits for the product with v.  E4M3 caches: rows are widened to fp16, and q too,
+ * scaled by a power of two for each head.  A new token that sees nothing gives
+ * zeros and an lse of -inf; rows of out and lse from m on are left as they were.
+ * Lengths outside their bounds count as the nearer one, new_lens above seq_lens as that, a page
+ * outside the cache as absent tokens; these are reported in `status`.  Slots at or
+ * behind seq_lens[b] may hold anything.  Results do not depend on timing. */
+mkv_status mkv_paged_attend(const mkv_paged_cache* cache, const mkv_paged_attend_args* args, mkv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -14,130 +14,25 @@
 // heads it handles.
 #include "decode_common.cuh"
 #include "paged_internal.cuh"
+#include "rope_common.cuh"
 
 namespace mkv {
 namespace {
 
 constexpr int RT = 256;   // threads per block
 
-struct alignas(16) Vec16 {
-  uint32_t w[4];
-};
-
-template <typename T>
-struct Elem;
-template <>
-struct Elem<__half> {
-  static constexpr int V = 8;
-  static __device__ __forceinline__ void unpack(const Vec16& v, float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&v.w[i]));
-      f[2 * i] = t.x;
-      f[2 * i + 1] = t.y;
-    }
-  }
-  static __device__ __forceinline__ Vec16 pack(const float (&f)[8]) {
-    Vec16 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-      v.w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return v;
-  }
-  static __device__ __forceinline__ float get(__half x) { return __half2float(x); }
-  static __device__ __forceinline__ __half put(float x) { return __float2half_rn(x); }
-};
-template <>
-struct Elem<__nv_bfloat16> {
-  static constexpr int V = 8;
-  static __device__ __forceinline__ void unpack(const Vec16& v, float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(v.w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(v.w[i] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ Vec16 pack(const float (&f)[8]) {
-    Vec16 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      v.w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return v;
-  }
-  static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
-  static __device__ __forceinline__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
-};
-template <>
-struct Elem<float> {
-  static constexpr int V = 4;
-  static __device__ __forceinline__ void unpack(const Vec16& v, float (&f)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v.w[i]);
-  }
-  static __device__ __forceinline__ Vec16 pack(const float (&f)[4]) {
-    Vec16 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v.w[i] = __float_as_uint(f[i]);
-    return v;
-  }
-  static __device__ __forceinline__ float get(float x) { return x; }
-  static __device__ __forceinline__ float put(float x) { return x; }
-};
-
-// m * (cos, sin) of position * turn.
-__device__ __forceinline__ void angle(int32_t pos, uint64_t turn, float mult, float sin_mult,
-                                      float& c, float& s) {
-  const uint64_t phase = (uint64_t)(int64_t)pos * turn;
-  const float half_turns = (float)(int32_t)(uint32_t)(phase >> 32) * 4.656612873077393e-10f;  // 2^-31
-  sincospif(half_turns, &s, &c);
-  c *= mult;
-  s *= sin_mult;
-}
-
-// Angles of one thread's unit: V pairs (half pairs: two vectors of V elements,
-// rot/2 apart) or V/2 pairs (interleaved: one vector).
+// Angles of NP pairs from `first` on of token t: the position is the token's, or,
+// with axes, that of each pair's own axis (all read first, then chosen from).
 template <int NP>
-__device__ __forceinline__ void angles(const mkv_rope_plan& plan, int first, int32_t pos, float sign,
-                                       float (&c)[NP], float (&s)[NP]) {
-#pragma unroll
-  for (int i = 0; i < NP; ++i) angle(pos, plan.turn[first + i], plan.mult, plan.mult * sign, c[i], s[i]);
+__device__ __forceinline__ void unit_angles(const RopeParams& p, int first, int b, int64_t t, float (&c)[NP],
+                                            float (&s)[NP]) {
+  const int32_t pos = p.pos ? p.pos[b * p.pos_stride + t] : (int32_t)(p.first_pos + t);
+  angles<NP>(p.plan, first, pos, p.sign, c, s);
 }
-
-template <int V>
-__device__ __forceinline__ void turn_half(float (&a)[V], float (&b)[V], const float (&c)[V],
-                                          const float (&s)[V]) {
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const float x = a[i], y = b[i];
-    a[i] = x * c[i] - y * s[i];
-    b[i] = x * s[i] + y * c[i];
-  }
-}
-template <int V>
-__device__ __forceinline__ void turn_inter(float (&a)[V], const float (&c)[V / 2],
-                                           const float (&s)[V / 2]) {
-#pragma unroll
-  for (int i = 0; i < V / 2; ++i) {
-    const float x = a[2 * i], y = a[2 * i + 1];
-    a[2 * i] = x * c[i] - y * s[i];
-    a[2 * i + 1] = x * s[i] + y * c[i];
-  }
-}
-
-// i / units and i % units of a 64-bit i; nearly always in 32 bits.
-__device__ __forceinline__ void split_index(int64_t i, int units, int64_t& q, int& r) {
-  if (i < (int64_t)1 << 32) {
-    const uint32_t u = (uint32_t)i;
-    q = u / (uint32_t)units;
-    r = (int)(u - (uint32_t)q * (uint32_t)units);
-  } else {
-    q = i / units;
-    r = (int)(i - q * units);
-  }
+template <int NP>
+__device__ __forceinline__ void unit_angles(const RopeMultiParams& p, int first, int b, int64_t t, float (&c)[NP],
+                                            float (&s)[NP]) {
+  axes_angles<NP>(p.plan, p.axes, p.pos + b * p.pos_stride + t, p.pos_axis_stride, first, p.sign, c, s);
 }
 
 // One unit (first vector at e0; half pairs: second at e1) of HB heads at a time,
@@ -184,8 +79,8 @@ __device__ __forceinline__ void turn_heads(int h0, int h1, bool turns, const flo
 // us in a graph, a launch.
 // grid: (ceil(tokens * units / 256), ceil(heads / heads_per), batch)
 // ---------------------------------------------------------------------------
-template <typename T, bool HALF>
-__global__ void __launch_bounds__(RT) rope_vec_kernel(const __grid_constant__ RopeParams p) {
+template <typename T, bool HALF, typename P>
+__global__ void __launch_bounds__(RT) rope_vec_kernel(const __grid_constant__ P p) {
   griddep_wait();
   griddep_launch();
   constexpr int V = Elem<T>::V, NP = HALF ? V : V / 2;
@@ -200,10 +95,7 @@ __global__ void __launch_bounds__(RT) rope_vec_kernel(const __grid_constant__ Ro
   T* o = static_cast<T*>(p.out) + b * p.os[0] + t * p.os[1];
   const bool turns = u < p.rot_units;
   float c[NP], s[NP];
-  if (turns) {
-    const int32_t pos = p.pos ? p.pos[b * p.pos_stride + t] : (int32_t)(p.first_pos + t);
-    angles<NP>(p.plan, u * NP, pos, p.sign, c, s);
-  }
+  if (turns) unit_angles<NP>(p, u * NP, b, t, c, s);
   const int e0 = turns ? u * V : p.plan.rot_dim + (u - p.rot_units) * V, e1 = e0 + p.plan.rot_dim / 2;
   const int64_t xh = p.xs[2], oh = p.os[2];
   turn_heads<T, HALF>(
@@ -223,8 +115,8 @@ __global__ void __launch_bounds__(RT) rope_vec_kernel(const __grid_constant__ Ro
 // a time, bound it: 4 x 32768 tokens of 8 fp16 heads of 128 off a 16-byte boundary
 // take 169 us, 3.2 TB/s (80 us on one); heads of 80 with 40 in half pairs 179 us,
 // 1.9 TB/s (all 80: 54).
-template <typename T>
-__global__ void __launch_bounds__(RT) rope_elem_kernel(const __grid_constant__ RopeParams p) {
+template <typename T, typename P>
+__global__ void __launch_bounds__(RT) rope_elem_kernel(const __grid_constant__ P p) {
   griddep_wait();
   griddep_launch();
   using E = Elem<T>;
@@ -241,9 +133,9 @@ __global__ void __launch_bounds__(RT) rope_elem_kernel(const __grid_constant__ R
     for (int h = h0; h < h1; ++h) o[h * p.os[2] + e] = x[h * p.xs[2] + e];
     return;
   }
-  const int32_t pos = p.pos ? p.pos[b * p.pos_stride + t] : (int32_t)(p.first_pos + t);
-  float c, s;
-  angle(pos, p.plan.turn[u], p.plan.mult, p.plan.mult * p.sign, c, s);
+  float ca[1], sa[1];
+  unit_angles<1>(p, u, b, t, ca, sa);
+  const float c = ca[0], s = sa[0];
   const int e0 = p.plan.interleaved ? 2 * u : u;
   const int e1 = p.plan.interleaved ? 2 * u + 1 : u + p.plan.rot_dim / 2;
   for (int h = h0; h < h1; ++h) {
@@ -253,13 +145,13 @@ __global__ void __launch_bounds__(RT) rope_elem_kernel(const __grid_constant__ R
   }
 }
 
-template <typename T>
-cudaError_t launch_rope_t(const RopeParams& p, bool vec, cudaStream_t st) {
+template <typename T, typename P>
+cudaError_t launch_rope_t(const P& p, bool vec, cudaStream_t st) {
   const int64_t blocks = (p.tokens * p.units + RT - 1) / RT;
   const dim3 grid((unsigned)blocks, (p.heads + p.heads_per - 1) / p.heads_per, p.batch);
-  if (!vec) return launch_kernel(rope_elem_kernel<T>, grid, dim3(RT), 0, st, true, 0, p);
-  if (p.plan.interleaved) return launch_kernel(rope_vec_kernel<T, false>, grid, dim3(RT), 0, st, true, 0, p);
-  return launch_kernel(rope_vec_kernel<T, true>, grid, dim3(RT), 0, st, true, 0, p);
+  if (!vec) return launch_kernel(rope_elem_kernel<T, P>, grid, dim3(RT), 0, st, true, 0, p);
+  if (p.plan.interleaved) return launch_kernel(rope_vec_kernel<T, false, P>, grid, dim3(RT), 0, st, true, 0, p);
+  return launch_kernel(rope_vec_kernel<T, true, P>, grid, dim3(RT), 0, st, true, 0, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -425,12 +317,21 @@ cudaError_t launch_append_t(const AppendRowsParams& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeParams& p, int dtype, bool vec, cudaStream_t st) {
+namespace {
+template <typename P>
+cudaError_t launch_rope_p(const P& p, int dtype, bool vec, cudaStream_t st) {
   switch (dtype) {
     case MKV_DT_F16: return launch_rope_t<__half>(p, vec, st);
     case MKV_DT_BF16: return launch_rope_t<__nv_bfloat16>(p, vec, st);
     default: return launch_rope_t<float>(p, vec, st);
   }
+}
+}  // namespace
+cudaError_t launch_rope(const RopeParams& p, int dtype, bool vec, cudaStream_t st) {
+  return launch_rope_p(p, dtype, vec, st);
+}
+cudaError_t launch_rope_multi(const RopeMultiParams& p, int dtype, bool vec, cudaStream_t st) {
+  return launch_rope_p(p, dtype, vec, st);
 }
 
 cudaError_t launch_append_rows(const AppendRowsParams& p, cudaStream_t st) {

@@ -1,38 +1,21 @@
 // Host side of the rotary and paged-cache calls in include/mkv.h: argument
 // checks, workspace layout and launch order.  No state is kept between calls.
-#include <algorithm>
-#include <cmath>
 #include <cstdio>
-#include <cstring>
 
 #include <cudaTypedefs.h>
 
-#include "paged_internal.cuh"
+#include "api_common.cuh"
 
 using namespace mkv;
 
 namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
-constexpr int64_t kMaxGrid = 0x7fffffff;
 
-#define CKP(call)                                              \
-  do {                                                         \
-    cudaError_t e_ = (call);                                   \
-    if (e_ != cudaSuccess) return set_cuda_error(e_, #call);   \
-  } while (0)
+}  // namespace
 
-mkv_status bad(const char* text) { return set_error(MKV_ERR_INVALID_ARG, text); }
+namespace mkv {
 
-int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool is16(int dtype) { return dtype == MKV_DT_F16 || dtype == MKV_DT_BF16; }
-// Stride of a dimension that is walked over: 16-byte accesses need multiples of 8
-// elements.  That of an extent of 1 is never used.
-bool stride8(int64_t stride, int64_t extent) { return extent <= 1 || stride % 8 == 0; }
-int elem_bytes(int dtype) { return dtype == MKV_DT_F32 ? 4 : dtype == MKV_DT_E4M3 ? 1 : 2; }
-
-// SMs of the current device.
 mkv_status sm_count(int* out) {
   int dev = 0;
   CKP(cudaGetDevice(&dev));
@@ -40,9 +23,8 @@ mkv_status sm_count(int* out) {
   return MKV_OK;
 }
 
-// Heads a thread takes so that its angles serve several heads while the grid
-// still has at least `want` threads: a 32K prefill of 8 heads takes 170, 100, 83
-// and 81 us with 1, 2, 4 and 8, one step of 8 x 32 heads 2.4 us with 1, 3.5 with 8.
+// A 32K prefill of 8 heads takes 170, 100, 83 and 81 us with 1, 2, 4 and 8, one
+// step of 8 x 32 heads 2.4 us with 1, 3.5 with 8.
 int heads_per_thread(int64_t threads, int heads, int64_t want, int most) {
   int per = 1;
   while (per < most && per < heads && threads * up(heads, 2 * per) >= want) per *= 2;
@@ -78,6 +60,17 @@ const char* check_cache(const mkv_paged_cache* c) {
     return "paged cache: too many pages (n_pages * n_kv_heads * page_size must be below 2^31)";
   return nullptr;
 }
+
+const char* check_axes(const mkv_rope_axes* x, const mkv_rope_plan* p) {
+  if (x->n_axes < 1 || x->n_axes > MKV_ROPE_MAX_AXES) return "the rope axes were not made by mkv_rope_axes_init";
+  for (int i = 0; p && i < p->rot_dim / 2 && i < MKV_ROPE_MAX_PAIRS; ++i)
+    if (x->axis[i] >= x->n_axes) return "the rope axes were not made by mkv_rope_axes_init";
+  return nullptr;
+}
+
+}  // namespace mkv
+
+namespace {
 
 // ---- decode ------------------------------------------------------------------
 
@@ -226,6 +219,124 @@ const char* check_evict(const mkv_paged_cache* c, const mkv_paged_evict_args* a)
   return nullptr;
 }
 
+// ---- rope --------------------------------------------------------------------
+
+const char* check_rope_config(const mkv_rope_config& c) {
+  if (c.head_dim < 1 || c.head_dim > 4096) return "mkv_rope_plan_init: head_dim must be 1..4096";
+  if (c.rot_dim < 2 || c.rot_dim % 2 != 0 || c.rot_dim > c.head_dim || c.rot_dim > 2 * MKV_ROPE_MAX_PAIRS)
+    return "mkv_rope_plan_init: rot_dim must be even, 2..min(head_dim, 256)";
+  if (c.interleaved < 0 || c.interleaved > 1) return "mkv_rope_plan_init: interleaved must be 0 or 1";
+  if (c.scaling < MKV_ROPE_NONE || c.scaling > MKV_ROPE_BANDED) return "mkv_rope_plan_init: unknown scaling";
+  if (!(c.base > 1.0) || !std::isfinite(c.base)) return "mkv_rope_plan_init: base must be > 1 and finite";
+  if (c.scaling != MKV_ROPE_NONE && (!(c.factor >= 1.0) || !std::isfinite(c.factor)))
+    return "mkv_rope_plan_init: factor must be >= 1 and finite";
+  if (c.scaling == MKV_ROPE_NTK && c.rot_dim < 4) return "mkv_rope_plan_init: NTK scaling needs rot_dim >= 4";
+  if (c.scaling >= MKV_ROPE_YARN && (!(c.original > 0.0) || !std::isfinite(c.original)))
+    return "mkv_rope_plan_init: original must be > 0 and finite";
+  if (c.scaling == MKV_ROPE_YARN &&
+      (!(c.beta_slow > 0.0) || !(c.beta_fast >= c.beta_slow) || !std::isfinite(c.beta_fast)))
+    return "mkv_rope_plan_init: beta_fast >= beta_slow > 0";
+  if (c.scaling == MKV_ROPE_BANDED &&
+      (!(c.low_freq > 0.0) || !(c.high_freq > c.low_freq) || !std::isfinite(c.high_freq)))
+    return "mkv_rope_plan_init: 0 < low_freq < high_freq";
+  if (!(c.attn_factor >= 0.0) || !std::isfinite((float)c.attn_factor))
+    return "mkv_rope_plan_init: attn_factor must be >= 0 and finite";
+  return nullptr;
+}
+
+// Turns per position, times 2^64, of `pairs` pairs whose frequencies are those of a
+// rotation of 2 * pairs elements; *mult: the factor on rotated elements.
+void fill_turns(const mkv_rope_config& c, int pairs, uint64_t* turn, float* mult_out) {
+  const double n = 2.0 * pairs;
+  double base = c.base, mult = 1.0;
+  if (c.scaling == MKV_ROPE_NTK) base *= std::pow(c.factor, n / (n - 2.0));
+  if (c.scaling == MKV_ROPE_YARN) mult = 0.1 * std::log(c.factor) + 1.0;
+  if (c.attn_factor > 0.0) mult = c.attn_factor;
+  *mult_out = (float)mult;
+  // YaRN: index of the pair that turns `turns` times over the original context
+  auto pair_of = [&](double turns) {
+    return n * std::log(c.original / (turns * kTwoPi)) / (2.0 * std::log(c.base));
+  };
+  double lo = 0.0, hi = 1.0;
+  if (c.scaling == MKV_ROPE_YARN) {
+    lo = std::max(0.0, std::floor(pair_of(c.beta_fast)));
+    hi = std::min(n - 1.0, std::ceil(pair_of(c.beta_slow)));
+  }
+  for (int i = 0; i < pairs; ++i) {
+    double f = std::pow(base, -2.0 * i / n);
+    if (c.scaling == MKV_ROPE_LINEAR) {
+      f /= c.factor;
+    } else if (c.scaling == MKV_ROPE_YARN) {
+      const double ramp = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
+      f = f * (1.0 - ramp) + f / c.factor * ramp;
+    } else if (c.scaling == MKV_ROPE_BANDED) {
+      const double turns = c.original * f / kTwoPi;   // original / wavelength
+      const double keep =
+          std::min(1.0, std::max(0.0, (turns - c.low_freq) / (c.high_freq - c.low_freq)));
+      f = f * keep + f / c.factor * (1.0 - keep);
+    }
+    // f <= 1 radian, so the fraction of a turn is below 2^62 of 2^64
+    turn[i] = (uint64_t)std::llround(std::ldexp(f / kTwoPi, 64));
+  }
+}
+
+// Checks a rotation's arguments and fills its parameters; *vec: 16-byte accesses fit.
+// p->tokens stays 0 where there is nothing to do.
+mkv_status rope_params(const mkv_rope_plan* plan, const mkv_rope_args* a, RopeParams* out, bool* vec_out) {
+  if (!plan || !a) return bad("mkv_rope: NULL plan or arguments");
+  if (const char* e = check_plan(plan)) return bad(e);
+  if (a->batch < 0 || a->heads < 0 || a->tokens < 0) return bad("mkv_rope: negative size");
+  if (a->batch > 65535 || a->heads > 65535) return bad("mkv_rope: batch and heads must be <= 65535");
+  if (a->dtype != MKV_DT_F16 && a->dtype != MKV_DT_BF16 && a->dtype != MKV_DT_F32)
+    return bad("mkv_rope: dtype must be F16, BF16 or F32");
+  if (a->transposed < 0 || a->transposed > 1) return bad("mkv_rope: transposed must be 0 or 1");
+  out->tokens = 0;
+  if (a->batch == 0 || a->heads == 0 || a->tokens == 0) return MKV_OK;
+  if (!a->x || !a->out) return bad("mkv_rope: NULL x or out");
+  if (!a->pos && (int64_t)a->first_pos + a->tokens > (int64_t)1 << 31)
+    return bad("mkv_rope: positions exceed 32 bits");
+  const int64_t extent[3] = {a->batch, a->tokens, a->heads};
+  for (int i = 0; i < 3; ++i) {
+    if (extent[i] > 1 && a->out_stride[i] <= 0) return bad("mkv_rope: out's strides must be positive");
+    if (a->x == a->out && extent[i] > 1 && a->x_stride[i] != a->out_stride[i])
+      return bad("mkv_rope: in place, x and out need the same strides");
+  }
+  const int es = elem_bytes(a->dtype), V = 16 / es;
+  const uintptr_t mask = reinterpret_cast<uintptr_t>(a->x) | reinterpret_cast<uintptr_t>(a->out);
+  if (mask & (uintptr_t)(es - 1)) return bad("mkv_rope: x and out must be aligned to their elements");
+  bool vec = (mask & 15u) == 0 && plan->head_dim % V == 0 &&
+             plan->rot_dim % (plan->interleaved ? V : 2 * V) == 0;
+  for (int i = 0; i < 3; ++i)
+    if (extent[i] > 1 && (a->x_stride[i] % V != 0 || a->out_stride[i] % V != 0)) vec = false;
+  RopeParams& p = *out;
+  p.plan = *plan;
+  p.x = a->x;
+  p.out = a->out;
+  p.pos = a->pos;
+  for (int i = 0; i < 3; ++i) p.xs[i] = a->x_stride[i], p.os[i] = a->out_stride[i];
+  p.pos_stride = a->pos_stride;
+  p.tokens = a->tokens;
+  p.batch = a->batch;
+  p.heads = a->heads;
+  p.first_pos = a->first_pos;
+  p.sign = a->transposed ? -1.f : 1.f;
+  const int rest = plan->head_dim - plan->rot_dim;
+  if (vec) {
+    p.rot_units = plan->interleaved ? plan->rot_dim / V : plan->rot_dim / (2 * V);
+    p.units = p.rot_units + rest / V;
+  } else {
+    p.rot_units = plan->rot_dim / 2;
+    p.units = p.rot_units + rest;
+  }
+  if (p.tokens > kMaxGrid / p.units * 256) return bad("mkv_rope: too many tokens");
+  int sms = 0;
+  mkv_status s = sm_count(&sms);
+  if (s != MKV_OK) return s;
+  p.heads_per = heads_per_thread((int64_t)a->batch * a->tokens * p.units, a->heads, (int64_t)sms * 2048, 8);
+  *vec_out = vec;
+  return MKV_OK;
+}
+
 }  // namespace
 
 namespace mkv {
@@ -260,117 +371,73 @@ extern "C" {
 
 mkv_status mkv_rope_plan_init(const mkv_rope_config* cfg, mkv_rope_plan* plan) {
   if (!cfg || !plan) return bad("mkv_rope_plan_init: NULL argument");
-  const mkv_rope_config& c = *cfg;
-  if (c.head_dim < 1 || c.head_dim > 4096) return bad("mkv_rope_plan_init: head_dim must be 1..4096");
-  if (c.rot_dim < 2 || c.rot_dim % 2 != 0 || c.rot_dim > c.head_dim || c.rot_dim > 2 * MKV_ROPE_MAX_PAIRS)
-    return bad("mkv_rope_plan_init: rot_dim must be even, 2..min(head_dim, 256)");
-  if (c.interleaved < 0 || c.interleaved > 1) return bad("mkv_rope_plan_init: interleaved must be 0 or 1");
-  if (c.scaling < MKV_ROPE_NONE || c.scaling > MKV_ROPE_BANDED) return bad("mkv_rope_plan_init: unknown scaling");
-  if (!(c.base > 1.0) || !std::isfinite(c.base)) return bad("mkv_rope_plan_init: base must be > 1 and finite");
-  if (c.scaling != MKV_ROPE_NONE && (!(c.factor >= 1.0) || !std::isfinite(c.factor)))
-    return bad("mkv_rope_plan_init: factor must be >= 1 and finite");
-  if (c.scaling == MKV_ROPE_NTK && c.rot_dim < 4) return bad("mkv_rope_plan_init: NTK scaling needs rot_dim >= 4");
-  if (c.scaling >= MKV_ROPE_YARN && (!(c.original > 0.0) || !std::isfinite(c.original)))
-    return bad("mkv_rope_plan_init: original must be > 0 and finite");
-  if (c.scaling == MKV_ROPE_YARN &&
-      (!(c.beta_slow > 0.0) || !(c.beta_fast >= c.beta_slow) || !std::isfinite(c.beta_fast)))
-    return bad("mkv_rope_plan_init: beta_fast >= beta_slow > 0");
-  if (c.scaling == MKV_ROPE_BANDED &&
-      (!(c.low_freq > 0.0) || !(c.high_freq > c.low_freq) || !std::isfinite(c.high_freq)))
-    return bad("mkv_rope_plan_init: 0 < low_freq < high_freq");
-  if (!(c.attn_factor >= 0.0) || !std::isfinite((float)c.attn_factor))
-    return bad("mkv_rope_plan_init: attn_factor must be >= 0 and finite");
-
+  if (const char* e = check_rope_config(*cfg)) return bad(e);
   std::memset(plan, 0, sizeof(*plan));
-  plan->head_dim = c.head_dim;
-  plan->rot_dim = c.rot_dim;
-  plan->interleaved = c.interleaved;
-  const double n = c.rot_dim;
-  double base = c.base, mult = 1.0;
-  if (c.scaling == MKV_ROPE_NTK) base *= std::pow(c.factor, n / (n - 2.0));
-  if (c.scaling == MKV_ROPE_YARN) mult = 0.1 * std::log(c.factor) + 1.0;
-  if (c.attn_factor > 0.0) mult = c.attn_factor;
-  plan->mult = (float)mult;
-  // YaRN: index of the pair that turns `turns` times over the original context
-  auto pair_of = [&](double turns) {
-    return n * std::log(c.original / (turns * kTwoPi)) / (2.0 * std::log(c.base));
-  };
-  double lo = 0.0, hi = 1.0;
-  if (c.scaling == MKV_ROPE_YARN) {
-    lo = std::max(0.0, std::floor(pair_of(c.beta_fast)));
-    hi = std::min(n - 1.0, std::ceil(pair_of(c.beta_slow)));
+  plan->head_dim = cfg->head_dim;
+  plan->rot_dim = cfg->rot_dim;
+  plan->interleaved = cfg->interleaved;
+  fill_turns(*cfg, cfg->rot_dim / 2, plan->turn, &plan->mult);
+  return MKV_OK;
+}
+
+mkv_status mkv_rope_axes_init(const mkv_rope_config* cfg, const int32_t* sections, int32_t n_axes, int32_t order,
+                              int32_t restart, mkv_rope_plan* plan, mkv_rope_axes* axes) {
+  if (!cfg || !sections || !plan || !axes) return bad("mkv_rope_axes_init: NULL argument");
+  if (const char* e = check_rope_config(*cfg)) return bad(e);
+  if (n_axes < 1 || n_axes > MKV_ROPE_MAX_AXES) return bad("mkv_rope_axes_init: 1 to 4 axes");
+  if (order != MKV_AXES_BLOCKS && order != MKV_AXES_CYCLIC) return bad("mkv_rope_axes_init: unknown order");
+  if (restart < 0 || restart > 1) return bad("mkv_rope_axes_init: restart must be 0 or 1");
+  int64_t sum = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (sections[a] < 1) return bad("mkv_rope_axes_init: every axis needs a pair");
+    if (restart && cfg->scaling == MKV_ROPE_NTK && sections[a] < 2)
+      return bad("mkv_rope_axes_init: NTK scaling needs two pairs an axis");
+    sum += sections[a];
   }
-  for (int i = 0; i < c.rot_dim / 2; ++i) {
-    double f = std::pow(base, -2.0 * i / n);
-    if (c.scaling == MKV_ROPE_LINEAR) {
-      f /= c.factor;
-    } else if (c.scaling == MKV_ROPE_YARN) {
-      const double ramp = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
-      f = f * (1.0 - ramp) + f / c.factor * ramp;
-    } else if (c.scaling == MKV_ROPE_BANDED) {
-      const double turns = c.original * f / kTwoPi;   // original / wavelength
-      const double keep =
-          std::min(1.0, std::max(0.0, (turns - c.low_freq) / (c.high_freq - c.low_freq)));
-      f = f * keep + f / c.factor * (1.0 - keep);
+  if (sum != cfg->rot_dim / 2) return bad("mkv_rope_axes_init: the sections must add up to rot_dim / 2");
+  if (mkv_status s = mkv_rope_plan_init(cfg, plan)) return s;
+  std::memset(axes, 0, sizeof(*axes));
+  axes->n_axes = n_axes;
+  int left[MKV_ROPE_MAX_AXES] = {0, 0, 0, 0};
+  for (int a = 0; a < n_axes; ++a) left[a] = sections[a];
+  for (int i = 0, a = 0; i < sum; ++i) {
+    if (order == MKV_AXES_CYCLIC && i > 0) a = (a + 1) % n_axes;
+    while (left[a] == 0) a = (a + 1) % n_axes;
+    --left[a];
+    axes->axis[i] = (uint8_t)a;
+  }
+  if (restart)
+    for (int a = 0; a < n_axes; ++a) {
+      uint64_t turn[MKV_ROPE_MAX_PAIRS];
+      fill_turns(*cfg, sections[a], turn, &plan->mult);
+      for (int i = 0, k = 0; i < sum; ++i)
+        if (axes->axis[i] == a) plan->turn[i] = turn[k++];
     }
-    // f <= 1 radian, so the fraction of a turn is below 2^62 of 2^64
-    plan->turn[i] = (uint64_t)std::llround(std::ldexp(f / kTwoPi, 64));
-  }
   return MKV_OK;
 }
 
 mkv_status mkv_rope(const mkv_rope_plan* plan, const mkv_rope_args* a, mkv_stream_t stream) {
-  if (!plan || !a) return bad("mkv_rope: NULL plan or arguments");
-  if (const char* e = check_plan(plan)) return bad(e);
-  if (a->batch < 0 || a->heads < 0 || a->tokens < 0) return bad("mkv_rope: negative size");
-  if (a->batch > 65535 || a->heads > 65535) return bad("mkv_rope: batch and heads must be <= 65535");
-  if (a->dtype != MKV_DT_F16 && a->dtype != MKV_DT_BF16 && a->dtype != MKV_DT_F32)
-    return bad("mkv_rope: dtype must be F16, BF16 or F32");
-  if (a->transposed < 0 || a->transposed > 1) return bad("mkv_rope: transposed must be 0 or 1");
-  if (a->batch == 0 || a->heads == 0 || a->tokens == 0) return MKV_OK;
-  if (!a->x || !a->out) return bad("mkv_rope: NULL x or out");
-  if (!a->pos && (int64_t)a->first_pos + a->tokens > (int64_t)1 << 31)
-    return bad("mkv_rope: positions exceed 32 bits");
-  const int64_t extent[3] = {a->batch, a->tokens, a->heads};
-  for (int i = 0; i < 3; ++i) {
-    if (extent[i] > 1 && a->out_stride[i] <= 0) return bad("mkv_rope: out's strides must be positive");
-    if (a->x == a->out && extent[i] > 1 && a->x_stride[i] != a->out_stride[i])
-      return bad("mkv_rope: in place, x and out need the same strides");
-  }
-  const int es = elem_bytes(a->dtype), V = 16 / es;
-  const uintptr_t mask = reinterpret_cast<uintptr_t>(a->x) | reinterpret_cast<uintptr_t>(a->out);
-  if (mask & (uintptr_t)(es - 1)) return bad("mkv_rope: x and out must be aligned to their elements");
-  bool vec = (mask & 15u) == 0 && plan->head_dim % V == 0 &&
-             plan->rot_dim % (plan->interleaved ? V : 2 * V) == 0;
-  for (int i = 0; i < 3; ++i)
-    if (extent[i] > 1 && (a->x_stride[i] % V != 0 || a->out_stride[i] % V != 0)) vec = false;
   RopeParams p;
   std::memset(&p, 0, sizeof(p));
-  p.plan = *plan;
-  p.x = a->x;
-  p.out = a->out;
-  p.pos = a->pos;
-  for (int i = 0; i < 3; ++i) p.xs[i] = a->x_stride[i], p.os[i] = a->out_stride[i];
-  p.pos_stride = a->pos_stride;
-  p.tokens = a->tokens;
-  p.batch = a->batch;
-  p.heads = a->heads;
-  p.first_pos = a->first_pos;
-  p.sign = a->transposed ? -1.f : 1.f;
-  const int rest = plan->head_dim - plan->rot_dim;
-  if (vec) {
-    p.rot_units = plan->interleaved ? plan->rot_dim / V : plan->rot_dim / (2 * V);
-    p.units = p.rot_units + rest / V;
-  } else {
-    p.rot_units = plan->rot_dim / 2;
-    p.units = p.rot_units + rest;
-  }
-  if (p.tokens > kMaxGrid / p.units * 256) return bad("mkv_rope: too many tokens");
-  int sms = 0;
-  mkv_status s = sm_count(&sms);
-  if (s != MKV_OK) return s;
-  p.heads_per = heads_per_thread((int64_t)a->batch * a->tokens * p.units, a->heads, (int64_t)sms * 2048, 8);
-  CKP(launch_rope(p, a->dtype, vec, reinterpret_cast<cudaStream_t>(stream)));
+  bool vec = false;
+  if (mkv_status s = rope_params(plan, a, &p, &vec)) return s;
+  if (p.tokens) CKP(launch_rope(p, a->dtype, vec, reinterpret_cast<cudaStream_t>(stream)));
+  return MKV_OK;
+}
+
+mkv_status mkv_rope_multi(const mkv_rope_plan* plan, const mkv_rope_axes* axes, const mkv_rope_args* a,
+                          int64_t pos_axis_stride, mkv_stream_t stream) {
+  if (!axes) return bad("mkv_rope_multi: NULL axes");
+  if (const char* e = check_axes(axes, plan)) return bad(e);
+  if (a && a->batch > 0 && a->heads > 0 && a->tokens > 0 && !a->pos) return bad("mkv_rope_multi: NULL pos");
+  RopeMultiParams p;
+  std::memset(&p, 0, sizeof(p));
+  bool vec = false;
+  if (mkv_status s = rope_params(plan, a, &p, &vec)) return s;
+  if (!p.tokens) return MKV_OK;
+  p.axes = *axes;
+  p.pos_axis_stride = pos_axis_stride;
+  CKP(launch_rope_multi(p, a->dtype, vec, reinterpret_cast<cudaStream_t>(stream)));
   return MKV_OK;
 }
 

@@ -36,6 +36,36 @@ struct RopeParams {
 };
 cudaError_t launch_rope(const RopeParams& p, int dtype, bool vec, cudaStream_t st);
 
+// With several axes: pos is [axes][batch][tokens].
+struct RopeMultiParams : RopeParams {
+  mkv_rope_axes axes;
+  int64_t pos_axis_stride;
+};
+cudaError_t launch_rope_multi(const RopeMultiParams& p, int dtype, bool vec, cudaStream_t st);
+
+// Norms of heads and their rotation.
+struct NormRopeParams {
+  mkv_rope_plan plan;
+  mkv_rope_axes axes;               // n_axes 0: one position a token, from pos or first_pos
+  const void *x[2], *grad[2], *weight[2];
+  void* out[2];
+  int64_t xs[2][3], os[2][3], gs[2][3];
+  const int32_t* pos;
+  int64_t pos_stride, pos_axis_stride;
+  int64_t tokens, items;            // items: batch * tokens * chunks
+  int batch, heads[2], first_pos;
+  int weight_f32[2];                // the weight's type (0: x's)
+  float eps, offset;
+  int units, rot_units;             // of a head, as in RopeParams
+  int lanes;                        // that share a head: a power of two up to 32
+  int heads_per, chunks;            // heads a group of lanes takes, of the list of both sides' heads
+  float* part;                      // gradient: [blocks][2][head_dim] sums of a block, or NULL
+  float* weight_grad[2];
+  int blocks;
+};
+// form: 0 elements, 1 vectors of half pairs, 2 vectors of interleaved pairs
+cudaError_t launch_norm_rope(const NormRopeParams& p, int dtype, int form, bool grad, cudaStream_t st);
+
 struct AppendRowsParams {
   mkv_rope_plan plan;             // rot_dim 0: no rotation
   mkv_paged_cache c;

@@ -26,6 +26,14 @@ struct Entries {
   decltype(&mkv_paged_decode) decode;
   decltype(&mkv_paged_evict_workspace) evict_workspace;
   decltype(&mkv_paged_evict) evict;
+  decltype(&mkv_rope_multi) rope_multi;
+  decltype(&mkv_norm_rope) norm_rope;
+  decltype(&mkv_norm_rope_grad) norm_rope_grad;
+  decltype(&mkv_norm_rope_grad_workspace) norm_rope_grad_workspace;
+  decltype(&mkv_prefill) prefill;
+  decltype(&mkv_prefill_workspace) prefill_workspace;
+  decltype(&mkv_paged_attend) attend;
+  decltype(&mkv_paged_attend_workspace) attend_workspace;
 } lib;
 
 struct Fail {
@@ -124,19 +132,11 @@ struct Launch {
   }
 };
 
-// Fills a call's workspace: the caller's tensor, or a new one whose memory
-// belongs to the launching stream and which *keep holds until the call is issued.
+// Fills a call's workspace: a new tensor whose memory belongs to the launching
+// stream and which *keep holds until the call is issued, or the caller's.
 // False where the library refused the sizes.
-template <typename Args, typename Size>
-bool workspace(PyObject* o, const Launch& l, int dev, const mkv_paged_cache* c, Args* a, Size size, at::Tensor* keep) {
-  if (o != Py_None) {
-    const at::Tensor& t = tensor(o, "workspace");
-    a->workspace = flat<void>(o, "workspace", dev, at::kByte, {t.numel()});
-    a->workspace_bytes = (uint64_t)t.numel();
-    return true;
-  }
-  const uint64_t need = size(c, a);
-  if (need == 0) return false;
+template <typename Args>
+bool workspace_of(const Launch& l, int dev, Args* a, uint64_t need, at::Tensor* keep) {
   const auto options = at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)dev);
   if (l.given) {
     c10::cuda::CUDAStreamGuard on(
@@ -150,17 +150,55 @@ bool workspace(PyObject* o, const Launch& l, int dev, const mkv_paged_cache* c, 
   return true;
 }
 
+// The caller's workspace; false: there is none.
+template <typename Args>
+bool given_workspace(PyObject* o, int dev, Args* a) {
+  if (o == Py_None) return false;
+  const at::Tensor& t = tensor(o, "workspace");
+  a->workspace = flat<void>(o, "workspace", dev, at::kByte, {t.numel()});
+  a->workspace_bytes = (uint64_t)t.numel();
+  return true;
+}
+
+template <typename Args, typename Size>
+bool workspace(PyObject* o, const Launch& l, int dev, const mkv_paged_cache* c, Args* a, Size size, at::Tensor* keep) {
+  if (given_workspace(o, dev, a)) return true;
+  const uint64_t need = size(c, a);
+  return need != 0 && workspace_of(l, dev, a, need, keep);
+}
+// For sizes of which 0 means that none is needed and UINT64_MAX that the library refused.
+template <typename Args>
+bool workspace_or_none(PyObject* o, const Launch& l, int dev, Args* a, uint64_t need, at::Tensor* keep) {
+  if (given_workspace(o, dev, a)) return true;
+  if (need == UINT64_MAX) return false;
+  return need == 0 || workspace_of(l, dev, a, need, keep);
+}
+
+void strides3(const at::Tensor& t, int64_t* out) {
+  for (int i = 0; i < 3; ++i) out[i] = t.stride(i);
+}
+int32_t size32(int64_t n, const char* name) {
+  if (n > INT32_MAX) value_error(std::string(name) + " is too large");
+  return (int32_t)n;
+}
+float number(PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    type_error(std::string(name) + " must be a number");
+  }
+  return (float)v;
+}
 void strides2(const at::Tensor& t, int64_t* out) {
   out[0] = t.stride(0);
   out[1] = t.stride(1);
 }
 
-// rope(plan, x, pos, out, transposed, first_pos, stream) -> status
-long rope(PyObject* const* v) {
-  const mkv_rope_plan* plan = address<mkv_rope_plan>(v[0]);
-  const at::Tensor& x = tensor(v[1], "x");
-  const at::Tensor& out = tensor(v[3], "out");
-  const int dev = x.get_device();
+// What rope and rope_multi have in common.
+mkv_rope_args rope_args(const mkv_rope_plan* plan, PyObject* px, PyObject* pout, int* device) {
+  const at::Tensor& x = tensor(px, "x");
+  const at::Tensor& out = tensor(pout, "out");
+  const int dev = *device = x.get_device();
   if (dev < 0) value_error("x must be on a CUDA device");
   if (x.dim() != 4 || x.size(3) != plan->head_dim)
     value_error("x must be [batch, tokens, heads, " + std::to_string(plan->head_dim) + "], got " + text(x.sizes()));
@@ -170,21 +208,212 @@ long rope(PyObject* const* v) {
   if (out.scalar_type() != x.scalar_type()) type_error("out must be " + name_of(x.scalar_type()) + ", got " + name_of(out.scalar_type()));
   a.x = rows(x, "x", dev, {x.size(0), x.size(1), x.size(2), x.size(3)});
   a.out = rows(out, "out", dev, {x.size(0), x.size(1), x.size(2), x.size(3)});
-  for (int i = 0; i < 3; ++i) a.x_stride[i] = x.stride(i), a.out_stride[i] = out.stride(i);
-  if (v[2] != Py_None) {
-    const at::Tensor& pos = tensor(v[2], "pos");
-    if (pos.scalar_type() != at::kInt) type_error("pos must be Int, got " + name_of(pos.scalar_type()));
-    a.pos = static_cast<const int32_t*>(rows(pos, "pos", dev, {x.size(0), x.size(1)}));
-    a.pos_stride = pos.stride(0);
-  }
+  strides3(x, a.x_stride);
+  strides3(out, a.out_stride);
   if (x.size(0) > INT32_MAX || x.size(2) > INT32_MAX) value_error("x is too large");
   a.batch = (int32_t)x.size(0);
   a.tokens = x.size(1);
   a.heads = (int32_t)x.size(2);
+  return a;
+}
+
+// rope(plan, x, pos, out, transposed, first_pos, stream) -> status
+long rope(PyObject* const* v) {
+  const mkv_rope_plan* plan = address<mkv_rope_plan>(v[0]);
+  int dev = 0;
+  mkv_rope_args a = rope_args(plan, v[1], v[3], &dev);
+  if (v[2] != Py_None) {
+    const at::Tensor& pos = tensor(v[2], "pos");
+    if (pos.scalar_type() != at::kInt) type_error("pos must be Int, got " + name_of(pos.scalar_type()));
+    a.pos = static_cast<const int32_t*>(rows(pos, "pos", dev, {a.batch, a.tokens}));
+    a.pos_stride = pos.stride(0);
+  }
   a.transposed = integer32(v[4], "transposed");
   a.first_pos = integer32(v[5], "first_pos");
   const Launch l(dev, v[6]);
   return lib.rope(plan, &a, l.stream);
+}
+
+// Positions [axes, batch, tokens] with a contiguous last dimension.
+const int32_t* axes_pos(PyObject* o, int dev, int64_t axes, int64_t batch, int64_t tokens, int64_t* stride,
+                        int64_t* axis_stride) {
+  const at::Tensor& pos = tensor(o, "pos");
+  if (pos.scalar_type() != at::kInt) type_error("pos must be Int, got " + name_of(pos.scalar_type()));
+  void* p = rows(pos, "pos", dev, {axes, batch, tokens});
+  *axis_stride = pos.stride(0);
+  *stride = pos.stride(1);
+  return static_cast<const int32_t*>(p);
+}
+
+// rope_multi(plan, axes, x, pos, out, transposed, stream) -> status
+long rope_multi(PyObject* const* v) {
+  const mkv_rope_plan* plan = address<mkv_rope_plan>(v[0]);
+  const mkv_rope_axes* axes = address<mkv_rope_axes>(v[1]);
+  int dev = 0;
+  mkv_rope_args a = rope_args(plan, v[2], v[4], &dev);
+  int64_t axis_stride = 0;
+  a.pos = axes_pos(v[3], dev, axes->n_axes, a.batch, a.tokens, &a.pos_stride, &axis_stride);
+  a.transposed = integer32(v[5], "transposed");
+  const Launch l(dev, v[6]);
+  return lib.rope_multi(plan, axes, &a, axis_stride, l.stream);
+}
+
+// norm_rope(plan, axes | None, pos, q, q_weight, q_out, k, k_weight, k_out, eps, weight_offset, first_pos, stream,
+//           dq, dk, q_weight_grad, k_weight_grad, workspace) -> status; a gradient where dq is not None
+long norm_rope(PyObject* const* v) {
+  const mkv_rope_plan* plan = address<mkv_rope_plan>(v[0]);
+  const mkv_rope_axes* axes = v[1] == Py_None ? nullptr : address<mkv_rope_axes>(v[1]);
+  const bool grad = v[13] != Py_None;
+  mkv_norm_rope_args a;
+  std::memset(&a, 0, sizeof(a));
+  const char* const names[2][5] = {{"q", "q_weight", "q_out", "dq", "q_weight_grad"}, {"k", "k_weight", "k_out", "dk", "k_weight_grad"}};
+  int dev = -1;
+  int wt = -1;
+  at::ScalarType type = at::kFloat;
+  for (int s = 0; s < 2; ++s) {
+    PyObject* const* w = v + 3 + 3 * s;
+    if (s == 1 && w[0] == Py_None) {
+      if (w[1] != Py_None || w[2] != Py_None || v[14] != Py_None || v[16] != Py_None)
+        value_error("k_weight, k_out, dk and k_weight_grad need k");
+      break;
+    }
+    const at::Tensor& x = tensor(w[0], names[s][0]);
+    if (s == 0) {
+      dev = x.get_device();
+      if (dev < 0) value_error("q must be on a CUDA device");
+      type = x.scalar_type();
+      a.dtype = dtype_of(x, "q");
+      if (x.dim() != 4) value_error("q must be [batch, tokens, heads, head_dim]");
+      a.batch = size32(x.size(0), "q");
+      a.tokens = x.size(1);
+    }
+    if (x.dim() != 4) value_error("k must be [batch, tokens, heads, head_dim]");
+    a.heads[s] = size32(x.size(2), names[s][0]);
+    const std::initializer_list<int64_t> shape = {a.batch, a.tokens, a.heads[s], plan->head_dim};
+    auto same = [&](const at::Tensor& t, const char* name) {
+      if (t.scalar_type() != type) type_error(std::string(name) + " must be " + name_of(type) + ", got " + name_of(t.scalar_type()));
+      return rows(t, name, dev, shape);
+    };
+    a.x[s] = same(x, names[s][0]);
+    strides3(x, a.x_stride[s]);
+    const at::Tensor& out = tensor(w[2], names[s][2]);
+    a.out[s] = same(out, names[s][2]);
+    strides3(out, a.out_stride[s]);
+    if (w[1] != Py_None) {
+      const at::Tensor& weight = tensor(w[1], names[s][1]);
+      const int t = dtype_of(weight, names[s][1]);
+      if (wt >= 0 && wt != t) type_error("q_weight and k_weight must be of one type");
+      wt = t;
+      a.weight[s] = rows(weight, names[s][1], dev, {plan->head_dim});
+    }
+    if (grad) {
+      const at::Tensor& g = tensor(v[13 + s], names[s][3]);
+      a.grad[s] = same(g, names[s][3]);
+      strides3(g, a.grad_stride[s]);
+      a.weight_grad[s] = flat<float>(v[15 + s], names[s][4], dev, at::kFloat, {plan->head_dim});
+    }
+  }
+  a.weight_dtype = wt < 0 ? MKV_DT_F32 : wt;
+  if (axes) {
+    a.pos = axes_pos(v[2], dev, axes->n_axes, a.batch, a.tokens, &a.pos_stride, &a.pos_axis_stride);
+  } else if (v[2] != Py_None) {
+    const at::Tensor& pos = tensor(v[2], "pos");
+    if (pos.scalar_type() != at::kInt) type_error("pos must be Int, got " + name_of(pos.scalar_type()));
+    a.pos = static_cast<const int32_t*>(rows(pos, "pos", dev, {a.batch, a.tokens}));
+    a.pos_stride = pos.stride(0);
+  }
+  a.eps = number(v[9], "eps");
+  a.weight_offset = number(v[10], "weight_offset");
+  a.first_pos = integer32(v[11], "first_pos");
+  const Launch l(dev, v[12]);
+  if (!grad) return lib.norm_rope(plan, axes, &a, l.stream);
+  at::Tensor keep;
+  const bool wants = a.weight_grad[0] || a.weight_grad[1];
+  if (!given_workspace(v[17], dev, &a) && wants) {
+    const uint64_t need = lib.norm_rope_grad_workspace(plan, &a);
+    if (need == 0) return MKV_ERR_INVALID_ARG;
+    workspace_of(l, dev, &a, need, &keep);
+  }
+  return lib.norm_rope_grad(plan, axes, &a, l.stream);
+}
+
+// prefill(q, k, v, out, lse, q_lens, kv_lens, prefix, docs, slopes, causal, window, scale, cap, workspace, stream)
+//   -> status
+long prefill(PyObject* const* v) {
+  const at::Tensor &q = tensor(v[0], "q"), &k = tensor(v[1], "k"), &val = tensor(v[2], "v"), &out = tensor(v[3], "out");
+  const int dev = q.get_device();
+  if (dev < 0) value_error("q must be on a CUDA device");
+  if (q.dim() != 4) value_error("q must be [batch, tokens, heads, head_dim]");
+  if (k.dim() != 4) value_error("k must be [batch, kv_tokens, kv_heads, head_dim]");
+  mkv_prefill_args a;
+  std::memset(&a, 0, sizeof(a));
+  a.dtype = dtype_of(q, "q", false);
+  if (k.scalar_type() != q.scalar_type() || val.scalar_type() != q.scalar_type() || out.scalar_type() != q.scalar_type())
+    type_error("q, k, v and out must be of one type");
+  a.batch = size32(q.size(0), "q");
+  a.q_tokens = q.size(1);
+  a.n_q_heads = size32(q.size(2), "q");
+  a.head_dim = size32(q.size(3), "q");
+  a.kv_tokens = k.size(1);
+  a.n_kv_heads = size32(k.size(2), "k");
+  a.q = rows(q, "q", dev, {a.batch, a.q_tokens, a.n_q_heads, a.head_dim});
+  a.k = rows(k, "k", dev, {a.batch, a.kv_tokens, a.n_kv_heads, a.head_dim});
+  a.v = rows(val, "v", dev, {a.batch, a.kv_tokens, a.n_kv_heads, a.head_dim});
+  a.out = rows(out, "out", dev, {a.batch, a.q_tokens, a.n_q_heads, a.head_dim});
+  strides3(q, a.q_stride);
+  strides3(k, a.k_stride);
+  strides3(val, a.v_stride);
+  strides3(out, a.out_stride);
+  a.lse = flat<float>(v[4], "lse", dev, at::kFloat, {a.batch, a.q_tokens, a.n_q_heads});
+  a.q_lens = flat<int32_t>(v[5], "q_lens", dev, at::kInt, {a.batch});
+  a.kv_lens = flat<int32_t>(v[6], "kv_lens", dev, at::kInt, {a.batch});
+  a.prefix = flat<int32_t>(v[7], "prefix", dev, at::kInt, {a.batch});
+  if (v[8] != Py_None) {
+    const at::Tensor& docs = tensor(v[8], "docs");
+    if (docs.scalar_type() != at::kInt) type_error("docs must be Int, got " + name_of(docs.scalar_type()));
+    a.docs = static_cast<const int32_t*>(rows(docs, "docs", dev, {a.batch, a.kv_tokens}));
+    a.docs_stride = docs.stride(0);
+  }
+  a.slopes = flat<float>(v[9], "slopes", dev, at::kFloat, {a.n_q_heads});
+  a.causal = integer32(v[10], "causal");
+  a.window = integer32(v[11], "window");
+  a.scale = number(v[12], "scale");
+  a.cap = number(v[13], "cap");
+  const Launch l(dev, v[15]);
+  at::Tensor keep;
+  if (!workspace_or_none(v[14], l, dev, &a, lib.prefill_workspace(&a), &keep)) return MKV_ERR_INVALID_ARG;
+  return lib.prefill(&a, l.stream);
+}
+
+// attend(cache, dev, q, seq_lens, out, lse, new_lens, tree, slopes, max_len, window, scale, cap, workspace, stream)
+//   -> status
+long attend(PyObject* const* v) {
+  const mkv_paged_cache* c = address<mkv_paged_cache>(v[0]);
+  const int dev = integer32(v[1], "device");
+  const at::Tensor &q = tensor(v[2], "q"), &out = tensor(v[4], "out");
+  if (q.dim() != 4) value_error("q must be [batch, new_tokens, q_heads, head_dim]");
+  mkv_paged_attend_args a;
+  std::memset(&a, 0, sizeof(a));
+  a.n = size32(q.size(1), "q");
+  a.n_q_heads = size32(q.size(2), "q");
+  a.q_dtype = dtype_of(q, "q", false);
+  a.q = rows(q, "q", dev, {c->batch, a.n, a.n_q_heads, c->head_dim});
+  strides3(q, a.q_stride);
+  a.out = flat<void>(v[4], "out", dev, q.scalar_type(), {c->batch, a.n, a.n_q_heads, c->head_dim});
+  tensor(v[3], "seq_lens");
+  a.seq_lens = flat<int32_t>(v[3], "seq_lens", dev, at::kInt, {c->batch});
+  a.lse = flat<float>(v[5], "lse", dev, at::kFloat, {c->batch, a.n, a.n_q_heads});
+  a.new_lens = flat<int32_t>(v[6], "new_lens", dev, at::kInt, {c->batch});
+  a.tree = reinterpret_cast<const uint64_t*>(flat<int64_t>(v[7], "tree", dev, at::kLong, {c->batch, a.n}));
+  a.slopes = flat<float>(v[8], "slopes", dev, at::kFloat, {a.n_q_heads});
+  a.max_len = integer(v[9]);
+  a.window = integer32(v[10], "window");
+  a.scale = number(v[11], "scale");
+  a.cap = number(v[12], "cap");
+  const Launch l(dev, v[14]);
+  at::Tensor keep;
+  if (!workspace_or_none(v[13], l, dev, &a, lib.attend_workspace(c, &a), &keep)) return MKV_ERR_INVALID_ARG;
+  return lib.attend(c, &a, l.stream);
 }
 
 // append(cache, dev, plan | None, k, v, slot, seq, pos, q, q_out, acc, pos_meta, stream) -> status
@@ -252,12 +481,7 @@ long decode(PyObject* const* v) {
   a.acc = meta<float>(v[7], "acc", dev, at::kFloat, c, &a.acc_stride);
   a.max_len = integer(v[8]);
   if (a.acc && a.max_len == 0) a.max_len = std::min(integer(v[2]), a.acc_stride);
-  const double scale = PyFloat_AsDouble(v[9]);
-  if (scale == -1.0 && PyErr_Occurred()) {
-    PyErr_Clear();
-    type_error("scale must be a number");
-  }
-  a.scale = (float)scale;
+  a.scale = number(v[9], "scale");
   const Launch l(dev, v[11]);
   at::Tensor keep;
   if (!workspace(v[10], l, dev, c, &a, lib.decode_workspace, &keep)) return MKV_ERR_INVALID_ARG;
@@ -317,7 +541,7 @@ PyObject* entry(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return nullptr;
 }
 
-// bind(addresses of the six entry points)
+// bind(addresses of the entry points)
 long bind(PyObject* const* v) {
   lib.rope = reinterpret_cast<decltype(lib.rope)>(address<void>(v[0]));
   lib.append = reinterpret_cast<decltype(lib.append)>(address<void>(v[1]));
@@ -325,11 +549,20 @@ long bind(PyObject* const* v) {
   lib.decode = reinterpret_cast<decltype(lib.decode)>(address<void>(v[3]));
   lib.evict_workspace = reinterpret_cast<decltype(lib.evict_workspace)>(address<void>(v[4]));
   lib.evict = reinterpret_cast<decltype(lib.evict)>(address<void>(v[5]));
+  lib.rope_multi = reinterpret_cast<decltype(lib.rope_multi)>(address<void>(v[6]));
+  lib.norm_rope = reinterpret_cast<decltype(lib.norm_rope)>(address<void>(v[7]));
+  lib.norm_rope_grad = reinterpret_cast<decltype(lib.norm_rope_grad)>(address<void>(v[8]));
+  lib.norm_rope_grad_workspace = reinterpret_cast<decltype(lib.norm_rope_grad_workspace)>(address<void>(v[9]));
+  lib.prefill = reinterpret_cast<decltype(lib.prefill)>(address<void>(v[10]));
+  lib.prefill_workspace = reinterpret_cast<decltype(lib.prefill_workspace)>(address<void>(v[11]));
+  lib.attend = reinterpret_cast<decltype(lib.attend)>(address<void>(v[12]));
+  lib.attend_workspace = reinterpret_cast<decltype(lib.attend_workspace)>(address<void>(v[13]));
   return 0;
 }
 
 #define ENTRY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<name, n>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(bind, 6), ENTRY(rope, 7), ENTRY(append, 13), ENTRY(decode, 12), ENTRY(evict, 17),
+PyMethodDef methods[] = {ENTRY(bind, 14), ENTRY(rope, 7), ENTRY(append, 13), ENTRY(decode, 12), ENTRY(evict, 17),
+                         ENTRY(rope_multi, 7), ENTRY(norm_rope, 18), ENTRY(prefill, 16), ENTRY(attend, 15),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -121,11 +121,58 @@ class mkv_paged_evict_args(Structure):
                 ("max_len", c_int64), ("budget", c_int32), ("sink", c_int32), ("recent", c_int32)]
 
 
+ROPE_ORDERS = {"blocks": 0, "cyclic": 1}
+MKV_ROPE_MAX_AXES = 4
+
+
+class mkv_rope_axes(Structure):
+    _fields_ = [("n_axes", c_int32), ("axis", c_uint8 * MKV_ROPE_MAX_PAIRS)]
+
+
+class MkvRopeAxes:
+    """A rotation with several axes ready to use (mkv_rope_axes_init): plain host data."""
+
+    def __init__(self):
+        self.plan, self.axes = MkvRopePlan(), mkv_rope_axes()
+        self.address, self.axes_address = self.plan.address, ctypes.addressof(self.axes)
+
+
+class mkv_norm_rope_args(Structure):
+    _fields_ = [("x", c_void_p * 2), ("out", c_void_p * 2), ("grad", c_void_p * 2),
+                ("weight", c_void_p * 2), ("weight_grad", c_void_p * 2), ("pos", c_void_p),
+                ("workspace", c_void_p), ("workspace_bytes", c_uint64),
+                ("x_stride", c_int64 * 3 * 2), ("out_stride", c_int64 * 3 * 2),
+                ("grad_stride", c_int64 * 3 * 2), ("pos_stride", c_int64),
+                ("pos_axis_stride", c_int64), ("tokens", c_int64), ("batch", c_int32),
+                ("heads", c_int32 * 2), ("dtype", c_int32), ("weight_dtype", c_int32),
+                ("first_pos", c_int32), ("eps", c_float), ("weight_offset", c_float)]
+
+
+class mkv_prefill_args(Structure):
+    _fields_ = [("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("out", c_void_p),
+                ("lse", c_void_p), ("q_lens", c_void_p), ("kv_lens", c_void_p),
+                ("prefix", c_void_p), ("docs", c_void_p), ("slopes", c_void_p),
+                ("workspace", c_void_p), ("workspace_bytes", c_uint64), ("q_stride", c_int64 * 3),
+                ("k_stride", c_int64 * 3), ("v_stride", c_int64 * 3), ("out_stride", c_int64 * 3),
+                ("docs_stride", c_int64), ("q_tokens", c_int64), ("kv_tokens", c_int64),
+                ("batch", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32),
+                ("head_dim", c_int32), ("dtype", c_int32), ("causal", c_int32),
+                ("window", c_int32), ("scale", c_float), ("cap", c_float)]
+
+
+class mkv_paged_attend_args(Structure):
+    _fields_ = [("q", c_void_p), ("out", c_void_p), ("lse", c_void_p), ("seq_lens", c_void_p),
+                ("new_lens", c_void_p), ("tree", c_void_p), ("slopes", c_void_p),
+                ("workspace", c_void_p), ("workspace_bytes", c_uint64), ("q_stride", c_int64 * 3),
+                ("max_len", c_int64), ("n", c_int32), ("n_q_heads", c_int32), ("q_dtype", c_int32),
+                ("window", c_int32), ("scale", c_float), ("cap", c_float)]
+
+
 class MkvError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
         msg = f"{where}: {mkv_status_string(status)}"
-        if status in (MKV_ERR_CUDA, MKV_ERR_OOM) or where.startswith(("mkv_rope", "mkv_paged")):
+        if status in (MKV_ERR_CUDA, MKV_ERR_OOM) or where.startswith(("mkv_rope", "mkv_paged", "mkv_norm", "mkv_prefill")):
             msg += f" ({mkv_last_error_string()})"
         super().__init__(msg)
 
@@ -164,6 +211,15 @@ def _load():
         "mkv_paged_evict_workspace": (c_uint64, [P, P]),
         "mkv_paged_evict": (c_int, [P, P, P]),
         "mkv_paged_check": (c_int, [P]),
+        "mkv_rope_axes_init": (c_int, [P, P, c_int32, c_int32, c_int32, P, P]),
+        "mkv_rope_multi": (c_int, [P, P, P, c_int64, P]),
+        "mkv_norm_rope": (c_int, [P, P, P, P]),
+        "mkv_norm_rope_grad": (c_int, [P, P, P, P]),
+        "mkv_norm_rope_grad_workspace": (c_uint64, [P, P]),
+        "mkv_prefill_workspace": (c_uint64, [P]),
+        "mkv_prefill": (c_int, [P, P]),
+        "mkv_paged_attend_workspace": (c_uint64, [P, P]),
+        "mkv_paged_attend": (c_int, [P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -417,7 +473,9 @@ def _native():
                               "torch: run python -m two_compressed_kv_gb300.build_lib") from e
         _marshal.bind(*(ctypes.cast(getattr(_lib, f), c_void_p).value for f in (
             "mkv_rope", "mkv_paged_append", "mkv_paged_decode_workspace", "mkv_paged_decode",
-            "mkv_paged_evict_workspace", "mkv_paged_evict")))
+            "mkv_paged_evict_workspace", "mkv_paged_evict", "mkv_rope_multi", "mkv_norm_rope",
+            "mkv_norm_rope_grad", "mkv_norm_rope_grad_workspace", "mkv_prefill",
+            "mkv_prefill_workspace", "mkv_paged_attend", "mkv_paged_attend_workspace")))
         _T, _M = torch, _marshal
     return _M
 
@@ -599,6 +657,143 @@ def mkv_paged_evict(cache, acc, pos, seq_lens, next_pos, budget, sink=0, recent=
     _check(_M.evict(cache._address, cache._dev, cache._capacity, acc, pos, seq_lens, next_pos, budget, sink, recent,
                    acc_out, pos_out, lens_out, src, max_len, workspace, _address(stream)), "mkv_paged_evict")
     return src
+
+
+# ---- between projections and caches -----------------------------------------------------------
+
+def mkv_rope_axes_plan(head_dim, sections, order="blocks", restart=False, rot_dim=None, base=10000.0,
+                       interleaved=False, scaling="none", factor=1.0, original=0.0, low_freq=1.0,
+                       high_freq=4.0, beta_fast=32.0, beta_slow=1.0, attn_factor=0.0) -> MkvRopeAxes:
+    """A rotation with several axes (time, height, width): sections[a] pairs turn by the position of
+    axis a, in "blocks" or dealt in turn ("cyclic"); restart: every axis has frequencies of its own,
+    from 1 down.  rot_dim: twice the sections' sum where None."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    if order not in ROPE_ORDERS:
+        raise ValueError(f"order must be one of {sorted(ROPE_ORDERS)}, got {order!r}")
+    cfg = mkv_rope_config(head_dim, 2 * sum(sections) if rot_dim is None else rot_dim,
+                          int(interleaved), ROPE_SCALINGS[scaling], base, factor, original, low_freq,
+                          high_freq, beta_fast, beta_slow, attn_factor)
+    made = MkvRopeAxes()
+    n = len(sections)
+    _check(_lib.mkv_rope_axes_init(ctypes.byref(cfg), (c_int32 * max(1, n))(*sections), n,
+                                   ROPE_ORDERS[order], int(restart), made.address,
+                                   made.axes_address), "mkv_rope_axes_init")
+    return made
+
+
+def mkv_rope_multi(plan, x, pos, out=None, transposed=False, stream=None):
+    """mkv_rope with a rotation of several axes (mkv_rope_axes_plan): pos int32 [axes, batch,
+    tokens].  transposed: the gradient of the call."""
+    m = _native()
+    if out is None and isinstance(x, _T.Tensor):
+        out = _new(x.shape, x.dtype, x.device, stream)
+    _check(m.rope_multi(plan.address, plan.axes_address, x, pos, out, transposed, _address(stream)),
+           "mkv_rope_multi")
+    return out
+
+
+def mkv_norm_rope(plan, q, q_weight=None, pos=None, k=None, k_weight=None, eps=1e-6,
+                  weight_offset=0.0, q_out=None, k_out=None, first_pos=0, stream=None):
+    """RMS norm over every head of q (and k) [batch, tokens, heads, head_dim] and its rotation, in
+    one pass: y = R(pos) (x / sqrt(mean(x^2) + eps) * (weight + weight_offset)).  plan:
+    mkv_rope_plan, with pos int32 [batch, tokens] or None (first_pos + token), or
+    mkv_rope_axes_plan, with pos [axes, batch, tokens].  Weights [head_dim]: of q's type or fp32,
+    or None (1).  Returns q_out, or (q_out, k_out) with k (new where None; may be q and k)."""
+    m = _native()
+    if q_out is None and isinstance(q, _T.Tensor):
+        q_out = _new(q.shape, q.dtype, q.device, stream)
+    if k_out is None and isinstance(k, _T.Tensor):
+        k_out = _new(k.shape, k.dtype, k.device, stream)
+    _check(m.norm_rope(plan.address, getattr(plan, "axes_address", None), pos, q, q_weight, q_out, k, k_weight,
+                       k_out, eps, weight_offset, first_pos, _address(stream), None, None, None, None, None),
+           "mkv_norm_rope")
+    return q_out if k is None else (q_out, k_out)
+
+
+def mkv_norm_rope_grad(plan, dq, q, q_weight=None, pos=None, dk=None, k=None, k_weight=None, eps=1e-6,
+                       weight_offset=0.0, dq_out=None, dk_out=None, q_weight_grad=None,
+                       k_weight_grad=None, first_pos=0, workspace=None, stream=None):
+    """Gradients of mkv_norm_rope: dq, dk are those of its results; q, k and the rest are its own
+    arguments.  Returns (gradient of q, gradient of q_weight), or with k (of q, of k, of q_weight,
+    of k_weight); those of the weights are fp32, written and not added to (None without a weight).
+    workspace: a uint8 tensor of mkv_norm_rope_grad_workspace bytes (None: taken from torch's
+    allocator)."""
+    m = _native()
+    if dq is None:
+        raise TypeError("dq must be a torch tensor")
+    if dq_out is None and isinstance(q, _T.Tensor):
+        dq_out = _new(q.shape, q.dtype, q.device, stream)
+    if dk_out is None and isinstance(k, _T.Tensor):
+        dk_out = _new(k.shape, k.dtype, k.device, stream)
+    if q_weight_grad is None and isinstance(q_weight, _T.Tensor):
+        q_weight_grad = _new(q_weight.shape, _T.float32, q_weight.device, stream)
+    if k_weight_grad is None and isinstance(k_weight, _T.Tensor):
+        k_weight_grad = _new(k_weight.shape, _T.float32, k_weight.device, stream)
+    _check(m.norm_rope(plan.address, getattr(plan, "axes_address", None), pos, q, q_weight, dq_out, k, k_weight,
+                       dk_out, eps, weight_offset, first_pos, _address(stream), dq, dk, q_weight_grad,
+                       k_weight_grad, workspace), "mkv_norm_rope_grad")
+    return (dq_out, q_weight_grad) if k is None else (dq_out, dk_out, q_weight_grad, k_weight_grad)
+
+
+def mkv_norm_rope_grad_workspace(plan, device=None) -> int:
+    """Bytes of workspace of mkv_norm_rope_grad with a weight on `device` (None: the current one)."""
+    _native()
+    p = plan.plan if isinstance(plan, MkvRopeAxes) else plan
+    a = mkv_norm_rope_args(dtype=MKV_DT_F32, weight_dtype=MKV_DT_F32)
+    a.weight_grad[0] = 1
+    with _T.cuda.device(device):
+        n = _lib.mkv_norm_rope_grad_workspace(p.address, ctypes.byref(a))
+    if n == 0:
+        raise MkvError(MKV_ERR_INVALID_ARG, "mkv_norm_rope_grad_workspace")
+    return n
+
+
+def mkv_prefill(q, k, v, out=None, lse=None, causal=True, window=0, prefix=None, docs=None, q_lens=None,
+                kv_lens=None, scale=0.0, cap=0.0, slopes=None, workspace=None, stream=None):
+    """Attention of a prompt: q [batch, tokens, q_heads, head_dim] over k, v [batch, kv_tokens,
+    kv_heads, head_dim] (fp16 or bf16, strided; a transposed view of a [batch, heads, tokens,
+    head_dim] tensor is as good).  The last query stands at the last key; q_lens, kv_lens int32
+    [batch]: how many there are of each sequence.  causal, window (keys less than that far away),
+    prefix (int32 [batch]: keys seen by all queries), docs (int32 [batch, kv_tokens]: only keys of
+    the query's document): which keys a query sees.  cap: scores become cap * tanh(score / cap);
+    slopes (fp32 [q_heads]): slope * distance is taken off.  lse: fp32 [batch, tokens, q_heads] or
+    None.  Returns out (new where None), of q's shape and type; rows behind q_lens are left as they
+    were."""
+    m = _native()
+    if out is None and isinstance(q, _T.Tensor):
+        out = _new(q.shape, q.dtype, q.device, stream)
+    _check(m.prefill(q, k, v, out, lse, q_lens, kv_lens, prefix, docs, slopes, causal, window, scale, cap, workspace,
+                     _address(stream)), "mkv_prefill")
+    return out
+
+
+def mkv_paged_attend(cache, q, seq_lens, tree=None, new_lens=None, out=None, lse=None, max_len=0, window=0,
+                     scale=0.0, cap=0.0, slopes=None, workspace=None, stream=None):
+    """Attention of the last new_lens (int32 [batch]; None: all) tokens of every sequence, q [batch,
+    new_tokens, q_heads, head_dim], over its seq_lens (int32 [batch]) cached tokens, their own among
+    them.  tree: int64 [batch, new_tokens], up to 64 of them: bit j of row i says that token i sees
+    token j (None: a chain).  window, cap, slopes: as in mkv_prefill.  max_len: a bound on seq_lens
+    (0: the page table's capacity); one near the lengths is faster.  lse: fp32 [batch, new_tokens,
+    q_heads] or None.  workspace: a uint8 tensor of mkv_paged_attend_workspace bytes (None: taken
+    from torch's allocator).  Returns out (new where None); rows behind new_lens are left as they
+    were."""
+    if out is None and isinstance(q, _T.Tensor):
+        out = _new(q.shape, q.dtype, q.device, stream)
+    _check(_M.attend(cache._address, cache._dev, q, seq_lens, out, lse, new_lens, tree, slopes, max_len, window, scale,
+                     cap, workspace, _address(stream)), "mkv_paged_attend")
+    return out
+
+
+def mkv_paged_attend_workspace(cache, new_tokens, q_heads, max_len=0) -> int:
+    """Bytes of workspace of mkv_paged_attend for these sizes."""
+    qt = MKV_DT_F16 if cache.view.dtype == MKV_DT_E4M3 else cache.view.dtype
+    a = mkv_paged_attend_args(n=new_tokens, n_q_heads=q_heads, max_len=max_len, q_dtype=qt)
+    with _T.cuda.device(cache.device):
+        n = _lib.mkv_paged_attend_workspace(ctypes.byref(cache.view), ctypes.byref(a))
+    if n == 2**64 - 1:
+        raise MkvError(MKV_ERR_INVALID_ARG, "mkv_paged_attend_workspace")
+    return n
 
 
 class Mkv:
