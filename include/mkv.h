@@ -724,6 +724,7 @@ typedef struct {
   const int32_t* docs;       /* device [batch][kv_tokens], or NULL: the document of each place (any numbers, in
                                 any order); keys of other documents than the query's are not seen */
   const float* slopes;       /* device [n_q_heads], or NULL */
+  int32_t* status;           /* device word, or NULL: as in mkv_paged_cache, for waits that gave up */
   void* workspace;           /* device, 16-byte aligned, of mkv_prefill_workspace bytes (NULL where that is 0) */
   uint64_t workspace_bytes;
   int64_t q_stride[3];       /* elements between batches, tokens, heads: positive multiples of 8 where the */

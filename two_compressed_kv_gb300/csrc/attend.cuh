@@ -1,0 +1,918 @@
+// Attention of many queries over keys in tensors or in pages on the fifth-generation
+// tensor cores, included by one translation unit per head dimension.
+//
+//   z_ij = score(q_i, k_j) over the keys j that query i sees, o_i = softmax(z_i) v
+//
+// in one pass over the keys with a running reference m_i of the exponents and sum
+// l_i.  The g query heads of a KV head share its keys: a row tile is 128 / g tokens
+// times g heads, so that few tokens still fill the 128 rows of a product and the
+// keys of a group are read once.
+//
+// A CTA holds one or two row tiles and walks over blocks of 128 (D = 256: 64) keys:
+//   S = Q K^T       tcgen05, both operands in shared memory, S in tensor memory;
+//   softmax         a warpgroup per row tile, one row a thread (no shuffles): scores
+//                   out of tensor memory, exponents, 16-bit weights back over them;
+//   O += P V        tcgen05, P in tensor memory, V in shared memory, O in tensor
+//                   memory (fp32).
+// Roles: one warp copies (TMA, 128-byte swizzle, a ring of K and V tiles), one
+// issues products, a warpgroup per row tile does the softmax.  Two S buffers keep the
+// tensor cores busy while a softmax runs: with two row tiles one belongs to each,
+// with one tile consecutive blocks take turns.  The products of a buffer are issued
+// in the order S, P V, next S by one thread, which is the order they execute in.
+//
+// O is scaled down only where a row's maximum passes its reference by 2^6: after the
+// first blocks that hardly happens, and no work on O lies between the products.
+// Weights carry a factor 2^8, which cancels: fp16 ones stay normal down to 2^-22 of
+// the largest, and below 2^14.  The rounding of the weights to 16 bits is half a step
+// of the output's own type; their sum is of the unrounded ones.
+//
+// 8-bit pages: a further warpgroup widens the raw tiles to fp16 between the copies and
+// the products.
+#pragma once
+
+#include <math_constants.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "attend_internal.cuh"
+#include "decode_common.cuh"
+#include "ptx.cuh"
+#include "tc05.cuh"
+
+namespace mkv {
+namespace {
+
+enum { FROM_TENSORS = 0, FROM_PAGES = 1, FROM_BYTES = 2 };
+
+template <int D, int TILES, int FROM>
+struct AT {
+  static constexpr int NB = attend_block(D);
+  static constexpr bool E4 = FROM == FROM_BYTES;
+  static constexpr int G = D / 64;                         // groups of 64 channels
+  static constexpr int QTILE = 128 * D * 2;
+  static constexpr int TILE = NB * D * 2;                  // bytes of a K or V tile
+  static constexpr int RAW = NB * D;
+  static constexpr int STAGES = E4 ? (D == 64 ? 5 : 3) : D == 64 ? 8 : TILES == 2 ? 5 : D == 256 ? 5 : 6;
+  static constexpr int RAWS = E4 ? (D == 256 ? 3 : 5) : 0;
+  static constexpr int SMEM = TILES * QTILE + STAGES * TILE + RAWS * RAW + 1024;
+  static constexpr int THREADS = TILES == 2 || E4 ? 384 : 256;
+  static constexpr int S_COL = 0, O_COL = 2 * NB;          // tensor memory columns
+  static_assert(O_COL + TILES * D <= 512, "tensor memory");
+  static_assert(SMEM <= 225 * 1024 + 512, "shared memory");
+  static_assert(!(E4 && TILES == 2), "the second warpgroup widens");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// tanh(x), |x| given times 2 log2(e): within 2^-22 of it.
+__device__ __forceinline__ float tanh_of(float x2) {
+  const float t = fmaf(-2.f, rcp_fast(ex2(fabsf(x2)) + 1.f), 1.f);
+  return copysignf(t, x2);
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// K-major operand: 64 channels a 128-byte row, groups of channels apart.
+// MN-major operand (V): channels contiguous, groups of 64 channels `lead` bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lead) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(lead >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// D[tmem] (+)= A[tmem] B
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* u) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]),
+      "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]),
+      "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* u) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+          taddr),
+      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+template <int R>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R));
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// mbar_wait without a call: a kernel that moves registers between its warps has none.
+__device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity) {
+  uint64_t since = 0;
+  for (int i = 0; !mbar_test(bar, parity); ++i) {
+    if (i < 4096) continue;
+    const uint64_t now = globaltimer_ns();
+    if (i == 4096) since = now;
+    if (now - since > WAIT_LIMIT_NS) return false;
+    i = 4096 + 1;
+  }
+  return true;
+}
+
+// The blocks of keys that a CTA walks over, the same in every role (a warp asks as a
+// whole): all of a range, or those in which some document of its queries occurs.
+struct Blocks {
+  int j, end, base;
+  uint32_t bits;
+  const int2* range;     // of the sequence's blocks; NULL: all
+  int2 own;              // of the queries' documents
+  __device__ __forceinline__ int next() {
+    if (!range) return j < end ? j++ : -1;
+    const int lane = threadIdx.x & 31;
+    while (j < end) {
+      if (j >= base + 32) {
+        base = j;
+        bool hit = false;
+        if (base + lane < end) {
+          const int2 r = range[base + lane];
+          hit = r.x <= own.y && r.y >= own.x;
+        }
+        bits = __ballot_sync(~0u, hit);
+      }
+      const uint32_t rest = bits >> (j - base);
+      if (rest) {
+        j += __ffs(rest);
+        return j - 1;
+      }
+      j = base + 32;
+    }
+    return -1;
+  }
+};
+
+// Bits of the columns [lo, hi) of a block among the 32 from `first` on.
+__device__ __forceinline__ uint32_t columns(int lo, int hi, int first) {
+  const int a = max(lo - first, 0), b = min(hi - first, 32);
+  return a >= b ? 0u : (~0u << a) & (~0u >> (32 - b));
+}
+
+struct AttendShared {
+  uint64_t q_full;
+  uint64_t full[8], empty[8];          // K and V tiles as the products take them
+  uint64_t raw_full[8], raw_empty[8];  // 8-bit tiles
+  uint64_t s_full[2], p_full[2];       // scores there; weights there
+  uint64_t o_done[2];                  // another product of a row tile is in O
+  uint64_t o_last[2];                  // all are
+  uint64_t drained;
+  uint32_t tmem;
+  int depth[64];                       // of a tree's new tokens
+  float q_scale[128];                  // 8-bit pages: what a row of q was divided by
+};
+
+// ---------------------------------------------------------------------------
+// grid: B * H * groups * splits; block AT::THREADS; dynamic smem AT::SMEM
+// ---------------------------------------------------------------------------
+template <int D, int TILES, int FROM, bool BF16>
+__global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
+    attend_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap qmap,
+                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int unit) {
+  using C = AT<D, TILES, FROM>;
+  constexpr int NB = C::NB, G = C::G;
+  constexpr bool E4 = C::E4, PAGED = FROM != FROM_TENSORS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ AttendShared sh;
+  const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const smem_p = smem_raw + (smem0 - smem_u32(smem_raw));
+  const uint32_t ring = smem0 + TILES * C::QTILE, raws = ring + C::STAGES * C::TILE;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (warp == 1) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    mbar_init(&sh.q_full, E4 ? 4 : 1);
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&sh.full[i], E4 ? 4 : 1);
+      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.o_done[i], 1);
+      mbar_init(&sh.o_last[i], 1);
+    }
+    mbar_init(&sh.drained, 1);
+    mbar_init_fence();
+  }
+  griddep_wait();
+  griddep_launch();
+
+  // this CTA's part: row tiles [tile0, tile0 + TILES) of (b, h), the part-th share of their keys
+  int item = blockIdx.x;
+  const int part = item % p.splits;
+  item /= p.splits;
+  const int group = p.groups - 1 - item % p.groups;      // causal: the longest first
+  const int bh = item / p.groups, b = bh / p.H, h = bh - b * p.H;
+  const int TT = p.tile_tokens, t0 = group * TILES * TT;
+  int m, L;
+  bool outside;
+  attend_lens(p, b, m, L, outside);
+  if (outside && PAGED && p.status && h == 0 && group == 0 && part == 0 && tid == 0) atomicOr(p.status, DEV_ERR_CHECK);
+  const int base = L - m;
+  const int t1 = min(m, t0 + TILES * TT);                // tokens of this CTA: [t0, t1)
+  const int prefix = p.prefix ? p.prefix[b] : 0;
+  // keys that a token at place `at` sees, as a range
+  auto first_key = [&](int at) { return p.window ? max(0, at - p.window + 1) : 0; };
+  auto end_key = [&](int at) {
+    if (p.causal) return min(L, max(at + 1, prefix));
+    return p.window ? min(L, at + p.window) : L;
+  };
+  int lo = 0, hi = 0;
+  if (t0 < t1) {
+    lo = first_key(base + t0);
+    hi = end_key(base + t1 - 1);
+    if (p.tree) lo = first_key(base), hi = L;
+  }
+  const int32_t* docs = p.docs ? p.docs + b * p.docs_stride : nullptr;
+  Blocks blocks;
+  blocks.range = nullptr;
+  {
+    const int from = lo / NB, n = hi > lo ? (hi + NB - 1) / NB - from : 0;
+    blocks.j = from + (int)((int64_t)n * part / p.splits);
+    blocks.end = from + (int)((int64_t)n * (part + 1) / p.splits);
+    blocks.base = blocks.j - 32;
+  }
+  if (docs && hi > lo) {
+    int2 own = make_int2(INT32_MAX, INT32_MIN);
+    for (int t = t0 + lane; t < t1; t += 32)
+      if (base + t >= 0) {
+        const int d = docs[base + t];
+        own.x = min(own.x, d), own.y = max(own.y, d);
+      }
+    blocks.own.x = __reduce_min_sync(~0u, own.x);
+    blocks.own.y = __reduce_max_sync(~0u, own.y);
+    blocks.range = p.doc_range + (int64_t)b * ((p.nk + NB - 1) / NB);
+  }
+  if (p.tree && tid < m) {
+    const uint64_t valid = m >= 64 ? ~0ull : (1ull << m) - 1;
+    sh.depth[tid] = __popcll(p.tree[(int64_t)b * p.nq + tid] & valid & ~(1ull << tid));
+  }
+  // a page outside the cache: its tokens are absent, which the softmax looks up again
+  bool absent = false;
+  if (PAGED && blocks.j < blocks.end) {
+    const int e1 = min(blocks.end * NB, L);
+    for (int e = blocks.j * NB / p.page_size + tid; e * p.page_size < e1; e += C::THREADS) {
+      const int page = p.table[b * p.table_stride + e];
+      absent |= page < 0 || page >= p.n_pages;
+    }
+    if (absent && p.status) atomicOr(p.status, DEV_ERR_CHECK);
+  }
+  tc_fence_before();
+  absent = __syncthreads_or(absent);
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = __all_sync(~0u, wait_here(bar, parity));
+    if (!ok && lane == 0 && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
+    return ok;
+  };
+
+  if (warp < 4) {
+    if constexpr (C::THREADS == 384) regs_down<88>();
+    if (warp == 0) {
+      // ---- copies -----------------------------------------------------------
+      const bool work = blocks.j < blocks.end;
+      if constexpr (!E4) {
+        if (work) {
+          if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, TILES * G * TT * p.g * 128);
+          __syncwarp();
+          if (lane < TILES * G) {
+            const int tile = lane / G, c = lane - tile * G;
+            tma_load_4d(smem0 + tile * C::QTILE + c * 128 * 128, &qmap, c * 64, h * p.g, t0 + tile * TT, b, &sh.q_full);
+          }
+        }
+      }
+      uint64_t* const full = E4 ? sh.raw_full : sh.full;
+      uint64_t* const empty = E4 ? sh.raw_empty : sh.empty;
+      constexpr int SLOTS = E4 ? C::RAWS : C::STAGES, BYTES = E4 ? C::RAW : C::TILE;
+      const uint32_t at0 = E4 ? raws : ring;
+      int n = 0, slot = 0;
+      uint32_t turn = 0;
+      bool ok = true;
+      int units_from = -1, entry = 0;    // pages: this lane's unit of the 32 from `units_from` on
+      const int per = NB / unit;
+      auto load = [&](const CUtensorMap& map, int j) {
+        if (!ok) return;
+        if (n >= SLOTS && !(ok = wait(&empty[slot], (turn & 1) ^ 1))) return;
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], BYTES);
+        const uint32_t at = at0 + slot * BYTES;
+        if constexpr (PAGED) {
+          const int u0 = j * per;
+          if (units_from < 0 || u0 < units_from || u0 >= units_from + 32) {
+            units_from = u0;
+            const int t = (u0 + lane) * unit;
+            entry = p.n_pages * p.H * p.page_size;     // behind the pool: zeros
+            if (t < L) {
+              const int pg = t / p.page_size;
+              const int page = p.table[b * p.table_stride + pg];
+              if (page >= 0 && page < p.n_pages) entry = (page * p.H + h) * p.page_size + (t - pg * p.page_size);
+            }
+          }
+          constexpr int W = E4 ? 1 : G;
+          const int u = lane / W, c = lane - u * W;
+          const int row = __shfl_sync(~0u, entry, (u0 - units_from + u) & 31);
+          __syncwarp();
+          if (u < per) tma_load_2d(at + c * NB * 128 + u * unit * (E4 ? D : 128), &map, c * 64, row, &full[slot]);
+        } else {
+          __syncwarp();
+          if (lane < G) tma_load_4d(at + lane * NB * 128, &map, lane * 64, j * NB, h, b, &full[slot]);
+        }
+        ++n;
+        if (++slot == SLOTS) slot = 0, ++turn;
+      };
+      int cur = blocks.next();
+      if (cur >= 0) load(kmap, cur);
+      if constexpr (TILES == 2) {
+        while (cur >= 0 && ok) {
+          const int nxt = blocks.next();
+          load(vmap, cur);
+          if (nxt >= 0) load(kmap, nxt);
+          cur = nxt;
+        }
+      } else {
+        int nxt = cur >= 0 ? blocks.next() : -1;
+        if (nxt >= 0) load(kmap, nxt);
+        while (cur >= 0 && ok) {
+          const int then = nxt >= 0 ? blocks.next() : -1;
+          load(vmap, cur);
+          if (then >= 0) load(kmap, then);
+          cur = nxt;
+          nxt = then;
+        }
+      }
+      // no copy may be in flight when the CTA ends
+      for (int i = max(0, n - SLOTS); i < n; ++i) wait_here(&full[i % SLOTS], (i / SLOTS) & 1);
+      if (!E4 && work) wait_here(&sh.q_full, 0);
+    } else if (warp == 1) {
+      // ---- products ---------------------------------------------------------
+      constexpr uint32_t IS = idesc_f16_f32(128, NB) | (BF16 && !E4 ? (1u << 7) | (1u << 10) : 0u);
+      constexpr uint32_t IO = idesc_f16_f32(128, D) | (BF16 && !E4 ? (1u << 7) | (1u << 10) : 0u) | (1u << 16);
+      int slot = 0;
+      uint32_t turn = 0;
+      bool ok = true;
+      auto pop = [&]() {       // the next tile of the ring, once it is there
+        const int s = slot;
+        ok = ok && wait(&sh.full[s], turn & 1);
+        if (++slot == C::STAGES) slot = 0, ++turn;
+        return s;
+      };
+      auto scores = [&](int tile, int buf, int s) {
+        if (lane == 0) {
+          const uint32_t qa = smem0 + tile * C::QTILE, ka = ring + s * C::TILE;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tc_mma_f16(tmem + C::S_COL + buf * NB, sdesc_k_sw128(qa + (k / 4) * 128 * 128 + (k % 4) * 32),
+                       sdesc_k_sw128(ka + (k / 4) * NB * 128 + (k % 4) * 32), IS, k > 0);
+          tc_commit(&sh.s_full[buf]);
+        }
+      };
+      auto values = [&](int tile, int buf, int s, bool first, bool last) {
+        if (lane == 0) {
+          const uint32_t va = ring + s * C::TILE;
+#pragma unroll
+          for (int k = 0; k < NB / 16; ++k)
+            tc_mma_ts(tmem + C::O_COL + tile * D, tmem + C::S_COL + buf * NB + k * 8, sdesc_mn(va + k * 2048, NB * 128),
+                      IO, !first || k > 0);
+          tc_commit(&sh.o_done[tile]);
+          if (last) tc_commit(&sh.o_last[tile]);
+        }
+      };
+      // What lies behind the sequence in its last block may be anything, and 0 times a
+      // NaN is one: those rows of V become zeros (8-bit pages: where they are widened).
+      auto clean = [&](int s, int j) {
+        if (E4 || !ok || (j + 1) * NB <= L) return;
+        uint8_t* at = smem_p + TILES * C::QTILE + s * C::TILE;
+        const int r0 = L - j * NB;
+        for (int i = lane; i < (NB - r0) * 8; i += 32) {
+#pragma unroll
+          for (int c = 0; c < G; ++c)
+            *reinterpret_cast<uint4*>(at + c * NB * 128 + (r0 + i / 8) * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        __syncwarp();
+      };
+      auto release = [&](int s) {
+        if (lane == 0) tc_commit(&sh.empty[s]);
+      };
+      int cur = blocks.next();
+      if (cur >= 0) {
+        ok = wait(&sh.q_full, 0);
+        tc_fence_after();
+        if constexpr (TILES == 2) {
+          int ks = pop();
+          tc_fence_after();
+          if (ok) {
+            scores(0, 0, ks);
+            scores(1, 1, ks);
+            release(ks);
+          }
+          for (uint32_t k = 0; cur >= 0 && ok; ++k) {
+            const int nxt = blocks.next();
+            int vs = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              ok = ok && wait(&sh.p_full[i], k & 1);
+              if (i == 0) {
+                vs = pop();
+                clean(vs, cur);
+              }
+              if (!ok) break;
+              tc_fence_after();
+              values(i, i, vs, k == 0, nxt < 0);
+              if (i == 1) release(vs);
+              if (nxt >= 0) {
+                if (i == 0) ks = pop();
+                if (!ok) break;
+                tc_fence_after();
+                scores(i, i, ks);
+                if (i == 1) release(ks);
+              }
+            }
+            cur = nxt;
+          }
+        } else {
+          int nxt = blocks.next();
+          for (int i = 0; i < 2 && ok; ++i)
+            if (i == 0 || nxt >= 0) {
+              const int ks = pop();
+              tc_fence_after();
+              if (!ok) break;
+              scores(0, i, ks);
+              release(ks);
+            }
+          for (uint32_t k = 0; cur >= 0 && ok; ++k) {
+            const int then = nxt >= 0 ? blocks.next() : -1;
+            ok = wait(&sh.p_full[k & 1], (k >> 1) & 1);
+            const int vs = pop();
+            clean(vs, cur);
+            if (!ok) break;
+            tc_fence_after();
+            values(0, k & 1, vs, k == 0, nxt < 0);
+            release(vs);
+            if (then >= 0) {
+              const int ks = pop();
+              if (!ok) break;
+              tc_fence_after();
+              scores(0, k & 1, ks);
+              release(ks);
+            }
+            cur = nxt;
+            nxt = then;
+          }
+        }
+      }
+      // no product may be in flight when the tensor memory goes
+      if (lane == 0) tc_commit(&sh.drained);
+      wait_here(&sh.drained, 0);
+    }
+  } else if (!E4 || warp < 8) {
+    // ---- softmax: a row a thread --------------------------------------------
+    if constexpr (C::THREADS == 384) regs_up<(E4 ? 240 : 208)>();
+    const int tile = TILES == 2 ? (warp >> 2) - 1 : 0;
+    const int row = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int rt = row / p.g, head = h * p.g + (row - rt * p.g);
+    const int token = t0 + tile * TT + rt;
+    const bool live = rt < TT && token < t1;
+    const bool any = __any_sync(~0u, live);
+    // what this row sees: keys [klo, khi), of its document, and the new tokens of its tree row
+    int place = base + token, klo = 0, khi = INT32_MAX;
+    uint64_t sees = 0;
+    if (live) {
+      if (p.tree) {
+        const uint64_t valid = m >= 64 ? ~0ull : (1ull << m) - 1;
+        sees = p.tree[(int64_t)b * p.nq + token] & valid;
+        place = base + sh.depth[token];
+        klo = first_key(place);
+        khi = base;
+        if (p.window)
+          for (int j = 0; j < m; ++j)
+            if (sh.depth[token] - sh.depth[j] >= p.window) sees &= ~(1ull << j);
+      } else {
+        klo = first_key(place);
+        khi = end_key(place);
+        if (docs && place < 0) khi = 0;
+      }
+    }
+    const int doc = docs && live && place >= 0 ? docs[place] : 0;
+    float sc = p.scale * 1.4426950408889634f;            // of the products, to log2
+    const float slope = p.slopes && live ? p.slopes[head] * 1.4426950408889634f : 0.f;
+    bool ok = true;
+    if constexpr (E4) {
+      ok = wait(&sh.q_full, 0);
+      sc *= sh.q_scale[row] * (p.k_scale ? p.k_scale[h] : 1.f);
+    }
+    {
+      const bool mods = p.cap > 0.f || p.slopes;
+      const float cap2 = p.cap * 1.4426950408889634f;
+      const float into = p.cap > 0.f ? 2.f * sc / p.cap : 0.f;  // products to 2 log2(e) times the tanh's argument
+      const float by = mods ? 1.f : sc;
+      float top = -CUDART_INF_F, mref = 1e38f, l = 0.f;
+      uint32_t k = 0;
+      const uint32_t o_at = tmem + lanes + C::O_COL + tile * D;
+      for (int j = ok ? blocks.next() : -1; j >= 0; j = blocks.next(), ++k) {
+        const int buf = TILES == 2 ? tile : k & 1;
+        const uint32_t s_at = tmem + lanes + C::S_COL + buf * NB;
+        if (!(ok = wait(&sh.s_full[buf], TILES == 2 ? k & 1 : (k >> 1) & 1))) break;
+        if (any) {
+          tc_fence_after();
+          const int j0 = j * NB;
+          const bool in_tree = p.tree && j0 + NB > base;
+          // columns that this row does not see
+          bool part_of = live && (klo > j0 || khi < j0 + NB);
+          int2 dr = make_int2(doc, doc);
+          if (docs) {
+            dr = blocks.range[j];
+            part_of |= live && (dr.x != doc || dr.y != doc);
+          }
+          const bool masked = __any_sync(~0u, part_of) || absent;
+          if (mods || masked) {
+            // scores formed and masked in tensor memory, 32 at a time: beside the pass below
+            // they would not fit the registers
+#pragma unroll 1
+            for (int c0 = 0; c0 < NB; c0 += 32) {
+              float v[32];
+              tmem_ld32(s_at + c0, v);
+              tmem_ld_wait();
+              if (p.cap > 0.f) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] = cap2 * tanh_of(v[c] * into);
+              } else if (mods) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] *= sc;
+              }
+              if (p.slopes) {
+                const float far = (float)(place - j0 - c0);
+                if (in_tree) {
+#pragma unroll
+                  for (int c = 0; c < 32; ++c) {
+                    const int t = j0 + c0 + c - base;
+                    v[c] -= slope * fabsf(t < 0 ? far - (float)c : (float)(place - base - sh.depth[min(t, 63)]));
+                  }
+                } else {
+#pragma unroll
+                  for (int c = 0; c < 32; ++c) v[c] -= slope * fabsf(far - (float)c);
+                }
+              }
+              if (masked) {
+                const int k0 = j0 + c0;
+                uint32_t bits = live ? columns(klo, khi, k0) : 0u;
+                if (in_tree) {
+                  const int off = k0 - base;
+                  bits |= off >= 0 ? (off < 64 ? (uint32_t)(sees >> off) : 0u) : off > -32 ? (uint32_t)sees << -off : 0u;
+                }
+                if (docs) {
+                  if (dr.x == dr.y) {
+                    bits = dr.x == doc ? bits : 0u;
+                  } else if (__any_sync(~0u, bits != 0u)) {
+                    uint32_t same = 0;
+                    for (int i = 0; i < 32; ++i)
+                      if (k0 + i < L && docs[k0 + i] == doc) same |= 1u << i;
+                    bits &= same;
+                  }
+                }
+                if (PAGED && absent) {
+                  for (int i = 0; i < 32; i += 16) {
+                    const int pg = (k0 + i) / p.page_size;
+                    const int page = k0 + i < L ? p.table[b * p.table_stride + pg] : 0;
+                    if (page < 0 || page >= p.n_pages) bits &= ~(0xffffu << i);
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!(bits >> i & 1)) v[i] = -CUDART_INF_F;
+              }
+              tmem_st32(s_at + c0, reinterpret_cast<const uint32_t*>(v));
+            }
+            tmem_st_wait();
+          }
+          float v[NB];
+#pragma unroll
+          for (int c = 0; c < NB; c += 32) tmem_ld32(s_at + c, v + c);
+          tmem_ld_wait();
+          float x0 = v[0], x1 = v[1], x2 = v[2], x3 = v[3];
+#pragma unroll
+          for (int c = 4; c < NB; c += 4)
+            x0 = fmaxf(x0, v[c]), x1 = fmaxf(x1, v[c + 1]), x2 = fmaxf(x2, v[c + 2]), x3 = fmaxf(x3, v[c + 3]);
+          const float x = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+          const bool grows = live && fmaf(x, by, mref) > AT_BIAS + AT_SLACK;
+          if (__any_sync(~0u, grows)) {
+            float f = 1.f;
+            if (grows) {
+              if (top != -CUDART_INF_F) f = ex2((top - x) * by);
+              top = x;
+              l *= f;
+              mref = AT_BIAS - __fmul_rn(x, by);
+            }
+            if (k > 0) {
+              // O by the same factor, between its products (these scores were issued behind the
+              // product before the last, so the parity is that of one of two phases)
+              if (!(ok = wait(&sh.o_done[tile], (k - 1) & 1))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_at + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st16(o_at + c, o);
+              }
+            }
+          }
+          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+          for (int c0 = 0; c0 < NB; c0 += 64) {
+            uint32_t w[32];
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+              float* e = v + c0 + c;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) e[i] = ex2(fmaf(e[i], by, mref));
+              s0 += e[0], s1 += e[1], s2 += e[2], s3 += e[3];
+              w[c / 2] = pack16<(BF16 && !E4)>(e[0], e[1]);
+              w[c / 2 + 1] = pack16<(BF16 && !E4)>(e[2], e[3]);
+            }
+            tmem_st32(s_at + c0 / 2, w);
+          }
+          l += (s0 + s1) + (s2 + s3);
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[buf]);
+      }
+      // ---- this row's result --------------------------------------------------
+      // (not by o_done: a warp that has not watched it may be two products behind, which its
+      // parity does not show)
+      if (ok && any && k > 0) ok = wait(&sh.o_last[tile], 0);
+      if (ok && any) {
+        tc_fence_after();
+        const float vscale = E4 && p.v_scale ? p.v_scale[h] : 1.f;
+        const float mine = top == -CUDART_INF_F ? top : __fmul_rn(top, by);
+        const int64_t part_row = ((int64_t)blockIdx.x * TILES + tile) * 128 + row;
+        const float inv = l > 0.f ? vscale / l : l == 0.f ? 0.f : l;   // a NaN stays one
+        uint16_t* out = static_cast<uint16_t*>(p.out) + b * p.os[0] + (int64_t)token * p.os[1] + head * p.os[2];
+        if (live) {
+          if (p.splits > 1) p.part_ml[part_row] = make_float2(mine, l);
+          else if (p.lse)
+            p.lse[((int64_t)b * p.nq + token) * p.Hq + head] =
+                l == 0.f ? -CUDART_INF_F : (mine + (log2f(l) - AT_BIAS)) * 0.6931471805599453f;
+        }
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          if (k > 0) {
+            tmem_ld32(o_at + c, o);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i];
+          if (live) {
+            if (p.splits > 1) {
+              float4* to = reinterpret_cast<float4*>(p.part_o + part_row * D + c);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                to[i] = make_float4(o[4 * i] * vscale, o[4 * i + 1] * vscale, o[4 * i + 2] * vscale, o[4 * i + 3] * vscale);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint4 u;
+                u.x = pack16<BF16>(o[8 * i] * inv, o[8 * i + 1] * inv);
+                u.y = pack16<BF16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
+                u.z = pack16<BF16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
+                u.w = pack16<BF16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
+                *reinterpret_cast<uint4*>(out + c + 8 * i) = u;
+              }
+            }
+          }
+        }
+      }
+    }
+  } else if constexpr (E4) {
+    // ---- widening: 8-bit tiles to fp16 ----------------------------------------
+    const int row = tid & 127;
+    {
+      // queries: fp16 and bf16 both go to fp16, a row scaled by a power of two so that its
+      // largest element lies in [1, 2)
+      const int rt = row / p.g, head = h * p.g + (row - rt * p.g), token = t0 + rt;
+      const bool live = rt < TT && token < t1;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q) + b * p.qs[0] + (int64_t)(live ? token : 0) * p.qs[1] +
+                          (live ? head : 0) * p.qs[2];
+      auto get = [&](uint32_t w, int i) {
+        const uint16_t u = (uint16_t)(w >> (16 * i));
+        return BF16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
+      };
+      float big = 0.f;
+      if (live)
+        for (int c = 0; c < D; c += 8) {
+          const uint4 u = *reinterpret_cast<const uint4*>(q + c);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(get(w[i / 2], i % 2)));
+        }
+      int e = (int)(__float_as_uint(big) >> 23) - 127;
+      if (e < -100 || e > 126) e = 0;                    // zero, tiny or infinite: as it is
+      const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+      sh.q_scale[row] = __uint_as_float((uint32_t)(127 + e) << 23);
+      for (int c = 0; c < D; c += 8) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (live) {
+          u = *reinterpret_cast<const uint4*>(q + c);
+          uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = pack16<false>(get(w[i], 0) * f, get(w[i], 1) * f);
+          u = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        *reinterpret_cast<uint4*>(smem_p + (c / 64) * 128 * 128 + row * 128 + (((c / 8) & 7) ^ (row & 7)) * 16) = u;
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full);
+    }
+    int n = 0;
+    bool ok = true;
+    auto widen = [&](int j, bool values) {
+      if (!ok) return;
+      const int rs = n % C::RAWS, s = n % C::STAGES;
+      if (!(ok = wait(&sh.raw_full[rs], (n / C::RAWS) & 1))) return;
+      if (n >= C::STAGES && !(ok = wait(&sh.empty[s], (n / C::STAGES - 1) & 1))) return;
+      const uint8_t* from = smem_p + C::QTILE + C::STAGES * C::TILE + rs * C::RAW;
+      uint8_t* to = smem_p + C::QTILE + s * C::TILE;
+      const int keep = values ? L - j * NB : NB;        // rows behind the sequence become zeros
+#pragma unroll 4
+      for (int i = row; i < NB * D / 16; i += 128) {
+        const int r = i / (D / 16), c = i - r * (D / 16);
+        const uint4 u = *reinterpret_cast<const uint4*>(from + i * 16);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+              : "=r"(o[2 * x]), "=r"(o[2 * x + 1])
+              : "r"(w[x]));
+        if (r >= keep) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) o[x] = 0u;
+        }
+        uint8_t* at = to + (c / 4) * NB * 128 + r * 128;
+        const int ch = (2 * c) & 7;
+        *reinterpret_cast<uint4*>(at + ((ch ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.raw_empty[rs]);
+        mbar_arrive(&sh.full[s]);
+      }
+      ++n;
+    };
+    int cur = blocks.next();
+    if (cur >= 0) widen(cur, false);
+    int nxt = cur >= 0 ? blocks.next() : -1;
+    if (nxt >= 0) widen(nxt, false);
+    while (cur >= 0 && ok) {
+      const int then = nxt >= 0 ? blocks.next() : -1;
+      widen(cur, true);
+      if (then >= 0) widen(then, false);
+      cur = nxt;
+      nxt = then;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, int TILES, int FROM, bool BF16>
+cudaError_t launch_at(const AttendParams& p, cudaStream_t st) {
+  using C = AT<D, TILES, FROM>;
+  CUtensorMap qmap, kmap, vmap;
+  std::memset(&qmap, 0, sizeof(qmap));
+  int unit = C::NB;
+  // the stride of an extent of 1 is never walked, but has to be one that a map takes
+  auto walked = [](int64_t stride, int64_t extent) { return (uint64_t)(extent > 1 ? stride * 2 : 16); };
+  if constexpr (FROM == FROM_TENSORS) {
+    const uint32_t box[4] = {64, (uint32_t)C::NB, 1, 1};
+    const uint64_t dim[4] = {(uint64_t)D, (uint64_t)std::max(p.nk, 1), (uint64_t)p.H, (uint64_t)p.B};
+    for (int i = 0; i < 2; ++i) {
+      const int64_t* s = i ? p.vs : p.ks;
+      const uint64_t stride[3] = {walked(s[1], p.nk), walked(s[2], p.H), walked(s[0], p.B)};
+      if (cudaError_t e = encode_map(i ? &vmap : &kmap, p.nk ? (i ? p.v : p.k) : p.q, false, 4, dim, stride, box, true)) return e;
+    }
+  } else {
+    int a = p.page_size, r = C::NB;
+    while (r) {
+      const int t = a % r;
+      a = r, r = t;
+    }
+    unit = a;
+    const uint64_t dim[2] = {(uint64_t)D, (uint64_t)p.n_pages * p.H * p.page_size};
+    const uint64_t stride[1] = {(uint64_t)D * (C::E4 ? 1 : 2)};
+    const uint32_t box[2] = {C::E4 ? (uint32_t)D : 64u, (uint32_t)unit};
+    for (int i = 0; i < 2; ++i)
+      if (cudaError_t e = encode_map(i ? &vmap : &kmap, i ? p.v : p.k, C::E4, 2, dim, stride, box, !C::E4)) return e;
+  }
+  if constexpr (!C::E4) {
+    const uint64_t dim[4] = {(uint64_t)D, (uint64_t)p.Hq, (uint64_t)p.nq, (uint64_t)p.B};
+    const uint64_t stride[3] = {walked(p.qs[2], p.Hq), walked(p.qs[1], p.nq), walked(p.qs[0], p.B)};
+    const uint32_t box[4] = {64, (uint32_t)p.g, (uint32_t)p.tile_tokens, 1};
+    if (cudaError_t e = encode_map(&qmap, p.q, false, 4, dim, stride, box, true)) return e;
+  }
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, TILES, FROM, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = (int64_t)p.B * p.H * p.groups * p.splits;
+  return launch_kernel(attend_kernel<D, TILES, FROM, BF16>, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, st, true, 0, p,
+                       qmap, kmap, vmap, unit);
+}
+
+template <int D, int TILES, bool BF16>
+cudaError_t launch_from(const AttendParams& p, cudaStream_t st) {
+  if (!p.table) return launch_at<D, TILES, FROM_TENSORS, BF16>(p, st);
+  if (p.cache_type != MKV_DT_E4M3) return launch_at<D, TILES, FROM_PAGES, BF16>(p, st);
+  return launch_at<D, 1, FROM_BYTES, BF16>(p, st);
+}
+
+template <int D>
+cudaError_t launch_attend_d(const AttendParams& p, cudaStream_t st) {
+  if constexpr (D < 256)
+    if (p.tiles == 2) return p.bf16 ? launch_from<D, 2, true>(p, st) : launch_from<D, 2, false>(p, st);
+  return p.bf16 ? launch_from<D, 1, true>(p, st) : launch_from<D, 1, false>(p, st);
+}
+
+}  // namespace
+}  // namespace mkv

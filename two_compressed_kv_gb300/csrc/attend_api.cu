@@ -183,6 +183,87 @@ bool strides_ok(const int64_t* s, int64_t e0, int64_t e1, int64_t e2) {
   return true;
 }
 
+// How a call's rows and keys are spread, and where its workspace's parts lie.
+struct AttendLayout {
+  int tiles, tile_tokens, groups, splits;
+  uint64_t docs, part_o, part_ml, total;   // byte offsets
+};
+
+// What a CTA costs apart from its blocks of keys, in blocks, and what a join costs.
+constexpr int kCtaBlocks = 4, kJoinBlocks = 3;
+
+// Row tiles: 128 / g tokens each.  Two to a CTA where there are two (each softmax then
+// has its own S buffer and K and V are read half as often), but not with heads of 256
+// (tensor memory) or 8-bit pages (their second warpgroup widens).
+AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, int window, bool e4m3, bool docs, int sms) {
+  AttendLayout l;
+  l.tile_tokens = 128 / g;
+  const int64_t all = up(std::max<int64_t>(nq, 1), l.tile_tokens);
+  l.tiles = all > 1 && D < 256 && !e4m3 ? 2 : 1;
+  l.groups = (int)up(all, l.tiles);
+  const int NB = attend_block(D);
+  const int64_t items = (int64_t)B * H * l.groups;
+  int64_t keys = nk;
+  if (window) keys = std::min<int64_t>(nk, (int64_t)window + l.tiles * l.tile_tokens + NB);
+  const int64_t blocks = up(keys, NB);
+  l.splits = 1;
+  // a few rows over many keys: parts of the keys, joined by a second kernel
+  int64_t best = up(items, sms) * (blocks + kCtaBlocks);
+  for (int s = 2; s <= 64 && s <= blocks && items * s <= 16 * (int64_t)sms; ++s) {
+    const int64_t cost = up(items * s, sms) * (up(blocks, s) + kCtaBlocks) + kJoinBlocks;
+    if (cost < best) best = cost, l.splits = s;
+  }
+  uint64_t at = 0;
+  auto place = [&](uint64_t bytes) {
+    const uint64_t here = at;
+    at += (bytes + 255) & ~(uint64_t)255;
+    return here;
+  };
+  const uint64_t rows = l.splits > 1 ? (uint64_t)items * l.splits * l.tiles * 128 : 0;
+  l.docs = place(docs ? (uint64_t)B * up(nk, NB) * 8 : 0);
+  l.part_o = place(rows * D * 4);
+  l.part_ml = place(rows * 8);
+  l.total = at;
+  return l;
+}
+
+AttendLayout prefill_layout(const mkv_prefill_args* a, int sms) {
+  return attend_layout(a->batch, a->n_kv_heads, a->n_q_heads / a->n_kv_heads, a->head_dim, a->q_tokens, a->kv_tokens,
+                       a->window, false, a->docs != nullptr, sms);
+}
+
+int64_t attend_limit(const mkv_paged_cache* c, const mkv_paged_attend_args* a) {
+  const int64_t cap = (int64_t)c->max_pages * c->page_size;
+  return a->max_len ? std::min(a->max_len, cap) : cap;
+}
+
+AttendLayout paged_layout(const mkv_paged_cache* c, const mkv_paged_attend_args* a, int sms) {
+  return attend_layout(c->batch, c->n_kv_heads, a->n_q_heads / c->n_kv_heads, c->head_dim, a->n, attend_limit(c, a),
+                       a->window, c->dtype == MKV_DT_E4M3, false, sms);
+}
+
+// Takes over a layout and launches.
+mkv_status attend(AttendParams& p, const AttendLayout& l, void* workspace, mkv_stream_t stream) {
+  if ((int64_t)p.B * p.H * l.groups * l.splits > kMaxGrid) return bad("attention: too many queries");
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.tiles = l.tiles;
+  p.tile_tokens = l.tile_tokens;
+  p.groups = l.groups;
+  p.splits = l.splits;
+  p.doc_range = reinterpret_cast<int2*>(ws + l.docs);
+  p.part_o = reinterpret_cast<float*>(ws + l.part_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (p.docs) CKP(launch_attend_docs(p, st));
+  switch (p.D) {
+    case 64: CKP(launch_attend_64(p, st)); break;
+    case 128: CKP(launch_attend_128(p, st)); break;
+    default: CKP(launch_attend_256(p, st)); break;
+  }
+  if (l.splits > 1) CKP(launch_attend_join(p, st));
+  return MKV_OK;
+}
+
 float scale_of(float scale, int head_dim) {
   return scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)head_dim));
 }
@@ -219,7 +300,9 @@ uint64_t mkv_prefill_workspace(const mkv_prefill_args* a) {
     bad(e);
     return UINT64_MAX;
   }
-  return 0;
+  int sms = 0;
+  if (a->batch == 0 || a->q_tokens == 0) return 0;
+  return sm_count(&sms) == MKV_OK ? prefill_layout(a, sms).total : UINT64_MAX;
 }
 
 mkv_status mkv_prefill(const mkv_prefill_args* a, mkv_stream_t stream) {
@@ -233,6 +316,11 @@ mkv_status mkv_prefill(const mkv_prefill_args* a, mkv_stream_t stream) {
       !strides_ok(a->k_stride, a->batch, a->kv_tokens, a->n_kv_heads) ||
       !strides_ok(a->v_stride, a->batch, a->kv_tokens, a->n_kv_heads))
     return bad("mkv_prefill: strides must be positive multiples of 8 elements");
+  int sms = 0;
+  if (mkv_status s = sm_count(&sms)) return s;
+  const AttendLayout l = prefill_layout(a, sms);
+  if (l.total && (!a->workspace || !aligned16(a->workspace))) return bad("mkv_prefill: workspace must be 16-byte aligned");
+  if (a->workspace_bytes < l.total) return bad("mkv_prefill: workspace too small");
   AttendParams p;
   std::memset(&p, 0, sizeof(p));
   p.q = a->q;
@@ -264,8 +352,8 @@ mkv_status mkv_prefill(const mkv_prefill_args* a, mkv_stream_t stream) {
   p.cap = a->cap;
   p.k = a->k;
   p.v = a->v;
-  CKP(launch_attend(p, reinterpret_cast<cudaStream_t>(stream)));
-  return MKV_OK;
+  p.status = a->status;
+  return attend(p, l, a->workspace, stream);
 }
 
 uint64_t mkv_paged_attend_workspace(const mkv_paged_cache* c, const mkv_paged_attend_args* a) {
@@ -273,7 +361,9 @@ uint64_t mkv_paged_attend_workspace(const mkv_paged_cache* c, const mkv_paged_at
     bad(e);
     return UINT64_MAX;
   }
-  return 0;
+  int sms = 0;
+  if (a->n == 0) return 0;
+  return sm_count(&sms) == MKV_OK ? paged_layout(c, a, sms).total : UINT64_MAX;
 }
 
 mkv_status mkv_paged_attend(const mkv_paged_cache* c, const mkv_paged_attend_args* a, mkv_stream_t stream) {
@@ -283,6 +373,12 @@ mkv_status mkv_paged_attend(const mkv_paged_cache* c, const mkv_paged_attend_arg
   if (!aligned16(a->q) || !aligned16(a->out)) return bad("mkv_paged_attend: q and out must be 16-byte aligned");
   if (!strides_ok(a->q_stride, c->batch, a->n, a->n_q_heads))
     return bad("mkv_paged_attend: q's strides must be positive multiples of 8 elements");
+  int sms = 0;
+  if (mkv_status s = sm_count(&sms)) return s;
+  const AttendLayout l = paged_layout(c, a, sms);
+  if (l.total && (!a->workspace || !aligned16(a->workspace)))
+    return bad("mkv_paged_attend: workspace must be 16-byte aligned");
+  if (a->workspace_bytes < l.total) return bad("mkv_paged_attend: workspace too small");
   AttendParams p;
   std::memset(&p, 0, sizeof(p));
   p.q = a->q;
@@ -298,8 +394,7 @@ mkv_status mkv_paged_attend(const mkv_paged_cache* c, const mkv_paged_attend_arg
   p.g = a->n_q_heads / c->n_kv_heads;
   p.D = c->head_dim;
   p.nq = a->n;
-  const int64_t cap = (int64_t)c->max_pages * c->page_size;
-  p.nk = (int)(a->max_len ? std::min(a->max_len, cap) : cap);
+  p.nk = (int)attend_limit(c, a);
   p.bf16 = a->q_dtype == MKV_DT_BF16;
   p.q_lens = a->new_lens;
   p.kv_lens = a->seq_lens;
@@ -319,8 +414,7 @@ mkv_status mkv_paged_attend(const mkv_paged_cache* c, const mkv_paged_attend_arg
   p.k_scale = c->k_scale;
   p.v_scale = c->v_scale;
   p.status = c->status;
-  CKP(launch_attend(p, reinterpret_cast<cudaStream_t>(stream)));
-  return MKV_OK;
+  return attend(p, l, a->workspace, stream);
 }
 
 }  // extern "C"

@@ -6,6 +6,12 @@
 
 namespace mkv {
 
+constexpr float AT_BIAS = 8.f;     // weights carry a factor 2^8 until the division by their sum
+constexpr float AT_SLACK = 6.f;    // how far scores (log2) may pass the reference of the exponents
+
+// Keys of a block: the step of the pass over the keys.
+constexpr int attend_block(int D) { return D == 256 ? 64 : 128; }
+
 struct AttendParams {
   const void* q;
   void* out;
@@ -19,10 +25,12 @@ struct AttendParams {
   const int32_t* prefix;
   const int32_t* docs;
   int64_t docs_stride;
+  int2* doc_range;             // workspace: [B][blocks of keys] smallest and largest document
   const uint64_t* tree;
   const float* slopes;
   int causal, window;
   float scale, cap;
+  int32_t* status;
   // keys in tensors
   const void *k, *v;
   int64_t ks[3], vs[3];
@@ -31,9 +39,32 @@ struct AttendParams {
   int64_t table_stride;
   int n_pages, page_size, cache_type;
   const float *k_scale, *v_scale;
-  int32_t* status;
+  // the grid: row tiles of a (sequence, KV head) in groups of `tiles`, their keys in `splits` parts
+  int tile_tokens;             // tokens of a row tile: 128 / g
+  int tiles;                   // row tiles of a CTA: 1 or 2
+  int groups;                  // of row tiles
+  int splits;
+  float* part_o;               // workspace: [item][tiles][128][D] sums over weights, splits > 1
+  float2* part_ml;             // [item][tiles][128] reference (log2 domain) and sum of weights
 };
 
-cudaError_t launch_attend(const AttendParams& p, cudaStream_t st);
+// What a sequence's lengths come to: queries and keys, both within their bounds.
+__device__ __forceinline__ void attend_lens(const AttendParams& p, int b, int& m, int& L, bool& outside) {
+  const int k = p.kv_lens ? p.kv_lens[b] : p.nk, q = p.q_lens ? p.q_lens[b] : p.nq;
+  L = max(0, min(k, p.nk));
+  m = max(0, min(q, p.nq));
+  if (p.table) m = min(m, L);
+  outside = L != k || (p.q_lens && m != q);
+}
+
+cudaError_t launch_attend_64(const AttendParams& p, cudaStream_t st);
+cudaError_t launch_attend_128(const AttendParams& p, cudaStream_t st);
+cudaError_t launch_attend_256(const AttendParams& p, cudaStream_t st);
+cudaError_t launch_attend_docs(const AttendParams& p, cudaStream_t st);
+cudaError_t launch_attend_join(const AttendParams& p, cudaStream_t st);
+
+// A tensor map of up to four dimensions (the first contiguous, strides in bytes), 128-byte swizzled or not.
+cudaError_t encode_map(CUtensorMap* map, const void* base, bool bytes, int rank, const uint64_t* dim,
+                       const uint64_t* stride, const uint32_t* box, bool swizzle);
 
 }  // namespace mkv

@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 
 #include "api_common.cuh"
+#include "attend_internal.cuh"
 
 using namespace mkv;
 
@@ -341,8 +342,9 @@ mkv_status rope_params(const mkv_rope_plan* plan, const mkv_rope_args* a, RopePa
 
 namespace mkv {
 
-cudaError_t encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int row_bytes, int box_rows) {
-  // the driver's encoder, looked up once: it is the process's, not a device's
+namespace {
+// The driver's encoder, looked up once: it is the process's, not a device's.
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -351,6 +353,12 @@ cudaError_t encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, in
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(
         e == cudaSuccess && found == cudaDriverEntryPointSuccess ? fn : nullptr);
   }();
+  return encode;
+}
+}  // namespace
+
+cudaError_t encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int row_bytes, int box_rows) {
+  const auto encode = encoder();
   if (!encode) return cudaErrorNotSupported;
   const cuuint32_t w = row_bytes < 128 ? row_bytes : 128;
   // columns of w bytes, rows, column groups of a row
@@ -361,6 +369,21 @@ cudaError_t encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, in
   const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dim, stride, box, step,
                             CU_TENSOR_MAP_INTERLEAVE_NONE,
                             w == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_map(CUtensorMap* map, const void* base, bool bytes, int rank, const uint64_t* dim,
+                       const uint64_t* stride, const uint32_t* box, bool swizzle) {
+  const auto encode = encoder();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  cuuint64_t d[4], s[3];
+  for (int i = 0; i < rank; ++i) d[i] = dim[i];
+  for (int i = 0; i + 1 < rank; ++i) s[i] = stride[i];
+  const CUresult r = encode(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, rank,
+                            const_cast<void*>(base), d, s, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

@@ -337,8 +337,8 @@ long norm_rope(PyObject* const* v) {
   return lib.norm_rope_grad(plan, axes, &a, l.stream);
 }
 
-// prefill(q, k, v, out, lse, q_lens, kv_lens, prefix, docs, slopes, causal, window, scale, cap, workspace, stream)
-//   -> status
+// prefill(q, k, v, out, lse, q_lens, kv_lens, prefix, docs, slopes, causal, window, scale, cap, workspace, stream,
+//         status) -> status
 long prefill(PyObject* const* v) {
   const at::Tensor &q = tensor(v[0], "q"), &k = tensor(v[1], "k"), &val = tensor(v[2], "v"), &out = tensor(v[3], "out");
   const int dev = q.get_device();
@@ -375,6 +375,7 @@ long prefill(PyObject* const* v) {
     a.docs_stride = docs.stride(0);
   }
   a.slopes = flat<float>(v[9], "slopes", dev, at::kFloat, {a.n_q_heads});
+  a.status = flat<int32_t>(v[16], "status", dev, at::kInt, {1});
   a.causal = integer32(v[10], "causal");
   a.window = integer32(v[11], "window");
   a.scale = number(v[12], "scale");
@@ -562,7 +563,7 @@ long bind(PyObject* const* v) {
 
 #define ENTRY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(bind, 14), ENTRY(rope, 7), ENTRY(append, 13), ENTRY(decode, 12), ENTRY(evict, 17),
-                         ENTRY(rope_multi, 7), ENTRY(norm_rope, 18), ENTRY(prefill, 16), ENTRY(attend, 15),
+                         ENTRY(rope_multi, 7), ENTRY(norm_rope, 18), ENTRY(prefill, 17), ENTRY(attend, 15),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

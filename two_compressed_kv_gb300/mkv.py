@@ -151,7 +151,7 @@ class mkv_norm_rope_args(Structure):
 class mkv_prefill_args(Structure):
     _fields_ = [("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("out", c_void_p),
                 ("lse", c_void_p), ("q_lens", c_void_p), ("kv_lens", c_void_p),
-                ("prefix", c_void_p), ("docs", c_void_p), ("slopes", c_void_p),
+                ("prefix", c_void_p), ("docs", c_void_p), ("slopes", c_void_p), ("status", c_void_p),
                 ("workspace", c_void_p), ("workspace_bytes", c_uint64), ("q_stride", c_int64 * 3),
                 ("k_stride", c_int64 * 3), ("v_stride", c_int64 * 3), ("out_stride", c_int64 * 3),
                 ("docs_stride", c_int64), ("q_tokens", c_int64), ("kv_tokens", c_int64),
@@ -750,7 +750,7 @@ def mkv_norm_rope_grad_workspace(plan, device=None) -> int:
 
 
 def mkv_prefill(q, k, v, out=None, lse=None, causal=True, window=0, prefix=None, docs=None, q_lens=None,
-                kv_lens=None, scale=0.0, cap=0.0, slopes=None, workspace=None, stream=None):
+                kv_lens=None, scale=0.0, cap=0.0, slopes=None, status=None, workspace=None, stream=None):
     """Attention of a prompt: q [batch, tokens, q_heads, head_dim] over k, v [batch, kv_tokens,
     kv_heads, head_dim] (fp16 or bf16, strided; a transposed view of a [batch, heads, tokens,
     head_dim] tensor is as good).  The last query stands at the last key; q_lens, kv_lens int32
@@ -758,13 +758,13 @@ def mkv_prefill(q, k, v, out=None, lse=None, causal=True, window=0, prefix=None,
     prefix (int32 [batch]: keys seen by all queries), docs (int32 [batch, kv_tokens]: only keys of
     the query's document): which keys a query sees.  cap: scores become cap * tanh(score / cap);
     slopes (fp32 [q_heads]): slope * distance is taken off.  lse: fp32 [batch, tokens, q_heads] or
-    None.  Returns out (new where None), of q's shape and type; rows behind q_lens are left as they
-    were."""
+    None.  status: int32 [1] or None: set where a bounded wait gave up (outputs undefined then).
+    Returns out (new where None), of q's shape and type; rows behind q_lens are left as they were."""
     m = _native()
     if out is None and isinstance(q, _T.Tensor):
         out = _new(q.shape, q.dtype, q.device, stream)
     _check(m.prefill(q, k, v, out, lse, q_lens, kv_lens, prefix, docs, slopes, causal, window, scale, cap, workspace,
-                     _address(stream)), "mkv_prefill")
+                     _address(stream), status), "mkv_prefill")
     return out
 
 
@@ -785,10 +785,11 @@ def mkv_paged_attend(cache, q, seq_lens, tree=None, new_lens=None, out=None, lse
     return out
 
 
-def mkv_paged_attend_workspace(cache, new_tokens, q_heads, max_len=0) -> int:
-    """Bytes of workspace of mkv_paged_attend for these sizes."""
+def mkv_paged_attend_workspace(cache, new_tokens, q_heads, max_len=0, window=0) -> int:
+    """Bytes of workspace of mkv_paged_attend for these sizes; 0: it needs none."""
     qt = MKV_DT_F16 if cache.view.dtype == MKV_DT_E4M3 else cache.view.dtype
-    a = mkv_paged_attend_args(n=new_tokens, n_q_heads=q_heads, max_len=max_len, q_dtype=qt)
+    a = mkv_paged_attend_args(n=new_tokens, n_q_heads=q_heads, max_len=max_len, q_dtype=qt,
+                              window=window)
     with _T.cuda.device(cache.device):
         n = _lib.mkv_paged_attend_workspace(ctypes.byref(cache.view), ctypes.byref(a))
     if n == 2**64 - 1:
