@@ -28,7 +28,7 @@ const char* norm_sizes(const mkv_rope_plan* plan, const mkv_norm_rope_args* a, b
     return "mkv_norm_rope: weights must be of x's type or F32";
   if (!(a->eps >= 0.f) || std::isinf(a->eps)) return "mkv_norm_rope: eps must be >= 0 and finite";
   if (!std::isfinite(a->weight_offset)) return "mkv_norm_rope: weight_offset must be finite";
-  const int es = elem_bytes(a->dtype), V = 16 / es;
+  const int es = elem_bytes(a->dtype), bytes = norm_vector_bytes(es == 2, grad), V = bytes / es;
   bool vec = plan->head_dim % V == 0 && plan->rot_dim % (plan->interleaved ? V : 2 * V) == 0;
   const int64_t extent[3] = {a->batch, a->tokens, 0};
   for (int s = 0; s < 2; ++s) {
@@ -36,7 +36,7 @@ const char* norm_sizes(const mkv_rope_plan* plan, const mkv_norm_rope_args* a, b
     uintptr_t mask = reinterpret_cast<uintptr_t>(a->x[s]) | reinterpret_cast<uintptr_t>(a->out[s]);
     if (grad) mask |= reinterpret_cast<uintptr_t>(a->grad[s]);
     if (mask & (uintptr_t)(es - 1)) return "mkv_norm_rope: tensors must be aligned to their elements";
-    vec = vec && (mask & 15u) == 0;
+    vec = vec && (mask & (uintptr_t)(bytes - 1)) == 0;
     for (int i = 0; i < 3; ++i) {
       const int64_t n = i < 2 ? extent[i] : a->heads[s];
       if (n <= 1) continue;
@@ -54,16 +54,33 @@ const char* norm_sizes(const mkv_rope_plan* plan, const mkv_norm_rope_args* a, b
   return nullptr;
 }
 
-// Heads a group of lanes takes, chunks of the list and blocks of the grid.
+// Blocks of both sides: at most so many per SM.  A gradient's are those that run at
+// once, as its sums of a block go through memory (84 us with 2, 94 with 4).
+constexpr int norm_blocks(bool grad) { return grad ? 2 : 4; }
+
+// Heads a group of lanes takes, a side's items and blocks.
 void norm_grid(const mkv_norm_rope_args* a, bool grad, int sms, NormRopeParams* p) {
-  const int heads = a->heads[0] + a->heads[1], per_block = 256 / p->lanes;
   const int64_t rows = (int64_t)a->batch * a->tokens;
-  p->heads_per = heads_per_thread(rows * p->lanes, heads, (int64_t)sms * 2048, 16);
-  p->chunks = (int)up(heads, p->heads_per);
-  p->items = rows * p->chunks;
-  const int64_t blocks = up(p->items, per_block);
-  // the gradient's sums of a block go through memory: as many blocks as run at once
-  p->blocks = (int)std::min<int64_t>(blocks, grad ? (int64_t)sms * 4 : (int64_t)sms * 64);
+  const int per_block = 256 / p->lanes;
+  const int heads[2] = {a->heads[0], a->heads[1]};
+  p->heads_per = heads_per_thread(rows * p->lanes, heads[0] + heads[1], (int64_t)sms * 2048, 16);
+  int64_t need[2], all = 0;
+  for (int s = 0; s < 2; ++s) {
+    p->chunks[s] = (int)up(heads[s], p->heads_per);
+    p->items[s] = rows * p->chunks[s];
+    need[s] = up(p->items[s], per_block);
+    all += need[s];
+  }
+  const int64_t most = (int64_t)sms * norm_blocks(grad);
+  for (int s = 0; s < 2; ++s) {
+    const int64_t share = heads[s] * most / (heads[0] + heads[1]);
+    p->blocks[s] = (int)(all <= most ? need[s] : std::min(need[s], std::max<int64_t>(share, 1)));
+  }
+}
+
+// A block more than the share of each side, at most.
+uint64_t norm_workspace(const mkv_rope_plan* plan, int sms) {
+  return (uint64_t)(sms * norm_blocks(true) + 2) * plan->head_dim * 4;
 }
 
 mkv_status norm_call(const mkv_rope_plan* plan, const mkv_rope_axes* axes, const mkv_norm_rope_args* a, bool grad,
@@ -124,7 +141,7 @@ mkv_status norm_call(const mkv_rope_plan* plan, const mkv_rope_axes* axes, const
   norm_grid(a, grad, sms, &p);
   if (wants) {
     if (!a->workspace || !aligned16(a->workspace)) return bad("mkv_norm_rope_grad: workspace must be 16-byte aligned");
-    if (a->workspace_bytes < (uint64_t)p.blocks * 2 * plan->head_dim * 4) return bad("mkv_norm_rope_grad: workspace too small");
+    if (a->workspace_bytes < norm_workspace(plan, sms)) return bad("mkv_norm_rope_grad: workspace too small");
     p.part = static_cast<float*>(a->workspace);
     for (int s = 0; s < 2; ++s) p.weight_grad[s] = a->weight_grad[s];
   }
@@ -291,8 +308,7 @@ uint64_t mkv_norm_rope_grad_workspace(const mkv_rope_plan* plan, const mkv_norm_
   }
   if (!a->weight_grad[0] && !a->weight_grad[1]) return 0;
   if (sm_count(&sms) != MKV_OK) return 0;
-  // enough for every form that these sizes may take
-  return (uint64_t)sms * 4 * 2 * plan->head_dim * 4;
+  return norm_workspace(plan, sms);
 }
 
 uint64_t mkv_prefill_workspace(const mkv_prefill_args* a) {
