@@ -58,6 +58,9 @@ struct AT {
   static constexpr int SMEM = TILES * QTILE + STAGES * TILE + RAWS * RAW + 1024;
   static constexpr int THREADS = TILES == 2 || E4 ? 384 : 256;
   static constexpr int S_COL = 0, O_COL = 2 * NB;          // tensor memory columns
+  // Weights are handed over in parts, so that the products with the first keys' values
+  // run while the other weights are formed.
+  static constexpr int PARTS = TILES == 2 ? 2 : 1, PK = NB / PARTS;
   static_assert(O_COL + TILES * D <= 512, "tensor memory");
   static_assert(SMEM <= 225 * 1024 + 512, "shared memory");
   static_assert(!(E4 && TILES == 2), "the second warpgroup widens");
@@ -89,23 +92,31 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
-// K-major operand: 64 channels a 128-byte row, groups of channels apart.
-// MN-major operand (V): channels contiguous, groups of 64 channels `lead` bytes apart.
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lead) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(lead >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0u;
+}
+// Operand descriptors, 128-byte swizzled, version 1: the upper word (rows of 8 1024
+// bytes apart) is the same for all, the lower one has the address / 16 and the distance
+// of groups of 64 channels / 16 (V, whose channels are contiguous; else not used).
+constexpr uint32_t DESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead) { return (saddr >> 4) | (lead >> 4) << 16; }
+// D[tmem] (+)= A B, A and B in shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "n"(DESC_HI)
+      : "memory");
 }
 // D[tmem] (+)= A[tmem] B
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "n"(DESC_HI)
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
@@ -182,18 +193,33 @@ struct Blocks {
   uint32_t bits;
   const int2* range;     // of the sequence's blocks; NULL: all
   int2 own;              // of the queries' documents
+  // bits of the 32 blocks from `from` on
+  __device__ __forceinline__ uint32_t hits(int from) const {
+    const int i = from + (threadIdx.x & 31);
+    bool hit = false;
+    if (i < end) {
+      const int2 r = range[i];
+      hit = r.x <= own.y && r.y >= own.x;
+    }
+    return __ballot_sync(~0u, hit);
+  }
+  // (how many, the last)
+  __device__ __forceinline__ int2 all() const {
+    if (!range) return make_int2(max(0, end - j), end - 1);
+    int2 r = make_int2(0, -1);
+    for (int from = j; from < end; from += 32) {
+      const uint32_t h = hits(from);
+      r.x += __popc(h);
+      if (h) r.y = from + 31 - __clz(h);
+    }
+    return r;
+  }
   __device__ __forceinline__ int next() {
     if (!range) return j < end ? j++ : -1;
-    const int lane = threadIdx.x & 31;
     while (j < end) {
       if (j >= base + 32) {
         base = j;
-        bool hit = false;
-        if (base + lane < end) {
-          const int2 r = range[base + lane];
-          hit = r.x <= own.y && r.y >= own.x;
-        }
-        bits = __ballot_sync(~0u, hit);
+        bits = hits(base);
       }
       const uint32_t rest = bits >> (j - base);
       if (rest) {
@@ -216,7 +242,7 @@ struct AttendShared {
   uint64_t q_full;
   uint64_t full[8], empty[8];          // K and V tiles as the products take them
   uint64_t raw_full[8], raw_empty[8];  // 8-bit tiles
-  uint64_t s_full[2], p_full[2];       // scores there; weights there
+  uint64_t s_full[2], p_full[2][2];    // scores there; a part of the weights there
   uint64_t o_done[2];                  // another product of a row tile is in O
   uint64_t o_last[2];                  // all are
   uint64_t drained;
@@ -240,7 +266,8 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
   const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const smem_p = smem_raw + (smem0 - smem_u32(smem_raw));
   const uint32_t ring = smem0 + TILES * C::QTILE, raws = ring + C::STAGES * C::TILE;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the same for a warp, and known to be: addresses and descriptors stay in uniform registers
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);
 
   if (warp == 1) {
     tmem_alloc(&sh.tmem, 512);
@@ -256,7 +283,8 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.p_full[i][0], 4);
+      mbar_init(&sh.p_full[i][1], 4);
       mbar_init(&sh.o_done[i], 1);
       mbar_init(&sh.o_last[i], 1);
     }
@@ -329,7 +357,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
   tc_fence_before();
   absent = __syncthreads_or(absent);
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = __shfl_sync(~0u, sh.tmem, 0);
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     const bool ok = __all_sync(~0u, wait_here(bar, parity));
     if (!ok && lane == 0 && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
@@ -337,7 +365,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
   };
 
   if (warp < 4) {
-    if constexpr (C::THREADS == 384) regs_down<88>();
+    if constexpr (C::THREADS == 384) regs_down<(E4 ? 88 : 72)>();
     if (warp == 0) {
       // ---- copies -----------------------------------------------------------
       const bool work = blocks.j < blocks.end;
@@ -416,40 +444,50 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
       // ---- products ---------------------------------------------------------
       constexpr uint32_t IS = idesc_f16_f32(128, NB) | (BF16 && !E4 ? (1u << 7) | (1u << 10) : 0u);
       constexpr uint32_t IO = idesc_f16_f32(128, D) | (BF16 && !E4 ? (1u << 7) | (1u << 10) : 0u) | (1u << 16);
+      // One lane does it all: between two products there is room for some hundred cycles.
+      const int2 all = blocks.all();
+      const int n = all.x;
+      const bool leader = elect_one();
       int slot = 0;
       uint32_t turn = 0;
       bool ok = true;
       auto pop = [&]() {       // the next tile of the ring, once it is there
         const int s = slot;
-        ok = ok && wait(&sh.full[s], turn & 1);
+        ok = ok && wait_here(&sh.full[s], turn & 1);
         if (++slot == C::STAGES) slot = 0, ++turn;
         return s;
       };
       auto scores = [&](int tile, int buf, int s) {
-        if (lane == 0) {
-          const uint32_t qa = smem0 + tile * C::QTILE, ka = ring + s * C::TILE;
+        if (!ok) return;
+        const uint32_t qa = desc_lo(smem0 + tile * C::QTILE, 16), ka = desc_lo(ring + s * C::TILE, 16);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc_mma_f16(tmem + C::S_COL + buf * NB, sdesc_k_sw128(qa + (k / 4) * 128 * 128 + (k % 4) * 32),
-                       sdesc_k_sw128(ka + (k / 4) * NB * 128 + (k % 4) * 32), IS, k > 0);
-          tc_commit(&sh.s_full[buf]);
-        }
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(tmem + C::S_COL + buf * NB, qa + ((k / 4) * 128 * 128 + (k % 4) * 32) / 16,
+                 ka + ((k / 4) * NB * 128 + (k % 4) * 32) / 16, IS, k > 0);
+        tc_commit(&sh.s_full[buf]);
       };
-      auto values = [&](int tile, int buf, int s, bool first, bool last) {
-        if (lane == 0) {
-          const uint32_t va = ring + s * C::TILE;
+      // the products with one part of the weights
+      auto values = [&](int tile, int buf, int s, int part, uint32_t parity, bool first, bool last) {
+        ok = ok && wait_here(&sh.p_full[buf][part], parity);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t va = desc_lo(ring + s * C::TILE, NB * 128) + part * C::PK * 128 / 16;
 #pragma unroll
-          for (int k = 0; k < NB / 16; ++k)
-            tc_mma_ts(tmem + C::O_COL + tile * D, tmem + C::S_COL + buf * NB + k * 8, sdesc_mn(va + k * 2048, NB * 128),
-                      IO, !first || k > 0);
+        for (int k = 0; k < C::PK / 16; ++k)
+          mma_ts(tmem + C::O_COL + tile * D, tmem + C::S_COL + buf * NB + part * (C::PK / 2) + k * 8, va + k * 2048 / 16,
+                 IO, !first || part > 0 || k > 0);
+        if (part == C::PARTS - 1) {
           tc_commit(&sh.o_done[tile]);
           if (last) tc_commit(&sh.o_last[tile]);
         }
       };
+      auto release = [&](int s) { tc_commit(&sh.empty[s]); };
       // What lies behind the sequence in its last block may be anything, and 0 times a
       // NaN is one: those rows of V become zeros (8-bit pages: where they are widened).
-      auto clean = [&](int s, int j) {
-        if (E4 || !ok || (j + 1) * NB <= L) return;
+      // It is the ring's last tile.
+      auto clean = [&](int j) {
+        const int s = (2 * n - 1) % C::STAGES;
+        wait_here(&sh.full[s], ((2 * n - 1) / C::STAGES) & 1);
         uint8_t* at = smem_p + TILES * C::QTILE + s * C::TILE;
         const int r0 = L - j * NB;
         for (int i = lane; i < (NB - r0) * 8; i += 32) {
@@ -458,85 +496,58 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
             *reinterpret_cast<uint4*>(at + c * NB * 128 + (r0 + i / 8) * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async();
-        __syncwarp();
       };
-      auto release = [&](int s) {
-        if (lane == 0) tc_commit(&sh.empty[s]);
-      };
-      int cur = blocks.next();
-      if (cur >= 0) {
-        ok = wait(&sh.q_full, 0);
+      const bool dirty = !E4 && n > 0 && (all.y + 1) * NB > L;
+      int ks = 0, vs = 0;
+      if (leader && n > 0) {
+        ok = wait_here(&sh.q_full, 0);
         tc_fence_after();
-        if constexpr (TILES == 2) {
-          int ks = pop();
-          tc_fence_after();
-          if (ok) {
-            scores(0, 0, ks);
-            scores(1, 1, ks);
-            release(ks);
-          }
-          for (uint32_t k = 0; cur >= 0 && ok; ++k) {
-            const int nxt = blocks.next();
-            int vs = 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              ok = ok && wait(&sh.p_full[i], k & 1);
-              if (i == 0) {
-                vs = pop();
-                clean(vs, cur);
-              }
-              if (!ok) break;
-              tc_fence_after();
-              values(i, i, vs, k == 0, nxt < 0);
-              if (i == 1) release(vs);
-              if (nxt >= 0) {
-                if (i == 0) ks = pop();
-                if (!ok) break;
-                tc_fence_after();
-                scores(i, i, ks);
-                if (i == 1) release(ks);
-              }
-            }
-            cur = nxt;
-          }
-        } else {
-          int nxt = blocks.next();
-          for (int i = 0; i < 2 && ok; ++i)
-            if (i == 0 || nxt >= 0) {
-              const int ks = pop();
-              tc_fence_after();
-              if (!ok) break;
-              scores(0, i, ks);
-              release(ks);
-            }
-          for (uint32_t k = 0; cur >= 0 && ok; ++k) {
-            const int then = nxt >= 0 ? blocks.next() : -1;
-            ok = wait(&sh.p_full[k & 1], (k >> 1) & 1);
-            const int vs = pop();
-            clean(vs, cur);
-            if (!ok) break;
-            tc_fence_after();
-            values(0, k & 1, vs, k == 0, nxt < 0);
-            release(vs);
-            if (then >= 0) {
-              const int ks = pop();
-              if (!ok) break;
-              tc_fence_after();
-              scores(0, k & 1, ks);
-              release(ks);
-            }
-            cur = nxt;
-            nxt = then;
-          }
+        for (int i = 0; i < 2; ++i) {
+          if (TILES == 1 && i == n) break;
+          if (TILES == 1 || i == 0) ks = pop();
+          scores(TILES == 2 ? i : 0, i, ks);
+          if (TILES == 1 || i == 1) release(ks);
         }
       }
+      for (int k = 0; k < n; ++k) {
+        if (k == n - 1 && dirty) {
+          __syncwarp();
+          clean(all.y);
+          __syncwarp();
+        }
+        if (!leader) continue;
+        vs = pop();
+        if constexpr (TILES == 2) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int h = 0; h < C::PARTS; ++h) values(i, i, vs, h, k & 1, k == 0, k == n - 1);
+            if (i == 1) release(vs);
+            if (k + 1 < n) {
+              if (i == 0) ks = pop();
+              scores(i, i, ks);
+              if (i == 1) release(ks);
+            }
+          }
+        } else {
+          values(0, k & 1, vs, 0, (k >> 1) & 1, k == 0, k == n - 1);
+          release(vs);
+          if (k + 2 < n) {
+            ks = pop();
+            scores(0, k & 1, ks);
+            release(ks);
+          }
+        }
+        if (k == n - 1) tc_commit(&sh.drained);
+      }
+      __syncwarp();
+      if (!ok && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
       // no product may be in flight when the tensor memory goes
-      if (lane == 0) tc_commit(&sh.drained);
-      wait_here(&sh.drained, 0);
+      if (n > 0) wait_here(&sh.drained, 0);
     }
   } else if (!E4 || warp < 8) {
     // ---- softmax: a row a thread --------------------------------------------
-    if constexpr (C::THREADS == 384) regs_up<(E4 ? 240 : 208)>();
+    if constexpr (C::THREADS == 384) regs_up<(E4 ? 240 : 216)>();
     const int tile = TILES == 2 ? (warp >> 2) - 1 : 0;
     const int row = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -659,11 +670,13 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < NB; c += 32) tmem_ld32(s_at + c, v + c);
           tmem_ld_wait();
-          float x0 = v[0], x1 = v[1], x2 = v[2], x3 = v[3];
+          float x = fmaxf(v[0], v[1]), x1 = fmaxf(v[2], v[3]);
 #pragma unroll
-          for (int c = 4; c < NB; c += 4)
-            x0 = fmaxf(x0, v[c]), x1 = fmaxf(x1, v[c + 1]), x2 = fmaxf(x2, v[c + 2]), x3 = fmaxf(x3, v[c + 3]);
-          const float x = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+          for (int c = 4; c < NB; c += 4) {
+            x = fmaxf(x, fmaxf(v[c], v[c + 1]));
+            x1 = fmaxf(x1, fmaxf(v[c + 2], v[c + 3]));
+          }
+          x = fmaxf(x, x1);
           const bool grows = live && fmaf(x, by, mref) > AT_BIAS + AT_SLACK;
           if (__any_sync(~0u, grows)) {
             float f = 1.f;
@@ -689,27 +702,40 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
               }
             }
           }
-          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+          float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+          const float2 by2 = twice(by), mref2 = twice(mref);
 #pragma unroll
-          for (int c0 = 0; c0 < NB; c0 += 64) {
-            uint32_t w[32];
+          for (int c0 = 0; c0 < NB; c0 += 32) {
+            uint32_t w[16];
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-              float* e = v + c0 + c;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) e[i] = ex2(fmaf(e[i], by, mref));
-              s0 += e[0], s1 += e[1], s2 += e[2], s3 += e[3];
-              w[c / 2] = pack16<(BF16 && !E4)>(e[0], e[1]);
-              w[c / 2 + 1] = pack16<(BF16 && !E4)>(e[2], e[3]);
+            for (int c = 0; c < 32; c += 4) {
+              float2 a = fma2(make_float2(v[c0 + c], v[c0 + c + 1]), by2, mref2);
+              float2 d = fma2(make_float2(v[c0 + c + 2], v[c0 + c + 3]), by2, mref2);
+              a = make_float2(ex2(a.x), ex2(a.y));
+              d = make_float2(ex2(d.x), ex2(d.y));
+              s0 = add2(s0, a);
+              s1 = add2(s1, d);
+              w[c / 2] = pack16<(BF16 && !E4)>(a.x, a.y);
+              w[c / 2 + 1] = pack16<(BF16 && !E4)>(d.x, d.y);
             }
-            tmem_st32(s_at + c0 / 2, w);
+            tmem_st16(s_at + c0 / 2, w);
+            if (c0 + 32 < NB && (c0 + 32) % C::PK == 0) {
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.p_full[buf][c0 / C::PK]);
+            }
           }
-          l += (s0 + s1) + (s2 + s3);
+          s0 = add2(s0, s1);
+          l += s0.x + s0.y;
           tmem_st_wait();
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[buf]);
+        if (lane == 0) {
+          if (!any && C::PARTS == 2) mbar_arrive(&sh.p_full[buf][0]);
+          mbar_arrive(&sh.p_full[buf][C::PARTS - 1]);
+        }
       }
       // ---- this row's result --------------------------------------------------
       // (not by o_done: a warp that has not watched it may be two products behind, which its

@@ -133,29 +133,6 @@ struct Unit {
   static __device__ __forceinline__ bool second(int i) { return FORM == HALF ? i >= V : i % 2; }
 };
 
-// Two products and sums at once.
-__device__ __forceinline__ uint64_t bits2(float2 v) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(v.x), "f"(v.y));
-  return r;
-}
-__device__ __forceinline__ float2 from2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-  return from2(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-  return from2(r);
-}
-__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
-
 template <typename T>
 __device__ __forceinline__ float weight_at(const NormRopeParams& p, int side, int e) {
   if (!p.weight[side]) return 1.f;
