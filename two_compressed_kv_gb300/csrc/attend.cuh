@@ -8,17 +8,18 @@
 // times g heads, so that few tokens still fill the 128 rows of a product and the
 // keys of a group are read once.
 //
-// A CTA holds one or two row tiles and walks over blocks of 128 (D = 256: 64) keys:
+// A CTA holds one row tile and walks over blocks of 128 keys (D = 256: 64), or two and
+// blocks of 64 (tensor memory has no room for more):
 //   S = Q K^T       tcgen05, both operands in shared memory, S in tensor memory;
 //   softmax         a warpgroup per row tile, one row a thread (no shuffles): scores
 //                   out of tensor memory, exponents, 16-bit weights back over them;
 //   O += P V        tcgen05, P in tensor memory, V in shared memory, O in tensor
 //                   memory (fp32).
-// Roles: one warp copies (TMA, 128-byte swizzle, a ring of K and V tiles), one
-// issues products, a warpgroup per row tile does the softmax.  Two S buffers keep the
-// tensor cores busy while a softmax runs: with two row tiles one belongs to each,
-// with one tile consecutive blocks take turns.  The products of a buffer are issued
-// in the order S, P V, next S by one thread, which is the order they execute in.
+// Roles: one warp copies (TMA, 128-byte swizzle, a ring of K and V tiles), one lane
+// issues products, a warpgroup per row tile does the softmax.  Every row tile has two S
+// buffers: the scores of the block after next are formed while a softmax runs, so that
+// none waits for products of its own.  The products of a buffer are issued in the order
+// S, P V, next S by one thread, which is the order they execute in.
 //
 // O is scaled down only where a row's maximum passes its reference by 2^6: after the
 // first blocks that hardly happens, and no work on O lies between the products.
@@ -47,20 +48,17 @@ enum { FROM_TENSORS = 0, FROM_PAGES = 1, FROM_BYTES = 2 };
 
 template <int D, int TILES, int FROM>
 struct AT {
-  static constexpr int NB = attend_block(D);
+  static constexpr int NB = attend_block(D, TILES, FROM == FROM_BYTES);
   static constexpr bool E4 = FROM == FROM_BYTES;
   static constexpr int G = D / 64;                         // groups of 64 channels
   static constexpr int QTILE = 128 * D * 2;
   static constexpr int TILE = NB * D * 2;                  // bytes of a K or V tile
   static constexpr int RAW = NB * D;
-  static constexpr int STAGES = E4 ? (D == 64 ? 5 : 3) : D == 64 ? 8 : TILES == 2 ? 5 : D == 256 ? 5 : 6;
-  static constexpr int RAWS = E4 ? (D == 256 ? 3 : 5) : 0;
+  static constexpr int STAGES = E4 ? (D == 64 ? 8 : D == 128 ? 6 : 3) : D == 256 ? 5 : D == 128 ? (TILES == 2 ? 10 : 6) : TILES == 2 ? 12 : 8;
+  static constexpr int RAWS = E4 ? (D == 256 ? 3 : 8) : 0;
   static constexpr int SMEM = TILES * QTILE + STAGES * TILE + RAWS * RAW + 1024;
   static constexpr int THREADS = TILES == 2 || E4 ? 384 : 256;
-  static constexpr int S_COL = 0, O_COL = 2 * NB;          // tensor memory columns
-  // Weights are handed over in parts, so that the products with the first keys' values
-  // run while the other weights are formed.
-  static constexpr int PARTS = TILES == 2 ? 2 : 1, PK = NB / PARTS;
+  static constexpr int O_COL = TILES * 2 * NB;             // tensor memory columns: S buffers, then O
   static_assert(O_COL + TILES * D <= 512, "tensor memory");
   static_assert(SMEM <= 225 * 1024 + 512, "shared memory");
   static_assert(!(E4 && TILES == 2), "the second warpgroup widens");
@@ -69,6 +67,11 @@ struct AT {
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 __device__ __forceinline__ float rcp_fast(float x) {
@@ -149,14 +152,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* u) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-template <int R>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(R));
-}
-template <int R>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R));
-}
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
@@ -173,7 +168,7 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// mbar_wait without a call: a kernel that moves registers between its warps has none.
+// mbar_wait without a call.
 __device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity) {
   uint64_t since = 0;
   for (int i = 0; !mbar_test(bar, parity); ++i) {
@@ -240,12 +235,10 @@ __device__ __forceinline__ uint32_t columns(int lo, int hi, int first) {
 
 struct AttendShared {
   uint64_t q_full;
-  uint64_t full[8], empty[8];          // K and V tiles as the products take them
+  uint64_t full[12], empty[12];        // K and V tiles as the products take them
   uint64_t raw_full[8], raw_empty[8];  // 8-bit tiles
-  uint64_t s_full[2], p_full[2][2];    // scores there; a part of the weights there
-  uint64_t o_done[2];                  // another product of a row tile is in O
-  uint64_t o_last[2];                  // all are
-  uint64_t drained;
+  uint64_t s_full[4], p_full[4];       // a buffer's scores are there; its weights are
+  uint64_t o_last[2];                  // all products of a row tile are in O
   uint32_t tmem;
   int depth[64];                       // of a tree's new tokens
   float q_scale[128];                  // 8-bit pages: what a row of q was divided by
@@ -275,20 +268,19 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
   }
   if (tid == 0) {
     mbar_init(&sh.q_full, E4 ? 4 : 1);
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 12; ++i) {
       mbar_init(&sh.full[i], E4 ? 4 : 1);
-      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.empty[i], TILES);
+    }
+    for (int i = 0; i < 8; ++i) {
       mbar_init(&sh.raw_full[i], 1);
       mbar_init(&sh.raw_empty[i], 4);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i][0], 4);
-      mbar_init(&sh.p_full[i][1], 4);
-      mbar_init(&sh.o_done[i], 1);
-      mbar_init(&sh.o_last[i], 1);
+      mbar_init(&sh.p_full[i], 4);
     }
-    mbar_init(&sh.drained, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.o_last[i], 1);
     mbar_init_fence();
   }
   griddep_wait();
@@ -365,7 +357,6 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
   };
 
   if (warp < 4) {
-    if constexpr (C::THREADS == 384) regs_down<(E4 ? 88 : 72)>();
     if (warp == 0) {
       // ---- copies -----------------------------------------------------------
       const bool work = blocks.j < blocks.end;
@@ -419,35 +410,30 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
       };
       int cur = blocks.next();
       if (cur >= 0) load(kmap, cur);
-      if constexpr (TILES == 2) {
-        while (cur >= 0 && ok) {
-          const int nxt = blocks.next();
-          load(vmap, cur);
-          if (nxt >= 0) load(kmap, nxt);
-          cur = nxt;
-        }
-      } else {
-        int nxt = cur >= 0 ? blocks.next() : -1;
-        if (nxt >= 0) load(kmap, nxt);
-        while (cur >= 0 && ok) {
-          const int then = nxt >= 0 ? blocks.next() : -1;
-          load(vmap, cur);
-          if (then >= 0) load(kmap, then);
-          cur = nxt;
-          nxt = then;
-        }
+      int nxt = cur >= 0 ? blocks.next() : -1;
+      if (nxt >= 0) load(kmap, nxt);
+      while (cur >= 0 && ok) {
+        const int then = nxt >= 0 ? blocks.next() : -1;
+        load(vmap, cur);
+        if (then >= 0) load(kmap, then);
+        cur = nxt;
+        nxt = then;
       }
       // no copy may be in flight when the CTA ends
       for (int i = max(0, n - SLOTS); i < n; ++i) wait_here(&full[i % SLOTS], (i / SLOTS) & 1);
       if (!E4 && work) wait_here(&sh.q_full, 0);
-    } else if (warp == 1) {
+    } else if (warp <= TILES) {
       // ---- products ---------------------------------------------------------
+      // One lane of a warp does it all for a row tile: between two products there is room
+      // for some hundred cycles, and while one tile's lane waits the other's products run.
       constexpr uint32_t IS = idesc_f16_f32(128, NB) | (BF16 && !E4 ? (1u << 7) | (1u << 10) : 0u);
       constexpr uint32_t IO = idesc_f16_f32(128, D) | (BF16 && !E4 ? (1u << 7) | (1u << 10) : 0u) | (1u << 16);
-      // One lane does it all: between two products there is room for some hundred cycles.
+      const int tile = warp - 1;
       const int2 all = blocks.all();
       const int n = all.x;
       const bool leader = elect_one();
+      const uint32_t s0 = tmem + 2 * tile * NB, o0 = tmem + C::O_COL + tile * D;
+      const uint32_t qa = desc_lo(smem0 + tile * C::QTILE, 16);
       int slot = 0;
       uint32_t turn = 0;
       bool ok = true;
@@ -457,34 +443,33 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
         if (++slot == C::STAGES) slot = 0, ++turn;
         return s;
       };
-      auto scores = [&](int tile, int buf, int s) {
-        if (!ok) return;
-        const uint32_t qa = desc_lo(smem0 + tile * C::QTILE, 16), ka = desc_lo(ring + s * C::TILE, 16);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + C::S_COL + buf * NB, qa + ((k / 4) * 128 * 128 + (k % 4) * 32) / 16,
-                 ka + ((k / 4) * NB * 128 + (k % 4) * 32) / 16, IS, k > 0);
-        tc_commit(&sh.s_full[buf]);
-      };
-      // the products with one part of the weights
-      auto values = [&](int tile, int buf, int s, int part, uint32_t parity, bool first, bool last) {
-        ok = ok && wait_here(&sh.p_full[buf][part], parity);
+      // scores of block k into buffer k mod 2, and the product with its weights
+      auto scores = [&](int k) {
+        const int s = pop();
         if (!ok) return;
         tc_fence_after();
-        const uint32_t va = desc_lo(ring + s * C::TILE, NB * 128) + part * C::PK * 128 / 16;
+        const uint32_t ka = desc_lo(ring + s * C::TILE, 16);
 #pragma unroll
-        for (int k = 0; k < C::PK / 16; ++k)
-          mma_ts(tmem + C::O_COL + tile * D, tmem + C::S_COL + buf * NB + part * (C::PK / 2) + k * 8, va + k * 2048 / 16,
-                 IO, !first || part > 0 || k > 0);
-        if (part == C::PARTS - 1) {
-          tc_commit(&sh.o_done[tile]);
-          if (last) tc_commit(&sh.o_last[tile]);
-        }
+        for (int c = 0; c < D / 16; ++c)
+          mma_ss(s0 + (k & 1) * NB, qa + ((c / 4) * 128 * 128 + (c % 4) * 32) / 16,
+                 ka + ((c / 4) * NB * 128 + (c % 4) * 32) / 16, IS, c > 0);
+        tc_commit(&sh.s_full[2 * tile + (k & 1)]);
+        tc_commit(&sh.empty[s]);
       };
-      auto release = [&](int s) { tc_commit(&sh.empty[s]); };
+      auto values = [&](int k) {
+        const int s = pop();
+        ok = ok && wait_here(&sh.p_full[2 * tile + (k & 1)], (k >> 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t va = desc_lo(ring + s * C::TILE, NB * 128);
+#pragma unroll
+        for (int c = 0; c < NB / 16; ++c)
+          mma_ts(o0, s0 + (k & 1) * NB + c * 8, va + c * 2048 / 16, IO, k > 0 || c > 0);
+        tc_commit(&sh.empty[s]);
+      };
       // What lies behind the sequence in its last block may be anything, and 0 times a
       // NaN is one: those rows of V become zeros (8-bit pages: where they are widened).
-      // It is the ring's last tile.
+      // It is the ring's last tile; of two warps both write the zeros they need.
       auto clean = [&](int j) {
         const int s = (2 * n - 1) % C::STAGES;
         wait_here(&sh.full[s], ((2 * n - 1) / C::STAGES) & 1);
@@ -497,57 +482,28 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
         }
         fence_proxy_async();
       };
-      const bool dirty = !E4 && n > 0 && (all.y + 1) * NB > L;
-      int ks = 0, vs = 0;
       if (leader && n > 0) {
         ok = wait_here(&sh.q_full, 0);
-        tc_fence_after();
-        for (int i = 0; i < 2; ++i) {
-          if (TILES == 1 && i == n) break;
-          if (TILES == 1 || i == 0) ks = pop();
-          scores(TILES == 2 ? i : 0, i, ks);
-          if (TILES == 1 || i == 1) release(ks);
+        scores(0);
+        if (n > 1) scores(1);
+        for (int k = 0; k + 1 < n && ok; ++k) {
+          values(k);
+          if (k + 2 < n) scores(k + 2);
         }
-      }
-      for (int k = 0; k < n; ++k) {
-        if (k == n - 1 && dirty) {
-          __syncwarp();
-          clean(all.y);
-          __syncwarp();
-        }
-        if (!leader) continue;
-        vs = pop();
-        if constexpr (TILES == 2) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int h = 0; h < C::PARTS; ++h) values(i, i, vs, h, k & 1, k == 0, k == n - 1);
-            if (i == 1) release(vs);
-            if (k + 1 < n) {
-              if (i == 0) ks = pop();
-              scores(i, i, ks);
-              if (i == 1) release(ks);
-            }
-          }
-        } else {
-          values(0, k & 1, vs, 0, (k >> 1) & 1, k == 0, k == n - 1);
-          release(vs);
-          if (k + 2 < n) {
-            ks = pop();
-            scores(0, k & 1, ks);
-            release(ks);
-          }
-        }
-        if (k == n - 1) tc_commit(&sh.drained);
       }
       __syncwarp();
-      if (!ok && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
-      // no product may be in flight when the tensor memory goes
-      if (n > 0) wait_here(&sh.drained, 0);
+      if (!E4 && n > 0 && (all.y + 1) * NB > L) clean(all.y);
+      __syncwarp();
+      if (leader && n > 0) {
+        values(n - 1);
+        tc_commit(&sh.o_last[tile]);
+        if (!ok && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
+        // no product may be in flight when the tensor memory goes
+        wait_here(&sh.o_last[tile], 0);
+      }
     }
   } else if (!E4 || warp < 8) {
     // ---- softmax: a row a thread --------------------------------------------
-    if constexpr (C::THREADS == 384) regs_up<(E4 ? 240 : 216)>();
     const int tile = TILES == 2 ? (warp >> 2) - 1 : 0;
     const int row = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -575,6 +531,9 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
       }
     }
     const int doc = docs && live && place >= 0 ? docs[place] : 0;
+    // blocks [whole0, whole1): all keys seen by all rows of the warp (but for their documents)
+    const int whole0 = ((int)__reduce_max_sync(~0u, live ? klo : 0) + NB - 1) / NB;
+    const int whole1 = absent ? 0 : (int)__reduce_min_sync(~0u, khi) / NB;
     float sc = p.scale * 1.4426950408889634f;            // of the products, to log2
     const float slope = p.slopes && live ? p.slopes[head] * 1.4426950408889634f : 0.f;
     bool ok = true;
@@ -591,21 +550,20 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
       uint32_t k = 0;
       const uint32_t o_at = tmem + lanes + C::O_COL + tile * D;
       for (int j = ok ? blocks.next() : -1; j >= 0; j = blocks.next(), ++k) {
-        const int buf = TILES == 2 ? tile : k & 1;
-        const uint32_t s_at = tmem + lanes + C::S_COL + buf * NB;
-        if (!(ok = wait(&sh.s_full[buf], TILES == 2 ? k & 1 : (k >> 1) & 1))) break;
+        const int buf = 2 * tile + (k & 1);
+        const uint32_t s_at = tmem + lanes + buf * NB;
+        if (!(ok = wait(&sh.s_full[buf], (k >> 1) & 1))) break;
         if (any) {
           tc_fence_after();
           const int j0 = j * NB;
           const bool in_tree = p.tree && j0 + NB > base;
-          // columns that this row does not see
-          bool part_of = live && (klo > j0 || khi < j0 + NB);
+          // columns that some row does not see
+          bool masked = j < whole0 || j >= whole1;
           int2 dr = make_int2(doc, doc);
           if (docs) {
             dr = blocks.range[j];
-            part_of |= live && (dr.x != doc || dr.y != doc);
+            masked |= __any_sync(~0u, live && (dr.x != doc || dr.y != doc));
           }
-          const bool masked = __any_sync(~0u, part_of) || absent;
           if (mods || masked) {
             // scores formed and masked in tensor memory, 32 at a time: beside the pass below
             // they would not fit the registers
@@ -673,8 +631,8 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
           float x = fmaxf(v[0], v[1]), x1 = fmaxf(v[2], v[3]);
 #pragma unroll
           for (int c = 4; c < NB; c += 4) {
-            x = fmaxf(x, fmaxf(v[c], v[c + 1]));
-            x1 = fmaxf(x1, fmaxf(v[c + 2], v[c + 3]));
+            x = max3(x, v[c], v[c + 1]);
+            x1 = max3(x1, v[c + 2], v[c + 3]);
           }
           x = fmaxf(x, x1);
           const bool grows = live && fmaf(x, by, mref) > AT_BIAS + AT_SLACK;
@@ -687,9 +645,10 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
               mref = AT_BIAS - __fmul_rn(x, by);
             }
             if (k > 0) {
-              // O by the same factor, between its products (these scores were issued behind the
-              // product before the last, so the parity is that of one of two phases)
-              if (!(ok = wait(&sh.o_done[tile], (k - 1) & 1))) break;
+              // O by the same factor, between its products: the last one has run when its V tile
+              // (the ring's 2 k-th, or the one before where there is but one block) is released
+              const int used = 2 * k;
+              if (!(ok = wait(&sh.empty[used % C::STAGES], (used / C::STAGES) & 1))) break;
               tc_fence_after();
 #pragma unroll
               for (int c = 0; c < D; c += 16) {
@@ -719,12 +678,6 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
               w[c / 2 + 1] = pack16<(BF16 && !E4)>(d.x, d.y);
             }
             tmem_st16(s_at + c0 / 2, w);
-            if (c0 + 32 < NB && (c0 + 32) % C::PK == 0) {
-              tmem_st_wait();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sh.p_full[buf][c0 / C::PK]);
-            }
           }
           s0 = add2(s0, s1);
           l += s0.x + s0.y;
@@ -732,14 +685,9 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) {
-          if (!any && C::PARTS == 2) mbar_arrive(&sh.p_full[buf][0]);
-          mbar_arrive(&sh.p_full[buf][C::PARTS - 1]);
-        }
+        if (lane == 0) mbar_arrive(&sh.p_full[buf]);
       }
       // ---- this row's result --------------------------------------------------
-      // (not by o_done: a warp that has not watched it may be two products behind, which its
-      // parity does not show)
       if (ok && any && k > 0) ok = wait(&sh.o_last[tile], 0);
       if (ok && any) {
         tc_fence_after();

@@ -218,7 +218,7 @@ AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, i
   const int64_t all = up(std::max<int64_t>(nq, 1), l.tile_tokens);
   l.tiles = all > 1 && D < 256 && !e4m3 ? 2 : 1;
   l.groups = (int)up(all, l.tiles);
-  const int NB = attend_block(D);
+  const int NB = attend_block(D, l.tiles, e4m3);
   const int64_t items = (int64_t)B * H * l.groups;
   int64_t keys = nk;
   if (window) keys = std::min<int64_t>(nk, (int64_t)window + l.tiles * l.tile_tokens + NB);

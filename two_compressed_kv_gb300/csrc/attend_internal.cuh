@@ -9,8 +9,10 @@ namespace mkv {
 constexpr float AT_BIAS = 8.f;     // weights carry a factor 2^8 until the division by their sum
 constexpr float AT_SLACK = 6.f;    // how far scores (log2) may pass the reference of the exponents
 
-// Keys of a block: the step of the pass over the keys.
-constexpr int attend_block(int D) { return D == 256 ? 64 : 128; }
+// Keys of a block, the step of the pass over the keys: tensor memory holds two blocks'
+// scores of every row tile and the outputs, and a thread a block of its row's scores
+// (168 registers where a third warpgroup runs).
+constexpr int attend_block(int D, int tiles, bool e4m3) { return D == 256 || tiles == 2 || e4m3 ? 64 : 128; }
 
 struct AttendParams {
   const void* q;
