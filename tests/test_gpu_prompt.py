@@ -354,6 +354,28 @@ def test_prefill_scores_far_apart(M):
         attend_near(f64(out[0]), None, ref, F16, n)
 
 
+@pytest.mark.parametrize("d,heads,kv", [(64, 24, 24), (128, 48, 16), (256, 24, 24)])
+@pytest.mark.parametrize("kw", [dict(), dict(window=100), dict(docs=True), dict(cap=10.0, causal=False)])
+def test_prefill_many_pieces(M, d, heads, kv, kw):
+    """More pieces of work than the GPU runs at once, of unequal lengths, some without any."""
+    kw = dict(kw)
+    n = 700
+    if kw.get("docs"):
+        kw["docs"] = np.sort(np.random.default_rng(3).integers(0, 9, (8, n)), 1)
+    lens = [700, 1, 0, 333, 64, 650, 129, 511]
+    prefill_check(M, BF16, 8, n, n, heads, kv, d, q_lens=lens, kv_lens=lens, stray=float("nan"), **kw)
+
+
+@pytest.mark.parametrize("ctype,qtype", [(F16, F16), (E4M3, BF16)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("m", [1, 40])
+def test_attend_many_pieces(M, ctype, qtype, d, m):
+    rng = np.random.default_rng(m)
+    lens = [int(x) for x in rng.integers(0, 700, 40)]
+    new = [min(m, n) if i % 3 else min(1, n) for i, n in enumerate(lens)]
+    attend_check(M, ctype, qtype, lens, m, 8, 5, d, 48, new=new, tree=[random_tree(rng, m) for _ in lens])
+
+
 def test_prefill_strided_views_and_streams(M):
     """q, k and v as views of one projection, the result into a view, on another stream."""
     proj = rnd((2, 150, 4 + 2 + 2, 128), BF16, 3)

@@ -55,8 +55,8 @@ struct AT {
   static constexpr int TILE = NB * D * 2;                  // bytes of a K or V tile
   static constexpr int RAW = NB * D;
   static constexpr int STAGES = E4 ? (D == 64 ? 8 : D == 128 ? 6 : 3) : D == 256 ? 5 : D == 128 ? (TILES == 2 ? 10 : 6) : TILES == 2 ? 12 : 8;
-  static constexpr int RAWS = E4 ? (D == 256 ? 3 : 8) : 0;
-  static constexpr int SMEM = TILES * QTILE + STAGES * TILE + RAWS * RAW + 1024;
+  static constexpr int RAWS = E4 ? (D == 256 ? 3 : 8) : 1;
+  static constexpr int SMEM = TILES * QTILE + STAGES * TILE + (E4 ? RAWS * RAW : 0) + 1024;
   static constexpr int THREADS = TILES == 2 || E4 ? 384 : 256;
   static constexpr int O_COL = TILES * 2 * NB;             // tensor memory columns: S buffers, then O
   static_assert(O_COL + TILES * D <= 512, "tensor memory");
@@ -168,6 +168,17 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ void tma_store_4d(uint32_t src, const CUtensorMap* map, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
+               : "memory");
+}
+// Until this thread's stores have read the shared memory.
+__device__ __forceinline__ void tma_store_read() {
+  asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;\n" ::: "memory");
+}
+
 // mbar_wait without a call.
 __device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity) {
   uint64_t since = 0;
@@ -239,18 +250,21 @@ struct AttendShared {
   uint64_t raw_full[8], raw_empty[8];  // 8-bit tiles
   uint64_t s_full[4], p_full[4];       // a buffer's scores are there; its weights are
   uint64_t o_last[2];                  // all products of a row tile are in O
+  uint64_t o_ready[2];                 // its output is in shared memory
   uint32_t tmem;
   int depth[64];                       // of a tree's new tokens
+  uint32_t absent[16];                 // pages: of the last 16 blocks, units whose page is not in the cache
   float q_scale[128];                  // 8-bit pages: what a row of q was divided by
 };
 
 // ---------------------------------------------------------------------------
-// grid: B * H * groups * splits; block AT::THREADS; dynamic smem AT::SMEM
+// grid: (groups * splits, H, B); block AT::THREADS; dynamic smem AT::SMEM
 // ---------------------------------------------------------------------------
 template <int D, int TILES, int FROM, bool BF16>
 __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
     attend_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap qmap,
-                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int unit) {
+                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const __grid_constant__ CUtensorMap omap, int unit) {
   using C = AT<D, TILES, FROM>;
   constexpr int NB = C::NB, G = C::G;
   constexpr bool E4 = C::E4, PAGED = FROM != FROM_TENSORS;
@@ -266,32 +280,31 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
-  if (tid == 0) {
-    mbar_init(&sh.q_full, E4 ? 4 : 1);
-    for (int i = 0; i < 12; ++i) {
-      mbar_init(&sh.full[i], E4 ? 4 : 1);
-      mbar_init(&sh.empty[i], TILES);
+  if (warp == 0) {
+    if (lane < 12) {
+      mbar_init(&sh.full[lane], E4 ? 4 : 1);
+      mbar_init(&sh.empty[lane], TILES);
+    } else if (lane < 20) {
+      mbar_init(&sh.raw_full[lane - 12], 1);
+      mbar_init(&sh.raw_empty[lane - 12], 4);
+    } else if (lane < 24) {
+      mbar_init(&sh.s_full[lane - 20], 1);
+      mbar_init(&sh.p_full[lane - 20], 4);
+    } else if (lane < 26) {
+      mbar_init(&sh.o_last[lane - 24], 1);
+      mbar_init(&sh.o_ready[lane - 24], 4);
+    } else if (lane == 26) {
+      mbar_init(&sh.q_full, E4 ? 4 : 1);
     }
-    for (int i = 0; i < 8; ++i) {
-      mbar_init(&sh.raw_full[i], 1);
-      mbar_init(&sh.raw_empty[i], 4);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
-    }
-    for (int i = 0; i < 2; ++i) mbar_init(&sh.o_last[i], 1);
     mbar_init_fence();
   }
   griddep_wait();
   griddep_launch();
 
   // this CTA's part: row tiles [tile0, tile0 + TILES) of (b, h), the part-th share of their keys
-  int item = blockIdx.x;
-  const int part = item % p.splits;
-  item /= p.splits;
-  const int group = p.groups - 1 - item % p.groups;      // causal: the longest first
-  const int bh = item / p.groups, b = bh / p.H, h = bh - b * p.H;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const int of = p.splits > 1 ? blockIdx.x / p.splits : blockIdx.x;
+  const int part = blockIdx.x - of * p.splits, group = p.groups - 1 - of;    // causal: the longest first
   const int TT = p.tile_tokens, t0 = group * TILES * TT;
   int m, L;
   bool outside;
@@ -317,8 +330,12 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
   blocks.range = nullptr;
   {
     const int from = lo / NB, n = hi > lo ? (hi + NB - 1) / NB - from : 0;
-    blocks.j = from + (int)((int64_t)n * part / p.splits);
-    blocks.end = from + (int)((int64_t)n * (part + 1) / p.splits);
+    blocks.j = from;
+    blocks.end = from + n;
+    if (p.splits > 1) {                // n * splits fits 32 bits: 2^24 blocks, 64 parts
+      blocks.j = from + (uint32_t)n * part / (uint32_t)p.splits;
+      blocks.end = from + (uint32_t)n * (part + 1) / (uint32_t)p.splits;
+    }
     blocks.base = blocks.j - 32;
   }
   if (docs && hi > lo) {
@@ -336,18 +353,8 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
     const uint64_t valid = m >= 64 ? ~0ull : (1ull << m) - 1;
     sh.depth[tid] = __popcll(p.tree[(int64_t)b * p.nq + tid] & valid & ~(1ull << tid));
   }
-  // a page outside the cache: its tokens are absent, which the softmax looks up again
-  bool absent = false;
-  if (PAGED && blocks.j < blocks.end) {
-    const int e1 = min(blocks.end * NB, L);
-    for (int e = blocks.j * NB / p.page_size + tid; e * p.page_size < e1; e += C::THREADS) {
-      const int page = p.table[b * p.table_stride + e];
-      absent |= page < 0 || page >= p.n_pages;
-    }
-    if (absent && p.status) atomicOr(p.status, DEV_ERR_CHECK);
-  }
   tc_fence_before();
-  absent = __syncthreads_or(absent);
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, sh.tmem, 0);
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -359,7 +366,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
   if (warp < 4) {
     if (warp == 0) {
       // ---- copies -----------------------------------------------------------
-      const bool work = blocks.j < blocks.end;
+      const bool work = blocks.all().x > 0;
       if constexpr (!E4) {
         if (work) {
           if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, TILES * G * TT * p.g * 128);
@@ -377,12 +384,12 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
       int n = 0, slot = 0;
       uint32_t turn = 0;
       bool ok = true;
-      int units_from = -1, entry = 0;    // pages: this lane's unit of the 32 from `units_from` on
+      int units_from = -1, entry = 0, step = 0;    // pages: this lane's unit of the 32 from `units_from` on
+      uint32_t gone = 0;                 // bits of those whose page is not in the cache
       const int per = NB / unit;
-      auto load = [&](const CUtensorMap& map, int j) {
+      auto load = [&](const CUtensorMap& map, int j, bool keys) {
         if (!ok) return;
         if (n >= SLOTS && !(ok = wait(&empty[slot], (turn & 1) ^ 1))) return;
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], BYTES);
         const uint32_t at = at0 + slot * BYTES;
         if constexpr (PAGED) {
           const int u0 = j * per;
@@ -390,18 +397,30 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
             units_from = u0;
             const int t = (u0 + lane) * unit;
             entry = p.n_pages * p.H * p.page_size;     // behind the pool: zeros
+            bool bad = false;
             if (t < L) {
               const int pg = t / p.page_size;
               const int page = p.table[b * p.table_stride + pg];
-              if (page >= 0 && page < p.n_pages) entry = (page * p.H + h) * p.page_size + (t - pg * p.page_size);
+              bad = page < 0 || page >= p.n_pages;
+              if (!bad) entry = (page * p.H + h) * p.page_size + (t - pg * p.page_size);
             }
+            gone = __ballot_sync(~0u, bad);
           }
+          const uint32_t lost = (gone >> (u0 - units_from)) & ((1u << per) - 1);
+          if (lane == 0) {
+            if (lost && p.status) atomicOr(p.status, DEV_ERR_CHECK);
+            // read by the softmax behind this block's scores, so behind this copy's arrival
+            if (keys) sh.absent[step & 15] = lost;
+            mbar_arrive_expect_tx(&full[slot], BYTES);
+          }
+          if (keys) ++step;
           constexpr int W = E4 ? 1 : G;
           const int u = lane / W, c = lane - u * W;
           const int row = __shfl_sync(~0u, entry, (u0 - units_from + u) & 31);
           __syncwarp();
           if (u < per) tma_load_2d(at + c * NB * 128 + u * unit * (E4 ? D : 128), &map, c * 64, row, &full[slot]);
         } else {
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], BYTES);
           __syncwarp();
           if (lane < G) tma_load_4d(at + lane * NB * 128, &map, lane * 64, j * NB, h, b, &full[slot]);
         }
@@ -409,13 +428,13 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
         if (++slot == SLOTS) slot = 0, ++turn;
       };
       int cur = blocks.next();
-      if (cur >= 0) load(kmap, cur);
+      if (cur >= 0) load(kmap, cur, true);
       int nxt = cur >= 0 ? blocks.next() : -1;
-      if (nxt >= 0) load(kmap, nxt);
+      if (nxt >= 0) load(kmap, nxt, true);
       while (cur >= 0 && ok) {
         const int then = nxt >= 0 ? blocks.next() : -1;
-        load(vmap, cur);
-        if (then >= 0) load(kmap, then);
+        load(vmap, cur, false);
+        if (then >= 0) load(kmap, then, true);
         cur = nxt;
         nxt = then;
       }
@@ -533,11 +552,11 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
     const int doc = docs && live && place >= 0 ? docs[place] : 0;
     // blocks [whole0, whole1): all keys seen by all rows of the warp (but for their documents)
     const int whole0 = ((int)__reduce_max_sync(~0u, live ? klo : 0) + NB - 1) / NB;
-    const int whole1 = absent ? 0 : (int)__reduce_min_sync(~0u, khi) / NB;
+    const int whole1 = (int)__reduce_min_sync(~0u, khi) / NB;
     float sc = p.scale * 1.4426950408889634f;            // of the products, to log2
     const float slope = p.slopes && live ? p.slopes[head] * 1.4426950408889634f : 0.f;
     bool ok = true;
-    if constexpr (E4) {
+    if (E4 && blocks.j < blocks.end) {
       ok = wait(&sh.q_full, 0);
       sc *= sh.q_scale[row] * (p.k_scale ? p.k_scale[h] : 1.f);
     }
@@ -559,6 +578,11 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
           const bool in_tree = p.tree && j0 + NB > base;
           // columns that some row does not see
           bool masked = j < whole0 || j >= whole1;
+          uint32_t absent = 0;
+          if constexpr (PAGED) {
+            absent = sh.absent[k & 15];
+            masked |= absent != 0;
+          }
           int2 dr = make_int2(doc, doc);
           if (docs) {
             dr = blocks.range[j];
@@ -609,13 +633,9 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
                     bits &= same;
                   }
                 }
-                if (PAGED && absent) {
-                  for (int i = 0; i < 32; i += 16) {
-                    const int pg = (k0 + i) / p.page_size;
-                    const int page = k0 + i < L ? p.table[b * p.table_stride + pg] : 0;
-                    if (page < 0 || page >= p.n_pages) bits &= ~(0xffffu << i);
-                  }
-                }
+                if (PAGED && absent)
+                  for (int i = 0; i < 32; i += 16)
+                    if (absent >> ((c0 + i) / unit) & 1) bits &= ~(0xffffu << i);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                   if (!(bits >> i & 1)) v[i] = -CUDART_INF_F;
@@ -689,12 +709,16 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
       }
       // ---- this row's result --------------------------------------------------
       if (ok && any && k > 0) ok = wait(&sh.o_last[tile], 0);
+      // A row tile without padding goes out by one copy, through the shared memory of its
+      // queries, which no product needs any more; otherwise every thread writes its row.
+      const bool whole = p.splits == 1 && t0 + (tile + 1) * TT <= t1;
       if (ok && any) {
         tc_fence_after();
         const float vscale = E4 && p.v_scale ? p.v_scale[h] : 1.f;
         const float mine = top == -CUDART_INF_F ? top : __fmul_rn(top, by);
-        const int64_t part_row = ((int64_t)blockIdx.x * TILES + tile) * 128 + row;
-        const float inv = l > 0.f ? vscale / l : l == 0.f ? 0.f : l;   // a NaN stays one
+        const int64_t cta = ((int64_t)b * p.H + h) * gridDim.x + blockIdx.x;
+        const int64_t part_row = (cta * TILES + tile) * 128 + row;
+        const float inv = p.splits > 1 ? vscale : l > 0.f ? vscale / l : l == 0.f ? 0.f : l;   // a NaN stays one
         uint16_t* out = static_cast<uint16_t*>(p.out) + b * p.os[0] + (int64_t)token * p.os[1] + head * p.os[2];
         if (live) {
           if (p.splits > 1) p.part_ml[part_row] = make_float2(mine, l);
@@ -710,32 +734,45 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
             tmem_ld_wait();
           }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i];
-          if (live) {
-            if (p.splits > 1) {
-              float4* to = reinterpret_cast<float4*>(p.part_o + part_row * D + c);
+          for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
+          if (p.splits > 1) {
+            float4* to = reinterpret_cast<float4*>(p.part_o + part_row * D + c);
+            if (live) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                to[i] = make_float4(o[4 * i] * vscale, o[4 * i + 1] * vscale, o[4 * i + 2] * vscale, o[4 * i + 3] * vscale);
-            } else {
+              for (int i = 0; i < 8; ++i) to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+          } else {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint4 u;
-                u.x = pack16<BF16>(o[8 * i] * inv, o[8 * i + 1] * inv);
-                u.y = pack16<BF16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
-                u.z = pack16<BF16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
-                u.w = pack16<BF16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
+            for (int i = 0; i < 4; ++i) {
+              uint4 u;
+              u.x = pack16<BF16>(o[8 * i], o[8 * i + 1]);
+              u.y = pack16<BF16>(o[8 * i + 2], o[8 * i + 3]);
+              u.z = pack16<BF16>(o[8 * i + 4], o[8 * i + 5]);
+              u.w = pack16<BF16>(o[8 * i + 6], o[8 * i + 7]);
+              if (whole)
+                *reinterpret_cast<uint4*>(smem_p + tile * C::QTILE + (c / 64) * 128 * 128 + row * 128 +
+                                          (((c / 8 + i) & 7) ^ (row & 7)) * 16) = u;
+              else if (live)
                 *reinterpret_cast<uint4*>(out + c + 8 * i) = u;
-              }
             }
           }
         }
+      }
+      if (ok && whole) {
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.o_ready[tile]);
+        if ((warp & 3) == 0 && wait(&sh.o_ready[tile], 0) && lane < G) {
+          tma_store_4d(smem0 + tile * C::QTILE + lane * 128 * 128, &omap, lane * 64, h * p.g, t0 + tile * TT, b);
+          tma_store_read();
+        }
+        __syncwarp();
       }
     }
   } else if constexpr (E4) {
     // ---- widening: 8-bit tiles to fp16 ----------------------------------------
     const int row = tid & 127;
-    {
+    if (blocks.j < blocks.end) {
       // queries: fp16 and bf16 both go to fp16, a row scaled by a power of two so that its
       // largest element lies in [1, 2)
       const int rt = row / p.g, head = h * p.g + (row - rt * p.g), token = t0 + rt;
@@ -834,7 +871,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
 template <int D, int TILES, int FROM, bool BF16>
 cudaError_t launch_at(const AttendParams& p, cudaStream_t st) {
   using C = AT<D, TILES, FROM>;
-  CUtensorMap qmap, kmap, vmap;
+  CUtensorMap qmap, kmap, vmap, omap;
   std::memset(&qmap, 0, sizeof(qmap));
   int unit = C::NB;
   // the stride of an extent of 1 is never walked, but has to be one that a map takes
@@ -860,18 +897,18 @@ cudaError_t launch_at(const AttendParams& p, cudaStream_t st) {
     for (int i = 0; i < 2; ++i)
       if (cudaError_t e = encode_map(i ? &vmap : &kmap, i ? p.v : p.k, C::E4, 2, dim, stride, box, !C::E4)) return e;
   }
-  if constexpr (!C::E4) {
+  for (int i = C::E4 ? 1 : 0; i < 2; ++i) {
+    const int64_t* s = i ? p.os : p.qs;
     const uint64_t dim[4] = {(uint64_t)D, (uint64_t)p.Hq, (uint64_t)p.nq, (uint64_t)p.B};
-    const uint64_t stride[3] = {walked(p.qs[2], p.Hq), walked(p.qs[1], p.nq), walked(p.qs[0], p.B)};
+    const uint64_t stride[3] = {walked(s[2], p.Hq), walked(s[1], p.nq), walked(s[0], p.B)};
     const uint32_t box[4] = {64, (uint32_t)p.g, (uint32_t)p.tile_tokens, 1};
-    if (cudaError_t e = encode_map(&qmap, p.q, false, 4, dim, stride, box, true)) return e;
+    if (cudaError_t e = encode_map(i ? &omap : &qmap, i ? p.out : p.q, false, 4, dim, stride, box, true)) return e;
   }
   cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, TILES, FROM, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::SMEM);
   if (e != cudaSuccess) return e;
-  const int64_t grid = (int64_t)p.B * p.H * p.groups * p.splits;
-  return launch_kernel(attend_kernel<D, TILES, FROM, BF16>, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, st, true, 0, p,
-                       qmap, kmap, vmap, unit);
+  return launch_kernel(attend_kernel<D, TILES, FROM, BF16>, dim3((unsigned)(p.groups * p.splits), p.H, p.B), dim3(C::THREADS),
+                       C::SMEM, st, true, 0, p, qmap, kmap, vmap, omap, unit);
 }
 
 template <int D, int TILES, bool BF16>
