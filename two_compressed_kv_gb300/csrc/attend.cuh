@@ -84,6 +84,20 @@ __device__ __forceinline__ float tanh_of(float x2) {
   const float t = fmaf(-2.f, rcp_fast(ex2(fabsf(x2)) + 1.f), 1.f);
   return copysignf(t, x2);
 }
+// tanh(x), |x| <= 1: x times the polynomial in x^2 of degree 6 with the smallest largest
+// relative error there (5e-8, found by exchange); within 3 u of it, without the two slow
+// functions of the other form (16K tokens in documents with capped scores: 840 us with
+// that form alone).
+__device__ __forceinline__ float2 tanh_small(float2 x) {
+  const float2 u = mul2(x, x);
+  float2 y = fma2(u, twice(0.0010410225950181484f), twice(-0.006203379016369581f));
+  y = fma2(u, y, twice(0.020289979875087738f));
+  y = fma2(u, y, twice(-0.05345702916383743f));
+  y = fma2(u, y, twice(0.13325203955173492f));
+  y = fma2(u, y, twice(-0.33332839608192444f));
+  y = fma2(u, y, twice(0.9999999403953552f));
+  return mul2(x, y);
+}
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   if constexpr (BF16) {
@@ -260,7 +274,7 @@ struct AttendShared {
 // ---------------------------------------------------------------------------
 // grid: (groups * splits, H, B); block AT::THREADS; dynamic smem AT::SMEM
 // ---------------------------------------------------------------------------
-template <int D, int TILES, int FROM, bool BF16>
+template <int D, int TILES, int FROM, bool BF16, bool MODS>
 __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
     attend_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -561,10 +575,9 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
       sc *= sh.q_scale[row] * (p.k_scale ? p.k_scale[h] : 1.f);
     }
     {
-      const bool mods = p.cap > 0.f || p.slopes;
       const float cap2 = p.cap * 1.4426950408889634f;
-      const float into = p.cap > 0.f ? 2.f * sc / p.cap : 0.f;  // products to 2 log2(e) times the tanh's argument
-      const float by = mods ? 1.f : sc;
+      const float into = p.cap > 0.f ? sc / cap2 : 0.f;       // products to the tanh's argument
+      const float by = MODS ? 1.f : sc;
       float top = -CUDART_INF_F, mref = 1e38f, l = 0.f;
       uint32_t k = 0;
       const uint32_t o_at = tmem + lanes + C::O_COL + tile * D;
@@ -575,7 +588,6 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
         if (any) {
           tc_fence_after();
           const int j0 = j * NB;
-          const bool in_tree = p.tree && j0 + NB > base;
           // columns that some row does not see
           bool masked = j < whole0 || j >= whole1;
           uint32_t absent = 0;
@@ -588,58 +600,41 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
             dr = blocks.range[j];
             masked |= __any_sync(~0u, live && (dr.x != doc || dr.y != doc));
           }
-          if (mods || masked) {
-            // scores formed and masked in tensor memory, 32 at a time: beside the pass below
-            // they would not fit the registers
+          // bits of the 32 columns from c0 on that this row sees
+          auto seen = [&](int c0) {
+            const int k0 = j0 + c0;
+            uint32_t bits = live ? columns(klo, khi, k0) : 0u;
+            if (p.tree) {
+              const int off = k0 - base;
+              bits |= off >= 0 ? (off < 64 ? (uint32_t)(sees >> off) : 0u) : off > -32 ? (uint32_t)sees << -off : 0u;
+            }
+            if (docs) {
+              if (dr.x == dr.y) {
+                bits = dr.x == doc ? bits : 0u;
+              } else if (__any_sync(~0u, bits != 0u)) {
+                uint32_t same = 0;
+                for (int i = 0; i < 32; ++i)
+                  if (k0 + i < L && docs[k0 + i] == doc) same |= 1u << i;
+                bits &= same;
+              }
+            }
+            if (PAGED && absent)
+              for (int i = 0; i < 32; i += 16)
+                if (absent >> ((c0 + i) / unit) & 1) bits &= ~(0xffffu << i);
+            return bits;
+          };
+          if (!MODS && masked) {
+            // in tensor memory, 32 at a time: beside the pass below it would cost plain blocks
+            // registers (8K prompts, batch 4: 1645 us instead of 1549)
 #pragma unroll 1
             for (int c0 = 0; c0 < NB; c0 += 32) {
               float v[32];
               tmem_ld32(s_at + c0, v);
               tmem_ld_wait();
-              if (p.cap > 0.f) {
+              const uint32_t bits = seen(c0);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = cap2 * tanh_of(v[c] * into);
-              } else if (mods) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] *= sc;
-              }
-              if (p.slopes) {
-                const float far = (float)(place - j0 - c0);
-                if (in_tree) {
-#pragma unroll
-                  for (int c = 0; c < 32; ++c) {
-                    const int t = j0 + c0 + c - base;
-                    v[c] -= slope * fabsf(t < 0 ? far - (float)c : (float)(place - base - sh.depth[min(t, 63)]));
-                  }
-                } else {
-#pragma unroll
-                  for (int c = 0; c < 32; ++c) v[c] -= slope * fabsf(far - (float)c);
-                }
-              }
-              if (masked) {
-                const int k0 = j0 + c0;
-                uint32_t bits = live ? columns(klo, khi, k0) : 0u;
-                if (in_tree) {
-                  const int off = k0 - base;
-                  bits |= off >= 0 ? (off < 64 ? (uint32_t)(sees >> off) : 0u) : off > -32 ? (uint32_t)sees << -off : 0u;
-                }
-                if (docs) {
-                  if (dr.x == dr.y) {
-                    bits = dr.x == doc ? bits : 0u;
-                  } else if (__any_sync(~0u, bits != 0u)) {
-                    uint32_t same = 0;
-                    for (int i = 0; i < 32; ++i)
-                      if (k0 + i < L && docs[k0 + i] == doc) same |= 1u << i;
-                    bits &= same;
-                  }
-                }
-                if (PAGED && absent)
-                  for (int i = 0; i < 32; i += 16)
-                    if (absent >> ((c0 + i) / unit) & 1) bits &= ~(0xffffu << i);
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (!(bits >> i & 1)) v[i] = -CUDART_INF_F;
-              }
+              for (int i = 0; i < 32; ++i)
+                if (!(bits >> i & 1)) v[i] = -CUDART_INF_F;
               tmem_st32(s_at + c0, reinterpret_cast<const uint32_t*>(v));
             }
             tmem_st_wait();
@@ -648,6 +643,48 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < NB; c += 32) tmem_ld32(s_at + c, v + c);
           tmem_ld_wait();
+          if constexpr (MODS) {
+            if (p.cap > 0.f) {
+              float big = 0.f;
+#pragma unroll
+              for (int c = 0; c < NB; c += 2) big = max3(big, fabsf(v[c]), fabsf(v[c + 1]));
+              if (__any_sync(~0u, !(big * into <= 1.f))) {
+#pragma unroll
+                for (int c = 0; c < NB; ++c) v[c] = cap2 * tanh_of(v[c] * into * 2.885390081777927f);
+              } else {
+#pragma unroll
+                for (int c = 0; c < NB; c += 2) {
+                  const float2 y = mul2(tanh_small(mul2(make_float2(v[c], v[c + 1]), twice(into))), twice(cap2));
+                  v[c] = y.x, v[c + 1] = y.y;
+                }
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < NB; ++c) v[c] *= sc;
+            }
+            if (p.slopes) {
+              const float far = (float)(place - j0);
+              if (p.tree && j0 + NB > base) {
+#pragma unroll
+                for (int c = 0; c < NB; ++c) {
+                  const int t = j0 + c - base;
+                  v[c] -= slope * fabsf(t < 0 ? far - (float)c : (float)(place - base - sh.depth[min(t, 63)]));
+                }
+              } else {
+#pragma unroll
+                for (int c = 0; c < NB; ++c) v[c] -= slope * fabsf(far - (float)c);
+              }
+            }
+            if (masked) {
+#pragma unroll
+              for (int c0 = 0; c0 < NB; c0 += 32) {
+                const uint32_t bits = seen(c0);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!(bits >> i & 1)) v[c0 + i] = -CUDART_INF_F;
+              }
+            }
+          }
           float x = fmaxf(v[0], v[1]), x1 = fmaxf(v[2], v[3]);
 #pragma unroll
           for (int c = 4; c < NB; c += 4) {
@@ -868,7 +905,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
   }
 }
 
-template <int D, int TILES, int FROM, bool BF16>
+template <int D, int TILES, int FROM, bool BF16, bool MODS>
 cudaError_t launch_at(const AttendParams& p, cudaStream_t st) {
   using C = AT<D, TILES, FROM>;
   CUtensorMap qmap, kmap, vmap, omap;
@@ -904,25 +941,33 @@ cudaError_t launch_at(const AttendParams& p, cudaStream_t st) {
     const uint32_t box[4] = {64, (uint32_t)p.g, (uint32_t)p.tile_tokens, 1};
     if (cudaError_t e = encode_map(i ? &omap : &qmap, i ? p.out : p.q, false, 4, dim, stride, box, true)) return e;
   }
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, TILES, FROM, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, TILES, FROM, BF16, MODS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attend_kernel<D, TILES, FROM, BF16>, dim3((unsigned)(p.groups * p.splits), p.H, p.B), dim3(C::THREADS),
+  return launch_kernel(attend_kernel<D, TILES, FROM, BF16, MODS>, dim3((unsigned)(p.groups * p.splits), p.H, p.B), dim3(C::THREADS),
                        C::SMEM, st, true, 0, p, qmap, kmap, vmap, omap, unit);
 }
 
-template <int D, int TILES, bool BF16>
+template <int D, int TILES, bool BF16, bool MODS>
 cudaError_t launch_from(const AttendParams& p, cudaStream_t st) {
-  if (!p.table) return launch_at<D, TILES, FROM_TENSORS, BF16>(p, st);
-  if (p.cache_type != MKV_DT_E4M3) return launch_at<D, TILES, FROM_PAGES, BF16>(p, st);
-  return launch_at<D, 1, FROM_BYTES, BF16>(p, st);
+  if (!p.table) return launch_at<D, TILES, FROM_TENSORS, BF16, MODS>(p, st);
+  if (p.cache_type != MKV_DT_E4M3) return launch_at<D, TILES, FROM_PAGES, BF16, MODS>(p, st);
+  return launch_at<D, 1, FROM_BYTES, BF16, MODS>(p, st);
+}
+
+// Scores that are capped or biased are a kernel of their own: their code would cost the
+// plain one registers.
+template <int D, int TILES>
+cudaError_t launch_tiles(const AttendParams& p, cudaStream_t st) {
+  if (p.cap > 0.f || p.slopes) return p.bf16 ? launch_from<D, TILES, true, true>(p, st) : launch_from<D, TILES, false, true>(p, st);
+  return p.bf16 ? launch_from<D, TILES, true, false>(p, st) : launch_from<D, TILES, false, false>(p, st);
 }
 
 template <int D>
 cudaError_t launch_attend_d(const AttendParams& p, cudaStream_t st) {
   if constexpr (D < 256)
-    if (p.tiles == 2) return p.bf16 ? launch_from<D, 2, true>(p, st) : launch_from<D, 2, false>(p, st);
-  return p.bf16 ? launch_from<D, 1, true>(p, st) : launch_from<D, 1, false>(p, st);
+    if (p.tiles == 2) return launch_tiles<D, 2>(p, st);
+  return launch_tiles<D, 1>(p, st);
 }
 
 }  // namespace
