@@ -84,20 +84,27 @@ __device__ __forceinline__ float tanh_of(float x2) {
   const float t = fmaf(-2.f, rcp_fast(ex2(fabsf(x2)) + 1.f), 1.f);
   return copysignf(t, x2);
 }
-// tanh(x), |x| <= 1: x times the polynomial in x^2 of degree 6 with the smallest largest
-// relative error there (5e-8, found by exchange); within 3 u of it, without the two slow
-// functions of the other form (16K tokens in documents with capped scores: 840 us with
-// that form alone).
-__device__ __forceinline__ float2 tanh_small(float2 x) {
-  const float2 u = mul2(x, x);
-  float2 y = fma2(u, twice(0.0010410225950181484f), twice(-0.006203379016369581f));
-  y = fma2(u, y, twice(0.020289979875087738f));
-  y = fma2(u, y, twice(-0.05345702916383743f));
-  y = fma2(u, y, twice(0.13325203955173492f));
-  y = fma2(u, y, twice(-0.33332839608192444f));
-  y = fma2(u, y, twice(0.9999999403953552f));
-  return mul2(x, y);
-}
+// cap2 tanh(a x), |a x| <= 1: x times the polynomial in x^2 of degree 6 with the smallest
+// largest relative error there (5e-8, found by exchange), the factors in its coefficients;
+// within 3 u of it, without the two slow functions of the other form (16K tokens in
+// documents with capped scores: 840 us with that form alone, 689 with this).
+struct SmallTanh {
+  float c[7];
+  __device__ __forceinline__ SmallTanh(float a, float cap2) {
+    const float of[7] = {0.9999999403953552f, -0.33332839608192444f, 0.13325203955173492f, -0.05345702916383743f,
+                         0.020289979875087738f, -0.006203379016369581f, 0.0010410225950181484f};
+    float f = a * cap2;
+#pragma unroll
+    for (int i = 0; i < 7; ++i, f *= a * a) c[i] = of[i] * f;
+  }
+  __device__ __forceinline__ float2 operator()(float2 x) const {
+    const float2 u = mul2(x, x);
+    float2 y = fma2(u, twice(c[6]), twice(c[5]));
+#pragma unroll
+    for (int i = 4; i >= 0; --i) y = fma2(u, y, twice(c[i]));
+    return mul2(x, y);
+  }
+};
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   if constexpr (BF16) {
@@ -210,25 +217,31 @@ __device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity) {
 // whole): all of a range, or those in which some document of its queries occurs.
 struct Blocks {
   int j, end, base;
-  uint32_t bits;
+  uint32_t bits;         // of the 32 blocks from base on: taken;
+  uint32_t lone;         // of one document alone, `doc`
+  int doc;
   const int2* range;     // of the sequence's blocks; NULL: all
   int2 own;              // of the queries' documents
-  // bits of the 32 blocks from `from` on
-  __device__ __forceinline__ uint32_t hits(int from) const {
+  __device__ __forceinline__ uint32_t hits(int from, uint32_t& one) const {
     const int i = from + (threadIdx.x & 31);
-    bool hit = false;
+    bool hit = false, same = false;
     if (i < end) {
       const int2 r = range[i];
       hit = r.x <= own.y && r.y >= own.x;
+      same = r.x == doc && r.y == doc;
     }
+    one = __ballot_sync(~0u, same);
     return __ballot_sync(~0u, hit);
   }
+  // block i, the last that next() gave, has nothing but `doc`
+  __device__ __forceinline__ bool plain(int i) const { return lone >> (i - base) & 1; }
   // (how many, the last)
   __device__ __forceinline__ int2 all() const {
     if (!range) return make_int2(max(0, end - j), end - 1);
     int2 r = make_int2(0, -1);
     for (int from = j; from < end; from += 32) {
-      const uint32_t h = hits(from);
+      uint32_t one;
+      const uint32_t h = hits(from, one);
       r.x += __popc(h);
       if (h) r.y = from + 31 - __clz(h);
     }
@@ -239,7 +252,7 @@ struct Blocks {
     while (j < end) {
       if (j >= base + 32) {
         base = j;
-        bits = hits(base);
+        bits = hits(base, lone);
       }
       const uint32_t rest = bits >> (j - base);
       if (rest) {
@@ -342,6 +355,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
   const int32_t* docs = p.docs ? p.docs + b * p.docs_stride : nullptr;
   Blocks blocks;
   blocks.range = nullptr;
+  blocks.doc = 0;
   {
     const int from = lo / NB, n = hi > lo ? (hi + NB - 1) / NB - from : 0;
     blocks.j = from;
@@ -567,6 +581,9 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
     // blocks [whole0, whole1): all keys seen by all rows of the warp (but for their documents)
     const int whole0 = ((int)__reduce_max_sync(~0u, live ? klo : 0) + NB - 1) / NB;
     const int whole1 = (int)__reduce_min_sync(~0u, khi) / NB;
+    // all rows of the warp of one document: its blocks are known 32 at a time
+    blocks.doc = __reduce_max_sync(~0u, live ? doc : INT32_MIN);
+    const bool one_doc = __all_sync(~0u, !live || doc == blocks.doc);
     float sc = p.scale * 1.4426950408889634f;            // of the products, to log2
     const float slope = p.slopes && live ? p.slopes[head] * 1.4426950408889634f : 0.f;
     bool ok = true;
@@ -577,6 +594,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
     {
       const float cap2 = p.cap * 1.4426950408889634f;
       const float into = p.cap > 0.f ? sc / cap2 : 0.f;       // products to the tanh's argument
+      const SmallTanh small(into, cap2);
       const float by = MODS ? 1.f : sc;
       float top = -CUDART_INF_F, mref = 1e38f, l = 0.f;
       uint32_t k = 0;
@@ -596,7 +614,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
             masked |= absent != 0;
           }
           int2 dr = make_int2(doc, doc);
-          if (docs) {
+          if (docs && !(one_doc && blocks.plain(j))) {
             dr = blocks.range[j];
             masked |= __any_sync(~0u, live && (dr.x != doc || dr.y != doc));
           }
@@ -654,7 +672,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
               } else {
 #pragma unroll
                 for (int c = 0; c < NB; c += 2) {
-                  const float2 y = mul2(tanh_small(mul2(make_float2(v[c], v[c + 1]), twice(into))), twice(cap2));
+                  const float2 y = small(make_float2(v[c], v[c + 1]));
                   v[c] = y.x, v[c + 1] = y.y;
                 }
               }
