@@ -89,19 +89,19 @@ __device__ __forceinline__ float tanh_of(float x2) {
 // within 3 u of it, without the two slow functions of the other form (16K tokens in
 // documents with capped scores: 840 us with that form alone, 689 with this).
 struct SmallTanh {
-  float c[7];
+  float2 c[7];
   __device__ __forceinline__ SmallTanh(float a, float cap2) {
     const float of[7] = {0.9999999403953552f, -0.33332839608192444f, 0.13325203955173492f, -0.05345702916383743f,
                          0.020289979875087738f, -0.006203379016369581f, 0.0010410225950181484f};
     float f = a * cap2;
 #pragma unroll
-    for (int i = 0; i < 7; ++i, f *= a * a) c[i] = of[i] * f;
+    for (int i = 0; i < 7; ++i, f *= a * a) c[i] = twice(of[i] * f);
   }
   __device__ __forceinline__ float2 operator()(float2 x) const {
     const float2 u = mul2(x, x);
-    float2 y = fma2(u, twice(c[6]), twice(c[5]));
+    float2 y = fma2(u, c[6], c[5]);
 #pragma unroll
-    for (int i = 4; i >= 0; --i) y = fma2(u, y, twice(c[i]));
+    for (int i = 4; i >= 0; --i) y = fma2(u, y, c[i]);
     return mul2(x, y);
   }
 };
@@ -872,13 +872,17 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
       const int rs = n % C::RAWS, s = n % C::STAGES;
       if (!(ok = wait(&sh.raw_full[rs], (n / C::RAWS) & 1))) return;
       if (n >= C::STAGES && !(ok = wait(&sh.empty[s], (n / C::STAGES - 1) & 1))) return;
-      const uint8_t* from = smem_p + C::QTILE + C::STAGES * C::TILE + rs * C::RAW;
-      uint8_t* to = smem_p + C::QTILE + s * C::TILE;
+      // a thread takes the same 16 channels of every RS-th row: a multiple of 8 rows, so that
+      // the swizzle is the same for all
+      constexpr int PIECES = D / 16, RS = 128 / PIECES;
+      const int r0 = row / PIECES, c = row % PIECES, ch = (2 * c) & 7;
+      const uint8_t* from = smem_p + C::QTILE + C::STAGES * C::TILE + rs * C::RAW + row * 16;
+      uint8_t* to = smem_p + C::QTILE + s * C::TILE + (c / 4) * NB * 128 + r0 * 128;
+      uint8_t *to0 = to + ((ch ^ (r0 & 7)) << 4), *to1 = to + (((ch + 1) ^ (r0 & 7)) << 4);
       const int keep = values ? L - j * NB : NB;        // rows behind the sequence become zeros
-#pragma unroll 4
-      for (int i = row; i < NB * D / 16; i += 128) {
-        const int r = i / (D / 16), c = i - r * (D / 16);
-        const uint4 u = *reinterpret_cast<const uint4*>(from + i * 16);
+#pragma unroll
+      for (int i = 0; i < NB / RS; ++i) {
+        const uint4 u = *reinterpret_cast<const uint4*>(from + i * 128 * 16);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
         uint32_t o[8];
 #pragma unroll
@@ -886,14 +890,12 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
           asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
               : "=r"(o[2 * x]), "=r"(o[2 * x + 1])
               : "r"(w[x]));
-        if (r >= keep) {
+        if (r0 + i * RS >= keep) {
 #pragma unroll
           for (int x = 0; x < 8; ++x) o[x] = 0u;
         }
-        uint8_t* at = to + (c / 4) * NB * 128 + r * 128;
-        const int ch = (2 * c) & 7;
-        *reinterpret_cast<uint4*>(at + ((ch ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        *reinterpret_cast<uint4*>(to0 + i * RS * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(to1 + i * RS * 128) = make_uint4(o[4], o[5], o[6], o[7]);
       }
       fence_proxy_async();
       __syncwarp();
