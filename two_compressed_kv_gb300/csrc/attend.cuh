@@ -27,6 +27,11 @@
 // the largest, and below 2^14.  The rounding of the weights to 16 bits is half a step
 // of the output's own type; their sum is of the unrounded ones.
 //
+// Few rows (32 or fewer of a KV head): four copies of them fill the 128 rows, one for each
+// softmax warp's lanes of tensor memory, and a warp takes a quarter of a block's columns,
+// with weights of zero in the others.  A block's softmax is then a quarter as long, where
+// otherwise one warp would work and three wait; the four parts are joined at the end.
+//
 // 8-bit pages: a further warpgroup widens the raw tiles to fp16 between the copies and
 // the products.
 #pragma once
@@ -46,21 +51,24 @@ namespace {
 
 enum { FROM_TENSORS = 0, FROM_PAGES = 1, FROM_BYTES = 2 };
 
-template <int D, int TILES, int FROM>
+template <int D, int TILES, int FROM, bool FEW>
 struct AT {
-  static constexpr int NB = attend_block(D, TILES, FROM == FROM_BYTES);
+  static constexpr int NB = attend_block(D, TILES, FROM == FROM_BYTES, FEW);
   static constexpr bool E4 = FROM == FROM_BYTES;
   static constexpr int G = D / 64;                         // groups of 64 channels
   static constexpr int QTILE = 128 * D * 2;
   static constexpr int TILE = NB * D * 2;                  // bytes of a K or V tile
   static constexpr int RAW = NB * D;
-  static constexpr int STAGES = E4 ? (D == 64 ? 8 : D == 128 ? 6 : 3) : D == 256 ? 5 : D == 128 ? (TILES == 2 ? 10 : 6) : TILES == 2 ? 12 : 8;
-  static constexpr int RAWS = E4 ? (D == 256 ? 3 : 8) : 1;
+  static constexpr int STAGES = E4 ? (D == 64 ? 8 : D == 128 ? 6 : 3) * (D < 256 ? 64 : NB) / NB : D == 256 ? 5 : D == 128 ? (TILES == 2 ? 10 : 6) : TILES == 2 ? 12 : 8;
+  static constexpr int RAWS = E4 ? (D == 256 ? 3 : FEW ? 5 : 8) : 1;
+  // columns of a block that a softmax warp takes, and rows of a row tile that are not copies
+  static constexpr int COLS = FEW ? NB / 4 : NB, ROWS = FEW ? 32 : 128;
   static constexpr int SMEM = TILES * QTILE + STAGES * TILE + (E4 ? RAWS * RAW : 0) + 1024;
   static constexpr int THREADS = TILES == 2 || E4 ? 384 : 256;
   static constexpr int O_COL = TILES * 2 * NB;             // tensor memory columns: S buffers, then O
   static_assert(O_COL + TILES * D <= 512, "tensor memory");
-  static_assert(SMEM <= 225 * 1024 + 512, "shared memory");
+  static_assert(SMEM + 2048 <= 227 * 1024, "shared memory");
+  static_assert(!FEW || 128 * (D + 4) * 4 + 1024 <= STAGES * TILE + (E4 ? RAWS * RAW : 0), "the join's area");
   static_assert(!(E4 && TILES == 2), "the second warpgroup widens");
 };
 
@@ -172,6 +180,22 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* u) {
       "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* u) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(u[0]), "r"(u[1]),
+               "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float* v) {
+  if constexpr (N == 32) tmem_ld32(taddr, v);
+  else tmem_ld16(taddr, reinterpret_cast<uint32_t*>(v));
+}
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t* u) {
+  if constexpr (N == 32) tmem_st32(taddr, u);
+  else if constexpr (N == 16) tmem_st16(taddr, u);
+  else tmem_st8(taddr, u);
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
   asm volatile(
@@ -282,17 +306,18 @@ struct AttendShared {
   int depth[64];                       // of a tree's new tokens
   uint32_t absent[16];                 // pages: of the last 16 blocks, units whose page is not in the cache
   float q_scale[128];                  // 8-bit pages: what a row of q was divided by
+  uint64_t joins[2];                   // few rows: references and sums are there; outputs
 };
 
 // ---------------------------------------------------------------------------
 // grid: (groups * splits, H, B); block AT::THREADS; dynamic smem AT::SMEM
 // ---------------------------------------------------------------------------
-template <int D, int TILES, int FROM, bool BF16, bool MODS>
-__global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
+template <int D, int TILES, int FROM, bool BF16, bool MODS, bool FEW>
+__global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
     attend_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __grid_constant__ CUtensorMap omap, int unit) {
-  using C = AT<D, TILES, FROM>;
+  using C = AT<D, TILES, FROM, FEW>;
   constexpr int NB = C::NB, G = C::G;
   constexpr bool E4 = C::E4, PAGED = FROM != FROM_TENSORS;
   extern __shared__ uint8_t smem_raw[];
@@ -322,6 +347,8 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
       mbar_init(&sh.o_ready[lane - 24], 4);
     } else if (lane == 26) {
       mbar_init(&sh.q_full, E4 ? 4 : 1);
+    } else if (lane < 29) {
+      mbar_init(&sh.joins[lane - 27], 4);
     }
     mbar_init_fence();
   }
@@ -397,11 +424,14 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
       const bool work = blocks.all().x > 0;
       if constexpr (!E4) {
         if (work) {
-          if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, TILES * G * TT * p.g * 128);
+          // few rows: four copies, one for the lanes of each softmax warp
+          constexpr int TIMES = FEW ? 4 : TILES;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, TIMES * G * TT * p.g * 128);
           __syncwarp();
-          if (lane < TILES * G) {
-            const int tile = lane / G, c = lane - tile * G;
-            tma_load_4d(smem0 + tile * C::QTILE + c * 128 * 128, &qmap, c * 64, h * p.g, t0 + tile * TT, b, &sh.q_full);
+          if (lane < TIMES * G) {
+            const int i = lane / G, c = lane - i * G;
+            tma_load_4d(smem0 + c * 128 * 128 + i * (FEW ? 32 * 128 : C::QTILE), &qmap, c * 64, h * p.g,
+                        t0 + (FEW ? 0 : i * TT), b, &sh.q_full);
           }
         }
       }
@@ -554,9 +584,10 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
     const int tile = TILES == 2 ? (warp >> 2) - 1 : 0;
     const int row = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const int rt = row / p.g, head = h * p.g + (row - rt * p.g);
+    const int rt = row % C::ROWS / p.g, head = h * p.g + (row % C::ROWS - rt * p.g);
     const int token = t0 + tile * TT + rt;
     const bool live = rt < TT && token < t1;
+    const int col0 = FEW ? (warp & 3) * C::COLS : 0;       // the warp's columns of a block
     const bool any = __any_sync(~0u, live);
     // what this row sees: keys [klo, khi), of its document, and the new tokens of its tree row
     int place = base + token, klo = 0, khi = INT32_MAX;
@@ -597,15 +628,16 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
       const SmallTanh small(into, cap2);
       const float by = MODS ? 1.f : sc;
       float top = -CUDART_INF_F, mref = 1e38f, l = 0.f;
+      constexpr int COLS = C::COLS, W = COLS < 32 ? COLS : 32;   // columns at a time
       uint32_t k = 0;
       const uint32_t o_at = tmem + lanes + C::O_COL + tile * D;
       for (int j = ok ? blocks.next() : -1; j >= 0; j = blocks.next(), ++k) {
         const int buf = 2 * tile + (k & 1);
-        const uint32_t s_at = tmem + lanes + buf * NB;
+        const uint32_t w_at = tmem + lanes + buf * NB, s_at = w_at + col0;
         if (!(ok = wait(&sh.s_full[buf], (k >> 1) & 1))) break;
         if (any) {
           tc_fence_after();
-          const int j0 = j * NB;
+          const int j0 = j * NB + col0;
           // columns that some row does not see
           bool masked = j < whole0 || j >= whole1;
           uint32_t absent = 0;
@@ -638,74 +670,74 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
             }
             if (PAGED && absent)
               for (int i = 0; i < 32; i += 16)
-                if (absent >> ((c0 + i) / unit) & 1) bits &= ~(0xffffu << i);
+                if (absent >> ((col0 + c0 + i) / unit) & 1) bits &= ~(0xffffu << i);
             return bits;
           };
           if (!MODS && masked) {
             // in tensor memory, 32 at a time: beside the pass below it would cost plain blocks
             // registers (8K prompts, batch 4: 1645 us instead of 1549)
 #pragma unroll 1
-            for (int c0 = 0; c0 < NB; c0 += 32) {
-              float v[32];
-              tmem_ld32(s_at + c0, v);
+            for (int c0 = 0; c0 < COLS; c0 += 32) {
+              float v[W];
+              tmem_load<W>(s_at + c0, v);
               tmem_ld_wait();
               const uint32_t bits = seen(c0);
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
+              for (int i = 0; i < W; ++i)
                 if (!(bits >> i & 1)) v[i] = -CUDART_INF_F;
-              tmem_st32(s_at + c0, reinterpret_cast<const uint32_t*>(v));
+              tmem_store<W>(s_at + c0, reinterpret_cast<const uint32_t*>(v));
             }
             tmem_st_wait();
           }
-          float v[NB];
+          float v[COLS];
 #pragma unroll
-          for (int c = 0; c < NB; c += 32) tmem_ld32(s_at + c, v + c);
+          for (int c = 0; c < COLS; c += W) tmem_load<W>(s_at + c, v + c);
           tmem_ld_wait();
           if constexpr (MODS) {
             if (p.cap > 0.f) {
               float big = 0.f;
 #pragma unroll
-              for (int c = 0; c < NB; c += 2) big = max3(big, fabsf(v[c]), fabsf(v[c + 1]));
+              for (int c = 0; c < COLS; c += 2) big = max3(big, fabsf(v[c]), fabsf(v[c + 1]));
               if (__any_sync(~0u, !(big * into <= 1.f))) {
 #pragma unroll
-                for (int c = 0; c < NB; ++c) v[c] = cap2 * tanh_of(v[c] * into * 2.885390081777927f);
+                for (int c = 0; c < COLS; ++c) v[c] = cap2 * tanh_of(v[c] * into * 2.885390081777927f);
               } else {
 #pragma unroll
-                for (int c = 0; c < NB; c += 2) {
+                for (int c = 0; c < COLS; c += 2) {
                   const float2 y = small(make_float2(v[c], v[c + 1]));
                   v[c] = y.x, v[c + 1] = y.y;
                 }
               }
             } else {
 #pragma unroll
-              for (int c = 0; c < NB; ++c) v[c] *= sc;
+              for (int c = 0; c < COLS; ++c) v[c] *= sc;
             }
             if (p.slopes) {
               const float far = (float)(place - j0);
               if (p.tree && j0 + NB > base) {
 #pragma unroll
-                for (int c = 0; c < NB; ++c) {
+                for (int c = 0; c < COLS; ++c) {
                   const int t = j0 + c - base;
                   v[c] -= slope * fabsf(t < 0 ? far - (float)c : (float)(place - base - sh.depth[min(t, 63)]));
                 }
               } else {
 #pragma unroll
-                for (int c = 0; c < NB; ++c) v[c] -= slope * fabsf(far - (float)c);
+                for (int c = 0; c < COLS; ++c) v[c] -= slope * fabsf(far - (float)c);
               }
             }
             if (masked) {
 #pragma unroll
-              for (int c0 = 0; c0 < NB; c0 += 32) {
+              for (int c0 = 0; c0 < COLS; c0 += 32) {
                 const uint32_t bits = seen(c0);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
+                for (int i = 0; i < W; ++i)
                   if (!(bits >> i & 1)) v[c0 + i] = -CUDART_INF_F;
               }
             }
           }
           float x = fmaxf(v[0], v[1]), x1 = fmaxf(v[2], v[3]);
 #pragma unroll
-          for (int c = 4; c < NB; c += 4) {
+          for (int c = 4; c < COLS; c += 4) {
             x = max3(x, v[c], v[c + 1]);
             x1 = max3(x1, v[c + 2], v[c + 3]);
           }
@@ -739,10 +771,10 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
           float2 s0 = make_float2(0.f, 0.f), s1 = s0;
           const float2 by2 = twice(by), mref2 = twice(mref);
 #pragma unroll
-          for (int c0 = 0; c0 < NB; c0 += 32) {
-            uint32_t w[16];
+          for (int c0 = 0; c0 < COLS; c0 += W) {
+            uint32_t w[W / 2];
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
+            for (int c = 0; c < W; c += 4) {
               float2 a = fma2(make_float2(v[c0 + c], v[c0 + c + 1]), by2, mref2);
               float2 d = fma2(make_float2(v[c0 + c + 2], v[c0 + c + 3]), by2, mref2);
               a = make_float2(ex2(a.x), ex2(a.y));
@@ -752,7 +784,15 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
               w[c / 2] = pack16<(BF16 && !E4)>(a.x, a.y);
               w[c / 2 + 1] = pack16<(BF16 && !E4)>(d.x, d.y);
             }
-            tmem_st16(s_at + c0 / 2, w);
+            tmem_store<W / 2>(w_at + (col0 + c0) / 2, w);
+          }
+          if constexpr (FEW) {
+            // the other warps' keys weigh nothing in this copy of the rows
+            uint32_t none[W / 2];
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) none[i] = 0u;
+#pragma unroll
+            for (int i = 1; i < 4; ++i) tmem_store<W / 2>(w_at + ((warp + i) & 3) * (W / 2), none);
           }
           s0 = add2(s0, s1);
           l += s0.x + s0.y;
@@ -766,8 +806,77 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
       if (ok && any && k > 0) ok = wait(&sh.o_last[tile], 0);
       // A row tile without padding goes out by one copy, through the shared memory of its
       // queries, which no product needs any more; otherwise every thread writes its row.
-      const bool whole = p.splits == 1 && t0 + (tile + 1) * TT <= t1;
-      if (ok && any) {
+      const bool whole = !FEW && p.splits == 1 && t0 + (tile + 1) * TT <= t1;
+      if (FEW && ok && any) {
+        // few rows: the four warps' parts of each, over a common reference, by way of the
+        // shared memory of K and V
+        tc_fence_after();
+        constexpr int LD = D + 4;
+        float* all = reinterpret_cast<float*>(smem_p + C::QTILE);
+        float2(*few_ml)[32] = reinterpret_cast<float2(*)[32]>(all + 128 * LD);
+        const float vscale = E4 && p.v_scale ? p.v_scale[h] : 1.f;
+        const int own = warp & 3;
+        few_ml[own][lane] = make_float2(top == -CUDART_INF_F ? top : __fmul_rn(top, by), l);
+        auto meet = [&](int i) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.joins[i]);
+          return wait(&sh.joins[i], 0);
+        };
+        ok = meet(0);
+        auto joined = [&](int r, float2& ml) {       // (reference, sum) of row r
+          ml = few_ml[0][r];
+#pragma unroll
+          for (int q = 1; q < 4; ++q) ml.x = fmaxf(ml.x, few_ml[q][r].x);
+          ml.y = 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 x = few_ml[q][r];
+            ml.y += x.x == -CUDART_INF_F ? x.y : x.y * ex2(x.x - ml.x);
+          }
+        };
+        float2 ml;
+        joined(lane, ml);
+        const float mine = few_ml[own][lane].x;
+        const float f = mine == -CUDART_INF_F ? 0.f : ex2(mine - ml.x) * vscale;
+        float* to = all + (own * 32 + lane) * LD;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          if (k > 0) {
+            tmem_ld32(o_at + c, o);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(to + c + 4 * i) =
+                l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
+        }
+        ok = ok && meet(1);
+        const int64_t cta = ((int64_t)b * p.H + h) * gridDim.x + blockIdx.x;
+        const int rows = (t1 - t0) * p.g;
+        for (int e = row; ok && e < rows * (D / 4); e += 128) {
+          const int r = e / (D / 4), c = (e - r * (D / 4)) * 4;
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 x = *reinterpret_cast<const float4*>(all + (q * 32 + r) * LD + c);
+            a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+          }
+          joined(r, ml);
+          const int tk = t0 + r / p.g, hd = h * p.g + r % p.g;
+          if (p.splits > 1) {
+            *reinterpret_cast<float4*>(p.part_o + (cta * 128 + r) * D + c) = a;
+            if (c == 0) p.part_ml[cta * 128 + r] = ml;
+          } else {
+            const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+            uint16_t* out = static_cast<uint16_t*>(p.out) + b * p.os[0] + (int64_t)tk * p.os[1] + hd * p.os[2] + c;
+            *reinterpret_cast<uint2*>(out) = make_uint2(pack16<BF16>(a.x * inv, a.y * inv), pack16<BF16>(a.z * inv, a.w * inv));
+            if (c == 0 && p.lse)
+              p.lse[((int64_t)b * p.nq + tk) * p.Hq + hd] =
+                  ml.y == 0.f ? -CUDART_INF_F : (ml.x + (log2f(ml.y) - AT_BIAS)) * 0.6931471805599453f;
+          }
+        }
+      } else if (ok && any) {
         tc_fence_after();
         const float vscale = E4 && p.v_scale ? p.v_scale[h] : 1.f;
         const float mine = top == -CUDART_INF_F ? top : __fmul_rn(top, by);
@@ -830,7 +939,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
     if (blocks.j < blocks.end) {
       // queries: fp16 and bf16 both go to fp16, a row scaled by a power of two so that its
       // largest element lies in [1, 2)
-      const int rt = row / p.g, head = h * p.g + (row - rt * p.g), token = t0 + rt;
+      const int rt = row % C::ROWS / p.g, head = h * p.g + (row % C::ROWS - rt * p.g), token = t0 + rt;
       const bool live = rt < TT && token < t1;
       const uint16_t* q = static_cast<const uint16_t*>(p.q) + b * p.qs[0] + (int64_t)(live ? token : 0) * p.qs[1] +
                           (live ? head : 0) * p.qs[2];
@@ -925,9 +1034,9 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM>::THREADS, 1)
   }
 }
 
-template <int D, int TILES, int FROM, bool BF16, bool MODS>
+template <int D, int TILES, int FROM, bool BF16, bool MODS, bool FEW>
 cudaError_t launch_at(const AttendParams& p, cudaStream_t st) {
-  using C = AT<D, TILES, FROM>;
+  using C = AT<D, TILES, FROM, FEW>;
   CUtensorMap qmap, kmap, vmap, omap;
   std::memset(&qmap, 0, sizeof(qmap));
   int unit = C::NB;
@@ -961,33 +1070,34 @@ cudaError_t launch_at(const AttendParams& p, cudaStream_t st) {
     const uint32_t box[4] = {64, (uint32_t)p.g, (uint32_t)p.tile_tokens, 1};
     if (cudaError_t e = encode_map(i ? &omap : &qmap, i ? p.out : p.q, false, 4, dim, stride, box, true)) return e;
   }
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, TILES, FROM, BF16, MODS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, TILES, FROM, BF16, MODS, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attend_kernel<D, TILES, FROM, BF16, MODS>, dim3((unsigned)(p.groups * p.splits), p.H, p.B), dim3(C::THREADS),
+  return launch_kernel(attend_kernel<D, TILES, FROM, BF16, MODS, FEW>, dim3((unsigned)(p.groups * p.splits), p.H, p.B), dim3(C::THREADS),
                        C::SMEM, st, true, 0, p, qmap, kmap, vmap, omap, unit);
 }
 
-template <int D, int TILES, bool BF16, bool MODS>
+template <int D, int TILES, bool BF16, bool MODS, bool FEW>
 cudaError_t launch_from(const AttendParams& p, cudaStream_t st) {
-  if (!p.table) return launch_at<D, TILES, FROM_TENSORS, BF16, MODS>(p, st);
-  if (p.cache_type != MKV_DT_E4M3) return launch_at<D, TILES, FROM_PAGES, BF16, MODS>(p, st);
-  return launch_at<D, 1, FROM_BYTES, BF16, MODS>(p, st);
+  if (!p.table) return launch_at<D, TILES, FROM_TENSORS, BF16, MODS, FEW>(p, st);
+  if (p.cache_type != MKV_DT_E4M3) return launch_at<D, TILES, FROM_PAGES, BF16, MODS, FEW>(p, st);
+  return launch_at<D, 1, FROM_BYTES, BF16, MODS, FEW>(p, st);
 }
 
 // Scores that are capped or biased are a kernel of their own: their code would cost the
 // plain one registers.
-template <int D, int TILES>
+template <int D, int TILES, bool FEW>
 cudaError_t launch_tiles(const AttendParams& p, cudaStream_t st) {
-  if (p.cap > 0.f || p.slopes) return p.bf16 ? launch_from<D, TILES, true, true>(p, st) : launch_from<D, TILES, false, true>(p, st);
-  return p.bf16 ? launch_from<D, TILES, true, false>(p, st) : launch_from<D, TILES, false, false>(p, st);
+  if (p.cap > 0.f || p.slopes)
+    return p.bf16 ? launch_from<D, TILES, true, true, FEW>(p, st) : launch_from<D, TILES, false, true, FEW>(p, st);
+  return p.bf16 ? launch_from<D, TILES, true, false, FEW>(p, st) : launch_from<D, TILES, false, false, FEW>(p, st);
 }
 
 template <int D>
 cudaError_t launch_attend_d(const AttendParams& p, cudaStream_t st) {
   if constexpr (D < 256)
-    if (p.tiles == 2) return launch_tiles<D, 2>(p, st);
-  return launch_tiles<D, 1>(p, st);
+    if (p.tiles == 2) return launch_tiles<D, 2, false>(p, st);
+  return launch_tiles<D, 1, false>(p, st);
 }
 
 }  // namespace

@@ -202,6 +202,7 @@ bool strides_ok(const int64_t* s, int64_t e0, int64_t e1, int64_t e2) {
 
 // How a call's rows and keys are spread, and where its workspace's parts lie.
 struct AttendLayout {
+  bool few;
   int tiles, tile_tokens, groups, splits;
   uint64_t docs, part_o, part_ml, total;   // byte offsets
 };
@@ -214,11 +215,12 @@ constexpr int kCtaBlocks = 4, kJoinBlocks = 3;
 // (tensor memory) or 8-bit pages (their second warpgroup widens).
 AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, int window, bool e4m3, bool docs, int sms) {
   AttendLayout l;
-  l.tile_tokens = 128 / g;
+  l.few = nq * g <= 32;
+  l.tile_tokens = (l.few ? 32 : 128) / g;
   const int64_t all = up(std::max<int64_t>(nq, 1), l.tile_tokens);
   l.tiles = all > 1 && D < 256 && !e4m3 ? 2 : 1;
   l.groups = (int)up(all, l.tiles);
-  const int NB = attend_block(D, l.tiles, e4m3);
+  const int NB = attend_block(D, l.tiles, e4m3, l.few);
   const int64_t items = (int64_t)B * H * l.groups;
   int64_t keys = nk;
   if (window) keys = std::min<int64_t>(nk, (int64_t)window + l.tiles * l.tile_tokens + NB);
@@ -264,6 +266,7 @@ mkv_status attend(AttendParams& p, const AttendLayout& l, void* workspace, mkv_s
   if ((int64_t)p.B * p.H * l.groups * l.splits > kMaxGrid) return bad("attention: too many queries");
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.tiles = l.tiles;
+  p.few = l.few;
   p.tile_tokens = l.tile_tokens;
   p.groups = l.groups;
   p.splits = l.splits;
@@ -272,7 +275,8 @@ mkv_status attend(AttendParams& p, const AttendLayout& l, void* workspace, mkv_s
   p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (p.docs) CKP(launch_attend_docs(p, st));
-  switch (p.D) {
+  if (p.few) CKP(p.D == 256 ? launch_attend_few_256(p, st) : launch_attend_few(p, st));
+  else switch (p.D) {
     case 64: CKP(launch_attend_64(p, st)); break;
     case 128: CKP(launch_attend_128(p, st)); break;
     default: CKP(launch_attend_256(p, st)); break;

@@ -10,9 +10,11 @@ constexpr float AT_BIAS = 8.f;     // weights carry a factor 2^8 until the divis
 constexpr float AT_SLACK = 6.f;    // how far scores (log2) may pass the reference of the exponents
 
 // Keys of a block, the step of the pass over the keys: tensor memory holds two blocks'
-// scores of every row tile and the outputs, and a thread a block of its row's scores
-// (168 registers where a third warpgroup runs).
-constexpr int attend_block(int D, int tiles, bool e4m3) { return D == 256 || tiles == 2 || e4m3 ? 64 : 128; }
+// scores of every row tile and the outputs, and a thread a block of its row's scores, or
+// with few rows a quarter (168 registers where a third warpgroup runs).
+constexpr int attend_block(int D, int tiles, bool e4m3, bool few) {
+  return D == 256 || tiles == 2 || (e4m3 && !few) ? 64 : 128;
+}
 
 struct AttendParams {
   const void* q;
@@ -42,7 +44,8 @@ struct AttendParams {
   int n_pages, page_size, cache_type;
   const float *k_scale, *v_scale;
   // the grid: row tiles of a (sequence, KV head) in groups of `tiles`, their keys in `splits` parts
-  int tile_tokens;             // tokens of a row tile: 128 / g
+  int few;                     // a row tile is four copies of 32 rows
+  int tile_tokens;             // tokens of a row tile: 128 / g, few rows: 32 / g
   int tiles;                   // row tiles of a CTA: 1 or 2
   int groups;                  // of row tiles
   int splits;
@@ -62,6 +65,8 @@ __device__ __forceinline__ void attend_lens(const AttendParams& p, int b, int& m
 cudaError_t launch_attend_64(const AttendParams& p, cudaStream_t st);
 cudaError_t launch_attend_128(const AttendParams& p, cudaStream_t st);
 cudaError_t launch_attend_256(const AttendParams& p, cudaStream_t st);
+cudaError_t launch_attend_few(const AttendParams& p, cudaStream_t st);   // heads of 64 and 128
+cudaError_t launch_attend_few_256(const AttendParams& p, cudaStream_t st);
 cudaError_t launch_attend_docs(const AttendParams& p, cudaStream_t st);
 cudaError_t launch_attend_join(const AttendParams& p, cudaStream_t st);
 

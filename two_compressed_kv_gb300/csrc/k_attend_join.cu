@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
 }  // namespace
 
 cudaError_t launch_attend_docs(const AttendParams& p, cudaStream_t st) {
-  const int block = attend_block(p.D, p.tiles, false), blocks = (p.nk + block - 1) / block;
+  const int block = attend_block(p.D, p.tiles, false, p.few), blocks = (p.nk + block - 1) / block;
   if (blocks == 0) return cudaSuccess;
   return launch_kernel(docs_kernel, dim3((blocks + 3) / 4, p.B), dim3(128), 0, st, true, 0, p, block, blocks);
 }
