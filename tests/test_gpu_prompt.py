@@ -505,6 +505,20 @@ def test_attend_ragged_new_tokens(M):
     attend_check(M, E4M3, BF16, lens, 20, 2, 4, 256, 48, new=new, tree=[random_tree(rng, 20) for _ in lens])
 
 
+@pytest.mark.parametrize("ctype,qtype", [(F16, F16), (BF16, BF16), (E4M3, BF16)])
+@pytest.mark.parametrize("m,g", [(2, 4), (3, 3), (8, 4), (11, 3), (9, 7), (16, 4), (13, 5), (64, 1)])
+def test_attend_few_rows(M, ctype, qtype, m, g):
+    """Rows of a KV head around 8, 32 and 64, with sequences that have fewer of them or none."""
+    rng = np.random.default_rng(m)
+    lens = [500, m, 1, 0, 90, 2222]
+    new = [m, min(m, 5), 1, 0, 0, max(1, m // 2)]
+    tree = [random_tree(rng, m) for _ in lens]
+    for d, ps in ((64, 32), (128, 16), (256, 80)):
+        attend_check(M, ctype, qtype, lens, m, 2, g, d, ps, new=new, seed=m)
+        attend_check(M, ctype, qtype, lens, m, 2, g, d, ps, new=new, tree=tree, seed=m, cap=5.0, window=300,
+                     slopes=[2.0**-(i + 1) for i in range(2 * g)])
+
+
 def test_attend_rows_that_see_nothing_and_odd_trees(M):
     """A row of zeros, one that does not see itself, bits of tokens that are not there, one that
     sees later ones."""

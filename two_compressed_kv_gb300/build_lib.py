@@ -23,7 +23,8 @@ SOURCES = ["mkv_api.cu", "k_compress.cu", "k_score.cu", "k_select.cu", "k_attn.c
            "k_append.cu", "paged_api.cu", "k_rope.cu", "k_paged_attn_64.cu", "k_paged_attn_128.cu",
            "k_paged_attn_256.cu", "k_paged_join.cu", "k_evict.cu",
            "attend_api.cu", "k_norm_rope.cu", "k_attend_64.cu", "k_attend_128.cu", "k_attend_256.cu",
-           "k_attend_few.cu", "k_attend_few_256.cu", "k_attend_join.cu"]
+           "k_attend_2.cu", "k_attend_4.cu", "k_attend_4_256.cu", "k_attend_join.cu",
+           "k_paged_opt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
          "--expt-relaxed-constexpr", "-I", os.path.join(HERE, "..", "include")]

@@ -39,4 +39,11 @@ const char* check_plan(const mkv_rope_plan* p);
 const char* check_axes(const mkv_rope_axes* x, const mkv_rope_plan* p);
 const char* check_cache(const mkv_paged_cache* c);
 
+// Few new tokens over 8-bit pages, by the streaming kernel of the single token: whether a
+// call is such a one.  Arguments have been checked; workspace: bytes, and whether the
+// caller's is enough.
+bool paged_attend_streams(const mkv_paged_cache* c, const mkv_paged_attend_args* a);
+mkv_status paged_attend_streaming(const mkv_paged_cache* c, const mkv_paged_attend_args* a, mkv_stream_t stream);
+uint64_t paged_attend_streaming_workspace(const mkv_paged_cache* c, const mkv_paged_attend_args* a);
+
 }  // namespace mkv

@@ -21,16 +21,18 @@
 // none waits for products of its own.  The products of a buffer are issued in the order
 // S, P V, next S by one thread, which is the order they execute in.
 //
-// O is scaled down only where a row's maximum passes its reference by 2^6: after the
+// O is scaled down only where a row's maximum passes its reference by 2^6 (bf16: 2^24): after the
 // first blocks that hardly happens, and no work on O lies between the products.
 // Weights carry a factor 2^8, which cancels: fp16 ones stay normal down to 2^-22 of
 // the largest, and below 2^14.  The rounding of the weights to 16 bits is half a step
 // of the output's own type; their sum is of the unrounded ones.
 //
-// Few rows (32 or fewer of a KV head): four copies of them fill the 128 rows, one for each
-// softmax warp's lanes of tensor memory, and a warp takes a quarter of a block's columns,
-// with weights of zero in the others.  A block's softmax is then a quarter as long, where
-// otherwise one warp would work and three wait; the four parts are joined at the end.
+// Few rows of a KV head: with 32 or fewer, four copies of them fill the 128 rows, one for
+// the lanes of tensor memory of each softmax warp, and a warp takes a quarter of a block's
+// columns, with weights of zero in the others; with up to 64 over 8-bit pages, two copies
+// and halves (16 drafts of 4 heads over 32 streams of 32768 slots: 111 us, 138 without;
+// 16-bit pages: no gain).  A block's softmax is then as much shorter, where otherwise some
+// warps would work and the others wait; the copies' parts are joined at the end.
 //
 // 8-bit pages: a further warpgroup widens the raw tiles to fp16 between the copies and
 // the products.
@@ -51,10 +53,11 @@ namespace {
 
 enum { FROM_TENSORS = 0, FROM_PAGES = 1, FROM_BYTES = 2 };
 
-template <int D, int TILES, int FROM, bool FEW>
+template <int D, int TILES, int FROM, int COPIES>
 struct AT {
-  static constexpr int NB = attend_block(D, TILES, FROM == FROM_BYTES, FEW);
+  static constexpr int NB = attend_block(D, TILES, FROM == FROM_BYTES, COPIES > 1);
   static constexpr bool E4 = FROM == FROM_BYTES;
+  static constexpr bool FEW = COPIES > 1;
   static constexpr int G = D / 64;                         // groups of 64 channels
   static constexpr int QTILE = 128 * D * 2;
   static constexpr int TILE = NB * D * 2;                  // bytes of a K or V tile
@@ -62,7 +65,7 @@ struct AT {
   static constexpr int STAGES = E4 ? (D == 64 ? 8 : D == 128 ? 6 : 3) * (D < 256 ? 64 : NB) / NB : D == 256 ? 5 : D == 128 ? (TILES == 2 ? 10 : 6) : TILES == 2 ? 12 : 8;
   static constexpr int RAWS = E4 ? (D == 256 ? 3 : FEW ? 5 : 8) : 1;
   // columns of a block that a softmax warp takes, and rows of a row tile that are not copies
-  static constexpr int COLS = FEW ? NB / 4 : NB, ROWS = FEW ? 32 : 128;
+  static constexpr int COLS = NB / COPIES, ROWS = 128 / COPIES;
   static constexpr int SMEM = TILES * QTILE + STAGES * TILE + (E4 ? RAWS * RAW : 0) + 1024;
   static constexpr int THREADS = TILES == 2 || E4 ? 384 : 256;
   static constexpr int O_COL = TILES * 2 * NB;             // tensor memory columns: S buffers, then O
@@ -310,16 +313,17 @@ struct AttendShared {
 };
 
 // ---------------------------------------------------------------------------
-// grid: (groups * splits, H, B); block AT::THREADS; dynamic smem AT::SMEM
+// grid: B * H * groups * splits; block AT::THREADS; dynamic smem AT::SMEM
 // ---------------------------------------------------------------------------
-template <int D, int TILES, int FROM, bool BF16, bool MODS, bool FEW>
-__global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
+template <int D, int TILES, int FROM, bool BF16, int MODS, int COPIES>
+__global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
     attend_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __grid_constant__ CUtensorMap omap, int unit) {
-  using C = AT<D, TILES, FROM, FEW>;
+  using C = AT<D, TILES, FROM, COPIES>;
   constexpr int NB = C::NB, G = C::G;
-  constexpr bool E4 = C::E4, PAGED = FROM != FROM_TENSORS;
+  constexpr bool CAP = (MODS & 1) != 0, SLOPES = (MODS & 2) != 0;      // scores are capped, biased
+  constexpr bool E4 = C::E4, PAGED = FROM != FROM_TENSORS, FEW = C::FEW;
   extern __shared__ uint8_t smem_raw[];
   __shared__ AttendShared sh;
   const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -356,9 +360,21 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
   griddep_launch();
 
   // this CTA's part: row tiles [tile0, tile0 + TILES) of (b, h), the part-th share of their keys
-  const int b = blockIdx.z, h = blockIdx.y;
-  const int of = p.splits > 1 ? blockIdx.x / p.splits : blockIdx.x;
-  const int part = blockIdx.x - of * p.splits, group = p.groups - 1 - of;    // causal: the longest first
+  // (in bundles of (sequence, KV head) pairs, whose keys several CTAs then read at the same
+  // time; of a bundle, what may see the most keys first)
+  int rest = blockIdx.x, streams = p.B * p.H, bh = 0;
+  if (streams > AT_BUNDLE) {
+    const int size = AT_BUNDLE * p.groups * p.splits, bundle = rest / size;
+    bh = bundle * AT_BUNDLE;
+    streams = min(streams - bh, AT_BUNDLE);
+    rest -= bundle * size;
+  }
+  const int width = streams * p.splits, of = rest / width;
+  rest -= of * width;
+  const int stream = p.splits > 1 ? rest / p.splits : rest, part = rest - stream * p.splits;
+  bh += stream;
+  const int group = p.groups - 1 - of, b = bh / p.H, h = bh - b * p.H;
+  const int64_t cta = ((int64_t)bh * p.groups + of) * p.splits + part;    // its place in the workspace
   const int TT = p.tile_tokens, t0 = group * TILES * TT;
   int m, L;
   bool outside;
@@ -424,13 +440,12 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
       const bool work = blocks.all().x > 0;
       if constexpr (!E4) {
         if (work) {
-          // few rows: four copies, one for the lanes of each softmax warp
-          constexpr int TIMES = FEW ? 4 : TILES;
+          constexpr int TIMES = FEW ? COPIES : TILES;
           if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, TIMES * G * TT * p.g * 128);
           __syncwarp();
           if (lane < TIMES * G) {
             const int i = lane / G, c = lane - i * G;
-            tma_load_4d(smem0 + c * 128 * 128 + i * (FEW ? 32 * 128 : C::QTILE), &qmap, c * 64, h * p.g,
+            tma_load_4d(smem0 + c * 128 * 128 + i * (FEW ? C::ROWS * 128 : C::QTILE), &qmap, c * 64, h * p.g,
                         t0 + (FEW ? 0 : i * TT), b, &sh.q_full);
           }
         }
@@ -587,7 +602,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
     const int rt = row % C::ROWS / p.g, head = h * p.g + (row % C::ROWS - rt * p.g);
     const int token = t0 + tile * TT + rt;
     const bool live = rt < TT && token < t1;
-    const int col0 = FEW ? (warp & 3) * C::COLS : 0;       // the warp's columns of a block
+    const int copy = row / C::ROWS, col0 = copy * C::COLS;   // which rows these are a copy of; its columns of a block
     const bool any = __any_sync(~0u, live);
     // what this row sees: keys [klo, khi), of its document, and the new tokens of its tree row
     int place = base + token, klo = 0, khi = INT32_MAX;
@@ -615,8 +630,10 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
     // all rows of the warp of one document: its blocks are known 32 at a time
     blocks.doc = __reduce_max_sync(~0u, live ? doc : INT32_MIN);
     const bool one_doc = __all_sync(~0u, !live || doc == blocks.doc);
+    // the first of the warp's places
+    const int nearest = MODS ? (int)__reduce_min_sync(~0u, live ? place : INT32_MAX) : 0;
     float sc = p.scale * 1.4426950408889634f;            // of the products, to log2
-    const float slope = p.slopes && live ? p.slopes[head] * 1.4426950408889634f : 0.f;
+    const float slope = SLOPES && live ? p.slopes[head] * 1.4426950408889634f : 0.f;
     bool ok = true;
     if (E4 && blocks.j < blocks.end) {
       ok = wait(&sh.q_full, 0);
@@ -624,7 +641,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
     }
     {
       const float cap2 = p.cap * 1.4426950408889634f;
-      const float into = p.cap > 0.f ? sc / cap2 : 0.f;       // products to the tanh's argument
+      const float into = CAP ? sc / cap2 : 0.f;       // products to the tanh's argument
       const SmallTanh small(into, cap2);
       const float by = MODS ? 1.f : sc;
       float top = -CUDART_INF_F, mref = 1e38f, l = 0.f;
@@ -693,8 +710,8 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < COLS; c += W) tmem_load<W>(s_at + c, v + c);
           tmem_ld_wait();
-          if constexpr (MODS) {
-            if (p.cap > 0.f) {
+          if constexpr (MODS != 0) {
+            if constexpr (CAP) {
               float big = 0.f;
 #pragma unroll
               for (int c = 0; c < COLS; c += 2) big = max3(big, fabsf(v[c]), fabsf(v[c + 1]));
@@ -708,11 +725,19 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
                   v[c] = y.x, v[c + 1] = y.y;
                 }
               }
+            } else if (j0 + COLS <= nearest + 1 && !(p.tree && j0 + COLS > base)) {
+              // all keys before all rows: the distance is linear
+              const float2 sc2 = twice(sc), slope2 = twice(slope), off2 = twice(-slope * (float)(place - j0));
+#pragma unroll
+              for (int c = 0; c < COLS; c += 2) {
+                const float2 y = fma2(make_float2(v[c], v[c + 1]), sc2, fma2(slope2, make_float2((float)c, (float)(c + 1)), off2));
+                v[c] = y.x, v[c + 1] = y.y;
+              }
             } else {
 #pragma unroll
               for (int c = 0; c < COLS; ++c) v[c] *= sc;
             }
-            if (p.slopes) {
+            if (SLOPES && (CAP || j0 + COLS > nearest + 1 || (p.tree && j0 + COLS > base))) {
               const float far = (float)(place - j0);
               if (p.tree && j0 + NB > base) {
 #pragma unroll
@@ -742,7 +767,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
             x1 = max3(x1, v[c + 2], v[c + 3]);
           }
           x = fmaxf(x, x1);
-          const bool grows = live && fmaf(x, by, mref) > AT_BIAS + AT_SLACK;
+          const bool grows = live && fmaf(x, by, mref) > AT_BIAS + (BF16 && !E4 ? AT_SLACK_BF16 : AT_SLACK);
           if (__any_sync(~0u, grows)) {
             float f = 1.f;
             if (grows) {
@@ -787,12 +812,12 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
             tmem_store<W / 2>(w_at + (col0 + c0) / 2, w);
           }
           if constexpr (FEW) {
-            // the other warps' keys weigh nothing in this copy of the rows
+            // the other copies' keys weigh nothing in this one
             uint32_t none[W / 2];
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) none[i] = 0u;
 #pragma unroll
-            for (int i = 1; i < 4; ++i) tmem_store<W / 2>(w_at + ((warp + i) & 3) * (W / 2), none);
+            for (int i = COLS; i < NB; i += W) tmem_store<W / 2>(w_at + (col0 + i) % NB / 2, none);
           }
           s0 = add2(s0, s1);
           l += s0.x + s0.y;
@@ -803,20 +828,21 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
         if (lane == 0) mbar_arrive(&sh.p_full[buf]);
       }
       // ---- this row's result --------------------------------------------------
-      if (ok && any && k > 0) ok = wait(&sh.o_last[tile], 0);
+      // (with copies of the rows every warp has its part in the join)
+      const bool joins = FEW ? t0 < t1 : any;
+      if (ok && joins && k > 0) ok = wait(&sh.o_last[tile], 0);
       // A row tile without padding goes out by one copy, through the shared memory of its
       // queries, which no product needs any more; otherwise every thread writes its row.
       const bool whole = !FEW && p.splits == 1 && t0 + (tile + 1) * TT <= t1;
-      if (FEW && ok && any) {
-        // few rows: the four warps' parts of each, over a common reference, by way of the
-        // shared memory of K and V
+      if (FEW && ok && joins) {
+        // few rows: the copies' parts of each, over a common reference, by way of the shared
+        // memory of K and V
         tc_fence_after();
         constexpr int LD = D + 4;
         float* all = reinterpret_cast<float*>(smem_p + C::QTILE);
-        float2(*few_ml)[32] = reinterpret_cast<float2(*)[32]>(all + 128 * LD);
+        float2* few_ml = reinterpret_cast<float2*>(all + 128 * LD);    // [copy][row]
         const float vscale = E4 && p.v_scale ? p.v_scale[h] : 1.f;
-        const int own = warp & 3;
-        few_ml[own][lane] = make_float2(top == -CUDART_INF_F ? top : __fmul_rn(top, by), l);
+        few_ml[row] = make_float2(top == -CUDART_INF_F ? top : __fmul_rn(top, by), l);
         auto meet = [&](int i) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.joins[i]);
@@ -824,21 +850,21 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
         };
         ok = meet(0);
         auto joined = [&](int r, float2& ml) {       // (reference, sum) of row r
-          ml = few_ml[0][r];
+          ml = few_ml[r];
 #pragma unroll
-          for (int q = 1; q < 4; ++q) ml.x = fmaxf(ml.x, few_ml[q][r].x);
+          for (int q = 1; q < COPIES; ++q) ml.x = fmaxf(ml.x, few_ml[q * C::ROWS + r].x);
           ml.y = 0.f;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float2 x = few_ml[q][r];
+          for (int q = 0; q < COPIES; ++q) {
+            const float2 x = few_ml[q * C::ROWS + r];
             ml.y += x.x == -CUDART_INF_F ? x.y : x.y * ex2(x.x - ml.x);
           }
         };
         float2 ml;
-        joined(lane, ml);
-        const float mine = few_ml[own][lane].x;
+        joined(row % C::ROWS, ml);
+        const float mine = few_ml[row].x;
         const float f = mine == -CUDART_INF_F ? 0.f : ex2(mine - ml.x) * vscale;
-        float* to = all + (own * 32 + lane) * LD;
+        float* to = all + row * LD;
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           float o[32];
@@ -852,20 +878,19 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
                 l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
         }
         ok = ok && meet(1);
-        const int64_t cta = ((int64_t)b * p.H + h) * gridDim.x + blockIdx.x;
         const int rows = (t1 - t0) * p.g;
         for (int e = row; ok && e < rows * (D / 4); e += 128) {
           const int r = e / (D / 4), c = (e - r * (D / 4)) * 4;
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 x = *reinterpret_cast<const float4*>(all + (q * 32 + r) * LD + c);
+          for (int q = 0; q < COPIES; ++q) {
+            const float4 x = *reinterpret_cast<const float4*>(all + (q * C::ROWS + r) * LD + c);
             a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
           }
           joined(r, ml);
           const int tk = t0 + r / p.g, hd = h * p.g + r % p.g;
           if (p.splits > 1) {
-            *reinterpret_cast<float4*>(p.part_o + (cta * 128 + r) * D + c) = a;
+            p.part_o[(cta * (D / 4) + c / 4) * 128 + r] = a;
             if (c == 0) p.part_ml[cta * 128 + r] = ml;
           } else {
             const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
@@ -880,7 +905,6 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
         tc_fence_after();
         const float vscale = E4 && p.v_scale ? p.v_scale[h] : 1.f;
         const float mine = top == -CUDART_INF_F ? top : __fmul_rn(top, by);
-        const int64_t cta = ((int64_t)b * p.H + h) * gridDim.x + blockIdx.x;
         const int64_t part_row = (cta * TILES + tile) * 128 + row;
         const float inv = p.splits > 1 ? vscale : l > 0.f ? vscale / l : l == 0.f ? 0.f : l;   // a NaN stays one
         uint16_t* out = static_cast<uint16_t*>(p.out) + b * p.os[0] + (int64_t)token * p.os[1] + head * p.os[2];
@@ -900,10 +924,10 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
           if (p.splits > 1) {
-            float4* to = reinterpret_cast<float4*>(p.part_o + part_row * D + c);
+            float4* to = p.part_o + ((cta * TILES + tile) * (D / 4) + c / 4) * 128 + row;
             if (live) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              for (int i = 0; i < 8; ++i) to[i * 128] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
           } else {
 #pragma unroll
@@ -1034,9 +1058,9 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, FEW>::THREADS, 1)
   }
 }
 
-template <int D, int TILES, int FROM, bool BF16, bool MODS, bool FEW>
+template <int D, int TILES, int FROM, bool BF16, int MODS, int COPIES>
 cudaError_t launch_at(const AttendParams& p, cudaStream_t st) {
-  using C = AT<D, TILES, FROM, FEW>;
+  using C = AT<D, TILES, FROM, COPIES>;
   CUtensorMap qmap, kmap, vmap, omap;
   std::memset(&qmap, 0, sizeof(qmap));
   int unit = C::NB;
@@ -1070,34 +1094,39 @@ cudaError_t launch_at(const AttendParams& p, cudaStream_t st) {
     const uint32_t box[4] = {64, (uint32_t)p.g, (uint32_t)p.tile_tokens, 1};
     if (cudaError_t e = encode_map(i ? &omap : &qmap, i ? p.out : p.q, false, 4, dim, stride, box, true)) return e;
   }
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, TILES, FROM, BF16, MODS, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, TILES, FROM, BF16, MODS, COPIES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attend_kernel<D, TILES, FROM, BF16, MODS, FEW>, dim3((unsigned)(p.groups * p.splits), p.H, p.B), dim3(C::THREADS),
+  return launch_kernel(attend_kernel<D, TILES, FROM, BF16, MODS, COPIES>, dim3((unsigned)((int64_t)p.B * p.H * p.groups * p.splits)), dim3(C::THREADS),
                        C::SMEM, st, true, 0, p, qmap, kmap, vmap, omap, unit);
-}
-
-template <int D, int TILES, bool BF16, bool MODS, bool FEW>
-cudaError_t launch_from(const AttendParams& p, cudaStream_t st) {
-  if (!p.table) return launch_at<D, TILES, FROM_TENSORS, BF16, MODS, FEW>(p, st);
-  if (p.cache_type != MKV_DT_E4M3) return launch_at<D, TILES, FROM_PAGES, BF16, MODS, FEW>(p, st);
-  return launch_at<D, 1, FROM_BYTES, BF16, MODS, FEW>(p, st);
 }
 
 // Scores that are capped or biased are a kernel of their own: their code would cost the
 // plain one registers.
-template <int D, int TILES, bool FEW>
-cudaError_t launch_tiles(const AttendParams& p, cudaStream_t st) {
-  if (p.cap > 0.f || p.slopes)
-    return p.bf16 ? launch_from<D, TILES, true, true, FEW>(p, st) : launch_from<D, TILES, false, true, FEW>(p, st);
-  return p.bf16 ? launch_from<D, TILES, true, false, FEW>(p, st) : launch_from<D, TILES, false, false, FEW>(p, st);
+template <int D, int TILES, int FROM, int COPIES>
+cudaError_t launch_options(const AttendParams& p, cudaStream_t st) {
+  const int mods = (p.cap > 0.f ? 1 : 0) | (p.slopes ? 2 : 0);
+  switch (mods) {
+    case 0: return p.bf16 ? launch_at<D, TILES, FROM, true, 0, COPIES>(p, st) : launch_at<D, TILES, FROM, false, 0, COPIES>(p, st);
+    case 1: return p.bf16 ? launch_at<D, TILES, FROM, true, 1, COPIES>(p, st) : launch_at<D, TILES, FROM, false, 1, COPIES>(p, st);
+    case 2: return p.bf16 ? launch_at<D, TILES, FROM, true, 2, COPIES>(p, st) : launch_at<D, TILES, FROM, false, 2, COPIES>(p, st);
+    default: return p.bf16 ? launch_at<D, TILES, FROM, true, 3, COPIES>(p, st) : launch_at<D, TILES, FROM, false, 3, COPIES>(p, st);
+  }
+}
+
+template <int D, int TILES, int COPIES>
+cudaError_t launch_from(const AttendParams& p, cudaStream_t st) {
+  if (!p.table) return launch_options<D, TILES, FROM_TENSORS, COPIES>(p, st);
+  if (p.cache_type != MKV_DT_E4M3) return launch_options<D, TILES, FROM_PAGES, COPIES>(p, st);
+  if constexpr (TILES == 1) return launch_options<D, 1, FROM_BYTES, COPIES>(p, st);
+  return cudaErrorInvalidValue;
 }
 
 template <int D>
 cudaError_t launch_attend_d(const AttendParams& p, cudaStream_t st) {
   if constexpr (D < 256)
-    if (p.tiles == 2) return launch_tiles<D, 2, false>(p, st);
-  return launch_tiles<D, 1, false>(p, st);
+    if (p.tiles == 2) return launch_from<D, 2, 1>(p, st);
+  return launch_from<D, 1, 1>(p, st);
 }
 
 }  // namespace

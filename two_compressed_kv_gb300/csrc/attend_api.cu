@@ -202,25 +202,25 @@ bool strides_ok(const int64_t* s, int64_t e0, int64_t e1, int64_t e2) {
 
 // How a call's rows and keys are spread, and where its workspace's parts lie.
 struct AttendLayout {
-  bool few;
+  int copies;
   int tiles, tile_tokens, groups, splits;
   uint64_t docs, part_o, part_ml, total;   // byte offsets
 };
 
 // What a CTA costs apart from its blocks of keys, in blocks, and what a join costs.
-constexpr int kCtaBlocks = 4, kJoinBlocks = 3;
+constexpr int kCtaBlocks = 8, kJoinBlocks = 4;
 
 // Row tiles: 128 / g tokens each.  Two to a CTA where there are two (each softmax then
 // has its own S buffer and K and V are read half as often), but not with heads of 256
 // (tensor memory) or 8-bit pages (their second warpgroup widens).
 AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, int window, bool e4m3, bool docs, int sms) {
   AttendLayout l;
-  l.few = nq * g <= 32;
-  l.tile_tokens = (l.few ? 32 : 128) / g;
+  l.copies = nq * g <= 32 ? 4 : nq * g <= 64 && e4m3 ? 2 : 1;
+  l.tile_tokens = 128 / l.copies / g;
   const int64_t all = up(std::max<int64_t>(nq, 1), l.tile_tokens);
   l.tiles = all > 1 && D < 256 && !e4m3 ? 2 : 1;
   l.groups = (int)up(all, l.tiles);
-  const int NB = attend_block(D, l.tiles, e4m3, l.few);
+  const int NB = attend_block(D, l.tiles, e4m3, l.copies > 1);
   const int64_t items = (int64_t)B * H * l.groups;
   int64_t keys = nk;
   if (window) keys = std::min<int64_t>(nk, (int64_t)window + l.tiles * l.tile_tokens + NB);
@@ -266,16 +266,17 @@ mkv_status attend(AttendParams& p, const AttendLayout& l, void* workspace, mkv_s
   if ((int64_t)p.B * p.H * l.groups * l.splits > kMaxGrid) return bad("attention: too many queries");
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.tiles = l.tiles;
-  p.few = l.few;
+  p.copies = l.copies;
   p.tile_tokens = l.tile_tokens;
   p.groups = l.groups;
   p.splits = l.splits;
   p.doc_range = reinterpret_cast<int2*>(ws + l.docs);
-  p.part_o = reinterpret_cast<float*>(ws + l.part_o);
+  p.part_o = reinterpret_cast<float4*>(ws + l.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (p.docs) CKP(launch_attend_docs(p, st));
-  if (p.few) CKP(p.D == 256 ? launch_attend_few_256(p, st) : launch_attend_few(p, st));
+  if (p.copies == 4) CKP(p.D == 256 ? launch_attend_4_256(p, st) : launch_attend_4(p, st));
+  else if (p.copies == 2) CKP(launch_attend_2(p, st));
   else switch (p.D) {
     case 64: CKP(launch_attend_64(p, st)); break;
     case 128: CKP(launch_attend_128(p, st)); break;
@@ -383,6 +384,7 @@ uint64_t mkv_paged_attend_workspace(const mkv_paged_cache* c, const mkv_paged_at
   }
   int sms = 0;
   if (a->n == 0) return 0;
+  if (paged_attend_streams(c, a)) return paged_attend_streaming_workspace(c, a);
   return sm_count(&sms) == MKV_OK ? paged_layout(c, a, sms).total : UINT64_MAX;
 }
 
@@ -393,6 +395,7 @@ mkv_status mkv_paged_attend(const mkv_paged_cache* c, const mkv_paged_attend_arg
   if (!aligned16(a->q) || !aligned16(a->out)) return bad("mkv_paged_attend: q and out must be 16-byte aligned");
   if (!strides_ok(a->q_stride, c->batch, a->n, a->n_q_heads))
     return bad("mkv_paged_attend: q's strides must be positive multiples of 8 elements");
+  if (paged_attend_streams(c, a)) return paged_attend_streaming(c, a, stream);
   int sms = 0;
   if (mkv_status s = sm_count(&sms)) return s;
   const AttendLayout l = paged_layout(c, a, sms);

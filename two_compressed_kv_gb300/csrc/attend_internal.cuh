@@ -7,7 +7,15 @@
 namespace mkv {
 
 constexpr float AT_BIAS = 8.f;     // weights carry a factor 2^8 until the division by their sum
-constexpr float AT_SLACK = 6.f;    // how far scores (log2) may pass the reference of the exponents
+constexpr float AT_SLACK = 6.f;    // how far scores (log2) may pass the reference of the exponents: fp16 weights,
+constexpr float AT_SLACK_BF16 = 24.f;   // bf16 ones, whose range is that of the sums (a bias by distance raises
+                                        // the maximum in every block of a row's keys)
+
+// Pairs of a sequence and a KV head whose CTAs are in one order: few, so that several CTAs
+// share keys in L2; many, so that short prompts begin with all their long pieces.  Us of 8K
+// prompts, batch 4, and of a ragged batch of 96 pairs with 8: 1542, 68; 16: 1550, 64; 32:
+// 1605, 58; pair by pair: 1549, 68 (and one 2K prompt 54, 39 with any of these).
+constexpr int AT_BUNDLE = 16;
 
 // Keys of a block, the step of the pass over the keys: tensor memory holds two blocks'
 // scores of every row tile and the outputs, and a thread a block of its row's scores, or
@@ -44,13 +52,13 @@ struct AttendParams {
   int n_pages, page_size, cache_type;
   const float *k_scale, *v_scale;
   // the grid: row tiles of a (sequence, KV head) in groups of `tiles`, their keys in `splits` parts
-  int few;                     // a row tile is four copies of 32 rows
-  int tile_tokens;             // tokens of a row tile: 128 / g, few rows: 32 / g
+  int copies;                  // of its rows that a row tile holds: 1, or with few rows 2 or 4
+  int tile_tokens;             // tokens of a row tile: 128 / copies / g
   int tiles;                   // row tiles of a CTA: 1 or 2
   int groups;                  // of row tiles
   int splits;
-  float* part_o;               // workspace: [item][tiles][128][D] sums over weights, splits > 1
-  float2* part_ml;             // [item][tiles][128] reference (log2 domain) and sum of weights
+  float4* part_o;              // workspace: [CTA][tiles][D / 4][128 rows] sums over weights, splits > 1
+  float2* part_ml;             // [CTA][tiles][128] reference (log2 domain) and sum of weights
 };
 
 // What a sequence's lengths come to: queries and keys, both within their bounds.
@@ -65,8 +73,9 @@ __device__ __forceinline__ void attend_lens(const AttendParams& p, int b, int& m
 cudaError_t launch_attend_64(const AttendParams& p, cudaStream_t st);
 cudaError_t launch_attend_128(const AttendParams& p, cudaStream_t st);
 cudaError_t launch_attend_256(const AttendParams& p, cudaStream_t st);
-cudaError_t launch_attend_few(const AttendParams& p, cudaStream_t st);   // heads of 64 and 128
-cudaError_t launch_attend_few_256(const AttendParams& p, cudaStream_t st);
+cudaError_t launch_attend_2(const AttendParams& p, cudaStream_t st);        // two copies, 8-bit pages
+cudaError_t launch_attend_4(const AttendParams& p, cudaStream_t st);        // four copies, heads of 64 and 128
+cudaError_t launch_attend_4_256(const AttendParams& p, cudaStream_t st);
 cudaError_t launch_attend_docs(const AttendParams& p, cudaStream_t st);
 cudaError_t launch_attend_join(const AttendParams& p, cudaStream_t st);
 

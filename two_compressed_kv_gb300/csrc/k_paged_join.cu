@@ -21,7 +21,7 @@ constexpr int JT = 256;
 // 1024).  Bound by three dependent latencies of L2: lengths, shares, parts.
 // grid: streams * g
 // ---------------------------------------------------------------------------
-template <int D, int T>
+template <int D, int T, bool OPT>
 __global__ void __launch_bounds__(T) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
   constexpr int LD = D / 4, NG = T / LD;       // threads of a part, parts at a time
   __shared__ float4 so[NG][LD];
@@ -33,8 +33,18 @@ __global__ void __launch_bounds__(T) paged_join_kernel(const __grid_constant__ P
   const int grp = threadIdx.x / LD, d = (threadIdx.x - grp * LD);
   griddep_wait();
   griddep_launch();
-  const int n = paged_len(p, b);
-  if (n == 0) {
+  int n, first_block = 0;
+  int64_t out_row = row;
+  if constexpr (OPT) {
+    const PagedReach reach(p, b);
+    if (head / p.heads >= reach.m) return;
+    n = reach.n;
+    first_block = reach.first;
+    out_row = paged_row(p, b, h, head);
+  } else {
+    n = paged_len(p, b);
+  }
+  if (!OPT && n == 0) {
     // no CTA of the split kernel meets an empty stream
     if (grp == 0) store_out4(p, row * D + 4 * d, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
     if (threadIdx.x == 0) {
@@ -44,7 +54,7 @@ __global__ void __launch_bounds__(T) paged_join_kernel(const __grid_constant__ P
     return;
   }
   const PagedShares shares(p, p.pre[p.B]);
-  const int64_t load = paged_load(p, n);
+  const int64_t load = paged_load(p, n, first_block);
   const int64_t first = p.pre[b] + h * load;
   const int i0 = shares.of(first + p.piece_load), i1 = shares.of(first + load - 1);
   if (i0 == i1) return;                        // written by its CTA
@@ -80,9 +90,9 @@ __global__ void __launch_bounds__(T) paged_join_kernel(const __grid_constant__ P
       sum += sl[k] * f;
       a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
     }
-    store_out4(p, row * D + 4 * d, a, sum == 0.f ? 0.f : 1.f / sum);
+    store_out4(p, out_row * D + 4 * d, a, sum == 0.f ? 0.f : 1.f / sum);
     if (d == 0) {
-      store_stat(p, row, top, sum);
+      store_stat(p, out_row, top, sum);
     }
   }
 }
@@ -144,8 +154,11 @@ template <int D>
 cudaError_t join_d(const PagedAttnParams& p, cudaStream_t st) {
   const int64_t rows = (int64_t)p.B * p.H * p.g;
   const dim3 grid((unsigned)rows);
-  if (rows <= 2 * p.sms) return launch_kernel(paged_join_kernel<D, 1024>, grid, dim3(1024), 0, st, true, 0, p);
-  return launch_kernel(paged_join_kernel<D, JT>, grid, dim3(JT), 0, st, true, 0, p);
+  if (rows <= 2 * p.sms)
+    return p.opt ? launch_kernel(paged_join_kernel<D, 1024, true>, grid, dim3(1024), 0, st, true, 0, p)
+                 : launch_kernel(paged_join_kernel<D, 1024, false>, grid, dim3(1024), 0, st, true, 0, p);
+  return p.opt ? launch_kernel(paged_join_kernel<D, JT, true>, grid, dim3(JT), 0, st, true, 0, p)
+               : launch_kernel(paged_join_kernel<D, JT, false>, grid, dim3(JT), 0, st, true, 0, p);
 }
 
 }  // namespace

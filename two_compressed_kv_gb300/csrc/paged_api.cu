@@ -171,6 +171,54 @@ DecodeLayout decode_layout(const mkv_paged_cache* c, const mkv_paged_decode_args
   return l;
 }
 
+// What a decode call and a call with few new tokens have in common.
+PagedAttnParams stream_params(const mkv_paged_cache* c, const DecodeLayout& l, void* workspace, float scale_arg, int sms) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  PagedAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.kp = static_cast<const uint8_t*>(c->k_pages);
+  p.vp = static_cast<const uint8_t*>(c->v_pages);
+  p.table = c->page_table;
+  p.ks = c->k_scale;
+  p.vs = c->v_scale;
+  p.status = c->status;
+  p.table_stride = c->table_stride;
+  p.rows = (int64_t)c->n_pages * c->n_kv_heads * c->page_size;
+  p.B = c->batch;
+  p.H = c->n_kv_heads;
+  p.n_pages = c->n_pages;
+  p.bpp = c->page_size / PA_BLOCK;
+  p.limit = (int)l.limit;
+  const double scale = scale_arg > 0.f ? (double)scale_arg : 1.0 / std::sqrt((double)c->head_dim);
+  p.scale2 = (float)(scale * 1.4426950408889634);
+  p.part_o = reinterpret_cast<float*>(ws + l.part_o);
+  p.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
+  p.stat = reinterpret_cast<float4*>(ws + l.stat);
+  p.pre = reinterpret_cast<int64_t*>(ws + l.pre);
+  p.score_stride = l.score_stride;
+  p.sms = sms;
+  p.G = l.G;
+  p.min_blocks = kMinBlocks;
+  p.split = l.split;
+  p.cluster = l.cluster;
+  p.piece_load = kPieceLoad;
+  p.tail16 = kTail16;
+  p.tail_from = kTailFrom;
+  return p;
+}
+
+// The decode call whose sizes a call with few new tokens has: their heads side by side.
+mkv_paged_decode_args as_decode(const mkv_paged_cache* c, const mkv_paged_attend_args* a) {
+  mkv_paged_decode_args d;
+  std::memset(&d, 0, sizeof(d));
+  d.n_q_heads = a->n_q_heads * a->n;
+  d.q_dtype = d.out_dtype = a->q_dtype;
+  const int64_t cap = (int64_t)c->max_pages * c->page_size;
+  d.max_len = a->max_len ? std::min(a->max_len, cap) : cap;
+  if (a->window) d.max_len = std::min<int64_t>(d.max_len, (int64_t)a->window + a->n + PA_BLOCK);
+  return d;
+}
+
 // ---- evict -------------------------------------------------------------------
 
 int64_t evict_limit(const mkv_paged_cache* c, const mkv_paged_evict_args* a) {
@@ -388,6 +436,54 @@ cudaError_t encode_map(CUtensorMap* map, const void* base, bool bytes, int rank,
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Rows of 8-bit pages that a few query rows share go through the streaming kernel, whose
+// products need no widened copy of them in shared memory: with 8 columns or fewer.  Us of
+// this kernel and of the one of many queries: 32 streams of 32768 slots of 128, 4 rows: 73,
+// 100; 256 streams of 2048, 16 rows: 90, 61.  16-bit pages: 98, 92, so they are not here.
+bool paged_attend_streams(const mkv_paged_cache* c, const mkv_paged_attend_args* a) {
+  return c->dtype == MKV_DT_E4M3 && (int64_t)a->n * (a->n_q_heads / c->n_kv_heads) <= 8;
+}
+
+uint64_t paged_attend_streaming_workspace(const mkv_paged_cache* c, const mkv_paged_attend_args* a) {
+  const mkv_paged_decode_args d = as_decode(c, a);
+  int sms = 0;
+  return sm_count(&sms) == MKV_OK ? decode_layout(c, &d, sms).total : UINT64_MAX;
+}
+
+mkv_status paged_attend_streaming(const mkv_paged_cache* c, const mkv_paged_attend_args* a, mkv_stream_t stream) {
+  const mkv_paged_decode_args d = as_decode(c, a);
+  int sms = 0;
+  if (mkv_status s = sm_count(&sms)) return s;
+  const DecodeLayout l = decode_layout(c, &d, sms);
+  if (!a->workspace || !aligned16(a->workspace)) return bad("mkv_paged_attend: workspace must be 16-byte aligned");
+  if (a->workspace_bytes < l.total) return bad("mkv_paged_attend: workspace too small");
+  PagedAttnParams p = stream_params(c, l, a->workspace, a->scale, sms);
+  const int64_t cap = (int64_t)c->max_pages * c->page_size;
+  p.limit = (int)(a->max_len ? std::min(a->max_len, cap) : cap);
+  p.opt = 1;
+  p.tokens = a->n;
+  p.heads = a->n_q_heads / c->n_kv_heads;
+  p.g = p.tokens * p.heads;
+  p.q = a->q;
+  p.q_sb = a->q_stride[0];
+  p.q_st = a->q_stride[1];
+  p.q_sh = a->q_stride[2];
+  p.q_bf16 = a->q_dtype == MKV_DT_BF16;
+  p.out = a->out;
+  p.out_type = a->q_dtype;
+  p.lse = a->lse;
+  p.lens = a->seq_lens;
+  p.new_lens = a->new_lens;
+  p.tree = a->tree;
+  p.slopes = a->slopes;
+  p.window = a->window;
+  p.cap2 = (float)(a->cap * 1.4426950408889634);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  CKP(launch_paged_opt(p, c->head_dim, st));
+  if (l.split) CKP(launch_paged_merge(p, c->head_dim, st));
+  return MKV_OK;
+}
+
 }  // namespace mkv
 
 extern "C" {
@@ -544,23 +640,8 @@ mkv_status mkv_paged_decode(const mkv_paged_cache* c, const mkv_paged_decode_arg
   if (a->workspace_bytes < l.total) return bad("mkv_paged_decode: workspace too small");
   if (a->acc && (int64_t)c->batch * c->n_kv_heads * up(l.limit, 1024) > kMaxGrid)
     return bad("mkv_paged_decode: too many tokens for accumulated weights");
-  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
-  PagedAttnParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.kp = static_cast<const uint8_t*>(c->k_pages);
-  p.vp = static_cast<const uint8_t*>(c->v_pages);
-  p.table = c->page_table;
-  p.ks = c->k_scale;
-  p.vs = c->v_scale;
-  p.status = c->status;
-  p.table_stride = c->table_stride;
-  p.rows = (int64_t)c->n_pages * c->n_kv_heads * c->page_size;
-  p.B = c->batch;
-  p.H = c->n_kv_heads;
+  PagedAttnParams p = stream_params(c, l, a->workspace, a->scale, sms);
   p.g = a->n_q_heads / c->n_kv_heads;
-  p.n_pages = c->n_pages;
-  p.bpp = c->page_size / PA_BLOCK;
-  p.limit = (int)l.limit;
   p.q = a->q;
   p.q_sb = a->q_stride[0];
   p.q_sh = a->q_stride[1];
@@ -569,24 +650,9 @@ mkv_status mkv_paged_decode(const mkv_paged_cache* c, const mkv_paged_decode_arg
   p.out_type = a->out_dtype;
   p.lse = a->lse;
   p.lens = a->seq_lens;
-  const double scale = a->scale > 0.f ? (double)a->scale : 1.0 / std::sqrt((double)c->head_dim);
-  p.scale2 = (float)(scale * 1.4426950408889634);
   p.acc = a->acc;
   p.acc_stride = a->acc_stride;
-  p.part_o = reinterpret_cast<float*>(ws + l.part_o);
-  p.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
-  p.stat = reinterpret_cast<float4*>(ws + l.stat);
-  p.pre = reinterpret_cast<int64_t*>(ws + l.pre);
-  p.scores = a->acc ? reinterpret_cast<float*>(ws + l.scores) : nullptr;
-  p.score_stride = l.score_stride;
-  p.sms = sms;
-  p.G = l.G;
-  p.min_blocks = kMinBlocks;
-  p.split = l.split;
-  p.cluster = l.cluster;
-  p.piece_load = kPieceLoad;
-  p.tail16 = kTail16;
-  p.tail_from = kTailFrom;
+  p.scores = a->acc ? reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + l.scores) : nullptr;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   switch (c->head_dim) {
     case 64: CKP(launch_paged_attn_64(p, c->dtype, st)); break;

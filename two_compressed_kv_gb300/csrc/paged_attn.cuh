@@ -160,9 +160,11 @@ __device__ __forceinline__ uint32_t piece_on(uint32_t at, int by) {
 }
 
 // ---------------------------------------------------------------------------
+// OPT: columns are new tokens times their heads, with a window, a tree, scores capped or
+// biased; a block's scores are changed in the registers that hold them.
 // grid: split ? 3 G : streams * cluster; cluster (cluster, 1, 1); block: NW warps; dynamic smem PA::SMEM
 // ---------------------------------------------------------------------------
-template <int CT, int D, bool WIDE, int NW, bool THIRD>
+template <int CT, int D, bool WIDE, int NW, bool THIRD, bool OPT>
 __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
     paged_attn_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
@@ -213,8 +215,15 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
     for (int k = 0; k < run; ++k) {
       const int i = tid * run + k;
       if (i < p.B) {
-        len_of[i] = paged_len(p, i);
-        sum += paged_load(p, len_of[i]) * p.H;
+        if constexpr (OPT) {
+          const PagedReach reach(p, i);
+          len_of[i] = reach.n;
+          sum += paged_load(p, reach.n, reach.first) * p.H;
+          if (blockIdx.x == 0 && reach.outside && p.status) atomicOr(p.status, DEV_ERR_CHECK);
+        } else {
+          len_of[i] = paged_len(p, i);
+          sum += paged_load(p, len_of[i]) * p.H;
+        }
       }
     }
     int64_t inc = sum;
@@ -231,7 +240,8 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
       const int i = tid * run + k;
       if (i < p.B) {
         pre[i] = base;
-        base += paged_load(p, len_of[i]) * p.H;
+        if constexpr (OPT) base += paged_load(p, len_of[i], PagedReach(p, i).first) * p.H;
+        else base += paged_load(p, len_of[i]) * p.H;
       }
       if (i == p.B - 1) pre[p.B] = base;
     }
@@ -253,31 +263,43 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
 
   while (true) {
     // next piece: blocks [j0, j1) of stream (b, h)
-    int h, j0, j1, n, nb;
+    int h, j0, j1, n, nb, first_block = 0;
     if (p.split) {
       if (at >= g1) break;
       while (pre[b + 1] <= at) ++b;
       n = len_of[b];
       nb = (n + PA_BLOCK - 1) / PA_BLOCK;
       const int64_t off = at - pre[b];
-      const int load = (int)paged_load(p, n);
+      if constexpr (OPT) first_block = PagedReach(p, b).first;
+      const int load = (int)paged_load(p, n, first_block);
       h = (int)div_small(off, load);
       const int v0 = (int)(off - (int64_t)h * load), v1 = (int)min((int64_t)load, v0 + (g1 - at));
       at += v1 - v0;
       j0 = max(0, v0 - p.piece_load);
       j1 = v1 - p.piece_load;
       if (j1 <= j0) continue;
+      j0 += first_block;
+      j1 += first_block;
     } else {
       const int s = blockIdx.x / p.cluster, rank = blockIdx.x - s * p.cluster;
       b = s / p.H;
       h = s - b * p.H;
-      n = paged_len(p, b);
+      bool outside;
+      if constexpr (OPT) {
+        const PagedReach reach(p, b);
+        n = reach.n;
+        first_block = reach.first;
+        outside = reach.outside;
+      } else {
+        n = paged_len(p, b);
+        outside = p.lens[b] != n;
+      }
       nb = (n + PA_BLOCK - 1) / PA_BLOCK;
-      j0 = (int)((int64_t)nb * rank / p.cluster);
-      j1 = (int)((int64_t)nb * (rank + 1) / p.cluster);
-      if (rank == 0 && h == 0 && tid == 0 && p.status && p.lens[b] != n) atomicOr(p.status, DEV_ERR_CHECK);
+      j0 = first_block + (int)((int64_t)(nb - first_block) * rank / p.cluster);
+      j1 = first_block + (int)((int64_t)(nb - first_block) * (rank + 1) / p.cluster);
+      if (rank == 0 && h == 0 && tid == 0 && p.status && outside) atomicOr(p.status, DEV_ERR_CHECK);
     }
-    if (p.split && h == 0 && j0 == 0 && tid == 0 && p.status && p.lens[b] != n)
+    if (!OPT && p.split && h == 0 && j0 == 0 && tid == 0 && p.status && p.lens[b] != n)
       atomicOr(p.status, DEV_ERR_CHECK);
     const int64_t stream = (int64_t)b * p.H + h;
 
@@ -328,8 +350,13 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
     for (int w = 0; w < NH; ++w) {
       const int i = r + 8 * w;
       const bool live = i < p.g;
-      const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)b * p.q_sb +
-                          (int64_t)(h * p.g + (live ? i : 0)) * p.q_sh;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)b * p.q_sb;
+      if constexpr (OPT) {
+        const int t = live ? i / p.heads : 0, hd = live ? i - t * p.heads : 0;
+        q += (int64_t)t * p.q_st + (int64_t)(h * p.heads + hd) * p.q_sh;
+      } else {
+        q += (int64_t)(h * p.g + (live ? i : 0)) * p.q_sh;
+      }
       if constexpr (E4) {
         // channels 64 i + 16 c + 4 j + {0, 1}, {2, 3} in step 4 i + j
         uint2 v[C::KS];
@@ -371,6 +398,38 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
             qb[w][s][k] = live ? v : 0u;
           }
       }
+    }
+
+    // OPT, for each of the lane's columns: the slots before the new tokens that it sees, from
+    // klo on, the new ones, its place and its slope.  Scores carry the factor sr themselves.
+    float sr[NH][2], slope[NH][2];
+    int klo[NH][2], place[NH][2], base = 0;
+    uint64_t sees[NH][2];
+    if constexpr (OPT) {
+      const int m = PagedReach(p, b).m;
+      base = n - m;
+      const uint64_t valid = (1ull << m) - 1;       // m <= 16
+#pragma unroll
+      for (int w = 0; w < NH; ++w)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int col = 8 * w + 2 * c + k, t = col / p.heads;
+          const bool live = col < p.g && t < m;
+          sr[w][k] = sc[w][k];
+          if (p.cap2 > 0.f || p.slopes) sc[w][k] = 1.f;
+          slope[w][k] = p.slopes && live ? p.slopes[h * p.heads + col - t * p.heads] * 1.4426950408889634f : 0.f;
+          uint64_t s = live ? (p.tree ? p.tree[(int64_t)b * p.tokens + t] & valid : (2ull << t) - 1) : 0ull;
+          int depth = t;
+          if (p.tree) depth = __popcll(s & ~(1ull << (t & 63)));
+          if (p.window)
+            for (int i = 0; i < m; ++i) {
+              const int other = p.tree ? __popcll(p.tree[(int64_t)b * p.tokens + i] & valid & ~(1ull << i)) : i;
+              if (depth - other >= p.window) s &= ~(1ull << i);
+            }
+          sees[w][k] = s;
+          place[w][k] = base + depth;
+          klo[w][k] = !live ? INT32_MAX : p.window ? max(0, place[w][k] - p.window + 1) : 0;
+        }
     }
 
     float o[NH][C::KS][4];                     // O^T: rows channels, columns heads
@@ -464,7 +523,26 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
             s[u][w][k] = part[0][w][k] + part[1][w][k];
             if constexpr (CH == 4) s[u][w][k] += part[2][w][k] + part[3][w][k];
           }
-        if (left[u] < PA_BLOCK) {
+        if constexpr (OPT) {
+          const int t0 = (j0 + warp + NW * (i + u)) * PA_BLOCK;
+#pragma unroll
+          for (int w = 0; w < NH; ++w)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int t = t0 + tok_r + 8 * (k >> 1), x = k & 1;
+              float z = s[u][w][k];
+              if (p.cap2 > 0.f) z = p.cap2 * tanh_log2(z * sr[w][x] * (2.885390081777927f / p.cap2));
+              else if (p.slopes) z *= sr[w][x];
+              if (p.slopes) {
+                int at = t;
+                if (p.tree && t >= base && t < n)
+                  at = base + __popcll(p.tree[(int64_t)b * p.tokens + t - base] & ((1ull << (n - base)) - 1) & ~(1ull << (t - base)));
+                z -= slope[w][x] * fabsf((float)(place[w][x] - at));
+              }
+              const bool seen = t < base ? t >= klo[w][x] : t - base < 16 && (sees[w][x] >> (t - base) & 1);
+              s[u][w][k] = seen && left[u] > 0 ? z : -CUDART_INF_F;
+            }
+        } else if (left[u] < PA_BLOCK) {
 #pragma unroll
           for (int w = 0; w < NH; ++w)
 #pragma unroll
@@ -662,10 +740,15 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
         }
       }
     __syncthreads();
-    const bool whole = j0 == 0 && j1 == nb && p.cluster == 1;
+    const bool whole = j0 == first_block && j1 == nb && p.cluster == 1;
+    // the output's row of a column; -1: a new token that is not there
+    auto row_of = [&](int col) {
+      if constexpr (OPT) return col / p.heads < n - base ? paged_row(p, b, h, col) : (int64_t)-1;
+      return stream * p.g + col;
+    };
     float* own = reinterpret_cast<float*>(smem + C::MERGE);
     const float vs = CT == MKV_DT_E4M3 && p.vs ? p.vs[h] : 1.f;
-    const int64_t part = 2 * (int64_t)blockIdx.x + (j0 == 0 ? 1 : 0);
+    const int64_t part = 2 * (int64_t)blockIdx.x + (j0 == first_block ? 1 : 0);
     for (int e = tid; e < p.g * (D / 4); e += NW * 32) {
       const int head = e / (D / 4), d = (e - head * (D / 4)) * 4;
       float top = sm_m[0][head];
@@ -683,7 +766,8 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
       a.x *= vs, a.y *= vs, a.z *= vs, a.w *= vs;
       if (whole) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t row = stream * p.g + head;
+        const int64_t row = row_of(head);
+        if (OPT && row < 0) continue;
         store_out4(p, row * D + d, a, inv);
         if (d == 0) {
           store_stat(p, row, top, sum);
@@ -728,7 +812,8 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
               sum += ml[q].y * f;
               a.x += v[q].x * f, a.y += v[q].y * f, a.z += v[q].z * f, a.w += v[q].w * f;
             }
-          const int64_t row = stream * p.g + head;
+          const int64_t row = row_of(head);
+          if (OPT && row < 0) continue;
           store_out4(p, row * D + d, a, sum == 0.f ? 0.f : 1.f / sum);
           if (d == 0) store_stat(p, row, top, sum);
         }
@@ -743,45 +828,45 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
   }
 }
 
-template <int CT, int D, bool WIDE, int NW, bool THIRD>
+template <int CT, int D, bool WIDE, int NW, bool THIRD, bool OPT>
 cudaError_t launch_pa_third(const PagedAttnParams& p, cudaStream_t st) {
   using C = PA<CT, D, WIDE, NW>;
   CUtensorMap kmap, vmap;
   if (cudaError_t e = encode_rows_map(&kmap, p.kp, p.rows, C::ROW, PA_BLOCK)) return e;
   if (cudaError_t e = encode_rows_map(&vmap, p.vp, p.rows, C::ROW, PA_BLOCK)) return e;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<CT, D, WIDE, NW, THIRD>,
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<CT, D, WIDE, NW, THIRD, OPT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t grid = p.split ? PA_SHARES * p.G : (int64_t)p.B * p.H * p.cluster;
-  return launch_kernel(paged_attn_kernel<CT, D, WIDE, NW, THIRD>, dim3((unsigned)grid), dim3(NW * 32), C::SMEM, st, true, p.cluster,
+  return launch_kernel(paged_attn_kernel<CT, D, WIDE, NW, THIRD, OPT>, dim3((unsigned)grid), dim3(NW * 32), C::SMEM, st, true, p.cluster,
                        p, kmap, vmap);
 }
 
-template <int CT, int D, bool WIDE, int NW>
+template <int CT, int D, bool WIDE, int NW, bool OPT>
 cudaError_t launch_pa_nw(const PagedAttnParams& p, cudaStream_t st) {
-  if constexpr (CT == MKV_DT_BF16)
-    if (p.out_type == MKV_DT_F32) return launch_pa_third<CT, D, WIDE, NW, true>(p, st);
-  return launch_pa_third<CT, D, WIDE, NW, false>(p, st);
+  if constexpr (CT == MKV_DT_BF16 && !OPT)
+    if (p.out_type == MKV_DT_F32) return launch_pa_third<CT, D, WIDE, NW, true, OPT>(p, st);
+  return launch_pa_third<CT, D, WIDE, NW, false, OPT>(p, st);
 }
 
 // 4 warps a CTA and several CTAs an SM; where all CTAs run at once with one an SM
 // (of 152 SMs clusters of 8 reach about half), 8 warps.  Rows of 512 bytes, whose
 // rings do not fit, apart.
-template <int CT, int D, bool WIDE>
+template <int CT, int D, bool WIDE, bool OPT>
 cudaError_t launch_pa(const PagedAttnParams& p, cudaStream_t st) {
   if constexpr (PA<CT, D, WIDE, 4>::ROW < 512)
     if ((p.split ? p.G : (int64_t)p.B * p.H * p.cluster) <= (p.cluster == 8 ? p.sms / 2 : p.sms))
-      return launch_pa_nw<CT, D, WIDE, 8>(p, st);
-  return launch_pa_nw<CT, D, WIDE, 4>(p, st);
+      return launch_pa_nw<CT, D, WIDE, 8, OPT>(p, st);
+  return launch_pa_nw<CT, D, WIDE, 4, OPT>(p, st);
 }
 
 template <int D>
 cudaError_t launch_pa_d(const PagedAttnParams& p, int cache_type, cudaStream_t st) {
   const bool wide = p.g > 8;
   switch (cache_type) {
-    case MKV_DT_F16: return wide ? launch_pa<MKV_DT_F16, D, true>(p, st) : launch_pa<MKV_DT_F16, D, false>(p, st);
-    case MKV_DT_BF16: return wide ? launch_pa<MKV_DT_BF16, D, true>(p, st) : launch_pa<MKV_DT_BF16, D, false>(p, st);
-    default: return wide ? launch_pa<MKV_DT_E4M3, D, true>(p, st) : launch_pa<MKV_DT_E4M3, D, false>(p, st);
+    case MKV_DT_F16: return wide ? launch_pa<MKV_DT_F16, D, true, false>(p, st) : launch_pa<MKV_DT_F16, D, false, false>(p, st);
+    case MKV_DT_BF16: return wide ? launch_pa<MKV_DT_BF16, D, true, false>(p, st) : launch_pa<MKV_DT_BF16, D, false, false>(p, st);
+    default: return wide ? launch_pa<MKV_DT_E4M3, D, true, false>(p, st) : launch_pa<MKV_DT_E4M3, D, false, false>(p, st);
   }
 }
 

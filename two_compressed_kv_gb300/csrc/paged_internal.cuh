@@ -126,7 +126,37 @@ struct PagedAttnParams {
   int tail_from;                  // from this many blocks a CTA on
   int split;                      // 0: a cluster of CTAs per stream
   int cluster;                    // its size, 1 to 8 (split: 1)
+  // Several new tokens, scores with options (kernels with OPT): the g "heads" of a stream are
+  // its new tokens times their heads.
+  int opt;
+  int tokens, heads;              // g = tokens * heads
+  int64_t q_st;                   // elements between tokens of q
+  const int32_t* new_lens;        // or NULL: tokens
+  const uint64_t* tree;           // or NULL: a chain
+  const float* slopes;
+  int window;
+  float cap2;                     // cap * log2(e); 0: none
 };
+
+// Cached and new tokens of sequence b with options, both within their bounds, and the
+// first block that one of the new tokens sees.
+struct PagedReach {
+  int n, m, first;
+  bool outside;
+  __device__ __forceinline__ PagedReach(const PagedAttnParams& p, int b) {
+    const int k = p.lens[b], q = p.new_lens ? p.new_lens[b] : p.tokens;
+    n = max(0, min(k, p.limit));
+    m = max(0, min(min(q, p.tokens), n));
+    outside = k != n || (p.new_lens && q != m);
+    first = p.window ? max(0, n - m - p.window + 1) / PA_BLOCK : 0;
+    if (m == 0) n = first = 0;    // nothing to attend for
+  }
+};
+// Row of the output for column `col` of stream (b, h).
+__device__ __forceinline__ int64_t paged_row(const PagedAttnParams& p, int64_t b, int h, int col) {
+  const int t = col / p.heads;
+  return (b * p.tokens + t) * (p.H * p.heads) + h * p.heads + col - t * p.heads;
+}
 
 // Cached tokens of sequence b as the kernels count them.
 __device__ __forceinline__ int paged_len(const PagedAttnParams& p, int b) {
@@ -141,8 +171,8 @@ __device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
 }
 
 // Load of a stream of n tokens: its blocks and a fixed cost.
-__device__ __forceinline__ int64_t paged_load(const PagedAttnParams& p, int n) {
-  return n == 0 ? 0 : (n + PA_BLOCK - 1) / PA_BLOCK + p.piece_load;
+__device__ __forceinline__ int64_t paged_load(const PagedAttnParams& p, int n, int first = 0) {
+  return n == 0 ? 0 : (n + PA_BLOCK - 1) / PA_BLOCK - first + p.piece_load;
 }
 
 // How the split kernel's CTAs share the load of all streams: the first G, which
@@ -199,10 +229,19 @@ __device__ __forceinline__ void store_stat(const PagedAttnParams& p, int64_t row
   if (p.scores) *reinterpret_cast<float2*>(p.stat + row) = make_float2(top, lg);
 }
 
+// a tanh: x is 2 log2(e) times the argument; within 2^-22 of it
+__device__ __forceinline__ float tanh_log2(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(fabsf(x)));
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(e + 1.f));
+  return copysignf(fmaf(-2.f, r, 1.f), x);
+}
+
 // g <= 8 and g <= 16 variants per head dim (one translation unit each)
 cudaError_t launch_paged_attn_64(const PagedAttnParams& p, int cache_type, cudaStream_t st);
 cudaError_t launch_paged_attn_128(const PagedAttnParams& p, int cache_type, cudaStream_t st);
 cudaError_t launch_paged_attn_256(const PagedAttnParams& p, int cache_type, cudaStream_t st);
+cudaError_t launch_paged_opt(const PagedAttnParams& p, int D, cudaStream_t st);   // E4M3, g <= 8
 cudaError_t launch_paged_merge(const PagedAttnParams& p, int D, cudaStream_t st);
 cudaError_t launch_paged_weights(const PagedAttnParams& p, cudaStream_t st);
 
