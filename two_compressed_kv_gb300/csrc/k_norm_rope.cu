@@ -13,7 +13,7 @@
 // What bounds it: memory, as long as enough loads are in flight beside the sums over a
 // head: two heads at a time, the next two loaded while these are worked on.  8192 x 4
 // tokens of 32 + 8 bf16 heads of 128: 128 us, 5.2 TB/s; the gradient of 4099 x 4 tokens
-// of 16 + 16: 84 us, 4.8 TB/s; 8 tokens: 3.9 us.  (One head at a time, not ahead: 168
+// of 16 + 16: 82 us, 4.9 TB/s; 8 tokens: 3.9 us.  (One head at a time, not ahead: 168
 // and 172 us; more resident warps with fewer registers: 162 to 185; four heads: 134.)
 #include <type_traits>
 
@@ -199,15 +199,20 @@ __global__ void __launch_bounds__(NT, FORM == ELEM ? 1 : 2)
     // the next heads' loads are in flight while these are worked on, the first ones' during
     // the angles
     typename U::Raw rx[HB][NU], rg[GRAD ? HB : 1][NU];
+    x += h0 * xh;
+    o += h0 * oh;
+    if constexpr (GRAD) g += h0 * gh;
     auto load = [&](int h) {
 #pragma unroll
       for (int k = 0; k < HB; ++k)
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
           const U unit(p.plan, lane + n * p.lanes, p.units, p.rot_units);
-          rx[k][n] = unit.load(x + (h + k) * xh, h + k < h1);
-          if constexpr (GRAD) rg[k][n] = unit.load(g + (h + k) * gh, h + k < h1);
+          rx[k][n] = unit.load(x + k * xh, h + k < h1);
+          if constexpr (GRAD) rg[k][n] = unit.load(g + k * gh, h + k < h1);
         }
+      x += HB * xh;
+      if constexpr (GRAD) g += HB * gh;
     };
     load(h0);
     float2 A[NU][NP], B[NU][NP];
@@ -314,9 +319,10 @@ __global__ void __launch_bounds__(NT, FORM == ELEM ? 1 : 2)
               y[i] = fma2(f[k][n][i], twice(-mean * r), mul2(u, w[n][i]));
             }
           }
-          if (h + k < h1 && unit.there) unit.store(o + (h + k) * oh, y);
+          if (h + k < h1 && unit.there) unit.store(o + k * oh, y);
         }
       }
+      o += HB * oh;
     }
   }
   if constexpr (GRAD) {
