@@ -768,7 +768,7 @@ mkv_status mkv_prefill(const mkv_prefill_args* args, mkv_stream_t stream);
 typedef struct {
   const void* q;             /* device [batch][n][n_q_heads][head_dim], 16-byte aligned; F16 or BF16, the cache's
                                 type unless that is E4M3 */
-  void* out;                 /* device, the same shape and type, contiguous, 16-byte aligned */
+  void* out;                 /* device, the same shape and type, contiguous, 16-byte aligned; not q */
   float* lse;                /* device [batch][n][n_q_heads], or NULL */
   const int32_t* seq_lens;   /* device [batch]: cached tokens with the new ones, 0 .. max_len */
   const int32_t* new_lens;   /* device [batch]: new tokens of each sequence, 0 .. n, or NULL: n, or seq_lens[b]

@@ -291,7 +291,7 @@ def test_prefill_heads(M, heads, kv, causal):
     prefill_check(M, BF16, 1, 70, 150, heads, kv, 128, causal=causal)
 
 
-MASKS = [dict(causal=False), dict(window=1), dict(window=50), dict(window=200, causal=False), dict(window=1, causal=False),
+MASKS = [dict(causal=False), dict(window=2**31 - 1), dict(window=2**31 - 1, causal=False), dict(window=1), dict(window=50), dict(window=200, causal=False), dict(window=1, causal=False),
          dict(prefix=[100, 0]), dict(prefix=[3, 1000]), dict(prefix=[260, 130], window=70),
          dict(docs="blocks"), dict(docs="mixed"), dict(docs="mixed", causal=False), dict(docs="blocks", window=40),
          dict(docs="blocks", prefix=[90, 200]), dict(docs="own"), dict(cap=2.0), dict(cap=30.0, size=4.0),
@@ -486,7 +486,7 @@ def test_attend_heads(M, h, g, m):
 
 @pytest.mark.parametrize("ctype,qtype", [(BF16, BF16), (E4M3, F16)])
 @pytest.mark.parametrize("kw", [dict(cap=3.0, size=4.0), dict(cap=30.0), dict(slopes=True), dict(window=1), dict(window=7),
-                                dict(window=130), dict(slopes=True, cap=4.0, window=60), dict(scale=0.5)])
+                                dict(window=130), dict(window=2**31 - 1), dict(slopes=True, cap=4.0, window=60), dict(scale=0.5)])
 def test_attend_scores(M, ctype, qtype, kw):
     kw = dict(kw)
     if kw.get("slopes"):
@@ -668,3 +668,33 @@ def test_calls_on_two_streams_at_once(M):
         got = [M.mkv_paged_attend(cache, x, lens, stream=s) for x, s in zip(q, streams)]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_workspaces_of_the_caller(M):
+    """A tensor of as many bytes as the call names is enough, and one byte less is refused."""
+    def room(n):
+        return torch.full((n,), 0xff, dtype=torch.uint8, device=DEV)
+
+    def check(call, n, outs):
+        want = call(None)
+        assert n > 0
+        assert all(torch.equal(a, b) for a, b in zip(outs(want), outs(call(room(n)))))
+        with pytest.raises(M.MkvError):
+            call(room(n - 1))
+
+    q, k, v = rnd((1, 3, 8, 64), BF16, 1), rnd((1, 5000, 2, 64), BF16, 2), rnd((1, 5000, 2, 64), BF16, 3)
+    docs = torch.zeros((1, 5000), dtype=torch.int32, device=DEV)
+    check(lambda w: M.mkv_prefill(q, k, v, docs=docs, workspace=w),
+          M.mkv_prefill_workspace(1, 3, 5000, 8, 2, 64, docs=True), lambda o: [o])
+    lens = i32([5000, 4000])
+    for ctype, m in ((F16, 3), (E4M3, 1), (E4M3, 40)):
+        cache = make_cache(M, ctype, 2, 2, 64, 64, 80, 3)
+        x = rnd((2, m, 8, 64), F16, 4)
+        check(lambda w: M.mkv_paged_attend(cache, x, lens, workspace=w),
+              M.mkv_paged_attend_workspace(cache, m, 8), lambda o: [o])
+    plan, w32 = M.mkv_rope_plan(64), rnd((64,), F32, 5)
+    g = rnd((1, 3, 8, 64), BF16, 6)
+    check(lambda w: M.mkv_norm_rope_grad(plan, g, q, w32, workspace=w), M.mkv_norm_rope_grad_workspace(plan), list)
+    assert M.mkv_prefill_workspace(2, 4096, 4096, 16, 16, 128) == 0   # many rows: no parts
+    with pytest.raises(M.MkvError):
+        M.mkv_prefill_workspace(1, 3, 5000, 8, 3, 64)

@@ -191,7 +191,7 @@ def test_prefill_sizes(M, kw):
 @pytest.mark.parametrize("kw", [
     dict(q=None), dict(k=None), dict(v=None), dict(out=None), dict(q=FAKE + 2), dict(out=FAKE + 8), dict(k=FAKE + 4),
     dict(q_stride=[7 * 512, 508, 128]), dict(k_stride=[9 * 256, 256, 0]), dict(v_stride=[-8, 256, 128]),
-    dict(out_stride=[0, 512, 128])])
+    dict(out_stride=[0, 512, 128]), dict(out=FAKE), dict(out=2 * FAKE), dict(out=3 * FAKE)])
 def test_prefill_pointers_and_strides(M, kw):
     a = _prefill_args(M, **kw)
     assert M.lib.mkv_prefill(ctypes.byref(a), None) == M.MKV_ERR_INVALID_ARG
@@ -237,7 +237,7 @@ def test_attend_sizes(M, kw):
 
 
 @pytest.mark.parametrize("kw", [dict(q=None), dict(out=None), dict(seq_lens=None), dict(q=FAKE + 2), dict(out=FAKE + 8),
-                                dict(q_stride=[2560, 512, 100]), dict(q_stride=[2560, 0, 128])])
+                                dict(q_stride=[2560, 512, 100]), dict(q_stride=[2560, 0, 128]), dict(out=FAKE)])
 def test_attend_pointers_and_strides(M, kw):
     c, a = _cache(M), _attend_args(M, **kw)
     assert M.lib.mkv_paged_attend(ctypes.byref(c), ctypes.byref(a), None) == M.MKV_ERR_INVALID_ARG

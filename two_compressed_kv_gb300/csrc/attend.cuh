@@ -15,14 +15,26 @@
 //                   out of tensor memory, exponents, 16-bit weights back over them;
 //   O += P V        tcgen05, P in tensor memory, V in shared memory, O in tensor
 //                   memory (fp32).
-// Roles: one warp copies (TMA, 128-byte swizzle, a ring of K and V tiles), one lane
-// issues products, a warpgroup per row tile does the softmax.  Every row tile has two S
-// buffers: the scores of the block after next are formed while a softmax runs, so that
-// none waits for products of its own.  The products of a buffer are issued in the order
-// S, P V, next S by one thread, which is the order they execute in.
+// Roles: one warp copies (TMA, 128-byte swizzle, a ring of K and V tiles), one lane a row
+// tile issues its products, a warpgroup a row tile does its softmax.  Every row tile has
+// two S buffers: the scores of the block after next are formed while a softmax runs, so
+// that none waits for products of its own.  The products of a buffer are issued in the
+// order S, P V, next S by one thread, which is the order they execute in.
 //
-// O is scaled down only where a row's maximum passes its reference by 2^6 (bf16: 2^24): after the
-// first blocks that hardly happens, and no work on O lies between the products.
+// What bounds it: the tensor cores, whose pipe is 82 % busy at 8192 tokens x 4 of 32 heads
+// over 8, causal: 1516 us, 1.45 PFLOP/s of the products that are needed (a library product
+// of large matrices: 1.89); without the causal mask, whose blocks on the diagonal are half
+// idle, 1.63.  With two row tiles a CTA one softmax runs beside the other's
+// products: 1549 us with two S buffers a tile, 2520 with one and an issuing lane for both.
+// A short prompt is bound by what a CTA does before its first product and after its last,
+// some 8000 cycles, and by its longest row tile: one prompt of 2048 tokens 35 us, 1.9 times
+// the products' time.  (Two CTAs an SM with a row tile each, whose starts and ends overlap:
+// the same 35 us, 72 instead of 62 for a ragged batch with biased scores, 1445 instead of
+// 1420 for 8192 x 4; 128 registers a thread are too few.)  Capped or biased scores: by the
+// softmax, 4096 x 2 tokens 296 and 301 us for 204.
+//
+// O is scaled down only where a row's maximum passes its reference by 2^6 (bf16: 2^24):
+// after the first blocks that hardly happens, and no work on O lies between the products.
 // Weights carry a factor 2^8, which cancels: fp16 ones stay normal down to 2^-22 of
 // the largest, and below 2^14.  The rounding of the weights to 16 bits is half a step
 // of the output's own type; their sum is of the unrounded ones.
@@ -62,7 +74,11 @@ struct AT {
   static constexpr int QTILE = 128 * D * 2;
   static constexpr int TILE = NB * D * 2;                  // bytes of a K or V tile
   static constexpr int RAW = NB * D;
-  static constexpr int STAGES = E4 ? (D == 64 ? 8 : D == 128 ? 6 : 3) * (D < 256 ? 64 : NB) / NB : D == 256 ? 5 : D == 128 ? (TILES == 2 ? 10 : 6) : TILES == 2 ? 12 : 8;
+  // tiles of the ring: what shared memory holds
+  static constexpr int STAGES = E4 ? (D == 64 ? 8 : D == 128 ? 6 : 3) * (D < 256 ? 64 : NB) / NB
+                                : D == 256 ? 5
+                                : D == 128 ? (TILES == 2 ? 10 : 6)
+                                           : (TILES == 2 ? 12 : 8);
   static constexpr int RAWS = E4 ? (D == 256 ? 3 : FEW ? 5 : 8) : 1;
   // columns of a block that a softmax warp takes, and rows of a row tile that are not copies
   static constexpr int COLS = NB / COPIES, ROWS = 128 / COPIES;
@@ -85,34 +101,24 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
-__device__ __forceinline__ float rcp_fast(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
-// tanh(x), |x| given times 2 log2(e): within 2^-22 of it.
-__device__ __forceinline__ float tanh_of(float x2) {
-  const float t = fmaf(-2.f, rcp_fast(ex2(fabsf(x2)) + 1.f), 1.f);
-  return copysignf(t, x2);
-}
-// cap2 tanh(a x), |a x| <= 1: x times the polynomial in x^2 of degree 6 with the smallest
-// largest relative error there (5e-8, found by exchange), the factors in its coefficients;
-// within 3 u of it, without the two slow functions of the other form (16K tokens in
-// documents with capped scores: 840 us with that form alone, 689 with this).
+// cap2 tanh(a x): x times a polynomial in x^2 with the smallest largest relative error
+// (found by exchange), the factors in its coefficients: of degree 4 for |a x| <= 1/2
+// (3e-8), of 6 up to 1 (7e-8), both within 3 u of it with their roundings, and without the
+// two slow functions of the other form.  16K tokens in documents, capped at 50: 840 us with
+// that form alone, 647 with degree 6, 551 with both.
+template <int N>
 struct SmallTanh {
-  float2 c[7];
-  __device__ __forceinline__ SmallTanh(float a, float cap2) {
-    const float of[7] = {0.9999999403953552f, -0.33332839608192444f, 0.13325203955173492f, -0.05345702916383743f,
-                         0.020289979875087738f, -0.006203379016369581f, 0.0010410225950181484f};
+  float c[N];
+  __device__ __forceinline__ SmallTanh(const float (&of)[N], float a, float cap2) {
     float f = a * cap2;
 #pragma unroll
-    for (int i = 0; i < 7; ++i, f *= a * a) c[i] = twice(of[i] * f);
+    for (int i = 0; i < N; ++i, f *= a * a) c[i] = of[i] * f;
   }
   __device__ __forceinline__ float2 operator()(float2 x) const {
     const float2 u = mul2(x, x);
-    float2 y = fma2(u, c[6], c[5]);
+    float2 y = fma2(u, twice(c[N - 1]), twice(c[N - 2]));
 #pragma unroll
-    for (int i = 4; i >= 0; --i) y = fma2(u, y, c[i]);
+    for (int i = N - 3; i >= 0; --i) y = fma2(u, y, twice(c[i]));
     return mul2(x, y);
   }
 };
@@ -357,7 +363,6 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
     mbar_init_fence();
   }
   griddep_wait();
-  griddep_launch();
 
   // this CTA's part: row tiles [tile0, tile0 + TILES) of (b, h), the part-th share of their keys
   // (in bundles of (sequence, KV head) pairs, whose keys several CTAs then read at the same
@@ -384,10 +389,10 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
   const int t1 = min(m, t0 + TILES * TT);                // tokens of this CTA: [t0, t1)
   const int prefix = p.prefix ? p.prefix[b] : 0;
   // keys that a token at place `at` sees, as a range
-  auto first_key = [&](int at) { return p.window ? max(0, at - p.window + 1) : 0; };
+  auto first_key = [&](int at) { return p.window ? (int)max((int64_t)0, (int64_t)at - p.window + 1) : 0; };
   auto end_key = [&](int at) {
     if (p.causal) return min(L, max(at + 1, prefix));
-    return p.window ? min(L, at + p.window) : L;
+    return p.window ? (int)min((int64_t)L, (int64_t)at + p.window) : L;
   };
   int lo = 0, hi = 0;
   if (t0 < t1) {
@@ -427,6 +432,9 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // only now: a kernel behind this one may take tensor memory before it waits for this one,
+  // which all of this grid has by then
+  griddep_launch();
   const uint32_t tmem = __shfl_sync(~0u, sh.tmem, 0);
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     const bool ok = __all_sync(~0u, wait_here(bar, parity));
@@ -457,8 +465,13 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
       int n = 0, slot = 0;
       uint32_t turn = 0;
       bool ok = true;
-      int units_from = -1, entry = 0, step = 0;    // pages: this lane's unit of the 32 from `units_from` on
-      uint32_t gone = 0;                 // bits of those whose page is not in the cache
+      // pages: this lane's unit of the 32 from `from` on, and bits of those whose page is not
+      // in the cache; apart for keys and values, which are two blocks behind
+      struct Units {
+        int from = -1, entry = 0;
+        uint32_t gone = 0;
+      } key_units, value_units;
+      int step = 0;
       const int per = NB / unit;
       auto load = [&](const CUtensorMap& map, int j, bool keys) {
         if (!ok) return;
@@ -466,10 +479,11 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
         const uint32_t at = at0 + slot * BYTES;
         if constexpr (PAGED) {
           const int u0 = j * per;
-          if (units_from < 0 || u0 < units_from || u0 >= units_from + 32) {
-            units_from = u0;
+          Units& units = keys ? key_units : value_units;
+          if (units.from < 0 || u0 >= units.from + 32) {
+            units.from = u0;
             const int t = (u0 + lane) * unit;
-            entry = p.n_pages * p.H * p.page_size;     // behind the pool: zeros
+            int entry = p.n_pages * p.H * p.page_size;     // behind the pool: zeros
             bool bad = false;
             if (t < L) {
               const int pg = t / p.page_size;
@@ -477,9 +491,10 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
               bad = page < 0 || page >= p.n_pages;
               if (!bad) entry = (page * p.H + h) * p.page_size + (t - pg * p.page_size);
             }
-            gone = __ballot_sync(~0u, bad);
+            units.entry = entry;
+            units.gone = __ballot_sync(~0u, bad);
           }
-          const uint32_t lost = (gone >> (u0 - units_from)) & ((1u << per) - 1);
+          const uint32_t lost = (units.gone >> (u0 - units.from)) & ((1u << per) - 1);
           if (lane == 0) {
             if (lost && p.status) atomicOr(p.status, DEV_ERR_CHECK);
             // read by the softmax behind this block's scores, so behind this copy's arrival
@@ -489,7 +504,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
           if (keys) ++step;
           constexpr int W = E4 ? 1 : G;
           const int u = lane / W, c = lane - u * W;
-          const int row = __shfl_sync(~0u, entry, (u0 - units_from + u) & 31);
+          const int row = __shfl_sync(~0u, units.entry, (u0 - units.from + u) & 31);
           __syncwarp();
           if (u < per) tma_load_2d(at + c * NB * 128 + u * unit * (E4 ? D : 128), &map, c * 64, row, &full[slot]);
         } else {
@@ -642,7 +657,8 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
     {
       const float cap2 = p.cap * 1.4426950408889634f;
       const float into = CAP ? sc / cap2 : 0.f;       // products to the tanh's argument
-      const SmallTanh small(into, cap2);
+      const SmallTanh<5> small({1.f, -0.3333306908607483f, 0.13324779272079468f, -0.05298607423901558f, 0.017135007306933403f},
+                               into, cap2);
       const float by = MODS ? 1.f : sc;
       float top = -CUDART_INF_F, mref = 1e38f, l = 0.f;
       constexpr int COLS = C::COLS, W = COLS < 32 ? COLS : 32;   // columns at a time
@@ -715,15 +731,25 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
               float big = 0.f;
 #pragma unroll
               for (int c = 0; c < COLS; c += 2) big = max3(big, fabsf(v[c]), fabsf(v[c + 1]));
-              if (__any_sync(~0u, !(big * into <= 1.f))) {
-#pragma unroll
-                for (int c = 0; c < COLS; ++c) v[c] = cap2 * tanh_of(v[c] * into * 2.885390081777927f);
-              } else {
+              if (__all_sync(~0u, big * into <= 0.5f)) {
 #pragma unroll
                 for (int c = 0; c < COLS; c += 2) {
                   const float2 y = small(make_float2(v[c], v[c + 1]));
                   v[c] = y.x, v[c + 1] = y.y;
                 }
+              } else if (__all_sync(~0u, big * into <= 1.f)) {
+                const SmallTanh<7> medium({0.9999999403953552f, -0.33332839608192444f, 0.13325203955173492f,
+                                           -0.05345702916383743f, 0.020289979875087738f, -0.006203379016369581f,
+                                           0.0010410225950181484f},
+                                          into, cap2);
+#pragma unroll
+                for (int c = 0; c < COLS; c += 2) {
+                  const float2 y = medium(make_float2(v[c], v[c + 1]));
+                  v[c] = y.x, v[c + 1] = y.y;
+                }
+              } else {
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) v[c] = cap2 * tanh_log2(v[c] * into * 2.885390081777927f);
               }
             } else if (j0 + COLS <= nearest + 1 && !(p.tree && j0 + COLS > base)) {
               // all keys before all rows: the distance is linear

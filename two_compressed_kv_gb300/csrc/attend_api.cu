@@ -54,12 +54,13 @@ const char* norm_sizes(const mkv_rope_plan* plan, const mkv_norm_rope_args* a, b
   return nullptr;
 }
 
-// Blocks of both sides: at most so many per SM.  A gradient's are those that run at
-// once, as its sums of a block go through memory (84 us with 2, 94 with 4).
-constexpr int norm_blocks(bool grad) { return grad ? 2 : 4; }
+// Blocks of both sides an SM: those that run at once.  8192 x 4 bf16 tokens of 16 + 16 heads
+// of 128: 94.5 us with 2, 112 with 3, 101 with 4 (32 + 8: 128, 149, 128); a gradient's sums
+// of a block go through memory (84 us with 2, 94 with 4).
+constexpr int kNormBlocks = 2;
 
 // Heads a group of lanes takes, a side's items and blocks.
-void norm_grid(const mkv_norm_rope_args* a, bool grad, int sms, NormRopeParams* p) {
+void norm_grid(const mkv_norm_rope_args* a, int sms, NormRopeParams* p) {
   const int64_t rows = (int64_t)a->batch * a->tokens;
   const int per_block = 256 / p->lanes;
   const int heads[2] = {a->heads[0], a->heads[1]};
@@ -71,7 +72,7 @@ void norm_grid(const mkv_norm_rope_args* a, bool grad, int sms, NormRopeParams* 
     need[s] = up(p->items[s], per_block);
     all += need[s];
   }
-  const int64_t most = (int64_t)sms * norm_blocks(grad);
+  const int64_t most = (int64_t)sms * kNormBlocks;
   for (int s = 0; s < 2; ++s) {
     const int64_t share = heads[s] * most / (heads[0] + heads[1]);
     p->blocks[s] = (int)(all <= most ? need[s] : std::min(need[s], std::max<int64_t>(share, 1)));
@@ -80,7 +81,7 @@ void norm_grid(const mkv_norm_rope_args* a, bool grad, int sms, NormRopeParams* 
 
 // A block more than the share of each side, at most.
 uint64_t norm_workspace(const mkv_rope_plan* plan, int sms) {
-  return (uint64_t)(sms * norm_blocks(true) + 2) * plan->head_dim * 4;
+  return (uint64_t)(sms * kNormBlocks + 2) * plan->head_dim * 4;
 }
 
 mkv_status norm_call(const mkv_rope_plan* plan, const mkv_rope_axes* axes, const mkv_norm_rope_args* a, bool grad,
@@ -138,7 +139,7 @@ mkv_status norm_call(const mkv_rope_plan* plan, const mkv_rope_axes* axes, const
   p.offset = a->weight_offset;
   int sms = 0;
   if (mkv_status s = sm_count(&sms)) return s;
-  norm_grid(a, grad, sms, &p);
+  norm_grid(a, sms, &p);
   if (wants) {
     if (!a->workspace || !aligned16(a->workspace)) return bad("mkv_norm_rope_grad: workspace must be 16-byte aligned");
     if (a->workspace_bytes < norm_workspace(plan, sms)) return bad("mkv_norm_rope_grad: workspace too small");
@@ -200,15 +201,19 @@ bool strides_ok(const int64_t* s, int64_t e0, int64_t e1, int64_t e2) {
   return true;
 }
 
-// How a call's rows and keys are spread, and where its workspace's parts lie.
+// How a call's rows and keys are spread, and where its workspace's parts lie.  Few rows are
+// held in copies, see the kernel.
 struct AttendLayout {
   int copies;
   int tiles, tile_tokens, groups, splits;
   uint64_t docs, part_o, part_ml, total;   // byte offsets
 };
 
-// What a CTA costs apart from its blocks of keys, in blocks, and what a join costs.
+// What a CTA costs apart from its blocks of keys, in blocks, and what a join costs: a new
+// token over 32 streams of 32768 slots takes 87 us with these, 97 with 4 and 3.  Parts of
+// outputs that a join reads, in the time of a block (some 0.7 us).
 constexpr int kCtaBlocks = 8, kJoinBlocks = 4;
+constexpr int64_t kJoinBytes = 4 << 20;
 
 // Row tiles: 128 / g tokens each.  Two to a CTA where there are two (each softmax then
 // has its own S buffer and K and V are read half as often), but not with heads of 256
@@ -227,9 +232,10 @@ AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, i
   const int64_t blocks = up(keys, NB);
   l.splits = 1;
   // a few rows over many keys: parts of the keys, joined by a second kernel
+  const int64_t part_bytes = (int64_t)B * H * g * nq * D * 8;      // written and read
   int64_t best = up(items, sms) * (blocks + kCtaBlocks);
   for (int s = 2; s <= 64 && s <= blocks && items * s <= 16 * (int64_t)sms; ++s) {
-    const int64_t cost = up(items * s, sms) * (up(blocks, s) + kCtaBlocks) + kJoinBlocks;
+    const int64_t cost = up(items * s, sms) * (up(blocks, s) + kCtaBlocks) + kJoinBlocks + s * part_bytes / kJoinBytes;
     if (cost < best) best = cost, l.splits = s;
   }
   uint64_t at = 0;
@@ -332,6 +338,7 @@ mkv_status mkv_prefill(const mkv_prefill_args* a, mkv_stream_t stream) {
   if (!a->q || !a->out || (a->kv_tokens && (!a->k || !a->v))) return bad("mkv_prefill: NULL q, k, v or out");
   if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->out))
     return bad("mkv_prefill: q, k, v and out must be 16-byte aligned");
+  if (a->out == a->q || a->out == a->k || a->out == a->v) return bad("mkv_prefill: out must not be an input");
   if (!strides_ok(a->q_stride, a->batch, a->q_tokens, a->n_q_heads) ||
       !strides_ok(a->out_stride, a->batch, a->q_tokens, a->n_q_heads) ||
       !strides_ok(a->k_stride, a->batch, a->kv_tokens, a->n_kv_heads) ||
@@ -393,6 +400,7 @@ mkv_status mkv_paged_attend(const mkv_paged_cache* c, const mkv_paged_attend_arg
   if (a->n == 0) return MKV_OK;
   if (!a->q || !a->out || !a->seq_lens) return bad("mkv_paged_attend: NULL q, out or seq_lens");
   if (!aligned16(a->q) || !aligned16(a->out)) return bad("mkv_paged_attend: q and out must be 16-byte aligned");
+  if (a->out == a->q) return bad("mkv_paged_attend: out must not be q");
   if (!strides_ok(a->q_stride, c->batch, a->n, a->n_q_heads))
     return bad("mkv_paged_attend: q's strides must be positive multiples of 8 elements");
   if (paged_attend_streams(c, a)) return paged_attend_streaming(c, a, stream);

@@ -759,6 +759,7 @@ def mkv_prefill(q, k, v, out=None, lse=None, causal=True, window=0, prefix=None,
     the query's document): which keys a query sees.  cap: scores become cap * tanh(score / cap);
     slopes (fp32 [q_heads]): slope * distance is taken off.  lse: fp32 [batch, tokens, q_heads] or
     None.  status: int32 [1] or None: set where a bounded wait gave up (outputs undefined then).
+    workspace: a uint8 tensor of mkv_prefill_workspace bytes (None: taken from torch's allocator).
     Returns out (new where None), of q's shape and type; rows behind q_lens are left as they were."""
     m = _native()
     if out is None and isinstance(q, _T.Tensor):
@@ -766,6 +767,21 @@ def mkv_prefill(q, k, v, out=None, lse=None, causal=True, window=0, prefix=None,
     _check(m.prefill(q, k, v, out, lse, q_lens, kv_lens, prefix, docs, slopes, causal, window, scale, cap, workspace,
                      _address(stream), status), "mkv_prefill")
     return out
+
+
+def mkv_prefill_workspace(batch, q_tokens, kv_tokens, q_heads, kv_heads, head_dim, window=0, docs=False,
+                          device=None) -> int:
+    """Bytes of workspace of mkv_prefill for these sizes on `device` (None: the current one); 0: it
+    needs none."""
+    _native()
+    a = mkv_prefill_args(batch=batch, q_tokens=q_tokens, kv_tokens=kv_tokens, n_q_heads=q_heads,
+                         n_kv_heads=kv_heads, head_dim=head_dim, dtype=MKV_DT_F16, window=window,
+                         docs=1 if docs else None)
+    with _T.cuda.device(device):
+        n = _lib.mkv_prefill_workspace(ctypes.byref(a))
+    if n == 2**64 - 1:
+        raise MkvError(MKV_ERR_INVALID_ARG, "mkv_prefill_workspace")
+    return n
 
 
 def mkv_paged_attend(cache, q, seq_lens, tree=None, new_lens=None, out=None, lse=None, max_len=0, window=0,
