@@ -247,18 +247,23 @@ __device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity) {
 }
 
 // The blocks of keys that a CTA walks over, the same in every role (a warp asks as a
-// whole): all of a range, or those in which some document of its queries occurs.
+// whole): all of a range, or those in which some document of its queries occurs.  DOWN: the
+// last first, for scores biased by distance, which are largest there: the exponents'
+// reference is near its final value from the start and outputs are rarely scaled (4096 x 2
+// tokens 243 us, 302 upwards; without a bias, heads of 256 take 239, 219 upwards: CTAs that
+// start together then read the same keys).
+template <bool DOWN>
 struct Blocks {
-  int j, end, base;
-  uint32_t bits;         // of the 32 blocks from base on: taken;
+  int j, end, base;      // left are [j, end)
+  uint32_t bits;         // of the 32 blocks from base on (which may be below 0): taken;
   uint32_t lone;         // of one document alone, `doc`
   int doc;
   const int2* range;     // of the sequence's blocks; NULL: all
   int2 own;              // of the queries' documents
   __device__ __forceinline__ uint32_t hits(int from, uint32_t& one) const {
-    const int i = from + (threadIdx.x & 31);
+    const int i = from + (int)(threadIdx.x & 31);
     bool hit = false, same = false;
-    if (i < end) {
+    if (i >= j && i < end) {
       const int2 r = range[i];
       hit = r.x <= own.y && r.y >= own.x;
       same = r.x == doc && r.y == doc;
@@ -268,7 +273,7 @@ struct Blocks {
   }
   // block i, the last that next() gave, has nothing but `doc`
   __device__ __forceinline__ bool plain(int i) const { return lone >> (i - base) & 1; }
-  // (how many, the last)
+  // before the walk: (how many, the highest)
   __device__ __forceinline__ int2 all() const {
     if (!range) return make_int2(max(0, end - j), end - 1);
     int2 r = make_int2(0, -1);
@@ -281,18 +286,20 @@ struct Blocks {
     return r;
   }
   __device__ __forceinline__ int next() {
-    if (!range) return j < end ? j++ : -1;
+    if (!range) return j < end ? DOWN ? --end : j++ : -1;
     while (j < end) {
-      if (j >= base + 32) {
-        base = j;
+      if (DOWN ? end <= base : j >= base + 32) {
+        base = DOWN ? end - 32 : j;
         bits = hits(base, lone);
       }
-      const uint32_t rest = bits >> (j - base);
+      const uint32_t rest = DOWN ? bits & (~0u >> (32 - (end - base))) : bits >> (j - base);
       if (rest) {
+        if (DOWN) return end = base + 31 - __clz(rest);
         j += __ffs(rest);
         return j - 1;
       }
-      j = base + 32;
+      if (DOWN) end = base;
+      else j = base + 32;
     }
     return -1;
   }
@@ -401,7 +408,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
     if (p.tree) lo = first_key(base), hi = L;
   }
   const int32_t* docs = p.docs ? p.docs + b * p.docs_stride : nullptr;
-  Blocks blocks;
+  Blocks<SLOPES> blocks;
   blocks.range = nullptr;
   blocks.doc = 0;
   {
@@ -412,7 +419,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
       blocks.j = from + (uint32_t)n * part / (uint32_t)p.splits;
       blocks.end = from + (uint32_t)n * (part + 1) / (uint32_t)p.splits;
     }
-    blocks.base = blocks.j - 32;
+    blocks.base = SLOPES ? blocks.end : blocks.j - 32;
   }
   if (docs && hi > lo) {
     int2 own = make_int2(INT32_MAX, INT32_MIN);
@@ -465,10 +472,10 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
       int n = 0, slot = 0;
       uint32_t turn = 0;
       bool ok = true;
-      // pages: this lane's unit of the 32 from `from` on, and bits of those whose page is not
+      // pages: this lane's unit of the 32 from `from` (which may be below 0) on, and bits of those whose page is not
       // in the cache; apart for keys and values, which are two blocks behind
       struct Units {
-        int from = -1, entry = 0;
+        int from = SLOPES ? INT32_MAX : INT32_MIN, entry = 0;
         uint32_t gone = 0;
       } key_units, value_units;
       int step = 0;
@@ -480,12 +487,12 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
         if constexpr (PAGED) {
           const int u0 = j * per;
           Units& units = keys ? key_units : value_units;
-          if (units.from < 0 || u0 >= units.from + 32) {
-            units.from = u0;
-            const int t = (u0 + lane) * unit;
+          if (SLOPES ? u0 < units.from : u0 - 32 >= units.from) {
+            units.from = SLOPES ? u0 + per - 32 : u0;
+            const int t = (units.from + lane) * unit;
             int entry = p.n_pages * p.H * p.page_size;     // behind the pool: zeros
             bool bad = false;
-            if (t < L) {
+            if (t >= 0 && t < L) {
               const int pg = t / p.page_size;
               const int page = p.table[b * p.table_stride + pg];
               bad = page < 0 || page >= p.n_pages;
@@ -576,10 +583,10 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
       };
       // What lies behind the sequence in its last block may be anything, and 0 times a
       // NaN is one: those rows of V become zeros (8-bit pages: where they are widened).
-      // It is the ring's last tile; of two warps both write the zeros they need.
+      // It is the last tile of V (DOWN: the first); of two warps both write the zeros they need.
       auto clean = [&](int j) {
-        const int s = (2 * n - 1) % C::STAGES;
-        wait_here(&sh.full[s], ((2 * n - 1) / C::STAGES) & 1);
+        const int at_n = SLOPES ? min(n, 2) : 2 * n - 1, s = at_n % C::STAGES;
+        wait_here(&sh.full[s], (at_n / C::STAGES) & 1);
         uint8_t* at = smem_p + TILES * C::QTILE + s * C::TILE;
         const int r0 = L - j * NB;
         for (int i = lane; i < (NB - r0) * 8; i += 32) {
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
         ok = wait_here(&sh.q_full, 0);
         scores(0);
         if (n > 1) scores(1);
-        for (int k = 0; k + 1 < n && ok; ++k) {
+        for (int k = 0; !SLOPES && k + 1 < n && ok; ++k) {
           values(k);
           if (k + 2 < n) scores(k + 2);
         }
@@ -602,7 +609,10 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
       if (!E4 && n > 0 && (all.y + 1) * NB > L) clean(all.y);
       __syncwarp();
       if (leader && n > 0) {
-        values(n - 1);
+        for (int k = SLOPES ? 0 : n - 1; k < n && ok; ++k) {
+          values(k);
+          if (SLOPES && k + 2 < n) scores(k + 2);
+        }
         tc_commit(&sh.o_last[tile]);
         if (!ok && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
         // no product may be in flight when the tensor memory goes
