@@ -31,7 +31,7 @@
 // the products' time.  (Two CTAs an SM with a row tile each, whose starts and ends overlap:
 // the same 35 us, 72 instead of 62 for a ragged batch with biased scores, 1445 instead of
 // 1420 for 8192 x 4; 128 registers a thread are too few.)  Capped or biased scores: by the
-// softmax, 4096 x 2 tokens 296 and 301 us for 204.
+// softmax, 4096 x 2 tokens 293 and 243 us for 204.
 //
 // O is scaled down only where a row's maximum passes its reference by 2^6 (bf16: 2^24):
 // after the first blocks that hardly happens, and no work on O lies between the products.
