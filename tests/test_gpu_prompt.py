@@ -698,3 +698,44 @@ def test_workspaces_of_the_caller(M):
     assert M.mkv_prefill_workspace(2, 4096, 4096, 16, 16, 128) == 0   # many rows: no parts
     with pytest.raises(M.MkvError):
         M.mkv_prefill_workspace(1, 3, 5000, 8, 3, 64)
+
+
+def test_offsets_past_32_bits(M):
+    """Two keys stand out of 2^25 and more whose rows take 2^32 elements, in a tensor and in pages:
+    the output is the mean of their values, up to the roundings of weights (bf16: half a step, 2^-9
+    with the two weights' ratio, 2^-9 with the output) and e^-30 times the others' number."""
+    n, d, page = 2**25 + 64 * 9, 128, 64
+    k = torch.zeros((1, n, 1, d), dtype=BF16, device=DEV)
+    v = torch.ones((1, n, 1, d), dtype=BF16, device=DEV)
+    q = torch.zeros((1, 1, 4, d), dtype=BF16, device=DEV)
+    q[..., 0] = 1.0
+    two = [77, n - 3]
+    for t in two:
+        k[0, t, 0, 0] = 30.0
+    v[0, two] = rnd((2, 1, d), BF16, 1, 4.0)
+    want = v[0, two].float().mean(0)
+    size = float(v[0, two].float().abs().max()) + 1.0
+    bound = size * (2.0**-8 + 2.0**-9 + n * float(np.exp(-30.0)) + 2.0**-16)
+    got = M.mkv_prefill(q, k, v, scale=1.0)
+    assert (got[0, 0].float() - want).abs().max() <= bound
+    table = torch.arange(n // page, dtype=torch.int32, device=DEV).view(1, -1)
+    cache = M.MkvPaged(k.view(n // page, 1, page, d), v.view(n // page, 1, page, d), table)
+    got = M.mkv_paged_attend(cache, q, i32([n]), scale=1.0)
+    assert (got[0, 0].float() - want).abs().max() <= bound and cache.check() == M.MKV_OK
+
+
+def test_many_sequences(M):
+    """As many sequences as a call takes: each sees its own one to three keys."""
+    b, d = 65535, 64
+    q, k, v = rnd((b, 1, 2, d), F16, 1), rnd((b, 3, 1, d), F16, 2), rnd((b, 3, 1, d), F16, 3)
+    lens = torch.arange(b, dtype=torch.int32, device=DEV) % 3 + 1
+    got = M.mkv_prefill(q, k, v, kv_lens=lens)
+    z = torch.einsum("bqhd,bkud->bhqk", q.double(), k.double()) / 8.0
+    z.masked_fill_(torch.arange(3, device=DEV).view(1, 1, 1, 3) >= lens.view(b, 1, 1, 1), -np.inf)
+    want = torch.einsum("bhqk,bkud->bqhd", torch.softmax(z, -1), v.double())
+    # scores of 64 products in fp32 (2^-18 of their size, here up to 2^6), weights and output half a step of fp16 each
+    bound = 2.0**-11 * (want.abs() + v.double().abs().amax((1, 2, 3), keepdim=True)) + 2.0**-11
+    assert ((got.double() - want).abs() <= bound).all()
+    w = rnd((d,), F32, 4)
+    y = M.mkv_norm_rope(M.mkv_rope_plan(d), q, w, first_pos=5)
+    assert torch.equal(y[-3:], M.mkv_norm_rope(M.mkv_rope_plan(d), q[-3:], w, first_pos=5))
