@@ -758,8 +758,9 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
                   v[c] = y.x, v[c + 1] = y.y;
                 }
               } else {
+                const CappedScore capped(cap2);
 #pragma unroll
-                for (int c = 0; c < COLS; ++c) v[c] = cap2 * tanh_log2(v[c] * into * 2.885390081777927f);
+                for (int c = 0; c < COLS; ++c) v[c] = capped(v[c] * sc);
               }
             } else if (j0 + COLS <= nearest + 1 && !(p.tree && j0 + COLS > base)) {
               // all keys before all rows: the distance is linear

@@ -525,22 +525,46 @@ __global__ void __launch_bounds__(NW * 32, PA<CT, D, WIDE, NW>::CTAS)
           }
         if constexpr (OPT) {
           const int t0 = (j0 + warp + NW * (i + u)) * PA_BLOCK;
+          uint32_t seen = 0;                      // bit 4 w + k
+          float big = 0.f;
+#pragma unroll
+          for (int w = 0; w < NH; ++w)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int t = t0 + tok_r + 8 * (k >> 1), x = k & 1;
+              const bool here = left[u] > 0 && (t < base ? t >= klo[w][x] : t - base < 16 && (sees[w][x] >> (t - base) & 1));
+              seen |= here ? 1u << (4 * w + k) : 0u;
+              if (p.cap2 > 0.f || p.slopes) s[u][w][k] *= sr[w][x];
+              if (here) big = fmaxf(big, fabsf(s[u][w][k]));
+            }
+          if (p.cap2 > 0.f) {
+            // the exponential only where a score needs it: the same results, in less time
+            const CappedScore capped(p.cap2);
+            if (__all_sync(~0u, big <= 0.5f * p.cap2)) {
+#pragma unroll
+              for (int w = 0; w < NH; ++w)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[u][w][k] = capped.small(s[u][w][k]);
+            } else {
+#pragma unroll
+              for (int w = 0; w < NH; ++w)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[u][w][k] = capped(s[u][w][k]);
+            }
+          }
 #pragma unroll
           for (int w = 0; w < NH; ++w)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int t = t0 + tok_r + 8 * (k >> 1), x = k & 1;
               float z = s[u][w][k];
-              if (p.cap2 > 0.f) z = p.cap2 * tanh_log2(z * sr[w][x] * (2.885390081777927f / p.cap2));
-              else if (p.slopes) z *= sr[w][x];
               if (p.slopes) {
                 int at = t;
                 if (p.tree && t >= base && t < n)
                   at = base + __popcll(p.tree[(int64_t)b * p.tokens + t - base] & ((1ull << (n - base)) - 1) & ~(1ull << (t - base)));
                 z -= slope[w][x] * fabsf((float)(place[w][x] - at));
               }
-              const bool seen = t < base ? t >= klo[w][x] : t - base < 16 && (sees[w][x] >> (t - base) & 1);
-              s[u][w][k] = seen && left[u] > 0 ? z : -CUDART_INF_F;
+              s[u][w][k] = seen >> (4 * w + k) & 1 ? z : -CUDART_INF_F;
             }
         } else if (left[u] < PA_BLOCK) {
 #pragma unroll

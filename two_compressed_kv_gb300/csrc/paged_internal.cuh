@@ -229,13 +229,28 @@ __device__ __forceinline__ void store_stat(const PagedAttnParams& p, int64_t row
   if (p.scores) *reinterpret_cast<float2*>(p.stat + row) = make_float2(top, lg);
 }
 
-// a tanh: x is 2 log2(e) times the argument; within 2^-22 of it
-__device__ __forceinline__ float tanh_log2(float x) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(fabsf(x)));
-  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(e + 1.f));
-  return copysignf(fmaf(-2.f, r, 1.f), x);
-}
+// cap tanh(z / cap) of a score in the log2 domain, cap2 its cap there.  Up to half the cap z
+// times a polynomial in (z / cap)^2 with the smallest largest relative error (found by
+// exchange): the error goes by z and not by the cap, however large that is.  Beyond it
+// 1 - 2 / (e + 1), whose error is one of the cap's last bits.  Within 2^-20 of the result.
+struct CappedScore {
+  float cap2, over;                // over: 1 / cap2, finite
+  __device__ __forceinline__ explicit CappedScore(float cap2_) : cap2(cap2_), over(fminf(1.f / cap2_, 3.402823466e38f)) {}
+  // |z| <= cap2 / 2
+  __device__ __forceinline__ float small(float z) const {
+    const float t = z * over, u = t * t;
+    float y = fmaf(u, 0.017135007306933403f, -0.05298607423901558f);
+    y = fmaf(u, y, 0.13324779272079468f);
+    y = fmaf(u, y, -0.3333306908607483f);
+    return z * fmaf(u, y, 1.f);
+  }
+  __device__ __forceinline__ float operator()(float z) const {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(fabsf(z * over) * 2.885390081777927f));
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(e + 1.f));
+    return fabsf(z) <= 0.5f * cap2 ? small(z) : cap2 * copysignf(fmaf(-2.f, r, 1.f), z);
+  }
+};
 
 // g <= 8 and g <= 16 variants per head dim (one translation unit each)
 cudaError_t launch_paged_attn_64(const PagedAttnParams& p, int cache_type, cudaStream_t st);
