@@ -1,5 +1,5 @@
-"""Scores of the attention of many queries where their forms meet: caps of any size, against
-the 64-bit oracle.
+"""Scores of the attention of many queries where their forms meet: caps of any size against
+the 64-bit oracle, and capped calls that repeat bit for bit.
 
 Tolerances, derived here once (u = 2^-24, e(t), scores, attend as in test_gpu_prompt.py):
 
@@ -72,3 +72,63 @@ def test_prompt_caps_of_any_size(M, dtype, d, cap):
     ref = O.attend(f64(q[0]), f64(k[0]).transpose(1, 0, 2), f64(v[0]).transpose(1, 0, 2), O.visible(n, n), np.arange(n),
                    np.arange(n), None, cap)
     capped_near(f64(out[0]), f64(lse[0]), ref, dtype, n)
+
+
+def prompt_call(M, d, heads, kv, cap, stray, slopes=None, dtype=BF16, nq=150, nk=333):
+    """A padded batch whose rows behind the lengths hold `stray`: (out, lse) of the rows that are there."""
+    q_lens, kv_lens = [150, 41, 7], [333, 300, 64]
+    q, k, v = rnd((3, nq, heads, d), dtype, 1), rnd((3, nk, kv, d), dtype, 2), rnd((3, nk, kv, d), dtype, 3)
+    for i in range(3):
+        q[i, q_lens[i]:] = stray
+        k[i, kv_lens[i]:] = stray
+        v[i, kv_lens[i]:] = stray
+    out, lse = torch.zeros_like(q), torch.zeros((3, nq, heads), device=DEV)
+    M.mkv_prefill(q, k, v, out=out, lse=lse, cap=cap, q_lens=i32(q_lens), kv_lens=i32(kv_lens),
+                  slopes=None if slopes is None else torch.tensor(slopes, dtype=torch.float32, device=DEV))
+    return out, lse
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("d,heads,kv", [(128, 7, 1), (128, 28, 4), (64, 3, 1), (256, 6, 2), (64, 40, 2)])
+def test_capped_prompts_do_not_depend_on_what_is_not_there(M, d, heads, kv, slopes):
+    """The same bits whatever lies behind the lengths, and whatever calls ran before: rows of a tile
+    that no query fills are what an earlier call left."""
+    slopes = [2.0**-(i % 8 + 1) for i in range(heads)] if slopes else None
+    want = prompt_call(M, d, heads, kv, 9.0, 0.0, slopes)
+    loud = [rnd((2, 500, 8, x), BF16, 5, 50.0) for x in (64, 128, 256)]
+    for stray in (0.0, 1e3, float("nan"), -1e30):
+        for x in loud:
+            M.mkv_prefill(x, x[:, :, :2], x[:, :, :2])
+        assert all(torch.equal(a, b) for a, b in zip(want, prompt_call(M, d, heads, kv, 9.0, stray, slopes)))
+
+
+@pytest.mark.parametrize("ctype,qtype", [(BF16, BF16), (E4M3, F16)])
+@pytest.mark.parametrize("m,g", [(1, 1), (5, 3), (9, 3), (4, 7), (20, 7)])
+def test_capped_pages_do_not_depend_on_what_is_not_there(M, ctype, qtype, m, g):
+    q = rnd((2, m, 2 * g, 128), qtype, 4)
+    lens, new = i32([300, 77]), i32([m, max(1, m // 2)])
+    loud = rnd((2, 500, 8, 128), qtype, 5, 50.0)
+    want = None
+    for stray in (0.0, 1.0, 400.0, -400.0):
+        cache = make_cache(M, ctype, 2, 2, 128, 32, 10, 3)
+        for b, n in enumerate((300, 77)):
+            for t in range(n, 320):
+                page = int(cache.page_table[b, t // 32])
+                cache.k_pages[page, :, t % 32] = stray
+                cache.v_pages[page, :, t % 32] = stray
+        x = q.clone()
+        x[1, max(1, m // 2):] = 10 * stray
+        M.mkv_prefill(loud, loud[:, :, :2], loud[:, :, :2])
+        out, lse = torch.zeros_like(x), torch.zeros((2, m, 2 * g), device=DEV)
+        M.mkv_paged_attend(cache, x, lens, new_lens=new, out=out, lse=lse, cap=9.0)
+        want = want or (out, lse)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_capped_prompts_repeat(M):
+    q, k, v = rnd((1, 3000, 28, 128), BF16, 1), rnd((1, 3000, 4, 128), BF16, 2), rnd((1, 3000, 4, 128), BF16, 3)
+    want = M.mkv_prefill(q, k, v, cap=50.0)
+    loud = rnd((2, 700, 14, 128), BF16, 5, 50.0)
+    for _ in range(5):
+        M.mkv_prefill(loud, loud[:, :, :2], loud[:, :, :2])
+        assert torch.equal(want, M.mkv_prefill(q, k, v, cap=50.0))

@@ -737,10 +737,23 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
           for (int c = 0; c < COLS; c += W) tmem_load<W>(s_at + c, v + c);
           tmem_ld_wait();
           if constexpr (MODS != 0) {
-            if constexpr (CAP) {
-              float big = 0.f;
+            uint32_t bits[(COLS + 31) / 32];           // of masked blocks: the columns that this row sees
+            if (masked) {
 #pragma unroll
-              for (int c = 0; c < COLS; c += 2) big = max3(big, fabsf(v[c]), fabsf(v[c + 1]));
+              for (int c0 = 0; c0 < COLS; c0 += 32) bits[c0 / 32] = seen(c0);
+            }
+            if constexpr (CAP) {
+              // only what is seen, and by rows that are there, decides on the form: the forms differ
+              // in their roundings, and the rest may be anything
+              float big = 0.f;
+              if (masked) {
+#pragma unroll
+                for (int c = 0; c < COLS; ++c)
+                  if (bits[c / 32] >> (c % 32) & 1) big = fmaxf(big, fabsf(v[c]));
+              } else if (live) {
+#pragma unroll
+                for (int c = 0; c < COLS; c += 2) big = max3(big, fabsf(v[c]), fabsf(v[c + 1]));
+              }
               if (__all_sync(~0u, big * into <= 0.5f)) {
 #pragma unroll
                 for (int c = 0; c < COLS; c += 2) {
@@ -789,12 +802,8 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
             }
             if (masked) {
 #pragma unroll
-              for (int c0 = 0; c0 < COLS; c0 += 32) {
-                const uint32_t bits = seen(c0);
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-                  if (!(bits >> i & 1)) v[c0 + i] = -CUDART_INF_F;
-              }
+              for (int c = 0; c < COLS; ++c)
+                if (!(bits[c / 32] >> (c % 32) & 1)) v[c] = -CUDART_INF_F;
             }
           }
           float x = fmaxf(v[0], v[1]), x1 = fmaxf(v[2], v[3]);
