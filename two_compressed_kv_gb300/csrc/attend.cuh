@@ -737,43 +737,83 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
           for (int c = 0; c < COLS; c += W) tmem_load<W>(s_at + c, v + c);
           tmem_ld_wait();
           if constexpr (MODS != 0) {
-            uint32_t bits[(COLS + 31) / 32];           // of masked blocks: the columns that this row sees
-            if (masked) {
-#pragma unroll
-              for (int c0 = 0; c0 < COLS; c0 += 32) bits[c0 / 32] = seen(c0);
-            }
             if constexpr (CAP) {
-              // only what is seen, and by rows that are there, decides on the form: the forms differ
-              // in their roundings, and the rest may be anything
-              float big = 0.f;
-              if (masked) {
+              float large[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int c = 0; c < COLS; ++c)
-                  if (bits[c / 32] >> (c % 32) & 1) big = fmaxf(big, fabsf(v[c]));
-              } else if (live) {
-#pragma unroll
-                for (int c = 0; c < COLS; c += 2) big = max3(big, fabsf(v[c]), fabsf(v[c + 1]));
-              }
+              for (int c = 0; c < COLS; c += 2) large[c / 2 % 4] = max3(large[c / 2 % 4], fabsf(v[c]), fabsf(v[c + 1]));
+              const float big = live ? fmaxf(max3(large[0], large[1], large[2]), large[3]) : 0.f;
+              // The form goes by the scores that rows which are there see: forms differ in their
+              // roundings, and the rest may be anything.  What the other forms need is hidden from
+              // the compiler until there: taken out of the loop over the blocks it costs this one
+              // its registers (4096 x 2 tokens: 316 us, 287).
               if (__all_sync(~0u, big * into <= 0.5f)) {
 #pragma unroll
-                for (int c = 0; c < COLS; c += 2) {
-                  const float2 y = small(make_float2(v[c], v[c + 1]));
-                  v[c] = y.x, v[c + 1] = y.y;
+                for (int i = 0; i < COLS; i += 2) {
+                  const float2 y = small(make_float2(v[i], v[i + 1]));
+                  v[i] = y.x, v[i + 1] = y.y;
                 }
+              } else if (masked) {
+                float a = into, top2 = cap2, by1 = sc;
+                asm volatile("" : "+f"(a), "+f"(top2), "+f"(by1));
+                // some score is larger, perhaps one that is not seen: W at a time
+#pragma unroll 1
+                for (int c0 = 0; c0 < COLS; c0 += W) {
+                  const uint32_t bits = seen(c0);
+                  float t[W];
+                  tmem_load<W>(s_at + c0, t);
+                  tmem_ld_wait();
+                  float most[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                  for (int i = 0; i < W; ++i)
+                    if (bits >> i & 1) most[i % 4] = fmaxf(most[i % 4], fabsf(t[i]));
+                  const float arg = fmaxf(max3(most[0], most[1], most[2]), most[3]) * a;
+                  if (__all_sync(~0u, arg <= 0.5f)) {
+#pragma unroll
+                    for (int i = 0; i < W; i += 2) {
+                      const float2 y = small(make_float2(t[i], t[i + 1]));
+                      t[i] = y.x, t[i + 1] = y.y;
+                    }
+                  } else {
+                    const CappedScore capped(top2);
+                    if (top2 <= 64.f) {
+                      const float to2 = fminf(a * 2.885390081777927f, 3.402823466e38f);
+#pragma unroll
+                      for (int i = 0; i < W; ++i) t[i] = capped.large(t[i] * to2);
+                    } else {
+#pragma unroll
+                      for (int i = 0; i < W; ++i) t[i] = capped(t[i] * by1);
+                    }
+                  }
+                  tmem_store<W>(s_at + c0, reinterpret_cast<const uint32_t*>(t));
+                }
+                tmem_st_wait();
+#pragma unroll
+                for (int c = 0; c < COLS; c += W) tmem_load<W>(s_at + c, v + c);
+                tmem_ld_wait();
               } else if (__all_sync(~0u, big * into <= 1.f)) {
+                float a = into, top2 = cap2;
+                asm volatile("" : "+f"(a), "+f"(top2));
                 const SmallTanh<7> medium({0.9999999403953552f, -0.33332839608192444f, 0.13325203955173492f,
                                            -0.05345702916383743f, 0.020289979875087738f, -0.006203379016369581f,
                                            0.0010410225950181484f},
-                                          into, cap2);
+                                          a, top2);
 #pragma unroll
-                for (int c = 0; c < COLS; c += 2) {
-                  const float2 y = medium(make_float2(v[c], v[c + 1]));
-                  v[c] = y.x, v[c + 1] = y.y;
+                for (int i = 0; i < COLS; i += 2) {
+                  const float2 y = medium(make_float2(v[i], v[i + 1]));
+                  v[i] = y.x, v[i + 1] = y.y;
                 }
               } else {
-                const CappedScore capped(cap2);
+                float a = into, top2 = cap2, by1 = sc;
+                asm volatile("" : "+f"(a), "+f"(top2), "+f"(by1));
+                const CappedScore capped(top2);
+                if (top2 <= 64.f) {      // an error of 2^-22 of so small a cap is less than the products'
+                  const float to2 = fminf(a * 2.885390081777927f, 3.402823466e38f);
 #pragma unroll
-                for (int c = 0; c < COLS; ++c) v[c] = capped(v[c] * sc);
+                  for (int i = 0; i < COLS; ++i) v[i] = capped.large(v[i] * to2);
+                } else {
+#pragma unroll
+                  for (int i = 0; i < COLS; ++i) v[i] = capped(v[i] * by1);
+                }
               }
             } else if (j0 + COLS <= nearest + 1 && !(p.tree && j0 + COLS > base)) {
               // all keys before all rows: the distance is linear
@@ -802,8 +842,12 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
             }
             if (masked) {
 #pragma unroll
-              for (int c = 0; c < COLS; ++c)
-                if (!(bits[c / 32] >> (c % 32) & 1)) v[c] = -CUDART_INF_F;
+              for (int c0 = 0; c0 < COLS; c0 += 32) {
+                const uint32_t bits = seen(c0);
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                  if (!(bits >> i & 1)) v[c0 + i] = -CUDART_INF_F;
+              }
             }
           }
           float x = fmaxf(v[0], v[1]), x1 = fmaxf(v[2], v[3]);

@@ -244,11 +244,15 @@ struct CappedScore {
     y = fmaf(u, y, -0.3333306908607483f);
     return z * fmaf(u, y, 1.f);
   }
-  __device__ __forceinline__ float operator()(float z) const {
+  // x: 2 log2(e) times z / cap
+  __device__ __forceinline__ float large(float x) const {
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(fabsf(z * over) * 2.885390081777927f));
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(fabsf(x)));
     asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(e + 1.f));
-    return fabsf(z) <= 0.5f * cap2 ? small(z) : cap2 * copysignf(fmaf(-2.f, r, 1.f), z);
+    return cap2 * copysignf(fmaf(-2.f, r, 1.f), x);
+  }
+  __device__ __forceinline__ float operator()(float z) const {
+    return fabsf(z) <= 0.5f * cap2 ? small(z) : large(z * over * 2.885390081777927f);
   }
 };
 
