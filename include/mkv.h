@@ -710,7 +710,8 @@ uint64_t mkv_norm_rope_grad_workspace(const mkv_rope_plan* plan, const mkv_norm_
 
 /* How scores are formed, here and in mkv_paged_attend, of a query at place p and
  * a key at place j of its sequence:
- *   z = scale q . k;  with cap: z = cap tanh(z / cap);  with slopes: z -= slope |p - j|. */
+ *   z = scale q . k;  with cap: z = cap tanh(z / cap);  with slopes: z -= slope |p - j|.
+ * scale and cap are at most 2^127. */
 typedef struct {
   const void* q;             /* device [batch][q_tokens][n_q_heads][head_dim] of `dtype`, 16-byte aligned */
   const void* k;             /* device [batch][kv_tokens][n_kv_heads][head_dim] */

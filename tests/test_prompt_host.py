@@ -299,3 +299,20 @@ def test_oracle_axes_reduce_to_one():
     axis, f, mult = O.axes_frequencies((2, 3, 1), "cyclic", False, 1000.0)
     want = P.rope(x, pos, *P.rope_frequencies(12, 1000.0))
     assert np.allclose(O.spin(x, np.stack([pos] * 3), axis, f, mult), want)
+
+
+@pytest.mark.parametrize("name", ["scale", "cap"])
+def test_factors_that_overflow_are_refused(M, name):
+    """Scores are formed in the log2 domain: a factor of 1.4427 has to fit. 2^127 does."""
+    for x in (1.8e38, 2.4e38, 3.4e38):
+        a = _prefill_args(M, **{name: x})
+        assert M.lib.mkv_prefill(ctypes.byref(a), None) == M.MKV_ERR_INVALID_ARG
+        assert name in M.mkv_last_error_string()
+        assert M.lib.mkv_prefill_workspace(ctypes.byref(a)) == 2**64 - 1
+        c, a = _cache(M), _attend_args(M, **{name: x})
+        assert M.lib.mkv_paged_attend(ctypes.byref(c), ctypes.byref(a), None) == M.MKV_ERR_INVALID_ARG
+        assert name in M.mkv_last_error_string()
+    a = _prefill_args(M, q=None, out=None, batch=0, **{name: 2.0**127})
+    assert M.lib.mkv_prefill(ctypes.byref(a), None) == M.MKV_OK
+    c, a = _cache(M), _attend_args(M, n=0, q=None, out=None, **{name: 2.0**127})
+    assert M.lib.mkv_paged_attend(ctypes.byref(c), ctypes.byref(a), None) == M.MKV_OK

@@ -10,6 +10,9 @@ namespace {
 
 constexpr int kMaxGroup = 128;
 
+// A scale or a cap of scores: 0 (a default), or a number that log2(e) times leaves finite.
+bool factor_ok(float x) { return x >= 0.f && x <= 0x1p127f; }
+
 // ---- norms -------------------------------------------------------------------
 
 // Checks the sizes of a norm call and fills the part of its parameters that no
@@ -166,8 +169,8 @@ const char* check_prefill(const mkv_prefill_args* a) {
     return "mkv_prefill: q_tokens and kv_tokens must be 0..2^30";
   if (a->causal < 0 || a->causal > 1) return "mkv_prefill: causal must be 0 or 1";
   if (a->window < 0) return "mkv_prefill: window must be >= 0";
-  if (!(a->scale >= 0.f) || std::isinf(a->scale)) return "mkv_prefill: scale must be >= 0 and finite";
-  if (!(a->cap >= 0.f) || std::isinf(a->cap)) return "mkv_prefill: cap must be >= 0 and finite";
+  if (!factor_ok(a->scale)) return "mkv_prefill: scale must be 0..2^127";
+  if (!factor_ok(a->cap)) return "mkv_prefill: cap must be 0..2^127";
   if (a->prefix && !a->causal) return "mkv_prefill: prefix goes with causal";
   if ((int64_t)a->batch * a->n_q_heads > kMaxGrid || (double)a->batch * a->n_q_heads * a->q_tokens > 1.0 * kMaxGrid)
     return "mkv_prefill: too many queries";
@@ -187,8 +190,8 @@ const char* check_attend(const mkv_paged_cache* c, const mkv_paged_attend_args* 
   if (a->max_len < 0 || a->max_len > (int64_t)c->max_pages * c->page_size)
     return "mkv_paged_attend: max_len must be 0..max_pages * page_size";
   if (a->window < 0) return "mkv_paged_attend: window must be >= 0";
-  if (!(a->scale >= 0.f) || std::isinf(a->scale)) return "mkv_paged_attend: scale must be >= 0 and finite";
-  if (!(a->cap >= 0.f) || std::isinf(a->cap)) return "mkv_paged_attend: cap must be >= 0 and finite";
+  if (!factor_ok(a->scale)) return "mkv_paged_attend: scale must be 0..2^127";
+  if (!factor_ok(a->cap)) return "mkv_paged_attend: cap must be 0..2^127";
   if ((double)c->batch * a->n_q_heads * a->n > 1.0 * kMaxGrid) return "mkv_paged_attend: too many queries";
   return nullptr;
 }
