@@ -74,6 +74,29 @@ def test_prompt_caps_of_any_size(M, dtype, d, cap):
     capped_near(f64(out[0]), f64(lse[0]), ref, dtype, n, cap)
 
 
+TINY = [1e-3, 1e-4, 1e-6, 1e-8, 1e-20, 1e-37, 2.0**-149]
+
+
+@pytest.mark.parametrize("cap", TINY)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_tiny_caps(M, dtype, cap):
+    """Queries of zeros, of which every score is 0, beside ones whose scores reach the cap."""
+    for d, heads, kv in ((128, 2, 1), (64, 5, 1), (256, 2, 1)):
+        n = 150
+        q, k, v = rnd((1, n, heads, d), dtype, 1), rnd((1, n, kv, d), dtype, 2), rnd((1, n, kv, d), dtype, 3)
+        q[:, :70] = 0.0
+        lse = torch.empty((1, n, heads), device=DEV)
+        out = M.mkv_prefill(q, k, v, lse=lse, cap=cap)
+        ref = O.attend(f64(q[0]), f64(k[0]).transpose(1, 0, 2), f64(v[0]).transpose(1, 0, 2), O.visible(n, n),
+                       np.arange(n), np.arange(n), None, cap)
+        capped_near(f64(out[0]), f64(lse[0]), ref, dtype, n, cap)
+    for ctype in (dtype, E4M3):
+        for m, g in ((2, 4), (12, 4)):
+            q = rnd((1, m, g, 128), dtype, 3)
+            q[:, :m // 2] = 0.0
+            pages_check(M, ctype, dtype, 300, m, g, 128, cap, q=q)
+
+
 def prompt_call(M, d, heads, kv, cap, stray, slopes=None, dtype=BF16, nq=150, nk=333):
     """A padded batch whose rows behind the lengths hold `stray`: (out, lse) of the rows that are there."""
     q_lens, kv_lens = [150, 41, 7], [333, 300, 64]

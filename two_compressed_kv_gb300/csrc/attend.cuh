@@ -109,8 +109,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 template <int N>
 struct SmallTanh {
   float c[N];
-  __device__ __forceinline__ SmallTanh(const float (&of)[N], float a, float cap2) {
-    float f = a * cap2;
+  // factor: a cap2
+  __device__ __forceinline__ SmallTanh(const float (&of)[N], float a, float factor) {
+    float f = factor;
 #pragma unroll
     for (int i = 0; i < N; ++i, f *= a * a) c[i] = of[i] * f;
   }
@@ -665,10 +666,15 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
       sc *= sh.q_scale[row] * (p.k_scale ? p.k_scale[h] : 1.f);
     }
     {
-      const float cap2 = p.cap * 1.4426950408889634f;
-      const float into = CAP ? sc / cap2 : 0.f;       // products to the tanh's argument
+      // products to the tanh's argument; for caps so small that the polynomials' factors would
+      // overflow infinite, which sends all scores to the exact form
+      float into = CAP ? sc / (p.cap * 1.4426950408889634f) : 0.f;
+      if constexpr (CAP) {
+        const float f = into * into * into;
+        if (!(sc * f * f * f * f <= 1e30f)) into = CUDART_INF_F;
+      }
       const SmallTanh<5> small({1.f, -0.3333306908607483f, 0.13324779272079468f, -0.05298607423901558f, 0.017135007306933403f},
-                               into, cap2);
+                               into, sc);
       const float by = MODS ? 1.f : sc;
       float top = -CUDART_INF_F, mref = 1e38f, l = 0.f;
       constexpr int COLS = C::COLS, W = COLS < 32 ? COLS : 32;   // columns at a time
@@ -752,13 +758,16 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
                   const float2 y = small(make_float2(v[i], v[i + 1]));
                   v[i] = y.x, v[i + 1] = y.y;
                 }
-              } else if (masked) {
-                float a = into, top2 = cap2, by1 = sc;
+              } else if (E4 || masked) {
+                float a = into, top2 = p.cap, by1 = sc;
                 asm volatile("" : "+f"(a), "+f"(top2), "+f"(by1));
-                // some score is larger, perhaps one that is not seen: W at a time
+                top2 *= 1.4426950408889634f;
+                // some score is larger, perhaps one that is not seen: W at a time.  8-bit pages' kernels,
+                // which have the fewest registers, know no other way (64 drafts over 4 streams of
+                // 65536 slots of 64: 271 us, 231).
 #pragma unroll 1
                 for (int c0 = 0; c0 < COLS; c0 += W) {
-                  const uint32_t bits = seen(c0);
+                  const uint32_t bits = masked ? seen(c0) : live ? ~0u : 0u;
                   float t[W];
                   tmem_load<W>(s_at + c0, t);
                   tmem_ld_wait();
@@ -776,7 +785,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
                   } else {
                     const CappedScore capped(top2);
                     if (top2 <= 64.f) {
-                      const float to2 = fminf(a * 2.885390081777927f, 3.402823466e38f);
+                      const float to2 = fminf(by1 / top2 * 2.885390081777927f, 3.402823466e38f);
 #pragma unroll
                       for (int i = 0; i < W; ++i) t[i] = capped.large(t[i] * to2);
                     } else {
@@ -791,23 +800,24 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
                 for (int c = 0; c < COLS; c += W) tmem_load<W>(s_at + c, v + c);
                 tmem_ld_wait();
               } else if (__all_sync(~0u, big * into <= 1.f)) {
-                float a = into, top2 = cap2;
-                asm volatile("" : "+f"(a), "+f"(top2));
+                float a = into, by1 = sc;
+                asm volatile("" : "+f"(a), "+f"(by1));
                 const SmallTanh<7> medium({0.9999999403953552f, -0.33332839608192444f, 0.13325203955173492f,
                                            -0.05345702916383743f, 0.020289979875087738f, -0.006203379016369581f,
                                            0.0010410225950181484f},
-                                          a, top2);
+                                          a, by1);
 #pragma unroll
                 for (int i = 0; i < COLS; i += 2) {
                   const float2 y = medium(make_float2(v[i], v[i + 1]));
                   v[i] = y.x, v[i + 1] = y.y;
                 }
               } else {
-                float a = into, top2 = cap2, by1 = sc;
-                asm volatile("" : "+f"(a), "+f"(top2), "+f"(by1));
+                float top2 = p.cap, by1 = sc;
+                asm volatile("" : "+f"(top2), "+f"(by1));
+                top2 *= 1.4426950408889634f;
                 const CappedScore capped(top2);
                 if (top2 <= 64.f) {      // an error of 2^-22 of so small a cap is less than the products'
-                  const float to2 = fminf(a * 2.885390081777927f, 3.402823466e38f);
+                  const float to2 = fminf(by1 / top2 * 2.885390081777927f, 3.402823466e38f);
 #pragma unroll
                   for (int i = 0; i < COLS; ++i) v[i] = capped.large(v[i] * to2);
                 } else {
