@@ -747,8 +747,8 @@ typedef struct {
 } mkv_prefill_args;
 
 /* Bytes of workspace of mkv_prefill with these arguments on the current device
- * (pointers are not looked at, except whether docs is NULL), or UINT64_MAX for
- * invalid ones.  0 is enough for most calls. */
+ * (pointers are not looked at, except whether docs and prefix are NULL), or UINT64_MAX
+ * for invalid ones.  0 is enough for most calls. */
 uint64_t mkv_prefill_workspace(const mkv_prefill_args* args);
 
 /* Attention of a prompt, or of a part of one over what came before it: softmax of

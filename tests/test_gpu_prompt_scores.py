@@ -155,3 +155,26 @@ def test_capped_prompts_repeat(M):
     for _ in range(5):
         M.mkv_prefill(loud, loud[:, :, :2], loud[:, :, :2])
         assert torch.equal(want, M.mkv_prefill(q, k, v, cap=50.0))
+
+
+def test_windows_both_ways_are_split_for_what_they_reach(M):
+    """Without the causal mask a window of w sees as many keys as one of 2 w with it, and with a
+    prefix any number: the parts of the keys, and the workspace, go by that."""
+    sizes = (1, 4, 1 << 17, 8, 2, 128)
+    both, one = (M.mkv_prefill_workspace(*sizes, window=w, causal=c, prefix=False)
+                 for w, c in ((4096, False), (8192, True)))
+    assert both == one != M.mkv_prefill_workspace(*sizes, window=4096, causal=True, prefix=False)
+    assert M.mkv_prefill_workspace(*sizes, window=4096, prefix=True) == M.mkv_prefill_workspace(*sizes)
+    assert M.mkv_prefill_workspace(*sizes, window=4096) == M.mkv_prefill_workspace(*sizes)
+    q, k, v = rnd((1, 4, 8, 128), BF16, 1), rnd((1, 30000, 2, 128), BF16, 2), rnd((1, 30000, 2, 128), BF16, 3)
+    for kw in (dict(window=4096, causal=False), dict(window=300, causal=False), dict(window=4096), dict(window=700, prefix=[9000])):
+        kw = dict(kw)
+        prefix = kw.pop("prefix", None)
+        room = torch.empty(M.mkv_prefill_workspace(1, 4, 30000, 8, 2, 128, window=kw["window"], causal=kw.get("causal", True),
+                                                   prefix=prefix is not None), dtype=torch.uint8, device=DEV)
+        lse = torch.empty((1, 4, 8), device=DEV)
+        out = M.mkv_prefill(q, k, v, lse=lse, prefix=None if prefix is None else i32(prefix), workspace=room, **kw)
+        see = O.visible(4, 30000, kw.get("causal", True), kw["window"], None if prefix is None else prefix[0])
+        ref = O.attend(f64(q[0]), f64(k[0]).transpose(1, 0, 2), f64(v[0]).transpose(1, 0, 2), see,
+                       np.arange(29996, 30000), np.arange(30000))
+        capped_near(f64(out[0]), f64(lse[0]), ref, BF16, 30000, 0.0)

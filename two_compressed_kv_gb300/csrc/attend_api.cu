@@ -221,7 +221,9 @@ constexpr int64_t kJoinBytes = 4 << 20;
 // Row tiles: 128 / g tokens each.  Two to a CTA where there are two (each softmax then
 // has its own S buffer and K and V are read half as often), but not with heads of 256
 // (tensor memory) or 8-bit pages (their second warpgroup widens).
-AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, int window, bool e4m3, bool docs, int sms) {
+// `reach`: how far from a query the keys that it sees may lie, both ways together; 0: anywhere.
+AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, int64_t reach, bool e4m3, bool docs,
+                           int sms) {
   AttendLayout l;
   l.copies = nq * g <= 32 ? 4 : nq * g <= 64 && e4m3 ? 2 : 1;
   l.tile_tokens = 128 / l.copies / g;
@@ -231,7 +233,7 @@ AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, i
   const int NB = attend_block(D, l.tiles, e4m3, l.copies > 1);
   const int64_t items = (int64_t)B * H * l.groups;
   int64_t keys = nk;
-  if (window) keys = std::min<int64_t>(nk, (int64_t)window + l.tiles * l.tile_tokens + NB);
+  if (reach) keys = std::min<int64_t>(nk, reach + l.tiles * l.tile_tokens + NB);
   const int64_t blocks = up(keys, NB);
   l.splits = 1;
   // a few rows over many keys: parts of the keys, joined by a second kernel
@@ -255,9 +257,11 @@ AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, i
   return l;
 }
 
+// A window reaches both ways without the causal mask, and a prefix past it.
 AttendLayout prefill_layout(const mkv_prefill_args* a, int sms) {
-  return attend_layout(a->batch, a->n_kv_heads, a->n_q_heads / a->n_kv_heads, a->head_dim, a->q_tokens, a->kv_tokens,
-                       a->window, false, a->docs != nullptr, sms);
+  const int64_t reach = a->prefix ? 0 : a->causal ? a->window : 2 * (int64_t)a->window;
+  return attend_layout(a->batch, a->n_kv_heads, a->n_q_heads / a->n_kv_heads, a->head_dim, a->q_tokens, a->kv_tokens, reach,
+                       false, a->docs != nullptr, sms);
 }
 
 int64_t attend_limit(const mkv_paged_cache* c, const mkv_paged_attend_args* a) {

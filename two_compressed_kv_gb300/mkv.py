@@ -770,18 +770,23 @@ def mkv_prefill(q, k, v, out=None, lse=None, causal=True, window=0, prefix=None,
 
 
 def mkv_prefill_workspace(batch, q_tokens, kv_tokens, q_heads, kv_heads, head_dim, window=0, docs=False,
-                          device=None) -> int:
+                          device=None, causal=None, prefix=None) -> int:
     """Bytes of workspace of mkv_prefill for these sizes on `device` (None: the current one); 0: it
-    needs none."""
+    needs none.  causal, prefix: whether the call has them; None: enough for either."""
     _native()
-    a = mkv_prefill_args(batch=batch, q_tokens=q_tokens, kv_tokens=kv_tokens, n_q_heads=q_heads,
-                         n_kv_heads=kv_heads, head_dim=head_dim, dtype=MKV_DT_F16, window=window,
-                         docs=1 if docs else None)
-    with _T.cuda.device(device):
-        n = _lib.mkv_prefill_workspace(ctypes.byref(a))
-    if n == 2**64 - 1:
-        raise MkvError(MKV_ERR_INVALID_ARG, "mkv_prefill_workspace")
-    return n
+    most = 0
+    for c, p in [(1, 0), (1, 1), (0, 0)]:
+        if c != (c if causal is None else bool(causal)) or p != (p if prefix is None else bool(prefix)):
+            continue
+        a = mkv_prefill_args(batch=batch, q_tokens=q_tokens, kv_tokens=kv_tokens, n_q_heads=q_heads,
+                             n_kv_heads=kv_heads, head_dim=head_dim, dtype=MKV_DT_F16, window=window,
+                             docs=1 if docs else None, causal=c, prefix=p or None)
+        with _T.cuda.device(device):
+            n = _lib.mkv_prefill_workspace(ctypes.byref(a))
+        if n == 2**64 - 1:
+            raise MkvError(MKV_ERR_INVALID_ARG, "mkv_prefill_workspace")
+        most = max(most, n)
+    return most
 
 
 def mkv_paged_attend(cache, q, seq_lens, tree=None, new_lens=None, out=None, lse=None, max_len=0, window=0,
