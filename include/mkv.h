@@ -761,7 +761,8 @@ uint64_t mkv_prefill_workspace(const mkv_prefill_args* args);
  * they were, and keys and values behind its keys may hold anything.
  * Lengths outside 0..q_tokens or 0..kv_tokens count as the nearer bound.
  * Scores, their sums and the sum of values are in fp32; the weights are rounded
- * to `dtype` for the product with v.  A value row with an infinity or a NaN may
+ * to `dtype` for the product with v.  The tensor cores cut sums off towards zero, by
+ * 1e-4 of an output of values of one sign at most (capped scores: 2e-4 up to 2^21 keys).  A value row with an infinity or a NaN may
  * make that channel non-finite for queries that do not see it too.  Results do not
  * depend on timing.  Overlap of out with an input is not allowed. */
 mkv_status mkv_prefill(const mkv_prefill_args* args, mkv_stream_t stream);

@@ -1,5 +1,5 @@
 """Scores of the attention of many queries where their forms meet: caps of any size against
-the 64-bit oracle, and capped calls that repeat bit for bit.
+the 64-bit oracle, capped calls that repeat bit for bit, and sums over very many keys.
 
 Tolerances, derived here once (u = 2^-24, e(t), scores, attend as in test_gpu_prompt.py):
 
@@ -8,7 +8,13 @@ capped   A capped score is within 2^-20 of itself: up to half the cap z times a 
          argument's rounding, 2^-23 t (1 - tanh^2) / tanh <= 2^-23, of the exponential 2^-22, worth
          (1 - tanh^2) / (2 tanh) <= 0.86 of it, of the reciprocal 2^-23, worth 2 r / tanh <= 1.2, two
          roundings more: less than 2.5 2^-22.  So 2^-20 A in place of test_gpu_prompt.py's 2^-21 cap: it
-         does not grow with the cap.
+         does not grow with the cap.  Caps up to 64 ln 2 = 44.4 (64 in the log2 domain) may take the second
+         form for all scores of a block: its sum 1 - 2 r is off by 2^-23 for the reciprocal, 2^-23 for the
+         exponential and 2^-24 more, together below 2^-21 of the cap, which comes on top.
+long     The products' sums are cut off by less than 2 u of themselves in each of the 1024 steps of 16384
+         keys; those of several times 16384 are added with u each, and the sum of weights, a block of 64
+         or 128 keys at a time, by u of itself: (2048 + n / 16384 + n / 64) u in place of n u.  Capped
+         scores: 2048 steps of 32768 keys.
 """
 import numpy as np
 import pytest
@@ -178,3 +184,107 @@ def test_windows_both_ways_are_split_for_what_they_reach(M):
         ref = O.attend(f64(q[0]), f64(k[0]).transpose(1, 0, 2), f64(v[0]).transpose(1, 0, 2), see,
                        np.arange(29996, 30000), np.arange(30000))
         capped_near(f64(out[0]), f64(lse[0]), ref, BF16, 30000, 0.0)
+
+
+def long_check(got, q, k, v, rows, base, cap=0.0, steps=1024):
+    """Outputs of some rows of queries at places base + row, over keys and values [n, kv heads, d], against
+    64 bits, and the mean of their relative errors where values have one sign."""
+    n, hk, d = k.shape
+    g = q.shape[1] // hk
+    e, lost = HALF[got.dtype], []
+    for h in range(q.shape[1]):
+        kk, vv, qq = k[:, h // g].double(), v[:, h // g].double(), q[rows, h].double()
+        z = qq @ kk.T / d**0.5
+        size = (qq.abs() @ kk.abs().T / d**0.5).amax(-1, keepdim=True)
+        z = cap * torch.tanh(z / cap) if cap else z
+        z.masked_fill_(torch.arange(n, device=DEV)[None] > base + rows[:, None], -np.inf)
+        w = torch.softmax(z, -1)
+        want, spread = w @ vv, w @ vv.abs()
+        # the roundings of the weights and of values held in 16 bits, and of the output
+        tol = (2 * (d / 16 + 4) * 2.0**-22 * size + 2.0**-16 + e + (2 * steps + n / 16 / steps + n / 64 + 64) * U) * spread
+        tol = tol + e * want.abs() * 1.01 + 2.0**-25
+        assert ((got[rows, h].double() - want).abs() <= tol).all()
+        lost.append((got[rows, h].double() / want - 1).flatten())
+    return float(torch.cat(lost).mean())
+
+
+def many(shape, dtype, seed, size=1.0, mean=0.0):
+    """As rnd(), drawn on the GPU."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return (torch.randn(shape, generator=g, device=DEV) * size + mean).to(dtype)
+
+
+def ramp(n, hk, d, dtype, seed, size):
+    """Keys whose scores with a first channel of 1 grow by `size` over all places."""
+    k = many((1, n, hk, d), dtype, seed, 0.5)
+    k[..., 0] = (torch.linspace(0, size * d**0.5, n, device=DEV)[:, None]).to(dtype)
+    return k
+
+
+@pytest.mark.parametrize("d,nq,heads,kv", [(256, 4096, 8, 4), (128, 8192, 16, 4), (64, 8192, 16, 4), (128, 3, 8, 2),
+                                           (256, 1, 4, 1), (64, 20, 4, 1)])
+@pytest.mark.parametrize("size", [0.0, 25.0])
+def test_long_walks_lose_nothing(M, d, nq, heads, kv, size):
+    """Values of one sign over many keys, scores nearly equal or growing all the way."""
+    n = (1 << 21) + 77 if nq < 100 else (1 << 17) + 77
+    q = rnd((1, nq, heads, d), F16, 1, 0.25)
+    q[..., 0] = 1.0
+    k = ramp(n, kv, d, F16, 2, size)
+    v = many((1, n, kv, d), F16, 3, 0.25, 1.5)
+    out = M.mkv_prefill(q, k, v)
+    lost = long_check(out[0], q[0], k[0], v[0], torch.arange(0, nq, max(1, nq // 16), device=DEV), n - nq)
+    # 1024 steps cut off by less than 2 u, blocks of the sum of weights u each, and the mean of roundings
+    # of which there are thousands: six deviations of a step of 2^-11 over the square root of their number
+    parts = n if nq >= 100 else n / 64
+    assert abs(lost) <= (2048 + parts / 64) * U + 6 * 2.0**-11 / (3 * 16 * d) ** 0.5
+
+
+@pytest.mark.parametrize("d,nq,heads,kv", [(256, 4096, 8, 4), (128, 8192, 16, 4)])
+@pytest.mark.parametrize("size", [0.0, 25.0])
+def test_long_capped_walks_lose_little(M, d, nq, heads, kv, size):
+    n = (1 << 19) + 77
+    q = rnd((1, nq, heads, d), F16, 1, 0.25)
+    q[..., 0] = 1.0
+    k = ramp(n, kv, d, F16, 2, size)
+    v = many((1, n, kv, d), F16, 3, 0.25, 1.5)
+    out = M.mkv_prefill(q, k, v, cap=30.0)
+    lost = long_check(out[0], q[0], k[0], v[0], torch.arange(0, nq, nq // 16, device=DEV), n - nq, 30.0, 2048)
+    assert abs(lost) <= (4096 + n / 64) * U + 6 * 2.0**-11 / (3 * 16 * d) ** 0.5
+
+
+@pytest.mark.parametrize("ctype,qtype", [(F16, F16), (E4M3, F16)])
+@pytest.mark.parametrize("m,g", [(512, 4), (40, 4), (4, 4)])
+@pytest.mark.parametrize("size", [0.0, 25.0])
+def test_long_walks_over_pages_lose_nothing(M, ctype, qtype, m, g, size):
+    n, kv, d, ps = (1 << 17) * (4 if m < 512 else 1), 8 if m == 512 else 1, 128, 128
+    q = rnd((1, m, kv * g, d), qtype, 1, 0.25)
+    q[..., 0] = 1.0
+    k = ramp(n, kv, d, F16, 2, size).to(ctype)
+    v = many((1, n, kv, d), F16, 3, 0.25, 1.5).to(ctype)
+    pages = [x.view(n // ps, ps, kv, d).view(torch.uint8 if ctype == E4M3 else ctype).transpose(1, 2).contiguous().view(ctype)
+             for x in (k, v)]
+    cache = M.MkvPaged(*pages, torch.arange(n // ps, dtype=torch.int32, device=DEV).view(1, -1))
+    out = M.mkv_paged_attend(cache, q, i32([n]))
+    long_check(out[0], q[0], k[0].float(), v[0].float(), torch.arange(0, m, max(1, m // 16), device=DEV), n - m)
+    assert cache.check() == M.MKV_OK
+
+
+def test_long_walks_with_options(M):
+    """Biased scores walk from the last key down; capped ones; documents and windows skip blocks."""
+    n, nq = 40000, 4096
+    q, k = rnd((1, nq, 8, 128), BF16, 1), rnd((1, n, 2, 128), BF16, 2)
+    v = (rnd((1, n, 2, 128), torch.float32, 3, 0.25) + 1.5).to(BF16)
+    rows = [0, 1234, nq - 1]
+    docs = ((torch.arange(n, device=DEV)[None] // 3000) % 2).int()
+    for kw in (dict(slopes=[1e-4 * (i + 1) for i in range(8)]), dict(cap=5.0), dict(docs=docs), dict(window=20000),
+               dict(window=12000, causal=False), dict(slopes=[-1e-4] * 8, cap=9.0)):
+        call = dict(kw)
+        if "slopes" in kw:
+            call["slopes"] = torch.tensor(kw["slopes"], dtype=torch.float32, device=DEV)
+        lse = torch.empty((1, nq, 8), device=DEV)
+        out = M.mkv_prefill(q, k, v, lse=lse, **call)
+        see = O.visible(nq, n, kw.get("causal", True), kw.get("window", 0), None,
+                        docs[0].cpu().numpy() if "docs" in kw else None)[rows]
+        ref = O.attend(f64(q[0, rows]), f64(k[0]).transpose(1, 0, 2), f64(v[0]).transpose(1, 0, 2), see,
+                       n - nq + np.array(rows), np.arange(n), None, kw.get("cap", 0.0), kw.get("slopes"))
+        capped_near(f64(out[0, rows]), f64(lse[0, rows]), ref, BF16, 1024 + n / 64, kw.get("cap", 0.0))

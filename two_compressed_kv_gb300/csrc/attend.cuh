@@ -337,6 +337,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
   using C = AT<D, TILES, FROM, COPIES>;
   constexpr int NB = C::NB, G = C::G;
   constexpr bool CAP = (MODS & 1) != 0, SLOPES = (MODS & 2) != 0;      // scores are capped, biased
+  constexpr bool FOLDS = !CAP;             // see AT_FOLD
   constexpr bool E4 = C::E4, PAGED = FROM != FROM_TENSORS, FEW = C::FEW;
   extern __shared__ uint8_t smem_raw[];
   __shared__ AttendShared sh;
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
         const uint32_t va = desc_lo(ring + s * C::TILE, NB * 128);
 #pragma unroll
         for (int c = 0; c < NB / 16; ++c)
-          mma_ts(o0, s0 + (k & 1) * NB + c * 8, va + c * 2048 / 16, IO, k > 0 || c > 0);
+          mma_ts(o0, s0 + (k & 1) * NB + c * 8, va + c * 2048 / 16, IO, (FOLDS ? (k & p.fold) != 0 : k > 0) || c > 0);
         tc_commit(&sh.empty[s]);
       };
       // What lies behind the sequence in its last block may be anything, and 0 times a
@@ -868,7 +869,8 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
           }
           x = fmaxf(x, x1);
           const bool grows = live && fmaf(x, by, mref) > AT_BIAS + (BF16 && !E4 ? AT_SLACK_BF16 : AT_SLACK);
-          if (__any_sync(~0u, grows)) {
+          const bool folds = FOLDS && (k & p.fold) == 0 && k > 0;
+          if (__any_sync(~0u, grows) || folds) {
             float f = 1.f;
             if (grows) {
               if (top != -CUDART_INF_F) f = ex2((top - x) * by);
@@ -882,6 +884,27 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
               const int used = 2 * k;
               if (!(ok = wait(&sh.empty[used % C::STAGES], (used / C::STAGES) & 1))) break;
               tc_fence_after();
+              const bool held = FOLDS && (int)k - 1 > p.fold;       // some are in the workspace
+              if (folds || held) {
+                int at = row;
+                asm volatile("" : "+r"(at));               // addressed here: outside the loop it costs registers
+                float4* kept = p.part_o + (cta * TILES + tile) * (D / 4) * 128 + at;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16, kept += 4 * 128) {
+                  uint32_t o[16];
+                  tmem_ld16(o_at + c, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    float4 w = held ? kept[i * 128] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (folds) {
+                      w.x += __uint_as_float(o[4 * i]), w.y += __uint_as_float(o[4 * i + 1]);
+                      w.z += __uint_as_float(o[4 * i + 2]), w.w += __uint_as_float(o[4 * i + 3]);
+                    }
+                    kept[i * 128] = make_float4(w.x * f, w.y * f, w.z * f, w.w * f);
+                  }
+                }
+              }
 #pragma unroll
               for (int c = 0; c < D; c += 16) {
                 uint32_t o[16];
@@ -931,6 +954,19 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
       // (with copies of the rows every warp has its part in the join)
       const bool joins = FEW ? t0 < t1 : any;
       if (ok && joins && k > 0) ok = wait(&sh.o_last[tile], 0);
+      // 32 channels of the row's sums, those in the workspace among them
+      auto sums = [&](int c, float (&o)[32]) {
+        tmem_ld32(o_at + c, o);
+        tmem_ld_wait();
+        if (FOLDS && (int)k - 1 > p.fold) {
+          const float4* kept = p.part_o + ((cta * TILES + tile) * (D / 4) + c / 4) * 128 + row;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 w = kept[i * 128];
+            o[4 * i] += w.x, o[4 * i + 1] += w.y, o[4 * i + 2] += w.z, o[4 * i + 3] += w.w;
+          }
+        }
+      };
       // A row tile without padding goes out by one copy, through the shared memory of its
       // queries, which no product needs any more; otherwise every thread writes its row.
       const bool whole = !FEW && p.splits == 1 && t0 + (tile + 1) * TT <= t1;
@@ -968,10 +1004,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           float o[32];
-          if (k > 0) {
-            tmem_ld32(o_at + c, o);
-            tmem_ld_wait();
-          }
+          if (k > 0) sums(c, o);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             *reinterpret_cast<float4*>(to + c + 4 * i) =
@@ -1017,10 +1050,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           float o[32];
-          if (k > 0) {
-            tmem_ld32(o_at + c, o);
-            tmem_ld_wait();
-          }
+          if (k > 0) sums(c, o);
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
           if (p.splits > 1) {

@@ -209,6 +209,7 @@ bool strides_ok(const int64_t* s, int64_t e0, int64_t e1, int64_t e2) {
 struct AttendLayout {
   int copies;
   int tiles, tile_tokens, groups, splits;
+  int fold;                                // as in AttendParams
   uint64_t docs, part_o, part_ml, total;   // byte offsets
 };
 
@@ -223,7 +224,7 @@ constexpr int64_t kJoinBytes = 4 << 20;
 // (tensor memory) or 8-bit pages (their second warpgroup widens).
 // `reach`: how far from a query the keys that it sees may lie, both ways together; 0: anywhere.
 AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, int64_t reach, bool e4m3, bool docs,
-                           int sms) {
+                           bool capped, int sms) {
   AttendLayout l;
   l.copies = nq * g <= 32 ? 4 : nq * g <= 64 && e4m3 ? 2 : 1;
   l.tile_tokens = 128 / l.copies / g;
@@ -236,6 +237,8 @@ AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, i
   if (reach) keys = std::min<int64_t>(nk, reach + l.tiles * l.tile_tokens + NB);
   const int64_t blocks = up(keys, NB);
   l.splits = 1;
+  // the new tokens of a tree, 64 at most, see keys from the first one's on
+  const int64_t walk = up(reach ? std::min<int64_t>(nk, keys + 64) : keys, NB);
   // a few rows over many keys: parts of the keys, joined by a second kernel
   const int64_t part_bytes = (int64_t)B * H * g * nq * D * 8;      // written and read
   int64_t best = up(items, sms) * (blocks + kCtaBlocks);
@@ -249,10 +252,12 @@ AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, i
     at += (bytes + 255) & ~(uint64_t)255;
     return here;
   };
-  const uint64_t rows = l.splits > 1 ? (uint64_t)items * l.splits * l.tiles * 128 : 0;
+  if (capped) l.splits = std::max(l.splits, (int)std::min<int64_t>(64, up(walk, AT_PART_CAPPED / NB)));
+  l.fold = !capped && up(walk, l.splits) > AT_FOLD / NB ? AT_FOLD / NB - 1 : INT32_MAX;
+  const uint64_t rows = l.splits > 1 || l.fold != INT32_MAX ? (uint64_t)items * l.splits * l.tiles * 128 : 0;
   l.docs = place(docs ? (uint64_t)B * up(nk, NB) * 8 : 0);
   l.part_o = place(rows * D * 4);
-  l.part_ml = place(rows * 8);
+  l.part_ml = place(l.splits > 1 ? rows * 8 : 0);
   l.total = at;
   return l;
 }
@@ -261,7 +266,7 @@ AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, i
 AttendLayout prefill_layout(const mkv_prefill_args* a, int sms) {
   const int64_t reach = a->prefix ? 0 : a->causal ? a->window : 2 * (int64_t)a->window;
   return attend_layout(a->batch, a->n_kv_heads, a->n_q_heads / a->n_kv_heads, a->head_dim, a->q_tokens, a->kv_tokens, reach,
-                       false, a->docs != nullptr, sms);
+                       false, a->docs != nullptr, a->cap > 0.f, sms);
 }
 
 int64_t attend_limit(const mkv_paged_cache* c, const mkv_paged_attend_args* a) {
@@ -271,7 +276,7 @@ int64_t attend_limit(const mkv_paged_cache* c, const mkv_paged_attend_args* a) {
 
 AttendLayout paged_layout(const mkv_paged_cache* c, const mkv_paged_attend_args* a, int sms) {
   return attend_layout(c->batch, c->n_kv_heads, a->n_q_heads / c->n_kv_heads, c->head_dim, a->n, attend_limit(c, a),
-                       a->window, c->dtype == MKV_DT_E4M3, false, sms);
+                       a->window, c->dtype == MKV_DT_E4M3, false, a->cap > 0.f, sms);
 }
 
 // Takes over a layout and launches.
@@ -283,6 +288,7 @@ mkv_status attend(AttendParams& p, const AttendLayout& l, void* workspace, mkv_s
   p.tile_tokens = l.tile_tokens;
   p.groups = l.groups;
   p.splits = l.splits;
+  p.fold = l.fold;
   p.doc_range = reinterpret_cast<int2*>(ws + l.docs);
   p.part_o = reinterpret_cast<float4*>(ws + l.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);

@@ -24,6 +24,15 @@ constexpr int attend_block(int D, int tiles, bool e4m3, bool few) {
   return D == 256 || tiles == 2 || (e4m3 && !few) ? 64 : 128;
 }
 
+// Keys whose weighted values tensor memory sums up by itself.  The products cut their sums off
+// towards zero, which adds up: outputs of values of one sign come out too small by up to 6e-9 of
+// themselves a key (131072 keys: 8e-4, more than half a step of fp16).  So after AT_FOLD keys the
+// sums are added to those in the workspace, with rounding to nearest, and begin again: 1e-4.  (8192
+// keys: 5e-5, but 512 queries over 32768 keys take 203 us instead of 197.)
+// Kernels of capped scores have no registers for that (4096 x 2 tokens: 312 us, 291 without): their
+// keys are cut into parts of at most AT_PART_CAPPED, up to 64 of them, which the join adds: 2e-4.
+constexpr int AT_FOLD = 16384, AT_PART_CAPPED = 32768;
+
 struct AttendParams {
   const void* q;
   void* out;
@@ -57,7 +66,8 @@ struct AttendParams {
   int tiles;                   // row tiles of a CTA: 1 or 2
   int groups;                  // of row tiles
   int splits;
-  float4* part_o;              // workspace: [CTA][tiles][D / 4][128 rows] sums over weights, splits > 1
+  int fold;                    // AT_FOLD in blocks, less 1; INT32_MAX where no walk is as long
+  float4* part_o;              // workspace: [CTA][tiles][D / 4][128 rows] sums over weights, splits > 1 or fold
   float2* part_ml;             // [CTA][tiles][128] reference (log2 domain) and sum of weights
 };
 

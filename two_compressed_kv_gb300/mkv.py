@@ -8,6 +8,7 @@ stream.  A missing library is an ImportError, never a fallback.
 from __future__ import annotations
 
 import ctypes
+import itertools
 import os
 from ctypes import (POINTER, Structure, c_char_p, c_double, c_float, c_int, c_int32, c_int64,
                     c_uint8, c_uint16, c_uint32, c_uint64, c_void_p)
@@ -770,17 +771,17 @@ def mkv_prefill(q, k, v, out=None, lse=None, causal=True, window=0, prefix=None,
 
 
 def mkv_prefill_workspace(batch, q_tokens, kv_tokens, q_heads, kv_heads, head_dim, window=0, docs=False,
-                          device=None, causal=None, prefix=None) -> int:
+                          device=None, causal=None, prefix=None, capped=None) -> int:
     """Bytes of workspace of mkv_prefill for these sizes on `device` (None: the current one); 0: it
-    needs none.  causal, prefix: whether the call has them; None: enough for either."""
+    needs none.  causal, prefix, capped: whether the call has them; None: enough for either."""
     _native()
     most = 0
-    for c, p in [(1, 0), (1, 1), (0, 0)]:
-        if c != (c if causal is None else bool(causal)) or p != (p if prefix is None else bool(prefix)):
+    for c, p, t in itertools.product((1, 0), (0, 1), (0, 1)):
+        if p > c or any(x is not None and y != bool(x) for x, y in ((causal, c), (prefix, p), (capped, t))):
             continue
         a = mkv_prefill_args(batch=batch, q_tokens=q_tokens, kv_tokens=kv_tokens, n_q_heads=q_heads,
                              n_kv_heads=kv_heads, head_dim=head_dim, dtype=MKV_DT_F16, window=window,
-                             docs=1 if docs else None, causal=c, prefix=p or None)
+                             docs=1 if docs else None, causal=c, prefix=p or None, cap=t)
         with _T.cuda.device(device):
             n = _lib.mkv_prefill_workspace(ctypes.byref(a))
         if n == 2**64 - 1:
@@ -806,16 +807,20 @@ def mkv_paged_attend(cache, q, seq_lens, tree=None, new_lens=None, out=None, lse
     return out
 
 
-def mkv_paged_attend_workspace(cache, new_tokens, q_heads, max_len=0, window=0) -> int:
-    """Bytes of workspace of mkv_paged_attend for these sizes; 0: it needs none."""
+def mkv_paged_attend_workspace(cache, new_tokens, q_heads, max_len=0, window=0, capped=None) -> int:
+    """Bytes of workspace of mkv_paged_attend for these sizes; 0: it needs none.  capped: whether the
+    call has a cap; None: enough for either."""
     qt = MKV_DT_F16 if cache.view.dtype == MKV_DT_E4M3 else cache.view.dtype
-    a = mkv_paged_attend_args(n=new_tokens, n_q_heads=q_heads, max_len=max_len, q_dtype=qt,
-                              window=window)
-    with _T.cuda.device(cache.device):
-        n = _lib.mkv_paged_attend_workspace(ctypes.byref(cache.view), ctypes.byref(a))
-    if n == 2**64 - 1:
-        raise MkvError(MKV_ERR_INVALID_ARG, "mkv_paged_attend_workspace")
-    return n
+    most = 0
+    for t in (0, 1) if capped is None else (int(bool(capped)),):
+        a = mkv_paged_attend_args(n=new_tokens, n_q_heads=q_heads, max_len=max_len, q_dtype=qt,
+                                  window=window, cap=t)
+        with _T.cuda.device(cache.device):
+            n = _lib.mkv_paged_attend_workspace(ctypes.byref(cache.view), ctypes.byref(a))
+        if n == 2**64 - 1:
+            raise MkvError(MKV_ERR_INVALID_ARG, "mkv_paged_attend_workspace")
+        most = max(most, n)
+    return most
 
 
 class Mkv:
