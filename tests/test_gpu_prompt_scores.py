@@ -288,3 +288,44 @@ def test_long_walks_with_options(M):
         ref = O.attend(f64(q[0, rows]), f64(k[0]).transpose(1, 0, 2), f64(v[0]).transpose(1, 0, 2), see,
                        n - nq + np.array(rows), np.arange(n), None, kw.get("cap", 0.0), kw.get("slopes"))
         capped_near(f64(out[0, rows]), f64(lse[0, rows]), ref, BF16, 1024 + n / 64, kw.get("cap", 0.0))
+
+
+@pytest.mark.parametrize("m,g", [(1, 4), (2, 4), (3, 3), (4, 8), (12, 5), (40, 4)])
+@pytest.mark.parametrize("d,ps", [(64, 16), (128, 32), (256, 48)])
+@pytest.mark.parametrize("kw", [{}, dict(cap=9.0), dict(slopes=True)])
+def test_nan_behind_a_sequence_of_8_bit_pages(M, d, ps, m, g, kw):
+    """Slots from the length on may hold anything, NaN too, which e4m3 has (0x7f, 0xff)."""
+    lens = [300, 33 + m, m]
+    clean = make_cache(M, E4M3, 3, 2, d, ps, -(-320 // ps), 5)
+    q = rnd((3, m, 2 * g, d), F16, 4)
+    call = dict(kw)
+    if "slopes" in kw:
+        call["slopes"] = torch.tensor([2.0**-(i % 6 + 1) for i in range(2 * g)], dtype=torch.float32, device=DEV)
+    got = []
+    for stray in (0x00, 0x7f, 0xff):
+        for b, n in enumerate(lens):
+            for t in range(n, clean.page_table.shape[1] * ps):
+                page = int(clean.page_table[b, t // ps])
+                for pool in (clean.k_pages, clean.v_pages):
+                    pool.view(torch.uint8)[page, :, t % ps] = stray
+        lse = torch.empty((3, m, 2 * g), device=DEV)
+        got.append((M.mkv_paged_attend(clean, q, i32(lens), lse=lse, **call), lse))
+    assert clean.check() == M.MKV_OK
+    for out, lse in got:
+        assert torch.isfinite(out.float()).all() and torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+    for i, n in enumerate(lens):
+        ref = O.attend(f64(q[i]), rows_of(clean, 0, i, n), rows_of(clean, 1, i, n), O.visible(m, n), np.arange(n - m, n),
+                       np.arange(n), None, kw.get("cap", 0.0), f64(call["slopes"]) if "slopes" in kw else None)
+        capped_near(f64(got[1][0][i]), f64(got[1][1][i]), ref, F16, n, kw.get("cap", 0.0))
+
+
+def test_the_status_word_of_prompts(M):
+    """Left as it is where every wait was over in time, whatever the lengths, and not needed."""
+    q, k = rnd((2, 140, 4, 128), BF16, 1), rnd((2, 300, 2, 128), BF16, 2)
+    want = M.mkv_prefill(q, k, k, q_lens=i32([140, 500]), kv_lens=i32([300, -4]))
+    for word in (0, 64):
+        status = i32([word])
+        got = M.mkv_prefill(q, k, k, q_lens=i32([140, 500]), kv_lens=i32([300, -4]), status=status)
+        assert torch.equal(got, want) and int(status) == word
+    with pytest.raises((TypeError, ValueError)):
+        M.mkv_prefill(q, k, k, status=torch.zeros(1, dtype=torch.int64, device=DEV))
