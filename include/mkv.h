@@ -725,7 +725,8 @@ typedef struct {
   const int32_t* docs;       /* device [batch][kv_tokens], or NULL: the document of each place (any numbers, in
                                 any order); keys of other documents than the query's are not seen */
   const float* slopes;       /* device [n_q_heads], or NULL */
-  int32_t* status;           /* device word, or NULL: as in mkv_paged_cache, for waits that gave up */
+  int32_t* status;           /* device word, or NULL: as in mkv_paged_cache, for waits that gave up, whose
+                                outputs are undefined; without it nothing reports them */
   void* workspace;           /* device, 16-byte aligned, of mkv_prefill_workspace bytes (NULL where that is 0) */
   uint64_t workspace_bytes;
   int64_t q_stride[3];       /* elements between batches, tokens, heads: positive multiples of 8 where the */
@@ -747,8 +748,8 @@ typedef struct {
 } mkv_prefill_args;
 
 /* Bytes of workspace of mkv_prefill with these arguments on the current device
- * (pointers are not looked at, except whether docs and prefix are NULL), or UINT64_MAX
- * for invalid ones.  0 is enough for most calls. */
+ * (pointers are not looked at, except whether docs, prefix and slopes are NULL), or
+ * UINT64_MAX for invalid ones.  0 is enough for most calls. */
 uint64_t mkv_prefill_workspace(const mkv_prefill_args* args);
 
 /* Attention of a prompt, or of a part of one over what came before it: softmax of
@@ -762,7 +763,8 @@ uint64_t mkv_prefill_workspace(const mkv_prefill_args* args);
  * Lengths outside 0..q_tokens or 0..kv_tokens count as the nearer bound.
  * Scores, their sums and the sum of values are in fp32; the weights are rounded
  * to `dtype` for the product with v.  The tensor cores cut sums off towards zero, by
- * 1e-4 of an output of values of one sign at most (capped scores: 2e-4 up to 2^21 keys).  A value row with an infinity or a NaN may
+ * 1e-4 of an output of values of one sign at most (capped or biased scores: 2e-4 up to
+ * 2^21 keys).  A value row with an infinity or a NaN may
  * make that channel non-finite for queries that do not see it too.  Results do not
  * depend on timing.  Overlap of out with an input is not allowed. */
 mkv_status mkv_prefill(const mkv_prefill_args* args, mkv_stream_t stream);
@@ -791,8 +793,8 @@ typedef struct {
   float cap;
 } mkv_paged_attend_args;
 
-/* Bytes of workspace of mkv_paged_attend on the current device, or UINT64_MAX for
- * invalid arguments. */
+/* Bytes of workspace of mkv_paged_attend on the current device (of the pointers in
+ * args only whether slopes is NULL counts), or UINT64_MAX for invalid arguments. */
 uint64_t mkv_paged_attend_workspace(const mkv_paged_cache* cache, const mkv_paged_attend_args* args);
 
 /* Attention of several new tokens per sequence over its cached tokens: a prompt's
@@ -812,7 +814,10 @@ uint64_t mkv_paged_attend_workspace(const mkv_paged_cache* cache, const mkv_page
  * zeros and an lse of -inf; rows of out and lse from m on are left as they were.
  * Lengths outside their bounds count as the nearer one, new_lens above seq_lens as that, a page
  * outside the cache as absent tokens; these are reported in `status`.  Slots at or
- * behind seq_lens[b] may hold anything.  Results do not depend on timing. */
+ * behind seq_lens[b] may hold anything; a value row before it with an infinity or a
+ * NaN may make that channel non-finite for new tokens that do not see it too.
+ * Results do not depend on timing.  Neither this call nor mkv_prefill adds to the
+ * accumulated weights that mkv_paged_evict ranks by: only mkv_paged_decode does. */
 mkv_status mkv_paged_attend(const mkv_paged_cache* cache, const mkv_paged_attend_args* args, mkv_stream_t stream);
 
 #ifdef __cplusplus

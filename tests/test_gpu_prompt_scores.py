@@ -14,7 +14,7 @@ capped   A capped score is within 2^-20 of itself: up to half the cap z times a 
 long     The products' sums are cut off by less than 2 u of themselves in each of the 1024 steps of 16384
          keys; those of several times 16384 are added with u each, and the sum of weights, a block of 64
          or 128 keys at a time, by u of itself: (2048 + n / 16384 + n / 64) u in place of n u.  Capped
-         scores: 2048 steps of 32768 keys.
+         or biased scores: 2048 steps of 32768 keys.
 """
 import numpy as np
 import pytest
@@ -287,7 +287,7 @@ def test_long_walks_with_options(M):
                         docs[0].cpu().numpy() if "docs" in kw else None)[rows]
         ref = O.attend(f64(q[0, rows]), f64(k[0]).transpose(1, 0, 2), f64(v[0]).transpose(1, 0, 2), see,
                        n - nq + np.array(rows), np.arange(n), None, kw.get("cap", 0.0), kw.get("slopes"))
-        capped_near(f64(out[0, rows]), f64(lse[0, rows]), ref, BF16, 1024 + n / 64, kw.get("cap", 0.0))
+        capped_near(f64(out[0, rows]), f64(lse[0, rows]), ref, BF16, 4096 + n / 64, kw.get("cap", 0.0))
 
 
 @pytest.mark.parametrize("m,g", [(1, 4), (2, 4), (3, 3), (4, 8), (12, 5), (40, 4)])

@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
   using C = AT<D, TILES, FROM, COPIES>;
   constexpr int NB = C::NB, G = C::G;
   constexpr bool CAP = (MODS & 1) != 0, SLOPES = (MODS & 2) != 0;      // scores are capped, biased
-  constexpr bool FOLDS = !CAP;             // see AT_FOLD
+  constexpr bool FOLDS = MODS == 0;        // see AT_FOLD
   constexpr bool E4 = C::E4, PAGED = FROM != FROM_TENSORS, FEW = C::FEW;
   extern __shared__ uint8_t smem_raw[];
   __shared__ AttendShared sh;

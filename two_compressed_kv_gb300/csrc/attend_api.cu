@@ -223,8 +223,9 @@ constexpr int64_t kJoinBytes = 4 << 20;
 // has its own S buffer and K and V are read half as often), but not with heads of 256
 // (tensor memory) or 8-bit pages (their second warpgroup widens).
 // `reach`: how far from a query the keys that it sees may lie, both ways together; 0: anywhere.
+// `mods`: scores are capped or biased.
 AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, int64_t reach, bool e4m3, bool docs,
-                           bool capped, int sms) {
+                           bool mods, int sms) {
   AttendLayout l;
   l.copies = nq * g <= 32 ? 4 : nq * g <= 64 && e4m3 ? 2 : 1;
   l.tile_tokens = 128 / l.copies / g;
@@ -252,8 +253,8 @@ AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, i
     at += (bytes + 255) & ~(uint64_t)255;
     return here;
   };
-  if (capped) l.splits = std::max(l.splits, (int)std::min<int64_t>(64, up(walk, AT_PART_CAPPED / NB)));
-  l.fold = !capped && up(walk, l.splits) > AT_FOLD / NB ? AT_FOLD / NB - 1 : INT32_MAX;
+  if (mods) l.splits = std::max(l.splits, (int)std::min<int64_t>(64, up(walk, AT_PART / NB)));
+  l.fold = !mods && up(walk, l.splits) > AT_FOLD / NB ? AT_FOLD / NB - 1 : INT32_MAX;
   const uint64_t rows = l.splits > 1 || l.fold != INT32_MAX ? (uint64_t)items * l.splits * l.tiles * 128 : 0;
   l.docs = place(docs ? (uint64_t)B * up(nk, NB) * 8 : 0);
   l.part_o = place(rows * D * 4);
@@ -266,7 +267,7 @@ AttendLayout attend_layout(int B, int H, int g, int D, int64_t nq, int64_t nk, i
 AttendLayout prefill_layout(const mkv_prefill_args* a, int sms) {
   const int64_t reach = a->prefix ? 0 : a->causal ? a->window : 2 * (int64_t)a->window;
   return attend_layout(a->batch, a->n_kv_heads, a->n_q_heads / a->n_kv_heads, a->head_dim, a->q_tokens, a->kv_tokens, reach,
-                       false, a->docs != nullptr, a->cap > 0.f, sms);
+                       false, a->docs != nullptr, a->cap > 0.f || a->slopes, sms);
 }
 
 int64_t attend_limit(const mkv_paged_cache* c, const mkv_paged_attend_args* a) {
@@ -276,7 +277,7 @@ int64_t attend_limit(const mkv_paged_cache* c, const mkv_paged_attend_args* a) {
 
 AttendLayout paged_layout(const mkv_paged_cache* c, const mkv_paged_attend_args* a, int sms) {
   return attend_layout(c->batch, c->n_kv_heads, a->n_q_heads / c->n_kv_heads, c->head_dim, a->n, attend_limit(c, a),
-                       a->window, c->dtype == MKV_DT_E4M3, false, a->cap > 0.f, sms);
+                       a->window, c->dtype == MKV_DT_E4M3, false, a->cap > 0.f || a->slopes, sms);
 }
 
 // Takes over a layout and launches.

@@ -29,9 +29,10 @@ constexpr int attend_block(int D, int tiles, bool e4m3, bool few) {
 // themselves a key (131072 keys: 8e-4, more than half a step of fp16).  So after AT_FOLD keys the
 // sums are added to those in the workspace, with rounding to nearest, and begin again: 1e-4.  (8192
 // keys: 5e-5, but 512 queries over 32768 keys take 203 us instead of 197.)
-// Kernels of capped scores have no registers for that (4096 x 2 tokens: 312 us, 291 without): their
-// keys are cut into parts of at most AT_PART_CAPPED, up to 64 of them, which the join adds: 2e-4.
-constexpr int AT_FOLD = 16384, AT_PART_CAPPED = 32768;
+// Kernels of capped or biased scores have no registers for that (4096 x 2 tokens, capped: 312 us,
+// 291 without; a ragged batch with a bias 58, 53): their keys are cut into parts of at most
+// AT_PART, up to 64 of them, which the join adds: 2e-4.
+constexpr int AT_FOLD = 16384, AT_PART = 32768;
 
 struct AttendParams {
   const void* q;

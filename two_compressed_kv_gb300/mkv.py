@@ -760,7 +760,9 @@ def mkv_prefill(q, k, v, out=None, lse=None, causal=True, window=0, prefix=None,
     the query's document): which keys a query sees.  cap: scores become cap * tanh(score / cap);
     slopes (fp32 [q_heads]): slope * distance is taken off.  lse: fp32 [batch, tokens, q_heads] or
     None.  status: int32 [1] or None: set where a bounded wait gave up (outputs undefined then).
-    workspace: a uint8 tensor of mkv_prefill_workspace bytes (None: taken from torch's allocator).
+    workspace: a uint8 tensor of mkv_prefill_workspace bytes (None: taken from torch's allocator):
+    for more than 16384 keys it takes four bytes an element of q, with a cap or slopes for each part
+    of 32768 keys.
     Returns out (new where None), of q's shape and type; rows behind q_lens are left as they were."""
     m = _native()
     if out is None and isinstance(q, _T.Tensor):
@@ -773,7 +775,7 @@ def mkv_prefill(q, k, v, out=None, lse=None, causal=True, window=0, prefix=None,
 def mkv_prefill_workspace(batch, q_tokens, kv_tokens, q_heads, kv_heads, head_dim, window=0, docs=False,
                           device=None, causal=None, prefix=None, capped=None) -> int:
     """Bytes of workspace of mkv_prefill for these sizes on `device` (None: the current one); 0: it
-    needs none.  causal, prefix, capped: whether the call has them; None: enough for either."""
+    needs none.  causal, prefix, capped (or biased): whether the call is so; None: enough for either."""
     _native()
     most = 0
     for c, p, t in itertools.product((1, 0), (0, 1), (0, 1)):
@@ -809,7 +811,7 @@ def mkv_paged_attend(cache, q, seq_lens, tree=None, new_lens=None, out=None, lse
 
 def mkv_paged_attend_workspace(cache, new_tokens, q_heads, max_len=0, window=0, capped=None) -> int:
     """Bytes of workspace of mkv_paged_attend for these sizes; 0: it needs none.  capped: whether the
-    call has a cap; None: enough for either."""
+    call has a cap or slopes; None: enough for either."""
     qt = MKV_DT_F16 if cache.view.dtype == MKV_DT_E4M3 else cache.view.dtype
     most = 0
     for t in (0, 1) if capped is None else (int(bool(capped)),):
