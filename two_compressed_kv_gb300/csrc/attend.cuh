@@ -21,17 +21,19 @@
 // that none waits for products of its own.  The products of a buffer are issued in the
 // order S, P V, next S by one thread, which is the order they execute in.
 //
-// What bounds it: the tensor cores, whose pipe is 82 % busy at 8192 tokens x 4 of 32 heads
-// over 8, causal: 1516 us, 1.45 PFLOP/s of the products that are needed (a library product
-// of large matrices: 1.89); without the causal mask, whose blocks on the diagonal are half
-// idle, 1.63.  With two row tiles a CTA one softmax runs beside the other's
-// products: 1549 us with two S buffers a tile, 2520 with one and an issuing lane for both.
+// What bounds it: the tensor cores' pipe, occupied 82 % of the time at 8192 tokens x 4 of 32
+// heads over 8, causal, 66 % with arithmetic and the rest with reading operands: 1520 us in
+// calls in a row (1425 for one launch by itself, at the clock that a short run has), 1.45
+// PFLOP/s of the products that are needed (a library product of large matrices: 1.89);
+// without the causal mask, whose blocks on the diagonal are half idle, 1.61.  With two row
+// tiles a CTA one softmax runs beside the other's products: of calls in a row 1549 us with
+// two S buffers a tile, 2520 with one and an issuing lane for both.
 // A short prompt is bound by what a CTA does before its first product and after its last,
 // some 8000 cycles, and by its longest row tile: one prompt of 2048 tokens 35 us, 1.9 times
 // the products' time.  (Two CTAs an SM with a row tile each, whose starts and ends overlap:
-// the same 35 us, 72 instead of 62 for a ragged batch with biased scores, 1445 instead of
-// 1420 for 8192 x 4; 128 registers a thread are too few.)  Capped or biased scores: by the
-// softmax, 4096 x 2 tokens 293 and 243 us for 204.
+// the same 35 us, and before biased scores were walked from the last key down 72 instead of 62
+// for a ragged batch of them; 128 registers a thread are too few.)  Capped or biased scores: by
+// the softmax, 4096 x 2 tokens 292 and 243 us for 207.
 //
 // O is scaled down only where a row's maximum passes its reference by 2^6 (bf16: 2^24):
 // after the first blocks that hardly happens, and no work on O lies between the products.
@@ -105,7 +107,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // (found by exchange), the factors in its coefficients: of degree 4 for |a x| <= 1/2
 // (3e-8), of 6 up to 1 (7e-8), both within 3 u of it with their roundings, and without the
 // two slow functions of the other form.  16K tokens in documents, capped at 50: 840 us with
-// that form alone, 647 with degree 6, 551 with both.
+// that form alone, 647 with degree 6, 548 with both.
 template <int N>
 struct SmallTanh {
   float c[N];
@@ -752,7 +754,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
               // The form goes by the scores that rows which are there see: forms differ in their
               // roundings, and the rest may be anything.  What the other forms need is hidden from
               // the compiler until there: taken out of the loop over the blocks it costs this one
-              // its registers (4096 x 2 tokens: 316 us, 287).
+              // its registers (4096 x 2 tokens: 316 us, 292).
               if (__all_sync(~0u, big * into <= 0.5f)) {
 #pragma unroll
                 for (int i = 0; i < COLS; i += 2) {

@@ -438,8 +438,10 @@ cudaError_t encode_map(CUtensorMap* map, const void* base, bool bytes, int rank,
 
 // Rows of 8-bit pages that a few query rows share go through the streaming kernel, whose
 // products need no widened copy of them in shared memory: with 8 columns or fewer.  Us of
-// this kernel and of the one of many queries: 32 streams of 32768 slots of 128, 4 rows: 73,
-// 100; 256 streams of 2048, 16 rows: 90, 61.  16-bit pages: 98, 92, so they are not here.
+// this kernel and of the one of many queries, 4 rows, 32 streams of 32768 slots of 128: 70, 100;
+// 8 rows, 32 streams of 4 MB of keys: heads of 64 97, 129, of 128 73, 104, of 256 73, 111; 256
+// streams of 2048: 36, 42; 46, 60; 52, 116; 8 streams of 300: 8.0, 7.8; 9.0, 10.9; 9.8, 17.6.
+// 16 rows, 256 streams of 2048: 90, 61.  16-bit pages: 98, 92, so they are not here.
 bool paged_attend_streams(const mkv_paged_cache* c, const mkv_paged_attend_args* a) {
   return c->dtype == MKV_DT_E4M3 && (int64_t)a->n * (a->n_q_heads / c->n_kv_heads) <= 8;
 }
