@@ -8,9 +8,12 @@ capped   A capped score is within 2^-20 of itself: up to half the cap z times a 
          argument's rounding, 2^-23 t (1 - tanh^2) / tanh <= 2^-23, of the exponential 2^-22, worth
          (1 - tanh^2) / (2 tanh) <= 0.86 of it, of the reciprocal 2^-23, worth 2 r / tanh <= 1.2, two
          roundings more: less than 2.5 2^-22.  So 2^-20 A in place of test_gpu_prompt.py's 2^-21 cap: it
-         does not grow with the cap.  Caps up to 64 ln 2 = 44.4 (64 in the log2 domain) may take the second
+         does not grow with the cap.  Caps up to 128 ln 2 = 88.7 (128 in the log2 domain) may take the second
          form for all scores of a block: its sum 1 - 2 r is off by 2^-23 for the reciprocal, 2^-23 for the
          exponential and 2^-24 more, together below 2^-21 of the cap, which comes on top.
+pages    8-bit caches have fp16 weights whatever the queries' type is, so the 2^-33 sum |v| of such
+         weights below the normal range (attend) holds for bf16 queries too: one key of weight 1 whose
+         value is 0 leaves an output of 1e-9, of the other keys, where 2^-33 sum |v| is 1.4e-8.
 long     The products' sums are cut off by less than 2 u of themselves in each of the 1024 steps of 16384
          keys; those of several times 16384 are added with u each, and the sum of weights, a block of 64
          or 128 keys at a time, by u of itself: (2048 + n / 16384 + n / 64) u in place of n u.  Capped
@@ -26,12 +29,13 @@ from test_gpu_prompt import (BF16, DEV, E4M3, F16, HALF, M, U, f64, i32, make_ca
 pytestmark = pytest.mark.gpu
 
 
-def capped_near(got, lse, ref, dtype, n, cap):
+def capped_near(got, lse, ref, dtype, n, cap, fp16_weights=False):
     out, want_lse, spread, size, total = ref
-    d = ((out.shape[-1] / 16 + 4) * 2.0**-22 + 2.0**-20) * size + (2.0**-21 * cap if cap <= 44.4 else 0.0)
+    d = ((out.shape[-1] / 16 + 4) * 2.0**-22 + 2.0**-20) * size + (2.0**-21 * cap if cap <= 88.7 else 0.0)
     e = HALF[dtype]
     tol = (2 * d[..., None] + 2.0**-16 + e + (n + 64) * U) * spread + e * np.abs(out) * 1.01
-    near(got, out, tol + (2.0**-33 * total + 2.0**-25 if dtype == F16 else 0.0))
+    tol = tol + (2.0**-33 * total if dtype == F16 or fp16_weights else 0.0)
+    near(got, out, tol + (2.0**-25 if dtype == F16 else 0.0))
     near(lse, want_lse, d + (n + 64) * U + 2.0**-22 * np.abs(want_lse) + 2.0**-21)
 
 
@@ -44,7 +48,7 @@ def pages_check(M, ctype, qtype, n, m, g, d, cap, q=None, scale=0.0, slopes=None
                              slopes=None if slopes is None else torch.tensor(slopes, dtype=torch.float32, device=DEV))
     ref = O.attend(f64(q[0]), rows_of(cache, 0, 0, n), rows_of(cache, 1, 0, n), O.visible(m, n), np.arange(n - m, n),
                    np.arange(n), scale or None, cap, slopes)
-    capped_near(f64(out[0]), f64(lse[0]), ref, qtype, n, cap)
+    capped_near(f64(out[0]), f64(lse[0]), ref, qtype, n, cap, ctype == E4M3)
 
 
 CAPS = [0.01, 1.0, 20.0, 1e3, 1e4, 1e5, 1e6, 1e8, 1e18, 1e30, 1e37, 2.0**127]
@@ -78,6 +82,24 @@ def test_prompt_caps_of_any_size(M, dtype, d, cap):
     ref = O.attend(f64(q[0]), f64(k[0]).transpose(1, 0, 2), f64(v[0]).transpose(1, 0, 2), O.visible(n, n), np.arange(n),
                    np.arange(n), None, cap)
     capped_near(f64(out[0]), f64(lse[0]), ref, dtype, n, cap)
+
+
+@pytest.mark.parametrize("cap", [2.0, 50.0, 88.0, 90.0, 200.0])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_scores_past_the_cap(M, dtype, cap):
+    """Scores of some 45 in size, so that caps of any of the forms are reached."""
+    for d, heads, kv in ((128, 4, 1), (64, 5, 1), (256, 2, 1)):
+        n = 200
+        q, k, v = rnd((1, n, heads, d), dtype, 1), rnd((1, n, kv, d), dtype, 2), rnd((1, n, kv, d), dtype, 3)
+        lse = torch.empty((1, n, heads), device=DEV)
+        scale = 45.0 / d**0.5
+        out = M.mkv_prefill(q, k, v, lse=lse, cap=cap, scale=scale)
+        ref = O.attend(f64(q[0]), f64(k[0]).transpose(1, 0, 2), f64(v[0]).transpose(1, 0, 2), O.visible(n, n),
+                       np.arange(n), np.arange(n), scale, cap)
+        capped_near(f64(out[0]), f64(lse[0]), ref, dtype, n, cap)
+    for ctype in (dtype, E4M3):
+        for m, g in ((2, 4), (12, 4), (40, 4)):
+            pages_check(M, ctype, dtype, 300, m, g, 128, cap, scale=4.0)
 
 
 TINY = [1e-3, 1e-4, 1e-6, 1e-8, 1e-20, 1e-37, 2.0**-149]

@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
                     }
                   } else {
                     const CappedScore capped(top2);
-                    if (top2 <= 64.f) {
+                    if (top2 <= 128.f) {
                       const float to2 = fminf(by1 / top2 * 2.885390081777927f, 3.402823466e38f);
 #pragma unroll
                       for (int i = 0; i < W; ++i) t[i] = capped.large(t[i] * to2);
@@ -819,7 +819,7 @@ __global__ void __launch_bounds__(AT<D, TILES, FROM, COPIES>::THREADS, 1)
                 asm volatile("" : "+f"(top2), "+f"(by1));
                 top2 *= 1.4426950408889634f;
                 const CappedScore capped(top2);
-                if (top2 <= 64.f) {      // an error of 2^-22 of so small a cap is less than the products'
+                if (top2 <= 128.f) {     // an error of 2^-22 of so small a cap is less than the products'
                   const float to2 = fminf(by1 / top2 * 2.885390081777927f, 3.402823466e38f);
 #pragma unroll
                   for (int i = 0; i < COLS; ++i) v[i] = capped.large(v[i] * to2);
