@@ -351,3 +351,32 @@ def test_the_status_word_of_prompts(M):
         assert torch.equal(got, want) and int(status) == word
     with pytest.raises((TypeError, ValueError)):
         M.mkv_prefill(q, k, k, status=torch.zeros(1, dtype=torch.int64, device=DEV))
+
+
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_long_walks_captured_and_on_two_streams(M, cap):
+    """The sums of a call lie in its own workspace: a replayed graph and calls side by side give the
+    same bits, whatever the workspace held before."""
+    q = [many((1, 4096, 8, 128), BF16, s) for s in (1, 2)]
+    k, v = many((1, 40000, 2, 128), BF16, 3), many((1, 40000, 2, 128), BF16, 4)
+    need = M.mkv_prefill_workspace(1, 4096, 40000, 8, 2, 128, capped=cap > 0)
+    assert need > 0
+    want = [M.mkv_prefill(x, k, v, cap=cap) for x in q]
+    torch.cuda.synchronize()
+    room = torch.full((need,), 0xff, dtype=torch.uint8, device=DEV)
+    x = torch.zeros_like(q[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = M.mkv_prefill(x, k, v, cap=cap, workspace=room)
+    for i in (0, 1, 0):
+        x.copy_(q[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i])
+    streams = [torch.cuda.Stream() for _ in q]
+    for _ in range(3):
+        got = [M.mkv_prefill(y, k, v, cap=cap, stream=s) for y, s in zip(q, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with pytest.raises(M.MkvError):
+        M.mkv_prefill(q[0], k, v, cap=cap, workspace=room[:-1])
